@@ -365,6 +365,106 @@ int pkv_decode_step_noalloc(const pkv_shape_t *shape, const pkv_plan_cfg_t *cfg,
                             const int32_t *d_block_table, const int32_t *d_seq_lens,
                             void *d_o, float *d_lse, void *stream);
 
+/* ------------------------------- 4-bit KV cache and windowed attention */
+
+/* (Neither is a step of the pages' method: a cache of a third the bytes, and
+ * the mask of models whose layers see a window, over the same block table.)
+ *
+ * The 4-bit cache is one buffer for K and V, uint8
+ *   quant_cache [num_pages][Hkv][page_size * d * 5 / 4],
+ * 5 bits per value: 32 neighbouring dims of one token, head and side share two
+ * fp16 numbers s and b, and code n in 0..15 stands for the fp16 number nearest
+ * to s (16 + n) + b.  With lo and hi the least and greatest of the 32 values,
+ * values beyond +-16384 (infinities too) taken as it:
+ *   s = the least fp16 number with 15 s >= hi - lo,
+ *   b = the fp16 number nearest to lo - 16 s (the lower one on a tie),
+ *   n = the integer nearest to (x - b) / s - 16 (the upper one on a tie)
+ *       within 0..15, and 0 where s = 0;
+ * a group that holds a NaN reads back as NaNs.  A value is off by at most
+ * s / 2 plus one fp16 step of b.  The codes are computed exactly, so that they
+ * do not depend on how tokens are split over calls.
+ * Layout of a page of one head (GR = d / 32, TB = min(page_size, 64)): blocks
+ * of TB tokens, TB * d * 5 / 4 bytes each, in four parts,
+ *   K codes   [token][t 4][j GR][e 2] 16-bit halves; field f of a half is the
+ *             code of dim 32 j + 8 f + 2 t + e
+ *   K params  [token][s | b][j GR] fp16
+ *   V codes   [token / 8][g 8][t 4][j GR][e 2] halves; field f is the code of
+ *             dim 32 j + 8 f + g of token 2 t + e of the eight
+ *   V params  [token / 8][t 4][j GR][s | b][e 2] fp16
+ * where field 0 of a half is bits 6-9, field 1 bits 2-5, field 2 bits 10-13 and
+ * field 3 the code's low two bits at 14-15 and its high two at 0-1.
+ *
+ * The calls below take one workspace of pkv_attn_workspace_size() bytes, zeroed
+ * once after allocation; its counters are back at zero after every launch, and
+ * pkv_get_error() reads its error word.  Calls on one workspace must not
+ * overlap on the GPU (two graphs that may run at once need one each).  They use
+ * the shape's B, Hkv, d, page_size, num_pages and bt_stride; the decodes Hq and
+ * scale too. */
+
+/* Tokens a query sees: the first `sinks` of its row and the last `window`
+ * (both >= 0; they may overlap).  With both 0 it sees none. */
+typedef struct {
+    int32_t window;
+    int32_t sinks;
+} pkv_window_t;
+
+/* Bytes of one page of the 4-bit cache, all KV heads: Hkv*page_size*d*5/4
+ * (0 for a bad shape). */
+size_t pkv_quant_page_bytes(const pkv_shape_t *shape);
+
+/* Bytes of the workspace of the four calls below (0 for a bad shape).  It
+ * depends on B, Hq / Hkv and d only. */
+size_t pkv_attn_workspace_size(const pkv_shape_t *shape);
+
+/* pkv_quant_append -- quantise new tokens into the 4-bit cache.
+ * One kernel launch.  Row i's new tokens are rows
+ * d_new_offsets[i] .. d_new_offsets[i + 1] of d_k_new and d_v_new (int32
+ * offsets [B + 1]; NULL: one token per row, total_new = B), fp16 [Hkv][d] each,
+ * `new_stride` elements apart (a multiple of 8, >= Hkv*d: a slice of a fused
+ * projection is taken as it is).  They go to positions seq_lens[i] .. of row i,
+ * whose block table must already name the pages; then
+ * seq_lens_out[i] = seq_lens[i] + their number (seq_lens_out may be seq_lens,
+ * or another array, which leaves seq_lens as it was).
+ * total_new: rows of d_k_new / d_v_new.  Rows behind the last offset are not
+ * read.  A row with a negative length, offsets outside the buffer or no room in
+ * its block table is refused whole; one that meets a page id out of range
+ * writes its other tokens.  Either keeps its length, and the error word records
+ * the first.  New tokens of one call must not share a cache position. */
+int pkv_quant_append(const pkv_shape_t *shape, void *d_ws, const void *d_k_new, const void *d_v_new,
+                     int64_t new_stride, int32_t total_new, const int32_t *d_new_offsets,
+                     const int32_t *d_block_table, const int32_t *d_seq_lens, int32_t *d_seq_lens_out,
+                     void *d_quant_cache, void *stream);
+
+/* pkv_quant_read -- read tokens of the 4-bit cache back as fp16.
+ * One kernel launch.  Rows d_out_offsets[i] .. d_out_offsets[i + 1] of d_k_out
+ * and d_v_out ([Hkv][d] each, `out_stride` elements apart, as above) get tokens
+ * d_first[i] .. of row i (d_first NULL: from token 0).  Output rows outside
+ * every row's span are left as they were.  A token outside [0, seq_lens[i]) or
+ * on a page id out of range is written as zeros and recorded in the error
+ * word. */
+int pkv_quant_read(const pkv_shape_t *shape, void *d_ws, const void *d_quant_cache,
+                   const int32_t *d_block_table, const int32_t *d_seq_lens, const int32_t *d_first,
+                   const int32_t *d_out_offsets, int32_t total_out, void *d_k_out, void *d_v_out,
+                   int64_t out_stride, void *stream);
+
+/* pkv_quant_decode -- one decode step's attention over the 4-bit cache.
+ * One kernel launch.  o and lse are those of pkv_single_pass over the fp16
+ * values that pkv_quant_read returns, with fp32 sums.  win NULL: every token
+ * of the row; else only those a pkv_window_t leaves visible (the row's last
+ * token is the query's own position).  A row that sees no token gets o = 0,
+ * lse = -inf.  No token outside the visible ones' pages is read. */
+int pkv_quant_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d_ws, const void *d_q,
+                     const void *d_quant_cache, const int32_t *d_block_table, const int32_t *d_seq_lens,
+                     void *d_o, float *d_lse, void *stream);
+
+/* pkv_window_decode -- one decode step's attention over the fp16 pages, for
+ * layers whose queries see a sliding window and the row's first tokens
+ * ("sinks").  One kernel launch; as pkv_quant_decode, over k_cache / v_cache.
+ * `win` is required. */
+int pkv_window_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d_ws, const void *d_q,
+                      const void *d_k_cache, const void *d_v_cache, const int32_t *d_block_table,
+                      const int32_t *d_seq_lens, void *d_o, float *d_lse, void *stream);
+
 /* ------------------------------------------------------------- policy */
 
 /* Thresholds of the calibrated policy (Methodology 2).  The pages route

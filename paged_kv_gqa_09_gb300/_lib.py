@@ -46,6 +46,8 @@ EXPORTS = [
     "pkv_decode_step_host", "pkv_append_decode_step_host",
     "pkv_append", "pkv_append_plan", "pkv_exact_length_groups", "pkv_policy_default", "pkv_policy",
     "pkv_cost_model_default", "pkv_policy_learned",
+    "pkv_quant_page_bytes", "pkv_attn_workspace_size", "pkv_quant_append", "pkv_quant_read",
+    "pkv_quant_decode", "pkv_window_decode",
     "pkv_get_counters", "pkv_reset_counters", "pkv_step_model", "pkv_get_error",
     "pkv_test_starve_next_decodes", "pkv_last_error_string", "pkv_version",
 ]
@@ -72,6 +74,11 @@ class PlanCfg(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int32), ("split_tokens", ctypes.c_int32),
                 ("bucket_len", ctypes.c_int32), ("max_tasks", ctypes.c_int32),
                 ("merge", ctypes.c_int32), ("plan", ctypes.c_int32)]
+
+
+class Window(ctypes.Structure):
+    """Tokens a query sees: the first `sinks` and the last `window` of its row."""
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
 
 class PolicyCfg(ctypes.Structure):
@@ -131,6 +138,7 @@ def load() -> ctypes.CDLL:
         L = ctypes.CDLL(path)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         S, C, PC = ctypes.POINTER(Shape), ctypes.POINTER(PlanCfg), ctypes.POINTER(PolicyCfg)
+        W = ctypes.POINTER(Window)
         sig = {
             "pkv_plan_workspace_size": (sz, [S, C]),
             "pkv_partials_size": (sz, [S, C]),
@@ -147,6 +155,12 @@ def load() -> ctypes.CDLL:
             "pkv_append": (ctypes.c_int, [S, vp, vp, vp, vp, vp, vp, vp, vp]),
             "pkv_append_plan": (ctypes.c_int, [S, C] + [vp] * 10),
             "pkv_exact_length_groups": (ctypes.c_int, [vp, i32, vp, vp, vp, ctypes.POINTER(ctypes.c_int32)]),
+            "pkv_quant_page_bytes": (sz, [S]),
+            "pkv_attn_workspace_size": (sz, [S]),
+            "pkv_quant_append": (ctypes.c_int, [S, vp, vp, vp, ctypes.c_int64, i32] + [vp] * 6),
+            "pkv_quant_read": (ctypes.c_int, [S] + [vp] * 6 + [i32, vp, vp, ctypes.c_int64, vp]),
+            "pkv_quant_decode": (ctypes.c_int, [S, W] + [vp] * 8),
+            "pkv_window_decode": (ctypes.c_int, [S, W] + [vp] * 9),
             "pkv_policy_default": (None, [PC]),
             "pkv_policy": (ctypes.c_int, [i32, i32, PC, ctypes.POINTER(ctypes.c_int32),
                                           ctypes.POINTER(ctypes.c_int32)]),

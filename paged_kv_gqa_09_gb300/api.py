@@ -19,7 +19,7 @@ from . import _lib
 from ._lib import (PKV_MERGE_FUSED, PKV_MERGE_SEPARATE, PKV_PATH_BUCKETED_SPLIT,
                    PKV_PATH_SINGLE_PASS, PKV_PATH_WORKQUEUE, PKV_PLAN_IN_DECODE,
                    PKV_PLAN_SEPARATE, PKV_SELF_PLAN_MAX_B, Counters,
-                   PlanCfg, PolicyCfg, Shape, StepModel, check)
+                   PlanCfg, PolicyCfg, Shape, StepModel, Window, check)
 
 __all__ = [
     "Shape", "PlanCfg", "PolicyCfg", "make_shape", "make_cfg",
@@ -29,7 +29,9 @@ __all__ = [
     "pkv_decode_step", "pkv_decode_step_noalloc",
     "pkv_decode_step_host", "pkv_append_decode_step_host", "pkv_decode_step_rows",
     "exact_length_buckets_step", "pkv_exact_length_groups", "pkv_append",
-    "pkv_append_plan", "pkv_policy", "pkv_policy_default",
+    "pkv_append_plan", "Window", "make_quant_shape", "quant_cache_zeros", "pkv_quant_page_bytes",
+    "pkv_attn_workspace_size", "pkv_quant_append", "pkv_quant_read", "pkv_quant_decode",
+    "pkv_window_decode", "pkv_policy", "pkv_policy_default",
     "pkv_cost_model_default", "pkv_policy_learned",
     "pkv_get_counters", "pkv_reset_counters", "pkv_step_model", "pkv_get_error", "pkv_version",
     "PagedDecoder", "HostDecodeLoop",
@@ -337,6 +339,146 @@ def pkv_append_plan(shape, cfg, ws, k_new, v_new, block_table, seq_lens, k_cache
                             _dev(k_cache, "k_cache", torch.float16),
                             _dev(v_cache, "v_cache", torch.float16), _stream(stream)),
           "pkv_append_plan")
+
+
+# ------------------------------------------ 4-bit cache and windowed attention
+
+def make_quant_shape(Hq: int, d: int, quant_cache: torch.Tensor, block_table: torch.Tensor,
+                     scale: Optional[float] = None) -> Shape:
+    """Shape of a 4-bit cache uint8 [num_pages, Hkv, page_size * d * 5 / 4] for
+    Hq query heads of d dims and block_table [B, bt_stride]."""
+    num_pages, Hkv, nbytes = quant_cache.shape
+    P = nbytes * 4 // (5 * d)
+    if P * d * 5 // 4 != nbytes:
+        raise ValueError(f"quant_cache pages of {nbytes} bytes are no whole tokens of d={d}")
+    return Shape(int(block_table.shape[0]), int(Hq), int(Hkv), int(d), int(P), int(num_pages),
+                 int(block_table.shape[1]), float(1.0 / math.sqrt(d) if scale is None else scale))
+
+
+def quant_cache_zeros(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda") -> torch.Tensor:
+    """A 4-bit cache of num_pages pages, every value 0."""
+    return torch.zeros((num_pages, Hkv, page_size * d * 5 // 4), dtype=torch.uint8, device=device)
+
+
+def pkv_quant_page_bytes(shape: Shape) -> int:
+    n = _lib.load().pkv_quant_page_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise _lib.PkvError(_lib.PKV_EINVAL, "pkv_quant_page_bytes", _lib.last_error())
+    return int(n)
+
+
+def pkv_attn_workspace_size(shape: Shape) -> int:
+    n = _lib.load().pkv_attn_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise _lib.PkvError(_lib.PKV_EINVAL, "pkv_attn_workspace_size", _lib.last_error())
+    return int(n)
+
+
+def _size(t: torch.Tensor, name: str, n: int) -> torch.Tensor:
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
+    return t
+
+
+def _attn_ws(shape: Shape, ws: torch.Tensor) -> int:
+    need = pkv_attn_workspace_size(shape)
+    if ws.numel() * ws.element_size() < need:
+        raise ValueError(f"workspace has {ws.numel() * ws.element_size()} bytes, needs {need}")
+    return _ws(ws)
+
+
+def _quant(shape: Shape, t: torch.Tensor) -> int:
+    return _dev(_size(t, "quant_cache", shape.num_pages * shape.Hkv * (shape.page_size * shape.d * 5 // 4)),
+                "quant_cache", torch.uint8)
+
+
+def _packed(shape: Shape, k: torch.Tensor, v: torch.Tensor, what: str) -> tuple[int, int, int, int]:
+    """(k pointer, v pointer, tokens, token stride) of packed fp16 K and V
+    [T, Hkv, d], whose tokens may be strided (alike in both)."""
+    T = int(k.shape[0])
+    for t, name in ((k, f"k_{what}"), (v, f"v_{what}")):
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must be a CUDA tensor on the current device (got {t.device})")
+        if t.dtype != torch.float16:
+            raise ValueError(f"{name} must be torch.float16 (got {t.dtype})")
+        if tuple(t.shape) != (T, shape.Hkv, shape.d):
+            raise ValueError(f"{name} must be [{T}, {shape.Hkv}, {shape.d}] (got {tuple(t.shape)})")
+        if T and (t.stride(2) != 1 or (shape.Hkv > 1 and t.stride(1) != shape.d)):
+            raise ValueError(f"{name} must be contiguous within a token (strides {t.stride()})")
+    stride = int(k.stride(0)) if T > 1 else shape.Hkv * shape.d
+    if T > 1 and int(v.stride(0)) != stride:
+        raise ValueError(f"k_{what} and v_{what} must have one token stride")
+    return k.data_ptr(), v.data_ptr(), T, stride
+
+
+def pkv_quant_append(shape, ws, k_new, v_new, block_table, seq_lens, quant_cache, new_offsets=None,
+                     seq_lens_out=None, stream=None) -> None:
+    """Quantise new tokens k_new, v_new [T, Hkv, d] into the 4-bit cache behind
+    each row's seq_lens tokens: row i's are new_offsets[i] .. new_offsets[i + 1]
+    (None: one per row).  The advanced lengths go to seq_lens_out (None: in
+    place).  See include/pkv.h."""
+    kp, vp, T, stride = _packed(shape, k_new, v_new, "new")
+    out = seq_lens if seq_lens_out is None else seq_lens_out
+    if new_offsets is not None:
+        _size(new_offsets, "new_offsets", shape.B + 1)
+    check(_lib.load().pkv_quant_append(
+        ctypes.byref(shape), _attn_ws(shape, ws), kp, vp, stride, T,
+        _dev(new_offsets, "new_offsets", torch.int32, nullable=True),
+        _dev(_size(block_table, "block_table", shape.B * shape.bt_stride), "block_table", torch.int32),
+        _dev(_size(seq_lens, "seq_lens", shape.B), "seq_lens", torch.int32),
+        _dev(_size(out, "seq_lens_out", shape.B), "seq_lens_out", torch.int32),
+        _quant(shape, quant_cache), _stream(stream)), "pkv_quant_append")
+
+
+def pkv_quant_read(shape, ws, quant_cache, block_table, seq_lens, out_offsets, k_out, v_out, first=None,
+                   stream=None) -> None:
+    """Read tokens first[i] .. of each row (None: from token 0) back as fp16 into
+    rows out_offsets[i] .. out_offsets[i + 1] of k_out, v_out [T, Hkv, d]."""
+    kp, vp, T, stride = _packed(shape, k_out, v_out, "out")
+    if first is not None:
+        _size(first, "first", shape.B)
+    check(_lib.load().pkv_quant_read(
+        ctypes.byref(shape), _attn_ws(shape, ws), _quant(shape, quant_cache),
+        _dev(_size(block_table, "block_table", shape.B * shape.bt_stride), "block_table", torch.int32),
+        _dev(_size(seq_lens, "seq_lens", shape.B), "seq_lens", torch.int32),
+        _dev(first, "first", torch.int32, nullable=True),
+        _dev(_size(out_offsets, "out_offsets", shape.B + 1), "out_offsets", torch.int32), T, kp, vp, stride,
+        _stream(stream)), "pkv_quant_read")
+
+
+def _attend_args(shape, q, block_table, seq_lens, o, lse):
+    n = shape.B * shape.Hq
+    return (_dev(_size(q, "q", n * shape.d), "q", torch.float16),
+            _dev(_size(block_table, "block_table", shape.B * shape.bt_stride), "block_table", torch.int32),
+            _dev(_size(seq_lens, "seq_lens", shape.B), "seq_lens", torch.int32),
+            _dev(_size(o, "o", n * shape.d), "o", torch.float16),
+            0 if lse is None else _dev(_size(lse, "lse", n), "lse", torch.float32))
+
+
+def pkv_quant_decode(shape, ws, q, quant_cache, block_table, seq_lens, o, lse=None, window=None, sinks=0,
+                     stream=None) -> None:
+    """Decode attention over the 4-bit cache: the whole row (window None), or its
+    first `sinks` and last `window` tokens."""
+    if window is None and sinks:
+        raise ValueError("sinks go with a window")
+    qp, bp, sp, op, lp = _attend_args(shape, q, block_table, seq_lens, o, lse)
+    win = None if window is None else ctypes.byref(Window(int(window), int(sinks)))
+    check(_lib.load().pkv_quant_decode(ctypes.byref(shape), win, _attn_ws(shape, ws), qp,
+                                       _quant(shape, quant_cache), bp, sp, op, lp, _stream(stream)),
+          "pkv_quant_decode")
+
+
+def pkv_window_decode(shape, ws, q, k_cache, v_cache, block_table, seq_lens, window, sinks, o, lse=None,
+                      stream=None) -> None:
+    """Decode attention over the fp16 pages, of each row's first `sinks` and last
+    `window` tokens."""
+    qp, bp, sp, op, lp = _attend_args(shape, q, block_table, seq_lens, o, lse)
+    n = shape.num_pages * shape.page_size * shape.Hkv * shape.d
+    check(_lib.load().pkv_window_decode(ctypes.byref(shape), ctypes.byref(Window(int(window), int(sinks))),
+                                        _attn_ws(shape, ws), qp,
+                                        _dev(_size(k_cache, "k_cache", n), "k_cache", torch.float16),
+                                        _dev(_size(v_cache, "v_cache", n), "v_cache", torch.float16),
+                                        bp, sp, op, lp, _stream(stream)), "pkv_window_decode")
 
 
 def pkv_policy_default() -> PolicyCfg:

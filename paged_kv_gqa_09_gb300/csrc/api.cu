@@ -5,6 +5,7 @@
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "plan_map.cuh"
+#include "quant_format.cuh"
 
 #include <atomic>
 #include <cmath>
@@ -1094,6 +1095,207 @@ int pkv_step_model(int32_t path, const pkv_shape_t *s, int32_t C, int32_t bucket
     return PKV_OK;
 }
 
+// ------------------------------------- the 4-bit cache and windowed attention
+
+}  // extern "C"
+
+namespace {
+
+int64_t quant_page_head_bytes(const pkv_shape_t *s) { return (int64_t)s->page_size * s->d * 5 / 4; }
+
+int tb_log2(const pkv_shape_t *s) { return ilog2(quant_block_tokens(s->page_size)); }
+
+// Threads of a launch that takes 16 bytes of one side of one token's head each.
+int check_packed(const pkv_shape_t *s, int32_t T, int64_t stride, const char *name)
+{
+    if (T < 0)
+        return fail(PKV_EINVAL, "%s has %d tokens", name, T);
+    if (stride < (int64_t)s->Hkv * s->d || stride % 8)
+        return fail(PKV_EINVAL, "%s: token stride %lld must be a multiple of 8 and at least Hkv*d=%d", name,
+                    (long long)stride, s->Hkv * s->d);
+    if ((int64_t)T * s->Hkv * s->d > (int64_t)0x7fffffff * 64)
+        return fail(PKV_EUNSUPPORTED, "%s: %d tokens of %d heads exceed one launch", name, T, s->Hkv);
+    return PKV_OK;
+}
+
+int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const void *q, const void *k,
+               const void *v, const void *cache, const int32_t *bt, const int32_t *sl, void *o, float *lse,
+               void *stream)
+{
+    if (win && (win->window < 0 || win->sinks < 0))
+        return fail(PKV_EINVAL, "negative window=%d or sinks=%d", win->window, win->sinks);
+    PKV_TRY(check_ptr(d_ws, "workspace"));
+    PKV_TRY(check_ptr(q, "q"));
+    if (cache) {
+        PKV_TRY(check_ptr(cache, "quant_cache"));
+    } else {
+        PKV_TRY(check_ptr(k, "k_cache"));
+        PKV_TRY(check_ptr(v, "v_cache"));
+    }
+    PKV_TRY(check_ptr(bt, "block_table"));
+    PKV_TRY(check_ptr(sl, "seq_lens"));
+    PKV_TRY(check_ptr(o, "o"));
+    PKV_TRY(check_ptr(lse, "lse", true));
+    AttendParams p = {};
+    p.q = static_cast<const __half *>(q);
+    p.bt = bt;
+    p.seq_lens = sl;
+    p.k = static_cast<const __half *>(k);
+    p.v = static_cast<const __half *>(v);
+    p.cache = static_cast<const uint8_t *>(cache);
+    p.ws = ws_hdr(d_ws);
+    p.counters = reinterpret_cast<int32_t *>(static_cast<char *>(d_ws) + aws_counters_off(s->B));
+    p.partials = reinterpret_cast<float *>(static_cast<char *>(d_ws) + aws_partials_off(s->B));
+    p.o = static_cast<__half *>(o);
+    p.lse = lse;
+    p.page_head_bytes = quant_page_head_bytes(s);
+    p.B = s->B;
+    p.Hq = s->Hq;
+    p.Hkv = s->Hkv;
+    p.G = s->Hq / s->Hkv;
+    p.num_pages = s->num_pages;
+    p.bt_stride = s->bt_stride;
+    p.log2P = ilog2(s->page_size);
+    p.tb_log2 = tb_log2(s);
+    p.len_cap = len_cap(s);
+    // no window: every token of the longest row the table can hold is inside it
+    p.window = win ? win->window : len_cap(s);
+    p.sinks = win ? win->sinks : 0;
+    p.scale_log2 = s->scale * 1.4426950408889634f;
+    cudaError_t e = launch_attend(s->d, cache != nullptr, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "attention launch");
+    g_cnt.decode++;
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_quant_page_bytes(const pkv_shape_t *s)
+{
+    if (check_shape(s))
+        return 0;
+    return (size_t)quant_page_head_bytes(s) * s->Hkv;
+}
+
+size_t pkv_attn_workspace_size(const pkv_shape_t *s)
+{
+    if (check_shape(s))
+        return 0;
+    return aws_partials_off(s->B) +
+           (size_t)2 * kAttnMaxCtas * (s->Hq / s->Hkv) * (size_t)(s->d + 2) * sizeof(float);
+}
+
+int pkv_quant_append(const pkv_shape_t *s, void *d_ws, const void *k_new, const void *v_new, int64_t new_stride,
+                     int32_t total_new, const int32_t *d_new_offsets, const int32_t *bt, const int32_t *sl,
+                     int32_t *sl_out, void *cache, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    if (s->B == 0)
+        return PKV_OK;  // an empty batch: nothing to do
+    PKV_TRY(check_packed(s, total_new, new_stride, "k_new"));
+    if (!d_new_offsets && total_new != s->B)
+        return fail(PKV_EINVAL, "without offsets every row has one token: total_new=%d, B=%d", total_new, s->B);
+    PKV_TRY(check_ptr(d_ws, "workspace"));
+    PKV_TRY(check_ptr(k_new, "k_new", total_new == 0));
+    PKV_TRY(check_ptr(v_new, "v_new", total_new == 0));
+    PKV_TRY(check_ptr(d_new_offsets, "new_offsets", true));
+    PKV_TRY(check_ptr(bt, "block_table"));
+    PKV_TRY(check_ptr(sl, "seq_lens"));
+    PKV_TRY(check_ptr(sl_out, "seq_lens_out"));
+    PKV_TRY(check_ptr(cache, "quant_cache"));
+    QuantAppendParams p = {};
+    p.k_new = static_cast<const __half *>(k_new);
+    p.v_new = static_cast<const __half *>(v_new);
+    p.new_stride = new_stride;
+    p.offsets = d_new_offsets;
+    p.bt = bt;
+    p.seq_lens = sl;
+    p.seq_lens_out = sl_out;
+    p.cache = static_cast<uint8_t *>(cache);
+    p.ws = ws_hdr(d_ws);
+    p.row_bad = reinterpret_cast<int32_t *>(static_cast<char *>(d_ws) + aws_row_bad_off());
+    p.page_head_bytes = quant_page_head_bytes(s);
+    p.T = total_new;
+    p.B = s->B;
+    p.Hkv = s->Hkv;
+    p.log2P = ilog2(s->page_size);
+    p.tb_log2 = tb_log2(s);
+    p.num_pages = s->num_pages;
+    p.bt_stride = s->bt_stride;
+    p.len_cap = len_cap(s);
+    cudaError_t e = launch_quant_append(s->d, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "quant append launch");
+    g_cnt.append++;
+    return PKV_OK;
+}
+
+int pkv_quant_read(const pkv_shape_t *s, void *d_ws, const void *cache, const int32_t *bt, const int32_t *sl,
+                   const int32_t *d_first, const int32_t *d_out_offsets, int32_t total_out, void *k_out, void *v_out,
+                   int64_t out_stride, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    if (s->B == 0 || total_out == 0)
+        return PKV_OK;  // nothing to read
+    PKV_TRY(check_packed(s, total_out, out_stride, "k_out"));
+    PKV_TRY(check_ptr(d_ws, "workspace"));
+    PKV_TRY(check_ptr(cache, "quant_cache"));
+    PKV_TRY(check_ptr(bt, "block_table"));
+    PKV_TRY(check_ptr(sl, "seq_lens"));
+    PKV_TRY(check_ptr(d_first, "first", true));
+    PKV_TRY(check_ptr(d_out_offsets, "out_offsets"));
+    PKV_TRY(check_ptr(k_out, "k_out"));
+    PKV_TRY(check_ptr(v_out, "v_out"));
+    QuantReadParams p = {};
+    p.cache = static_cast<const uint8_t *>(cache);
+    p.bt = bt;
+    p.seq_lens = sl;
+    p.first = d_first;
+    p.offsets = d_out_offsets;
+    p.k_out = static_cast<__half *>(k_out);
+    p.v_out = static_cast<__half *>(v_out);
+    p.out_stride = out_stride;
+    p.ws = ws_hdr(d_ws);
+    p.page_head_bytes = quant_page_head_bytes(s);
+    p.T = total_out;
+    p.B = s->B;
+    p.Hkv = s->Hkv;
+    p.log2P = ilog2(s->page_size);
+    p.tb_log2 = tb_log2(s);
+    p.num_pages = s->num_pages;
+    p.bt_stride = s->bt_stride;
+    p.len_cap = len_cap(s);
+    cudaError_t e = launch_quant_read(s->d, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "quant read launch");
+    return PKV_OK;
+}
+
+int pkv_quant_decode(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const void *q, const void *cache,
+                     const int32_t *bt, const int32_t *sl, void *o, float *lse, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    if (s->B == 0)
+        return PKV_OK;  // an empty batch: nothing to do
+    if (!cache)
+        return fail(PKV_EINVAL, "quant_cache is NULL");
+    return run_attend(s, win, d_ws, q, nullptr, nullptr, cache, bt, sl, o, lse, stream);
+}
+
+int pkv_window_decode(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const void *q, const void *k,
+                      const void *v, const int32_t *bt, const int32_t *sl, void *o, float *lse, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    if (s->B == 0)
+        return PKV_OK;  // an empty batch: nothing to do
+    if (!win)
+        return fail(PKV_EINVAL, "window is NULL");
+    return run_attend(s, win, d_ws, q, k, v, nullptr, bt, sl, o, lse, stream);
+}
+
 // ------------------------------------------------------------------ errors
 
 int pkv_get_error(void *d_ws, void *stream)
@@ -1124,6 +1326,8 @@ int pkv_get_error(void *d_ws, void *stream)
     case kErrNoPage:
         return fail(PKV_EDEVICE, "no free page for row %d at length %d (%d pages were free)", h[1],
                     h[2], h[3]);
+    case kErrBadSpan:
+        return fail(PKV_EDEVICE, "row %d has %d packed tokens from offset %d, outside the packed buffer", h[1], h[3], h[2]);
     case kErrBadRow:
         return fail(PKV_EDEVICE, "row list entry %d is %d, outside [0, %d)", h[1], h[2], h[3]);
     case kErrTimeout:

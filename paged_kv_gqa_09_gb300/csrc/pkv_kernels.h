@@ -108,6 +108,59 @@ struct AppendParams {
     int B, Hkv, d, log2P, num_pages, bt_stride;
 };
 
+// Workspace of the windowed and 4-bit operators: the header, one int per row
+// (rows that an append refuses), one counter per CTA, then the partial states.
+constexpr int kAttnMaxCtas = 512;
+inline size_t aws_row_bad_off() { return kWsHeaderBytes; }
+inline size_t aws_counters_off(int B) { return (kWsHeaderBytes + sizeof(int32_t) * (size_t)B + 15) & ~(size_t)15; }
+inline size_t aws_partials_off(int B) { return aws_counters_off(B) + sizeof(int32_t) * (size_t)kAttnMaxCtas; }
+
+struct QuantAppendParams {
+    const __half *k_new, *v_new;
+    int64_t new_stride;         // elements between tokens of k_new / v_new
+    const int32_t *offsets;     // [B + 1]; nullptr: one token per row
+    const int32_t *bt, *seq_lens;
+    int32_t *seq_lens_out;      // may be seq_lens
+    uint8_t *cache;
+    WsHeader *ws;
+    int32_t *row_bad;           // [B], zero between launches
+    int64_t page_head_bytes;    // one page of one head
+    int T, B, Hkv, log2P, tb_log2, num_pages, bt_stride, len_cap;
+};
+
+struct QuantReadParams {
+    const uint8_t *cache;
+    const int32_t *bt, *seq_lens;
+    const int32_t *first;    // [B] first token of each row to read; nullptr: 0
+    const int32_t *offsets;  // [B + 1]
+    __half *k_out, *v_out;
+    int64_t out_stride;
+    WsHeader *ws;
+    int64_t page_head_bytes;
+    int T, B, Hkv, log2P, tb_log2, num_pages, bt_stride, len_cap;
+};
+
+// Decode attention over the tokens [0, sinks) and [N - window, N) of each row.
+struct AttendParams {
+    const __half *q;
+    const int32_t *bt, *seq_lens;
+    const __half *k, *v;      // fp16 pages, or
+    const uint8_t *cache;     // the 4-bit cache
+    WsHeader *ws;
+    int32_t *counters;        // [kAttnMaxCtas], zero between launches
+    float *partials;
+    __half *o;
+    float *lse;  // nullable
+    int64_t page_head_bytes;
+    int B, Hq, Hkv, G, num_pages, bt_stride, log2P, tb_log2, len_cap;
+    int window, sinks;
+    float scale_log2;
+};
+
+cudaError_t launch_quant_append(int d, const QuantAppendParams &p, cudaStream_t s);
+cudaError_t launch_quant_read(int d, const QuantReadParams &p, cudaStream_t s);
+cudaError_t launch_attend(int d, bool quant, const AttendParams &p, cudaStream_t s);
+
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t s, bool pdl);
 cudaError_t launch_decode(int d, int mode, const CUtensorMap &tk, const CUtensorMap &tv,
                           const DecodeParams &p, int grid, cudaStream_t s, bool pdl);
