@@ -188,6 +188,25 @@ struct DevInfo {
 std::mutex g_dev_mu;
 DevInfo g_dev[64];
 
+// SMs of the current device.
+int device_sms(int *out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= 64)
+        return fail(PKV_EUNSUPPORTED, "device ordinal %d", dev);
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    if (!g_dev[dev].sms) {
+        e = cudaDeviceGetAttribute(&g_dev[dev].sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaDeviceGetAttribute");
+    }
+    *out = g_dev[dev].sms;
+    return PKV_OK;
+}
+
 // Resident decode CTAs the current device holds at once (SMs x occupancy).
 int device_slots(int d, int *out)
 {
@@ -1140,8 +1159,6 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     p.q = static_cast<const __half *>(q);
     p.bt = bt;
     p.seq_lens = sl;
-    p.k = static_cast<const __half *>(k);
-    p.v = static_cast<const __half *>(v);
     p.cache = static_cast<const uint8_t *>(cache);
     p.ws = ws_hdr(d_ws);
     p.counters = reinterpret_cast<int32_t *>(static_cast<char *>(d_ws) + aws_counters_off(s->B));
@@ -1162,7 +1179,15 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     p.window = win ? win->window : len_cap(s);
     p.sinks = win ? win->sinks : 0;
     p.scale_log2 = s->scale * 1.4426950408889634f;
-    cudaError_t e = launch_attend(s->d, cache != nullptr, p, static_cast<cudaStream_t>(stream));
+    int sms = 0;
+    PKV_TRY(device_sms(&sms));
+    alignas(64) CUtensorMap tk = {}, tv = {};
+    if (!cache) {
+        const int box_tok = quant_block_tokens(s->page_size);
+        PKV_TRY(encode_kv_map(&tk, k, s, box_tok));
+        PKV_TRY(encode_kv_map(&tv, v, s, box_tok));
+    }
+    cudaError_t e = launch_attend(s->d, tk, tv, p, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "attention launch");
     g_cnt.decode++;

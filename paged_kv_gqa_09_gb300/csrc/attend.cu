@@ -1,9 +1,33 @@
 // attend.cu -- decode attention over the tokens a sliding window and the row's
 // first tokens leave visible, from the fp16 pages or from the 4-bit cache.
 //
-// One CTA per (row, KV head): tiles of 32 visible tokens are brought to shared
-// memory as fp16, scored for the G query heads, and folded into a running
-// maximum, sum and fp32 accumulator (the online softmax).
+// For query head h of row i with visible tokens t:
+//   s_t = scale q_h . K_t,  o = sum_t exp(s_t - m) V_t / l,  lse = m + ln l,
+//   m = max_t s_t,  l = sum_t exp(s_t - m).
+// One pass over the cache: 4 d flops per visible token and query head against
+// 2.5 d bytes (4-bit) or 4 d (fp16) per token and KV head; HBM bounds it.
+//
+// Work split.  A row's visible tokens lie in T_i tiles of 64 tokens (tiles
+// between the sinks and the window are never touched).  All tiles of the batch
+// in (row, KV head, tile) order form one line, which the CTAs cut into equal
+// runs: every CTA derives the line's length and its own run from the row
+// lengths, so one launch balances rows of any lengths without a plan.  The
+// tiles that a CTA takes of one (row, head) are a piece; a piece that is the
+// whole (row, head) writes o and lse, any other its state (m, l, acc in fp32),
+// and the CTA that finishes a (row, head)'s last piece merges its states in
+// piece order (so the result does not depend on who came last).
+//
+// CTA: warp 4 is the producer, warps 0..3 the consumers.  The producer walks
+// the run, reads block-table entries a batch of tiles ahead and streams each
+// tile into a ring of shared-memory stages: fp16 pages with tiled TMA copies
+// (128-byte swizzle), the 4-bit cache -- whose pages hold K and V of a head in
+// one contiguous run per 64 tokens or page -- with plain bulk copies; a piece's
+// first tile brings its q rows.  Consumer warp w takes tokens [16w, 16w + 16)
+// of every tile with its own online softmax: scores S^T = K q^T (16 tokens x 8
+// heads) and O^T += V^T P^T (d x 8 heads) on mma.sync m16n8k16, fp16 in, fp32
+// accumulate.  N = 8 heads is all a KV head has, so a tcgen05 tile would be
+// 1/16 full; the registers that mma.sync reads are what the 4-bit codes are
+// unpacked into.  Every wait is bounded (1 s).
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
@@ -11,142 +35,828 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kTile = 32;
+constexpr int kCW = 4;                    // consumer warps
+constexpr int kTile = 16 * kCW;           // tokens per stage
+constexpr int kThreads = 32 * (kCW + 1);  // + producer warp
+constexpr int kMaxG = 8;
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kDrainNs = 20000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e30f;  // running maximum before the first score (finite: -inf - it is -inf)
+
+// The running maximum of the softmax follows a tile's only when that exceeds it
+// by more than this (in log2 units): weights then stay below 2^8, well inside
+// fp16, and most tiles need neither a reduction over tokens nor a rescaling.
+constexpr float kMaxSlack = 8.f;
+
+constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 
 template <int D, bool QUANT>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p)
+struct Layout {
+    static constexpr int kTileBytes = kTile * D * 2;  // fp16: one of K, V
+    static constexpr int kKvBytes = QUANT ? kTile * D * 5 / 4 : 2 * kTileBytes;
+    static constexpr int kQBytes = kMaxG * D * 2;
+    static constexpr int kStageBytes = kKvBytes + kQBytes;
+    static constexpr int kCtasPerSm = QUANT ? 3 : 2;
+    static constexpr int kStages = QUANT ? (D == 128 ? 5 : 10) : (D == 128 ? 3 : 6);
+    static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
+    static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
+    static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
+    static constexpr int kBytes = kBarOff + (2 * kStages + 1) * 8;
+    static constexpr int kAlloc = kBytes + 1024;
+    // at a piece's end the warps exchange their states through its last stage
+    static_assert(kStageBytes >= (kCW - 1) * kMaxG * D * 4, "a stage holds three warps' states");
+    static_assert(QUANT || kStageBytes % 1024 == 0, "swizzled tiles keep 1024-byte alignment");
+    static_assert(kCtasPerSm * (kAlloc + 1024) <= 228 * 1024, "resident CTAs");
+};
+
+// What of a row of N tokens is visible: tokens [0, ns) and [w0, N), in tiles
+// [0, a) and [b, b + T - a).
+struct RowSpan {
+    int N, ns, w0, a, b, T;
+    __device__ __forceinline__ int tile(int k) const { return k < a ? k : b + (k - a); }
+};
+
+__device__ __forceinline__ RowSpan row_span(const AttendParams &p, int len)
+{
+    RowSpan r;
+    r.N = min(max(len, 0), p.len_cap);
+    r.ns = min(p.sinks, r.N);
+    r.w0 = max(r.ns, r.N - p.window);
+    r.a = (int)(((unsigned)r.ns + kTile - 1) / kTile);
+    r.b = max(r.a, r.w0 / kTile);
+    r.T = r.a;
+    if (r.w0 < r.N)
+        r.T += max(0, (int)(((unsigned)r.N + kTile - 1) / kTile) - r.b);
+    return r;
+}
+
+__device__ __forceinline__ bool visible(int tok, int ns, int w0, int N) { return tok < ns || (tok >= w0 && tok < N); }
+
+// Byte offset of token t inside a K/V tile that TMA filled with swizzled boxes
+// of (1 << btl) tokens x D columns, laid out [box][64-column block][token][128 bytes].
+template <int D>
+__device__ __forceinline__ uint32_t row_base(int t, int btl)
+{
+    const int b = t >> btl, s = t & ((1 << btl) - 1);
+    return (uint32_t)(((b << btl) * (D / 64) + s) * 128);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// ---------------------------------------------------------------- producer
+
+template <int D, bool QUANT>
+__device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const AttendParams &p,
+                                             uint32_t sbase, uint8_t *basep, int4 *meta, uint32_t full0, uint32_t empty0)
+{
+    using L = Layout<D, QUANT>;
+    using Q = QuantLayout<D>;
+    const int lane = threadIdx.x & 31;
+    const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
+    const int tbl = p.tb_log2, tb = 1 << tbl;
+    const int nbl = 6 - tbl;  // log2 of the blocks per tile
+    const uint32_t blk_bytes = QUANT ? (uint32_t)Q::bytes(tb) : (uint32_t)(tb * D * 2);
+    const uint64_t pol = l2_evict_first_policy();
+
+    // the line of tiles and this CTA's run of it
+    long long W = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        const int len = p.seq_lens[i];
+        if (cta == 0 && (len < 0 || len > p.len_cap))
+            report_error(p.ws, len < 0 ? kErrNegLen : kErrTooLong, i, len, p.len_cap);
+        W += row_span(p, len).T;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        W += __shfl_xor_sync(0xffffffffu, W, o);
+    W *= p.Hkv;
+    const long long chunk = max((W + grid - 1) / grid, 1ll);
+    const long long start = cta * chunk, end = min(start + chunk, W);
+
+    int stage = 0;
+    uint32_t ph = 0, pend = 0, pend_par = 0;
+    bool ok = true;
+    if (start < end) {
+        // rows [wb, wb + 32), one per lane; row_start: line index of the current row
+        int wb = 0, cur = 0;
+        long long row_start = 0;
+        RowSpan mine;
+        for (; wb < p.B; wb += 32) {  // ends earlier: the run starts inside the line
+            mine = row_span(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
+            int incl = mine.T;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += y;
+            }
+            const int tot = __shfl_sync(0xffffffffu, incl, 31);
+            if (start < row_start + (long long)tot * p.Hkv) {
+                const unsigned m = __ballot_sync(0xffffffffu, start < row_start + (long long)incl * p.Hkv);
+                cur = __ffs(m) - 1;
+                row_start += (long long)__shfl_sync(0xffffffffu, incl - mine.T, cur) * p.Hkv;
+                break;
+            }
+            row_start += (long long)tot * p.Hkv;
+        }
+        long long f = start;
+        RowSpan rs;
+        auto take = [&](int src) {
+            rs.N = __shfl_sync(0xffffffffu, mine.N, src);
+            rs.ns = __shfl_sync(0xffffffffu, mine.ns, src);
+            rs.w0 = __shfl_sync(0xffffffffu, mine.w0, src);
+            rs.a = __shfl_sync(0xffffffffu, mine.a, src);
+            rs.b = __shfl_sync(0xffffffffu, mine.b, src);
+            rs.T = __shfl_sync(0xffffffffu, mine.T, src);
+        };
+        take(cur);
+        int h = rs.T > 0 ? (int)((f - row_start) / rs.T) : 0;
+        while (f < end && ok && rs.T > 0) {
+            const int i = wb + cur;
+            const long long u0 = row_start + (long long)h * rs.T, u1 = u0 + rs.T;
+            const int k0 = (int)(f - u0), k1 = (int)(min(u1, end) - u0);
+            const int c0 = u0 >= start ? cta : (int)(u0 / chunk), c1 = u1 <= end ? cta : (int)((u1 - 1) / chunk);
+            const int slot = c0 == c1 ? -1 : cta == c0 ? 2 * cta + 1 : 2 * cta;
+            // Block-table entries: lane l holds block l & (2^nbl - 1) of the batch's tile
+            // l >> nbl, a batch ahead of the copies; -1: nothing visible in it, num_pages: bad id.
+            auto page_of = [&](int kb) {
+                const int k = kb + (lane >> nbl);
+                if (k >= k1)
+                    return -1;
+                const int tok = rs.tile(k) * kTile + ((lane & ((1 << nbl) - 1)) << tbl);
+                if (!(tok < rs.ns || (tok + tb > rs.w0 && tok < rs.N)))
+                    return -1;
+                const int pg = p.bt[(int64_t)i * p.bt_stride + (tok >> p.log2P)];
+                if (pg < 0 || pg >= p.num_pages) {
+                    report_error(p.ws, kErrBadPage, i, tok >> p.log2P, pg);
+                    return p.num_pages;
+                }
+                return pg;
+            };
+            int pid = page_of(k0), pnx = -1;
+            for (int k = k0; k < k1; ++k) {
+                const int in_batch = (k - k0) & ((32 >> nbl) - 1);
+                if (in_batch == 0) {
+                    if (k != k0)
+                        pid = pnx;
+                    pnx = page_of(k + (32 >> nbl));
+                }
+                const int tok0 = rs.tile(k) * kTile;
+                const uint32_t full = full0 + stage * 8;
+                if (!__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
+                    report_error(p.ws, kErrTimeout, cta, stage, 0);
+                    ok = false;
+                    break;
+                }
+                pend &= ~(1u << stage);
+                const uint32_t dst = sbase + stage * L::kStageBytes;
+                const bool mine_now = (lane >> nbl) == in_batch && pid >= 0;
+                const int b = lane & ((1 << nbl) - 1);
+                const bool bad = QUANT && mine_now && pid == p.num_pages;
+                if (bad) {  // a bad page reads as zeros: zero params make every code 0
+                    uint8_t *blk = basep + (dst - sbase) + b * blk_bytes;
+                    for (int x = 0; x < tb * Q::kParamRow; x += 4) {
+                        *reinterpret_cast<uint32_t *>(blk + Q::k_params(tb) + x) = 0;
+                        *reinterpret_cast<uint32_t *>(blk + Q::v_params(tb) + x) = 0;
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();  // lane 0's arrival publishes the zeros
+                const int copies = __popc(__ballot_sync(0xffffffffu, mine_now && !bad));
+                if (lane == 0) {
+                    const bool whole = rs.ns >= tok0 + kTile || (tok0 >= rs.w0 && tok0 + kTile <= rs.N);
+                    const int flags = (k == k0 ? kFirst : 0) | (k == k1 - 1 ? kLast : 0) | (whole ? 0 : kMasked);
+                    meta[2 * stage] = make_int4(i * p.Hkv + h, tok0, flags, slot);
+                    meta[2 * stage + 1] = make_int4(rs.ns, rs.w0, rs.N, c0 | ((c1 - c0) << 16));
+                    mbar_arrive_expect_tx(full, copies * blk_bytes * (QUANT ? 1 : 2) +
+                                                    (k == k0 ? (uint32_t)(p.G * D * 2) : 0u));
+                    if (k == k0)
+                        bulk_load(dst + L::kKvBytes, p.q + ((int64_t)i * p.Hq + h * p.G) * D, p.G * D * 2, full, pol);
+                }
+                __syncwarp();
+                if (mine_now && !bad) {
+                    const int slot_in = (tok0 + (b << tbl)) & ((1 << p.log2P) - 1);
+                    if constexpr (QUANT) {
+                        bulk_load(dst + b * blk_bytes,
+                                  p.cache + ((int64_t)pid * p.Hkv + h) * p.page_head_bytes +
+                                      (int64_t)(slot_in >> tbl) * blk_bytes,
+                                  blk_bytes, full, pol);
+                    } else {
+                        tma_load_5d(dst + b * blk_bytes, tmK, full, 0, slot_in, 0, h, pid, pol);
+                        tma_load_5d(dst + L::kTileBytes + b * blk_bytes, tmV, full, 0, slot_in, 0, h, pid, pol);
+                    }
+                }
+                pend |= 1u << stage;
+                pend_par = (pend_par & ~(1u << stage)) | (ph << stage);
+                if (++stage == L::kStages) {
+                    stage = 0;
+                    ph ^= 1;
+                }
+            }
+            f = u0 + k1;
+            if (++h == p.Hkv && f < end) {  // the next row with visible tokens
+                row_start += (long long)rs.T * p.Hkv;
+                h = 0;
+                unsigned m = __ballot_sync(0xffffffffu, mine.T > 0 && lane > cur);
+                while (!m && wb < p.B) {
+                    wb += 32;
+                    mine = row_span(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
+                    m = __ballot_sync(0xffffffffu, mine.T > 0);
+                }
+                if (!m)
+                    break;  // the lengths changed under the launch
+                cur = __ffs(m) - 1;
+                take(cur);
+            }
+        }
+    }
+    if (ok) {
+        if (__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
+            pend &= ~(1u << stage);
+            if (lane == 0) {
+                meta[2 * stage] = make_int4(0, 0, kEnd, 0);
+                mbar_arrive(full0 + stage * 8);
+            }
+        } else {
+            report_error(p.ws, kErrTimeout, cta, stage, 1);
+            ok = false;
+        }
+    }
+    if (!ok && lane == 0)  // let every copy this CTA issued land before its shared memory goes away
+        for (int s = 0; s < L::kStages; ++s)
+            if (pend & (1u << s))
+                mbar_wait(full0 + s * 8, (pend_par >> s) & 1u, kDrainNs);
+}
+
+// ---------------------------------------------------------------- consumers
+
+// All consumer warps meet (bounded); what each wrote before is visible after.
+__device__ __forceinline__ bool meet(uint32_t bar, uint32_t &phase)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, kWaitNs));
+    phase ^= 1;
+    return ok;
+}
+
+// The state of one warp for the 8 heads of a piece: lane (r0, h0 / 2) holds
+// heads h0, h0 + 1 and dims 16 x + r0, 16 x + r0 + 8.
+template <int D>
+struct State {
+    static constexpr int KS = D / 16;
+    float m0, m1, l0, l1, O[KS][4];
+    __device__ __forceinline__ void clear()
+    {
+        m0 = m1 = kNoMax;
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < KS; ++x)
+            O[x][0] = O[x][1] = O[x][2] = O[x][3] = 0.f;
+    }
+};
+
+// Scores x0, x1 (token r0, heads h0 and h0 + 1) and x2, x3 (token r0 + 8), in
+// log2 units, enter the running softmax; returns their weights as the B
+// operands of the PV product.  The weights are rounded to fp16, the tensor
+// cores' operand type, which costs o about as much as its own rounding; their
+// sum is kept in fp32 before that rounding.
+template <int D>
+__device__ __forceinline__ void softmax_step(State<D> &st, float x0, float x1, float x2, float x3, uint32_t &P0, uint32_t &P1)
+{
+    const float a = fmaxf(x0, x2), b = fmaxf(x1, x3);
+    if (__any_sync(0xffffffffu, a > st.m0 + kMaxSlack || b > st.m1 + kMaxSlack)) {
+        float n0 = fmaxf(a, st.m0), n1 = fmaxf(b, st.m1);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+        }
+        const float f0 = ex2(st.m0 - n0), f1 = ex2(st.m1 - n1);
+        st.m0 = n0;
+        st.m1 = n1;
+        st.l0 *= f0;
+        st.l1 *= f1;
+#pragma unroll
+        for (int x = 0; x < State<D>::KS; ++x) {
+            st.O[x][0] *= f0;
+            st.O[x][1] *= f1;
+            st.O[x][2] *= f0;
+            st.O[x][3] *= f1;
+        }
+    }
+    const float p0 = ex2(x0 - st.m0), p1 = ex2(x1 - st.m1), p2 = ex2(x2 - st.m0), p3 = ex2(x3 - st.m1);
+    st.l0 += p0 + p2;
+    st.l1 += p1 + p3;
+    P0 = movmatrix_t(pack_half2(p0, p1));
+    P1 = movmatrix_t(pack_half2(p2, p3));
+}
+
+// One tile of the fp16 pages: this warp's 16 tokens, of which `vis` (a bit per
+// token) are visible.
+template <int D>
+__device__ __forceinline__ void fp16_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], uint32_t kt, uint8_t *ktp, uint32_t vis,
+                                          int w, int btl, float sl2)
+{
+    constexpr int KS = D / 16;
+    const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7, r0 = lane >> 2;
+    const uint32_t blk = 128u << btl;
+    const uint32_t vt = kt + kTile * D * 2;
+    const uint32_t rowK = row_base<D>(16 * w + (mi & 1) * 8 + r8, btl), rowV = row_base<D>(16 * w + (mi >> 1) * 8 + r8, btl);
+    if (vis != 0xffffu) {
+        // masked rows hold anything: zero them in V so that p = 0 meets no NaN
+        uint8_t *vtp = ktp + kTile * D * 2;
+        for (int x = lane; x < 16 * (D / 8); x += 32) {
+            const int tok = 16 * w + x / (D / 8), c = x % (D / 8);
+            if (!(vis >> (tok & 15) & 1))
+                *reinterpret_cast<int4 *>(vtp + row_base<D>(tok, btl) + (c >> 3) * blk + (((c & 7) ^ (tok & 7)) << 4)) =
+                    make_int4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    }
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+        const uint32_t cc = (uint32_t)((((2 * x) & 7) + (mi >> 1)) ^ r8) << 4;
+        uint32_t a0, a1, a2, a3;
+        ldsm_x4(kt + rowK + (x >> 2) * blk + cc, a0, a1, a2, a3);
+        mma_16816(x & 1 ? sb : sa, a0, a1, a2, a3, qf[x][0], qf[x][1]);
+    }
+    const bool v0 = vis >> r0 & 1, v1 = vis >> (r0 + 8) & 1;
+    uint32_t P0, P1;
+    softmax_step<D>(st, v0 ? (sa[0] + sb[0]) * sl2 : -INFINITY, v0 ? (sa[1] + sb[1]) * sl2 : -INFINITY,
+                    v1 ? (sa[2] + sb[2]) * sl2 : -INFINITY, v1 ? (sa[3] + sb[3]) * sl2 : -INFINITY, P0, P1);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+        const uint32_t cc = (uint32_t)((((2 * x) & 7) + (mi & 1)) ^ r8) << 4;
+        uint32_t a0, a1, a2, a3;
+        ldsm_x4_t(vt + rowV + (x >> 2) * blk + cc, a0, a1, a2, a3);
+        mma_16816(st.O[x], a0, a1, a2, a3, P0, P1);
+    }
+}
+
+template <int GR>
+__device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[GR])
+{
+    if constexpr (GR == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    }
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+
+// One tile of the 4-bit cache: codes go from shared memory to the fragments of
+// the tensor cores' A operand in registers (see quant_format.cuh).
+template <int D>
+__device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], const uint8_t *kv, uint32_t vis, int w,
+                                           int tbl, float sl2)
 {
     using Q = QuantLayout<D>;
-    constexpr int CH = D / 8;
-    __shared__ __align__(16) __half s_k[kTile][D + 8], s_v[kTile][D + 8];
-    __shared__ __align__(16) __half s_q[8][D];
-    __shared__ float s_p[8][kTile], s_m[8], s_l[8], s_a[8];
-    pdl_wait();
-    pdl_trigger();
-    const int i = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, tid = threadIdx.x;
-    int N = p.seq_lens[i];
-    if (N < 0 || N > p.len_cap) {
-        if (h == 0 && tid == 0)
-            report_error(p.ws, N < 0 ? kErrNegLen : kErrTooLong, i, N, p.len_cap);
-        N = N < 0 ? 0 : p.len_cap;
+    constexpr int GR = Q::GR;
+    const int lane = threadIdx.x & 31, r0 = lane >> 2, t = lane & 3;
+    const int tb = 1 << tbl;
+    // the warp's two groups of eight tokens
+    const uint8_t *blk[2];
+    int in[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int tok = 16 * w + 8 * u;
+        blk[u] = kv + (tok >> tbl) * Q::bytes(tb);
+        in[u] = tok & (tb - 1);
     }
-    const int ns = min(p.sinks, N), w0 = max(ns, N - p.window), nv = ns + (N - w0);
-    for (int x = tid; x < p.G * CH; x += kThreads)
-        reinterpret_cast<uint4 *>(s_q)[x] = reinterpret_cast<const uint4 *>(p.q + ((int64_t)i * p.Hq + h * p.G) * D)[x];
-    if (tid < 8) {
-        s_m[tid] = -INFINITY;
-        s_l[tid] = 0.f;
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+        uint32_t k0[GR], k1[GR], c0[GR], c1[GR];
+        lds_words<GR>(blk[0] + (in[0] + r0) * Q::kRow + t * GR * 4, k0);
+        lds_words<GR>(blk[1] + (in[1] + r0) * Q::kRow + t * GR * 4, k1);
+        lds_words<GR>(blk[0] + Q::k_params(tb) + (in[0] + r0) * Q::kParamRow, c0);  // s of GR groups, then b
+        lds_words<GR>(blk[1] + Q::k_params(tb) + (in[1] + r0) * Q::kParamRow, c1);
+#pragma unroll
+        for (int j = 0; j < GR; ++j) {
+            const __half2 s0 = as_half2(c0[j >> 1]), b0 = as_half2(c0[(GR + j) >> 1]);
+            const __half2 s1 = as_half2(c1[j >> 1]), b1 = as_half2(c1[(GR + j) >> 1]);
+            const __half2 s0j = (j & 1) ? __high2half2(s0) : __low2half2(s0), b0j = (j & 1) ? __high2half2(b0) : __low2half2(b0);
+            const __half2 s1j = (j & 1) ? __high2half2(s1) : __low2half2(s1), b1j = (j & 1) ? __high2half2(b1) : __low2half2(b1);
+            mma_16816(sa, quant_value(quant_field<0>(k0[j]), s0j, b0j), quant_value(quant_field<0>(k1[j]), s1j, b1j),
+                      quant_value(quant_field<1>(k0[j]), s0j, b0j), quant_value(quant_field<1>(k1[j]), s1j, b1j),
+                      qf[2 * j][0], qf[2 * j][1]);
+            mma_16816(sb, quant_value(quant_field<2>(k0[j]), s0j, b0j), quant_value(quant_field<2>(k1[j]), s1j, b1j),
+                      quant_value(quant_field<3>(k0[j]), s0j, b0j), quant_value(quant_field<3>(k1[j]), s1j, b1j),
+                      qf[2 * j + 1][0], qf[2 * j + 1][1]);
+        }
     }
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // dim tid of each head (tid < D)
-    for (int v0 = 0; v0 < nv; v0 += kTile) {
-        __syncthreads();
-        const int n = min(kTile, nv - v0);
-        for (int x = tid; x < kTile * CH * 2; x += kThreads) {
-            const int side = x & 1, c = (x >> 1) % CH, t = (x >> 1) / CH;
-            uint32_t out[4] = {0, 0, 0, 0};
-            if (t < n) {
-                const int vis = v0 + t, pos = vis < ns ? vis : vis - ns + w0;
-                const int page = p.bt[(int64_t)i * p.bt_stride + (pos >> p.log2P)];
-                const int slot = pos & ((1 << p.log2P) - 1);
-                if (page < 0 || page >= p.num_pages) {
-                    report_error(p.ws, kErrBadPage, i, pos >> p.log2P, page);
-                } else if (!QUANT) {
-                    const uint4 u = reinterpret_cast<const uint4 *>(
-                        (side ? p.v : p.k) + ((((int64_t)page << p.log2P) + slot) * p.Hkv + h) * D)[c];
-                    out[0] = u.x;
-                    out[1] = u.y;
-                    out[2] = u.z;
-                    out[3] = u.w;
-                } else {
-                    const int tb = 1 << p.tb_log2, r = slot & (tb - 1), t2 = (r & 7) >> 1, e = r & 1, j = c >> 2, f = c & 3;
-                    const uint8_t *blk = p.cache + ((int64_t)page * p.Hkv + h) * p.page_head_bytes +
-                                         (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
-                    const __half *par = side == 0
-                        ? reinterpret_cast<const __half *>(blk + Q::k_params(tb)) + r * 2 * Q::GR + j
-                        : reinterpret_cast<const __half *>(blk + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup) +
-                              (t2 * Q::GR + j) * 4 + e;
-                    const __half2 s2 = __half2half2(par[0]), b2 = __half2half2(par[side == 0 ? Q::GR : 2]);
-                    const uint16_t *vc = reinterpret_cast<const uint16_t *>(blk + Q::v_codes(tb) + (r >> 3) * Q::kVGroup);
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t w;
-                        if (side == 0)
-                            w = reinterpret_cast<const uint32_t *>(blk)[r * (D / 8) + u * Q::GR + j];
-                        else
-                            w = (uint32_t)vc[((2 * u * 4 + t2) * Q::GR + j) * 2 + e] |
-                                (uint32_t)vc[(((2 * u + 1) * 4 + t2) * Q::GR + j) * 2 + e] << 16;
-                        const uint32_t n16 = f == 0 ? quant_field<0>(w) : f == 1 ? quant_field<1>(w)
-                                             : f == 2 ? quant_field<2>(w) : quant_field<3>(w);
-                        out[u] = quant_value(n16, s2, b2);
+    float x0 = (sa[0] + sb[0]) * sl2, x1 = (sa[1] + sb[1]) * sl2, x2 = (sa[2] + sb[2]) * sl2, x3 = (sa[3] + sb[3]) * sl2;
+    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // masked tokens' V params become 0: their values are 0, whatever the page holds
+    if (vis != 0xffffu) {
+        if (!(vis >> r0 & 1))
+            x0 = x1 = -INFINITY;
+        if (!(vis >> (r0 + 8) & 1))
+            x2 = x3 = -INFINITY;
+        const uint32_t a = vis >> (2 * t), b = vis >> (8 + 2 * t);
+        keep0 = ((a & 1) ? 0xffffu : 0u) | ((a & 2) ? 0xffff0000u : 0u);
+        keep1 = ((b & 1) ? 0xffffu : 0u) | ((b & 2) ? 0xffff0000u : 0u);
+    }
+    uint32_t v0[GR], v1[GR], c0[2 * GR], c1[2 * GR];
+    lds_words<GR>(blk[0] + Q::v_codes(tb) + (in[0] >> 3) * Q::kVGroup + lane * GR * 4, v0);
+    lds_words<GR>(blk[1] + Q::v_codes(tb) + (in[1] >> 3) * Q::kVGroup + lane * GR * 4, v1);
+    {
+        const uint8_t *a = blk[0] + Q::v_params(tb) + (in[0] >> 3) * Q::kVParamGroup + t * GR * 8;
+        const uint8_t *b = blk[1] + Q::v_params(tb) + (in[1] >> 3) * Q::kVParamGroup + t * GR * 8;
+#pragma unroll
+        for (int j = 0; j < GR; j += 2) {
+            uint32_t x[4];
+            lds_words<4>(a + j * 8, x);
+            c0[2 * j] = x[0] & keep0, c0[2 * j + 1] = x[1] & keep0, c0[2 * j + 2] = x[2] & keep0, c0[2 * j + 3] = x[3] & keep0;
+            lds_words<4>(b + j * 8, x);
+            c1[2 * j] = x[0] & keep1, c1[2 * j + 1] = x[1] & keep1, c1[2 * j + 2] = x[2] & keep1, c1[2 * j + 3] = x[3] & keep1;
+        }
+    }
+    uint32_t P0, P1;
+    softmax_step<D>(st, x0, x1, x2, x3, P0, P1);
+#pragma unroll
+    for (int j = 0; j < GR; ++j) {
+        const __half2 s0 = as_half2(c0[2 * j]), b0 = as_half2(c0[2 * j + 1]);
+        const __half2 s1 = as_half2(c1[2 * j]), b1 = as_half2(c1[2 * j + 1]);
+        mma_16816(st.O[2 * j], quant_value(quant_field<0>(v0[j]), s0, b0), quant_value(quant_field<1>(v0[j]), s0, b0),
+                  quant_value(quant_field<0>(v1[j]), s1, b1), quant_value(quant_field<1>(v1[j]), s1, b1), P0, P1);
+        mma_16816(st.O[2 * j + 1], quant_value(quant_field<2>(v0[j]), s0, b0), quant_value(quant_field<3>(v0[j]), s0, b0),
+                  quant_value(quant_field<2>(v1[j]), s1, b1), quant_value(quant_field<3>(v1[j]), s1, b1), P0, P1);
+    }
+}
+
+// The states of a (row, head)'s pieces, merged in piece order by the CTA that
+// finished last: warp w takes heads w, w + 4.
+template <int D>
+__device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, int c0, int n)
+{
+    constexpr int VPL = D / 32, kBatch = 8;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t slots = 2 * kAttnMaxCtas;
+    const float *pm = p.partials + slots * p.G * D, *pl = pm + slots * p.G;
+    for (int g = w; g < p.G; g += kCW) {
+        float M = kNoMax, Lsum = 0.f, acc[VPL];
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            acc[v] = 0.f;
+        for (int j0 = 0; j0 < n; j0 += kBatch) {
+            float mj[kBatch], lj[kBatch], x[kBatch][VPL];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                mj[u] = kNoMax;
+                lj[u] = 0.f;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    x[u][v] = 0.f;
+                const int j = j0 + u;
+                if (j < n) {
+                    const int64_t s = (int64_t)(j == 0 ? 2 * c0 + 1 : 2 * (c0 + j)) * p.G + g;
+                    mj[u] = __ldcg(pm + s);
+                    lj[u] = __ldcg(pl + s);
+                    if constexpr (VPL == 4) {
+                        const float4 t = __ldcg(reinterpret_cast<const float4 *>(p.partials + s * D) + lane);
+                        x[u][0] = t.x, x[u][1] = t.y, x[u][2] = t.z, x[u][3] = t.w;
+                    } else {
+                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(p.partials + s * D) + lane);
+                        x[u][0] = t.x, x[u][1] = t.y;
                     }
                 }
             }
-            *reinterpret_cast<uint4 *>(side ? &s_v[t][c * 8] : &s_k[t][c * 8]) = make_uint4(out[0], out[1], out[2], out[3]);
-        }
-        __syncthreads();
-        for (int x = tid; x < p.G * kTile; x += kThreads) {
-            const int g = x / kTile, t = x % kTile;
-            float s = 0.f;
-            for (int e = 0; e < D; ++e)
-                s += __half2float(s_q[g][e]) * __half2float(s_k[t][e]);
-            s_p[g][t] = t < n ? s * p.scale_log2 : -INFINITY;
-        }
-        __syncthreads();
-        if (tid < p.G) {
-            float m = s_m[tid];
-            for (int t = 0; t < n; ++t)
-                m = fmaxf(m, s_p[tid][t]);
-            const float a = m == -INFINITY ? 1.f : ex2(s_m[tid] - m);
-            float l = s_l[tid] * a;
-            for (int t = 0; t < kTile; ++t) {
-                const float e = m == -INFINITY ? 0.f : ex2(s_p[tid][t] - m);
-                s_p[tid][t] = e;
-                l += e;
+            float mn = M;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                mn = fmaxf(mn, mj[u]);
+            const float so = ex2(M - mn);
+            M = mn;
+            Lsum *= so;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                acc[v] *= so;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float sj = ex2(mj[u] - mn);
+                Lsum += lj[u] * sj;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    acc[v] += x[u][v] * sj;
             }
-            s_m[tid] = m;
-            s_l[tid] = l;
-            s_a[tid] = a;
         }
-        __syncthreads();
-        if (tid < D)
-            for (int g = 0; g < p.G; ++g) {
-                float y = acc[g] * s_a[g];
-                for (int t = 0; t < n; ++t)
-                    y += s_p[g][t] * __half2float(s_v[t][tid]);
-                acc[g] = y;
-            }
+        const float inv = 1.f / Lsum;
+        const int64_t oh = (int64_t)unit * p.G + g;  // unit = row * Hkv + head
+        __half *out = p.o + oh * D + lane * VPL;
+        if constexpr (VPL == 4)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv), pack_half2(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(out) = pack_half2(acc[0] * inv, acc[1] * inv);
+        if (p.lse && lane == 0)
+            p.lse[oh] = (M + log2f(Lsum)) * kLn2;
     }
-    __syncthreads();
-    if (tid < D)
-        for (int g = 0; g < p.G; ++g)
-            p.o[((int64_t)i * p.Hq + h * p.G + g) * D + tid] = __float2half_rn(nv > 0 ? acc[g] / s_l[g] : 0.f);
-    if (p.lse && tid < p.G)
-        p.lse[(int64_t)i * p.Hq + h * p.G + tid] = nv > 0 ? (s_m[tid] + log2f(s_l[tid])) * kLn2 : -INFINITY;
+}
+
+// A piece's end: the four warps' states become one, each warp merging its
+// quarter of the dims, and go to o and lse or to the piece's slot.
+template <int D>
+__device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st, uint8_t *stage, float *red, int *s_last,
+                                             uint32_t cbar, uint32_t &cph, uint32_t empty, int4 mt, int4 mt2)
+{
+    constexpr int KS = D / 16, KQ = KS / kCW;  // 16-dim blocks a warp merges
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = lane >> 2, h0 = 2 * (lane & 3);
+    const int G = p.G;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
+        st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
+    }
+    if (lane < 4) {
+        red[w * 16 + h0] = st.m0;
+        red[w * 16 + h0 + 1] = st.m1;
+        red[w * 16 + 8 + h0] = st.l0;
+        red[w * 16 + 8 + h0 + 1] = st.l1;
+    }
+    if (!meet(cbar, cph))  // every warp has read the stage's tile
+        return false;
+    // block x of warp w goes to its owner x / KQ: [owner][writer slot][block][lane] float4
+    float4 *ex = reinterpret_cast<float4 *>(stage);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+        const int own = x / KQ;
+        if (own != w)
+            ex[((own * (kCW - 1) + (w - (w > own))) * KQ + x % KQ) * 32 + lane] =
+                make_float4(st.O[x][0], st.O[x][1], st.O[x][2], st.O[x][3]);
+    }
+    if (!meet(cbar, cph))
+        return false;
+    float M0 = kNoMax, M1 = kNoMax, L0 = 0.f, L1 = 0.f;
+#pragma unroll
+    for (int v = 0; v < kCW; ++v) {
+        M0 = fmaxf(M0, red[v * 16 + h0]);
+        M1 = fmaxf(M1, red[v * 16 + h0 + 1]);
+    }
+    float f0[kCW], f1[kCW];
+#pragma unroll
+    for (int v = 0; v < kCW; ++v) {
+        f0[v] = ex2(red[v * 16 + h0] - M0);
+        f1[v] = ex2(red[v * 16 + h0 + 1] - M1);
+        L0 += red[v * 16 + 8 + h0] * f0[v];
+        L1 += red[v * 16 + 8 + h0 + 1] * f1[v];
+    }
+    float R[KQ][4];
+#pragma unroll
+    for (int y = 0; y < KQ; ++y) {
+        R[y][0] = R[y][1] = R[y][2] = R[y][3] = 0.f;
+#pragma unroll
+        for (int v = 0; v < kCW; ++v) {
+            float4 s;
+            if (v == w) {
+#pragma unroll
+                for (int ww = 0; ww < kCW; ++ww)  // static indexing of the register state
+                    if (ww == w)
+                        s = make_float4(st.O[ww * KQ + y][0], st.O[ww * KQ + y][1], st.O[ww * KQ + y][2], st.O[ww * KQ + y][3]);
+            } else {
+                s = ex[((w * (kCW - 1) + (v - (v > w))) * KQ + y) * 32 + lane];
+            }
+            R[y][0] += s.x * f0[v];
+            R[y][1] += s.y * f1[v];
+            R[y][2] += s.z * f0[v];
+            R[y][3] += s.w * f1[v];
+        }
+    }
+    fence_proxy_async_smem();  // the stage is refilled by bulk copies
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(empty);
+    const int unit = mt.x, slot = mt.w;
+    const bool ok0 = h0 < G, ok1 = h0 + 1 < G;
+    if (slot < 0) {
+        const float i0 = 1.f / L0, i1 = 1.f / L1;
+        __half *out = p.o + (int64_t)unit * G * D;
+#pragma unroll
+        for (int y = 0; y < KQ; ++y) {
+            const int d0 = 16 * (w * KQ + y) + r0;
+            if (ok0) {
+                out[h0 * D + d0] = __float2half_rn(R[y][0] * i0);
+                out[h0 * D + d0 + 8] = __float2half_rn(R[y][2] * i0);
+            }
+            if (ok1) {
+                out[(h0 + 1) * D + d0] = __float2half_rn(R[y][1] * i1);
+                out[(h0 + 1) * D + d0 + 8] = __float2half_rn(R[y][3] * i1);
+            }
+        }
+        if (p.lse && w == 0 && lane < 4) {
+            if (ok0)
+                p.lse[(int64_t)unit * G + h0] = (M0 + log2f(L0)) * kLn2;
+            if (ok1)
+                p.lse[(int64_t)unit * G + h0 + 1] = (M1 + log2f(L1)) * kLn2;
+        }
+        return true;
+    }
+    {
+        float *acc = p.partials + (int64_t)slot * G * D;
+#pragma unroll
+        for (int y = 0; y < KQ; ++y) {
+            const int d0 = 16 * (w * KQ + y) + r0;
+            if (ok0) {
+                acc[h0 * D + d0] = R[y][0];
+                acc[h0 * D + d0 + 8] = R[y][2];
+            }
+            if (ok1) {
+                acc[(h0 + 1) * D + d0] = R[y][1];
+                acc[(h0 + 1) * D + d0 + 8] = R[y][3];
+            }
+        }
+        if (w == 0 && lane < 4) {
+            const int64_t slots = 2 * kAttnMaxCtas;
+            float *pm = p.partials + slots * G * D + (int64_t)slot * G, *pl = pm + slots * G;
+            if (ok0) {
+                pm[h0] = M0;
+                pl[h0] = L0;
+            }
+            if (ok1) {
+                pm[h0 + 1] = M1;
+                pl[h0 + 1] = L1;
+            }
+        }
+    }
+    const int c0 = mt2.w & 0xffff, n = (mt2.w >> 16) + 1;
+    __threadfence();
+    if (!meet(cbar, cph))
+        return false;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        *s_last = atomicAdd(p.counters + c0, 1) == n - 1;
+        if (*s_last)
+            p.counters[c0] = 0;  // ready for the next launch
+        __threadfence();
+    }
+    if (!meet(cbar, cph))
+        return false;
+    if (*s_last)
+        merge_pieces<D>(p, unit, c0, n);
+    return true;
 }
 
 template <int D, bool QUANT>
-cudaError_t launch_one(const AttendParams &p, cudaStream_t s)
+__device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sbase, uint8_t *basep, const int4 *meta,
+                                             uint32_t full0, uint32_t empty0, uint32_t cbar, int *s_last)
 {
+    using L = Layout<D, QUANT>;
+    constexpr int KS = D / 16;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = lane >> 2;
+    // two buffers: a warp may reach the next piece's end while another still reads this one's
+    float *red = reinterpret_cast<float *>(basep + L::kRedOff);
+    int parity = 0;
+    State<D> st;
+    st.clear();
+    uint32_t qf[KS][2];
+    int stage = 0;
+    uint32_t ph = 0, cph = 0;
+    for (;;) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full0 + stage * 8, ph, kWaitNs))) {
+            report_error(p.ws, kErrTimeout, (int)blockIdx.x, stage, 2);
+            return;
+        }
+        const int4 mt = meta[2 * stage];
+        if (mt.z & kEnd)
+            break;
+        uint8_t *sp = basep + stage * L::kStageBytes;
+        if (mt.z & kFirst) {
+            const uint8_t *qs = sp + L::kKvBytes;
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+                qf[x][0] = qf[x][1] = 0u;
+                if (r0 < p.G) {
+                    const uint32_t *row = reinterpret_cast<const uint32_t *>(qs + r0 * D * 2);
+                    qf[x][0] = row[8 * x + (lane & 3)];
+                    qf[x][1] = row[8 * x + 4 + (lane & 3)];
+                }
+            }
+        }
+        uint32_t vis = 0xffffu;
+        int4 mt2 = make_int4(0, 0, 0, 0);
+        if (mt.z & (kMasked | kLast))
+            mt2 = meta[2 * stage + 1];
+        if (mt.z & kMasked)
+            vis = __ballot_sync(0xffffffffu, lane < 16 && visible(mt.y + 16 * w + lane, mt2.x, mt2.y, mt2.z));
+        if (vis) {
+            if constexpr (QUANT)
+                quant_tile<D>(st, qf, sp, vis, w, p.tb_log2, p.scale_log2);
+            else
+                fp16_tile<D>(st, qf, sbase + stage * L::kStageBytes, sp, vis, w, p.tb_log2, p.scale_log2);
+        }
+        __syncwarp();
+        if (mt.z & kLast) {
+            if (!finish_piece<D>(p, st, sp, red + parity * kCW * 2 * kMaxG, s_last, cbar, cph, empty0 + stage * 8, mt, mt2)) {
+                report_error(p.ws, kErrTimeout, (int)blockIdx.x, stage, 3);
+                return;
+            }
+            st.clear();
+            parity ^= 1;
+        } else if (lane == 0) {
+            mbar_arrive(empty0 + stage * 8);
+        }
+        if (++stage == L::kStages) {
+            stage = 0;
+            ph ^= 1;
+        }
+    }
+    // rows that see no token
+    for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
+        if (row_span(p, p.seq_lens[i]).T > 0)
+            continue;
+        int4 *out = reinterpret_cast<int4 *>(p.o + (int64_t)i * p.Hq * D);
+        for (int x = threadIdx.x; x < p.Hq * D / 8; x += 32 * kCW)
+            out[x] = make_int4(0, 0, 0, 0);
+        if (p.lse)
+            for (int x = threadIdx.x; x < p.Hq; x += 32 * kCW)
+                p.lse[(int64_t)i * p.Hq + x] = -INFINITY;
+    }
+}
+
+template <int D, bool QUANT>
+__global__ void __launch_bounds__(kThreads, Layout<D, QUANT>::kCtasPerSm)
+    attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendParams p)
+{
+    using L = Layout<D, QUANT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_last;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *basep = smem_raw + (sbase - raw);
+    int4 *meta = reinterpret_cast<int4 *>(basep + L::kMetaOff);
+    const uint32_t full0 = sbase + L::kBarOff, empty0 = full0 + L::kStages * 8, cbar = empty0 + L::kStages * 8;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(full0 + s * 8, 1);
+            mbar_init(empty0 + s * 8, kCW);
+        }
+        mbar_init(cbar, kCW);
+        fence_mbar_init();
+    }
+    if (!QUANT && threadIdx.x == 32 * kCW) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x >= 32 * kCW)
+        run_producer<D, QUANT>(&tmK, &tmV, p, sbase, basep, meta, full0, empty0);
+    else
+        run_consumer<D, QUANT>(p, sbase, basep, meta, full0, empty0, cbar, &s_last);
+}
+
+template <int D, bool QUANT>
+cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms, cudaStream_t s)
+{
+    using L = Layout<D, QUANT>;
+    auto kern = attend_kernel<D, QUANT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    if (e != cudaSuccess)
+        return e;
+    // no more CTAs than the longest rows could keep busy
+    const int64_t by_len = ((int64_t)p.len_cap + kTile - 1) / kTile;
+    const int64_t by_win = ((int64_t)p.window + kTile - 1) / kTile + 1 + ((int64_t)p.sinks + kTile - 1) / kTile;
+    const int64_t tiles = (int64_t)p.B * p.Hkv * (by_len < by_win ? by_len : by_win);
+    int64_t grid = (int64_t)sms * L::kCtasPerSm;
+    grid = grid < kAttnMaxCtas ? grid : kAttnMaxCtas;
+    grid = grid < tiles ? grid : tiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.B * p.Hkv);
+    cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kAlloc;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_kernel<D, QUANT>, p);
+    return cudaLaunchKernelEx(&cfg, kern, tk, tv, p);
 }
 
 }  // namespace
 
-cudaError_t launch_attend(int d, bool quant, const AttendParams &p, cudaStream_t s)
+cudaError_t launch_attend(int d, const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms, cudaStream_t s)
 {
+    const bool quant = p.cache != nullptr;
     if (d == 128)
-        return quant ? launch_one<128, true>(p, s) : launch_one<128, false>(p, s);
-    return quant ? launch_one<64, true>(p, s) : launch_one<64, false>(p, s);
+        return quant ? launch_one<128, true>(tk, tv, p, sms, s) : launch_one<128, false>(tk, tv, p, sms, s);
+    return quant ? launch_one<64, true>(tk, tv, p, sms, s) : launch_one<64, false>(tk, tv, p, sms, s);
 }
 
 }  // namespace pkv

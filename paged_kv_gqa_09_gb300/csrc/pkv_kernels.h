@@ -144,8 +144,7 @@ struct QuantReadParams {
 struct AttendParams {
     const __half *q;
     const int32_t *bt, *seq_lens;
-    const __half *k, *v;      // fp16 pages, or
-    const uint8_t *cache;     // the 4-bit cache
+    const uint8_t *cache;     // the 4-bit cache (nullptr: fp16 pages, through the tensor maps)
     WsHeader *ws;
     int32_t *counters;        // [kAttnMaxCtas], zero between launches
     float *partials;
@@ -159,7 +158,8 @@ struct AttendParams {
 
 cudaError_t launch_quant_append(int d, const QuantAppendParams &p, cudaStream_t s);
 cudaError_t launch_quant_read(int d, const QuantReadParams &p, cudaStream_t s);
-cudaError_t launch_attend(int d, bool quant, const AttendParams &p, cudaStream_t s);
+cudaError_t launch_attend(int d, const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms,
+                          cudaStream_t s);
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t s, bool pdl);
 cudaError_t launch_decode(int d, int mode, const CUtensorMap &tk, const CUtensorMap &tv,
