@@ -7,7 +7,8 @@
 // One pass over the cache: 4 d flops per visible token and query head against
 // 2.5 d bytes (4-bit) or 4 d (fp16) per token and KV head; HBM bounds it.
 //
-// Work split.  A row's visible tokens lie in T_i tiles of 64 tokens (tiles
+// Work split.  A row's visible tokens lie in T_i tiles (64 tokens of fp16
+// pages, 128 of the 4-bit cache; tiles
 // between the sinks and the window are never touched).  All tiles of the batch
 // in (row, KV head, tile) order form one line, which the CTAs cut into equal
 // runs: every CTA derives the line's length and its own run from the row
@@ -36,7 +37,6 @@ namespace pkv {
 namespace {
 
 constexpr int kCW = 4;                    // consumer warps
-constexpr int kTile = 16 * kCW;           // tokens per stage
 constexpr int kThreads = 32 * (kCW + 1);  // + producer warp
 constexpr int kMaxG = 8;
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -51,14 +51,25 @@ constexpr float kMaxSlack = 8.f;
 
 constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 
-template <int D, bool QUANT>
+// TBL: log2 of the tokens per block of the 4-bit cache, whose tiles' addresses
+// are then constants; kFp16 for the fp16 pages.
+constexpr int kFp16 = 0;
+
+template <int D, int TBL>
 struct Layout {
+    static constexpr bool QUANT = TBL != kFp16;
+    // 16-token blocks of a tile per consumer warp: with two, the 4-bit tile's
+    // barriers, flags and page lookups cost half as much per token, and one
+    // block's unpacking overlaps the other's products
+    static constexpr int MT = QUANT ? 2 : 1;
+    static constexpr int kTile = 16 * kCW * MT;       // tokens per stage
+    static constexpr int kTileLog2 = QUANT ? 7 : 6;
     static constexpr int kTileBytes = kTile * D * 2;  // fp16: one of K, V
     static constexpr int kKvBytes = QUANT ? kTile * D * 5 / 4 : 2 * kTileBytes;
     static constexpr int kQBytes = kMaxG * D * 2;
     static constexpr int kStageBytes = kKvBytes + kQBytes;
     static constexpr int kCtasPerSm = QUANT ? 3 : 2;
-    static constexpr int kStages = QUANT ? (D == 128 ? 5 : 10) : (D == 128 ? 3 : 6);
+    static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
@@ -77,6 +88,7 @@ struct RowSpan {
     __device__ __forceinline__ int tile(int k) const { return k < a ? k : b + (k - a); }
 };
 
+template <int kTile>
 __device__ __forceinline__ RowSpan row_span(const AttendParams &p, int len)
 {
     RowSpan r;
@@ -112,16 +124,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // ---------------------------------------------------------------- producer
 
-template <int D, bool QUANT>
+template <int D, int TBL>
 __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const AttendParams &p,
                                              uint32_t sbase, uint8_t *basep, int4 *meta, uint32_t full0, uint32_t empty0)
 {
-    using L = Layout<D, QUANT>;
+    using L = Layout<D, TBL>;
     using Q = QuantLayout<D>;
+    constexpr bool QUANT = L::QUANT;
+    constexpr int kTile = L::kTile;
     const int lane = threadIdx.x & 31;
     const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
-    const int tbl = p.tb_log2, tb = 1 << tbl;
-    const int nbl = 6 - tbl;  // log2 of the blocks per tile
+    const int tbl = QUANT ? TBL : p.tb_log2, tb = 1 << tbl;
+    const int nbl = L::kTileLog2 - tbl;  // log2 of the blocks per tile
     const uint32_t blk_bytes = QUANT ? (uint32_t)Q::bytes(tb) : (uint32_t)(tb * D * 2);
     const uint64_t pol = l2_evict_first_policy();
 
@@ -131,7 +145,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
         const int len = p.seq_lens[i];
         if (cta == 0 && (len < 0 || len > p.len_cap))
             report_error(p.ws, len < 0 ? kErrNegLen : kErrTooLong, i, len, p.len_cap);
-        W += row_span(p, len).T;
+        W += row_span<L::kTile>(p, len).T;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -149,7 +163,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
         long long row_start = 0;
         RowSpan mine;
         for (; wb < p.B; wb += 32) {  // ends earlier: the run starts inside the line
-            mine = row_span(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
+            mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
             int incl = mine.T;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -267,7 +281,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
                 unsigned m = __ballot_sync(0xffffffffu, mine.T > 0 && lane > cur);
                 while (!m && wb < p.B) {
                     wb += 32;
-                    mine = row_span(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
+                    mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
                     m = __ballot_sync(0xffffffffu, mine.T > 0);
                 }
                 if (!m)
@@ -324,17 +338,44 @@ struct State {
     }
 };
 
-// Scores x0, x1 (token r0, heads h0 and h0 + 1) and x2, x3 (token r0 + 8), in
-// log2 units, enter the running softmax; returns their weights as the B
-// operands of the PV product.  The weights are rounded to fp16, the tensor
-// cores' operand type, which costs o about as much as its own rounding; their
-// sum is kept in fp32 before that rounding.
-template <int D>
-__device__ __forceinline__ void softmax_step(State<D> &st, float x0, float x1, float x2, float x3, uint32_t &P0, uint32_t &P1)
+// Raw scores x[b] of MT blocks of 16 tokens -- x[b][0], x[b][1]: token r0 with
+// heads h0 and h0 + 1, x[b][2], x[b][3]: token r0 + 8; bit 16 b + token of
+// `vis` set where visible -- enter the running softmax in units of log2;
+// returns the weights as the B operands of the PV product.  The weights are
+// rounded to fp16, the tensor cores' operand type, which costs o about as much
+// as its own rounding; their sum is kept in fp32 before that rounding.
+template <int D, int MT>
+__device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][4], uint32_t vis, float sl2, uint32_t (&P)[MT][2])
 {
-    const float a = fmaxf(x0, x2), b = fmaxf(x1, x3);
-    if (__any_sync(0xffffffffu, a > st.m0 + kMaxSlack || b > st.m1 + kMaxSlack)) {
-        float n0 = fmaxf(a, st.m0), n1 = fmaxf(b, st.m1);
+    constexpr uint32_t kAll = MT == 2 ? 0xffffffffu : 0xffffu;
+    const int r0 = (threadIdx.x & 31) >> 2;
+    float y[MT][4];
+    auto scaled = [&](float m0, float m1) {
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[u][e] = fmaf(x[u][e], sl2, (e & 1) ? -m1 : -m0);
+        if (vis != kAll) {
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(vis >> (16 * u + 8 * (e >> 1) + r0) & 1))
+                        y[u][e] = -INFINITY;
+        }
+    };
+    auto most = [&](int odd) {
+        float a = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+            a = fmaxf(a, fmaxf(y[u][odd], y[u][2 + odd]));
+        return a;
+    };
+    scaled(st.m0, st.m1);
+    if (__any_sync(0xffffffffu, fmaxf(most(0), most(1)) > kMaxSlack)) {
+        scaled(0.f, 0.f);
+        float n0 = fmaxf(st.m0, most(0)), n1 = fmaxf(st.m1, most(1));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
@@ -346,18 +387,22 @@ __device__ __forceinline__ void softmax_step(State<D> &st, float x0, float x1, f
         st.l0 *= f0;
         st.l1 *= f1;
 #pragma unroll
-        for (int x = 0; x < State<D>::KS; ++x) {
-            st.O[x][0] *= f0;
-            st.O[x][1] *= f1;
-            st.O[x][2] *= f0;
-            st.O[x][3] *= f1;
+        for (int z = 0; z < State<D>::KS; ++z) {
+            st.O[z][0] *= f0;
+            st.O[z][1] *= f1;
+            st.O[z][2] *= f0;
+            st.O[z][3] *= f1;
         }
+        scaled(n0, n1);
     }
-    const float p0 = ex2(x0 - st.m0), p1 = ex2(x1 - st.m1), p2 = ex2(x2 - st.m0), p3 = ex2(x3 - st.m1);
-    st.l0 += p0 + p2;
-    st.l1 += p1 + p3;
-    P0 = movmatrix_t(pack_half2(p0, p1));
-    P1 = movmatrix_t(pack_half2(p2, p3));
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+        const float p0 = ex2(y[u][0]), p1 = ex2(y[u][1]), p2 = ex2(y[u][2]), p3 = ex2(y[u][3]);
+        st.l0 += p0 + p2;
+        st.l1 += p1 + p3;
+        P[u][0] = movmatrix_t(pack_half2(p0, p1));
+        P[u][1] = movmatrix_t(pack_half2(p2, p3));
+    }
 }
 
 // One tile of the fp16 pages: this warp's 16 tokens, of which `vis` (a bit per
@@ -366,8 +411,8 @@ template <int D>
 __device__ __forceinline__ void fp16_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], uint32_t kt, uint8_t *ktp, uint32_t vis,
                                           int w, int btl, float sl2)
 {
-    constexpr int KS = D / 16;
-    const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7, r0 = lane >> 2;
+    constexpr int KS = D / 16, kTile = Layout<D, kFp16>::kTile;
+    const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
     const uint32_t blk = 128u << btl;
     const uint32_t vt = kt + kTile * D * 2;
     const uint32_t rowK = row_base<D>(16 * w + (mi & 1) * 8 + r8, btl), rowV = row_base<D>(16 * w + (mi >> 1) * 8 + r8, btl);
@@ -391,16 +436,15 @@ __device__ __forceinline__ void fp16_tile(State<D> &st, const uint32_t (&qf)[D /
         ldsm_x4(kt + rowK + (x >> 2) * blk + cc, a0, a1, a2, a3);
         mma_16816(x & 1 ? sb : sa, a0, a1, a2, a3, qf[x][0], qf[x][1]);
     }
-    const bool v0 = vis >> r0 & 1, v1 = vis >> (r0 + 8) & 1;
-    uint32_t P0, P1;
-    softmax_step<D>(st, v0 ? (sa[0] + sb[0]) * sl2 : -INFINITY, v0 ? (sa[1] + sb[1]) * sl2 : -INFINITY,
-                    v1 ? (sa[2] + sb[2]) * sl2 : -INFINITY, v1 ? (sa[3] + sb[3]) * sl2 : -INFINITY, P0, P1);
+    const float x[1][4] = {{sa[0] + sb[0], sa[1] + sb[1], sa[2] + sb[2], sa[3] + sb[3]}};
+    uint32_t P[1][2];
+    softmax_step<D, 1>(st, x, vis, sl2, P);
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
         const uint32_t cc = (uint32_t)((((2 * x) & 7) + (mi & 1)) ^ r8) << 4;
         uint32_t a0, a1, a2, a3;
         ldsm_x4_t(vt + rowV + (x >> 2) * blk + cc, a0, a1, a2, a3);
-        mma_16816(st.O[x], a0, a1, a2, a3, P0, P1);
+        mma_16816(st.O[x], a0, a1, a2, a3, P[0][0], P[0][1]);
     }
 }
 
@@ -422,82 +466,78 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[GR])
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 
-// One tile of the 4-bit cache: codes go from shared memory to the fragments of
-// the tensor cores' A operand in registers (see quant_format.cuh).
-template <int D>
+// One tile of the 4-bit cache, of which this warp takes 32 tokens, four groups
+// of eight: codes go from shared memory to the fragments of the tensor cores' A
+// operand in registers (see quant_format.cuh).
+template <int D, int TBL>
 __device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], const uint8_t *kv, uint32_t vis, int w,
-                                           int tbl, float sl2)
+                                           float sl2)
 {
     using Q = QuantLayout<D>;
-    constexpr int GR = Q::GR;
+    constexpr int GR = Q::GR, TB = 1 << TBL, MT = 2;
     const int lane = threadIdx.x & 31, r0 = lane >> 2, t = lane & 3;
-    const int tb = 1 << tbl;
-    // the warp's two groups of eight tokens
-    const uint8_t *blk[2];
-    int in[2];
+    auto group = [&](int u) { return kv + ((32 * w + 8 * u) >> TBL) * Q::bytes(TB); };  // its block
+    auto in = [&](int u) { return (32 * w + 8 * u) & (TB - 1); };                       // its first token there
+    float x[MT][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int tok = 16 * w + 8 * u;
-        blk[u] = kv + (tok >> tbl) * Q::bytes(tb);
-        in[u] = tok & (tb - 1);
-    }
-    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-    {
+    for (int u = 0; u < MT; ++u) {
         uint32_t k0[GR], k1[GR], c0[GR], c1[GR];
-        lds_words<GR>(blk[0] + (in[0] + r0) * Q::kRow + t * GR * 4, k0);
-        lds_words<GR>(blk[1] + (in[1] + r0) * Q::kRow + t * GR * 4, k1);
-        lds_words<GR>(blk[0] + Q::k_params(tb) + (in[0] + r0) * Q::kParamRow, c0);  // s of GR groups, then b
-        lds_words<GR>(blk[1] + Q::k_params(tb) + (in[1] + r0) * Q::kParamRow, c1);
+        const uint8_t *g0 = group(2 * u), *g1 = group(2 * u + 1);
+        lds_words<GR>(g0 + (in(2 * u) + r0) * Q::kRow + t * GR * 4, k0);
+        lds_words<GR>(g1 + (in(2 * u + 1) + r0) * Q::kRow + t * GR * 4, k1);
+        lds_words<GR>(g0 + Q::k_params(TB) + (in(2 * u) + r0) * Q::kParamRow, c0);  // s of GR groups, then b
+        lds_words<GR>(g1 + Q::k_params(TB) + (in(2 * u + 1) + r0) * Q::kParamRow, c1);
+        x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < GR; ++j) {
             const __half2 s0 = as_half2(c0[j >> 1]), b0 = as_half2(c0[(GR + j) >> 1]);
             const __half2 s1 = as_half2(c1[j >> 1]), b1 = as_half2(c1[(GR + j) >> 1]);
             const __half2 s0j = (j & 1) ? __high2half2(s0) : __low2half2(s0), b0j = (j & 1) ? __high2half2(b0) : __low2half2(b0);
             const __half2 s1j = (j & 1) ? __high2half2(s1) : __low2half2(s1), b1j = (j & 1) ? __high2half2(b1) : __low2half2(b1);
-            mma_16816(sa, quant_value(quant_field<0>(k0[j]), s0j, b0j), quant_value(quant_field<0>(k1[j]), s1j, b1j),
+            mma_16816(x[u], quant_value(quant_field<0>(k0[j]), s0j, b0j), quant_value(quant_field<0>(k1[j]), s1j, b1j),
                       quant_value(quant_field<1>(k0[j]), s0j, b0j), quant_value(quant_field<1>(k1[j]), s1j, b1j),
                       qf[2 * j][0], qf[2 * j][1]);
-            mma_16816(sb, quant_value(quant_field<2>(k0[j]), s0j, b0j), quant_value(quant_field<2>(k1[j]), s1j, b1j),
+            mma_16816(x[u], quant_value(quant_field<2>(k0[j]), s0j, b0j), quant_value(quant_field<2>(k1[j]), s1j, b1j),
                       quant_value(quant_field<3>(k0[j]), s0j, b0j), quant_value(quant_field<3>(k1[j]), s1j, b1j),
                       qf[2 * j + 1][0], qf[2 * j + 1][1]);
         }
     }
-    float x0 = (sa[0] + sb[0]) * sl2, x1 = (sa[1] + sb[1]) * sl2, x2 = (sa[2] + sb[2]) * sl2, x3 = (sa[3] + sb[3]) * sl2;
-    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // masked tokens' V params become 0: their values are 0, whatever the page holds
-    if (vis != 0xffffu) {
-        if (!(vis >> r0 & 1))
-            x0 = x1 = -INFINITY;
-        if (!(vis >> (r0 + 8) & 1))
-            x2 = x3 = -INFINITY;
-        const uint32_t a = vis >> (2 * t), b = vis >> (8 + 2 * t);
-        keep0 = ((a & 1) ? 0xffffu : 0u) | ((a & 2) ? 0xffff0000u : 0u);
-        keep1 = ((b & 1) ? 0xffffu : 0u) | ((b & 2) ? 0xffff0000u : 0u);
-    }
-    uint32_t v0[GR], v1[GR], c0[2 * GR], c1[2 * GR];
-    lds_words<GR>(blk[0] + Q::v_codes(tb) + (in[0] >> 3) * Q::kVGroup + lane * GR * 4, v0);
-    lds_words<GR>(blk[1] + Q::v_codes(tb) + (in[1] >> 3) * Q::kVGroup + lane * GR * 4, v1);
-    {
-        const uint8_t *a = blk[0] + Q::v_params(tb) + (in[0] >> 3) * Q::kVParamGroup + t * GR * 8;
-        const uint8_t *b = blk[1] + Q::v_params(tb) + (in[1] >> 3) * Q::kVParamGroup + t * GR * 8;
+    uint32_t P[MT][2];
+    softmax_step<D, MT>(st, x, vis, sl2, P);
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+        uint32_t v0[GR], v1[GR], c0[2 * GR], c1[2 * GR];
+        const uint8_t *g0 = group(2 * u), *g1 = group(2 * u + 1);
+        lds_words<GR>(g0 + Q::v_codes(TB) + (in(2 * u) >> 3) * Q::kVGroup + lane * GR * 4, v0);
+        lds_words<GR>(g1 + Q::v_codes(TB) + (in(2 * u + 1) >> 3) * Q::kVGroup + lane * GR * 4, v1);
+        g0 += Q::v_params(TB) + (in(2 * u) >> 3) * Q::kVParamGroup + t * GR * 8;
+        g1 += Q::v_params(TB) + (in(2 * u + 1) >> 3) * Q::kVParamGroup + t * GR * 8;
 #pragma unroll
         for (int j = 0; j < GR; j += 2) {
-            uint32_t x[4];
-            lds_words<4>(a + j * 8, x);
-            c0[2 * j] = x[0] & keep0, c0[2 * j + 1] = x[1] & keep0, c0[2 * j + 2] = x[2] & keep0, c0[2 * j + 3] = x[3] & keep0;
-            lds_words<4>(b + j * 8, x);
-            c1[2 * j] = x[0] & keep1, c1[2 * j + 1] = x[1] & keep1, c1[2 * j + 2] = x[2] & keep1, c1[2 * j + 3] = x[3] & keep1;
+            const uint4 a = *reinterpret_cast<const uint4 *>(g0 + j * 8), b = *reinterpret_cast<const uint4 *>(g1 + j * 8);
+            c0[2 * j] = a.x, c0[2 * j + 1] = a.y, c0[2 * j + 2] = a.z, c0[2 * j + 3] = a.w;
+            c1[2 * j] = b.x, c1[2 * j + 1] = b.y, c1[2 * j + 2] = b.z, c1[2 * j + 3] = b.w;
         }
-    }
-    uint32_t P0, P1;
-    softmax_step<D>(st, x0, x1, x2, x3, P0, P1);
+        if (vis != 0xffffffffu) {
+            // masked tokens' params become 0, and with them their values, whatever the page holds
+            const uint32_t a = vis >> (16 * u + 2 * t), b = a >> 8;
+            const uint32_t keep0 = ((a & 1) ? 0xffffu : 0u) | ((a & 2) ? 0xffff0000u : 0u);
+            const uint32_t keep1 = ((b & 1) ? 0xffffu : 0u) | ((b & 2) ? 0xffff0000u : 0u);
 #pragma unroll
-    for (int j = 0; j < GR; ++j) {
-        const __half2 s0 = as_half2(c0[2 * j]), b0 = as_half2(c0[2 * j + 1]);
-        const __half2 s1 = as_half2(c1[2 * j]), b1 = as_half2(c1[2 * j + 1]);
-        mma_16816(st.O[2 * j], quant_value(quant_field<0>(v0[j]), s0, b0), quant_value(quant_field<1>(v0[j]), s0, b0),
-                  quant_value(quant_field<0>(v1[j]), s1, b1), quant_value(quant_field<1>(v1[j]), s1, b1), P0, P1);
-        mma_16816(st.O[2 * j + 1], quant_value(quant_field<2>(v0[j]), s0, b0), quant_value(quant_field<3>(v0[j]), s0, b0),
-                  quant_value(quant_field<2>(v1[j]), s1, b1), quant_value(quant_field<3>(v1[j]), s1, b1), P0, P1);
+            for (int j = 0; j < 2 * GR; ++j) {
+                c0[j] &= keep0;
+                c1[j] &= keep1;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < GR; ++j) {
+            const __half2 s0 = as_half2(c0[2 * j]), b0 = as_half2(c0[2 * j + 1]);
+            const __half2 s1 = as_half2(c1[2 * j]), b1 = as_half2(c1[2 * j + 1]);
+            mma_16816(st.O[2 * j], quant_value(quant_field<0>(v0[j]), s0, b0), quant_value(quant_field<1>(v0[j]), s0, b0),
+                      quant_value(quant_field<0>(v1[j]), s1, b1), quant_value(quant_field<1>(v1[j]), s1, b1), P[u][0], P[u][1]);
+            mma_16816(st.O[2 * j + 1], quant_value(quant_field<2>(v0[j]), s0, b0), quant_value(quant_field<3>(v0[j]), s0, b0),
+                      quant_value(quant_field<2>(v1[j]), s1, b1), quant_value(quant_field<3>(v1[j]), s1, b1), P[u][0], P[u][1]);
+        }
     }
 }
 
@@ -711,11 +751,11 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
     return true;
 }
 
-template <int D, bool QUANT>
+template <int D, int TBL>
 __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sbase, uint8_t *basep, const int4 *meta,
                                              uint32_t full0, uint32_t empty0, uint32_t cbar, int *s_last)
 {
-    using L = Layout<D, QUANT>;
+    using L = Layout<D, TBL>;
     constexpr int KS = D / 16;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = lane >> 2;
     // two buffers: a warp may reach the next piece's end while another still reads this one's
@@ -747,15 +787,16 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
                 }
             }
         }
-        uint32_t vis = 0xffffu;
+        constexpr int TW = 16 * L::MT;  // tokens of the tile for each warp
+        uint32_t vis = 0xffffffffu >> (32 - TW);
         int4 mt2 = make_int4(0, 0, 0, 0);
         if (mt.z & (kMasked | kLast))
             mt2 = meta[2 * stage + 1];
         if (mt.z & kMasked)
-            vis = __ballot_sync(0xffffffffu, lane < 16 && visible(mt.y + 16 * w + lane, mt2.x, mt2.y, mt2.z));
+            vis = __ballot_sync(0xffffffffu, lane < TW && visible(mt.y + TW * w + lane, mt2.x, mt2.y, mt2.z));
         if (vis) {
-            if constexpr (QUANT)
-                quant_tile<D>(st, qf, sp, vis, w, p.tb_log2, p.scale_log2);
+            if constexpr (L::QUANT)
+                quant_tile<D, TBL>(st, qf, sp, vis, w, p.scale_log2);
             else
                 fp16_tile<D>(st, qf, sbase + stage * L::kStageBytes, sp, vis, w, p.tb_log2, p.scale_log2);
         }
@@ -777,7 +818,7 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
     }
     // rows that see no token
     for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
-        if (row_span(p, p.seq_lens[i]).T > 0)
+        if (row_span<L::kTile>(p, p.seq_lens[i]).T > 0)
             continue;
         int4 *out = reinterpret_cast<int4 *>(p.o + (int64_t)i * p.Hq * D);
         for (int x = threadIdx.x; x < p.Hq * D / 8; x += 32 * kCW)
@@ -788,11 +829,11 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
     }
 }
 
-template <int D, bool QUANT>
-__global__ void __launch_bounds__(kThreads, Layout<D, QUANT>::kCtasPerSm)
+template <int D, int TBL>
+__global__ void __launch_bounds__(kThreads, Layout<D, TBL>::kCtasPerSm)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendParams p)
 {
-    using L = Layout<D, QUANT>;
+    using L = Layout<D, TBL>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_last;
     const uint32_t raw = smem_u32(smem_raw);
@@ -808,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, QUANT>::kCtasPerSm)
         mbar_init(cbar, kCW);
         fence_mbar_init();
     }
-    if (!QUANT && threadIdx.x == 32 * kCW) {
+    if (!L::QUANT && threadIdx.x == 32 * kCW) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
@@ -816,20 +857,21 @@ __global__ void __launch_bounds__(kThreads, Layout<D, QUANT>::kCtasPerSm)
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x >= 32 * kCW)
-        run_producer<D, QUANT>(&tmK, &tmV, p, sbase, basep, meta, full0, empty0);
+        run_producer<D, TBL>(&tmK, &tmV, p, sbase, basep, meta, full0, empty0);
     else
-        run_consumer<D, QUANT>(p, sbase, basep, meta, full0, empty0, cbar, &s_last);
+        run_consumer<D, TBL>(p, sbase, basep, meta, full0, empty0, cbar, &s_last);
 }
 
-template <int D, bool QUANT>
+template <int D, int TBL>
 cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms, cudaStream_t s)
 {
-    using L = Layout<D, QUANT>;
-    auto kern = attend_kernel<D, QUANT>;
+    using L = Layout<D, TBL>;
+    auto kern = attend_kernel<D, TBL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess)
         return e;
     // no more CTAs than the longest rows could keep busy
+    constexpr int kTile = L::kTile;
     const int64_t by_len = ((int64_t)p.len_cap + kTile - 1) / kTile;
     const int64_t by_win = ((int64_t)p.window + kTile - 1) / kTile + 1 + ((int64_t)p.sinks + kTile - 1) / kTile;
     const int64_t tiles = (int64_t)p.B * p.Hkv * (by_len < by_win ? by_len : by_win);
@@ -849,14 +891,28 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, const Atten
     return cudaLaunchKernelEx(&cfg, kern, tk, tv, p);
 }
 
+template <int D>
+cudaError_t launch_d(const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms, cudaStream_t s)
+{
+    if (!p.cache)
+        return launch_one<D, kFp16>(tk, tv, p, sms, s);
+    switch (p.tb_log2) {
+    case 3:
+        return launch_one<D, 3>(tk, tv, p, sms, s);
+    case 4:
+        return launch_one<D, 4>(tk, tv, p, sms, s);
+    case 5:
+        return launch_one<D, 5>(tk, tv, p, sms, s);
+    default:
+        return launch_one<D, 6>(tk, tv, p, sms, s);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_attend(int d, const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms, cudaStream_t s)
 {
-    const bool quant = p.cache != nullptr;
-    if (d == 128)
-        return quant ? launch_one<128, true>(tk, tv, p, sms, s) : launch_one<128, false>(tk, tv, p, sms, s);
-    return quant ? launch_one<64, true>(tk, tv, p, sms, s) : launch_one<64, false>(tk, tv, p, sms, s);
+    return d == 128 ? launch_d<128>(tk, tv, p, sms, s) : launch_d<64>(tk, tv, p, sms, s);
 }
 
 }  // namespace pkv

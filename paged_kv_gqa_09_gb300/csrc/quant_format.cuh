@@ -57,7 +57,9 @@ template <int F>
 __device__ __forceinline__ uint32_t quant_field(uint32_t w)
 {
     const uint32_t x = F == 0 ? w : F == 1 ? w << 4 : F == 2 ? w >> 4 : __byte_perm(w, 0, 0x2301);
-    return (x & 0x03c003c0u) | 0x4c004c00u;
+    uint32_t n;  // (x & mask) | 16: one instruction, which the compiler makes two of when both constants are immediates
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(n) : "r"(x), "r"(0x03c003c0u), "r"(0x4c004c00u));
+    return n;
 }
 
 // s (16 + n) + b of a packed pair, rounded once.
