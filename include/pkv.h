@@ -426,10 +426,11 @@ size_t pkv_attn_workspace_size(const pkv_shape_t *shape);
  * seq_lens_out[i] = seq_lens[i] + their number (seq_lens_out may be seq_lens,
  * or another array, which leaves seq_lens as it was).
  * total_new: rows of d_k_new / d_v_new.  Rows behind the last offset are not
- * read.  A row with a negative length, offsets outside the buffer or no room in
- * its block table is refused whole; one that meets a page id out of range
- * writes its other tokens.  Either keeps its length, and the error word records
- * the first.  New tokens of one call must not share a cache position. */
+ * read.  A row with a negative length or no room in its block table is refused
+ * whole; one that meets a page id out of range writes its other tokens.  Either
+ * keeps its length, and the error word records the first.  Offsets that do not
+ * ascend within [0, total_new] leave every row at its length.  New tokens of
+ * one call must not share a cache position. */
 int pkv_quant_append(const pkv_shape_t *shape, void *d_ws, const void *d_k_new, const void *d_v_new,
                      int64_t new_stride, int32_t total_new, const int32_t *d_new_offsets,
                      const int32_t *d_block_table, const int32_t *d_seq_lens, int32_t *d_seq_lens_out,

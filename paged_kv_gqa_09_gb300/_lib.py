@@ -127,6 +127,8 @@ def lib_path() -> str:
 def load() -> ctypes.CDLL:
     """Load libpkv.so (built by ``paged_kv_gqa_09_gb300.build.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -374,40 +374,70 @@ def pkv_attn_workspace_size(shape: Shape) -> int:
     return int(n)
 
 
-def _size(t: torch.Tensor, name: str, n: int) -> torch.Tensor:
-    if t.numel() < n:
-        raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
-    return t
+# These calls are made per layer and token, so their checks read each tensor
+# once and the current device and stream once per call.
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, dev: int, n: int) -> int:
+    """Pointer of a contiguous CUDA tensor of `dtype` with at least n elements on device `dev`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous() \
+            and t.numel() >= n:
+        return t.data_ptr()
+    _dev(t, name, dtype)  # raises unless the size is what is wrong
+    raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
 
 
-def _attn_ws(shape: Shape, ws: torch.Tensor) -> int:
-    need = pkv_attn_workspace_size(shape)
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+_attn_ws_bytes: dict = {}
+
+
+def _attn_ws(shape: Shape, ws: torch.Tensor, dev: int) -> int:
+    key = (shape.B, shape.Hq, shape.Hkv, shape.d)
+    need = _attn_ws_bytes.get(key)
+    if need is None:
+        need = pkv_attn_workspace_size(shape)
+        if len(_attn_ws_bytes) < 4096:
+            _attn_ws_bytes[key] = need
+    if not (isinstance(ws, torch.Tensor) and ws.get_device() == dev and ws.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
     if ws.numel() * ws.element_size() < need:
         raise ValueError(f"workspace has {ws.numel() * ws.element_size()} bytes, needs {need}")
-    return _ws(ws)
+    return ws.data_ptr()
 
 
-def _quant(shape: Shape, t: torch.Tensor) -> int:
-    return _dev(_size(t, "quant_cache", shape.num_pages * shape.Hkv * (shape.page_size * shape.d * 5 // 4)),
-                "quant_cache", torch.uint8)
+def _table(shape: Shape, block_table, seq_lens, dev: int) -> tuple[int, int]:
+    return (_arg(block_table, "block_table", torch.int32, dev, shape.B * shape.bt_stride),
+            _arg(seq_lens, "seq_lens", torch.int32, dev, shape.B))
 
 
-def _packed(shape: Shape, k: torch.Tensor, v: torch.Tensor, what: str) -> tuple[int, int, int, int]:
+def _quant(shape: Shape, t: torch.Tensor, dev: int) -> int:
+    return _arg(t, "quant_cache", torch.uint8, dev, shape.num_pages * shape.Hkv * (shape.page_size * shape.d * 5 // 4))
+
+
+def _packed(shape: Shape, k: torch.Tensor, v: torch.Tensor, what: str, dev: int) -> tuple[int, int, int, int]:
     """(k pointer, v pointer, tokens, token stride) of packed fp16 K and V
     [T, Hkv, d], whose tokens may be strided (alike in both)."""
-    T = int(k.shape[0])
-    for t, name in ((k, f"k_{what}"), (v, f"v_{what}")):
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} must be a CUDA tensor on the current device (got {t.device})")
-        if t.dtype != torch.float16:
-            raise ValueError(f"{name} must be torch.float16 (got {t.dtype})")
-        if tuple(t.shape) != (T, shape.Hkv, shape.d):
-            raise ValueError(f"{name} must be [{T}, {shape.Hkv}, {shape.d}] (got {tuple(t.shape)})")
-        if T and (t.stride(2) != 1 or (shape.Hkv > 1 and t.stride(1) != shape.d)):
-            raise ValueError(f"{name} must be contiguous within a token (strides {t.stride()})")
-    stride = int(k.stride(0)) if T > 1 else shape.Hkv * shape.d
-    if T > 1 and int(v.stride(0)) != stride:
-        raise ValueError(f"k_{what} and v_{what} must have one token stride")
+    Hkv, d = shape.Hkv, shape.d
+    T = k.shape[0]
+    stride = k.stride(0) if T > 1 else Hkv * d
+    for t, name in ((k, "k_"), (v, "v_")):
+        if t.get_device() != dev:
+            raise ValueError(f"{name}{what} must be a CUDA tensor on the current device (got {t.device})")
+        if t.dtype is not torch.float16:
+            raise ValueError(f"{name}{what} must be torch.float16 (got {t.dtype})")
+        if t.shape != (T, Hkv, d):
+            raise ValueError(f"{name}{what} must be [{T}, {Hkv}, {d}] (got {tuple(t.shape)})")
+        s0, s1, s2 = t.stride()
+        if T and (s2 != 1 or (Hkv > 1 and s1 != d)):
+            raise ValueError(f"{name}{what} must be contiguous within a token (strides {t.stride()})")
+        if T > 1 and s0 != stride:
+            raise ValueError(f"k_{what} and v_{what} must have one token stride")
     return k.data_ptr(), v.data_ptr(), T, stride
 
 
@@ -417,42 +447,26 @@ def pkv_quant_append(shape, ws, k_new, v_new, block_table, seq_lens, quant_cache
     each row's seq_lens tokens: row i's are new_offsets[i] .. new_offsets[i + 1]
     (None: one per row).  The advanced lengths go to seq_lens_out (None: in
     place).  See include/pkv.h."""
-    kp, vp, T, stride = _packed(shape, k_new, v_new, "new")
-    out = seq_lens if seq_lens_out is None else seq_lens_out
-    if new_offsets is not None:
-        _size(new_offsets, "new_offsets", shape.B + 1)
-    check(_lib.load().pkv_quant_append(
-        ctypes.byref(shape), _attn_ws(shape, ws), kp, vp, stride, T,
-        _dev(new_offsets, "new_offsets", torch.int32, nullable=True),
-        _dev(_size(block_table, "block_table", shape.B * shape.bt_stride), "block_table", torch.int32),
-        _dev(_size(seq_lens, "seq_lens", shape.B), "seq_lens", torch.int32),
-        _dev(_size(out, "seq_lens_out", shape.B), "seq_lens_out", torch.int32),
-        _quant(shape, quant_cache), _stream(stream)), "pkv_quant_append")
+    L, dev = _lib.load(), _device()
+    kp, vp, T, stride = _packed(shape, k_new, v_new, "new", dev)
+    bp, sp = _table(shape, block_table, seq_lens, dev)
+    op = 0 if new_offsets is None else _arg(new_offsets, "new_offsets", torch.int32, dev, shape.B + 1)
+    lp = sp if seq_lens_out is None else _arg(seq_lens_out, "seq_lens_out", torch.int32, dev, shape.B)
+    check(L.pkv_quant_append(ctypes.byref(shape), _attn_ws(shape, ws, dev), kp, vp, stride, T, op, bp, sp, lp,
+                             _quant(shape, quant_cache, dev), _raw_stream(stream, dev)), "pkv_quant_append")
 
 
 def pkv_quant_read(shape, ws, quant_cache, block_table, seq_lens, out_offsets, k_out, v_out, first=None,
                    stream=None) -> None:
     """Read tokens first[i] .. of each row (None: from token 0) back as fp16 into
     rows out_offsets[i] .. out_offsets[i + 1] of k_out, v_out [T, Hkv, d]."""
-    kp, vp, T, stride = _packed(shape, k_out, v_out, "out")
-    if first is not None:
-        _size(first, "first", shape.B)
-    check(_lib.load().pkv_quant_read(
-        ctypes.byref(shape), _attn_ws(shape, ws), _quant(shape, quant_cache),
-        _dev(_size(block_table, "block_table", shape.B * shape.bt_stride), "block_table", torch.int32),
-        _dev(_size(seq_lens, "seq_lens", shape.B), "seq_lens", torch.int32),
-        _dev(first, "first", torch.int32, nullable=True),
-        _dev(_size(out_offsets, "out_offsets", shape.B + 1), "out_offsets", torch.int32), T, kp, vp, stride,
-        _stream(stream)), "pkv_quant_read")
-
-
-def _attend_args(shape, q, block_table, seq_lens, o, lse):
-    n = shape.B * shape.Hq
-    return (_dev(_size(q, "q", n * shape.d), "q", torch.float16),
-            _dev(_size(block_table, "block_table", shape.B * shape.bt_stride), "block_table", torch.int32),
-            _dev(_size(seq_lens, "seq_lens", shape.B), "seq_lens", torch.int32),
-            _dev(_size(o, "o", n * shape.d), "o", torch.float16),
-            0 if lse is None else _dev(_size(lse, "lse", n), "lse", torch.float32))
+    L, dev = _lib.load(), _device()
+    kp, vp, T, stride = _packed(shape, k_out, v_out, "out", dev)
+    bp, sp = _table(shape, block_table, seq_lens, dev)
+    fp = 0 if first is None else _arg(first, "first", torch.int32, dev, shape.B)
+    op = _arg(out_offsets, "out_offsets", torch.int32, dev, shape.B + 1)
+    check(L.pkv_quant_read(ctypes.byref(shape), _attn_ws(shape, ws, dev), _quant(shape, quant_cache, dev), bp, sp, fp,
+                           op, T, kp, vp, stride, _raw_stream(stream, dev)), "pkv_quant_read")
 
 
 def pkv_quant_decode(shape, ws, q, quant_cache, block_table, seq_lens, o, lse=None, window=None, sinks=0,
@@ -461,24 +475,32 @@ def pkv_quant_decode(shape, ws, q, quant_cache, block_table, seq_lens, o, lse=No
     first `sinks` and last `window` tokens."""
     if window is None and sinks:
         raise ValueError("sinks go with a window")
-    qp, bp, sp, op, lp = _attend_args(shape, q, block_table, seq_lens, o, lse)
-    win = None if window is None else ctypes.byref(Window(int(window), int(sinks)))
-    check(_lib.load().pkv_quant_decode(ctypes.byref(shape), win, _attn_ws(shape, ws), qp,
-                                       _quant(shape, quant_cache), bp, sp, op, lp, _stream(stream)),
-          "pkv_quant_decode")
+    L, dev = _lib.load(), _device()
+    n = shape.B * shape.Hq
+    bp, sp = _table(shape, block_table, seq_lens, dev)
+    win = None if window is None else ctypes.byref(Window(window, sinks))
+    check(L.pkv_quant_decode(ctypes.byref(shape), win, _attn_ws(shape, ws, dev),
+                             _arg(q, "q", torch.float16, dev, n * shape.d), _quant(shape, quant_cache, dev), bp, sp,
+                             _arg(o, "o", torch.float16, dev, n * shape.d),
+                             0 if lse is None else _arg(lse, "lse", torch.float32, dev, n),
+                             _raw_stream(stream, dev)), "pkv_quant_decode")
 
 
 def pkv_window_decode(shape, ws, q, k_cache, v_cache, block_table, seq_lens, window, sinks, o, lse=None,
                       stream=None) -> None:
     """Decode attention over the fp16 pages, of each row's first `sinks` and last
     `window` tokens."""
-    qp, bp, sp, op, lp = _attend_args(shape, q, block_table, seq_lens, o, lse)
-    n = shape.num_pages * shape.page_size * shape.Hkv * shape.d
-    check(_lib.load().pkv_window_decode(ctypes.byref(shape), ctypes.byref(Window(int(window), int(sinks))),
-                                        _attn_ws(shape, ws), qp,
-                                        _dev(_size(k_cache, "k_cache", n), "k_cache", torch.float16),
-                                        _dev(_size(v_cache, "v_cache", n), "v_cache", torch.float16),
-                                        bp, sp, op, lp, _stream(stream)), "pkv_window_decode")
+    L, dev = _lib.load(), _device()
+    n = shape.B * shape.Hq
+    pages = shape.num_pages * shape.page_size * shape.Hkv * shape.d
+    bp, sp = _table(shape, block_table, seq_lens, dev)
+    check(L.pkv_window_decode(ctypes.byref(shape), ctypes.byref(Window(window, sinks)), _attn_ws(shape, ws, dev),
+                              _arg(q, "q", torch.float16, dev, n * shape.d),
+                              _arg(k_cache, "k_cache", torch.float16, dev, pages),
+                              _arg(v_cache, "v_cache", torch.float16, dev, pages), bp, sp,
+                              _arg(o, "o", torch.float16, dev, n * shape.d),
+                              0 if lse is None else _arg(lse, "lse", torch.float32, dev, n),
+                              _raw_stream(stream, dev)), "pkv_window_decode")
 
 
 def pkv_policy_default() -> PolicyCfg:

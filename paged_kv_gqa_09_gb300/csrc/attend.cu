@@ -33,6 +33,8 @@
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
 
+#include <atomic>
+
 namespace pkv {
 namespace {
 
@@ -867,9 +869,17 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, const Atten
 {
     using L = Layout<D, TBL>;
     auto kern = attend_kernel<D, TBL>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    static std::atomic<uint64_t> ready{0};  // devices whose limit on shared memory is raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    if (!(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if (e != cudaSuccess)
+            return e;
+        ready.fetch_or(1ull << (dev & 63));
+    }
     // no more CTAs than the longest rows could keep busy
     constexpr int kTile = L::kTile;
     const int64_t by_len = ((int64_t)p.len_cap + kTile - 1) / kTile;

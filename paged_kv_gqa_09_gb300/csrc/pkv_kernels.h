@@ -126,6 +126,8 @@ struct QuantAppendParams {
     int32_t *row_bad;           // [B], zero between launches
     int64_t page_head_bytes;    // one page of one head
     int T, B, Hkv, log2P, tb_log2, num_pages, bt_stride, len_cap;
+    int64_t groups;             // set by the launcher: groups of eight positions,
+    int parts, heads_per_part;  // and how heads are split over warps
 };
 
 struct QuantReadParams {
@@ -138,6 +140,7 @@ struct QuantReadParams {
     WsHeader *ws;
     int64_t page_head_bytes;
     int T, B, Hkv, log2P, tb_log2, num_pages, bt_stride, len_cap;
+    int parts, heads_per_part;  // set by the launcher
 };
 
 // Decode attention over the tokens [0, sinks) and [N - window, N) of each row.
@@ -156,8 +159,8 @@ struct AttendParams {
     float scale_log2;
 };
 
-cudaError_t launch_quant_append(int d, const QuantAppendParams &p, cudaStream_t s);
-cudaError_t launch_quant_read(int d, const QuantReadParams &p, cudaStream_t s);
+cudaError_t launch_quant_append(int d, QuantAppendParams p, cudaStream_t s);
+cudaError_t launch_quant_read(int d, QuantReadParams p, cudaStream_t s);
 cudaError_t launch_attend(int d, const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms,
                           cudaStream_t s);
 

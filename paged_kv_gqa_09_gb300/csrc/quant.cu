@@ -4,6 +4,15 @@
 // tokens, become codes in the pages their rows' block tables name, at positions
 // seq_lens[i] .. ; lengths advance once every CTA has read them.
 // read: tokens of the cache become packed fp16 K and V again.
+//
+// Both are one pass over their data: append reads 2 bytes per value and writes
+// 0.625, read the other way round; HBM bounds them, append closely followed by
+// its arithmetic (about eleven instructions per value).  A warp takes eight
+// tokens, four lanes each, and loops over KV heads and sides, so that rows,
+// pages and offsets are looked up once for all of them; short calls split the
+// heads over more warps.  Lane t of a token's four holds dims 32 j + 8 t ..
+// (16 bytes of the packed row) on the fp16 side and words (t, j) on the code
+// side; an exchange among the four lanes leads from one to the other.
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
@@ -12,22 +21,21 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
-// Row of packed token x: the i with offsets[i] <= x < offsets[i + 1], or -1.
-// (Without offsets a row has one token.)
-__device__ __forceinline__ int row_of(const int32_t *offsets, int B, int x)
+// The last i in [0, B] with key(i) <= x, for ascending key with key(0) <= x.
+template <class F>
+__device__ __forceinline__ int last_not_above(int B, int64_t x, F key)
 {
-    if (!offsets)
-        return x < B ? x : -1;
-    int lo = 0, hi = B;  // the first i with offsets[i + 1] > x
+    int lo = 0, hi = B;
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (offsets[mid + 1] > x)
-            hi = mid;
+        const int mid = (lo + hi + 1) >> 1;
+        if (key(mid) <= x)
+            lo = mid;
         else
-            lo = mid + 1;
+            hi = mid - 1;
     }
-    return lo < B && offsets[lo] <= x ? lo : -1;
+    return lo;
 }
 
 // OR over the four lanes of a quad of four words each; lane f ends with word f.
@@ -41,15 +49,54 @@ __device__ __forceinline__ uint32_t quad_or_transpose(const uint32_t (&c)[4], in
     return mine | __shfl_xor_sync(0xffffffffu, (f & 1) ? k0 : k1, 1);
 }
 
-// Whether row i's n new tokens fit behind its N tokens; the reason goes to the
+// 4x4 transpose over a quad: lane t gives word f of v to lane f, which gets
+// them in the order of t.
+__device__ __forceinline__ uint4 quad_transpose(const uint32_t (&v)[4], int t)
+{
+    const bool up = (t & 2) != 0, odd = (t & 1) != 0;
+    const uint32_t k0 = up ? v[2] : v[0], k1 = up ? v[3] : v[1];
+    const uint32_t r0 = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 2);
+    const uint32_t r1 = __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 2);
+    const uint32_t own = odd ? k1 : k0, across = odd ? r1 : r0;
+    const uint32_t near = __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
+    const uint32_t far = __shfl_xor_sync(0xffffffffu, odd ? r0 : r1, 1);
+    const uint32_t a0 = odd ? near : own, a1 = odd ? own : near;          // lanes of this half of the quad
+    const uint32_t b0 = odd ? far : across, b1 = odd ? across : far;      // of the other half
+    return up ? make_uint4(b0, b1, a0, a1) : make_uint4(a0, a1, b0, b1);
+}
+
+template <int GR>
+__device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[GR])
+{
+    if constexpr (GR == 4) {
+        const uint4 v = *static_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+        const uint2 v = *static_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+
+template <int GR>
+__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[GR])
+{
+    if constexpr (GR == 4)
+        *static_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+        *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+__device__ __forceinline__ uint32_t as_word(__half lo, __half hi) { return as_word(__halves2half2(lo, hi)); }
+
+// Whether row i's n new tokens, packed from `off` on, are inside the packed
+// buffer and fit behind its N tokens; what is wrong with the length goes to the
 // error word when `report` is set.
 __device__ __forceinline__ bool append_fits(const QuantAppendParams &p, int i, int N, int off, int n, bool report)
 {
-    if (n < 0 || off < 0 || (int64_t)off + n > p.T) {
-        if (report)
-            report_error(p.ws, kErrBadSpan, i, off, n);
+    if (n < 0 || off < 0 || (int64_t)off + n > p.T)
         return false;
-    }
     if (N < 0) {
         if (report)
             report_error(p.ws, kErrNegLen, i, N, 0);
@@ -63,169 +110,329 @@ __device__ __forceinline__ bool append_fits(const QuantAppendParams &p, int i, i
     return true;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantAppendParams p)
+// Codes of the eight values of x (this lane's field f of four words), packed
+// in pairs as they lie in the words.
+//
+// y = (x - b) / s - 16 comes from one fused multiply-add in fp32 and is at most
+// (|c| + 16) 2^-21 off (three roundings of x / s, four of c = -(16 s + b) / s,
+// |x / s| <= |c| + 16).  Where it lies further than twice that from every
+// border (halves of a step) the rounded y is the code; elsewhere -- a few in
+// 10^5 -- and where values are beyond the limit quant_code() decides exactly.
+__device__ __forceinline__ void quant_codes(const uint32_t (&x)[4], uint32_t sb, bool wide, int f, uint32_t (&w)[4])
 {
-    using Q = QuantLayout<D>;
-    constexpr int CH = D / 8;  // threads of one (token, head, side), eight dims each
-    __shared__ int s_last;
-    pdl_wait();
-    pdl_trigger();
-    const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / CH;  // (token, head, side)
-    const int c = threadIdx.x % CH, j = c >> 2, f = c & 3;
-    const int side = (int)(unit & 1);
-    const int64_t th = unit >> 1;
-    const int x = (int)min(th / p.Hkv, (int64_t)0x7fffffff), h = (int)(th % p.Hkv);
-    const int i = x < p.T ? row_of(p.offsets, p.B, x) : -1;
-    bool live = i >= 0;
-    int N = 0, pos = 0, page = 0;
-    if (live) {
-        N = p.seq_lens[i];
-        const int off = p.offsets ? p.offsets[i] : i, n = p.offsets ? p.offsets[i + 1] - off : 1;
-        live = append_fits(p, i, N, off, n, false);
-        pos = N + (x - off);
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
+    const float s = __low2float(as_half2(sb)), b = __high2float(as_half2(sb));
+    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;  // a NaN group's codes are 0, as are those of s = 0
+    const float c = s > 0.f ? -__fmaf_rn(16.f, s, b) * inv : 0.f;
+    const float i15 = inv * (1.f / 15.f), c15 = c * (1.f / 15.f);
+    const float edge = 0.5f - (fabsf(c) + 32.f) * 0x1p-20f;
+    const int sh = f == 1 ? 2 : f == 2 ? 10 : 6;
+    const uint32_t swap = f == 3 ? 0x2301 : 0x3210;
+    float worst = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float2 v = __half22float2(as_half2(x[u]));
+        const float y0 = __saturatef(fmaf(v.x, i15, c15)), y1 = __saturatef(fmaf(v.y, i15, c15));
+        const float n0 = fmaf(y0, 15.f, kMagic), n1 = fmaf(y1, 15.f, kMagic);
+        const float d0 = fmaf(y0, 15.f, kMagic - n0), d1 = fmaf(y1, 15.f, kMagic - n1);
+        worst = fmaxf(worst, fmaxf(fabsf(d0), fabsf(d1)));
+        const uint32_t pair = __byte_perm(__float_as_uint(n0), __float_as_uint(n1), 0x5410);
+        w[u] = __byte_perm(pair << sh, 0, swap);
     }
-    if (live) {
-        page = p.bt[(int64_t)i * p.bt_stride + (pos >> p.log2P)];
-        if (page < 0 || page >= p.num_pages) {
-            report_error(p.ws, kErrBadPage, i, pos >> p.log2P, page);
-            p.row_bad[i] = 1;
-            live = false;
+    if (worst > edge || wide) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float2 v = __half22float2(as_half2(x[u]));
+            const int n0 = s > 0.f ? quant_code(fminf(fmaxf(v.x, -kQuantLimit), kQuantLimit), s, b, inv) : 0;
+            const int n1 = s > 0.f ? quant_code(fminf(fmaxf(v.y, -kQuantLimit), kQuantLimit), s, b, inv) : 0;
+            w[u] = __byte_perm((uint32_t)(n0 | n1 << 16) << sh, 0, swap);
         }
     }
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live)
-        raw = *reinterpret_cast<const uint4 *>((side ? p.v_new : p.k_new) + (int64_t)x * p.new_stride + h * D + c * 8);
-    const __half2 *r2 = reinterpret_cast<const __half2 *>(&raw);
-    __half2 mn = __hmin2_nan(__hmin2_nan(r2[0], r2[1]), __hmin2_nan(r2[2], r2[3]));
-    __half2 mx = __hmax2_nan(__hmax2_nan(r2[0], r2[1]), __hmax2_nan(r2[2], r2[3]));
+}
+
+// One head's K or V of the warp's eight tokens: x[j] are this lane's dims
+// 32 j + 8 t .. of its token; w[j] becomes its word (t, j), sb[j] the groups'
+// s | b << 16 (the same in all four lanes).
+template <int GR>
+__device__ __forceinline__ void quantise_rows(const uint4 (&x)[GR], int t, uint32_t (&w)[GR], uint32_t (&sb)[GR])
+{
+    uint32_t mm[4];  // least | greatest of the lane's eight values of group j (twice over for GR = 2)
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-        mn = __hmin2_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = __hmax2_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int j = 0; j < GR; ++j) {
+        const __half2 a = as_half2(x[j].x), b = as_half2(x[j].y), c = as_half2(x[j].z), d = as_half2(x[j].w);
+        const __half2 mn = __hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)), mx = __hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d));
+        mm[j] = as_word(__hmin_nan(__low2half(mn), __high2half(mn)), __hneg(__hmax_nan(__low2half(mx), __high2half(mx))));
+        if (GR == 2)
+            mm[j + 2] = mm[j];
     }
-    const float lo0 = __half2float(__hmin_nan(mn.x, mn.y)), hi0 = __half2float(__hmax_nan(mx.x, mx.y));
-    const bool nan = lo0 != lo0 || hi0 != hi0;
+    // lane t ends with group j = t & (GR - 1) of its token: least | -greatest
+    const bool up = (t & 2) != 0, odd = (t & 1) != 0;
+    auto least = [](uint32_t a, uint32_t b) { return as_word(__hmin2_nan(as_half2(a), as_half2(b))); };
+    const uint32_t k0 = least(up ? mm[2] : mm[0], __shfl_xor_sync(0xffffffffu, up ? mm[0] : mm[2], 2));
+    const uint32_t k1 = least(up ? mm[3] : mm[1], __shfl_xor_sync(0xffffffffu, up ? mm[1] : mm[3], 2));
+    const uint32_t m = least(odd ? k1 : k0, __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1));
+    const float lo0 = __low2float(as_half2(m)), hi0 = -__high2float(as_half2(m));
     const float lo = fminf(fmaxf(lo0, -kQuantLimit), kQuantLimit), hi = fminf(fmaxf(hi0, -kQuantLimit), kQuantLimit);
     __half s, b;
     quant_params(lo, hi, s, b);
-    const float sf = __half2float(s), bf = __half2float(b), inv = sf > 0.f ? 1.f / sf : 0.f;
-    int n[8];
+    uint32_t mine = as_word(s, b);
+    if (lo0 != lo0 || hi0 != hi0)
+        mine = 0x7fff7fffu;  // a NaN in the group
+    const bool wide_mine = lo != lo0 || hi != hi0;
+    const unsigned wide = __ballot_sync(0xffffffffu, wide_mine);
+    const int base = threadIdx.x & 28;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const float v = __half2float(u & 1 ? r2[u >> 1].y : r2[u >> 1].x);
-        n[u] = nan ? 0 : quant_code(fminf(fmaxf(v, -kQuantLimit), kQuantLimit), sf, bf, inv);
+    for (int j = 0; j < GR; ++j) {
+        sb[j] = __shfl_sync(0xffffffffu, mine, base + j);
+        const uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        uint32_t c[4];
+        quant_codes(v, sb[j], wide >> (base + j) & 1, t, c);
+        w[j] = quad_or_transpose(c, t);
     }
-    if (nan)
-        s = b = __ushort_as_half(0x7fff);
-    uint32_t w[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)  // dims 2t and 2t+1 of the eight
-        w[t] = quant_place(n[2 * t], f) | quant_place(n[2 * t + 1], f) << 16;
-    const uint32_t word = quad_or_transpose(w, f);
-    if (live) {
-        const int tb = 1 << p.tb_log2, slot = pos & ((1 << p.log2P) - 1);
-        const int r = slot & (tb - 1);
-        uint8_t *blk = p.cache + ((int64_t)page * p.Hkv + h) * p.page_head_bytes +
-                       (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
-        if (side == 0) {
-            reinterpret_cast<uint32_t *>(blk)[r * (D / 8) + f * Q::GR + j] = word;
-            if (f < 2)
-                reinterpret_cast<__half *>(blk + Q::k_params(tb))[r * 2 * Q::GR + f * Q::GR + j] = f ? b : s;
-        } else {
-            // this lane holds the halves g = 2 f, 2 f + 1 of its token
-            const int t = (r & 7) >> 1, e = r & 1;
-            uint16_t *vc = reinterpret_cast<uint16_t *>(blk + Q::v_codes(tb) + (r >> 3) * Q::kVGroup);
-            vc[((2 * f * 4 + t) * Q::GR + j) * 2 + e] = (uint16_t)word;
-            vc[(((2 * f + 1) * 4 + t) * Q::GR + j) * 2 + e] = (uint16_t)(word >> 16);
-            if (f < 2)
-                reinterpret_cast<__half *>(blk + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup)[((t * Q::GR + j) * 2 + f) * 2 + e] =
-                    f ? b : s;
+}
+
+// A warp takes the eight cache positions 8 k .. of one row, and heads
+// [h0, h0 + nh).  Rows share one line of such groups: row i's are at
+// offsets[i] / 8 + 2 i .., which leaves room for a first and a last group that
+// are not full and needs no sum over the rows before; what is left over is idle.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAppendParams p)
+{
+    using Q = QuantLayout<D>;
+    constexpr int GR = Q::GR;
+    __shared__ int s_last;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t gs = unit / p.parts;
+    const int h0 = (int)(unit - gs * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
+    bool bad = false;
+    do {
+        if (gs >= p.groups)
+            break;
+        int i = (int)gs, off = i, n = 1, k = 0;
+        if (p.offsets) {
+            i = min(last_not_above(p.B, gs, [&](int r) { return (int64_t)(p.offsets[r] >> 3) + 2 * (int64_t)r; }), p.B - 1);
+            off = p.offsets[i];
+            n = p.offsets[i + 1] - off;
+            k = (int)(gs - (off >> 3) - 2 * (int64_t)i);
         }
-    }
+        const int N = p.seq_lens[i];
+        if (k < 0 || !append_fits(p, i, N, off, n, false))
+            break;
+        const int64_t pos0 = ((int64_t)(N >> 3) + k) * 8;
+        if (pos0 >= (int64_t)N + n)
+            break;
+        const int page = p.bt[(int64_t)i * p.bt_stride + (pos0 >> p.log2P)];
+        if (page < 0 || page >= p.num_pages) {
+            if (lane == 0) {
+                report_error(p.ws, kErrBadPage, i, (int)(pos0 >> p.log2P), page);
+                p.row_bad[i] = 1;
+            }
+            bad = true;
+            break;
+        }
+        const int tb = 1 << p.tb_log2, slot = (int)pos0 & ((1 << p.log2P) - 1), r = slot & (tb - 1);
+        uint8_t *blk = p.cache + (int64_t)page * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
+        const int pos = (int)pos0 + g;
+        const bool live = pos >= N && pos < N + n;
+        const unsigned lives = __ballot_sync(0xffffffffu, live);
+        const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
+        const int64_t src = (int64_t)(off + (pos - N)) * p.new_stride + 8 * t;
+        const int e = g & 1, t2 = g >> 1;
+        for (int h = h0; h < h1; ++h) {
+            uint4 xk[GR], xv[GR];
+#pragma unroll
+            for (int j = 0; j < GR; ++j) {
+                xk[j] = xv[j] = make_uint4(0, 0, 0, 0);
+                if (live) {
+                    xk[j] = __ldcs(reinterpret_cast<const uint4 *>(p.k_new + src + h * D + 32 * j));
+                    xv[j] = __ldcs(reinterpret_cast<const uint4 *>(p.v_new + src + h * D + 32 * j));
+                }
+            }
+            uint8_t *hb = blk + h * p.page_head_bytes;
+            uint32_t w[GR], sb[GR];
+            quantise_rows<GR>(xk, t, w, sb);
+            if (live) {
+                store_words<GR>(hb + (r + g) * Q::kRow + t * GR * 4, w);
+                // s of the groups, then b: lane t writes two of the 2 GR halves
+                const int j = (2 * t) & (GR - 1);
+                const uint32_t a = GR == 4 ? (j ? sb[GR - 2] : sb[0]) : sb[0], c = GR == 4 ? (j ? sb[GR - 1] : sb[1]) : sb[1];
+                if (2 * t < 2 * GR)
+                    reinterpret_cast<uint32_t *>(hb + Q::k_params(tb) + (r + g) * Q::kParamRow)[t] =
+                        __byte_perm(a, c, 2 * t < GR ? 0x5410 : 0x7632);
+            }
+            quantise_rows<GR>(xv, t, w, sb);
+            // this lane holds the halves g' = 2 t (low) and 2 t + 1 of its token; with the neighbouring token's it
+            // makes the words g' = 2 t + e whole
+            uint32_t o[GR], so[GR];
+#pragma unroll
+            for (int j = 0; j < GR; ++j) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 4);
+                o[j] = e ? __byte_perm(other, w[j], 0x7632) : __byte_perm(w[j], other, 0x5410);
+                so[j] = __shfl_xor_sync(0xffffffffu, sb[j], 4);
+            }
+            uint8_t *vc = hb + Q::v_codes(tb) + (r >> 3) * Q::kVGroup, *vp = hb + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup;
+            if (pair) {
+                store_words<GR>(vc + ((2 * t + e) * 4 + t2) * GR * 4, o);
+                // words s s and b b of group j: lane t's of the token with e = 0 and e = 1
+                uint32_t a = sb[0], c = so[0];
+#pragma unroll
+                for (int j = 1; j < GR; ++j)
+                    if (j == t)
+                        a = sb[j], c = so[j];
+                if (t < GR)
+                    reinterpret_cast<uint32_t *>(vp)[(t2 * GR + t) * 2 + e] = e ? __byte_perm(c, a, 0x7632) : __byte_perm(a, c, 0x5410);
+            } else if (live) {
+                uint16_t *c16 = reinterpret_cast<uint16_t *>(vc), *p16 = reinterpret_cast<uint16_t *>(vp);
+#pragma unroll
+                for (int j = 0; j < GR; ++j) {
+                    c16[((2 * t * 4 + t2) * GR + j) * 2 + e] = (uint16_t)w[j];
+                    c16[(((2 * t + 1) * 4 + t2) * GR + j) * 2 + e] = (uint16_t)(w[j] >> 16);
+                    if (j == t) {
+                        p16[(t2 * GR + j) * 4 + e] = (uint16_t)sb[j];
+                        p16[(t2 * GR + j) * 4 + 2 + e] = (uint16_t)(sb[j] >> 16);
+                    }
+                }
+            }
+        }
+    } while (false);
     // the last CTA to get here advances the lengths: every other one has read
     // them by then, and its rows' flags are set
-    __syncthreads();
+    const int any_bad = __syncthreads_or(bad ? 1 : 0);
     if (threadIdx.x == 0) {
-        __threadfence();
+        if (any_bad)
+            __threadfence();
         s_last = atomicAdd(&p.ws->append_done, 1) == (int)gridDim.x - 1;
     }
     __syncthreads();
     if (!s_last)
         return;
     __threadfence();
+    // offsets that do not ascend within the buffer give tokens to no row or to two: the whole call is refused
+    bool span = false;
+    if (p.offsets)
+        for (int r = threadIdx.x; r < p.B; r += kThreads) {
+            const int off = p.offsets[r], nr = p.offsets[r + 1] - off;
+            if (off < 0 || nr < 0 || (int64_t)off + nr > p.T) {
+                report_error(p.ws, kErrBadSpan, r, off, nr);
+                span = true;
+            }
+        }
+    span = __syncthreads_or(span ? 1 : 0) != 0;
     for (int r = threadIdx.x; r < p.B; r += kThreads) {
         const int Nr = p.seq_lens[r];
         const int off = p.offsets ? p.offsets[r] : r, nr = p.offsets ? p.offsets[r + 1] - off : 1;
-        const bool ok = append_fits(p, r, Nr, off, nr, true) && !__ldcg(p.row_bad + r);
+        const int flag = __ldcg(p.row_bad + r);
+        const bool ok = !span && append_fits(p, r, Nr, off, nr, true) && !flag;
         p.seq_lens_out[r] = ok ? Nr + nr : Nr;
-        p.row_bad[r] = 0;
+        if (flag)
+            p.row_bad[r] = 0;
     }
     if (threadIdx.x == 0)
         p.ws->append_done = 0;
 }
 
-// One thread reads eight dims of one (token, head, side).
+// A warp takes eight packed tokens, one per quad, and heads [h0, h0 + nh).  A
+// token's V halves are gathered to the words its K row has: the halves g' = 2 t
+// and 2 t + 1 of its words become lane t's word (t, j).
 template <int D>
-__global__ void __launch_bounds__(kThreads) quant_read_kernel(const QuantReadParams p)
+__global__ void __launch_bounds__(kThreads, 4) quant_read_kernel(const QuantReadParams p)
 {
     using Q = QuantLayout<D>;
-    constexpr int CH = D / 8;
+    constexpr int GR = Q::GR;
     pdl_wait();
     pdl_trigger();
-    const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / CH;
-    const int c = threadIdx.x % CH, j = c >> 2, f = c & 3;
-    const int side = (int)(unit & 1);
-    const int64_t th = unit >> 1;
-    const int x = (int)min(th / p.Hkv, (int64_t)0x7fffffff), h = (int)(th % p.Hkv);
-    const int i = x < p.T ? row_of(p.offsets, p.B, x) : -1;
-    if (i < 0)
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t chunk = unit / p.parts;
+    const int h0 = (int)(unit - chunk * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
+    if (chunk * 8 >= p.T)
         return;
-    const int N = min(p.seq_lens[i], p.len_cap);
-    const int64_t pos = (int64_t)(p.first ? p.first[i] : 0) + (x - p.offsets[i]);
-    uint32_t out[4] = {0, 0, 0, 0};
+    const int x = (int)min(chunk * 8 + g, (int64_t)0x7fffffff);
+    bool live = x < p.T && x >= p.offsets[0] && x < p.offsets[p.B];  // in some row's span
     int page = -1;
-    if (pos < 0 || pos >= N) {
-        report_error(p.ws, kErrTooLong, i, (int)min(max(pos + 1, (int64_t)-0x7fffffff), (int64_t)0x7fffffff), N);
-    } else {
-        page = p.bt[(int64_t)i * p.bt_stride + (pos >> p.log2P)];
-        if (page < 0 || page >= p.num_pages) {
-            report_error(p.ws, kErrBadPage, i, (int)(pos >> p.log2P), page);
-            page = -1;
+    int64_t pos = 0;
+    if (live) {
+        const int i = min(last_not_above(p.B, x, [&](int r) { return (int64_t)p.offsets[r]; }), p.B - 1);
+        const int N = min(p.seq_lens[i], p.len_cap);
+        pos = (int64_t)(p.first ? p.first[i] : 0) + (x - p.offsets[i]);
+        if (x >= p.offsets[i + 1]) {
+            live = false;  // offsets that do not ascend
+        } else if (pos < 0 || pos >= N) {
+            if (t == 0)
+                report_error(p.ws, kErrTooLong, i, (int)min(max(pos + 1, (int64_t)-0x7fffffff), (int64_t)0x7fffffff), N);
+        } else {
+            page = p.bt[(int64_t)i * p.bt_stride + (pos >> p.log2P)];
+            if (page < 0 || page >= p.num_pages) {
+                if (t == 0)
+                    report_error(p.ws, kErrBadPage, i, (int)(pos >> p.log2P), page);
+                page = -1;
+            }
         }
     }
-    if (page >= 0) {
-        const int tb = 1 << p.tb_log2, slot = (int)pos & ((1 << p.log2P) - 1);
-        const int r = slot & (tb - 1), t2 = (r & 7) >> 1, e = r & 1;
-        const uint8_t *blk = p.cache + ((int64_t)page * p.Hkv + h) * p.page_head_bytes +
-                             (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
-        const __half *par = side == 0 ? reinterpret_cast<const __half *>(blk + Q::k_params(tb)) + r * 2 * Q::GR + j
-                                      : reinterpret_cast<const __half *>(blk + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup) +
-                                            (t2 * Q::GR + j) * 4 + e;
-        const __half2 s2 = __half2half2(par[0]), b2 = __half2half2(par[side == 0 ? Q::GR : 2]);
-        const uint16_t *vc = reinterpret_cast<const uint16_t *>(blk + Q::v_codes(tb) + (r >> 3) * Q::kVGroup);
+    const int tb = 1 << p.tb_log2, slot = (int)pos & ((1 << p.log2P) - 1), r = slot & (tb - 1), t2 = (r & 7) >> 1, e = r & 1;
+    const bool there = page >= 0;
+    const uint8_t *blk = p.cache + (int64_t)(there ? page : 0) * p.Hkv * p.page_head_bytes +
+                         (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
+    const int64_t dst = (int64_t)x * p.out_stride + 8 * t;
+    for (int h = h0; h < h1; ++h) {
+        const uint8_t *hb = blk + h * p.page_head_bytes;
+        uint32_t k[GR], kp[GR], v0[GR], v1[GR], vp[2 * GR];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {  // dims 2t and 2t+1 of the eight
-            uint32_t w;
-            if (side == 0)
-                w = reinterpret_cast<const uint32_t *>(blk)[r * (D / 8) + t * Q::GR + j];
-            else
-                w = (uint32_t)vc[((2 * t * 4 + t2) * Q::GR + j) * 2 + e] |
-                    (uint32_t)vc[(((2 * t + 1) * 4 + t2) * Q::GR + j) * 2 + e] << 16;
-            const uint32_t n16 = f == 0 ? quant_field<0>(w) : f == 1 ? quant_field<1>(w)
-                                 : f == 2 ? quant_field<2>(w) : quant_field<3>(w);
-            out[t] = quant_value(n16, s2, b2);
+        for (int j = 0; j < GR; ++j)
+            k[j] = kp[j] = v0[j] = v1[j] = vp[j] = vp[GR + j] = 0;
+        if (there) {
+            load_words<GR>(hb + r * Q::kRow + t * GR * 4, k);
+            load_words<GR>(hb + Q::k_params(tb) + r * Q::kParamRow, kp);
+            const uint8_t *vc = hb + Q::v_codes(tb) + (r >> 3) * Q::kVGroup;
+            load_words<GR>(vc + (2 * t * 4 + t2) * GR * 4, v0);
+            load_words<GR>(vc + ((2 * t + 1) * 4 + t2) * GR * 4, v1);
+            const uint8_t *q = hb + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup + t2 * GR * 8;
+#pragma unroll
+            for (int j = 0; j < GR; j += 2) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(q + j * 8);
+                vp[2 * j] = a.x, vp[2 * j + 1] = a.y, vp[2 * j + 2] = a.z, vp[2 * j + 3] = a.w;
+            }
         }
+        auto give = [&](__half *out, uint32_t w, uint32_t s2, uint32_t b2, int j) {
+            const __half2 s = as_half2(s2), b = as_half2(b2);
+            const uint32_t v[4] = {quant_value(quant_field<0>(w), s, b), quant_value(quant_field<1>(w), s, b),
+                                   quant_value(quant_field<2>(w), s, b), quant_value(quant_field<3>(w), s, b)};
+            const uint4 y = quad_transpose(v, t);
+            if (live)
+                *reinterpret_cast<uint4 *>(out + dst + h * D + 32 * j) = y;
+        };
+#pragma unroll
+        for (int j = 0; j < GR; ++j)
+            give(p.k_out, k[j], __byte_perm(kp[j >> 1], 0, j & 1 ? 0x3232 : 0x1010),
+                 __byte_perm(kp[(GR + j) >> 1], 0, j & 1 ? 0x3232 : 0x1010), j);
+        const uint32_t pick = e ? 0x7632 : 0x5410, both = e ? 0x3232 : 0x1010;
+#pragma unroll
+        for (int j = 0; j < GR; ++j)
+            give(p.v_out, __byte_perm(v0[j], v1[j], pick), __byte_perm(vp[2 * j], 0, both), __byte_perm(vp[2 * j + 1], 0, both), j);
     }
-    *reinterpret_cast<uint4 *>((side ? p.v_out : p.k_out) + (int64_t)x * p.out_stride + h * D + c * 8) =
-        make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Heads are split over `parts` warps while the launch has fewer warps than the
+// GPU holds at once (152 SMs x 32): a token's lookups are then repeated, which
+// a launch of that size does not notice, and its heads run side by side.
+int split_heads(int64_t warps, int Hkv, int &heads_per_part)
+{
+    int parts = 1;
+    while (parts < Hkv && warps * parts < 152 * 32)
+        parts *= 2;
+    heads_per_part = (Hkv + parts - 1) / parts;
+    return (Hkv + heads_per_part - 1) / heads_per_part;
 }
 
 template <class K, class P>
-cudaError_t launch(K kern, const P &p, int64_t threads, cudaStream_t s)
+cudaError_t launch(K kern, const P &p, int64_t warps, cudaStream_t s)
 {
+    const int64_t grid = (warps + kWarps - 1) / kWarps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((threads + kThreads - 1) / kThreads > 0 ? (threads + kThreads - 1) / kThreads : 1));
+    cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -238,16 +445,20 @@ cudaError_t launch(K kern, const P &p, int64_t threads, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_quant_append(int d, const QuantAppendParams &p, cudaStream_t s)
+cudaError_t launch_quant_append(int d, QuantAppendParams p, cudaStream_t s)
 {
-    const int64_t threads = (int64_t)p.T * p.Hkv * 2 * (d / 8);
-    return d == 128 ? launch(quant_append_kernel<128>, p, threads, s) : launch(quant_append_kernel<64>, p, threads, s);
+    p.groups = p.offsets ? (int64_t)p.T / 8 + 2 * (int64_t)p.B : p.B;
+    p.parts = split_heads(p.groups, p.Hkv, p.heads_per_part);
+    const int64_t warps = p.groups * p.parts;
+    return d == 128 ? launch(quant_append_kernel<128>, p, warps, s) : launch(quant_append_kernel<64>, p, warps, s);
 }
 
-cudaError_t launch_quant_read(int d, const QuantReadParams &p, cudaStream_t s)
+cudaError_t launch_quant_read(int d, QuantReadParams p, cudaStream_t s)
 {
-    const int64_t threads = (int64_t)p.T * p.Hkv * 2 * (d / 8);
-    return d == 128 ? launch(quant_read_kernel<128>, p, threads, s) : launch(quant_read_kernel<64>, p, threads, s);
+    const int64_t chunks = ((int64_t)p.T + 7) / 8;
+    p.parts = split_heads(chunks, p.Hkv, p.heads_per_part);
+    const int64_t warps = chunks * p.parts;
+    return d == 128 ? launch(quant_read_kernel<128>, p, warps, s) : launch(quant_read_kernel<64>, p, warps, s);
 }
 
 }  // namespace pkv
