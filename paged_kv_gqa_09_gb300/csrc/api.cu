@@ -1251,7 +1251,9 @@ int pkv_quant_append(const pkv_shape_t *s, void *d_ws, const void *k_new, const 
     p.num_pages = s->num_pages;
     p.bt_stride = s->bt_stride;
     p.len_cap = len_cap(s);
-    cudaError_t e = launch_quant_append(s->d, p, static_cast<cudaStream_t>(stream));
+    int sms = 0;
+    PKV_TRY(device_sms(&sms));
+    cudaError_t e = launch_quant_append(s->d, p, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "quant append launch");
     g_cnt.append++;
@@ -1293,7 +1295,9 @@ int pkv_quant_read(const pkv_shape_t *s, void *d_ws, const void *cache, const in
     p.num_pages = s->num_pages;
     p.bt_stride = s->bt_stride;
     p.len_cap = len_cap(s);
-    cudaError_t e = launch_quant_read(s->d, p, static_cast<cudaStream_t>(stream));
+    int sms = 0;
+    PKV_TRY(device_sms(&sms));
+    cudaError_t e = launch_quant_read(s->d, p, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "quant read launch");
     return PKV_OK;

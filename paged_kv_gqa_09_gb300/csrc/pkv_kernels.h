@@ -159,8 +159,8 @@ struct AttendParams {
     float scale_log2;
 };
 
-cudaError_t launch_quant_append(int d, QuantAppendParams p, cudaStream_t s);
-cudaError_t launch_quant_read(int d, QuantReadParams p, cudaStream_t s);
+cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_t s);
+cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s);
 cudaError_t launch_attend(int d, const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms,
                           cudaStream_t s);
 

@@ -86,6 +86,14 @@ __device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[GR])
         *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
+// 1 / x for normal x, within 2^-23 of itself.
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half lo, __half hi) { return as_word(__halves2half2(lo, hi)); }
@@ -110,22 +118,39 @@ __device__ __forceinline__ bool append_fits(const QuantAppendParams &p, int i, i
     return true;
 }
 
+// The four code pairs of quant_codes() below, decided exactly; out of line, so
+// that the loop that hardly ever calls it stays small.
+__device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b)
+{
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const float inv = 1.f / s;
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+        const float2 v = __half22float2(as_half2(w[u]));
+        w[u] = (uint32_t)(quant_code(fminf(fmaxf(v.x, -kQuantLimit), kQuantLimit), s, b, inv) |
+                          quant_code(fminf(fmaxf(v.y, -kQuantLimit), kQuantLimit), s, b, inv) << 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Codes of the eight values of x (this lane's field f of four words), packed
 // in pairs as they lie in the words.
 //
-// y = (x - b) / s - 16 comes from one fused multiply-add in fp32 and is at most
-// (|c| + 16) 2^-21 off (three roundings of x / s, four of c = -(16 s + b) / s,
-// |x / s| <= |c| + 16).  Where it lies further than twice that from every
-// border (halves of a step) the rounded y is the code; elsewhere -- a few in
-// 10^5 -- and where values are beyond the limit quant_code() decides exactly.
-__device__ __forceinline__ void quant_codes(const uint32_t (&x)[4], uint32_t sb, bool wide, int f, uint32_t (&w)[4])
+// y = (x - b) / s - 16 comes, over 15, from one fused multiply-add in fp32 and
+// is at most (|c| + 16) 2^-21 off: 1 / (15 s) is within 2^-23 of itself,
+// c = -(16 s + b) / s within 2^-22, and |x / s| <= |c| + 16.  Where it lies
+// further than twice that from every border (halves of a step) the rounded y
+// is the code; elsewhere -- a few in 10^5 -- and where values are beyond the
+// limit, quant_code() decides exactly.
+__device__ __forceinline__ void quant_codes(const uint4 &x4, uint32_t sb, bool wide, int f, uint32_t (&w)[4])
 {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
+    const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
     const float s = __low2float(as_half2(sb)), b = __high2float(as_half2(sb));
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;  // a NaN group's codes are 0, as are those of s = 0
-    const float c = s > 0.f ? -__fmaf_rn(16.f, s, b) * inv : 0.f;
-    const float i15 = inv * (1.f / 15.f), c15 = c * (1.f / 15.f);
-    const float edge = 0.5f - (fabsf(c) + 32.f) * 0x1p-20f;
+    float i15 = rcp_approx(15.f * s);
+    i15 = s > 0.f ? i15 : 0.f;  // s = 0: code 0; a NaN group: y is NaN, which saturates to 0
+    const float c15 = -fmaf(16.f, s, b) * i15;
+    const float edge = 0.5f - fmaf(fabsf(c15), 15.f * 0x1p-20f, 0x1p-15f);
     const int sh = f == 1 ? 2 : f == 2 ? 10 : 6;
     const uint32_t swap = f == 3 ? 0x2301 : 0x3210;
     float worst = 0.f;
@@ -135,19 +160,16 @@ __device__ __forceinline__ void quant_codes(const uint32_t (&x)[4], uint32_t sb,
         const float y0 = __saturatef(fmaf(v.x, i15, c15)), y1 = __saturatef(fmaf(v.y, i15, c15));
         const float n0 = fmaf(y0, 15.f, kMagic), n1 = fmaf(y1, 15.f, kMagic);
         const float d0 = fmaf(y0, 15.f, kMagic - n0), d1 = fmaf(y1, 15.f, kMagic - n1);
-        worst = fmaxf(worst, fmaxf(fabsf(d0), fabsf(d1)));
-        const uint32_t pair = __byte_perm(__float_as_uint(n0), __float_as_uint(n1), 0x5410);
-        w[u] = __byte_perm(pair << sh, 0, swap);
+        worst = fmaxf(fmaxf(worst, fabsf(d0)), fabsf(d1));
+        w[u] = __byte_perm(__float_as_uint(n0), __float_as_uint(n1), 0x5410);
     }
-    if (worst > edge || wide) {
+    if ((worst > edge || wide) && s > 0.f) {
+        const uint4 e = quant_codes_exact(x4, s, b);
+        w[0] = e.x, w[1] = e.y, w[2] = e.z, w[3] = e.w;
+    }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float2 v = __half22float2(as_half2(x[u]));
-            const int n0 = s > 0.f ? quant_code(fminf(fmaxf(v.x, -kQuantLimit), kQuantLimit), s, b, inv) : 0;
-            const int n1 = s > 0.f ? quant_code(fminf(fmaxf(v.y, -kQuantLimit), kQuantLimit), s, b, inv) : 0;
-            w[u] = __byte_perm((uint32_t)(n0 | n1 << 16) << sh, 0, swap);
-        }
-    }
+    for (int u = 0; u < 4; ++u)
+        w[u] = __byte_perm(w[u] << sh, 0, swap);
 }
 
 // One head's K or V of the warp's eight tokens: x[j] are this lane's dims
@@ -156,16 +178,17 @@ __device__ __forceinline__ void quant_codes(const uint32_t (&x)[4], uint32_t sb,
 template <int GR>
 __device__ __forceinline__ void quantise_rows(const uint4 (&x)[GR], int t, uint32_t (&w)[GR], uint32_t (&sb)[GR])
 {
-    uint32_t mm[4];  // least | greatest of the lane's eight values of group j (twice over for GR = 2)
+    uint32_t mm[4];  // least | -greatest of the lane's eight values of group j (twice over for GR = 2)
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
         const __half2 a = as_half2(x[j].x), b = as_half2(x[j].y), c = as_half2(x[j].z), d = as_half2(x[j].w);
-        const __half2 mn = __hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)), mx = __hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d));
-        mm[j] = as_word(__hmin_nan(__low2half(mn), __high2half(mn)), __hneg(__hmax_nan(__low2half(mx), __high2half(mx))));
+        const uint32_t mn = as_word(__hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)));
+        const uint32_t mx = as_word(__hneg2(__hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d))));
+        mm[j] = as_word(__hmin2_nan(as_half2(__byte_perm(mn, mx, 0x5410)), as_half2(__byte_perm(mn, mx, 0x7632))));
         if (GR == 2)
             mm[j + 2] = mm[j];
     }
-    // lane t ends with group j = t & (GR - 1) of its token: least | -greatest
+    // lane t ends with group j = t & (GR - 1) of its token
     const bool up = (t & 2) != 0, odd = (t & 1) != 0;
     auto least = [](uint32_t a, uint32_t b) { return as_word(__hmin2_nan(as_half2(a), as_half2(b))); };
     const uint32_t k0 = least(up ? mm[2] : mm[0], __shfl_xor_sync(0xffffffffu, up ? mm[0] : mm[2], 2));
@@ -178,23 +201,22 @@ __device__ __forceinline__ void quantise_rows(const uint4 (&x)[GR], int t, uint3
     uint32_t mine = as_word(s, b);
     if (lo0 != lo0 || hi0 != hi0)
         mine = 0x7fff7fffu;  // a NaN in the group
-    const bool wide_mine = lo != lo0 || hi != hi0;
-    const unsigned wide = __ballot_sync(0xffffffffu, wide_mine);
+    const unsigned wide = __ballot_sync(0xffffffffu, lo != lo0 || hi != hi0);
     const int base = threadIdx.x & 28;
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
         sb[j] = __shfl_sync(0xffffffffu, mine, base + j);
-        const uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
         uint32_t c[4];
-        quant_codes(v, sb[j], wide >> (base + j) & 1, t, c);
+        quant_codes(x[j], sb[j], wide >> (base + j) & 1, t, c);
         w[j] = quad_or_transpose(c, t);
     }
 }
 
 // A warp takes the eight cache positions 8 k .. of one row, and heads
-// [h0, h0 + nh).  Rows share one line of such groups: row i's are at
-// offsets[i] / 8 + 2 i .., which leaves room for a first and a last group that
-// are not full and needs no sum over the rows before; what is left over is idle.
+// [h0, h1), then the next such unit a grid further on.  Rows share one line of
+// such groups: row i's are at offsets[i] / 8 + 2 i .., which leaves room for a
+// first and a last group that are not full and needs no sum over the rows
+// before; what is left over is idle.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAppendParams p)
 {
@@ -204,13 +226,13 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t gs = unit / p.parts;
-    const int h0 = (int)(unit - gs * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
+    const int e = g & 1, t2 = g >> 1;
+    const int tb = 1 << p.tb_log2;
     bool bad = false;
-    do {
-        if (gs >= p.groups)
-            break;
+    for (int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < p.groups * p.parts;
+         unit += (int64_t)gridDim.x * kWarps) {
+        const int64_t gs = unit / p.parts;
+        const int h0 = (int)(unit - gs * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
         int i = (int)gs, off = i, n = 1, k = 0;
         if (p.offsets) {
             i = min(last_not_above(p.B, gs, [&](int r) { return (int64_t)(p.offsets[r] >> 3) + 2 * (int64_t)r; }), p.B - 1);
@@ -220,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
         }
         const int N = p.seq_lens[i];
         if (k < 0 || !append_fits(p, i, N, off, n, false))
-            break;
+            continue;
         const int64_t pos0 = ((int64_t)(N >> 3) + k) * 8;
         if (pos0 >= (int64_t)N + n)
-            break;
+            continue;
         const int page = p.bt[(int64_t)i * p.bt_stride + (pos0 >> p.log2P)];
         if (page < 0 || page >= p.num_pages) {
             if (lane == 0) {
@@ -231,73 +253,76 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
                 p.row_bad[i] = 1;
             }
             bad = true;
-            break;
+            continue;
         }
-        const int tb = 1 << p.tb_log2, slot = (int)pos0 & ((1 << p.log2P) - 1), r = slot & (tb - 1);
-        uint8_t *blk = p.cache + (int64_t)page * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
+        const int slot = (int)pos0 & ((1 << p.log2P) - 1), r = slot & (tb - 1);
+        uint8_t *hb = p.cache + ((int64_t)page * p.Hkv + h0) * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
         const int pos = (int)pos0 + g;
         const bool live = pos >= N && pos < N + n;
         const unsigned lives = __ballot_sync(0xffffffffu, live);
         const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
-        const int64_t src = (int64_t)(off + (pos - N)) * p.new_stride + 8 * t;
-        const int e = g & 1, t2 = g >> 1;
-        for (int h = h0; h < h1; ++h) {
-            uint4 xk[GR], xv[GR];
+        const int64_t src = live ? (int64_t)(off + (pos - N)) * p.new_stride + 8 * t : 0;
+        // K and V of a head in turn, the next one's values on their way while one is quantised
+        auto fetch = [&](int it, uint4 (&x)[GR]) {
+            const __half *from = (it & 1 ? p.v_new : p.k_new) + src + (h0 + (it >> 1)) * D;
 #pragma unroll
-            for (int j = 0; j < GR; ++j) {
-                xk[j] = xv[j] = make_uint4(0, 0, 0, 0);
-                if (live) {
-                    xk[j] = __ldcs(reinterpret_cast<const uint4 *>(p.k_new + src + h * D + 32 * j));
-                    xv[j] = __ldcs(reinterpret_cast<const uint4 *>(p.v_new + src + h * D + 32 * j));
-                }
-            }
-            uint8_t *hb = blk + h * p.page_head_bytes;
+            for (int j = 0; j < GR; ++j)
+                x[j] = live ? __ldcs(reinterpret_cast<const uint4 *>(from + 32 * j)) : make_uint4(0, 0, 0, 0);
+        };
+        uint4 next[GR];
+        fetch(0, next);
+#pragma unroll 1
+        for (int it = 0; it < 2 * (h1 - h0); ++it) {
+            uint4 x[GR];
+#pragma unroll
+            for (int j = 0; j < GR; ++j)
+                x[j] = next[j];
+            if (it + 1 < 2 * (h1 - h0))
+                fetch(it + 1, next);
             uint32_t w[GR], sb[GR];
-            quantise_rows<GR>(xk, t, w, sb);
-            if (live) {
-                store_words<GR>(hb + (r + g) * Q::kRow + t * GR * 4, w);
-                // s of the groups, then b: lane t writes two of the 2 GR halves
-                const int j = (2 * t) & (GR - 1);
-                const uint32_t a = GR == 4 ? (j ? sb[GR - 2] : sb[0]) : sb[0], c = GR == 4 ? (j ? sb[GR - 1] : sb[1]) : sb[1];
-                if (2 * t < 2 * GR)
-                    reinterpret_cast<uint32_t *>(hb + Q::k_params(tb) + (r + g) * Q::kParamRow)[t] =
-                        __byte_perm(a, c, 2 * t < GR ? 0x5410 : 0x7632);
+            quantise_rows<GR>(x, t, w, sb);
+            if (!(it & 1)) {
+                if (live) {
+                    store_words<GR>(hb + (r + g) * Q::kRow + t * GR * 4, w);
+                    // s of the groups, then b: lane t writes two of the 2 GR halves
+                    const int j = (2 * t) & (GR - 1);
+                    const uint32_t a = j ? sb[GR - 2] : sb[0], c = j ? sb[GR - 1] : sb[1];
+                    if (t < GR)
+                        reinterpret_cast<uint32_t *>(hb + Q::k_params(tb) + (r + g) * Q::kParamRow)[t] =
+                            __byte_perm(a, c, 2 * t < GR ? 0x5410 : 0x7632);
+                }
+                continue;
             }
-            quantise_rows<GR>(xv, t, w, sb);
             // this lane holds the halves g' = 2 t (low) and 2 t + 1 of its token; with the neighbouring token's it
             // makes the words g' = 2 t + e whole
-            uint32_t o[GR], so[GR];
+            uint32_t o[GR], so = 0, si = 0;  // s | b of group t: the neighbour's, its own
 #pragma unroll
             for (int j = 0; j < GR; ++j) {
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 4);
                 o[j] = e ? __byte_perm(other, w[j], 0x7632) : __byte_perm(w[j], other, 0x5410);
-                so[j] = __shfl_xor_sync(0xffffffffu, sb[j], 4);
+                si = j == t ? sb[j] : si;
             }
+            so = __shfl_xor_sync(0xffffffffu, si, 4);
             uint8_t *vc = hb + Q::v_codes(tb) + (r >> 3) * Q::kVGroup, *vp = hb + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup;
             if (pair) {
                 store_words<GR>(vc + ((2 * t + e) * 4 + t2) * GR * 4, o);
-                // words s s and b b of group j: lane t's of the token with e = 0 and e = 1
-                uint32_t a = sb[0], c = so[0];
-#pragma unroll
-                for (int j = 1; j < GR; ++j)
-                    if (j == t)
-                        a = sb[j], c = so[j];
                 if (t < GR)
-                    reinterpret_cast<uint32_t *>(vp)[(t2 * GR + t) * 2 + e] = e ? __byte_perm(c, a, 0x7632) : __byte_perm(a, c, 0x5410);
+                    reinterpret_cast<uint32_t *>(vp)[(t2 * GR + t) * 2 + e] = e ? __byte_perm(so, si, 0x7632) : __byte_perm(si, so, 0x5410);
             } else if (live) {
                 uint16_t *c16 = reinterpret_cast<uint16_t *>(vc), *p16 = reinterpret_cast<uint16_t *>(vp);
 #pragma unroll
                 for (int j = 0; j < GR; ++j) {
                     c16[((2 * t * 4 + t2) * GR + j) * 2 + e] = (uint16_t)w[j];
                     c16[(((2 * t + 1) * 4 + t2) * GR + j) * 2 + e] = (uint16_t)(w[j] >> 16);
-                    if (j == t) {
-                        p16[(t2 * GR + j) * 4 + e] = (uint16_t)sb[j];
-                        p16[(t2 * GR + j) * 4 + 2 + e] = (uint16_t)(sb[j] >> 16);
-                    }
+                }
+                if (t < GR) {
+                    p16[(t2 * GR + t) * 4 + e] = (uint16_t)si;
+                    p16[(t2 * GR + t) * 4 + 2 + e] = (uint16_t)(si >> 16);
                 }
             }
+            hb += p.page_head_bytes;
         }
-    } while (false);
+    }
     // the last CTA to get here advances the lengths: every other one has read
     // them by then, and its rows' flags are set
     const int any_bad = __syncthreads_or(bad ? 1 : 0);
@@ -415,22 +440,21 @@ __global__ void __launch_bounds__(kThreads, 4) quant_read_kernel(const QuantRead
     }
 }
 
-// Heads are split over `parts` warps while the launch has fewer warps than the
-// GPU holds at once (152 SMs x 32): a token's lookups are then repeated, which
-// a launch of that size does not notice, and its heads run side by side.
-int split_heads(int64_t warps, int Hkv, int &heads_per_part)
+// Heads are split over `parts` warps until the launch has at least `want`.
+int split_heads(int64_t warps, int Hkv, int64_t want, int &heads_per_part)
 {
     int parts = 1;
-    while (parts < Hkv && warps * parts < 152 * 32)
+    while (parts < Hkv && warps * parts < want)
         parts *= 2;
     heads_per_part = (Hkv + parts - 1) / parts;
     return (Hkv + heads_per_part - 1) / heads_per_part;
 }
 
 template <class K, class P>
-cudaError_t launch(K kern, const P &p, int64_t warps, cudaStream_t s)
+cudaError_t launch(K kern, const P &p, int64_t warps, int64_t most, cudaStream_t s)
 {
-    const int64_t grid = (warps + kWarps - 1) / kWarps;
+    int64_t grid = (warps + kWarps - 1) / kWarps;
+    grid = grid < most ? grid : most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
     cfg.blockDim = dim3(kThreads);
@@ -445,20 +469,24 @@ cudaError_t launch(K kern, const P &p, int64_t warps, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_quant_append(int d, QuantAppendParams p, cudaStream_t s)
+cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_t s)
 {
     p.groups = p.offsets ? (int64_t)p.T / 8 + 2 * (int64_t)p.B : p.B;
-    p.parts = split_heads(p.groups, p.Hkv, p.heads_per_part);
+    // resident CTAs walk the units: fine ones, so that they end together
+    const int64_t ctas = 3 * (int64_t)sms;
+    p.parts = split_heads(p.groups, p.Hkv, 8 * ctas * kWarps, p.heads_per_part);
     const int64_t warps = p.groups * p.parts;
-    return d == 128 ? launch(quant_append_kernel<128>, p, warps, s) : launch(quant_append_kernel<64>, p, warps, s);
+    return d == 128 ? launch(quant_append_kernel<128>, p, warps, ctas, s) : launch(quant_append_kernel<64>, p, warps, ctas, s);
 }
 
-cudaError_t launch_quant_read(int d, QuantReadParams p, cudaStream_t s)
+cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
 {
     const int64_t chunks = ((int64_t)p.T + 7) / 8;
-    p.parts = split_heads(chunks, p.Hkv, p.heads_per_part);
+    // several waves of short warps: 116k tokens of 8 heads took 104 us with one
+    // wave or three, 99 with eight, 111 with 32
+    p.parts = split_heads(chunks, p.Hkv, 8 * 32 * (int64_t)sms, p.heads_per_part);
     const int64_t warps = chunks * p.parts;
-    return d == 128 ? launch(quant_read_kernel<128>, p, warps, s) : launch(quant_read_kernel<64>, p, warps, s);
+    return d == 128 ? launch(quant_read_kernel<128>, p, warps, INT64_MAX, s) : launch(quant_read_kernel<64>, p, warps, INT64_MAX, s);
 }
 
 }  // namespace pkv
