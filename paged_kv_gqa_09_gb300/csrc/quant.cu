@@ -133,51 +133,21 @@ __device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Codes of the eight values of x (this lane's field f of four words), packed
-// in pairs as they lie in the words.
+// One head's K or V of the warp's eight tokens: x[j] are this lane's dims
+// 32 j + 8 t .. of its token; w[j] becomes its word (t, j).  Returns s | b << 16
+// of group t & (GR - 1) of the token.
 //
-// y = (x - b) / s - 16 comes, over 15, from one fused multiply-add in fp32 and
-// is at most (|c| + 16) 2^-21 off: 1 / (15 s) is within 2^-23 of itself,
-// c = -(16 s + b) / s within 2^-22, and |x / s| <= |c| + 16.  Where it lies
-// further than twice that from every border (halves of a step) the rounded y
-// is the code; elsewhere -- a few in 10^5 -- and where values are beyond the
-// limit, quant_code() decides exactly.
-__device__ __forceinline__ void quant_codes(const uint4 &x4, uint32_t sb, bool wide, int f, uint32_t (&w)[4])
+// In units of codes y = (x - b) / s - 16 comes, over 15, from one fused
+// multiply-add with i = 1 / (15 s) and c = -(16 s + b) i in fp32.  i is within
+// 2^-23 of itself, which scales y as a whole, c is rounded twice more and y
+// once: y is at most (|16 + b / s| + 23) 2^-23 off.  Where it lies further than
+// twice that from every border (halves of a step) the rounded y is the code;
+// elsewhere -- one value in 10^5 -- and where values are beyond the limit,
+// quant_code() decides exactly.
+template <int GR>
+__device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, uint32_t (&w)[GR])
 {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
-    const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-    const float s = __low2float(as_half2(sb)), b = __high2float(as_half2(sb));
-    float i15 = rcp_approx(15.f * s);
-    i15 = s > 0.f ? i15 : 0.f;  // s = 0: code 0; a NaN group: y is NaN, which saturates to 0
-    const float c15 = -fmaf(16.f, s, b) * i15;
-    const float edge = 0.5f - fmaf(fabsf(c15), 15.f * 0x1p-20f, 0x1p-15f);
-    const int sh = f == 1 ? 2 : f == 2 ? 10 : 6;
-    const uint32_t swap = f == 3 ? 0x2301 : 0x3210;
-    float worst = 0.f;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const float2 v = __half22float2(as_half2(x[u]));
-        const float y0 = __saturatef(fmaf(v.x, i15, c15)), y1 = __saturatef(fmaf(v.y, i15, c15));
-        const float n0 = fmaf(y0, 15.f, kMagic), n1 = fmaf(y1, 15.f, kMagic);
-        const float d0 = fmaf(y0, 15.f, kMagic - n0), d1 = fmaf(y1, 15.f, kMagic - n1);
-        worst = fmaxf(fmaxf(worst, fabsf(d0)), fabsf(d1));
-        w[u] = __byte_perm(__float_as_uint(n0), __float_as_uint(n1), 0x5410);
-    }
-    if ((worst > edge || wide) && s > 0.f) {
-        const uint4 e = quant_codes_exact(x4, s, b);
-        w[0] = e.x, w[1] = e.y, w[2] = e.z, w[3] = e.w;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-        w[u] = __byte_perm(w[u] << sh, 0, swap);
-}
-
-// One head's K or V of the warp's eight tokens: x[j] are this lane's dims
-// 32 j + 8 t .. of its token; w[j] becomes its word (t, j), sb[j] the groups'
-// s | b << 16 (the same in all four lanes).
-template <int GR>
-__device__ __forceinline__ void quantise_rows(const uint4 (&x)[GR], int t, uint32_t (&w)[GR], uint32_t (&sb)[GR])
-{
     uint32_t mm[4];  // least | -greatest of the lane's eight values of group j (twice over for GR = 2)
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
@@ -188,7 +158,7 @@ __device__ __forceinline__ void quantise_rows(const uint4 (&x)[GR], int t, uint3
         if (GR == 2)
             mm[j + 2] = mm[j];
     }
-    // lane t ends with group j = t & (GR - 1) of its token
+    // lane t ends with group t & (GR - 1) of its token
     const bool up = (t & 2) != 0, odd = (t & 1) != 0;
     auto least = [](uint32_t a, uint32_t b) { return as_word(__hmin2_nan(as_half2(a), as_half2(b))); };
     const uint32_t k0 = least(up ? mm[2] : mm[0], __shfl_xor_sync(0xffffffffu, up ? mm[0] : mm[2], 2));
@@ -196,20 +166,48 @@ __device__ __forceinline__ void quantise_rows(const uint4 (&x)[GR], int t, uint3
     const uint32_t m = least(odd ? k1 : k0, __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1));
     const float lo0 = __low2float(as_half2(m)), hi0 = -__high2float(as_half2(m));
     const float lo = fminf(fmaxf(lo0, -kQuantLimit), kQuantLimit), hi = fminf(fmaxf(hi0, -kQuantLimit), kQuantLimit);
+    const bool nan = lo0 != lo0 || hi0 != hi0;
     __half s, b;
     quant_params(lo, hi, s, b);
-    uint32_t mine = as_word(s, b);
-    if (lo0 != lo0 || hi0 != hi0)
-        mine = 0x7fff7fffu;  // a NaN in the group
-    const unsigned wide = __ballot_sync(0xffffffffu, lo != lo0 || hi != hi0);
+    const uint32_t mine = nan ? 0x7fff7fffu : as_word(s, b);
+    const float sf = __half2float(s);
+    // s = 0 or NaN: every code is 0
+    const float i_mine = sf > 0.f && !nan ? rcp_approx(15.f * sf) : 0.f;
+    const float c_mine = -fmaf(16.f, sf, __half2float(b)) * i_mine;
+    const unsigned wide = __ballot_sync(0xffffffffu, (lo != lo0 || hi != hi0) && !nan);
     const int base = threadIdx.x & 28;
+    const int sh = t == 1 ? 2 : t == 2 ? 10 : 6;
+    const uint32_t swap = t == 3 ? 0x2301 : 0x3210;
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
-        sb[j] = __shfl_sync(0xffffffffu, mine, base + j);
-        uint32_t c[4];
-        quant_codes(x[j], sb[j], wide >> (base + j) & 1, t, c);
+        const float i15 = __shfl_sync(0xffffffffu, i_mine, base + j), c15 = __shfl_sync(0xffffffffu, c_mine, base + j);
+        const float edge = 0.5f - fmaf(fabsf(c15), 15.f * 0x1p-22f, 0x1p-17f);
+        const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        float worst = 0.f;
+        uint32_t c[4];  // the lane's codes: field t of four words
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float2 v = __half22float2(as_half2(xs[u]));
+            const float y0 = __saturatef(fmaf(v.x, i15, c15)), y1 = __saturatef(fmaf(v.y, i15, c15));
+            const float n0 = fmaf(y0, 15.f, kMagic), n1 = fmaf(y1, 15.f, kMagic);
+            const float d0 = fmaf(y0, 15.f, kMagic - n0), d1 = fmaf(y1, 15.f, kMagic - n1);
+            worst = fmaxf(fmaxf(worst, fabsf(d0)), fabsf(d1));
+            c[u] = __byte_perm(__float_as_uint(n0), __float_as_uint(n1), 0x5410);
+        }
+        const bool near = worst > edge || (wide >> (base + j) & 1);
+        if (__any_sync(0xffffffffu, near)) {
+            const __half2 sb = as_half2(__shfl_sync(0xffffffffu, mine, base + j));
+            if (near && __low2float(sb) > 0.f) {
+                const uint4 e = quant_codes_exact(x[j], __low2float(sb), __high2float(sb));
+                c[0] = e.x, c[1] = e.y, c[2] = e.z, c[3] = e.w;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            c[u] = __byte_perm(c[u] << sh, 0, swap);
         w[j] = quad_or_transpose(c, t);
     }
+    return mine;
 }
 
 // A warp takes the eight cache positions 8 k .. of one row, and heads
@@ -229,10 +227,11 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
     const int e = g & 1, t2 = g >> 1;
     const int tb = 1 << p.tb_log2;
     bool bad = false;
-    for (int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < p.groups * p.parts;
-         unit += (int64_t)gridDim.x * kWarps) {
-        const int64_t gs = unit / p.parts;
-        const int h0 = (int)(unit - gs * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
+    // a warp keeps its part of the heads (those left over when the parts do not divide the warps stay idle)
+    const unsigned warp = blockIdx.x * kWarps + (threadIdx.x >> 5), lines = gridDim.x * kWarps / (unsigned)p.parts;
+    const unsigned line = warp / (unsigned)p.parts;
+    const int h0 = (int)(warp - line * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
+    for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
         int i = (int)gs, off = i, n = 1, k = 0;
         if (p.offsets) {
             i = min(last_not_above(p.B, gs, [&](int r) { return (int64_t)(p.offsets[r] >> 3) + 2 * (int64_t)r; }), p.B - 1);
@@ -279,14 +278,14 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
                 x[j] = next[j];
             if (it + 1 < 2 * (h1 - h0))
                 fetch(it + 1, next);
-            uint32_t w[GR], sb[GR];
-            quantise_rows<GR>(x, t, w, sb);
+            uint32_t w[GR];
+            const uint32_t si = quantise_rows<GR>(x, t, w);  // s | b of group t & (GR - 1)
             if (!(it & 1)) {
+                // s of the groups, then b: lane t writes two of the 2 GR halves
+                const int j = (lane & 28) + ((2 * t) & (GR - 1));
+                const uint32_t a = __shfl_sync(0xffffffffu, si, j), c = __shfl_sync(0xffffffffu, si, j + 1);
                 if (live) {
                     store_words<GR>(hb + (r + g) * Q::kRow + t * GR * 4, w);
-                    // s of the groups, then b: lane t writes two of the 2 GR halves
-                    const int j = (2 * t) & (GR - 1);
-                    const uint32_t a = j ? sb[GR - 2] : sb[0], c = j ? sb[GR - 1] : sb[1];
                     if (t < GR)
                         reinterpret_cast<uint32_t *>(hb + Q::k_params(tb) + (r + g) * Q::kParamRow)[t] =
                             __byte_perm(a, c, 2 * t < GR ? 0x5410 : 0x7632);
@@ -295,14 +294,13 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
             }
             // this lane holds the halves g' = 2 t (low) and 2 t + 1 of its token; with the neighbouring token's it
             // makes the words g' = 2 t + e whole
-            uint32_t o[GR], so = 0, si = 0;  // s | b of group t: the neighbour's, its own
+            uint32_t o[GR];
 #pragma unroll
             for (int j = 0; j < GR; ++j) {
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 4);
                 o[j] = e ? __byte_perm(other, w[j], 0x7632) : __byte_perm(w[j], other, 0x5410);
-                si = j == t ? sb[j] : si;
             }
-            so = __shfl_xor_sync(0xffffffffu, si, 4);
+            const uint32_t so = __shfl_xor_sync(0xffffffffu, si, 4);
             uint8_t *vc = hb + Q::v_codes(tb) + (r >> 3) * Q::kVGroup, *vp = hb + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup;
             if (pair) {
                 store_words<GR>(vc + ((2 * t + e) * 4 + t2) * GR * 4, o);
@@ -474,7 +472,7 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
     p.groups = p.offsets ? (int64_t)p.T / 8 + 2 * (int64_t)p.B : p.B;
     // resident CTAs walk the units: fine ones, so that they end together
     const int64_t ctas = 3 * (int64_t)sms;
-    p.parts = split_heads(p.groups, p.Hkv, 8 * ctas * kWarps, p.heads_per_part);
+    p.parts = split_heads(p.groups, p.Hkv, 4 * ctas * kWarps, p.heads_per_part);
     const int64_t warps = p.groups * p.parts;
     return d == 128 ? launch(quant_append_kernel<128>, p, warps, ctas, s) : launch(quant_append_kernel<64>, p, warps, ctas, s);
 }
