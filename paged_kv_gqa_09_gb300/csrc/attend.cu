@@ -51,6 +51,8 @@ constexpr float kNoMax = -1e30f;  // running maximum before the first score (fin
 // fp16, and most tiles need neither a reduction over tokens nor a rescaling.
 constexpr float kMaxSlack = 8.f;
 
+constexpr int kTableLines = 32;  // lines of the block table each CTA brings into L2 at its start
+
 constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 
 // TBL: log2 of the tokens per block of the 4-bit cache, whose tiles' addresses
@@ -544,61 +546,78 @@ __device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D 
 }
 
 // The states of a (row, head)'s pieces, merged in piece order by the CTA that
-// finished last: warp w takes heads w, w + 4.
+// finished last: warp w takes heads w, w + 4.  Up to 32 pieces at a time: one
+// lane each for the maxima and sums, and their accumulators sixteen loads deep,
+// issued beside those (one L2 round trip for up to sixteen pieces; a long row
+// alone on the GPU has some fifty).
 template <int D>
 __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, int c0, int n)
 {
-    constexpr int VPL = D / 32, kBatch = 8;
+    constexpr int VPL = D / 32, kBatch = 16;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t slots = 2 * kAttnMaxCtas;
     const float *pm = p.partials + slots * p.G * D, *pl = pm + slots * p.G;
+    auto state = [&](int j, int g) { return (int64_t)(j == 0 ? 2 * c0 + 1 : 2 * (c0 + j)) * p.G + g; };
     for (int g = w; g < p.G; g += kCW) {
         float M = kNoMax, Lsum = 0.f, acc[VPL];
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
             acc[v] = 0.f;
-        for (int j0 = 0; j0 < n; j0 += kBatch) {
-            float mj[kBatch], lj[kBatch], x[kBatch][VPL];
+        for (int j0 = 0; j0 < n; j0 += 32) {
+            const int nj = min(n - j0, 32);
+            float mj = kNoMax, lj = 0.f, wj = 0.f;
+            if (lane < nj) {
+                mj = __ldcg(pm + state(j0 + lane, g));
+                lj = __ldcg(pl + state(j0 + lane, g));
+            }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                mj[u] = kNoMax;
-                lj[u] = 0.f;
+            for (int half = 0; half < 32; half += kBatch) {
+                if (half >= nj)
+                    break;
+                float x[kBatch][VPL];
 #pragma unroll
-                for (int v = 0; v < VPL; ++v)
-                    x[u][v] = 0.f;
-                const int j = j0 + u;
-                if (j < n) {
-                    const int64_t s = (int64_t)(j == 0 ? 2 * c0 + 1 : 2 * (c0 + j)) * p.G + g;
-                    mj[u] = __ldcg(pm + s);
-                    lj[u] = __ldcg(pl + s);
-                    if constexpr (VPL == 4) {
-                        const float4 t = __ldcg(reinterpret_cast<const float4 *>(p.partials + s * D) + lane);
-                        x[u][0] = t.x, x[u][1] = t.y, x[u][2] = t.z, x[u][3] = t.w;
+                for (int u = 0; u < kBatch; ++u) {
+                    const int j = half + u;
+                    if (j < nj) {
+                        const float *a = p.partials + state(j0 + j, g) * D;
+                        if constexpr (VPL == 4) {
+                            const float4 t = __ldcg(reinterpret_cast<const float4 *>(a) + lane);
+                            x[u][0] = t.x, x[u][1] = t.y, x[u][2] = t.z, x[u][3] = t.w;
+                        } else {
+                            const float2 t = __ldcg(reinterpret_cast<const float2 *>(a) + lane);
+                            x[u][0] = t.x, x[u][1] = t.y;
+                        }
                     } else {
-                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(p.partials + s * D) + lane);
-                        x[u][0] = t.x, x[u][1] = t.y;
+#pragma unroll
+                        for (int v = 0; v < VPL; ++v)
+                            x[u][v] = 0.f;
                     }
                 }
-            }
-            float mn = M;
+                if (half == 0) {
+                    float mn = fmaxf(mj, M);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                mn = fmaxf(mn, mj[u]);
-            const float so = ex2(M - mn);
-            M = mn;
-            Lsum *= so;
+                    for (int o = 16; o > 0; o >>= 1)
+                        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                    const float f = ex2(M - mn);
+                    M = mn;
+                    wj = ex2(mj - mn);
+                    Lsum = Lsum * f + lj * wj;  // this lane's share
 #pragma unroll
-            for (int v = 0; v < VPL; ++v)
-                acc[v] *= so;
+                    for (int v = 0; v < VPL; ++v)
+                        acc[v] *= f;
+                }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const float sj = ex2(mj[u] - mn);
-                Lsum += lj[u] * sj;
+                for (int u = 0; u < kBatch; ++u) {
+                    const float a = __shfl_sync(0xffffffffu, wj, half + u);
 #pragma unroll
-                for (int v = 0; v < VPL; ++v)
-                    acc[v] += x[u][v] * sj;
+                    for (int v = 0; v < VPL; ++v)
+                        acc[v] = fmaf(x[u][v], a, acc[v]);
+                }
             }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            Lsum += __shfl_xor_sync(0xffffffffu, Lsum, o);
         const float inv = 1.f / Lsum;
         const int64_t oh = (int64_t)unit * p.G + g;  // unit = row * Hkv + head
         __half *out = p.o + oh * D + lane * VPL;
@@ -736,15 +755,16 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
         }
     }
     const int c0 = mt2.w & 0xffff, n = (mt2.w >> 16) + 1;
-    __threadfence();
+    // the barrier orders the warps' states before thread 0's arrival, whose
+    // release and acquire carry that order to the other CTAs of the unit
     if (!meet(cbar, cph))
         return false;
     if (threadIdx.x == 0) {
-        __threadfence();
-        *s_last = atomicAdd(p.counters + c0, 1) == n - 1;
-        if (*s_last)
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.counters + c0) : "memory");
+        *s_last = before == n - 1;
+        if (before == n - 1)
             p.counters[c0] = 0;  // ready for the next launch
-        __threadfence();
     }
     if (!meet(cbar, cph))
         return false;
@@ -856,6 +876,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, TBL>::kCtasPerSm)
         prefetch_tmap(&tmV);
     }
     __syncthreads();
+    // The lengths, the table entries they lead to and the pages behind those are
+    // three DRAM latencies in a row: the CTAs bring the table into L2 together
+    // while the lengths are on their way (a hint: nothing is read).
+    if (threadIdx.x < kTableLines) {
+        const int64_t line = (int64_t)blockIdx.x + (int64_t)threadIdx.x * gridDim.x;
+        if (line * 128 < (int64_t)p.B * p.bt_stride * 4)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.bt) + line * 128));
+    }
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x >= 32 * kCW)
