@@ -1210,7 +1210,7 @@ size_t pkv_attn_workspace_size(const pkv_shape_t *s)
     if (check_shape(s))
         return 0;
     return aws_partials_off(s->B) +
-           (size_t)2 * kAttnMaxCtas * (s->Hq / s->Hkv) * (size_t)(s->d + 2) * sizeof(float);
+           (size_t)2 * kAttnMaxSegs * (s->Hq / s->Hkv) * (size_t)(s->d + 2) * sizeof(float);
 }
 
 int pkv_quant_append(const pkv_shape_t *s, void *d_ws, const void *k_new, const void *v_new, int64_t new_stride,

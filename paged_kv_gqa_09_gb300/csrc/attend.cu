@@ -8,15 +8,18 @@
 // 2.5 d bytes (4-bit) or 4 d (fp16) per token and KV head; HBM bounds it.
 //
 // Work split.  A row's visible tokens lie in T_i tiles (64 tokens of fp16
-// pages, 128 of the 4-bit cache; tiles
-// between the sinks and the window are never touched).  All tiles of the batch
-// in (row, KV head, tile) order form one line, which the CTAs cut into equal
-// runs: every CTA derives the line's length and its own run from the row
-// lengths, so one launch balances rows of any lengths without a plan.  The
-// tiles that a CTA takes of one (row, head) are a piece; a piece that is the
-// whole (row, head) writes o and lse, any other its state (m, l, acc in fp32),
-// and the CTA that finishes a (row, head)'s last piece merges its states in
-// piece order (so the result does not depend on who came last).
+// pages, 128 of the 4-bit cache; those between the sinks and the window are
+// never touched).  All tiles of the batch in (row, KV head, tile) order form one
+// line, cut into equal runs, one per CTA: every CTA derives the line's length
+// and the cuts from the row lengths, so one launch balances rows of any lengths
+// without a plan.  SMs do not stream equally fast (equal runs ended between 0.85
+// and 1.1 of their mean time), so a long run's last three sixteenths are cut off
+// in two parts, which the CTAs claim as they come free.  The tiles that a
+// segment (a run, or a part of one) holds of one (row, head) are a piece; a
+// piece that is the whole (row, head) writes o and lse, any other its state (m,
+// l, acc in fp32), and the CTA that finishes a (row, head)'s last piece merges
+// its states in piece order: the cuts do not depend on who takes a segment or
+// comes last, so neither does the result.
 //
 // CTA: warp 4 is the producer, warps 0..3 the consumers.  The producer walks
 // the run, reads block-table entries a batch of tiles ahead and streams each
@@ -34,6 +37,7 @@
 #include "quant_format.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace pkv {
 namespace {
@@ -126,6 +130,45 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
+// The cuts of the line of W tiles: run r is [r R, (r + 1) R), its segments
+// parts * r + 0 .. parts - 1 in line order: H tiles, then M, then the rest.
+struct Cuts {
+    long long W, R;
+    int H, M, parts;
+    __device__ __forceinline__ int segment(long long x) const
+    {
+        const int r = (int)(x / R);
+        if (parts == 1)
+            return r;
+        const int y = (int)(x - r * R);
+        return 3 * r + (y >= H) + (y >= H + M);
+    }
+    __device__ __forceinline__ long long begin(int r, int part) const { return min(r * R + (part == 0 ? 0 : part == 1 ? H : H + M), W); }
+    __device__ __forceinline__ long long end(int r, int part) const
+    {
+        return part == parts - 1 ? min((r + 1) * R, W) : begin(r, part + 1);
+    }
+};
+
+// Runs of fewer tiles stay whole: their parts would be single tiles, whose
+// states cost as much as they balance.
+constexpr int kMinSplitRun = 48;
+// A claimed part finds its row by a scan over the batch; beyond this many rows
+// runs stay whole too.
+constexpr int kMaxSplitRows = 1024;
+
+__device__ __forceinline__ Cuts make_cuts(long long W, int grid, int B)
+{
+    Cuts c;
+    c.W = W;
+    c.R = max((W + grid - 1) / grid, 1ll);
+    c.parts = c.R >= kMinSplitRun && c.R < (1 << 30) && B <= kMaxSplitRows ? 3 : 1;
+    const int R = (int)min(c.R, 1ll << 30);
+    c.H = R - 3 * (R / 16);
+    c.M = 2 * (R / 16);
+    return c;
+}
+
 // ---------------------------------------------------------------- producer
 
 template <int D, int TBL>
@@ -154,146 +197,165 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         W += __shfl_xor_sync(0xffffffffu, W, o);
-    W *= p.Hkv;
-    const long long chunk = max((W + grid - 1) / grid, 1ll);
-    const long long start = cta * chunk, end = min(start + chunk, W);
+    const Cuts cuts = make_cuts(W * p.Hkv, grid, p.B);
 
     int stage = 0;
     uint32_t ph = 0, pend = 0, pend_par = 0;
     bool ok = true;
-    if (start < end) {
-        // rows [wb, wb + 32), one per lane; row_start: line index of the current row
-        int wb = 0, cur = 0;
-        long long row_start = 0;
-        RowSpan mine;
-        for (; wb < p.B; wb += 32) {  // ends earlier: the run starts inside the line
-            mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
-            int incl = mine.T;
+    int run = cta, part = 0;  // this CTA's own run first
+    while (ok) {
+        const long long start = cuts.begin(run, part), end = cuts.end(run, part);
+        const int seg = cuts.parts * run + part;
+        if (start < end) {
+            // rows [wb, wb + 32), one per lane; row_start: line index of the current row
+            int wb = 0, cur = 0;
+            long long row_start = 0;
+            RowSpan mine;
+            for (; wb < p.B; wb += 32) {  // ends earlier: the segment starts inside the line
+                mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
+                int incl = mine.T;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += y;
-            }
-            const int tot = __shfl_sync(0xffffffffu, incl, 31);
-            if (start < row_start + (long long)tot * p.Hkv) {
-                const unsigned m = __ballot_sync(0xffffffffu, start < row_start + (long long)incl * p.Hkv);
-                cur = __ffs(m) - 1;
-                row_start += (long long)__shfl_sync(0xffffffffu, incl - mine.T, cur) * p.Hkv;
-                break;
-            }
-            row_start += (long long)tot * p.Hkv;
-        }
-        long long f = start;
-        RowSpan rs;
-        auto take = [&](int src) {
-            rs.N = __shfl_sync(0xffffffffu, mine.N, src);
-            rs.ns = __shfl_sync(0xffffffffu, mine.ns, src);
-            rs.w0 = __shfl_sync(0xffffffffu, mine.w0, src);
-            rs.a = __shfl_sync(0xffffffffu, mine.a, src);
-            rs.b = __shfl_sync(0xffffffffu, mine.b, src);
-            rs.T = __shfl_sync(0xffffffffu, mine.T, src);
-        };
-        take(cur);
-        int h = rs.T > 0 ? (int)((f - row_start) / rs.T) : 0;
-        while (f < end && ok && rs.T > 0) {
-            const int i = wb + cur;
-            const long long u0 = row_start + (long long)h * rs.T, u1 = u0 + rs.T;
-            const int k0 = (int)(f - u0), k1 = (int)(min(u1, end) - u0);
-            const int c0 = u0 >= start ? cta : (int)(u0 / chunk), c1 = u1 <= end ? cta : (int)((u1 - 1) / chunk);
-            const int slot = c0 == c1 ? -1 : cta == c0 ? 2 * cta + 1 : 2 * cta;
-            // Block-table entries: lane l holds block l & (2^nbl - 1) of the batch's tile
-            // l >> nbl, a batch ahead of the copies; -1: nothing visible in it, num_pages: bad id.
-            auto page_of = [&](int kb) {
-                const int k = kb + (lane >> nbl);
-                if (k >= k1)
-                    return -1;
-                const int tok = rs.tile(k) * kTile + ((lane & ((1 << nbl) - 1)) << tbl);
-                if (!(tok < rs.ns || (tok + tb > rs.w0 && tok < rs.N)))
-                    return -1;
-                const int pg = p.bt[(int64_t)i * p.bt_stride + (tok >> p.log2P)];
-                if (pg < 0 || pg >= p.num_pages) {
-                    report_error(p.ws, kErrBadPage, i, tok >> p.log2P, pg);
-                    return p.num_pages;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o)
+                        incl += y;
                 }
-                return pg;
-            };
-            int pid = page_of(k0), pnx = -1;
-            for (int k = k0; k < k1; ++k) {
-                const int in_batch = (k - k0) & ((32 >> nbl) - 1);
-                if (in_batch == 0) {
-                    if (k != k0)
-                        pid = pnx;
-                    pnx = page_of(k + (32 >> nbl));
-                }
-                const int tok0 = rs.tile(k) * kTile;
-                const uint32_t full = full0 + stage * 8;
-                if (!__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
-                    report_error(p.ws, kErrTimeout, cta, stage, 0);
-                    ok = false;
+                const int tot = __shfl_sync(0xffffffffu, incl, 31);
+                if (start < row_start + (long long)tot * p.Hkv) {
+                    const unsigned m = __ballot_sync(0xffffffffu, start < row_start + (long long)incl * p.Hkv);
+                    cur = __ffs(m) - 1;
+                    row_start += (long long)__shfl_sync(0xffffffffu, incl - mine.T, cur) * p.Hkv;
                     break;
                 }
-                pend &= ~(1u << stage);
-                const uint32_t dst = sbase + stage * L::kStageBytes;
-                const bool mine_now = (lane >> nbl) == in_batch && pid >= 0;
-                const int b = lane & ((1 << nbl) - 1);
-                const bool bad = QUANT && mine_now && pid == p.num_pages;
-                if (bad) {  // a bad page reads as zeros: zero params make every code 0
-                    uint8_t *blk = basep + (dst - sbase) + b * blk_bytes;
-                    for (int x = 0; x < tb * Q::kParamRow; x += 4) {
-                        *reinterpret_cast<uint32_t *>(blk + Q::k_params(tb) + x) = 0;
-                        *reinterpret_cast<uint32_t *>(blk + Q::v_params(tb) + x) = 0;
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();  // lane 0's arrival publishes the zeros
-                const int copies = __popc(__ballot_sync(0xffffffffu, mine_now && !bad));
-                if (lane == 0) {
-                    const bool whole = rs.ns >= tok0 + kTile || (tok0 >= rs.w0 && tok0 + kTile <= rs.N);
-                    const int flags = (k == k0 ? kFirst : 0) | (k == k1 - 1 ? kLast : 0) | (whole ? 0 : kMasked);
-                    meta[2 * stage] = make_int4(i * p.Hkv + h, tok0, flags, slot);
-                    meta[2 * stage + 1] = make_int4(rs.ns, rs.w0, rs.N, c0 | ((c1 - c0) << 16));
-                    mbar_arrive_expect_tx(full, copies * blk_bytes * (QUANT ? 1 : 2) +
-                                                    (k == k0 ? (uint32_t)(p.G * D * 2) : 0u));
-                    if (k == k0)
-                        bulk_load(dst + L::kKvBytes, p.q + ((int64_t)i * p.Hq + h * p.G) * D, p.G * D * 2, full, pol);
-                }
-                __syncwarp();
-                if (mine_now && !bad) {
-                    const int slot_in = (tok0 + (b << tbl)) & ((1 << p.log2P) - 1);
-                    if constexpr (QUANT) {
-                        bulk_load(dst + b * blk_bytes,
-                                  p.cache + ((int64_t)pid * p.Hkv + h) * p.page_head_bytes +
-                                      (int64_t)(slot_in >> tbl) * blk_bytes,
-                                  blk_bytes, full, pol);
-                    } else {
-                        tma_load_5d(dst + b * blk_bytes, tmK, full, 0, slot_in, 0, h, pid, pol);
-                        tma_load_5d(dst + L::kTileBytes + b * blk_bytes, tmV, full, 0, slot_in, 0, h, pid, pol);
-                    }
-                }
-                pend |= 1u << stage;
-                pend_par = (pend_par & ~(1u << stage)) | (ph << stage);
-                if (++stage == L::kStages) {
-                    stage = 0;
-                    ph ^= 1;
-                }
+                row_start += (long long)tot * p.Hkv;
             }
-            f = u0 + k1;
-            if (++h == p.Hkv && f < end) {  // the next row with visible tokens
-                row_start += (long long)rs.T * p.Hkv;
-                h = 0;
-                unsigned m = __ballot_sync(0xffffffffu, mine.T > 0 && lane > cur);
-                while (!m && wb < p.B) {
-                    wb += 32;
-                    mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
-                    m = __ballot_sync(0xffffffffu, mine.T > 0);
+            long long f = start;
+            RowSpan rs;
+            auto take = [&](int src) {
+                rs.N = __shfl_sync(0xffffffffu, mine.N, src);
+                rs.ns = __shfl_sync(0xffffffffu, mine.ns, src);
+                rs.w0 = __shfl_sync(0xffffffffu, mine.w0, src);
+                rs.a = __shfl_sync(0xffffffffu, mine.a, src);
+                rs.b = __shfl_sync(0xffffffffu, mine.b, src);
+                rs.T = __shfl_sync(0xffffffffu, mine.T, src);
+            };
+            take(cur);
+            int h = rs.T > 0 ? (int)((f - row_start) / rs.T) : 0;
+            while (f < end && ok && rs.T > 0) {
+                const int i = wb + cur;
+                const long long u0 = row_start + (long long)h * rs.T, u1 = u0 + rs.T;
+                const int k0 = (int)(f - u0), k1 = (int)(min(u1, end) - u0);
+                const int c0 = u0 >= start ? seg : cuts.segment(u0), c1 = u1 <= end ? seg : cuts.segment(u1 - 1);
+                const int slot = c0 == c1 ? -1 : seg == c0 ? 2 * seg + 1 : 2 * seg;
+                // Block-table entries: lane l holds block l & (2^nbl - 1) of the batch's tile
+                // l >> nbl, a batch ahead of the copies; -1: nothing visible in it, num_pages: bad id.
+                auto page_of = [&](int kb) {
+                    const int k = kb + (lane >> nbl);
+                    if (k >= k1)
+                        return -1;
+                    const int tok = rs.tile(k) * kTile + ((lane & ((1 << nbl) - 1)) << tbl);
+                    if (!(tok < rs.ns || (tok + tb > rs.w0 && tok < rs.N)))
+                        return -1;
+                    const int pg = p.bt[(int64_t)i * p.bt_stride + (tok >> p.log2P)];
+                    if (pg < 0 || pg >= p.num_pages) {
+                        report_error(p.ws, kErrBadPage, i, tok >> p.log2P, pg);
+                        return p.num_pages;
+                    }
+                    return pg;
+                };
+                int pid = page_of(k0), pnx = -1;
+                for (int k = k0; k < k1; ++k) {
+                    const int in_batch = (k - k0) & ((32 >> nbl) - 1);
+                    if (in_batch == 0) {
+                        if (k != k0)
+                            pid = pnx;
+                        pnx = page_of(k + (32 >> nbl));
+                    }
+                    const int tok0 = rs.tile(k) * kTile;
+                    const uint32_t full = full0 + stage * 8;
+                    if (!__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
+                        report_error(p.ws, kErrTimeout, cta, stage, 0);
+                        ok = false;
+                        break;
+                    }
+                    pend &= ~(1u << stage);
+                    const uint32_t dst = sbase + stage * L::kStageBytes;
+                    const bool mine_now = (lane >> nbl) == in_batch && pid >= 0;
+                    const int b = lane & ((1 << nbl) - 1);
+                    const bool bad = QUANT && mine_now && pid == p.num_pages;
+                    if (bad) {  // a bad page reads as zeros: zero params make every code 0
+                        uint8_t *blk = basep + (dst - sbase) + b * blk_bytes;
+                        for (int x = 0; x < tb * Q::kParamRow; x += 4) {
+                            *reinterpret_cast<uint32_t *>(blk + Q::k_params(tb) + x) = 0;
+                            *reinterpret_cast<uint32_t *>(blk + Q::v_params(tb) + x) = 0;
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();  // lane 0's arrival publishes the zeros
+                    const int copies = __popc(__ballot_sync(0xffffffffu, mine_now && !bad));
+                    if (lane == 0) {
+                        const bool whole = rs.ns >= tok0 + kTile || (tok0 >= rs.w0 && tok0 + kTile <= rs.N);
+                        const int flags = (k == k0 ? kFirst : 0) | (k == k1 - 1 ? kLast : 0) | (whole ? 0 : kMasked);
+                        meta[2 * stage] = make_int4(i * p.Hkv + h, tok0, flags, slot);
+                        meta[2 * stage + 1] = make_int4(rs.ns, rs.w0, rs.N, c0 | ((c1 - c0) << 16));
+                        mbar_arrive_expect_tx(full, copies * blk_bytes * (QUANT ? 1 : 2) +
+                                                        (k == k0 ? (uint32_t)(p.G * D * 2) : 0u));
+                        if (k == k0)
+                            bulk_load(dst + L::kKvBytes, p.q + ((int64_t)i * p.Hq + h * p.G) * D, p.G * D * 2, full, pol);
+                    }
+                    __syncwarp();
+                    if (mine_now && !bad) {
+                        const int slot_in = (tok0 + (b << tbl)) & ((1 << p.log2P) - 1);
+                        if constexpr (QUANT) {
+                            bulk_load(dst + b * blk_bytes,
+                                      p.cache + ((int64_t)pid * p.Hkv + h) * p.page_head_bytes +
+                                          (int64_t)(slot_in >> tbl) * blk_bytes,
+                                      blk_bytes, full, pol);
+                        } else {
+                            tma_load_5d(dst + b * blk_bytes, tmK, full, 0, slot_in, 0, h, pid, pol);
+                            tma_load_5d(dst + L::kTileBytes + b * blk_bytes, tmV, full, 0, slot_in, 0, h, pid, pol);
+                        }
+                    }
+                    pend |= 1u << stage;
+                    pend_par = (pend_par & ~(1u << stage)) | (ph << stage);
+                    if (++stage == L::kStages) {
+                        stage = 0;
+                        ph ^= 1;
+                    }
                 }
-                if (!m)
-                    break;  // the lengths changed under the launch
-                cur = __ffs(m) - 1;
-                take(cur);
+                f = u0 + k1;
+                if (++h == p.Hkv && f < end) {  // the next row with visible tokens
+                    row_start += (long long)rs.T * p.Hkv;
+                    h = 0;
+                    unsigned m = __ballot_sync(0xffffffffu, mine.T > 0 && lane > cur);
+                    while (!m && wb < p.B) {
+                        wb += 32;
+                        mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
+                        m = __ballot_sync(0xffffffffu, mine.T > 0);
+                    }
+                    if (!m)
+                        break;  // the lengths changed under the launch
+                    cur = __ffs(m) - 1;
+                    take(cur);
+                }
             }
         }
+        if (cuts.parts == 1)
+            break;
+        // the next part to be claimed: every run's second, then every run's last
+        int q = 0;
+        if (lane == 0)
+            q = atomicAdd(&p.ws->next_task, 1);
+        q = __shfl_sync(0xffffffffu, q, 0);
+        if (q >= 2 * grid)
+            break;
+        part = q < grid ? 1 : 2;
+        run = q < grid ? q : q - grid;
+    }
+    if (cuts.parts > 1 && lane == 0 && atomicAdd(&p.ws->done_ctas, 1) == grid - 1) {
+        // every CTA has made its last claim: ready for the next launch
+        p.ws->next_task = 0;
+        p.ws->done_ctas = 0;
     }
     if (ok) {
         if (__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
@@ -483,29 +545,31 @@ __device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D 
     auto group = [&](int u) { return kv + ((32 * w + 8 * u) >> TBL) * Q::bytes(TB); };  // its block
     auto in = [&](int u) { return (32 * w + 8 * u) & (TB - 1); };                       // its first token there
     float x[MT][4];
+    uint32_t k0[MT][GR], k1[MT][GR], c0[MT][GR], c1[MT][GR];  // K words of tokens r0 and r0 + 8, and their s and b
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
-        uint32_t k0[GR], k1[GR], c0[GR], c1[GR];
         const uint8_t *g0 = group(2 * u), *g1 = group(2 * u + 1);
-        lds_words<GR>(g0 + (in(2 * u) + r0) * Q::kRow + t * GR * 4, k0);
-        lds_words<GR>(g1 + (in(2 * u + 1) + r0) * Q::kRow + t * GR * 4, k1);
-        lds_words<GR>(g0 + Q::k_params(TB) + (in(2 * u) + r0) * Q::kParamRow, c0);  // s of GR groups, then b
-        lds_words<GR>(g1 + Q::k_params(TB) + (in(2 * u + 1) + r0) * Q::kParamRow, c1);
+        lds_words<GR>(g0 + (in(2 * u) + r0) * Q::kRow + t * GR * 4, k0[u]);
+        lds_words<GR>(g1 + (in(2 * u + 1) + r0) * Q::kRow + t * GR * 4, k1[u]);
+        lds_words<GR>(g0 + Q::k_params(TB) + (in(2 * u) + r0) * Q::kParamRow, c0[u]);
+        lds_words<GR>(g1 + Q::k_params(TB) + (in(2 * u + 1) + r0) * Q::kParamRow, c1[u]);
         x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
+    }
 #pragma unroll
-        for (int j = 0; j < GR; ++j) {
-            const __half2 s0 = as_half2(c0[j >> 1]), b0 = as_half2(c0[(GR + j) >> 1]);
-            const __half2 s1 = as_half2(c1[j >> 1]), b1 = as_half2(c1[(GR + j) >> 1]);
+    for (int j = 0; j < GR; ++j)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {  // the two blocks' accumulations in turn: neither waits for its last product
+            const __half2 s0 = as_half2(c0[u][j >> 1]), b0 = as_half2(c0[u][(GR + j) >> 1]);
+            const __half2 s1 = as_half2(c1[u][j >> 1]), b1 = as_half2(c1[u][(GR + j) >> 1]);
             const __half2 s0j = (j & 1) ? __high2half2(s0) : __low2half2(s0), b0j = (j & 1) ? __high2half2(b0) : __low2half2(b0);
             const __half2 s1j = (j & 1) ? __high2half2(s1) : __low2half2(s1), b1j = (j & 1) ? __high2half2(b1) : __low2half2(b1);
-            mma_16816(x[u], quant_value(quant_field<0>(k0[j]), s0j, b0j), quant_value(quant_field<0>(k1[j]), s1j, b1j),
-                      quant_value(quant_field<1>(k0[j]), s0j, b0j), quant_value(quant_field<1>(k1[j]), s1j, b1j),
+            mma_16816(x[u], quant_value(quant_field<0>(k0[u][j]), s0j, b0j), quant_value(quant_field<0>(k1[u][j]), s1j, b1j),
+                      quant_value(quant_field<1>(k0[u][j]), s0j, b0j), quant_value(quant_field<1>(k1[u][j]), s1j, b1j),
                       qf[2 * j][0], qf[2 * j][1]);
-            mma_16816(x[u], quant_value(quant_field<2>(k0[j]), s0j, b0j), quant_value(quant_field<2>(k1[j]), s1j, b1j),
-                      quant_value(quant_field<3>(k0[j]), s0j, b0j), quant_value(quant_field<3>(k1[j]), s1j, b1j),
+            mma_16816(x[u], quant_value(quant_field<2>(k0[u][j]), s0j, b0j), quant_value(quant_field<2>(k1[u][j]), s1j, b1j),
+                      quant_value(quant_field<3>(k0[u][j]), s0j, b0j), quant_value(quant_field<3>(k1[u][j]), s1j, b1j),
                       qf[2 * j + 1][0], qf[2 * j + 1][1]);
         }
-    }
     uint32_t P[MT][2];
     softmax_step<D, MT>(st, x, vis, sl2, P);
 #pragma unroll
@@ -545,89 +609,112 @@ __device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D 
     }
 }
 
-// The states of a (row, head)'s pieces, merged in piece order by the CTA that
-// finished last: warp w takes heads w, w + 4.  Up to 32 pieces at a time: one
-// lane each for the maxima and sums, and their accumulators sixteen loads deep,
-// issued beside those (one L2 round trip for up to sixteen pieces; a long row
-// alone on the GPU has some fifty).
+// The states of a (row, head)'s n pieces, merged in piece order by the CTA that
+// finished last.  A warp takes a head at a time, or two when there are more
+// heads than warps.  Up to 32 pieces: one lane each for the maxima and sums, and
+// their accumulators eight loads deep, issued beside those.
 template <int D>
 __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, int c0, int n)
 {
-    constexpr int VPL = D / 32, kBatch = 16;
+    constexpr int VPL = D / 32, kBatch = 8;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t slots = 2 * kAttnMaxCtas;
+    const int64_t slots = 2 * kAttnMaxSegs;
     const float *pm = p.partials + slots * p.G * D, *pl = pm + slots * p.G;
-    auto state = [&](int j, int g) { return (int64_t)(j == 0 ? 2 * c0 + 1 : 2 * (c0 + j)) * p.G + g; };
-    for (int g = w; g < p.G; g += kCW) {
-        float M = kNoMax, Lsum = 0.f, acc[VPL];
+    auto state = [&](int j, int g) { return (j == 0 ? 2 * c0 + 1 : 2 * (c0 + j)) * p.G + g; };
+    auto merge = [&](auto heads) {  // heads w, w + 4, .. heads of them
+        constexpr int NH = decltype(heads)::value, kPer = kBatch / NH;
+        float M[NH], L[NH], acc[NH][VPL];
 #pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            acc[v] = 0.f;
+        for (int q = 0; q < NH; ++q) {
+            M[q] = kNoMax;
+            L[q] = 0.f;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                acc[q][v] = 0.f;
+        }
         for (int j0 = 0; j0 < n; j0 += 32) {
             const int nj = min(n - j0, 32);
-            float mj = kNoMax, lj = 0.f, wj = 0.f;
-            if (lane < nj) {
-                mj = __ldcg(pm + state(j0 + lane, g));
-                lj = __ldcg(pl + state(j0 + lane, g));
+            float mj[NH], lj[NH], wj[NH];
+#pragma unroll
+            for (int q = 0; q < NH; ++q) {
+                const int g = w + kCW * q;
+                mj[q] = kNoMax;
+                lj[q] = wj[q] = 0.f;
+                if (lane < nj && g < p.G) {
+                    mj[q] = __ldcg(pm + state(j0 + lane, g));
+                    lj[q] = __ldcg(pl + state(j0 + lane, g));
+                }
             }
+            for (int b = 0; b < nj; b += kPer) {
+                float x[kPer][NH][VPL];
 #pragma unroll
-            for (int half = 0; half < 32; half += kBatch) {
-                if (half >= nj)
-                    break;
-                float x[kBatch][VPL];
+                for (int u = 0; u < kPer; ++u)
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int j = half + u;
-                    if (j < nj) {
-                        const float *a = p.partials + state(j0 + j, g) * D;
-                        if constexpr (VPL == 4) {
-                            const float4 t = __ldcg(reinterpret_cast<const float4 *>(a) + lane);
-                            x[u][0] = t.x, x[u][1] = t.y, x[u][2] = t.z, x[u][3] = t.w;
-                        } else {
-                            const float2 t = __ldcg(reinterpret_cast<const float2 *>(a) + lane);
-                            x[u][0] = t.x, x[u][1] = t.y;
-                        }
-                    } else {
+                    for (int q = 0; q < NH; ++q) {
+                        const int g = w + kCW * q;
 #pragma unroll
                         for (int v = 0; v < VPL; ++v)
-                            x[u][v] = 0.f;
+                            x[u][q][v] = 0.f;
+                        if (b + u < nj && g < p.G) {
+                            const float *a = p.partials + (int64_t)state(j0 + b + u, g) * D;
+                            if constexpr (VPL == 4) {
+                                const float4 t = __ldcg(reinterpret_cast<const float4 *>(a) + lane);
+                                x[u][q][0] = t.x, x[u][q][1] = t.y, x[u][q][2] = t.z, x[u][q][3] = t.w;
+                            } else {
+                                const float2 t = __ldcg(reinterpret_cast<const float2 *>(a) + lane);
+                                x[u][q][0] = t.x, x[u][q][1] = t.y;
+                            }
+                        }
                     }
-                }
-                if (half == 0) {
-                    float mn = fmaxf(mj, M);
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1)
-                        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-                    const float f = ex2(M - mn);
-                    M = mn;
-                    wj = ex2(mj - mn);
-                    Lsum = Lsum * f + lj * wj;  // this lane's share
+                for (int q = 0; q < NH; ++q) {
+                    if (b == 0) {
+                        float mn = fmaxf(mj[q], M[q]);
 #pragma unroll
-                    for (int v = 0; v < VPL; ++v)
-                        acc[v] *= f;
-                }
+                        for (int o = 16; o > 0; o >>= 1)
+                            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                        const float f = ex2(M[q] - mn);
+                        M[q] = mn;
+                        wj[q] = ex2(mj[q] - mn);
+                        L[q] = L[q] * f + lj[q] * wj[q];  // this lane's share
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const float a = __shfl_sync(0xffffffffu, wj, half + u);
+                        for (int v = 0; v < VPL; ++v)
+                            acc[q][v] *= f;
+                    }
 #pragma unroll
-                    for (int v = 0; v < VPL; ++v)
-                        acc[v] = fmaf(x[u][v], a, acc[v]);
+                    for (int u = 0; u < kPer; ++u) {
+                        const float a = __shfl_sync(0xffffffffu, wj[q], b + u);
+#pragma unroll
+                        for (int v = 0; v < VPL; ++v)
+                            acc[q][v] = fmaf(x[u][q][v], a, acc[q][v]);
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            Lsum += __shfl_xor_sync(0xffffffffu, Lsum, o);
-        const float inv = 1.f / Lsum;
-        const int64_t oh = (int64_t)unit * p.G + g;  // unit = row * Hkv + head
-        __half *out = p.o + oh * D + lane * VPL;
-        if constexpr (VPL == 4)
-            *reinterpret_cast<uint2 *>(out) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv), pack_half2(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t *>(out) = pack_half2(acc[0] * inv, acc[1] * inv);
-        if (p.lse && lane == 0)
-            p.lse[oh] = (M + log2f(Lsum)) * kLn2;
-    }
+        for (int q = 0; q < NH; ++q) {
+            const int g = w + kCW * q;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                L[q] += __shfl_xor_sync(0xffffffffu, L[q], o);
+            if (g >= p.G)
+                continue;
+            const float inv = 1.f / L[q];
+            const int64_t oh = (int64_t)unit * p.G + g;  // unit = row * Hkv + head
+            __half *out = p.o + oh * D + lane * VPL;
+            if constexpr (VPL == 4)
+                *reinterpret_cast<uint2 *>(out) = make_uint2(pack_half2(acc[q][0] * inv, acc[q][1] * inv),
+                                                             pack_half2(acc[q][2] * inv, acc[q][3] * inv));
+            else
+                *reinterpret_cast<uint32_t *>(out) = pack_half2(acc[q][0] * inv, acc[q][1] * inv);
+            if (p.lse && lane == 0)
+                p.lse[oh] = (M[q] + log2f(L[q])) * kLn2;
+        }
+    };
+    if (p.G > kCW)
+        merge(std::integral_constant<int, 2>());
+    else
+        merge(std::integral_constant<int, 1>());
 }
 
 // A piece's end: the four warps' states become one, each warp merging its
@@ -742,7 +829,7 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
             }
         }
         if (w == 0 && lane < 4) {
-            const int64_t slots = 2 * kAttnMaxCtas;
+            const int64_t slots = 2 * kAttnMaxSegs;
             float *pm = p.partials + slots * G * D + (int64_t)slot * G, *pl = pm + slots * G;
             if (ok0) {
                 pm[h0] = M0;

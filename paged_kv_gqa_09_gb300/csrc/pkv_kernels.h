@@ -109,11 +109,13 @@ struct AppendParams {
 };
 
 // Workspace of the windowed and 4-bit operators: the header, one int per row
-// (rows that an append refuses), one counter per CTA, then the partial states.
+// (rows that an append refuses), one counter per segment of the attention's
+// work (at most three per CTA), then two partial states per segment.
 constexpr int kAttnMaxCtas = 512;
+constexpr int kAttnMaxSegs = 3 * kAttnMaxCtas;
 inline size_t aws_row_bad_off() { return kWsHeaderBytes; }
 inline size_t aws_counters_off(int B) { return (kWsHeaderBytes + sizeof(int32_t) * (size_t)B + 15) & ~(size_t)15; }
-inline size_t aws_partials_off(int B) { return aws_counters_off(B) + sizeof(int32_t) * (size_t)kAttnMaxCtas; }
+inline size_t aws_partials_off(int B) { return aws_counters_off(B) + sizeof(int32_t) * (size_t)kAttnMaxSegs; }
 
 struct QuantAppendParams {
     const __half *k_new, *v_new;
@@ -149,7 +151,7 @@ struct AttendParams {
     const int32_t *bt, *seq_lens;
     const uint8_t *cache;     // the 4-bit cache (nullptr: fp16 pages, through the tensor maps)
     WsHeader *ws;
-    int32_t *counters;        // [kAttnMaxCtas], zero between launches
+    int32_t *counters;        // [kAttnMaxSegs], zero between launches
     float *partials;
     __half *o;
     float *lse;  // nullable
