@@ -6,10 +6,11 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
-from .build import LIB
+from .build import CALL, LIB
 
 PKV_OK = 0
 PKV_EINVAL = -1
@@ -184,6 +185,27 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = L
         return L
+
+
+_call = None
+
+
+def load_call():
+    """The compiled argument marshalling (csrc/binding.cpp), bound to the loaded libpkv."""
+    global _call
+    if _call is None:
+        L = load()
+        if not os.path.exists(CALL):
+            raise PkvLibraryError(f"_pkv_call.so not found at {CALL}: build it with "
+                                  "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_pkv_call", CALL)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
+                 ("pkv_attn_workspace_size", "pkv_quant_append", "pkv_quant_read", "pkv_quant_decode",
+                  "pkv_window_decode")))
+        _call = m
+    return _call
 
 
 def last_error() -> str:

@@ -374,99 +374,33 @@ def pkv_attn_workspace_size(shape: Shape) -> int:
     return int(n)
 
 
-# These calls are made per layer and token, so their checks read each tensor
-# once and the current device and stream once per call.
-
-def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, dev: int, n: int) -> int:
-    """Pointer of a contiguous CUDA tensor of `dtype` with at least n elements on device `dev`."""
-    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous() \
-            and t.numel() >= n:
-        return t.data_ptr()
-    _dev(t, name, dtype)  # raises unless the size is what is wrong
-    raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
-
-
-def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-_attn_ws_bytes: dict = {}
-
-
-def _attn_ws(shape: Shape, ws: torch.Tensor, dev: int) -> int:
-    key = (shape.B, shape.Hq, shape.Hkv, shape.d)
-    need = _attn_ws_bytes.get(key)
-    if need is None:
-        need = pkv_attn_workspace_size(shape)
-        if len(_attn_ws_bytes) < 4096:
-            _attn_ws_bytes[key] = need
-    if not (isinstance(ws, torch.Tensor) and ws.get_device() == dev and ws.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
-    if ws.numel() * ws.element_size() < need:
-        raise ValueError(f"workspace has {ws.numel() * ws.element_size()} bytes, needs {need}")
-    return ws.data_ptr()
-
-
-def _table(shape: Shape, block_table, seq_lens, dev: int) -> tuple[int, int]:
-    return (_arg(block_table, "block_table", torch.int32, dev, shape.B * shape.bt_stride),
-            _arg(seq_lens, "seq_lens", torch.int32, dev, shape.B))
-
-
-def _quant(shape: Shape, t: torch.Tensor, dev: int) -> int:
-    return _arg(t, "quant_cache", torch.uint8, dev, shape.num_pages * shape.Hkv * (shape.page_size * shape.d * 5 // 4))
-
-
-def _packed(shape: Shape, k: torch.Tensor, v: torch.Tensor, what: str, dev: int) -> tuple[int, int, int, int]:
-    """(k pointer, v pointer, tokens, token stride) of packed fp16 K and V
-    [T, Hkv, d], whose tokens may be strided (alike in both)."""
-    Hkv, d = shape.Hkv, shape.d
-    T = k.shape[0]
-    stride = k.stride(0) if T > 1 else Hkv * d
-    for t, name in ((k, "k_"), (v, "v_")):
-        if t.get_device() != dev:
-            raise ValueError(f"{name}{what} must be a CUDA tensor on the current device (got {t.device})")
-        if t.dtype is not torch.float16:
-            raise ValueError(f"{name}{what} must be torch.float16 (got {t.dtype})")
-        if t.shape != (T, Hkv, d):
-            raise ValueError(f"{name}{what} must be [{T}, {Hkv}, {d}] (got {tuple(t.shape)})")
-        s0, s1, s2 = t.stride()
-        if T and (s2 != 1 or (Hkv > 1 and s1 != d)):
-            raise ValueError(f"{name}{what} must be contiguous within a token (strides {t.stride()})")
-        if T > 1 and s0 != stride:
-            raise ValueError(f"k_{what} and v_{what} must have one token stride")
-    return k.data_ptr(), v.data_ptr(), T, stride
-
+# These four are called per layer and token, where the host's share counts: their
+# tensors are checked and unpacked by compiled code (csrc/binding.cpp), which
+# raises TypeError or ValueError as the functions above do.
 
 def pkv_quant_append(shape, ws, k_new, v_new, block_table, seq_lens, quant_cache, new_offsets=None,
                      seq_lens_out=None, stream=None) -> None:
     """Quantise new tokens k_new, v_new [T, Hkv, d] into the 4-bit cache behind
     each row's seq_lens tokens: row i's are new_offsets[i] .. new_offsets[i + 1]
     (None: one per row).  The advanced lengths go to seq_lens_out (None: in
-    place).  See include/pkv.h."""
-    L, dev = _lib.load(), _device()
-    kp, vp, T, stride = _packed(shape, k_new, v_new, "new", dev)
-    bp, sp = _table(shape, block_table, seq_lens, dev)
-    op = 0 if new_offsets is None else _arg(new_offsets, "new_offsets", torch.int32, dev, shape.B + 1)
-    lp = sp if seq_lens_out is None else _arg(seq_lens_out, "seq_lens_out", torch.int32, dev, shape.B)
-    check(L.pkv_quant_append(ctypes.byref(shape), _attn_ws(shape, ws, dev), kp, vp, stride, T, op, bp, sp, lp,
-                             _quant(shape, quant_cache, dev), _raw_stream(stream, dev)), "pkv_quant_append")
+    place).  Tokens may be strided (a slice of a fused projection).  See
+    include/pkv.h."""
+    st = (_lib._call or _lib.load_call()).quant_append(
+        shape, ws, k_new, v_new, block_table, seq_lens, quant_cache, new_offsets, seq_lens_out,
+        None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_quant_append")
 
 
 def pkv_quant_read(shape, ws, quant_cache, block_table, seq_lens, out_offsets, k_out, v_out, first=None,
                    stream=None) -> None:
     """Read tokens first[i] .. of each row (None: from token 0) back as fp16 into
     rows out_offsets[i] .. out_offsets[i + 1] of k_out, v_out [T, Hkv, d]."""
-    L, dev = _lib.load(), _device()
-    kp, vp, T, stride = _packed(shape, k_out, v_out, "out", dev)
-    bp, sp = _table(shape, block_table, seq_lens, dev)
-    fp = 0 if first is None else _arg(first, "first", torch.int32, dev, shape.B)
-    op = _arg(out_offsets, "out_offsets", torch.int32, dev, shape.B + 1)
-    check(L.pkv_quant_read(ctypes.byref(shape), _attn_ws(shape, ws, dev), _quant(shape, quant_cache, dev), bp, sp, fp,
-                           op, T, kp, vp, stride, _raw_stream(stream, dev)), "pkv_quant_read")
+    st = (_lib._call or _lib.load_call()).quant_read(
+        shape, ws, quant_cache, block_table, seq_lens, out_offsets, k_out, v_out, first,
+        None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_quant_read")
 
 
 def pkv_quant_decode(shape, ws, q, quant_cache, block_table, seq_lens, o, lse=None, window=None, sinks=0,
@@ -475,32 +409,22 @@ def pkv_quant_decode(shape, ws, q, quant_cache, block_table, seq_lens, o, lse=No
     first `sinks` and last `window` tokens."""
     if window is None and sinks:
         raise ValueError("sinks go with a window")
-    L, dev = _lib.load(), _device()
-    n = shape.B * shape.Hq
-    bp, sp = _table(shape, block_table, seq_lens, dev)
-    win = None if window is None else ctypes.byref(Window(window, sinks))
-    check(L.pkv_quant_decode(ctypes.byref(shape), win, _attn_ws(shape, ws, dev),
-                             _arg(q, "q", torch.float16, dev, n * shape.d), _quant(shape, quant_cache, dev), bp, sp,
-                             _arg(o, "o", torch.float16, dev, n * shape.d),
-                             0 if lse is None else _arg(lse, "lse", torch.float32, dev, n),
-                             _raw_stream(stream, dev)), "pkv_quant_decode")
+    st = (_lib._call or _lib.load_call()).quant_decode(
+        shape, ws, q, quant_cache, block_table, seq_lens, o, lse, window, sinks,
+        None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_quant_decode")
 
 
 def pkv_window_decode(shape, ws, q, k_cache, v_cache, block_table, seq_lens, window, sinks, o, lse=None,
                       stream=None) -> None:
     """Decode attention over the fp16 pages, of each row's first `sinks` and last
     `window` tokens."""
-    L, dev = _lib.load(), _device()
-    n = shape.B * shape.Hq
-    pages = shape.num_pages * shape.page_size * shape.Hkv * shape.d
-    bp, sp = _table(shape, block_table, seq_lens, dev)
-    check(L.pkv_window_decode(ctypes.byref(shape), ctypes.byref(Window(window, sinks)), _attn_ws(shape, ws, dev),
-                              _arg(q, "q", torch.float16, dev, n * shape.d),
-                              _arg(k_cache, "k_cache", torch.float16, dev, pages),
-                              _arg(v_cache, "v_cache", torch.float16, dev, pages), bp, sp,
-                              _arg(o, "o", torch.float16, dev, n * shape.d),
-                              0 if lse is None else _arg(lse, "lse", torch.float32, dev, n),
-                              _raw_stream(stream, dev)), "pkv_window_decode")
+    st = (_lib._call or _lib.load_call()).window_decode(
+        shape, ws, q, k_cache, v_cache, block_table, seq_lens, window, sinks, o, lse,
+        None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_window_decode")
 
 
 def pkv_policy_default() -> PolicyCfg:

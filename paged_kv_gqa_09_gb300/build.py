@@ -1,8 +1,9 @@
 """Build libpkv.so (the CUDA kernels and the C ABI) for sm_103a, in-tree.
 
 Each ``csrc/*.cu`` is compiled to an object in parallel by nvcc and linked
-into ``paged_kv_gqa_09_gb300/_build/libpkv.so``.  Runs on a machine without a
-GPU (nvcc cross-compiles).
+into ``paged_kv_gqa_09_gb300/_build/libpkv.so``; beside it the host compiler
+builds ``_pkv_call.so`` from ``csrc/binding.cpp`` against the running Python
+and PyTorch.  Runs on a machine without a GPU (nvcc cross-compiles).
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
+CALL = os.path.join(OUT_DIR, "_pkv_call.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,11 +45,23 @@ def _deps():
         glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "pkv.h")]
 
 
+def _call_command(out: str) -> list[str]:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    libs = os.path.join(home, "lib")
+    return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+            *[x for i in inc for x in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALL)):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
+    return all(os.path.getmtime(f) <= t for f in [*_deps(), os.path.join(CSRC, "binding.cpp")])
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -65,8 +80,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
+    def compile_call():
+        out = CALL + f".tmp{os.getpid()}"
+        r = subprocess.run(_call_command(out), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the host compiler failed on binding.cpp:\n{r.stderr}")
+        return out
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        call = ex.submit(compile_call)
         results = list(ex.map(compile_one, _sources()))
+        call_tmp = call.result()
     if verbose or ptxas_verbose:
         for _, err in results:
             if err:
@@ -77,6 +101,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(call_tmp, CALL)
     return LIB
 
 

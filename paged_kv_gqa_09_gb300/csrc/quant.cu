@@ -210,6 +210,81 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, u
     return mine;
 }
 
+// V of one token alone, by its quad: the halves it owns in words it shares with
+// its neighbour (token 2 t2 + e of the eight from r & ~7 of block hb).
+template <int D>
+__device__ __forceinline__ void store_v_token(uint8_t *hb, int tb, int r, int t, int t2, int e,
+                                              const uint32_t (&w)[QuantLayout<D>::GR], uint32_t si)
+{
+    using Q = QuantLayout<D>;
+    constexpr int GR = Q::GR;
+    uint16_t *c16 = reinterpret_cast<uint16_t *>(hb + Q::v_codes(tb) + (r >> 3) * Q::kVGroup);
+    uint16_t *p16 = reinterpret_cast<uint16_t *>(hb + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup);
+#pragma unroll
+    for (int j = 0; j < GR; ++j) {
+        c16[((2 * t * 4 + t2) * GR + j) * 2 + e] = (uint16_t)w[j];
+        c16[(((2 * t + 1) * 4 + t2) * GR + j) * 2 + e] = (uint16_t)(w[j] >> 16);
+    }
+    if (t < GR) {
+        p16[(t2 * GR + t) * 4 + e] = (uint16_t)si;
+        p16[(t2 * GR + t) * 4 + 2 + e] = (uint16_t)(si >> 16);
+    }
+}
+
+// One new token per row: a CTA per row, which alone reads and advances its
+// length; warp 0 takes K and warp 1 V, eight heads at a time, a quad each.  The
+// values do not depend on the length, so the three loads a token's place hangs
+// on (length, table entry) run beside theirs.
+template <int D>
+__global__ void __launch_bounds__(64) quant_append_one_kernel(const QuantAppendParams p)
+{
+    using Q = QuantLayout<D>;
+    constexpr int GR = Q::GR;
+    pdl_wait();
+    pdl_trigger();
+    const int i = blockIdx.x, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, side = threadIdx.x >> 5;
+    const __half *from = (side ? p.v_new : p.k_new) + (int64_t)i * p.new_stride + 8 * t;
+    const int N = p.seq_lens[i];
+    int page = -1;
+    if (N < 0 || N >= p.len_cap) {
+        if (threadIdx.x == 0)
+            report_error(p.ws, N < 0 ? kErrNegLen : kErrTooLong, i, N < 0 ? N : N + 1, N < 0 ? 0 : p.len_cap);
+    } else {
+        page = p.bt[(int64_t)i * p.bt_stride + (N >> p.log2P)];
+        if (page < 0 || page >= p.num_pages) {
+            if (threadIdx.x == 0)
+                report_error(p.ws, kErrBadPage, i, N >> p.log2P, page);
+            page = -1;
+        }
+    }
+    const int tb = 1 << p.tb_log2, slot = N & ((1 << p.log2P) - 1), r = slot & (tb - 1), t2 = (r & 7) >> 1, e = r & 1;
+    uint8_t *blk = p.cache + (int64_t)max(page, 0) * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
+    for (int h0 = 0; h0 < p.Hkv; h0 += 8) {
+        const int h = h0 + g;
+        uint4 x[GR];
+#pragma unroll
+        for (int j = 0; j < GR; ++j)
+            x[j] = h < p.Hkv ? *reinterpret_cast<const uint4 *>(from + h * D + 32 * j) : make_uint4(0, 0, 0, 0);
+        uint32_t w[GR];
+        const uint32_t si = quantise_rows<GR>(x, t, w);
+        const int j = (lane & 28) + ((2 * t) & (GR - 1));
+        const uint32_t a = __shfl_sync(0xffffffffu, si, j), c = __shfl_sync(0xffffffffu, si, j + 1);
+        if (page < 0 || h >= p.Hkv)
+            continue;
+        uint8_t *hb = blk + h * p.page_head_bytes;
+        if (side == 0) {
+            store_words<GR>(hb + r * Q::kRow + t * GR * 4, w);
+            if (t < GR)
+                reinterpret_cast<uint32_t *>(hb + Q::k_params(tb) + r * Q::kParamRow)[t] = __byte_perm(a, c, 2 * t < GR ? 0x5410 : 0x7632);
+        } else {
+            store_v_token<D>(hb, tb, r, t, t2, e, w, si);
+        }
+    }
+    __syncthreads();  // every thread has read N before it changes
+    if (threadIdx.x == 0)
+        p.seq_lens_out[i] = page >= 0 ? N + 1 : N;
+}
+
 // A warp takes the eight cache positions 8 k .. of one row, and heads
 // [h0, h1), then the next such unit a grid further on.  Rows share one line of
 // such groups: row i's are at offsets[i] / 8 + 2 i .., which leaves room for a
@@ -232,13 +307,9 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
     const unsigned line = warp / (unsigned)p.parts;
     const int h0 = (int)(warp - line * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
     for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
-        int i = (int)gs, off = i, n = 1, k = 0;
-        if (p.offsets) {
-            i = min(last_not_above(p.B, gs, [&](int r) { return (int64_t)(p.offsets[r] >> 3) + 2 * (int64_t)r; }), p.B - 1);
-            off = p.offsets[i];
-            n = p.offsets[i + 1] - off;
-            k = (int)(gs - (off >> 3) - 2 * (int64_t)i);
-        }
+        const int i = min(last_not_above(p.B, gs, [&](int r) { return (int64_t)(p.offsets[r] >> 3) + 2 * (int64_t)r; }), p.B - 1);
+        const int off = p.offsets[i], n = p.offsets[i + 1] - off;
+        const int k = (int)(gs - (off >> 3) - 2 * (int64_t)i);
         const int N = p.seq_lens[i];
         if (k < 0 || !append_fits(p, i, N, off, n, false))
             continue;
@@ -307,16 +378,7 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
                 if (t < GR)
                     reinterpret_cast<uint32_t *>(vp)[(t2 * GR + t) * 2 + e] = e ? __byte_perm(so, si, 0x7632) : __byte_perm(si, so, 0x5410);
             } else if (live) {
-                uint16_t *c16 = reinterpret_cast<uint16_t *>(vc), *p16 = reinterpret_cast<uint16_t *>(vp);
-#pragma unroll
-                for (int j = 0; j < GR; ++j) {
-                    c16[((2 * t * 4 + t2) * GR + j) * 2 + e] = (uint16_t)w[j];
-                    c16[(((2 * t + 1) * 4 + t2) * GR + j) * 2 + e] = (uint16_t)(w[j] >> 16);
-                }
-                if (t < GR) {
-                    p16[(t2 * GR + t) * 4 + e] = (uint16_t)si;
-                    p16[(t2 * GR + t) * 4 + 2 + e] = (uint16_t)(si >> 16);
-                }
+                store_v_token<D>(hb, tb, r, t, t2, e, w, si);
             }
             hb += p.page_head_bytes;
         }
@@ -335,18 +397,17 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
     __threadfence();
     // offsets that do not ascend within the buffer give tokens to no row or to two: the whole call is refused
     bool span = false;
-    if (p.offsets)
-        for (int r = threadIdx.x; r < p.B; r += kThreads) {
-            const int off = p.offsets[r], nr = p.offsets[r + 1] - off;
-            if (off < 0 || nr < 0 || (int64_t)off + nr > p.T) {
-                report_error(p.ws, kErrBadSpan, r, off, nr);
-                span = true;
-            }
+    for (int r = threadIdx.x; r < p.B; r += kThreads) {
+        const int off = p.offsets[r], nr = p.offsets[r + 1] - off;
+        if (off < 0 || nr < 0 || (int64_t)off + nr > p.T) {
+            report_error(p.ws, kErrBadSpan, r, off, nr);
+            span = true;
         }
+    }
     span = __syncthreads_or(span ? 1 : 0) != 0;
     for (int r = threadIdx.x; r < p.B; r += kThreads) {
         const int Nr = p.seq_lens[r];
-        const int off = p.offsets ? p.offsets[r] : r, nr = p.offsets ? p.offsets[r + 1] - off : 1;
+        const int off = p.offsets[r], nr = p.offsets[r + 1] - off;
         const int flag = __ldcg(p.row_bad + r);
         const bool ok = !span && append_fits(p, r, Nr, off, nr, true) && !flag;
         p.seq_lens_out[r] = ok ? Nr + nr : Nr;
@@ -449,13 +510,11 @@ int split_heads(int64_t warps, int Hkv, int64_t want, int &heads_per_part)
 }
 
 template <class K, class P>
-cudaError_t launch(K kern, const P &p, int64_t warps, int64_t most, cudaStream_t s)
+cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s)
 {
-    int64_t grid = (warps + kWarps - 1) / kWarps;
-    grid = grid < most ? grid : most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -469,12 +528,15 @@ cudaError_t launch(K kern, const P &p, int64_t warps, int64_t most, cudaStream_t
 
 cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_t s)
 {
-    p.groups = p.offsets ? (int64_t)p.T / 8 + 2 * (int64_t)p.B : p.B;
+    if (!p.offsets)
+        return d == 128 ? launch(quant_append_one_kernel<128>, p, p.B, 64, s) : launch(quant_append_one_kernel<64>, p, p.B, 64, s);
+    p.groups = (int64_t)p.T / 8 + 2 * (int64_t)p.B;
     // resident CTAs walk the units: fine ones, so that they end together
     const int64_t ctas = 3 * (int64_t)sms;
     p.parts = split_heads(p.groups, p.Hkv, 4 * ctas * kWarps, p.heads_per_part);
-    const int64_t warps = p.groups * p.parts;
-    return d == 128 ? launch(quant_append_kernel<128>, p, warps, ctas, s) : launch(quant_append_kernel<64>, p, warps, ctas, s);
+    int64_t grid = (p.groups * p.parts + kWarps - 1) / kWarps;
+    grid = grid < ctas ? grid : ctas;
+    return d == 128 ? launch(quant_append_kernel<128>, p, grid, kThreads, s) : launch(quant_append_kernel<64>, p, grid, kThreads, s);
 }
 
 cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
@@ -483,8 +545,8 @@ cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
     // several waves of short warps: 116k tokens of 8 heads took 104 us with one
     // wave or three, 99 with eight, 111 with 32
     p.parts = split_heads(chunks, p.Hkv, 8 * 32 * (int64_t)sms, p.heads_per_part);
-    const int64_t warps = chunks * p.parts;
-    return d == 128 ? launch(quant_read_kernel<128>, p, warps, INT64_MAX, s) : launch(quant_read_kernel<64>, p, warps, INT64_MAX, s);
+    const int64_t grid = (chunks * p.parts + kWarps - 1) / kWarps;
+    return d == 128 ? launch(quant_read_kernel<128>, p, grid, kThreads, s) : launch(quant_read_kernel<64>, p, grid, kThreads, s);
 }
 
 }  // namespace pkv
