@@ -611,26 +611,26 @@ __device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D 
 
 // The states of a (row, head)'s n pieces, merged in piece order by the CTA that
 // finished last.  A warp takes a head at a time, or two when there are more
-// heads than warps.  Up to 32 pieces: one lane each for the maxima and sums, and
-// their accumulators eight loads deep, issued beside those.
+// heads than warps, and with d = 64 two pieces side by side.  Up to 32 pieces:
+// one lane each for the maxima and sums, and their accumulators kBatch loads
+// deep, issued beside those: each batch is an L2 round trip.
 template <int D>
 __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, int c0, int n)
 {
-    constexpr int VPL = D / 32, kBatch = 8;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kBatch = 8, LP = D / 4, NP = 32 / LP;  // lanes per piece, pieces side by side
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LP, at = lane % LP;
     const int64_t slots = 2 * kAttnMaxSegs;
     const float *pm = p.partials + slots * p.G * D, *pl = pm + slots * p.G;
     auto state = [&](int j, int g) { return (j == 0 ? 2 * c0 + 1 : 2 * (c0 + j)) * p.G + g; };
     auto merge = [&](auto heads) {  // heads w, w + 4, .. heads of them
         constexpr int NH = decltype(heads)::value, kPer = kBatch / NH;
-        float M[NH], L[NH], acc[NH][VPL];
+        float M[NH], L[NH];
+        float4 acc[NH];
 #pragma unroll
         for (int q = 0; q < NH; ++q) {
             M[q] = kNoMax;
             L[q] = 0.f;
-#pragma unroll
-            for (int v = 0; v < VPL; ++v)
-                acc[q][v] = 0.f;
+            acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         for (int j0 = 0; j0 < n; j0 += 32) {
             const int nj = min(n - j0, 32);
@@ -645,26 +645,16 @@ __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, in
                     lj[q] = __ldcg(pl + state(j0 + lane, g));
                 }
             }
-            for (int b = 0; b < nj; b += kPer) {
-                float x[kPer][NH][VPL];
+            for (int b = 0; b < nj; b += kPer * NP) {
+                float4 x[kPer][NH];
 #pragma unroll
                 for (int u = 0; u < kPer; ++u)
 #pragma unroll
                     for (int q = 0; q < NH; ++q) {
-                        const int g = w + kCW * q;
-#pragma unroll
-                        for (int v = 0; v < VPL; ++v)
-                            x[u][q][v] = 0.f;
-                        if (b + u < nj && g < p.G) {
-                            const float *a = p.partials + (int64_t)state(j0 + b + u, g) * D;
-                            if constexpr (VPL == 4) {
-                                const float4 t = __ldcg(reinterpret_cast<const float4 *>(a) + lane);
-                                x[u][q][0] = t.x, x[u][q][1] = t.y, x[u][q][2] = t.z, x[u][q][3] = t.w;
-                            } else {
-                                const float2 t = __ldcg(reinterpret_cast<const float2 *>(a) + lane);
-                                x[u][q][0] = t.x, x[u][q][1] = t.y;
-                            }
-                        }
+                        const int g = w + kCW * q, j = b + u * NP + sub;
+                        x[u][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (j < nj && g < p.G)
+                            x[u][q] = __ldcg(reinterpret_cast<const float4 *>(p.partials + (int64_t)state(j0 + j, g) * D) + at);
                     }
 #pragma unroll
                 for (int q = 0; q < NH; ++q) {
@@ -677,16 +667,13 @@ __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, in
                         M[q] = mn;
                         wj[q] = ex2(mj[q] - mn);
                         L[q] = L[q] * f + lj[q] * wj[q];  // this lane's share
-#pragma unroll
-                        for (int v = 0; v < VPL; ++v)
-                            acc[q][v] *= f;
+                        acc[q].x *= f, acc[q].y *= f, acc[q].z *= f, acc[q].w *= f;
                     }
 #pragma unroll
                     for (int u = 0; u < kPer; ++u) {
-                        const float a = __shfl_sync(0xffffffffu, wj[q], b + u);
-#pragma unroll
-                        for (int v = 0; v < VPL; ++v)
-                            acc[q][v] = fmaf(x[u][q][v], a, acc[q][v]);
+                        const float a = __shfl_sync(0xffffffffu, wj[q], (b + u * NP + sub) & 31);
+                        acc[q].x = fmaf(x[u][q].x, a, acc[q].x), acc[q].y = fmaf(x[u][q].y, a, acc[q].y);
+                        acc[q].z = fmaf(x[u][q].z, a, acc[q].z), acc[q].w = fmaf(x[u][q].w, a, acc[q].w);
                     }
                 }
             }
@@ -695,18 +682,22 @@ __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, in
         for (int q = 0; q < NH; ++q) {
             const int g = w + kCW * q;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
+            for (int o = 16; o > 0; o >>= 1) {
                 L[q] += __shfl_xor_sync(0xffffffffu, L[q], o);
+                if (o >= LP) {
+                    acc[q].x += __shfl_xor_sync(0xffffffffu, acc[q].x, o);
+                    acc[q].y += __shfl_xor_sync(0xffffffffu, acc[q].y, o);
+                    acc[q].z += __shfl_xor_sync(0xffffffffu, acc[q].z, o);
+                    acc[q].w += __shfl_xor_sync(0xffffffffu, acc[q].w, o);
+                }
+            }
             if (g >= p.G)
                 continue;
             const float inv = 1.f / L[q];
             const int64_t oh = (int64_t)unit * p.G + g;  // unit = row * Hkv + head
-            __half *out = p.o + oh * D + lane * VPL;
-            if constexpr (VPL == 4)
-                *reinterpret_cast<uint2 *>(out) = make_uint2(pack_half2(acc[q][0] * inv, acc[q][1] * inv),
-                                                             pack_half2(acc[q][2] * inv, acc[q][3] * inv));
-            else
-                *reinterpret_cast<uint32_t *>(out) = pack_half2(acc[q][0] * inv, acc[q][1] * inv);
+            if (sub == 0)
+                *reinterpret_cast<uint2 *>(p.o + oh * D + at * 4) =
+                    make_uint2(pack_half2(acc[q].x * inv, acc[q].y * inv), pack_half2(acc[q].z * inv, acc[q].w * inv));
             if (p.lse && lane == 0)
                 p.lse[oh] = (M[q] + log2f(L[q])) * kLn2;
         }
