@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kAppendCtas = 4;  // resident per SM
 
 // The last i in [0, B] with key(i) <= x, for ascending key with key(0) <= x.
 template <class F>
@@ -94,6 +95,14 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
+// x y + z, rounded once, within [0, 1]; 0 for a NaN.
+__device__ __forceinline__ float fma_sat(float x, float y, float z)
+{
+    float r;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half lo, __half hi) { return as_word(__halves2half2(lo, hi)); }
@@ -118,17 +127,27 @@ __device__ __forceinline__ bool append_fits(const QuantAppendParams &p, int i, i
     return true;
 }
 
-// The four code pairs of quant_codes() below, decided exactly; out of line, so
-// that the loop that hardly ever calls it stays small.
-__device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b)
+// The four code pairs of quantise_rows() below, decided exactly; out of line, so
+// that the loop around it stays small.  y is near enough to tell the two codes
+// in question, and the border between them decides.
+__device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b, float i15, float c15)
 {
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    const float inv = 1.f / s;
-#pragma unroll 1
+    constexpr float kMagic = 12582912.f;
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    uint32_t w[4];
+#pragma unroll
     for (int u = 0; u < 4; ++u) {
-        const float2 v = __half22float2(as_half2(w[u]));
-        w[u] = (uint32_t)(quant_code(fminf(fmaxf(v.x, -kQuantLimit), kQuantLimit), s, b, inv) |
-                          quant_code(fminf(fmaxf(v.y, -kQuantLimit), kQuantLimit), s, b, inv) << 16);
+        const float2 v = __half22float2(as_half2(xs[u]));
+        float n[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float z = fminf(fmaxf(e ? v.y : v.x, -kQuantLimit), kQuantLimit);
+            const float y = fma_sat(z, i15, c15);
+            const float near = fmaf(y, 15.f, kMagic) - kMagic;
+            const float below = fmaf(y, 15.f, -near) < 0.f ? near - 1.f : near;  // the lower of the two, -1 at the least
+            n[e] = z >= __fmaf_ru(below + 16.5f, s, b) ? fminf(below + 1.f, 15.f) : fmaxf(below, 0.f);
+        }
+        w[u] = __byte_perm(__float_as_uint(n[0] + kMagic), __float_as_uint(n[1] + kMagic), 0x5410);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -142,8 +161,9 @@ __device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b)
 // 2^-23 of itself, which scales y as a whole, c is rounded twice more and y
 // once: y is at most (|16 + b / s| + 23) 2^-23 off.  Where it lies further than
 // twice that from every border (halves of a step) the rounded y is the code;
-// elsewhere -- one value in 10^5 -- and where values are beyond the limit,
-// quant_code() decides exactly.
+// elsewhere -- one value in some 2000, nearly all of them ties, since x, s and
+// b lie on coarse grids -- and where values are beyond the limit, the border
+// itself decides.
 template <int GR>
 __device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, uint32_t (&w)[GR])
 {
@@ -188,7 +208,7 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, u
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const float2 v = __half22float2(as_half2(xs[u]));
-            const float y0 = __saturatef(fmaf(v.x, i15, c15)), y1 = __saturatef(fmaf(v.y, i15, c15));
+            const float y0 = fma_sat(v.x, i15, c15), y1 = fma_sat(v.y, i15, c15);
             const float n0 = fmaf(y0, 15.f, kMagic), n1 = fmaf(y1, 15.f, kMagic);
             const float d0 = fmaf(y0, 15.f, kMagic - n0), d1 = fmaf(y1, 15.f, kMagic - n1);
             worst = fmaxf(fmaxf(worst, fabsf(d0)), fabsf(d1));
@@ -198,7 +218,7 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, u
         if (__any_sync(0xffffffffu, near)) {
             const __half2 sb = as_half2(__shfl_sync(0xffffffffu, mine, base + j));
             if (near && __low2float(sb) > 0.f) {
-                const uint4 e = quant_codes_exact(x[j], __low2float(sb), __high2float(sb));
+                const uint4 e = quant_codes_exact(x[j], __low2float(sb), __high2float(sb), i15, c15);
                 c[0] = e.x, c[1] = e.y, c[2] = e.z, c[3] = e.w;
             }
         }
@@ -291,7 +311,7 @@ __global__ void __launch_bounds__(64) quant_append_one_kernel(const QuantAppendP
 // first and a last group that are not full and needs no sum over the rows
 // before; what is left over is idle.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAppendParams p)
+__global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(const QuantAppendParams p)
 {
     using Q = QuantLayout<D>;
     constexpr int GR = Q::GR;
@@ -331,24 +351,17 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
         const bool live = pos >= N && pos < N + n;
         const unsigned lives = __ballot_sync(0xffffffffu, live);
         const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
-        const int64_t src = live ? (int64_t)(off + (pos - N)) * p.new_stride + 8 * t : 0;
-        // K and V of a head in turn, the next one's values on their way while one is quantised
-        auto fetch = [&](int it, uint4 (&x)[GR]) {
-            const __half *from = (it & 1 ? p.v_new : p.k_new) + src + (h0 + (it >> 1)) * D;
-#pragma unroll
-            for (int j = 0; j < GR; ++j)
-                x[j] = live ? __ldcs(reinterpret_cast<const uint4 *>(from + 32 * j)) : make_uint4(0, 0, 0, 0);
-        };
-        uint4 next[GR];
-        fetch(0, next);
+        // a quad without a new token reads the nearest one's and stores nothing
+        const int64_t src = (int64_t)(off + (min(max(pos, N), N + n - 1) - N)) * p.new_stride + 8 * t + h0 * D;
+        const __half *kx = p.k_new + src, *vx = p.v_new + src;
+        // K and V of a head in turn
 #pragma unroll 1
         for (int it = 0; it < 2 * (h1 - h0); ++it) {
             uint4 x[GR];
+            const __half *from = it & 1 ? vx : kx;
 #pragma unroll
             for (int j = 0; j < GR; ++j)
-                x[j] = next[j];
-            if (it + 1 < 2 * (h1 - h0))
-                fetch(it + 1, next);
+                x[j] = __ldcs(reinterpret_cast<const uint4 *>(from + 32 * j));
             uint32_t w[GR];
             const uint32_t si = quantise_rows<GR>(x, t, w);  // s | b of group t & (GR - 1)
             if (!(it & 1)) {
@@ -381,6 +394,8 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAp
                 store_v_token<D>(hb, tb, r, t, t2, e, w, si);
             }
             hb += p.page_head_bytes;
+            kx += D;
+            vx += D;
         }
     }
     // the last CTA to get here advances the lengths: every other one has read
@@ -532,7 +547,7 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
         return d == 128 ? launch(quant_append_one_kernel<128>, p, p.B, 64, s) : launch(quant_append_one_kernel<64>, p, p.B, 64, s);
     p.groups = (int64_t)p.T / 8 + 2 * (int64_t)p.B;
     // resident CTAs walk the units: fine ones, so that they end together
-    const int64_t ctas = 3 * (int64_t)sms;
+    const int64_t ctas = kAppendCtas * (int64_t)sms;
     p.parts = split_heads(p.groups, p.Hkv, 4 * ctas * kWarps, p.heads_per_part);
     int64_t grid = (p.groups * p.parts + kWarps - 1) / kWarps;
     grid = grid < ctas ? grid : ctas;

@@ -69,14 +69,6 @@ __device__ __forceinline__ uint32_t quant_value(uint32_t n16, __half2 s, __half2
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The fp16 number `by` places above h (ordered by value; -0 and +0 are one).
-__device__ __forceinline__ __half half_step(__half h, int by)
-{
-    int i = (int)(int16_t)__half_as_ushort(h);
-    i = (i < 0 ? -(i & 0x7fff) : i) + by;
-    return __ushort_as_half((unsigned short)(i < 0 ? (-i) | 0x8000 : i));
-}
-
 // s and b of a group with least value lo and greatest hi (both within
 // +-kQuantLimit), exactly as the format defines them, although (hi - lo) / 15
 // and lo - 16 s need more bits than fp32 has: every comparison of an exact sum
@@ -88,39 +80,17 @@ __device__ __forceinline__ void quant_params(float lo, float hi, __half &s, __ha
     // least fp16 s with 15 s >= hi - lo: rounding up all the way gives it or,
     // past a representable quotient, its successor
     const __half s1 = __float2half_ru(__fmul_ru(__fsub_ru(hi, lo), 0x1.111112p-4f));
-    const __half s0 = half_step(s1, -1);
-    s = (hi > lo && __fmaf_rd(15.f, __half2float(s0), lo) >= hi) ? s0 : s1;
-    if (!(hi > lo))
-        s = __ushort_as_half(0);
+    // (its bits less one are its predecessor's)
+    const __half s0 = __ushort_as_half((unsigned short)(__half_as_ushort(s1) - 1));
+    s = __fmaf_rd(15.f, __half2float(s0), lo) >= hi ? s0 : s1;
+    s = hi > lo ? s : __ushort_as_half(0);
     // nearest to lo - 16 s, the lower one on a tie
     const float sf = __half2float(s);
     const __half b0 = __float2half_rd(__fmaf_rd(-16.f, sf, lo));
-    const __half b1 = half_step(b0, 1);
+    const unsigned short bits = __half_as_ushort(b0);
+    const __half b1 = __ushort_as_half(bits & 0x8000 ? (bits == 0x8000 ? 1 : bits - 1) : bits + 1);  // its successor
     const float mid = 0.5f * (__half2float(b0) + __half2float(b1));
     b = __fmaf_rd(16.f, sf, mid) < lo ? b1 : b0;
-}
-
-// Code of x (within +-kQuantLimit): the integer nearest to (x - b) / s - 16,
-// the upper one on a tie, within 0..15; 0 where s = 0.  The fp32 quotient is
-// within one of it, and the borders b + s (16.5 + k) decide.
-__device__ __forceinline__ int quant_code(float x, float s, float b, float inv_s)
-{
-    if (s == 0.f)
-        return 0;
-    const float y = (x - __fmaf_rn(16.f, s, b)) * inv_s;
-    int n = (int)fminf(fmaxf(floorf(y + 0.5f), 0.f), 15.f);
-    if (n > 0 && x < __fmaf_ru((float)n + 15.5f, s, b))
-        --n;
-    else if (n < 15 && x >= __fmaf_ru((float)n + 16.5f, s, b))
-        ++n;
-    return n;
-}
-
-// A code in field f of a 16-bit half.
-__device__ __forceinline__ uint32_t quant_place(int n, int f)
-{
-    return f == 0 ? (uint32_t)n << 6 : f == 1 ? (uint32_t)n << 2 : f == 2 ? (uint32_t)n << 10
-                  : ((uint32_t)(n & 3) << 14) | ((uint32_t)n >> 2);
 }
 
 #endif  // __CUDACC__
