@@ -395,8 +395,9 @@ int pkv_decode_step_noalloc(const pkv_shape_t *shape, const pkv_plan_cfg_t *cfg,
  * field 3 the code's low two bits at 14-15 and its high two at 0-1.
  *
  * The calls below take one workspace of pkv_attn_workspace_size() bytes, zeroed
- * once after allocation; its counters are back at zero after every launch, and
- * pkv_get_error() reads its error word.  Calls on one workspace must not
+ * once after allocation; its counters are back at zero after every launch (zero
+ * it again after one that reported PKV_ETIMEOUT), and pkv_get_error() reads its
+ * error word.  Calls on one workspace must not
  * overlap on the GPU (two graphs that may run at once need one each).  They use
  * the shape's B, Hkv, d, page_size, num_pages and bt_stride; the decodes Hq and
  * scale too. */

@@ -513,6 +513,7 @@ class PagedDecoder:
         self._ws: dict = {}
         self._part: dict = {}
         self._key: dict = {}
+        self._attn: dict = {}
 
     def route(self, B: int, n_max: int, n_sum: Optional[int] = None) -> tuple[int, int]:
         """(path, split_tokens) for a batch: the calibrated thresholds, or with
@@ -576,6 +577,53 @@ class PagedDecoder:
 
     def workspace(self, device) -> Optional[torch.Tensor]:
         return self._ws.get(device)
+
+    def attn_workspace(self, shape: Shape, device) -> torch.Tensor:
+        """The workspace of step_window, step_quant and append_quant for this
+        shape on this device (zeroed when it is made)."""
+        key = (device, shape.B, shape.Hq // shape.Hkv, shape.d)
+        ws = self._attn.get(key)
+        if ws is None:
+            ws = self._attn[key] = torch.zeros(pkv_attn_workspace_size(shape), dtype=torch.uint8, device=device)
+        return ws
+
+    def step_window(self, q, k_cache, v_cache, block_table, seq_lens, window: int, sinks: int = 0,
+                    o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                    scale: Optional[float] = None, stream=None):
+        """One decode step of a layer whose queries see their row's first `sinks`
+        and last `window` tokens; returns (o, lse)."""
+        shape = make_shape(q, k_cache, block_table, scale)
+        o, lse = self._outputs(q, o, lse, want_lse)
+        pkv_window_decode(shape, self.attn_workspace(shape, q.device), q, k_cache, v_cache, block_table, seq_lens,
+                          window, sinks, o, lse, stream)
+        return o, lse
+
+    def step_quant(self, q, quant_cache, block_table, seq_lens, window: Optional[int] = None, sinks: int = 0,
+                   o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                   scale: Optional[float] = None, stream=None):
+        """One decode step over a 4-bit cache, whole rows or a window; returns (o, lse)."""
+        shape = make_quant_shape(q.shape[1], q.shape[2], quant_cache, block_table, scale)
+        if shape.B != q.shape[0]:
+            raise ValueError("q and block_table disagree on B")
+        o, lse = self._outputs(q, o, lse, want_lse)
+        pkv_quant_decode(shape, self.attn_workspace(shape, q.device), q, quant_cache, block_table, seq_lens, o, lse,
+                         window, sinks, stream)
+        return o, lse
+
+    def append_quant(self, k_new, v_new, quant_cache, block_table, seq_lens, new_offsets=None, seq_lens_out=None,
+                     stream=None) -> None:
+        """Quantise new tokens k_new, v_new [T, Hkv, d] into a 4-bit cache (see pkv_quant_append)."""
+        shape = make_quant_shape(quant_cache.shape[1], k_new.shape[2], quant_cache, block_table)
+        pkv_quant_append(shape, self.attn_workspace(shape, quant_cache.device), k_new, v_new, block_table, seq_lens,
+                         quant_cache, new_offsets, seq_lens_out, stream)
+
+    @staticmethod
+    def _outputs(q, o, lse, want_lse):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        return o, lse
 
 
 class HostDecodeLoop:

@@ -45,6 +45,15 @@ struct Counters {
 
 std::atomic<int32_t> g_starve{0};  // decode launches left to run with the test hook
 
+// Whether the next decode launch is one of them.
+bool take_starve()
+{
+    for (int32_t n = g_starve.load(); n > 0;)
+        if (g_starve.compare_exchange_weak(n, n - 1))
+            return true;
+    return false;
+}
+
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int ilog2(int x)
 {
@@ -309,11 +318,7 @@ int run_decode(const pkv_shape_t *s, int mode, const pkv_plan_cfg_t *c, void *d_
     p.box_log2 = ilog2(box_tok);
     p.len_cap = len_cap(s);
     p.scale_log2 = s->scale * 1.4426950408889634f;
-    for (int32_t n = g_starve.load(); n > 0;)
-        if (g_starve.compare_exchange_weak(n, n - 1)) {
-            p.starve_first_stage = 1;
-            break;
-        }
+    p.starve_first_stage = take_starve() ? 1 : 0;
     int64_t ntasks = 0;
     if (mode == kModeSingle) {
         p.o = static_cast<__half *>(o);
@@ -1143,6 +1148,9 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
 {
     if (win && (win->window < 0 || win->sinks < 0))
         return fail(PKV_EINVAL, "negative window=%d or sinks=%d", win->window, win->sinks);
+    if ((int64_t)s->bt_stride * s->page_size > 0x7fffff00LL)  // the end of a row's last tile is an int32
+        return fail(PKV_EUNSUPPORTED, "rows of %lld tokens (bt_stride * page_size; supported: up to 2^31 - 256)",
+                    (long long)s->bt_stride * s->page_size);
     PKV_TRY(check_ptr(d_ws, "workspace"));
     PKV_TRY(check_ptr(q, "q"));
     if (cache) {
@@ -1175,6 +1183,7 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     p.log2P = ilog2(s->page_size);
     p.tb_log2 = tb_log2(s);
     p.len_cap = len_cap(s);
+    p.starve_first_stage = take_starve() ? 1 : 0;
     // no window: every token of the longest row the table can hold is inside it
     p.window = win ? win->window : len_cap(s);
     p.sinks = win ? win->sinks : 0;

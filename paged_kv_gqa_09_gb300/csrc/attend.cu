@@ -279,6 +279,14 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
                         break;
                     }
                     pend &= ~(1u << stage);
+                    if (p.starve_first_stage && cta == 0 && stage == 0 && ph == 0) {
+                        // test hook: neither arrival nor copies, so the consumers' bounded wait runs out
+                        if (++stage == L::kStages) {
+                            stage = 0;
+                            ph ^= 1;
+                        }
+                        continue;
+                    }
                     const uint32_t dst = sbase + stage * L::kStageBytes;
                     const bool mine_now = (lane >> nbl) == in_batch && pid >= 0;
                     const int b = lane & ((1 << nbl) - 1);

@@ -159,6 +159,7 @@ struct AttendParams {
     int B, Hq, Hkv, G, num_pages, bt_stride, log2P, tb_log2, len_cap;
     int window, sinks;
     float scale_log2;
+    int starve_first_stage;   // test hook: CTA 0 never fills its first stage
 };
 
 cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_t s);

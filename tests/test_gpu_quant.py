@@ -428,6 +428,110 @@ def test_the_same_call_gives_the_same_bits():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+def repeated(B, Hkv, G, d, P, distinct, times, seed):
+    """A batch whose rows repeat `distinct` pages `times` times over: long rows over a small cache."""
+    b = Batch([distinct * P] * B, Hkv=Hkv, G=G, d=d, P=P, seed=seed)
+    b.grow([distinct * P] * B)
+    b.bt = b.bt.repeat(1, times).contiguous()
+    b.shape.bt_stride = distinct * times
+    b.lens = b.lens * times
+    return b
+
+
+def test_quant_decode_of_runs_that_are_split():
+    """Runs long enough that their ends are claimed by whichever CTA is free (more than 48 tiles a CTA): every
+    row repeats its pages 64 times, so o is that of one repetition and lse larger by ln 64."""
+    times = 64
+    b = repeated(8, 8, 8, 128, 64, 16, times, seed=41)
+    b.lens[3] = 0
+    b.lens[5] = b.lens[5] // times
+    q = queries(b)
+    first = b.decode(q)
+    for _ in range(4):
+        again = b.decode(q)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    ks, vs = ([R.values(x) for x in y] for y in (b.k, b.v))
+    ks[3], vs[3] = ks[3][:0], vs[3][:0]
+    ro, rl, to, tl = R.attention(q.cpu().numpy(), ks, vs, float(np.float32(b.shape.scale)))
+    rl[[0, 1, 2, 4, 6, 7]] += np.log(times)
+    x, y = first[0].cpu().numpy().astype(np.float64), first[1].cpu().numpy().astype(np.float64)
+    # a repetition adds to the weights' roundings below 2^-14 only: 64 times the term for those
+    extra = 2.0 ** -25 * 1024 * times * max(np.abs(v).max() for v in vs if v.size)
+    assert (np.abs(x - ro) <= to + extra).all()
+    assert (y[3] == -np.inf).all()
+    rows = [i for i in range(8) if i != 3]
+    # fp32 sums of 65536 weights: 2^-24 times the depth of the sums (tiles per warp and merges, some 2^12)
+    assert (np.abs(y[rows] - rl[rows]) <= tl[rows] + 2.0 ** -12).all()
+    b.ok()
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """The bounded wait: CTA 0's first stage is left unfilled, the consumers give up after a second, the error
+    is reported and the next launch is right."""
+    for make in (lambda: Batch([400, 30], seed=42), lambda: Batch([400], d=64, seed=43)):
+        b = make()
+        b.grow([len_ for len_ in ([400, 30] if b.B == 2 else [400])])
+        q = queries(b)
+        b.check(q)
+        assert _lib.load().pkv_test_starve_next_decodes(1) == 0
+        b.decode(q)
+        assert api.pkv_get_error(b.ws)[0] == _lib.PKV_ETIMEOUT
+        b.ws.zero_()  # the counters of a launch that gave up
+        b.check(q)
+
+
+def test_binding_refuses_wrong_tensors():
+    b = Batch([40, 40], seed=44)
+    b.grow([20, 20])
+    q = queries(b)
+    o = torch.empty_like(q)
+    good = dict(shape=b.shape, ws=b.ws, q=q, quant_cache=b.cache, block_table=b.bt, seq_lens=b.lens, o=o)
+    for bad, kind in ((dict(q=q.float()), ValueError), (dict(q=q[:1]), ValueError), (dict(q=q.transpose(0, 1)), ValueError),
+                      (dict(q=q.cpu()), ValueError), (dict(q=None), TypeError), (dict(ws=b.ws[:100]), ValueError),
+                      (dict(ws=None), TypeError), (dict(quant_cache=b.cache[1:]), ValueError),
+                      (dict(block_table=b.bt.long()), ValueError), (dict(block_table=b.bt[:1]), ValueError),
+                      (dict(seq_lens=b.lens[:1]), ValueError), (dict(o=o.float()), ValueError),
+                      (dict(lse=torch.empty(2, 8, dtype=torch.float16, device="cuda")), ValueError),
+                      (dict(window=2 ** 31), ValueError), (dict(window="4"), TypeError), (dict(shape=3), TypeError),
+                      (dict(window=-1), _lib.PkvError), (dict(sinks=1), ValueError)):
+        with pytest.raises(kind):
+            api.pkv_quant_decode(**{**good, **bad})
+    x = torch.zeros(2, 2, 128, dtype=torch.float16, device="cuda")
+    wide = torch.zeros(2, 2, 256, dtype=torch.float16, device="cuda")
+    for k, v in ((x.float(), x), (x, x[:1]), (x[:, :1], x[:, :1]), (x, wide[:, :, :128]), (wide[:, :, ::2], wide[:, :, ::2]),
+                 (x.cpu(), x.cpu()), (x[0], x[0])):
+        with pytest.raises(ValueError):
+            api.pkv_quant_append(b.shape, b.ws, k, v, b.bt, b.lens, b.cache)
+    with pytest.raises(_lib.PkvError):  # three tokens for two rows
+        y = torch.zeros(3, 2, 128, dtype=torch.float16, device="cuda")
+        api.pkv_quant_append(b.shape, b.ws, y, y, b.bt, b.lens, b.cache)
+    b.ok()
+
+
+def test_decoder_object_runs_the_new_steps():
+    """PagedDecoder: append, then decode over the 4-bit cache and over fp16 pages in a window, with its own
+    workspaces."""
+    dec = api.PagedDecoder()
+    b = Batch([60, 33], Hkv=2, G=4, d=64, P=8, seed=45)
+    k, v = [b.normal(50), b.normal(20)], [b.normal(50), b.normal(20)]
+    off = dev(np.array([0, 50, 70], np.int32))
+    dec.append_quant(dev(np.concatenate(k)), dev(np.concatenate(v)), b.cache, b.bt, b.lens, off)
+    k1, v1 = b.normal(2), b.normal(2)
+    dec.append_quant(dev(k1), dev(v1), b.cache, b.bt, b.lens)
+    ks = [R.values(np.concatenate([k[i], k1[i:i + 1]])) for i in range(2)]
+    vs = [R.values(np.concatenate([v[i], v1[i:i + 1]])) for i in range(2)]
+    q = queries(b)
+    o, lse = dec.step_quant(q, b.cache, b.bt, b.lens)
+    compare(o, lse, q, ks, vs, b.shape.scale, None, 0)
+    o, lse = dec.step_quant(q, b.cache, b.bt, b.lens, window=9, sinks=2)
+    compare(o, lse, q, ks, vs, b.shape.scale, 9, 2)
+    f = Pages([70, 5], Hkv=2, G=4, d=64, P=8, seed=46)
+    o, lse = dec.step_window(f.q, f.kc, f.vc, f.bt, f.lens, 30, 3)
+    compare(o, lse, f.q, f.k, f.v, f.shape.scale, 30, 3)
+    o, lse = dec.step_window(f.q, f.kc, f.vc, f.bt, f.lens, 30, 3, want_lse=False)
+    assert lse is None
+
+
 # ------------------------------------------------------------------ the window over fp16 pages
 
 class Pages:
@@ -543,3 +647,21 @@ def test_calls_on_two_streams_with_a_workspace_each():
             api.pkv_window_decode(b.shape, w, b.q, b.kc, b.vc, b.bt, b.lens, 1500, 4, o, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[0])
+
+
+def test_window_decode_of_runs_that_are_split():
+    """As for the 4-bit cache: rows that repeat their pages, all of them inside the window."""
+    times = 64
+    b = Pages([1024] * 8, Hkv=8, G=4, d=64, P=64, seed=47)
+    b.bt = b.bt.repeat(1, times).contiguous()
+    b.shape.bt_stride *= times
+    b.lens = b.lens * times
+    o, lse = b.decode(1 << 30, 0)
+    again = b.decode(1 << 30, 0)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    ro, rl, to, tl = R.attention(b.q.cpu().numpy(), b.k, b.v, float(np.float32(b.shape.scale)))
+    extra = 2.0 ** -25 * 1024 * times * max(np.abs(v).max() for v in b.v)
+    assert (np.abs(o.cpu().numpy().astype(np.float64) - ro) <= to + extra).all()
+    assert (np.abs(lse.cpu().numpy().astype(np.float64) - np.log(times) - rl) <= tl + 2.0 ** -12).all()
+    assert api.pkv_get_error(b.ws)[0] == 0
+    clean(b.ws, b.B)

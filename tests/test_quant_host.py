@@ -76,6 +76,12 @@ def test_too_many_tokens_are_rejected(L):
     assert calls(L, s, **big)["read"]() == _lib.PKV_EUNSUPPORTED
 
 
+def test_rows_at_the_end_of_int32_are_rejected(L):
+    s = shape(page_size=8, bt_stride=(1 << 28) - 1)
+    assert calls(L, s)["quant"]() == _lib.PKV_EUNSUPPORTED
+    assert calls(L, s)["window"]() == _lib.PKV_EUNSUPPORTED
+
+
 def test_empty_batches_are_no_ops(L):
     none = dict.fromkeys(("ws", "k_new", "v_new", "bt", "sl", "out", "cache", "q", "k", "v", "o", "ooff", "win"))
     for call in calls(L, shape(B=0), T=0, **none).values():
