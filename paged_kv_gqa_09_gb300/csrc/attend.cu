@@ -81,7 +81,8 @@ struct Layout {
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
-    static constexpr int kBytes = kBarOff + (2 * kStages + 1) * 8;
+    static constexpr int kStateOff = (kBarOff + (2 * kStages + 1) * 8 + 15) & ~15;  // cluster: acc [head][D], m, l [head]
+    static constexpr int kBytes = kStateOff + kMaxG * (D + 2) * 4;
     static constexpr int kAlloc = kBytes + 1024;
     // at a piece's end the warps exchange their states through its last stage
     static_assert(kStageBytes >= (kCW - 1) * kMaxG * D * 4, "a stage holds three warps' states");
@@ -132,46 +133,74 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // The cuts of the line of W tiles: run r is [r R, (r + 1) R), its segments
 // parts * r + 0 .. parts - 1 in line order: H tiles, then M, then the rest.
+// (The host keeps W and W + grid within an int.)
 struct Cuts {
-    long long W, R;
-    int H, M, parts;
-    __device__ __forceinline__ int segment(long long x) const
+    int W, R, H, M, parts;
+    __device__ __forceinline__ int segment(int x) const
     {
-        const int r = (int)(x / R);
+        const int r = (int)((unsigned)x / (unsigned)R);
         if (parts == 1)
             return r;
-        const int y = (int)(x - r * R);
+        const int y = x - r * R;
         return 3 * r + (y >= H) + (y >= H + M);
     }
-    __device__ __forceinline__ long long begin(int r, int part) const { return min(r * R + (part == 0 ? 0 : part == 1 ? H : H + M), W); }
-    __device__ __forceinline__ long long end(int r, int part) const
-    {
-        return part == parts - 1 ? min((r + 1) * R, W) : begin(r, part + 1);
-    }
+    __device__ __forceinline__ int begin(int r, int part) const { return min(r * R + (part == 0 ? 0 : part == 1 ? H : H + M), W); }
+    __device__ __forceinline__ int end(int r, int part) const { return part == parts - 1 ? min((r + 1) * R, W) : begin(r, part + 1); }
 };
 
 // Runs of fewer tiles stay whole: their parts would be single tiles, whose
-// states cost as much as they balance.
+// states cost as much as they balance (eight mixed rows, runs of 17 tiles: 35 us
+// whole, 43 us in parts).
 constexpr int kMinSplitRun = 48;
 // A claimed part finds its row by a scan over the batch; beyond this many rows
 // runs stay whole too.
 constexpr int kMaxSplitRows = 1024;
 
-__device__ __forceinline__ Cuts make_cuts(long long W, int grid, int B)
+__device__ __forceinline__ Cuts make_cuts(int W, int grid, int B)
 {
     Cuts c;
     c.W = W;
-    c.R = max((W + grid - 1) / grid, 1ll);
-    c.parts = c.R >= kMinSplitRun && c.R < (1 << 30) && B <= kMaxSplitRows ? 3 : 1;
-    const int R = (int)min(c.R, 1ll << 30);
-    c.H = R - 3 * (R / 16);
-    c.M = 2 * (R / 16);
+    c.R = max((int)((unsigned)(W + grid - 1) / (unsigned)grid), 1);
+    c.parts = c.R >= kMinSplitRun && B <= kMaxSplitRows ? 3 : 1;
+    c.H = c.R - 3 * (c.R / 16);
+    c.M = 2 * (c.R / 16);
     return c;
+}
+
+// Small calls go to clusters of 1, 2, 4, 8 or 16 CTAs, one cluster per (row, KV
+// head): each CTA streams its share of the tiles, and the states are merged
+// through distributed shared memory instead of global memory and an arrival
+// there, which takes 2 us less.
+constexpr int kMaxCluster = 16;
+
+__device__ __forceinline__ void cluster_meet()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The same shared-memory place in CTA `rank` of the cluster, and loads from it.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float cluster_float(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_float4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
 }
 
 // ---------------------------------------------------------------- producer
 
-template <int D, int TBL>
+template <int D, int TBL, bool CLUSTER>
 __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const AttendParams &p,
                                              uint32_t sbase, uint8_t *basep, int4 *meta, uint32_t full0, uint32_t empty0)
 {
@@ -186,184 +215,201 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
     const uint32_t blk_bytes = QUANT ? (uint32_t)Q::bytes(tb) : (uint32_t)(tb * D * 2);
     const uint64_t pol = l2_evict_first_policy();
 
-    // the line of tiles and this CTA's run of it
-    long long W = 0;
-    for (int i = lane; i < p.B; i += 32) {
-        const int len = p.seq_lens[i];
-        if (cta == 0 && (len < 0 || len > p.len_cap))
-            report_error(p.ws, len < 0 ? kErrNegLen : kErrTooLong, i, len, p.len_cap);
-        W += row_span<L::kTile>(p, len).T;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        W += __shfl_xor_sync(0xffffffffu, W, o);
-    const Cuts cuts = make_cuts(W * p.Hkv, grid, p.B);
-
-    int stage = 0;
+    // test hook: the first stage is left out, so the consumers' bounded wait for it runs out
+    int stage = p.starve_first_stage && cta == 0 ? 1 : 0;
     uint32_t ph = 0, pend = 0, pend_par = 0;
     bool ok = true;
-    int run = cta, part = 0;  // this CTA's own run first
-    while (ok) {
-        const long long start = cuts.begin(run, part), end = cuts.end(run, part);
-        const int seg = cuts.parts * run + part;
-        if (start < end) {
-            // rows [wb, wb + 32), one per lane; row_start: line index of the current row
-            int wb = 0, cur = 0;
-            long long row_start = 0;
-            RowSpan mine;
-            for (; wb < p.B; wb += 32) {  // ends earlier: the segment starts inside the line
-                mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
-                int incl = mine.T;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o)
-                        incl += y;
-                }
-                const int tot = __shfl_sync(0xffffffffu, incl, 31);
-                if (start < row_start + (long long)tot * p.Hkv) {
-                    const unsigned m = __ballot_sync(0xffffffffu, start < row_start + (long long)incl * p.Hkv);
-                    cur = __ffs(m) - 1;
-                    row_start += (long long)__shfl_sync(0xffffffffu, incl - mine.T, cur) * p.Hkv;
-                    break;
-                }
-                row_start += (long long)tot * p.Hkv;
+
+    // Streams tiles [k0, k1) of (row i, KV head h): a piece, for `slot` (see finish_piece()).
+    auto stream = [&](int i, int h, const RowSpan &rs, int k0, int k1, int slot, int unit_pieces) {
+        // Block-table entries: lane l holds block l & (2^nbl - 1) of the batch's tile
+        // l >> nbl, a batch ahead of the copies; -1: nothing visible in it, num_pages: bad id.
+        auto page_of = [&](int kb) {
+            const int k = kb + (lane >> nbl);
+            if (k >= k1)
+                return -1;
+            const int tok = rs.tile(k) * kTile + ((lane & ((1 << nbl) - 1)) << tbl);
+            if (!(tok < rs.ns || (tok + tb > rs.w0 && tok < rs.N)))
+                return -1;
+            const int pg = p.bt[(int64_t)i * p.bt_stride + (tok >> p.log2P)];
+            if (pg < 0 || pg >= p.num_pages) {
+                report_error(p.ws, kErrBadPage, i, tok >> p.log2P, pg);
+                return p.num_pages;
             }
-            long long f = start;
-            RowSpan rs;
-            auto take = [&](int src) {
-                rs.N = __shfl_sync(0xffffffffu, mine.N, src);
-                rs.ns = __shfl_sync(0xffffffffu, mine.ns, src);
-                rs.w0 = __shfl_sync(0xffffffffu, mine.w0, src);
-                rs.a = __shfl_sync(0xffffffffu, mine.a, src);
-                rs.b = __shfl_sync(0xffffffffu, mine.b, src);
-                rs.T = __shfl_sync(0xffffffffu, mine.T, src);
-            };
-            take(cur);
-            int h = rs.T > 0 ? (int)((f - row_start) / rs.T) : 0;
-            while (f < end && ok && rs.T > 0) {
-                const int i = wb + cur;
-                const long long u0 = row_start + (long long)h * rs.T, u1 = u0 + rs.T;
-                const int k0 = (int)(f - u0), k1 = (int)(min(u1, end) - u0);
-                const int c0 = u0 >= start ? seg : cuts.segment(u0), c1 = u1 <= end ? seg : cuts.segment(u1 - 1);
-                const int slot = c0 == c1 ? -1 : seg == c0 ? 2 * seg + 1 : 2 * seg;
-                // Block-table entries: lane l holds block l & (2^nbl - 1) of the batch's tile
-                // l >> nbl, a batch ahead of the copies; -1: nothing visible in it, num_pages: bad id.
-                auto page_of = [&](int kb) {
-                    const int k = kb + (lane >> nbl);
-                    if (k >= k1)
-                        return -1;
-                    const int tok = rs.tile(k) * kTile + ((lane & ((1 << nbl) - 1)) << tbl);
-                    if (!(tok < rs.ns || (tok + tb > rs.w0 && tok < rs.N)))
-                        return -1;
-                    const int pg = p.bt[(int64_t)i * p.bt_stride + (tok >> p.log2P)];
-                    if (pg < 0 || pg >= p.num_pages) {
-                        report_error(p.ws, kErrBadPage, i, tok >> p.log2P, pg);
-                        return p.num_pages;
-                    }
-                    return pg;
-                };
-                int pid = page_of(k0), pnx = -1;
-                for (int k = k0; k < k1; ++k) {
-                    const int in_batch = (k - k0) & ((32 >> nbl) - 1);
-                    if (in_batch == 0) {
-                        if (k != k0)
-                            pid = pnx;
-                        pnx = page_of(k + (32 >> nbl));
-                    }
-                    const int tok0 = rs.tile(k) * kTile;
-                    const uint32_t full = full0 + stage * 8;
-                    if (!__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
-                        report_error(p.ws, kErrTimeout, cta, stage, 0);
-                        ok = false;
-                        break;
-                    }
-                    pend &= ~(1u << stage);
-                    if (p.starve_first_stage && cta == 0 && stage == 0 && ph == 0) {
-                        // test hook: neither arrival nor copies, so the consumers' bounded wait runs out
-                        if (++stage == L::kStages) {
-                            stage = 0;
-                            ph ^= 1;
-                        }
-                        continue;
-                    }
-                    const uint32_t dst = sbase + stage * L::kStageBytes;
-                    const bool mine_now = (lane >> nbl) == in_batch && pid >= 0;
-                    const int b = lane & ((1 << nbl) - 1);
-                    const bool bad = QUANT && mine_now && pid == p.num_pages;
-                    if (bad) {  // a bad page reads as zeros: zero params make every code 0
-                        uint8_t *blk = basep + (dst - sbase) + b * blk_bytes;
-                        for (int x = 0; x < tb * Q::kParamRow; x += 4) {
-                            *reinterpret_cast<uint32_t *>(blk + Q::k_params(tb) + x) = 0;
-                            *reinterpret_cast<uint32_t *>(blk + Q::v_params(tb) + x) = 0;
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();  // lane 0's arrival publishes the zeros
-                    const int copies = __popc(__ballot_sync(0xffffffffu, mine_now && !bad));
-                    if (lane == 0) {
-                        const bool whole = rs.ns >= tok0 + kTile || (tok0 >= rs.w0 && tok0 + kTile <= rs.N);
-                        const int flags = (k == k0 ? kFirst : 0) | (k == k1 - 1 ? kLast : 0) | (whole ? 0 : kMasked);
-                        meta[2 * stage] = make_int4(i * p.Hkv + h, tok0, flags, slot);
-                        meta[2 * stage + 1] = make_int4(rs.ns, rs.w0, rs.N, c0 | ((c1 - c0) << 16));
-                        mbar_arrive_expect_tx(full, copies * blk_bytes * (QUANT ? 1 : 2) +
-                                                        (k == k0 ? (uint32_t)(p.G * D * 2) : 0u));
-                        if (k == k0)
-                            bulk_load(dst + L::kKvBytes, p.q + ((int64_t)i * p.Hq + h * p.G) * D, p.G * D * 2, full, pol);
-                    }
-                    __syncwarp();
-                    if (mine_now && !bad) {
-                        const int slot_in = (tok0 + (b << tbl)) & ((1 << p.log2P) - 1);
-                        if constexpr (QUANT) {
-                            bulk_load(dst + b * blk_bytes,
-                                      p.cache + ((int64_t)pid * p.Hkv + h) * p.page_head_bytes +
-                                          (int64_t)(slot_in >> tbl) * blk_bytes,
-                                      blk_bytes, full, pol);
-                        } else {
-                            tma_load_5d(dst + b * blk_bytes, tmK, full, 0, slot_in, 0, h, pid, pol);
-                            tma_load_5d(dst + L::kTileBytes + b * blk_bytes, tmV, full, 0, slot_in, 0, h, pid, pol);
-                        }
-                    }
-                    pend |= 1u << stage;
-                    pend_par = (pend_par & ~(1u << stage)) | (ph << stage);
-                    if (++stage == L::kStages) {
-                        stage = 0;
-                        ph ^= 1;
-                    }
+            return pg;
+        };
+        int pid = page_of(k0), pnx = -1;
+        for (int k = k0; k < k1; ++k) {
+            const int in_batch = (k - k0) & ((32 >> nbl) - 1);
+            if (in_batch == 0) {
+                if (k != k0)
+                    pid = pnx;
+                pnx = page_of(k + (32 >> nbl));
+            }
+            const int tok0 = rs.tile(k) * kTile;
+            const uint32_t full = full0 + stage * 8;
+            if (!__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
+                report_error(p.ws, kErrTimeout, cta, stage, 0);
+                ok = false;
+                return;
+            }
+            pend &= ~(1u << stage);
+            const uint32_t dst = sbase + stage * L::kStageBytes;
+            const bool mine_now = (lane >> nbl) == in_batch && pid >= 0;
+            const int b = lane & ((1 << nbl) - 1);
+            const bool bad = QUANT && mine_now && pid == p.num_pages;
+            if (bad) {  // a bad page reads as zeros: zero params make every code 0
+                uint8_t *blk = basep + (dst - sbase) + b * blk_bytes;
+                for (int x = 0; x < tb * Q::kParamRow; x += 4) {
+                    *reinterpret_cast<uint32_t *>(blk + Q::k_params(tb) + x) = 0;
+                    *reinterpret_cast<uint32_t *>(blk + Q::v_params(tb) + x) = 0;
                 }
-                f = u0 + k1;
-                if (++h == p.Hkv && f < end) {  // the next row with visible tokens
-                    row_start += (long long)rs.T * p.Hkv;
-                    h = 0;
-                    unsigned m = __ballot_sync(0xffffffffu, mine.T > 0 && lane > cur);
-                    while (!m && wb < p.B) {
-                        wb += 32;
-                        mine = row_span<L::kTile>(p, wb + lane < p.B ? p.seq_lens[wb + lane] : 0);
-                        m = __ballot_sync(0xffffffffu, mine.T > 0);
-                    }
-                    if (!m)
-                        break;  // the lengths changed under the launch
-                    cur = __ffs(m) - 1;
-                    take(cur);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();  // lane 0's arrival publishes the zeros
+            const int copies = __popc(__ballot_sync(0xffffffffu, mine_now && !bad));
+            if (lane == 0) {
+                const bool whole = rs.ns >= tok0 + kTile || (tok0 >= rs.w0 && tok0 + kTile <= rs.N);
+                const int flags = (k == k0 ? kFirst : 0) | (k == k1 - 1 ? kLast : 0) | (whole ? 0 : kMasked);
+                meta[2 * stage] = make_int4(i * p.Hkv + h, tok0, flags, slot);
+                meta[2 * stage + 1] = make_int4(rs.ns, rs.w0, rs.N, unit_pieces);
+                mbar_arrive_expect_tx(full, copies * blk_bytes * (QUANT ? 1 : 2) + (k == k0 ? (uint32_t)(p.G * D * 2) : 0u));
+                if (k == k0)
+                    bulk_load(dst + L::kKvBytes, p.q + ((int64_t)i * p.Hq + h * p.G) * D, p.G * D * 2, full, pol);
+            }
+            __syncwarp();
+            if (mine_now && !bad) {
+                const int slot_in = (tok0 + (b << tbl)) & ((1 << p.log2P) - 1);
+                if constexpr (QUANT) {
+                    bulk_load(dst + b * blk_bytes,
+                              p.cache + ((int64_t)pid * p.Hkv + h) * p.page_head_bytes + (int64_t)(slot_in >> tbl) * blk_bytes,
+                              blk_bytes, full, pol);
+                } else {
+                    tma_load_5d(dst + b * blk_bytes, tmK, full, 0, slot_in, 0, h, pid, pol);
+                    tma_load_5d(dst + L::kTileBytes + b * blk_bytes, tmV, full, 0, slot_in, 0, h, pid, pol);
                 }
+            }
+            pend |= 1u << stage;
+            pend_par = (pend_par & ~(1u << stage)) | (ph << stage);
+            if (++stage == L::kStages) {
+                stage = 0;
+                ph ^= 1;
             }
         }
-        if (cuts.parts == 1)
-            break;
-        // the next part to be claimed: every run's second, then every run's last
-        int q = 0;
-        if (lane == 0)
-            q = atomicAdd(&p.ws->next_task, 1);
-        q = __shfl_sync(0xffffffffu, q, 0);
-        if (q >= 2 * grid)
-            break;
-        part = q < grid ? 1 : 2;
-        run = q < grid ? q : q - grid;
-    }
-    if (cuts.parts > 1 && lane == 0 && atomicAdd(&p.ws->done_ctas, 1) == grid - 1) {
-        // every CTA has made its last claim: ready for the next launch
-        p.ws->next_task = 0;
-        p.ws->done_ctas = 0;
+    };
+    auto check_len = [&](int i, int len) {
+        if (len < 0 || len > p.len_cap)
+            report_error(p.ws, len < 0 ? kErrNegLen : kErrTooLong, i, len, p.len_cap);
+    };
+
+    if constexpr (CLUSTER) {
+        // the cluster's (row, head), of which this CTA streams its share
+        const int cl = p.cluster_log2, unit = cta >> cl, r = cta - (unit << cl), i = unit / p.Hkv, h = unit - i * p.Hkv;
+        const int len = p.seq_lens[i];
+        if (h == 0 && r == 0 && lane == 0)
+            check_len(i, len);
+        const RowSpan rs = row_span<kTile>(p, len);
+        const int up = (1 << cl) - 1, k0 = (rs.T * r + up) >> cl, k1 = (rs.T * (r + 1) + up) >> cl;
+        if (k0 < k1)
+            stream(i, h, rs, k0, k1, cl == 0 ? -1 : 0, 0);
+    } else {
+        // the line of tiles and this CTA's run of it; rows [wb, wb + 32) are held one per lane
+        int wb = 0;
+        RowSpan mine;
+        auto window = [&](int at) {
+            const int len = at + lane < p.B ? p.seq_lens[at + lane] : 0;
+            if (cta == 0 && at + lane < p.B)
+                check_len(at + lane, len);
+            return row_span<kTile>(p, len);
+        };
+        mine = window(0);
+        int W = mine.T;
+        for (int at = 32; at < p.B; at += 32)
+            W += window(at).T;
+        const Cuts cuts = make_cuts(__reduce_add_sync(0xffffffffu, W) * p.Hkv, grid, p.B);
+
+        int run = cta, part = 0;  // this CTA's own run first
+        while (ok) {
+            const int start = cuts.begin(run, part), end = cuts.end(run, part);
+            const int seg = cuts.parts * run + part;
+            if (start < end) {
+                // row_start: line index of the current row
+                int cur = 0, row_start = 0;
+                if (wb != 0) {
+                    wb = 0;
+                    mine = window(0);
+                }
+                for (;;) {
+                    int incl = mine.T;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o)
+                            incl += y;
+                    }
+                    const int tot = __shfl_sync(0xffffffffu, incl, 31);
+                    if (start < row_start + tot * p.Hkv) {
+                        cur = __ffs(__ballot_sync(0xffffffffu, start < row_start + incl * p.Hkv)) - 1;
+                        row_start += __shfl_sync(0xffffffffu, incl - mine.T, cur) * p.Hkv;
+                        break;
+                    }
+                    row_start += tot * p.Hkv;
+                    wb += 32;
+                    if (wb >= p.B)
+                        break;  // the lengths changed under the launch: the segment lies inside the line
+                    mine = window(wb);
+                }
+                int f = start;
+                RowSpan rs;
+                auto take = [&](int src) {
+                    rs.N = __shfl_sync(0xffffffffu, mine.N, src);
+                    rs.ns = __shfl_sync(0xffffffffu, mine.ns, src);
+                    rs.w0 = __shfl_sync(0xffffffffu, mine.w0, src);
+                    rs.a = __shfl_sync(0xffffffffu, mine.a, src);
+                    rs.b = __shfl_sync(0xffffffffu, mine.b, src);
+                    rs.T = __shfl_sync(0xffffffffu, mine.T, src);
+                };
+                take(cur);
+                int h = rs.T > 0 ? (int)((unsigned)(f - row_start) / (unsigned)rs.T) : 0;
+                while (f < end && ok && rs.T > 0 && wb < p.B) {
+                    const int u0 = row_start + h * rs.T, u1 = u0 + rs.T;
+                    const int k1 = min(u1, end) - u0;
+                    const int c0 = u0 >= start ? seg : cuts.segment(u0), c1 = u1 <= end ? seg : cuts.segment(u1 - 1);
+                    stream(wb + cur, h, rs, f - u0, k1, c0 == c1 ? -1 : seg == c0 ? 2 * seg + 1 : 2 * seg, c0 | ((c1 - c0) << 16));
+                    f = u0 + k1;
+                    if (++h == p.Hkv && f < end) {  // the next row with visible tokens
+                        row_start += rs.T * p.Hkv;
+                        h = 0;
+                        unsigned m = __ballot_sync(0xffffffffu, mine.T > 0 && lane > cur);
+                        while (!m && wb < p.B) {
+                            wb += 32;
+                            mine = window(wb);
+                            m = __ballot_sync(0xffffffffu, mine.T > 0);
+                        }
+                        if (!m)
+                            break;  // the lengths changed under the launch
+                        cur = __ffs(m) - 1;
+                        take(cur);
+                    }
+                }
+            }
+            if (cuts.parts == 1)
+                break;
+            // the next part to be claimed: every run's second, then every run's last
+            int q = 0;
+            if (lane == 0)
+                q = atomicAdd(&p.ws->next_task, 1);
+            q = __shfl_sync(0xffffffffu, q, 0);
+            if (q >= 2 * grid)
+                break;
+            part = q < grid ? 1 : 2;
+            run = q < grid ? q : q - grid;
+        }
+        if (cuts.parts > 1 && lane == 0 && atomicAdd(&p.ws->done_ctas, 1) == grid - 1) {
+            // every CTA has made its last claim: ready for the next launch
+            p.ws->next_task = 0;
+            p.ws->done_ctas = 0;
+        }
     }
     if (ok) {
         if (__all_sync(0xffffffffu, mbar_wait(empty0 + stage * 8, ph ^ 1, kWaitNs))) {
@@ -717,9 +763,10 @@ __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, in
 }
 
 // A piece's end: the four warps' states become one, each warp merging its
-// quarter of the dims, and go to o and lse or to the piece's slot.
-template <int D>
-__device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st, uint8_t *stage, float *red, int *s_last,
+// quarter of the dims, and go to o and lse (slot < 0), to the piece's slot or, in
+// a cluster, to the CTA's state in shared memory.
+template <int D, bool CLUSTER>
+__device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st, uint8_t *stage, float *red, int *s_last, float *state,
                                              uint32_t cbar, uint32_t &cph, uint32_t empty, int4 mt, int4 mt2)
 {
     constexpr int KS = D / 16, KQ = KS / kCW;  // 16-dim blocks a warp merges
@@ -790,7 +837,25 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
         mbar_arrive(empty);
     const int unit = mt.x, slot = mt.w;
     const bool ok0 = h0 < G, ok1 = h0 + 1 < G;
-    if (slot < 0) {
+    if (CLUSTER && slot >= 0) {
+#pragma unroll
+        for (int y = 0; y < KQ; ++y) {
+            const int d0 = 16 * (w * KQ + y) + r0;
+            state[h0 * D + d0] = R[y][0];
+            state[h0 * D + d0 + 8] = R[y][2];
+            state[(h0 + 1) * D + d0] = R[y][1];
+            state[(h0 + 1) * D + d0 + 8] = R[y][3];
+        }
+        if (w == 0 && lane < 4) {
+            float *ml = state + kMaxG * D;
+            ml[h0] = M0;
+            ml[h0 + 1] = M1;
+            ml[kMaxG + h0] = L0;
+            ml[kMaxG + h0 + 1] = L1;
+        }
+        return true;
+    }
+    if (CLUSTER || slot < 0) {
         const float i0 = 1.f / L0, i1 = 1.f / L1;
         __half *out = p.o + (int64_t)unit * G * D;
 #pragma unroll
@@ -859,7 +924,7 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
     return true;
 }
 
-template <int D, int TBL>
+template <int D, int TBL, bool CLUSTER>
 __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sbase, uint8_t *basep, const int4 *meta,
                                              uint32_t full0, uint32_t empty0, uint32_t cbar, int *s_last)
 {
@@ -910,7 +975,8 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
         }
         __syncwarp();
         if (mt.z & kLast) {
-            if (!finish_piece<D>(p, st, sp, red + parity * kCW * 2 * kMaxG, s_last, cbar, cph, empty0 + stage * 8, mt, mt2)) {
+            if (!finish_piece<D, CLUSTER>(p, st, sp, red + parity * kCW * 2 * kMaxG, s_last,
+                                          reinterpret_cast<float *>(basep + L::kStateOff), cbar, cph, empty0 + stage * 8, mt, mt2)) {
                 report_error(p.ws, kErrTimeout, (int)blockIdx.x, stage, 3);
                 return;
             }
@@ -924,8 +990,8 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
             ph ^= 1;
         }
     }
-    // rows that see no token
-    for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
+    // rows that see no token (a cluster's merge knows its own)
+    for (int i = CLUSTER && p.cluster_log2 > 0 ? p.B : (int)blockIdx.x; i < p.B; i += gridDim.x) {
         if (row_span<L::kTile>(p, p.seq_lens[i]).T > 0)
             continue;
         int4 *out = reinterpret_cast<int4 *>(p.o + (int64_t)i * p.Hq * D);
@@ -937,7 +1003,57 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
     }
 }
 
-template <int D, int TBL>
+// The states of a cluster's CTAs become the (row, head)'s o and lse, each CTA
+// taking its share of the dims, a thread four of them.
+template <int D>
+__device__ __forceinline__ void merge_cluster(const AttendParams &p, uint32_t state)
+{
+    const int cl = p.cluster_log2, n = 1 << cl, per = (D / 4) >> cl;  // float4s of a head in this CTA's share
+    if (cl == 0)
+        return;  // the one CTA has written o and lse
+    const int unit = (int)blockIdx.x >> cl, r = (int)blockIdx.x - (unit << cl);
+    cluster_meet();  // every CTA's state is written
+    for (int x = threadIdx.x; x < p.G * per; x += kThreads) {
+        const int g = x / per, d = 4 * (r * per + x - g * per);
+        float m[kMaxCluster], l[kMaxCluster];
+        float4 a[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            m[c] = kNoMax;
+            l[c] = 0.f;
+            a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < n) {
+                const uint32_t at = cluster_addr(state, c);
+                m[c] = cluster_float(at + (kMaxG * D + g) * 4);
+                l[c] = cluster_float(at + (kMaxG * D + kMaxG + g) * 4);
+                a[c] = cluster_float4(at + (g * D + d) * 4);
+            }
+        }
+        float M = kNoMax, Ls = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+            M = fmaxf(M, m[c]);
+        bool live = false;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const float f = ex2(m[c] - M);
+            Ls += l[c] * f;
+            if (l[c] != 0.f) {  // else a CTA without tiles, whose accumulator was never written
+                A.x += a[c].x * f, A.y += a[c].y * f, A.z += a[c].z * f, A.w += a[c].w * f;
+                live = true;
+            }
+        }
+        const int64_t oh = (int64_t)unit * p.G + g;
+        const float inv = live ? 1.f / Ls : 0.f;
+        *reinterpret_cast<uint2 *>(p.o + oh * D + d) = make_uint2(pack_half2(A.x * inv, A.y * inv), pack_half2(A.z * inv, A.w * inv));
+        if (p.lse && d == 0)
+            p.lse[oh] = live ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+    }
+    cluster_meet();  // no CTA's shared memory goes away while another reads it
+}
+
+template <int D, int TBL, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, Layout<D, TBL>::kCtasPerSm)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendParams p)
 {
@@ -957,6 +1073,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, TBL>::kCtasPerSm)
         mbar_init(cbar, kCW);
         fence_mbar_init();
     }
+    if (CLUSTER && threadIdx.x < 2 * kMaxG)  // no tiles yet: no maximum, no sum
+        reinterpret_cast<float *>(basep + L::kStateOff)[kMaxG * D + threadIdx.x] = threadIdx.x < kMaxG ? kNoMax : 0.f;
     if (!L::QUANT && threadIdx.x == 32 * kCW) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
@@ -973,46 +1091,112 @@ __global__ void __launch_bounds__(kThreads, Layout<D, TBL>::kCtasPerSm)
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x >= 32 * kCW)
-        run_producer<D, TBL>(&tmK, &tmV, p, sbase, basep, meta, full0, empty0);
+        run_producer<D, TBL, CLUSTER>(&tmK, &tmV, p, sbase, basep, meta, full0, empty0);
     else
-        run_consumer<D, TBL>(p, sbase, basep, meta, full0, empty0, cbar, &s_last);
+        run_consumer<D, TBL, CLUSTER>(p, sbase, basep, meta, full0, empty0, cbar, &s_last);
+    if constexpr (CLUSTER)
+        merge_cluster<D>(p, sbase + L::kStateOff);
 }
 
-template <int D, int TBL>
-cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms, cudaStream_t s)
+// What is asked of a device once per kernel: whether its shared memory limit is
+// raised, and how many clusters of 2^k CTAs it holds at once (plus one).
+struct KernelOnDevice {
+    std::atomic<int> ready{0};
+    std::atomic<int> clusters[5] = {};
+};
+
+template <int D, int TBL, bool CLUSTER>
+cudaError_t prepare(KernelOnDevice *&k)
 {
-    using L = Layout<D, TBL>;
-    auto kern = attend_kernel<D, TBL>;
-    static std::atomic<uint64_t> ready{0};  // devices whose limit on shared memory is raised
+    static KernelOnDevice on[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    if (!(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-        if (e != cudaSuccess)
-            return e;
-        ready.fetch_or(1ull << (dev & 63));
+    k = &on[dev & 63];
+    if (k->ready.load(std::memory_order_acquire))
+        return cudaSuccess;
+    auto kern = attend_kernel<D, TBL, CLUSTER>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, TBL>::kAlloc);
+    if (e == cudaSuccess && CLUSTER)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        k->ready.store(1, std::memory_order_release);
+    return e;
+}
+
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Launch(int64_t grid, int smem, int cluster, cudaStream_t s)
+    {
+        cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = cluster > 0 ? 2 : 1;
     }
-    // no more CTAs than the longest rows could keep busy
+};
+
+// Tiles of a (row, head) per CTA of its cluster up to which clusters are used:
+// beyond, the line's equal runs gain more by their balance than the merge costs,
+// sooner over the 4-bit cache, where an idle warp costs more.  Rows of n / 4 .. n
+// tokens, d = 128, Hq = 32, Hkv = 8, clusters against runs: 4-bit, 4 tiles a CTA,
+// 8.8 and 12.2 us (one row), 9.5 and 11.9 us (32 rows); 8 tiles, 14.5 and 14.2 us
+// (eight rows).  fp16, 4 tiles, 7.9 and 11.2 us (16 rows); 16 tiles, 11.9 and 15.2
+// us (four rows); 32 tiles, 29.6 and 31.2 us (32 rows), where a batch less even
+// than these would lose.
+template <bool QUANT>
+constexpr int kMaxClusterTiles = QUANT ? 6 : 20;
+
+template <int D, int TBL>
+cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParams p, int sms, cudaStream_t s)
+{
+    using L = Layout<D, TBL>;
     constexpr int kTile = L::kTile;
+    // the most tiles of a (row, head), by the table's width and by the window
     const int64_t by_len = ((int64_t)p.len_cap + kTile - 1) / kTile;
     const int64_t by_win = ((int64_t)p.window + kTile - 1) / kTile + 1 + ((int64_t)p.sinks + kTile - 1) / kTile;
-    const int64_t tiles = (int64_t)p.B * p.Hkv * (by_len < by_win ? by_len : by_win);
+    const int64_t most = by_len < by_win ? by_len : by_win, units = (int64_t)p.B * p.Hkv, tiles = units * most;
+    KernelOnDevice *k;
+    // the largest cluster that leaves no CTA without a tile in the longest rows
+    // and of which the GPU holds one for every (row, head) at once (a second
+    // wave costs more than the merge saves)
+    int cl = 0;
+    while (cl < 4 && (2ll << cl) <= most && units << (cl + 1) <= (int64_t)sms * L::kCtasPerSm)
+        ++cl;
+    for (; cl >= 0 && most >= 2 && units << cl <= (int64_t)sms * L::kCtasPerSm &&
+           most <= (int64_t)kMaxClusterTiles<L::QUANT> << cl;
+         --cl) {
+        cudaError_t e = prepare<D, TBL, true>(k);
+        if (e != cudaSuccess)
+            return e;
+        Launch l(units << cl, L::kAlloc, 1 << cl, s);
+        int fit = k->clusters[cl].load(std::memory_order_relaxed) - 1;
+        if (fit < 0) {
+            e = cudaOccupancyMaxActiveClusters(&fit, attend_kernel<D, TBL, true>, &l.cfg);
+            if (e != cudaSuccess)
+                return e;
+            k->clusters[cl].store(fit + 1, std::memory_order_relaxed);
+        }
+        if (units > fit)
+            continue;
+        p.cluster_log2 = cl;
+        return cudaLaunchKernelEx(&l.cfg, attend_kernel<D, TBL, true>, tk, tv, p);
+    }
+    cudaError_t e = prepare<D, TBL, false>(k);
+    if (e != cudaSuccess)
+        return e;
     int64_t grid = (int64_t)sms * L::kCtasPerSm;
     grid = grid < kAttnMaxCtas ? grid : kAttnMaxCtas;
-    grid = grid < tiles ? grid : tiles;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::kAlloc;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tk, tv, p);
+    Launch l(grid < tiles ? grid : tiles, L::kAlloc, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, attend_kernel<D, TBL, false>, tk, tv, p);
 }
 
 template <int D>

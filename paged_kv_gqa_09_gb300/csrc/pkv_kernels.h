@@ -160,6 +160,7 @@ struct AttendParams {
     int window, sinks;
     float scale_log2;
     int starve_first_stage;   // test hook: CTA 0 never fills its first stage
+    int cluster_log2;         // set by the launcher where clusters take the rows
 };
 
 cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_t s);

@@ -80,6 +80,10 @@ def test_rows_at_the_end_of_int32_are_rejected(L):
     s = shape(page_size=8, bt_stride=(1 << 28) - 1)
     assert calls(L, s)["quant"]() == _lib.PKV_EUNSUPPORTED
     assert calls(L, s)["window"]() == _lib.PKV_EUNSUPPORTED
+    s = shape(B=1 << 20, page_size=64, bt_stride=1 << 14)  # more tiles than an int32 counts
+    assert calls(L, s, win=None)["quant"]() == _lib.PKV_EUNSUPPORTED
+    s = shape(B=(1 << 31) - 1)
+    assert calls(L, s)["window"]() == _lib.PKV_EUNSUPPORTED
 
 
 def test_empty_batches_are_no_ops(L):
