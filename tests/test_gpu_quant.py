@@ -293,6 +293,47 @@ def test_quant_decode_rows_of_every_length(d, P, Hkv, G):
     b.check(queries(b))
 
 
+def widen(b, columns=4096):
+    """A wide block table, whose further entries are no pages: rows could be long, so the work is cut into runs
+    instead of going to clusters."""
+    more = torch.full((b.B, columns), -7, dtype=torch.int32, device="cuda")
+    b.bt = torch.cat([b.bt, more], 1).contiguous()
+    b.shape.bt_stride += columns
+    return b
+
+
+@pytest.mark.parametrize("d,P,Hkv,G", [(128, 16, 2, 4), (64, 8, 3, 5), (128, 64, 1, 8), (64, 256, 2, 1), (128, 8, 8, 2),
+                                       (64, 16, 1, 7), (128, 128, 2, 3), (64, 32, 4, 6)])
+def test_quant_decode_over_a_wide_table(d, P, Hkv, G):
+    b = widen(Batch(LENS, Hkv=Hkv, G=G, d=d, P=P, seed=P + G))
+    b.grow(LENS)
+    q = queries(b)
+    b.check(q)
+    b.check(q, 10 ** 6, 0)
+    b.check(q, 2 ** 31 - 1, 2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("lens", [[4097], [8000, 1, 0, 129], [1500] * 9, [64] * 40 + [3000], [0, 0, 5000], [0] * 70 + [300]])
+def test_quant_decode_long_rows_over_a_wide_table(lens):
+    b = widen(Batch(lens, Hkv=2, G=8, d=128, P=32, seed=22))
+    b.grow(lens)
+    b.check(queries(b))
+
+
+@pytest.mark.parametrize("d,P,G", [(128, 16, 1), (64, 64, 3)])
+def test_many_rows(d, P, G):
+    """More (row, head) pairs than CTAs: runs of whole rows, and rows that see nothing among them."""
+    lens = LENS * 4
+    b = Batch(lens, Hkv=8, G=G, d=d, P=P, seed=51)
+    b.grow(lens)
+    f = Pages(lens, Hkv=8, G=G, d=d, P=P, seed=52)
+    q = queries(b)
+    b.check(q)
+    for window, sinks in ((0, 0), (0, 3), (16, 4), (100, 64), (1000, 0)):
+        b.check(q, window, sinks)
+        f.check(window, sinks)
+
+
 @pytest.mark.parametrize("window,sinks", [(0, 0), (0, 3), (1, 0), (5, 0), (16, 4), (64, 1), (63, 17), (100, 64), (130, 70),
                                           (10 ** 6, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)])
 @pytest.mark.parametrize("d,P", [(128, 16), (64, 64), (64, 8)])
@@ -665,3 +706,17 @@ def test_window_decode_of_runs_that_are_split():
     assert (np.abs(lse.cpu().numpy().astype(np.float64) - np.log(times) - rl) <= tl + 2.0 ** -12).all()
     assert api.pkv_get_error(b.ws)[0] == 0
     clean(b.ws, b.B)
+
+
+@pytest.mark.parametrize("d,P,Hkv,G", [(128, 16, 2, 4), (64, 8, 3, 5), (128, 64, 1, 8), (64, 256, 2, 1), (128, 128, 8, 2)])
+def test_window_decode_over_a_wide_table(d, P, Hkv, G):
+    b = widen(Pages(LENS, Hkv=Hkv, G=G, d=d, P=P, seed=P + G))
+    for window, sinks in ((10 ** 6, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 10 ** 6)):
+        b.check(window, sinks)
+
+
+@pytest.mark.parametrize("lens", [[4097], [8000, 1, 0, 129], [64] * 40 + [3000]])
+def test_window_decode_long_rows_over_a_wide_table(lens):
+    b = widen(Pages(lens, Hkv=2, G=8, d=128, P=16, seed=31))
+    for window, sinks in ((10 ** 6, 4), (20000, 100)):
+        b.check(window, sinks)
