@@ -7,8 +7,8 @@
 // One pass over the cache: 4 d flops per visible token and query head against
 // 2.5 d bytes (4-bit) or 4 d (fp16) per token and KV head; HBM bounds it.
 //
-// Work split.  A row's visible tokens lie in T_i tiles (64 tokens of fp16
-// pages, 128 of the 4-bit cache; those between the sinks and the window are
+// Work split.  A row's visible tokens lie in T_i tiles of 128 tokens (64 of fp16
+// pages with d = 128; those between the sinks and the window are
 // never touched).  All tiles of the batch in (row, KV head, tile) order form one
 // line, cut into equal runs, one per CTA: every CTA derives the line's length
 // and the cuts from the row lengths, so one launch balances rows of any lengths
@@ -63,21 +63,26 @@ constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 // are then constants; kFp16 for the fp16 pages.
 constexpr int kFp16 = 0;
 
-template <int D, int TBL>
+template <int D, int TBL, bool CLUSTER>
 struct Layout {
     static constexpr bool QUANT = TBL != kFp16;
-    // 16-token blocks of a tile per consumer warp: with two, the 4-bit tile's
-    // barriers, flags and page lookups cost half as much per token, and one
-    // block's unpacking overlaps the other's products
-    static constexpr int MT = QUANT ? 2 : 1;
+    // 16-token blocks of a tile per consumer warp: with two, a tile's barriers,
+    // flags and page lookups cost half as much per token, and one block's
+    // unpacking overlaps the other's products; one where a tile is 32 KB already
+    static constexpr int MT = QUANT || D == 64 ? 2 : 1;
     static constexpr int kTile = 16 * kCW * MT;       // tokens per stage
-    static constexpr int kTileLog2 = QUANT ? 7 : 6;
+    static constexpr int kTileLog2 = MT == 2 ? 7 : 6;
     static constexpr int kTileBytes = kTile * D * 2;  // fp16: one of K, V
     static constexpr int kKvBytes = QUANT ? kTile * D * 5 / 4 : 2 * kTileBytes;
     static constexpr int kQBytes = kMaxG * D * 2;
     static constexpr int kStageBytes = kKvBytes + kQBytes;
-    static constexpr int kCtasPerSm = QUANT ? 3 : 2;
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    // as many CTAs as registers or shared memory hold.  fp16 pages with d = 64 (a
+    // head's token is one 128-byte line among the others' heads) want more loads
+    // from more warps in flight: 64 rows in a window of 8191, three CTAs of two
+    // stages 166 us, two of three 208 us; clusters the latter (12.8 and 14.9 us
+    // for eight rows)
+    static constexpr int kCtasPerSm = QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
+    static constexpr int kStages = QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 2 : 3;
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
@@ -204,7 +209,7 @@ template <int D, int TBL, bool CLUSTER>
 __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const AttendParams &p,
                                              uint32_t sbase, uint8_t *basep, int4 *meta, uint32_t full0, uint32_t empty0)
 {
-    using L = Layout<D, TBL>;
+    using L = Layout<D, TBL, CLUSTER>;
     using Q = QuantLayout<D>;
     constexpr bool QUANT = L::QUANT;
     constexpr int kTile = L::kTile;
@@ -525,46 +530,57 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
     }
 }
 
-// One tile of the fp16 pages: this warp's 16 tokens, of which `vis` (a bit per
-// token) are visible.
+// One tile of the fp16 pages: this warp's 16 or 32 tokens, of which `vis` (a bit
+// per token) are visible.
 template <int D>
 __device__ __forceinline__ void fp16_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], uint32_t kt, uint8_t *ktp, uint32_t vis,
                                           int w, int btl, float sl2)
 {
-    constexpr int KS = D / 16, kTile = Layout<D, kFp16>::kTile;
+    using L = Layout<D, kFp16, false>;
+    constexpr int KS = D / 16, MT = L::MT, TW = 16 * MT;
     const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
     const uint32_t blk = 128u << btl;
-    const uint32_t vt = kt + kTile * D * 2;
-    const uint32_t rowK = row_base<D>(16 * w + (mi & 1) * 8 + r8, btl), rowV = row_base<D>(16 * w + (mi >> 1) * 8 + r8, btl);
-    if (vis != 0xffffu) {
+    const uint32_t vt = kt + L::kTileBytes;
+    if (vis != 0xffffffffu >> (32 - TW)) {
         // masked rows hold anything: zero them in V so that p = 0 meets no NaN
-        uint8_t *vtp = ktp + kTile * D * 2;
-        for (int x = lane; x < 16 * (D / 8); x += 32) {
-            const int tok = 16 * w + x / (D / 8), c = x % (D / 8);
-            if (!(vis >> (tok & 15) & 1))
+        uint8_t *vtp = ktp + L::kTileBytes;
+        for (int x = lane; x < TW * (D / 8); x += 32) {
+            const int tok = TW * w + x / (D / 8), c = x % (D / 8);
+            if (!(vis >> (tok & (TW - 1)) & 1))
                 *reinterpret_cast<int4 *>(vtp + row_base<D>(tok, btl) + (c >> 3) * blk + (((c & 7) ^ (tok & 7)) << 4)) =
                     make_int4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
     }
-    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+    float x[MT][4];
 #pragma unroll
-    for (int x = 0; x < KS; ++x) {
-        const uint32_t cc = (uint32_t)((((2 * x) & 7) + (mi >> 1)) ^ r8) << 4;
-        uint32_t a0, a1, a2, a3;
-        ldsm_x4(kt + rowK + (x >> 2) * blk + cc, a0, a1, a2, a3);
-        mma_16816(x & 1 ? sb : sa, a0, a1, a2, a3, qf[x][0], qf[x][1]);
+    for (int u = 0; u < MT; ++u) {
+        const uint32_t rowK = row_base<D>(TW * w + 16 * u + (mi & 1) * 8 + r8, btl);
+        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int z = 0; z < KS; ++z) {
+            const uint32_t cc = (uint32_t)((((2 * z) & 7) + (mi >> 1)) ^ r8) << 4;
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4(kt + rowK + (z >> 2) * blk + cc, a0, a1, a2, a3);
+            mma_16816(z & 1 ? sb : sa, a0, a1, a2, a3, qf[z][0], qf[z][1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[u][e] = sa[e] + sb[e];
     }
-    const float x[1][4] = {{sa[0] + sb[0], sa[1] + sb[1], sa[2] + sb[2], sa[3] + sb[3]}};
-    uint32_t P[1][2];
-    softmax_step<D, 1>(st, x, vis, sl2, P);
+    uint32_t P[MT][2];
+    softmax_step<D, MT>(st, x, vis, sl2, P);
 #pragma unroll
-    for (int x = 0; x < KS; ++x) {
-        const uint32_t cc = (uint32_t)((((2 * x) & 7) + (mi & 1)) ^ r8) << 4;
-        uint32_t a0, a1, a2, a3;
-        ldsm_x4_t(vt + rowV + (x >> 2) * blk + cc, a0, a1, a2, a3);
-        mma_16816(st.O[x], a0, a1, a2, a3, P[0][0], P[0][1]);
+    for (int u = 0; u < MT; ++u) {
+        const uint32_t rowV = row_base<D>(TW * w + 16 * u + (mi >> 1) * 8 + r8, btl);
+#pragma unroll
+        for (int z = 0; z < KS; ++z) {
+            const uint32_t cc = (uint32_t)((((2 * z) & 7) + (mi & 1)) ^ r8) << 4;
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4_t(vt + rowV + (z >> 2) * blk + cc, a0, a1, a2, a3);
+            mma_16816(st.O[z], a0, a1, a2, a3, P[u][0], P[u][1]);
+        }
     }
 }
 
@@ -928,7 +944,7 @@ template <int D, int TBL, bool CLUSTER>
 __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sbase, uint8_t *basep, const int4 *meta,
                                              uint32_t full0, uint32_t empty0, uint32_t cbar, int *s_last)
 {
-    using L = Layout<D, TBL>;
+    using L = Layout<D, TBL, CLUSTER>;
     constexpr int KS = D / 16;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = lane >> 2;
     // two buffers: a warp may reach the next piece's end while another still reads this one's
@@ -1054,10 +1070,10 @@ __device__ __forceinline__ void merge_cluster(const AttendParams &p, uint32_t st
 }
 
 template <int D, int TBL, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, Layout<D, TBL>::kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, Layout<D, TBL, CLUSTER>::kCtasPerSm)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendParams p)
 {
-    using L = Layout<D, TBL>;
+    using L = Layout<D, TBL, CLUSTER>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_last;
     const uint32_t raw = smem_u32(smem_raw);
@@ -1117,7 +1133,7 @@ cudaError_t prepare(KernelOnDevice *&k)
     if (k->ready.load(std::memory_order_acquire))
         return cudaSuccess;
     auto kern = attend_kernel<D, TBL, CLUSTER>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, TBL>::kAlloc);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, TBL, CLUSTER>::kAlloc);
     if (e == cudaSuccess && CLUSTER)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)
@@ -1158,7 +1174,8 @@ constexpr int kMaxClusterTiles = QUANT ? 6 : 20;
 template <int D, int TBL>
 cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParams p, int sms, cudaStream_t s)
 {
-    using L = Layout<D, TBL>;
+    using L = Layout<D, TBL, false>;
+    using LC = Layout<D, TBL, true>;
     constexpr int kTile = L::kTile;
     // the most tiles of a (row, head), by the table's width and by the window
     const int64_t by_len = ((int64_t)p.len_cap + kTile - 1) / kTile;
@@ -1169,15 +1186,15 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
     // and of which the GPU holds one for every (row, head) at once (a second
     // wave costs more than the merge saves)
     int cl = 0;
-    while (cl < 4 && (2ll << cl) <= most && units << (cl + 1) <= (int64_t)sms * L::kCtasPerSm)
+    while (cl < 4 && (2ll << cl) <= most && units << (cl + 1) <= (int64_t)sms * LC::kCtasPerSm)
         ++cl;
-    for (; cl >= 0 && most >= 2 && units << cl <= (int64_t)sms * L::kCtasPerSm &&
+    for (; cl >= 0 && most >= 2 && units << cl <= (int64_t)sms * LC::kCtasPerSm &&
            most <= (int64_t)kMaxClusterTiles<L::QUANT> << cl;
          --cl) {
         cudaError_t e = prepare<D, TBL, true>(k);
         if (e != cudaSuccess)
             return e;
-        Launch l(units << cl, L::kAlloc, 1 << cl, s);
+        Launch l(units << cl, LC::kAlloc, 1 << cl, s);
         int fit = k->clusters[cl].load(std::memory_order_relaxed) - 1;
         if (fit < 0) {
             e = cudaOccupancyMaxActiveClusters(&fit, attend_kernel<D, TBL, true>, &l.cfg);

@@ -111,7 +111,7 @@ struct AppendParams {
 // Workspace of the windowed and 4-bit operators: the header, one int per row
 // (rows that an append refuses), one counter per segment of the attention's
 // work (at most three per CTA), then two partial states per segment.
-constexpr int kAttnMaxCtas = 512;
+constexpr int kAttnMaxCtas = 640;
 constexpr int kAttnMaxSegs = 3 * kAttnMaxCtas;
 inline size_t aws_row_bad_off() { return kWsHeaderBytes; }
 inline size_t aws_counters_off(int B) { return (kWsHeaderBytes + sizeof(int32_t) * (size_t)B + 15) & ~(size_t)15; }

@@ -17,7 +17,7 @@ def dev(x):
 
 def clean(ws, B):
     """The workspace's row flags and counters are back at zero."""
-    assert int(ws[64:].view(torch.int32)[:(B + 3) // 4 * 4 + 1536].abs().sum()) == 0
+    assert int(ws[64:].view(torch.int32)[:(B + 3) // 4 * 4 + 1920].abs().sum()) == 0
     assert int(ws[16:64].view(torch.int32).abs().sum()) == 0
 
 
