@@ -129,7 +129,7 @@ struct QuantAppendParams {
     int64_t page_head_bytes;    // one page of one head
     int T, B, Hkv, log2P, tb_log2, num_pages, bt_stride, len_cap;
     int64_t groups;             // set by the launcher: groups of eight positions,
-    int parts, heads_per_part;  // and how heads are split over warps
+    int parts, its_per_part;    // and how the heads' sides are split over warps
 };
 
 struct QuantReadParams {

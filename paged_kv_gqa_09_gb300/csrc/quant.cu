@@ -24,14 +24,31 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAppendCtas = 4;  // resident per SM
 
-// The last i in [0, B] with key(i) <= x, for ascending key with key(0) <= x.
+// The last i in [0, B] with key(i) <= x, for ascending key with key(0) <= x;
+// whole warps only, with one x: 33 keys at a time, so that up to 32 rows take
+// one round trip.
 template <class F>
 __device__ __forceinline__ int last_not_above(int B, int64_t x, F key)
 {
-    int lo = 0, hi = B;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = B;  // the answer is in [lo, lo + n]
+    while (n > 0) {
+        const int step = (n + 31) / 32, at = lo + (lane + 1) * step;  // lo + step, lo + 2 step, ..
+        const unsigned m = __ballot_sync(0xffffffffu, at <= lo + n && key(at) <= x);
+        const int up = __popc(m) * step;
+        lo += up;
+        n = min(n - up, step - 1);
+    }
+    return lo;
+}
+
+// Row of packed token x, offsets[0] <= x < offsets[B]: the last i in [0, B) with offsets[i] <= x.
+__device__ __forceinline__ int row_of(const int32_t *offsets, int B, int x)
+{
+    int lo = 0, hi = B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (key(mid) <= x)
+        if (offsets[mid] <= x)
             lo = mid;
         else
             hi = mid - 1;
@@ -305,8 +322,8 @@ __global__ void __launch_bounds__(64) quant_append_one_kernel(const QuantAppendP
         p.seq_lens_out[i] = page >= 0 ? N + 1 : N;
 }
 
-// A warp takes the eight cache positions 8 k .. of one row, and heads
-// [h0, h1), then the next such unit a grid further on.  Rows share one line of
+// A warp takes the eight cache positions 8 k .. of one row, for some of the
+// heads' sides (2 h: K, 2 h + 1: V), then the next such unit a grid further on.  Rows share one line of
 // such groups: row i's are at offsets[i] / 8 + 2 i .., which leaves room for a
 // first and a last group that are not full and needs no sum over the rows
 // before; what is left over is idle.
@@ -315,17 +332,24 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
 {
     using Q = QuantLayout<D>;
     constexpr int GR = Q::GR;
-    __shared__ int s_last;
+    __shared__ int s_seen;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int e = g & 1, t2 = g >> 1;
     const int tb = 1 << p.tb_log2;
+    // what the last CTA needs of its first rows, on its way already
+    int my_off = 0, my_n = 0, my_N = 0;
+    if ((int)threadIdx.x < p.B) {
+        my_off = p.offsets[threadIdx.x];
+        my_n = p.offsets[threadIdx.x + 1] - my_off;
+        my_N = p.seq_lens[threadIdx.x];
+    }
     bool bad = false;
-    // a warp keeps its part of the heads (those left over when the parts do not divide the warps stay idle)
+    // a warp keeps its part of the heads' sides (those left over when the parts do not divide the warps stay idle)
     const unsigned warp = blockIdx.x * kWarps + (threadIdx.x >> 5), lines = gridDim.x * kWarps / (unsigned)p.parts;
     const unsigned line = warp / (unsigned)p.parts;
-    const int h0 = (int)(warp - line * p.parts) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, p.Hkv);
+    const int it0 = (int)(warp - line * p.parts) * p.its_per_part, it1 = min(it0 + p.its_per_part, 2 * p.Hkv);
     for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
         const int i = min(last_not_above(p.B, gs, [&](int r) { return (int64_t)(p.offsets[r] >> 3) + 2 * (int64_t)r; }), p.B - 1);
         const int off = p.offsets[i], n = p.offsets[i + 1] - off;
@@ -346,19 +370,20 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
             continue;
         }
         const int slot = (int)pos0 & ((1 << p.log2P) - 1), r = slot & (tb - 1);
-        uint8_t *hb = p.cache + ((int64_t)page * p.Hkv + h0) * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
+        uint8_t *blk = p.cache + (int64_t)page * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
         const int pos = (int)pos0 + g;
         const bool live = pos >= N && pos < N + n;
         const unsigned lives = __ballot_sync(0xffffffffu, live);
         const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
         // a quad without a new token reads the nearest one's and stores nothing
-        const int64_t src = (int64_t)(off + (min(max(pos, N), N + n - 1) - N)) * p.new_stride + 8 * t + h0 * D;
+        const int64_t src = (int64_t)(off + (min(max(pos, N), N + n - 1) - N)) * p.new_stride + 8 * t;
         const __half *kx = p.k_new + src, *vx = p.v_new + src;
         // K and V of a head in turn
 #pragma unroll 1
-        for (int it = 0; it < 2 * (h1 - h0); ++it) {
+        for (int it = it0; it < it1; ++it) {
             uint4 x[GR];
-            const __half *from = it & 1 ? vx : kx;
+            const __half *from = (it & 1 ? vx : kx) + (it >> 1) * D;
+            uint8_t *hb = blk + (it >> 1) * p.page_head_bytes;
 #pragma unroll
             for (int j = 0; j < GR; ++j)
                 x[j] = __ldcs(reinterpret_cast<const uint4 *>(from + 32 * j));
@@ -393,27 +418,28 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
             } else if (live) {
                 store_v_token<D>(hb, tb, r, t, t2, e, w, si);
             }
-            hb += p.page_head_bytes;
-            kx += D;
-            vx += D;
         }
     }
     // the last CTA to get here advances the lengths: every other one has read
-    // them by then, and its rows' flags are set
+    // them by then, and its rows' flags are set; CTAs that set one are counted above
+    constexpr int kBad = 1 << 20;
     const int any_bad = __syncthreads_or(bad ? 1 : 0);
     if (threadIdx.x == 0) {
         if (any_bad)
             __threadfence();
-        s_last = atomicAdd(&p.ws->append_done, 1) == (int)gridDim.x - 1;
+        s_seen = atomicAdd(&p.ws->append_done, any_bad ? 1 + kBad : 1) + (any_bad ? 1 + kBad : 1);
     }
     __syncthreads();
-    if (!s_last)
+    if ((s_seen & (kBad - 1)) != (int)gridDim.x)
         return;
-    __threadfence();
+    const bool flags = s_seen >= kBad;
+    if (flags)
+        __threadfence();
     // offsets that do not ascend within the buffer give tokens to no row or to two: the whole call is refused
     bool span = false;
     for (int r = threadIdx.x; r < p.B; r += kThreads) {
-        const int off = p.offsets[r], nr = p.offsets[r + 1] - off;
+        const bool first = r < kThreads;
+        const int off = first ? my_off : p.offsets[r], nr = first ? my_n : p.offsets[r + 1] - off;
         if (off < 0 || nr < 0 || (int64_t)off + nr > p.T) {
             report_error(p.ws, kErrBadSpan, r, off, nr);
             span = true;
@@ -421,9 +447,10 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
     }
     span = __syncthreads_or(span ? 1 : 0) != 0;
     for (int r = threadIdx.x; r < p.B; r += kThreads) {
-        const int Nr = p.seq_lens[r];
-        const int off = p.offsets[r], nr = p.offsets[r + 1] - off;
-        const int flag = __ldcg(p.row_bad + r);
+        const bool first = r < kThreads;
+        const int Nr = first ? my_N : p.seq_lens[r];
+        const int off = first ? my_off : p.offsets[r], nr = first ? my_n : p.offsets[r + 1] - off;
+        const int flag = flags ? __ldcg(p.row_bad + r) : 0;
         const bool ok = !span && append_fits(p, r, Nr, off, nr, true) && !flag;
         p.seq_lens_out[r] = ok ? Nr + nr : Nr;
         if (flag)
@@ -454,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 4) quant_read_kernel(const QuantRead
     int page = -1;
     int64_t pos = 0;
     if (live) {
-        const int i = min(last_not_above(p.B, x, [&](int r) { return (int64_t)p.offsets[r]; }), p.B - 1);
+        const int i = row_of(p.offsets, p.B, x);
         const int N = min(p.seq_lens[i], p.len_cap);
         pos = (int64_t)(p.first ? p.first[i] : 0) + (x - p.offsets[i]);
         if (x >= p.offsets[i + 1]) {
@@ -514,14 +541,15 @@ __global__ void __launch_bounds__(kThreads, 4) quant_read_kernel(const QuantRead
     }
 }
 
-// Heads are split over `parts` warps until the launch has at least `want`.
-int split_heads(int64_t warps, int Hkv, int64_t want, int &heads_per_part)
+// `n` things to do per token group (heads, or sides of heads) are split over
+// `parts` warps until the launch has at least `want`; each warp then does `per`.
+int split_work(int64_t warps, int n, int64_t want, int &per)
 {
     int parts = 1;
-    while (parts < Hkv && warps * parts < want)
+    while (parts < n && warps * parts < want)
         parts *= 2;
-    heads_per_part = (Hkv + parts - 1) / parts;
-    return (Hkv + heads_per_part - 1) / heads_per_part;
+    per = (n + parts - 1) / parts;
+    return (n + per - 1) / per;
 }
 
 template <class K, class P>
@@ -548,7 +576,7 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
     p.groups = (int64_t)p.T / 8 + 2 * (int64_t)p.B;
     // resident CTAs walk the units: fine ones, so that they end together
     const int64_t ctas = kAppendCtas * (int64_t)sms;
-    p.parts = split_heads(p.groups, p.Hkv, 4 * ctas * kWarps, p.heads_per_part);
+    p.parts = split_work(p.groups, 2 * p.Hkv, 4 * ctas * kWarps, p.its_per_part);
     int64_t grid = (p.groups * p.parts + kWarps - 1) / kWarps;
     grid = grid < ctas ? grid : ctas;
     return d == 128 ? launch(quant_append_kernel<128>, p, grid, kThreads, s) : launch(quant_append_kernel<64>, p, grid, kThreads, s);
@@ -559,7 +587,7 @@ cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
     const int64_t chunks = ((int64_t)p.T + 7) / 8;
     // several waves of short warps: 116k tokens of 8 heads took 104 us with one
     // wave or three, 99 with eight, 111 with 32
-    p.parts = split_heads(chunks, p.Hkv, 8 * 32 * (int64_t)sms, p.heads_per_part);
+    p.parts = split_work(chunks, p.Hkv, 8 * 32 * (int64_t)sms, p.heads_per_part);
     const int64_t grid = (chunks * p.parts + kWarps - 1) / kWarps;
     return d == 128 ? launch(quant_read_kernel<128>, p, grid, kThreads, s) : launch(quant_read_kernel<64>, p, grid, kThreads, s);
 }
