@@ -7,12 +7,15 @@
 //
 // Both are one pass over their data: append reads 2 bytes per value and writes
 // 0.625, read the other way round; HBM bounds them, append closely followed by
-// its arithmetic (about eleven instructions per value).  A warp takes eight
+// its arithmetic (some fifteen instructions per value).  A warp takes eight
 // tokens, four lanes each, and loops over KV heads and sides, so that rows,
 // pages and offsets are looked up once for all of them; short calls split the
-// heads over more warps.  Lane t of a token's four holds dims 32 j + 8 t ..
-// (16 bytes of the packed row) on the fp16 side and words (t, j) on the code
-// side; an exchange among the four lanes leads from one to the other.
+// heads over more warps.  Lane t of a token's four holds the words (t, j), the
+// codes of dims 32 j + 8 f + 2 t and the next (f = 0..3).  append reads just
+// those, four bytes at a time (a quad's 16 bytes side by side; all of a line is
+// used from L1): 16-byte reads of dims 32 j + 8 t .. cost an exchange among the
+// four lanes, two instructions per value.  read does make that exchange, since
+// four-byte stores would reach L2 one by one.
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
@@ -54,17 +57,6 @@ __device__ __forceinline__ int row_of(const int32_t *offsets, int B, int x)
             hi = mid - 1;
     }
     return lo;
-}
-
-// OR over the four lanes of a quad of four words each; lane f ends with word f.
-__device__ __forceinline__ uint32_t quad_or_transpose(const uint32_t (&c)[4], int f)
-{
-    const bool up = (f & 2) != 0;
-    uint32_t k0 = up ? c[2] : c[0], k1 = up ? c[3] : c[1];
-    k0 |= __shfl_xor_sync(0xffffffffu, up ? c[0] : c[2], 2);
-    k1 |= __shfl_xor_sync(0xffffffffu, up ? c[1] : c[3], 2);
-    const uint32_t mine = (f & 1) ? k1 : k0;
-    return mine | __shfl_xor_sync(0xffffffffu, (f & 1) ? k0 : k1, 1);
 }
 
 // 4x4 transpose over a quad: lane t gives word f of v to lane f, which gets
@@ -169,9 +161,9 @@ __device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b, float
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One head's K or V of the warp's eight tokens: x[j] are this lane's dims
-// 32 j + 8 t .. of its token; w[j] becomes its word (t, j).  Returns s | b << 16
-// of group t & (GR - 1) of the token.
+// One head's K or V of the warp's eight tokens: x[j][f] are this lane's dims
+// 32 j + 8 f + 2 t and the next of its token; w[j] becomes its word (t, j).
+// Returns s | b << 16 of group t & (GR - 1) of the token.
 //
 // In units of codes y = (x - b) / s - 16 comes, over 15, from one fused
 // multiply-add with i = 1 / (15 s) and c = -(16 s + b) i in fp32.  i is within
@@ -182,13 +174,13 @@ __device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b, float
 // b lie on coarse grids -- and where values are beyond the limit, the border
 // itself decides.
 template <int GR>
-__device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, uint32_t (&w)[GR])
+__device__ __forceinline__ uint32_t quantise_rows(const uint32_t (&x)[GR][4], int t, uint32_t (&w)[GR])
 {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
     uint32_t mm[4];  // least | -greatest of the lane's eight values of group j (twice over for GR = 2)
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
-        const __half2 a = as_half2(x[j].x), b = as_half2(x[j].y), c = as_half2(x[j].z), d = as_half2(x[j].w);
+        const __half2 a = as_half2(x[j][0]), b = as_half2(x[j][1]), c = as_half2(x[j][2]), d = as_half2(x[j][3]);
         const uint32_t mn = as_word(__hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)));
         const uint32_t mx = as_word(__hneg2(__hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d))));
         mm[j] = as_word(__hmin2_nan(as_half2(__byte_perm(mn, mx, 0x5410)), as_half2(__byte_perm(mn, mx, 0x7632))));
@@ -213,18 +205,15 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, u
     const float c_mine = -fmaf(16.f, sf, __half2float(b)) * i_mine;
     const unsigned wide = __ballot_sync(0xffffffffu, (lo != lo0 || hi != hi0) && !nan);
     const int base = threadIdx.x & 28;
-    const int sh = t == 1 ? 2 : t == 2 ? 10 : 6;
-    const uint32_t swap = t == 3 ? 0x2301 : 0x3210;
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
         const float i15 = __shfl_sync(0xffffffffu, i_mine, base + j), c15 = __shfl_sync(0xffffffffu, c_mine, base + j);
         const float edge = 0.5f - fmaf(fabsf(c15), 15.f * 0x1p-22f, 0x1p-17f);
-        const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
         float worst = 0.f;
-        uint32_t c[4];  // the lane's codes: field t of four words
+        uint32_t c[4];  // pairs of codes, one per field
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const float2 v = __half22float2(as_half2(xs[u]));
+            const float2 v = __half22float2(as_half2(x[j][u]));
             const float y0 = fma_sat(v.x, i15, c15), y1 = fma_sat(v.y, i15, c15);
             const float n0 = fmaf(y0, 15.f, kMagic), n1 = fmaf(y1, 15.f, kMagic);
             const float d0 = fmaf(y0, 15.f, kMagic - n0), d1 = fmaf(y1, 15.f, kMagic - n1);
@@ -235,14 +224,12 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint4 (&x)[GR], int t, u
         if (__any_sync(0xffffffffu, near)) {
             const __half2 sb = as_half2(__shfl_sync(0xffffffffu, mine, base + j));
             if (near && __low2float(sb) > 0.f) {
-                const uint4 e = quant_codes_exact(x[j], __low2float(sb), __high2float(sb), i15, c15);
+                const uint4 e = quant_codes_exact(make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]), __low2float(sb),
+                                                  __high2float(sb), i15, c15);
                 c[0] = e.x, c[1] = e.y, c[2] = e.z, c[3] = e.w;
             }
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            c[u] = __byte_perm(c[u] << sh, 0, swap);
-        w[j] = quad_or_transpose(c, t);
+        w[j] = (c[0] << 6) + (c[1] << 2) + (c[2] << 10) + __byte_perm(c[3] << 6, 0, 0x2301);
     }
     return mine;
 }
@@ -280,7 +267,7 @@ __global__ void __launch_bounds__(64) quant_append_one_kernel(const QuantAppendP
     pdl_wait();
     pdl_trigger();
     const int i = blockIdx.x, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, side = threadIdx.x >> 5;
-    const __half *from = (side ? p.v_new : p.k_new) + (int64_t)i * p.new_stride + 8 * t;
+    const __half *from = (side ? p.v_new : p.k_new) + (int64_t)i * p.new_stride + 2 * t;
     const int N = p.seq_lens[i];
     int page = -1;
     if (N < 0 || N >= p.len_cap) {
@@ -298,10 +285,12 @@ __global__ void __launch_bounds__(64) quant_append_one_kernel(const QuantAppendP
     uint8_t *blk = p.cache + (int64_t)max(page, 0) * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * Q::bytes(tb);
     for (int h0 = 0; h0 < p.Hkv; h0 += 8) {
         const int h = h0 + g;
-        uint4 x[GR];
+        uint32_t x[GR][4];
 #pragma unroll
         for (int j = 0; j < GR; ++j)
-            x[j] = h < p.Hkv ? *reinterpret_cast<const uint4 *>(from + h * D + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                x[j][f] = h < p.Hkv ? *reinterpret_cast<const uint32_t *>(from + h * D + 32 * j + 8 * f) : 0u;
         uint32_t w[GR];
         const uint32_t si = quantise_rows<GR>(x, t, w);
         const int j = (lane & 28) + ((2 * t) & (GR - 1));
@@ -376,17 +365,19 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
         const unsigned lives = __ballot_sync(0xffffffffu, live);
         const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
         // a quad without a new token reads the nearest one's and stores nothing
-        const int64_t src = (int64_t)(off + (min(max(pos, N), N + n - 1) - N)) * p.new_stride + 8 * t;
+        const int64_t src = (int64_t)(off + (min(max(pos, N), N + n - 1) - N)) * p.new_stride + 2 * t;
         const __half *kx = p.k_new + src, *vx = p.v_new + src;
         // K and V of a head in turn
 #pragma unroll 1
         for (int it = it0; it < it1; ++it) {
-            uint4 x[GR];
+            uint32_t x[GR][4];
             const __half *from = (it & 1 ? vx : kx) + (it >> 1) * D;
             uint8_t *hb = blk + (it >> 1) * p.page_head_bytes;
 #pragma unroll
             for (int j = 0; j < GR; ++j)
-                x[j] = __ldcs(reinterpret_cast<const uint4 *>(from + 32 * j));
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    x[j][f] = __ldg(reinterpret_cast<const uint32_t *>(from + 32 * j + 8 * f));
             uint32_t w[GR];
             const uint32_t si = quantise_rows<GR>(x, t, w);  // s | b of group t & (GR - 1)
             if (!(it & 1)) {
