@@ -1162,14 +1162,19 @@ struct Launch {
 
 // Tiles of a (row, head) per CTA of its cluster up to which clusters are used:
 // beyond, the line's equal runs gain more by their balance than the merge costs,
-// sooner over the 4-bit cache, where an idle warp costs more.  Rows of n / 4 .. n
-// tokens, d = 128, Hq = 32, Hkv = 8, clusters against runs: 4-bit, 4 tiles a CTA,
-// 8.8 and 12.2 us (one row), 9.5 and 11.9 us (32 rows); 8 tiles, 14.5 and 14.2 us
-// (eight rows).  fp16, 4 tiles, 7.9 and 11.2 us (16 rows); 16 tiles, 11.9 and 15.2
-// us (four rows); 32 tiles, 29.6 and 31.2 us (32 rows), where a batch less even
-// than these would lose.
+// sooner over the 4-bit cache, where an idle warp costs more, and the sooner the
+// more CTAs share an SM.  d = 128, four query heads per KV head, clusters against
+// runs: 4-bit, rows of n / 4 .. n tokens, 4 tiles a CTA, 8.8 and 12.2 us (one
+// row), 9.5 and 11.9 us (32 rows); 8 tiles, 13.3 and 15.7 us (one row), 13.8 and
+// 15.9 us (three), 14.5 and 14.2 us (eight); 12 tiles, 17.5 and 16.5 us (one).
+// fp16, 4 tiles, 7.9 and 11.2 us (16 rows); 16 tiles, 11.9 and 15.2 us (four
+// rows); 32 tiles, 29.6 and 31.2 us (32 rows), where a batch less even than these
+// would lose.
 template <bool QUANT>
-constexpr int kMaxClusterTiles = QUANT ? 6 : 20;
+constexpr int max_cluster_tiles(bool two_per_sm)
+{
+    return !QUANT ? 20 : two_per_sm ? 8 : 6;
+}
 
 template <int D, int TBL>
 cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParams p, int sms, cudaStream_t s)
@@ -1189,7 +1194,7 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
     while (cl < 4 && (2ll << cl) <= most && units << (cl + 1) <= (int64_t)sms * LC::kCtasPerSm)
         ++cl;
     for (; cl >= 0 && most >= 2 && units << cl <= (int64_t)sms * LC::kCtasPerSm &&
-           most <= (int64_t)kMaxClusterTiles<L::QUANT> << cl;
+           most <= (int64_t)max_cluster_tiles<L::QUANT>(units << cl <= 2 * sms) << cl;
          --cl) {
         cudaError_t e = prepare<D, TBL, true>(k);
         if (e != cudaSuccess)
