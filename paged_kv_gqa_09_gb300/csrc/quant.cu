@@ -576,9 +576,15 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
 cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
 {
     const int64_t chunks = ((int64_t)p.T + 7) / 8;
-    // several waves of short warps: 116k tokens of 8 heads took 104 us with one
-    // wave or three, 99 with eight, 111 with 32
-    p.parts = split_work(chunks, p.Hkv, 8 * 32 * (int64_t)sms, p.heads_per_part);
+    // several waves of warps, each with two heads or more unless the launch is a
+    // single wave: of eight heads, two per warp 38 us (42k tokens) and 99 us
+    // (117k), one 42 and 111 us, four 41 and 101 us, all eight 49 and 106 us
+    const int64_t wave = 32 * (int64_t)sms;
+    p.parts = split_work(chunks, p.Hkv, 8 * wave, p.heads_per_part);
+    if (p.heads_per_part == 1 && p.Hkv > 1 && chunks * p.parts > 2 * wave) {
+        p.heads_per_part = 2;
+        p.parts = (p.Hkv + 1) / 2;
+    }
     const int64_t grid = (chunks * p.parts + kWarps - 1) / kWarps;
     return d == 128 ? launch(quant_read_kernel<128>, p, grid, kThreads, s) : launch(quant_read_kernel<64>, p, grid, kThreads, s);
 }
