@@ -567,7 +567,7 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
     p.groups = (int64_t)p.T / 8 + 2 * (int64_t)p.B;
     // resident CTAs walk the units: fine ones, so that they end together
     const int64_t ctas = kAppendCtas * (int64_t)sms;
-    p.parts = split_work(p.groups, 2 * p.Hkv, 4 * ctas * kWarps, p.its_per_part);
+    p.parts = split_work(p.groups, 2 * p.Hkv, 2 * ctas * kWarps, p.its_per_part);
     int64_t grid = (p.groups * p.parts + kWarps - 1) / kWarps;
     grid = grid < ctas ? grid : ctas;
     return d == 128 ? launch(quant_append_kernel<128>, p, grid, kThreads, s) : launch(quant_append_kernel<64>, p, grid, kThreads, s);
