@@ -413,8 +413,9 @@ typedef struct {
  * (0 for a bad shape). */
 size_t pkv_quant_page_bytes(const pkv_shape_t *shape);
 
-/* Bytes of the workspace of the four calls below (0 for a bad shape).  It
- * depends on B, Hq / Hkv and d only. */
+/* Bytes of the workspace of the four calls below (0 for a bad shape).  It grows
+ * with Hq / Hkv and d only; one of a larger size serves every smaller shape, so
+ * batches of any B can share one. */
 size_t pkv_attn_workspace_size(const pkv_shape_t *shape);
 
 /* pkv_quant_append -- quantise new tokens into the 4-bit cache.

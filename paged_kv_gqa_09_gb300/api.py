@@ -580,10 +580,14 @@ class PagedDecoder:
 
     def attn_workspace(self, shape: Shape, device) -> torch.Tensor:
         """The workspace of step_window, step_quant and append_quant for this
-        shape on this device (zeroed when it is made)."""
-        key = (device, shape.B, shape.Hq // shape.Hkv, shape.d)
+        kind of shape on this device, zeroed when it is made -- which is not while
+        a graph is captured, whose replay alone would do it.  The decoder's calls
+        must not overlap on the GPU."""
+        key = (device, shape.Hq // shape.Hkv, shape.d)
         ws = self._attn.get(key)
         if ws is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("call the step (or attn_workspace) once before capturing it: its workspace is made by then")
             ws = self._attn[key] = torch.zeros(pkv_attn_workspace_size(shape), dtype=torch.uint8, device=device)
         return ws
 

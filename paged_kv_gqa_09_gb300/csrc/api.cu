@@ -1174,8 +1174,8 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     p.seq_lens = sl;
     p.cache = static_cast<const uint8_t *>(cache);
     p.ws = ws_hdr(d_ws);
-    p.counters = reinterpret_cast<int32_t *>(static_cast<char *>(d_ws) + aws_counters_off(s->B));
-    p.partials = reinterpret_cast<float *>(static_cast<char *>(d_ws) + aws_partials_off(s->B));
+    p.counters = reinterpret_cast<int32_t *>(static_cast<char *>(d_ws) + kAttnCountersOff);
+    p.partials = reinterpret_cast<float *>(static_cast<char *>(d_ws) + kAttnPartialsOff);
     p.o = static_cast<__half *>(o);
     p.lse = lse;
     p.page_head_bytes = quant_page_head_bytes(s);
@@ -1223,8 +1223,7 @@ size_t pkv_attn_workspace_size(const pkv_shape_t *s)
 {
     if (check_shape(s))
         return 0;
-    return aws_partials_off(s->B) +
-           (size_t)2 * kAttnMaxSegs * (s->Hq / s->Hkv) * (size_t)(s->d + 2) * sizeof(float);
+    return kAttnPartialsOff + (size_t)2 * kAttnMaxSegs * (s->Hq / s->Hkv) * (size_t)(s->d + 2) * sizeof(float);
 }
 
 int pkv_quant_append(const pkv_shape_t *s, void *d_ws, const void *k_new, const void *v_new, int64_t new_stride,
@@ -1255,7 +1254,6 @@ int pkv_quant_append(const pkv_shape_t *s, void *d_ws, const void *k_new, const 
     p.seq_lens_out = sl_out;
     p.cache = static_cast<uint8_t *>(cache);
     p.ws = ws_hdr(d_ws);
-    p.row_bad = reinterpret_cast<int32_t *>(static_cast<char *>(d_ws) + aws_row_bad_off());
     p.page_head_bytes = quant_page_head_bytes(s);
     p.T = total_new;
     p.B = s->B;

@@ -48,7 +48,8 @@ constexpr int kMaxG = 8;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 20000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;  // running maximum before the first score (finite: -inf - it is -inf)
+constexpr float kNoMax = -3.402823466e38f;  // running maximum before the first score: the least finite value (-inf - it is -inf)
+constexpr float kHalfMax = 65504.f;
 
 // The running maximum of the softmax follows a tile's only when that exceeds it
 // by more than this (in log2 units): weights then stay below 2^8, well inside
@@ -94,6 +95,13 @@ struct Layout {
     static_assert(QUANT || kStageBytes % 1024 == 0, "swizzled tiles keep 1024-byte alignment");
     static_assert(kCtasPerSm * (kAlloc + 1024) <= 228 * 1024, "resident CTAs");
 };
+
+// An output's rounding to fp16.  The weights sum up to a little more or less
+// rounded than unrounded (see softmax_step()), so that a mean of values at the
+// type's end could pass it and become infinite: finite results stay finite.
+__device__ __forceinline__ float within_half(float x) { return fabsf(x) < INFINITY ? fminf(fmaxf(x, -kHalfMax), kHalfMax) : x; }
+__device__ __forceinline__ __half out_half(float x) { return __float2half_rn(within_half(x)); }
+__device__ __forceinline__ uint32_t out_half2(float x, float y) { return pack_half2(within_half(x), within_half(y)); }
 
 // What of a row of N tokens is visible: tokens [0, ns) and [w0, N), in tiles
 // [0, a) and [b, b + T - a).
@@ -767,7 +775,7 @@ __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, in
             const int64_t oh = (int64_t)unit * p.G + g;  // unit = row * Hkv + head
             if (sub == 0)
                 *reinterpret_cast<uint2 *>(p.o + oh * D + at * 4) =
-                    make_uint2(pack_half2(acc[q].x * inv, acc[q].y * inv), pack_half2(acc[q].z * inv, acc[q].w * inv));
+                    make_uint2(out_half2(acc[q].x * inv, acc[q].y * inv), out_half2(acc[q].z * inv, acc[q].w * inv));
             if (p.lse && lane == 0)
                 p.lse[oh] = (M[q] + log2f(L[q])) * kLn2;
         }
@@ -878,12 +886,12 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
         for (int y = 0; y < KQ; ++y) {
             const int d0 = 16 * (w * KQ + y) + r0;
             if (ok0) {
-                out[h0 * D + d0] = __float2half_rn(R[y][0] * i0);
-                out[h0 * D + d0 + 8] = __float2half_rn(R[y][2] * i0);
+                out[h0 * D + d0] = out_half(R[y][0] * i0);
+                out[h0 * D + d0 + 8] = out_half(R[y][2] * i0);
             }
             if (ok1) {
-                out[(h0 + 1) * D + d0] = __float2half_rn(R[y][1] * i1);
-                out[(h0 + 1) * D + d0 + 8] = __float2half_rn(R[y][3] * i1);
+                out[(h0 + 1) * D + d0] = out_half(R[y][1] * i1);
+                out[(h0 + 1) * D + d0 + 8] = out_half(R[y][3] * i1);
             }
         }
         if (p.lse && w == 0 && lane < 4) {
@@ -1062,7 +1070,7 @@ __device__ __forceinline__ void merge_cluster(const AttendParams &p, uint32_t st
         }
         const int64_t oh = (int64_t)unit * p.G + g;
         const float inv = live ? 1.f / Ls : 0.f;
-        *reinterpret_cast<uint2 *>(p.o + oh * D + d) = make_uint2(pack_half2(A.x * inv, A.y * inv), pack_half2(A.z * inv, A.w * inv));
+        *reinterpret_cast<uint2 *>(p.o + oh * D + d) = make_uint2(out_half2(A.x * inv, A.y * inv), out_half2(A.z * inv, A.w * inv));
         if (p.lse && d == 0)
             p.lse[oh] = live ? (M + log2f(Ls)) * kLn2 : -INFINITY;
     }

@@ -108,14 +108,15 @@ struct AppendParams {
     int B, Hkv, d, log2P, num_pages, bt_stride;
 };
 
-// Workspace of the windowed and 4-bit operators: the header, one int per row
-// (rows that an append refuses), one counter per segment of the attention's
-// work (at most three per CTA), then two partial states per segment.
+// Workspace of the windowed and 4-bit operators: the header, one counter per
+// segment of the attention's work (at most three per CTA), then two partial
+// states per segment.  What has to be zero lies where it does for every shape,
+// so that calls of different batches can share a workspace.
 constexpr int kAttnMaxCtas = 640;
 constexpr int kAttnMaxSegs = 3 * kAttnMaxCtas;
-inline size_t aws_row_bad_off() { return kWsHeaderBytes; }
-inline size_t aws_counters_off(int B) { return (kWsHeaderBytes + sizeof(int32_t) * (size_t)B + 15) & ~(size_t)15; }
-inline size_t aws_partials_off(int B) { return aws_counters_off(B) + sizeof(int32_t) * (size_t)kAttnMaxSegs; }
+constexpr size_t kAttnCountersOff = kWsHeaderBytes;
+constexpr size_t kAttnPartialsOff = kAttnCountersOff + sizeof(int32_t) * kAttnMaxSegs;
+static_assert(kAttnPartialsOff % 16 == 0, "states are read 16 bytes at a time");
 
 struct QuantAppendParams {
     const __half *k_new, *v_new;
@@ -125,7 +126,6 @@ struct QuantAppendParams {
     int32_t *seq_lens_out;      // may be seq_lens
     uint8_t *cache;
     WsHeader *ws;
-    int32_t *row_bad;           // [B], zero between launches
     int64_t page_head_bytes;    // one page of one head
     int T, B, Hkv, log2P, tb_log2, num_pages, bt_stride, len_cap;
     int64_t groups;             // set by the launcher: groups of eight positions,

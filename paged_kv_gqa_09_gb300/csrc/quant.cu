@@ -351,10 +351,8 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
             continue;
         const int page = p.bt[(int64_t)i * p.bt_stride + (pos0 >> p.log2P)];
         if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) {
+            if (lane == 0)
                 report_error(p.ws, kErrBadPage, i, (int)(pos0 >> p.log2P), page);
-                p.row_bad[i] = 1;
-            }
             bad = true;
             continue;
         }
@@ -411,21 +409,18 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
             }
         }
     }
-    // the last CTA to get here advances the lengths: every other one has read
-    // them by then, and its rows' flags are set; CTAs that set one are counted above
+    // the last CTA to get here advances the lengths, which every other one has
+    // read by then; CTAs that met a bad page are counted above kBad
     constexpr int kBad = 1 << 20;
     const int any_bad = __syncthreads_or(bad ? 1 : 0);
     if (threadIdx.x == 0) {
-        if (any_bad)
-            __threadfence();
-        s_seen = atomicAdd(&p.ws->append_done, any_bad ? 1 + kBad : 1) + (any_bad ? 1 + kBad : 1);
+        const int add = any_bad ? 1 + kBad : 1;
+        s_seen = atomicAdd(&p.ws->append_done, add) + add;
     }
     __syncthreads();
     if ((s_seen & (kBad - 1)) != (int)gridDim.x)
         return;
-    const bool flags = s_seen >= kBad;
-    if (flags)
-        __threadfence();
+    const bool pages_bad = s_seen >= kBad;  // then the rows that met them are looked for again
     // offsets that do not ascend within the buffer give tokens to no row or to two: the whole call is refused
     bool span = false;
     for (int r = threadIdx.x; r < p.B; r += kThreads) {
@@ -441,11 +436,13 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
         const bool first = r < kThreads;
         const int Nr = first ? my_N : p.seq_lens[r];
         const int off = first ? my_off : p.offsets[r], nr = first ? my_n : p.offsets[r + 1] - off;
-        const int flag = flags ? __ldcg(p.row_bad + r) : 0;
-        const bool ok = !span && append_fits(p, r, Nr, off, nr, true) && !flag;
+        bool ok = !span && append_fits(p, r, Nr, off, nr, true);
+        if (pages_bad && ok && nr > 0)
+            for (int64_t b = Nr >> p.log2P; b <= ((int64_t)Nr + nr - 1) >> p.log2P; ++b) {
+                const int page = p.bt[(int64_t)r * p.bt_stride + b];
+                ok = ok && page >= 0 && page < p.num_pages;
+            }
         p.seq_lens_out[r] = ok ? Nr + nr : Nr;
-        if (flag)
-            p.row_bad[r] = 0;
     }
     if (threadIdx.x == 0)
         p.ws->append_done = 0;

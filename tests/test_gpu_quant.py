@@ -15,9 +15,9 @@ def dev(x):
     return torch.from_numpy(np.ascontiguousarray(x)).cuda()
 
 
-def clean(ws, B):
-    """The workspace's row flags and counters are back at zero."""
-    assert int(ws[64:].view(torch.int32)[:(B + 3) // 4 * 4 + 1920].abs().sum()) == 0
+def clean(ws):
+    """The workspace's counters are back at zero."""
+    assert int(ws[64:64 + 4 * 1920].view(torch.int32).abs().sum()) == 0
     assert int(ws[16:64].view(torch.int32).abs().sum()) == 0
 
 
@@ -85,7 +85,7 @@ class Batch:
     def ok(self):
         st, msg = api.pkv_get_error(self.ws)
         assert st == 0, msg
-        clean(self.ws, self.B)
+        clean(self.ws)
 
     def check(self, q, window=None, sinks=0):
         o, lse = self.decode(q, window, sinks)
@@ -612,7 +612,7 @@ class Pages:
         o, lse = self.decode(window, sinks)
         compare(o, lse, self.q, self.k, self.v, self.shape.scale, window, sinks)
         assert api.pkv_get_error(self.ws)[0] == 0
-        clean(self.ws, self.B)
+        clean(self.ws)
 
 
 @pytest.mark.parametrize("d,P,Hkv,G", [(128, 16, 2, 4), (64, 8, 3, 5), (128, 64, 1, 8), (64, 256, 2, 1), (128, 128, 8, 2),
@@ -705,7 +705,7 @@ def test_window_decode_of_runs_that_are_split():
     assert (np.abs(o.cpu().numpy().astype(np.float64) - ro) <= to + extra).all()
     assert (np.abs(lse.cpu().numpy().astype(np.float64) - np.log(times) - rl) <= tl + 2.0 ** -12).all()
     assert api.pkv_get_error(b.ws)[0] == 0
-    clean(b.ws, b.B)
+    clean(b.ws)
 
 
 @pytest.mark.parametrize("d,P,Hkv,G", [(128, 16, 2, 4), (64, 8, 3, 5), (128, 64, 1, 8), (64, 256, 2, 1), (128, 128, 8, 2)])
@@ -720,3 +720,105 @@ def test_window_decode_long_rows_over_a_wide_table(lens):
     b = widen(Pages(lens, Hkv=2, G=8, d=128, P=16, seed=31))
     for window, sinks in ((10 ** 6, 4), (20000, 100)):
         b.check(window, sinks)
+
+
+# ------------------------------------------------------------------ calls at the edges
+
+def test_one_workspace_serves_batches_of_any_size():
+    """Long rows whose states are split, then many rows, then an append that meets a bad page, over one workspace."""
+    few = widen(Batch([5000, 700], Hkv=2, G=4, d=64, P=16, seed=61))
+    many = Batch([300], Hkv=2, G=4, d=64, P=16, seed=62)
+    B = 2000
+    few.grow([5000, 700])
+    many.grow([300])
+    many.bt = many.bt.repeat(B, 1).contiguous()  # rows may share pages that are only read
+    many.lens = many.lens.repeat(B)
+    many.shape.B = B
+    ws = few.ws  # made for the small batch
+    q = dev(np.random.default_rng(63).standard_normal((1, many.Hq, 64)).astype(np.float16)).repeat(B, 1, 1)
+    ref = few.decode(queries(few))
+
+    def decode_many():
+        o = torch.full_like(q, float("nan"))
+        api.pkv_quant_decode(many.shape, ws, q, many.cache, many.bt, many.lens, o)
+        return o
+
+    for _ in range(2):
+        got = few.decode(queries(few))
+        assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+        o = decode_many()
+        ro, _, to, _ = R.attention(q[:1].cpu().numpy(), [R.values(many.k[0])], [R.values(many.v[0])],
+                                   float(np.float32(many.shape.scale)))
+        assert (np.abs(o.cpu().numpy().astype(np.float64) - ro) <= to).all()
+    # 2000 rows of one new token each, of which one names a bad page
+    lone = Batch([3] * B, Hkv=2, G=4, d=64, P=8, seed=64)
+    lone.bt[77, 0] = -1
+    off = dev(np.arange(B + 1, dtype=np.int32))
+    x = dev(np.random.default_rng(65).standard_normal((B, 2, 64)).astype(np.float16))
+    api.pkv_quant_append(lone.shape, ws, x, x, lone.bt, lone.lens, lone.cache, new_offsets=off)
+    assert lone.lens.cpu().tolist() == [0 if i == 77 else 1 for i in range(B)]
+    st, msg = api.pkv_get_error(ws)
+    assert st == _lib.PKV_EDEVICE and "row 77" in msg
+    clean(ws)
+
+
+@pytest.mark.parametrize("rows", [1, 300])  # a cluster's merge and a CTA's own rounding
+def test_a_mean_of_the_greatest_values_stays_finite(rows):
+    """Weights 1 and 128 (1 + 9/16 2^-10), of which fp16 holds the second as 128 (1 + 2^-10): over their sum
+    before rounding, values at the type's end come out 2^-11.2 beyond it."""
+    n = 600
+    b = Pages([n], Hkv=1, G=1, d=64, P=16, seed=66)
+    b.shape.scale = float(np.log(128 * (1 + 0.5625 / 1024)))
+    b.kc.fill_(0)
+    b.vc.fill_(65504.0)
+    b.kc[..., 0] = -100.0
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 0] = 1.0
+    for t, x in ((0, 0.0), (256, 1.0)):  # the same warp's: tiles of 128 tokens
+        b.kc[int(b.bt[0, t // 16]), t % 16, 0, 0] = x
+    b.bt, b.lens, b.q = b.bt.repeat(rows, 1).contiguous(), b.lens.repeat(rows), b.q.repeat(rows, 1, 1).contiguous()
+    b.shape.B = rows
+    o, _ = b.decode(10 ** 6, 0)
+    assert (o == 65504.0).all()
+    b.vc.fill_(-65504.0)
+    o, _ = b.decode(10 ** 6, 0)
+    assert (o == -65504.0).all()
+    b.vc.fill_(float("inf"))  # an infinite value stays one
+    o, _ = b.decode(10 ** 6, 0)
+    assert not torch.isfinite(o).any()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_of_any_size_have_a_greatest(wide):
+    """Equal scores of -1e32: their mean, not a row without a maximum."""
+    b = Pages([200, 1], Hkv=1, G=2, d=64, P=16, seed=67)
+    if wide:
+        b = widen(b)
+    b.shape.scale = -1e32
+    b.kc.fill_(0)
+    b.kc[..., 3] = 1.0
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 3] = 1.0
+    o, lse = b.decode(10 ** 6, 0)
+    for i in range(2):
+        # one rounding of the mean and fp32 sums of 200 terms of at most 8
+        assert np.abs(o[i].cpu().numpy().astype(np.float64) - b.v[i].mean(0)).max() <= 2.0 ** -11 * 8 + 200 * 8 * 2.0 ** -24
+        assert (lse[i] / -1e32 - 1).abs().max() <= 1e-6
+
+
+def test_a_decoder_makes_its_workspace_before_a_capture():
+    b = Batch([60, 33], Hkv=2, G=4, d=64, P=8, seed=68)
+    b.grow([50, 20])
+    dec, q = api.PagedDecoder(), queries(b)
+    o = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="before capturing"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            dec.step_quant(q, b.cache, b.bt, b.lens, o=o, want_lse=False)
+    want, _ = dec.step_quant(q, b.cache, b.bt, b.lens, want_lse=False)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dec.step_quant(q, b.cache, b.bt, b.lens, o=o, want_lse=False)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
