@@ -96,20 +96,25 @@ __device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[GR])
         *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
+// 16 bytes from global to shared memory, and waiting for all but the last N
+// batches of such copies.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 1 / x for normal x, within 2^-23 of itself.
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// x y + z, rounded once, within [0, 1]; 0 for a NaN.
-__device__ __forceinline__ float fma_sat(float x, float y, float z)
-{
-    float r;
-    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-    return r;
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
@@ -139,24 +144,24 @@ __device__ __forceinline__ bool append_fits(const QuantAppendParams &p, int i, i
 // The four code pairs of quantise_rows() below, decided exactly; out of line, so
 // that the loop around it stays small.  y is near enough to tell the two codes
 // in question, and the border between them decides.
-__device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b, float i15, float c15)
+__device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b)
 {
-    constexpr float kMagic = 12582912.f;
+    if (!(s > 0.f))  // 0 or NaN
+        return make_uint4(0, 0, 0, 0);
+    const float i = rcp_approx(s), c = -fmaf(16.f, s, b) * i;
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
     uint32_t w[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const float2 v = __half22float2(as_half2(xs[u]));
-        float n[2];
+        uint32_t n[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float z = fminf(fmaxf(e ? v.y : v.x, -kQuantLimit), kQuantLimit);
-            const float y = fma_sat(z, i15, c15);
-            const float near = fmaf(y, 15.f, kMagic) - kMagic;
-            const float below = fmaf(y, 15.f, -near) < 0.f ? near - 1.f : near;  // the lower of the two, -1 at the least
-            n[e] = z >= __fmaf_ru(below + 16.5f, s, b) ? fminf(below + 1.f, 15.f) : fmaxf(below, 0.f);
+            const float below = floorf(fminf(fmaxf(fmaf(z, i, c), -1.f), 15.f));  // the lower of the two
+            n[e] = (uint32_t)(z >= __fmaf_ru(below + 16.5f, s, b) ? fminf(below + 1.f, 15.f) : fmaxf(below, 0.f));
         }
-        w[u] = __byte_perm(__float_as_uint(n[0] + kMagic), __float_as_uint(n[1] + kMagic), 0x5410);
+        w[u] = n[0] | n[1] << 16;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -165,18 +170,23 @@ __device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b, float
 // 32 j + 8 f + 2 t and the next of its token; w[j] becomes its word (t, j).
 // Returns s | b << 16 of group t & (GR - 1) of the token.
 //
-// In units of codes y = (x - b) / s - 16 comes, over 15, from one fused
-// multiply-add with i = 1 / (15 s) and c = -(16 s + b) i in fp32.  i is within
-// 2^-23 of itself, which scales y as a whole, c is rounded twice more and y
-// once: y is at most (|16 + b / s| + 23) 2^-23 off.  Where it lies further than
-// twice that from every border (halves of a step) the rounded y is the code;
-// elsewhere -- one value in some 2000, nearly all of them ties, since x, s and
-// b lie on coarse grids -- and where values are beyond the limit, the border
-// itself decides.
+// n = x i + c, one fused multiply-add with i = 1 / s and c = M + 1/2 - (16 s + b) i,
+// M = 192, is the code in fixed point: floats in [128, 256) are 2^-16 apart, so
+// that the code stands in the bits from 16 on and the distance to the border
+// below it in the low 16.  i is within 2^-23 of itself, which scales the at most
+// 16 steps from lo as a whole (2^-19); 16 s + b, c and n are rounded once each.
+// With a = |16 + b / s| that makes 2^-24 a, 2^-17 + 2^-21.9 a and 2^-17, less
+// than E = 3 + a / 16 units of 2^-16 together (a is at most 15 2^10 or so, since
+// lo and hi differ by a step of fp16 at least).  A value whose low bits are E
+// from a border or further has its code; elsewhere -- one in some 2000, nearly
+// all of them ties, since x, s and b lie on coarse grids -- and where lo or hi
+// come out beyond the codes, are beyond the limit or NaN, the border itself
+// decides.
 template <int GR>
 __device__ __forceinline__ uint32_t quantise_rows(const uint32_t (&x)[GR][4], int t, uint32_t (&w)[GR])
 {
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
+    constexpr float kM = 192.f, kM5 = 192.5f;
+    constexpr uint32_t kMCode = 0x43404340u;  // two upper halves of M
     uint32_t mm[4];  // least | -greatest of the lane's eight values of group j (twice over for GR = 2)
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
@@ -200,36 +210,34 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint32_t (&x)[GR][4], in
     quant_params(lo, hi, s, b);
     const uint32_t mine = nan ? 0x7fff7fffu : as_word(s, b);
     const float sf = __half2float(s);
-    // s = 0 or NaN: every code is 0
-    const float i_mine = sf > 0.f && !nan ? rcp_approx(15.f * sf) : 0.f;
-    const float c_mine = -fmaf(16.f, sf, __half2float(b)) * i_mine;
-    const unsigned wide = __ballot_sync(0xffffffffu, (lo != lo0 || hi != hi0) && !nan);
+    const float i_mine = sf > 0.f ? rcp_approx(sf) : 0.f;  // s = 0: every code is 0
+    const float c_mine = fmaf(-fmaf(16.f, sf, __half2float(b)), i_mine, kM5);
+    const unsigned hard = __ballot_sync(0xffffffffu, lo != lo0 || hi != hi0 || fmaf(lo, i_mine, c_mine) < kM ||
+                                                         fmaf(hi, i_mine, c_mine) >= kM + 16.f);
     const int base = threadIdx.x & 28;
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
-        const float i15 = __shfl_sync(0xffffffffu, i_mine, base + j), c15 = __shfl_sync(0xffffffffu, c_mine, base + j);
-        const float edge = 0.5f - fmaf(fabsf(c15), 15.f * 0x1p-22f, 0x1p-17f);
-        float worst = 0.f;
-        uint32_t c[4];  // pairs of codes, one per field
+        const float i = __shfl_sync(0xffffffffu, i_mine, base + j), c = __shfl_sync(0xffffffffu, c_mine, base + j);
+        const uint32_t E = (uint32_t)fmaf(fabsf(c - kM5), 0.0625f, 4.f), EE = E * 0x10001u;
+        uint32_t nearest = 0xffffffffu;  // the least low bits, E further on, of either half
+        uint32_t code[4];                // pairs of codes, one per field, beside M
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const float2 v = __half22float2(as_half2(x[j][u]));
-            const float y0 = fma_sat(v.x, i15, c15), y1 = fma_sat(v.y, i15, c15);
-            const float n0 = fmaf(y0, 15.f, kMagic), n1 = fmaf(y1, 15.f, kMagic);
-            const float d0 = fmaf(y0, 15.f, kMagic - n0), d1 = fmaf(y1, 15.f, kMagic - n1);
-            worst = fmaxf(fmaxf(worst, fabsf(d0)), fabsf(d1));
-            c[u] = __byte_perm(__float_as_uint(n0), __float_as_uint(n1), 0x5410);
+            const uint32_t n0 = __float_as_uint(fmaf(v.x, i, c)), n1 = __float_as_uint(fmaf(v.y, i, c));
+            code[u] = __byte_perm(n0, n1, 0x7632);
+            nearest = __viaddmin_u16x2(__byte_perm(n0, n1, 0x5410), EE, nearest);
         }
-        const bool near = worst > edge || (wide >> (base + j) & 1);
+        w[j] = (code[0] << 6) + (code[1] << 2) + (code[2] << 10) - ((kMCode << 6) + (kMCode << 2) + (kMCode << 10)) +
+               __byte_perm((code[3] << 6) & 0x03c003c0u, 0, 0x2301);
+        const bool near = min(nearest & 0xffffu, nearest >> 16) < 2 * E || (hard >> (base + j) & 1);
         if (__any_sync(0xffffffffu, near)) {
             const __half2 sb = as_half2(__shfl_sync(0xffffffffu, mine, base + j));
-            if (near && __low2float(sb) > 0.f) {
-                const uint4 e = quant_codes_exact(make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]), __low2float(sb),
-                                                  __high2float(sb), i15, c15);
-                c[0] = e.x, c[1] = e.y, c[2] = e.z, c[3] = e.w;
+            if (near) {
+                const uint4 e = quant_codes_exact(make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]), __low2float(sb), __high2float(sb));
+                w[j] = (e.x << 6) + (e.y << 2) + (e.z << 10) + __byte_perm(e.w << 6, 0, 0x2301);
             }
         }
-        w[j] = (c[0] << 6) + (c[1] << 2) + (c[2] << 10) + __byte_perm(c[3] << 6, 0, 0x2301);
     }
     return mine;
 }
@@ -321,11 +329,14 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
 {
     using Q = QuantLayout<D>;
     constexpr int GR = Q::GR;
+    constexpr int kPitch = 2 * D + 16;  // bytes between tokens of a tile: the quads' words are in 32 banks
     __shared__ int s_seen;
+    __shared__ __align__(16) uint8_t s_tile[kWarps][2][8 * kPitch];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int e = g & 1, t2 = g >> 1;
+    uint8_t *tile = s_tile[threadIdx.x >> 5][0];
     const int tb = 1 << p.tb_log2;
     // what the last CTA needs of its first rows, on its way already
     int my_off = 0, my_n = 0, my_N = 0;
@@ -362,20 +373,40 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
         const bool live = pos >= N && pos < N + n;
         const unsigned lives = __ballot_sync(0xffffffffu, live);
         const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
-        // a quad without a new token reads the nearest one's and stores nothing
-        const int64_t src = (int64_t)(off + (min(max(pos, N), N + n - 1) - N)) * p.new_stride + 2 * t;
-        const __half *kx = p.k_new + src, *vx = p.v_new + src;
+        // where there is no new token, the nearest one's values are read and nothing is stored
+        auto fetch = [&](int it) {
+            constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a token, tokens at a time
+            const __half *from = (it & 1 ? p.v_new : p.k_new) + (it >> 1) * D + 8 * (lane % kLanes);
+            const uint32_t to = smem_u32(tile + (it & 1) * 8 * kPitch + 16 * (lane % kLanes));
+#pragma unroll
+            for (int r0 = 0; r0 < 8; r0 += kRows) {
+                const int row = r0 + lane / kLanes;
+                const int tok = off + (min(max((int)pos0 + row, N), N + n - 1) - N);
+                copy16_async(to + row * kPitch, from + (int64_t)tok * p.new_stride);
+            }
+            copies_commit();
+        };
+        __syncwarp();
+        fetch(it0);
         // K and V of a head in turn
 #pragma unroll 1
         for (int it = it0; it < it1; ++it) {
+            if (it + 1 < it1) {
+                fetch(it + 1);
+                copies_wait<1>();
+            } else {
+                copies_wait<0>();
+            }
+            __syncwarp();
             uint32_t x[GR][4];
-            const __half *from = (it & 1 ? vx : kx) + (it >> 1) * D;
+            const uint8_t *from = tile + (it & 1) * 8 * kPitch + g * kPitch + 4 * t;
             uint8_t *hb = blk + (it >> 1) * p.page_head_bytes;
 #pragma unroll
             for (int j = 0; j < GR; ++j)
 #pragma unroll
                 for (int f = 0; f < 4; ++f)
-                    x[j][f] = __ldg(reinterpret_cast<const uint32_t *>(from + 32 * j + 8 * f));
+                    x[j][f] = *reinterpret_cast<const uint32_t *>(from + 64 * j + 16 * f);
+            __syncwarp();  // the tile may be filled again
             uint32_t w[GR];
             const uint32_t si = quantise_rows<GR>(x, t, w);  // s | b of group t & (GR - 1)
             if (!(it & 1)) {
