@@ -6,16 +6,21 @@
 // read: tokens of the cache become packed fp16 K and V again.
 //
 // Both are one pass over their data: append reads 2 bytes per value and writes
-// 0.625, read the other way round; HBM bounds them, append closely followed by
-// its arithmetic (some fifteen instructions per value).  A warp takes eight
-// tokens, four lanes each, and loops over KV heads and sides, so that rows,
-// pages and offsets are looked up once for all of them; short calls split the
-// heads over more warps.  Lane t of a token's four holds the words (t, j), the
-// codes of dims 32 j + 8 f + 2 t and the next (f = 0..3).  append reads just
-// those, four bytes at a time (a quad's 16 bytes side by side; all of a line is
-// used from L1): 16-byte reads of dims 32 j + 8 t .. cost an exchange among the
-// four lanes, two instructions per value.  read does make that exchange, since
-// four-byte stores would reach L2 one by one.
+// 0.625, read the other way round.  42k tokens of 8 heads, d = 128, are 226 MB,
+// 33 us at the copy rate: read takes 38 us, append 55, where its some fourteen
+// instructions per value are the bound (issue 75%, ALU 64%, DRAM 50%).
+//
+// A warp takes eight tokens, four lanes each, and loops over KV heads and sides,
+// so that rows, pages and offsets are looked up once for all of them; short
+// calls split the heads over more warps.  Lane t of a token's four holds the
+// words (t, j), the codes of dims 32 j + 8 f + 2 t and the next (f = 0..3).
+// append brings a tile (eight tokens of one head and side) into shared memory
+// while it works on the one before, and reads its words from there: read from
+// global memory 16 bytes at a time they cost an exchange among the four lanes
+// (two instructions per value, 65 us), four bytes at a time as many L1 lookups
+// as shared memory takes cycles (no slower with d = 128, 39.2 against 37.7 us
+// with d = 64).  read does make that exchange, since four-byte stores would
+// reach L2 one by one.
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
@@ -177,8 +182,8 @@ __device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b)
 // 16 steps from lo as a whole (2^-19); 16 s + b, c and n are rounded once each.
 // With a = |16 + b / s| that makes 2^-24 a, 2^-17 + 2^-21.9 a and 2^-17, less
 // than E = 3 + a / 16 units of 2^-16 together (a is at most 15 2^10 or so, since
-// lo and hi differ by a step of fp16 at least).  A value whose low bits are E
-// from a border or further has its code; elsewhere -- one in some 2000, nearly
+// lo and hi differ by a step of fp16 at least; the warp takes its groups'
+// greatest E).  A value whose low bits are E from a border or further has its code; elsewhere -- one in some 2000, nearly
 // all of them ties, since x, s and b lie on coarse grids -- and where lo or hi
 // come out beyond the codes, are beyond the limit or NaN, the border itself
 // decides.
@@ -211,15 +216,17 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint32_t (&x)[GR][4], in
     const uint32_t mine = nan ? 0x7fff7fffu : as_word(s, b);
     const float sf = __half2float(s);
     const float i_mine = sf > 0.f ? rcp_approx(sf) : 0.f;  // s = 0: every code is 0
-    const float c_mine = fmaf(-fmaf(16.f, sf, __half2float(b)), i_mine, kM5);
-    const unsigned hard = __ballot_sync(0xffffffffu, lo != lo0 || hi != hi0 || fmaf(lo, i_mine, c_mine) < kM ||
-                                                         fmaf(hi, i_mine, c_mine) >= kM + 16.f);
+    float c_mine = fmaf(-fmaf(16.f, sf, __half2float(b)), i_mine, kM5);
+    const uint32_t E = __reduce_max_sync(0xffffffffu, min((uint32_t)fmaf(fabsf(c_mine - kM5), 0.0625f, 4.f), 0x3fffu));
+    const uint32_t EE = E * 0x10001u;  // one for the warp
+    // a NaN's low bits are ones: next to a border
+    if (lo != lo0 || hi != hi0 || fmaf(lo, i_mine, c_mine) < kM || fmaf(hi, i_mine, c_mine) >= kM + 16.f)
+        c_mine = __uint_as_float(0x7fffffffu);
     const int base = threadIdx.x & 28;
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
         const float i = __shfl_sync(0xffffffffu, i_mine, base + j), c = __shfl_sync(0xffffffffu, c_mine, base + j);
-        const uint32_t E = (uint32_t)fmaf(fabsf(c - kM5), 0.0625f, 4.f), EE = E * 0x10001u;
-        uint32_t nearest = 0xffffffffu;  // the least low bits, E further on, of either half
+        uint32_t nearest = 0x7fff7fffu;  // the least low bits, E further on, of either half
         uint32_t code[4];                // pairs of codes, one per field, beside M
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -230,7 +237,7 @@ __device__ __forceinline__ uint32_t quantise_rows(const uint32_t (&x)[GR][4], in
         }
         w[j] = (code[0] << 6) + (code[1] << 2) + (code[2] << 10) - ((kMCode << 6) + (kMCode << 2) + (kMCode << 10)) +
                __byte_perm((code[3] << 6) & 0x03c003c0u, 0, 0x2301);
-        const bool near = min(nearest & 0xffffu, nearest >> 16) < 2 * E || (hard >> (base + j) & 1);
+        const bool near = (~((nearest | 0x80008000u) - 2 * EE) & 0x80008000u) != 0;  // one of them below 2 E
         if (__any_sync(0xffffffffu, near)) {
             const __half2 sb = as_half2(__shfl_sync(0xffffffffu, mine, base + j));
             if (near) {
@@ -374,15 +381,17 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
         const unsigned lives = __ballot_sync(0xffffffffu, live);
         const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
         // where there is no new token, the nearest one's values are read and nothing is stored
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a token, tokens at a time
+        int64_t tok[8 / kRows];
+#pragma unroll
+        for (int r0 = 0; r0 < 8; r0 += kRows)
+            tok[r0 / kRows] = off + (min(max((int)pos0 + r0 + lane / kLanes, N), N + n - 1) - N);
         auto fetch = [&](int it) {
-            constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a token, tokens at a time
             const __half *from = (it & 1 ? p.v_new : p.k_new) + (it >> 1) * D + 8 * (lane % kLanes);
             const uint32_t to = smem_u32(tile + (it & 1) * 8 * kPitch + 16 * (lane % kLanes));
 #pragma unroll
             for (int r0 = 0; r0 < 8; r0 += kRows) {
-                const int row = r0 + lane / kLanes;
-                const int tok = off + (min(max((int)pos0 + row, N), N + n - 1) - N);
-                copy16_async(to + row * kPitch, from + (int64_t)tok * p.new_stride);
+                copy16_async(to + (r0 + lane / kLanes) * kPitch, from + tok[r0 / kRows] * p.new_stride);
             }
             copies_commit();
         };

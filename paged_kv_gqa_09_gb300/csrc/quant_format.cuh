@@ -86,9 +86,7 @@ __device__ __forceinline__ void quant_params(float lo, float hi, __half &s, __ha
     s = hi > lo ? s : __ushort_as_half(0);
     // nearest to lo - 16 s, the lower one on a tie
     const float sf = __half2float(s);
-    const __half b0 = __float2half_rd(__fmaf_rd(-16.f, sf, lo));
-    const unsigned short bits = __half_as_ushort(b0);
-    const __half b1 = __ushort_as_half(bits & 0x8000 ? (bits == 0x8000 ? 1 : bits - 1) : bits + 1);  // its successor
+    const __half b0 = __float2half_rd(__fmaf_rd(-16.f, sf, lo)), b1 = __float2half_ru(__fmaf_ru(-16.f, sf, lo));
     const float mid = 0.5f * (__half2float(b0) + __half2float(b1));
     b = __fmaf_rd(16.f, sf, mid) < lo ? b1 : b0;
 }
