@@ -7,7 +7,7 @@
 //
 // Both are one pass over their data: append reads 2 bytes per value and writes
 // 0.625, read the other way round.  42k tokens of 8 heads, d = 128, are 226 MB,
-// 33 us at the copy rate: read takes 38 us, append 55, where its some fourteen
+// 33 us at the copy rate: read takes 38 us, append 50, where its some fourteen
 // instructions per value are the bound (issue 75%, ALU 64%, DRAM 50%).
 //
 // A warp takes eight tokens, four lanes each, and loops over KV heads and sides,
@@ -17,9 +17,8 @@
 // append brings a tile (eight tokens of one head and side) into shared memory
 // while it works on the one before, and reads its words from there: read from
 // global memory 16 bytes at a time they cost an exchange among the four lanes
-// (two instructions per value, 65 us), four bytes at a time as many L1 lookups
-// as shared memory takes cycles (no slower with d = 128, 39.2 against 37.7 us
-// with d = 64).  read does make that exchange, since four-byte stores would
+// (two instructions per value, 65 against 62 us when this was tried), four bytes
+// at a time many L1 lookups (d = 64: 39.2 against 37.7 us).  read does make that exchange, since four-byte stores would
 // reach L2 one by one.
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
@@ -30,7 +29,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAppendCtas = 4;  // resident per SM
+// CTAs per SM of the append: with 80 registers a thread 49.6 us (42k tokens of 8
+// heads), with the 64 of four CTAs 55.3 us, with two CTAs 53.7 us.
+constexpr int kAppendCtas = 3;
 
 // The last i in [0, B] with key(i) <= x, for ascending key with key(0) <= x;
 // whole warps only, with one x: 33 keys at a time, so that up to 32 rows take
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
         const bool pair = live && (lives >> (lane ^ 4) & 1);  // its neighbour in the V words is new too
         // where there is no new token, the nearest one's values are read and nothing is stored
         constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a token, tokens at a time
-        int64_t tok[8 / kRows];
+        int tok[8 / kRows];
 #pragma unroll
         for (int r0 = 0; r0 < 8; r0 += kRows)
             tok[r0 / kRows] = off + (min(max((int)pos0 + r0 + lane / kLanes, N), N + n - 1) - N);
@@ -432,18 +433,19 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
             }
             // this lane holds the halves g' = 2 t (low) and 2 t + 1 of its token; with the neighbouring token's it
             // makes the words g' = 2 t + e whole
+            const uint32_t pick = e ? 0x3276 : 0x5410;
             uint32_t o[GR];
 #pragma unroll
             for (int j = 0; j < GR; ++j) {
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 4);
-                o[j] = e ? __byte_perm(other, w[j], 0x7632) : __byte_perm(w[j], other, 0x5410);
+                o[j] = __byte_perm(w[j], other, pick);
             }
             const uint32_t so = __shfl_xor_sync(0xffffffffu, si, 4);
             uint8_t *vc = hb + Q::v_codes(tb) + (r >> 3) * Q::kVGroup, *vp = hb + Q::v_params(tb) + (r >> 3) * Q::kVParamGroup;
             if (pair) {
                 store_words<GR>(vc + ((2 * t + e) * 4 + t2) * GR * 4, o);
                 if (t < GR)
-                    reinterpret_cast<uint32_t *>(vp)[(t2 * GR + t) * 2 + e] = e ? __byte_perm(so, si, 0x7632) : __byte_perm(si, so, 0x5410);
+                    reinterpret_cast<uint32_t *>(vp)[(t2 * GR + t) * 2 + e] = __byte_perm(si, so, pick);
             } else if (live) {
                 store_v_token<D>(hb, tb, r, t, t2, e, w, si);
             }
@@ -602,7 +604,9 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
     if (!p.offsets)
         return d == 128 ? launch(quant_append_one_kernel<128>, p, p.B, 64, s) : launch(quant_append_one_kernel<64>, p, p.B, 64, s);
     p.groups = (int64_t)p.T / 8 + 2 * (int64_t)p.B;
-    // resident CTAs walk the units: fine ones, so that they end together
+    // resident CTAs walk the units, some two to four per warp (42k tokens of 8
+    // heads: 49.6 us; coarser ones, of which some warps get two and some one,
+    // 62 us; finer ones, whose first tile nothing hides, 52 us)
     const int64_t ctas = kAppendCtas * (int64_t)sms;
     p.parts = split_work(p.groups, 2 * p.Hkv, 2 * ctas * kWarps, p.its_per_part);
     int64_t grid = (p.groups * p.parts + kWarps - 1) / kWarps;
