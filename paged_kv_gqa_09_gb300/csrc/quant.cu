@@ -18,8 +18,8 @@
 // while it works on the one before, and reads its words from there: read from
 // global memory 16 bytes at a time they cost an exchange among the four lanes
 // (two instructions per value, 65 against 62 us when this was tried), four bytes
-// at a time many L1 lookups (d = 64: 39.2 against 37.7 us).  read does make that exchange, since four-byte stores would
-// reach L2 one by one.
+// at a time many L1 lookups (d = 64: 39.2 against 37.7 us).  read does make that
+// exchange, since four-byte stores would reach L2 one by one.
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
