@@ -722,6 +722,21 @@ def test_window_decode_long_rows_over_a_wide_table(lens):
         b.check(window, sinks)
 
 
+@pytest.mark.parametrize("lens,Hkv,G,d", [([20000], 1, 8, 128), ([9000, 5], 1, 4, 64), ([16500, 0, 3000], 1, 5, 128)])
+def test_rows_of_so_many_pieces_that_groups_are_merged_first(lens, Hkv, G, d):
+    for b, window, sinks in ((widen(Batch(lens, Hkv=Hkv, G=G, d=d, P=64, seed=71)), None, 0),
+                             (widen(Pages(lens, Hkv=Hkv, G=G, d=d, P=64, seed=72)), 10 ** 6, 3)):
+        if isinstance(b, Batch):
+            b.grow(lens)
+            b.q = queries(b)
+            b.check(b.q, window, sinks)
+            first, again = b.decode(b.q), b.decode(b.q)
+        else:
+            b.check(window, sinks)
+            first, again = b.decode(window, sinks), b.decode(window, sinks)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 # ------------------------------------------------------------------ calls at the edges
 
 def test_one_workspace_serves_batches_of_any_size():
