@@ -111,6 +111,9 @@ __device__ __forceinline__ uint32_t out_half2(float x, float y) { return pack_ha
 // [0, a) and [b, b + T - a).
 struct RowSpan {
     int N, ns, w0, a, b, T;
+    // on the line of tiles each (row, head) that sees any takes one more: its
+    // end costs about what a tile does (1.5 us)
+    __device__ __forceinline__ int line() const { return T > 0 ? T + 1 : 0; }
     __device__ __forceinline__ int tile(int k) const { return k < a ? k : b + (k - a); }
 };
 
@@ -348,9 +351,9 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
             return row_span<kTile>(p, len);
         };
         mine = window(0);
-        int W = mine.T;
+        int W = mine.line();
         for (int at = 32; at < p.B; at += 32)
-            W += window(at).T;
+            W += window(at).line();
         const Cuts cuts(__reduce_add_sync(0xffffffffu, W) * p.Hkv, grid, p.B);
 
         int run = cta, part = 0;  // this CTA's own run first
@@ -365,7 +368,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
                     mine = window(0);
                 }
                 for (;;) {
-                    int incl = mine.T;
+                    int incl = mine.line();
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -375,7 +378,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
                     const int tot = __shfl_sync(0xffffffffu, incl, 31);
                     if (start < row_start + tot * p.Hkv) {
                         cur = __ffs(__ballot_sync(0xffffffffu, start < row_start + incl * p.Hkv)) - 1;
-                        row_start += __shfl_sync(0xffffffffu, incl - mine.T, cur) * p.Hkv;
+                        row_start += __shfl_sync(0xffffffffu, incl - mine.line(), cur) * p.Hkv;
                         break;
                     }
                     row_start += tot * p.Hkv;
@@ -395,15 +398,17 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmK, const CUten
                     rs.T = __shfl_sync(0xffffffffu, mine.T, src);
                 };
                 take(cur);
-                int h = rs.T > 0 ? (int)((unsigned)(f - row_start) / (unsigned)rs.T) : 0;
+                int h = rs.T > 0 ? (int)((unsigned)(f - row_start) / (unsigned)(rs.T + 1)) : 0;
                 while (f < end && ok && rs.T > 0 && wb < p.B) {
-                    const int u0 = row_start + h * rs.T, u1 = u0 + rs.T;
-                    const int k1 = min(u1, end) - u0;
-                    const int c0 = u0 >= start ? seg : cuts.segment(u0), c1 = u1 <= end ? seg : cuts.segment(u1 - 1);
-                    stream(wb + cur, h, rs, f - u0, k1, c0 == c1 ? -1 : seg == c0 ? 2 * seg + 1 : 2 * seg, c0 | ((c1 - c0) << 16));
-                    f = u0 + k1;
+                    const int u0 = row_start + h * (rs.T + 1), u1 = u0 + rs.T;
+                    if (f < u1) {
+                        const int c0 = u0 >= start ? seg : cuts.segment(u0), c1 = u1 <= end ? seg : cuts.segment(u1 - 1);
+                        stream(wb + cur, h, rs, f - u0, min(u1, end) - u0, c0 == c1 ? -1 : seg == c0 ? 2 * seg + 1 : 2 * seg,
+                               c0 | ((c1 - c0) << 16));
+                    }
+                    f = u1 + 1;
                     if (++h == p.Hkv && f < end) {  // the next row with visible tokens
-                        row_start += rs.T * p.Hkv;
+                        row_start += (rs.T + 1) * p.Hkv;
                         h = 0;
                         unsigned m = __ballot_sync(0xffffffffu, mine.T > 0 && lane > cur);
                         while (!m && wb < p.B) {
