@@ -159,11 +159,11 @@ constexpr int kMinSplitRun = 48;
 // runs stay whole too.
 constexpr int kMaxSplitRows = 1024;
 
-// From this many tiles on runs differ by one tile at most instead of leaving the
-// last CTAs without any (16 tiles and a little: 34.3 against 35.8 us).  Shorter
-// ones make more pieces that way, which costs as much (8 tiles, 24.2 against
-// 24.0 us; 4 tiles, 19.9 against 19.3 us), and runs in parts even out anyway.
-constexpr int kMinEvenRun = 12;
+// Longer runs differ by one tile at most, instead of leaving the last CTAs without
+// any (16 tiles and a little, 34.3 against 35.8 us; 9 tiles, 22.4 against 23.7
+// us).  Shorter ones make more pieces that way, which costs more (4 to 5 tiles,
+// 18.7 against 18.2 us), and runs in parts even out anyway.
+constexpr int kMinEvenRun = 7;
 
 // The cuts of the line of W tiles into runs of q tiles each, one more in the
 // first `rem`, which lie on different SMs.  Run r's segments are
