@@ -1228,18 +1228,19 @@ struct Launch {
 
 // Tiles of a (row, head) per CTA of its cluster up to which clusters are used:
 // beyond, the line's equal runs gain more by their balance than the merge costs,
-// sooner over the 4-bit cache, where an idle warp costs more, and the sooner the
-// more CTAs share an SM.  d = 128, four query heads per KV head, clusters against
-// runs: 4-bit, rows of n / 4 .. n tokens, 4 tiles a CTA, 8.8 and 12.2 us (one
-// row), 9.5 and 11.9 us (32 rows); 8 tiles, 13.3 and 15.7 us (one row), 13.8 and
-// 15.9 us (three), 14.5 and 14.2 us (eight); 12 tiles, 17.5 and 16.5 us (one).
-// fp16, 4 tiles, 7.9 and 11.2 us (16 rows); 16 tiles, 11.9 and 15.2 us (four
-// rows); 32 tiles, 29.6 and 31.2 us (32 rows), where a batch less even than these
+// sooner over the 4-bit cache, where an idle warp costs more, and sooner still
+// when CTAs share an SM.  d = 128, four query heads per KV head, clusters against
+// runs: 4-bit, one row of 8 tiles a CTA (16k tokens), 13.3 and 14.4 us, of 4 (8k)
+// 9.0 and 12.0 us; rows of n / 4 .. n tokens, two CTAs an SM, 4 tiles a CTA, 10.1
+// and 10.5 us (four rows), 10.4 and 9.9 us (eight); 8 tiles, 15.0 and 13.4 us
+// (eight).  fp16, 8 tiles a CTA, 8.2 and 10.7 us (eight rows); 16 tiles, 12.2 and
+// 13.0 us (eight), 11.3 and 13.0 us (32 rows); 17 tiles in windows, 19.4 and 21.5
+// us; 32 tiles, 29.6 and 31.2 us (32 rows), where a batch less even than these
 // would lose.
 template <bool QUANT>
-constexpr int max_cluster_tiles(bool two_per_sm)
+constexpr int max_cluster_tiles(bool one_per_sm)
 {
-    return !QUANT ? 20 : two_per_sm ? 8 : 6;
+    return !QUANT ? 20 : one_per_sm ? 8 : 4;
 }
 
 template <int D, int TBL>
@@ -1260,7 +1261,7 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
     while (cl < 4 && (2ll << cl) <= most && units << (cl + 1) <= (int64_t)sms * LC::kCtasPerSm)
         ++cl;
     for (; cl >= 0 && most >= 2 && units << cl <= (int64_t)sms * LC::kCtasPerSm &&
-           most <= (int64_t)max_cluster_tiles<L::QUANT>(units << cl <= 2 * sms) << cl;
+           most <= (int64_t)max_cluster_tiles<L::QUANT>(units << cl <= sms) << cl;
          --cl) {
         cudaError_t e = prepare<D, TBL, true>(k);
         if (e != cudaSuccess)
