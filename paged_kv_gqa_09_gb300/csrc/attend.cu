@@ -199,7 +199,7 @@ struct Cuts {
 // head): each CTA streams its share of the tiles, and the states are merged
 // through distributed shared memory instead of global memory and an arrival
 // there, which takes 2 us less.
-constexpr int kMaxCluster = 16;
+constexpr int kMaxClusterLog2 = 4, kMaxCluster = 1 << kMaxClusterLog2;
 
 __device__ __forceinline__ void cluster_meet()
 {
@@ -1228,20 +1228,18 @@ struct Launch {
 
 // Tiles of a (row, head) per CTA of its cluster up to which clusters are used:
 // beyond, the line's equal runs gain more by their balance than the merge costs,
-// sooner over the 4-bit cache, where an idle warp costs more, and sooner still
-// when CTAs share an SM.  d = 128, four query heads per KV head, clusters against
-// runs: 4-bit, one row of 8 tiles a CTA (16k tokens), 13.3 and 14.4 us, of 4 (8k)
-// 9.0 and 12.0 us; rows of n / 4 .. n tokens, two CTAs an SM, 4 tiles a CTA, 10.1
-// and 10.5 us (four rows), 10.4 and 9.9 us (eight); 8 tiles, 15.0 and 13.4 us
-// (eight).  fp16, 8 tiles a CTA, 8.2 and 10.7 us (eight rows); 16 tiles, 12.2 and
-// 13.0 us (eight), 11.3 and 13.0 us (32 rows); 17 tiles in windows, 19.4 and 21.5
-// us; 32 tiles, 29.6 and 31.2 us (32 rows), where a batch less even than these
-// would lose.
-template <bool QUANT>
-constexpr int max_cluster_tiles(bool one_per_sm)
-{
-    return !QUANT ? 20 : one_per_sm ? 8 : 4;
-}
+// sooner over the 4-bit cache, where an idle warp costs more.  d = 128, four
+// query heads per KV head, clusters against runs.  fp16: 8 tiles, 8.2 and 10.7 us
+// (eight rows of 512 .. 2048 tokens); 16 tiles, 12.2 and 13.0 us (eight), 11.3 and
+// 13.0 us (32 rows); 17 tiles in windows, 19.4 and 21.5 us; 32 tiles, 29.6 and
+// 31.2 us (32 rows), where a batch less even than these would lose.  4-bit, each
+// CTA with an SM of its own: 4 tiles, 9.0 and 12.0 us (one row of 8k); 8 tiles,
+// 13.3 and 14.4 us (one row of 16k), which two CTAs an SM of 4 tiles each better
+// where there can be (two rows of 2k .. 8k, 7.9 and 8.5 us); 4 tiles, two an SM,
+// 10.1 and 10.5 us (four rows), 8 tiles 15.0 and 13.4 us (eight).
+constexpr int kMaxTilesFp16 = 20;
+constexpr int kMaxTilesOwn[2] = {6, 8};  // CTAs with an SM of their own: tried first, tried last
+constexpr int kMaxTilesShared = 4;
 
 template <int D, int TBL>
 cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParams p, int sms, cudaStream_t s)
@@ -1254,15 +1252,23 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
     const int64_t by_win = ((int64_t)p.window + kTile - 1) / kTile + 1 + ((int64_t)p.sinks + kTile - 1) / kTile;
     const int64_t most = by_len < by_win ? by_len : by_win, units = (int64_t)p.B * p.Hkv, tiles = units * most;
     KernelOnDevice *k;
-    // the largest cluster that leaves no CTA without a tile in the longest rows
-    // and of which the GPU holds one for every (row, head) at once (a second
-    // wave costs more than the merge saves)
-    int cl = 0;
-    while (cl < 4 && (2ll << cl) <= most && units << (cl + 1) <= (int64_t)sms * LC::kCtasPerSm)
-        ++cl;
-    for (; cl >= 0 && most >= 2 && units << cl <= (int64_t)sms * LC::kCtasPerSm &&
-           most <= (int64_t)max_cluster_tiles<L::QUANT>(units << cl <= sms) << cl;
-         --cl) {
+    // Up to 2^top CTAs a cluster, none without a tile in the longest rows and all
+    // resident at once (a second wave costs more than the merge saves).  fp16: as
+    // many as that.  4-bit: as many as leave each an SM of its own, more only
+    // where their share is too long (two rows of 2057 tokens, 128 CTAs 5.3, 256
+    // 6.6 us; four, d = 64, 128, 256 and 512 CTAs 6.0, 6.2 and 9.2 us).
+    const int64_t room = (int64_t)sms * LC::kCtasPerSm;
+    int top = 0, own = 0;
+    while (top < kMaxClusterLog2 && (2ll << top) <= most && units << (top + 1) <= room)
+        ++top;
+    while (own < top && units << (own + 1) <= sms)
+        ++own;
+    const int n = top + 1, tries = most < 2 || units > room ? 0 : L::QUANT ? 2 * n : n;
+    for (int t = 0; t < tries; ++t) {
+        const int cl = L::QUANT ? own + t % n : top - t;
+        const int limit = !L::QUANT ? kMaxTilesFp16 : units << cl <= sms ? kMaxTilesOwn[t / n] : kMaxTilesShared;
+        if (cl > top || most > (int64_t)limit << cl)
+            continue;
         cudaError_t e = prepare<D, TBL, true>(k);
         if (e != cudaSuccess)
             return e;
