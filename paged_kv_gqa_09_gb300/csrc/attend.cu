@@ -8,31 +8,32 @@
 // 1.25 d bytes (4-bit) or 4 d (fp16) per token and KV head.  HBM bounds long
 // batches (d = 128: 64 rows, 1.9M tokens of the 4-bit cache, 2.44 GB in 383 us;
 // 64 rows in a window of 8191 over fp16 pages, 1.85 GB in 274 us at most); the
-// 4-bit cache's unpacking and latency short ones (117k tokens, 150 MB, 34.5 us;
-// one row of 32k, 42 MB, 18.3 us).
+// 4-bit cache's unpacking and latency short ones (117k tokens, 150 MB, 33.6 us;
+// one row of 32k, 42 MB, 18.2 us).
 //
 // Work split.  A row's visible tokens lie in T_i tiles of 128 tokens (64 of fp16
-// pages with d = 128; those between the sinks and the window are
-// never touched).  All tiles of the batch in (row, KV head, tile) order form one
-// line, cut into equal runs, one per CTA: every CTA derives the line's length
-// and the cuts from the row lengths, so one launch balances rows of any lengths
-// without a plan.  SMs do not stream equally fast (equal runs ended between 0.85
-// and 1.1 of their mean time), so a long run's last three sixteenths are cut off
-// in two parts, which the CTAs claim as they come free.  The tiles that a
-// segment (a run, or a part of one) holds of one (row, head) are a piece; a
-// piece that is the whole (row, head) writes o and lse, any other its state (m,
-// l, acc in fp32), and the CTA that finishes a (row, head)'s last piece merges
-// its states in piece order: the cuts do not depend on who takes a segment or
-// comes last, so neither does the result.
+// pages with d = 128; those between the sinks and the window are never touched).
+// All tiles of the batch in (row, KV head, tile) order form one line, with one
+// place more at each (row, head)'s end, cut into equal runs, one per CTA: every
+// CTA derives the line's length and the cuts from the row lengths, so one launch
+// balances rows of any lengths without a plan.  SMs do not stream equally fast
+// (equal runs ended between 0.85 and 1.1 of their mean time), so a long run's
+// last three sixteenths are cut off in two parts, which the CTAs claim as they
+// come free.  The tiles that a segment (a run, or a part of one) holds of one
+// (row, head) are a piece; a piece that is the whole (row, head) writes o and
+// lse, any other its state (m, l, acc in fp32), and the CTA that finishes a (row, head)'s last piece merges
+// its states in piece order, those of a very long row by groups first: the cuts
+// do not depend on who takes a segment or comes last, so neither does the
+// result.  Calls of few tiles go to clusters instead, one per (row, head).
 //
 // CTA: warp 4 is the producer, warps 0..3 the consumers.  The producer walks
 // the run, reads block-table entries a batch of tiles ahead and streams each
 // tile into a ring of shared-memory stages: fp16 pages with tiled TMA copies
 // (128-byte swizzle), the 4-bit cache -- whose pages hold K and V of a head in
 // one contiguous run per 64 tokens or page -- with plain bulk copies; a piece's
-// first tile brings its q rows.  Consumer warp w takes tokens [16w, 16w + 16)
-// of every tile with its own online softmax: scores S^T = K q^T (16 tokens x 8
-// heads) and O^T += V^T P^T (d x 8 heads) on mma.sync m16n8k16, fp16 in, fp32
+// first tile brings its q rows.  Consumer warp w takes a quarter of every tile's
+// tokens, 16 or 32, with its own online softmax: scores S^T = K q^T (16 tokens x
+// 8 heads) and O^T += V^T P^T (d x 8 heads) on mma.sync m16n8k16, fp16 in, fp32
 // accumulate.  N = 8 heads is all a KV head has, so a tcgen05 tile would be
 // 1/16 full; the registers that mma.sync reads are what the 4-bit codes are
 // unpacked into.  Every wait is bounded (1 s).
