@@ -1151,7 +1151,7 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     if ((int64_t)s->bt_stride * s->page_size > 0x7fffff00LL)  // the end of a row's last tile is an int32
         return fail(PKV_EUNSUPPORTED, "rows of %lld tokens (bt_stride * page_size; supported: up to 2^31 - 256)",
                     (long long)s->bt_stride * s->page_size);
-    // the work is counted in tiles of 64 tokens, in an int32
+    // the work is counted in tiles of 64 tokens or more, in an int32
     const int64_t cap = len_cap(s), seen = win ? (int64_t)win->window + win->sinks + 128 : cap;
     if ((int64_t)s->B * s->Hkv > 0x7ff00000LL || (int64_t)s->B * s->Hkv * ((cap < seen ? cap : seen) / 64 + 2) > 0x7ff00000LL)
         return fail(PKV_EUNSUPPORTED, "B=%d rows of %d KV heads and up to %lld tokens exceed 2^31 tiles", s->B, s->Hkv,

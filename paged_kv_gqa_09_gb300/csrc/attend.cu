@@ -12,7 +12,8 @@
 // one row of 32k, 42 MB, 18.2 us).
 //
 // Work split.  A row's visible tokens lie in T_i tiles of 128 tokens (64 of fp16
-// pages with d = 128; those between the sinks and the window are never touched).
+// pages with d = 128, 256 of the 4-bit cache with d = 64; those between the sinks
+// and the window are never touched).
 // All tiles of the batch in (row, KV head, tile) order form one line, with one
 // place more at each (row, head)'s end, cut into equal runs, one per CTA: every
 // CTA derives the line's length and the cuts from the row lengths, so one launch
@@ -32,7 +33,7 @@
 // (128-byte swizzle), the 4-bit cache -- whose pages hold K and V of a head in
 // one contiguous run per 64 tokens or page -- with plain bulk copies; a piece's
 // first tile brings its q rows.  Consumer warp w takes a quarter of every tile's
-// tokens, 16 or 32, with its own online softmax: scores S^T = K q^T (16 tokens x
+// tokens, 16 or 32 at a time, with its own online softmax: scores S^T = K q^T (16 tokens x
 // 8 heads) and O^T += V^T P^T (d x 8 heads) on mma.sync m16n8k16, fp16 in, fp32
 // accumulate.  N = 8 heads is all a KV head has, so a tcgen05 tile would be
 // 1/16 full; the registers that mma.sync reads are what the 4-bit codes are
@@ -76,8 +77,12 @@ struct Layout {
     // flags and page lookups cost half as much per token, and one block's
     // unpacking overlaps the other's products; one where a tile is 32 KB already
     static constexpr int MT = QUANT || D == 64 ? 2 : 1;
-    static constexpr int kTile = 16 * kCW * MT;       // tokens per stage
-    static constexpr int kTileLog2 = MT == 2 ? 7 : 6;
+    // and how often it takes as many: tiles of 20 KB over the 4-bit cache with d = 64
+    // too (64 rows, 0.98 GB, 182 us in 2 stages; twice the stages of half that 203
+    // us), but in clusters, whose shares are few tiles
+    static constexpr int NT = QUANT && D == 64 && !CLUSTER ? 2 : 1;
+    static constexpr int kTile = 16 * kCW * MT * NT;  // tokens per stage
+    static constexpr int kTileLog2 = MT * NT == 4 ? 8 : MT * NT == 2 ? 7 : 6;
     static constexpr int kTileBytes = kTile * D * 2;  // fp16: one of K, V
     static constexpr int kKvBytes = QUANT ? kTile * D * 5 / 4 : 2 * kTileBytes;
     static constexpr int kQBytes = kMaxG * D * 2;
@@ -88,7 +93,7 @@ struct Layout {
     // stages 166 us, two of three 208 us; clusters the latter (12.8 and 14.9 us
     // for eight rows)
     static constexpr int kCtasPerSm = QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
-    static constexpr int kStages = QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 2 : 3;
+    static constexpr int kStages = QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
@@ -1043,18 +1048,21 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
                 }
             }
         }
-        constexpr int TW = 16 * L::MT;  // tokens of the tile for each warp
-        uint32_t vis = 0xffffffffu >> (32 - TW);
+        constexpr int TW = 16 * L::MT;  // tokens of the tile a warp takes at a time
         int4 mt2 = make_int4(0, 0, 0, 0);
         if (mt.z & (kMasked | kLast))
             mt2 = meta[2 * stage + 1];
-        if (mt.z & kMasked)
-            vis = __ballot_sync(0xffffffffu, lane < TW && visible(mt.y + TW * w + lane, mt2.x, mt2.y, mt2.z));
-        if (vis) {
+#pragma unroll 1
+        for (int part = w * L::NT; part < (w + 1) * L::NT; ++part) {
+            uint32_t vis = 0xffffffffu >> (32 - TW);
+            if (mt.z & kMasked)
+                vis = __ballot_sync(0xffffffffu, lane < TW && visible(mt.y + TW * part + lane, mt2.x, mt2.y, mt2.z));
+            if (!vis)
+                continue;
             if constexpr (L::QUANT)
-                quant_tile<D, TBL>(st, qf, sp, vis, w, p.scale_log2);
+                quant_tile<D, TBL>(st, qf, sp, vis, part, p.scale_log2);
             else
-                fp16_tile<D>(st, qf, sbase + stage * L::kStageBytes, sp, vis, w, p.tb_log2, p.scale_log2);
+                fp16_tile<D>(st, qf, sbase + stage * L::kStageBytes, sp, vis, part, p.tb_log2, p.scale_log2);
         }
         __syncwarp();
         if (mt.z & kLast) {
@@ -1247,11 +1255,13 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
 {
     using L = Layout<D, TBL, false>;
     using LC = Layout<D, TBL, true>;
-    constexpr int kTile = L::kTile;
     // the most tiles of a (row, head), by the table's width and by the window
-    const int64_t by_len = ((int64_t)p.len_cap + kTile - 1) / kTile;
-    const int64_t by_win = ((int64_t)p.window + kTile - 1) / kTile + 1 + ((int64_t)p.sinks + kTile - 1) / kTile;
-    const int64_t most = by_len < by_win ? by_len : by_win, units = (int64_t)p.B * p.Hkv, tiles = units * most;
+    auto most_tiles = [&p](int64_t tile) {
+        const int64_t by_len = (p.len_cap + tile - 1) / tile;
+        const int64_t by_win = (p.window + tile - 1) / tile + 1 + (p.sinks + tile - 1) / tile;
+        return by_len < by_win ? by_len : by_win;
+    };
+    const int64_t most = most_tiles(LC::kTile), units = (int64_t)p.B * p.Hkv, tiles = units * most_tiles(L::kTile);
     KernelOnDevice *k;
     // Up to 2^top CTAs a cluster, none without a tile in the longest rows and all
     // resident at once (a second wave costs more than the merge saves).  fp16: as

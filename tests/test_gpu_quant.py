@@ -722,6 +722,16 @@ def test_window_decode_long_rows_over_a_wide_table(lens):
         b.check(window, sinks)
 
 
+@pytest.mark.parametrize("P", [8, 32, 128])
+def test_windows_over_a_wide_table(P):
+    """Windows and sinks that end inside a tile and at its ends, over rows around a tile's length (256, d = 64)."""
+    lens = [255, 256, 257, 384, 511, 512, 513, 700, 0, 1]
+    b = widen(Batch(lens, Hkv=2, G=4, d=64, P=P, seed=73))
+    b.grow(lens)
+    for window, sinks in ((None, 0), (255, 1), (256, 0), (257, 129), (64, 64), (1, 300), (0, 256)):
+        b.check(queries(b), window, sinks)
+
+
 @pytest.mark.parametrize("lens,Hkv,G,d", [([20000], 1, 8, 128), ([9000, 5], 1, 4, 64), ([16500, 0, 3000], 1, 5, 128)])
 def test_rows_of_so_many_pieces_that_groups_are_merged_first(lens, Hkv, G, d):
     for b, window, sinks in ((widen(Batch(lens, Hkv=Hkv, G=G, d=d, P=64, seed=71)), None, 0),
