@@ -20,6 +20,7 @@
 // (two instructions per value, 65 against 62 us when this was tried), four bytes
 // at a time many L1 lookups (d = 64: 39.2 against 37.7 us).  read does make that
 // exchange, since four-byte stores would reach L2 one by one.
+#include "append_map.cuh"
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
@@ -327,11 +328,9 @@ __global__ void __launch_bounds__(64) quant_append_one_kernel(const QuantAppendP
         p.seq_lens_out[i] = page >= 0 ? N + 1 : N;
 }
 
-// A warp takes the eight cache positions 8 k .. of one row, for some of the
-// heads' sides (2 h: K, 2 h + 1: V), then the next such unit a grid further on.  Rows share one line of
-// such groups: row i's are at offsets[i] / 8 + 2 i .., which leaves room for a
-// first and a last group that are not full and needs no sum over the rows
-// before; what is left over is idle.
+// A warp takes a group (append_map.cuh: eight cache positions of one row) for
+// some of the heads' sides (2 h: K, 2 h + 1: V), then the next such unit a grid
+// further on.
 template <int D>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(const QuantAppendParams p)
 {
@@ -359,14 +358,11 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
     const unsigned line = warp / (unsigned)p.parts;
     const int it0 = (int)(warp - line * p.parts) * p.its_per_part, it1 = min(it0 + p.its_per_part, 2 * p.Hkv);
     for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
-        const int i = min(last_not_above(p.B, gs, [&](int r) { return (int64_t)(p.offsets[r] >> 3) + 2 * (int64_t)r; }), p.B - 1);
+        const int i = min(last_not_above(p.B, gs, [&](int r) { return append_first_group(p.offsets[r], r); }), p.B - 1);
         const int off = p.offsets[i], n = p.offsets[i + 1] - off;
-        const int k = (int)(gs - (off >> 3) - 2 * (int64_t)i);
         const int N = p.seq_lens[i];
-        if (k < 0 || !append_fits(p, i, N, off, n, false))
-            continue;
-        const int64_t pos0 = ((int64_t)(N >> 3) + k) * 8;
-        if (pos0 >= (int64_t)N + n)
+        int64_t pos0;
+        if (!append_group(gs, i, off, n, N, pos0) || !append_fits(p, i, N, off, n, false))
             continue;
         const int page = p.bt[(int64_t)i * p.bt_stride + (pos0 >> p.log2P)];
         if (page < 0 || page >= p.num_pages) {
@@ -386,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
         int tok[8 / kRows];
 #pragma unroll
         for (int r0 = 0; r0 < 8; r0 += kRows)
-            tok[r0 / kRows] = off + (min(max((int)pos0 + r0 + lane / kLanes, N), N + n - 1) - N);
+            tok[r0 / kRows] = append_token((int)pos0 + r0 + lane / kLanes, off, n, N);
         auto fetch = [&](int it) {
             const __half *from = (it & 1 ? p.v_new : p.k_new) + (it >> 1) * D + 8 * (lane % kLanes);
             const uint32_t to = smem_u32(tile + (it & 1) * 8 * kPitch + 16 * (lane % kLanes));
@@ -603,7 +599,7 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
 {
     if (!p.offsets)
         return d == 128 ? launch(quant_append_one_kernel<128>, p, p.B, 64, s) : launch(quant_append_one_kernel<64>, p, p.B, 64, s);
-    p.groups = (int64_t)p.T / 8 + 2 * (int64_t)p.B;
+    p.groups = append_groups(p.T, p.B);
     // resident CTAs walk the units, some two to four per warp (42k tokens of 8
     // heads: 49.6 us; coarser ones, of which some warps get two and some one,
     // 62 us; finer ones, whose first tile nothing hides, 52 us)

@@ -1,0 +1,51 @@
+"""Calls of the 4-bit cache and windowed decode at their edges: rows without
+new tokens."""
+import numpy as np
+import pytest
+import torch
+
+import quant_ref as R
+from paged_kv_gqa_09_gb300 import _lib, api
+from test_gpu_quant import Batch, bits, dev
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ rows without new tokens
+
+@pytest.mark.parametrize("d,P", [(128, 16), (64, 8)])
+@pytest.mark.parametrize("new", [[0, 0, 4], [0, 0, 0, 9, 0], [0, 17, 0], [0, 1]])
+def test_rows_without_new_tokens_among_the_others(d, P, new):
+    """Empty rows first, last and between, at lengths that end inside eight positions; their own last page's entry
+    is not looked at."""
+    lens = [(3, 5, 9, 7, 1)[i] for i in range(len(new))]
+    b = Batch([n + m + 8 for n, m in zip(lens, new)], d=d, P=P, seed=81, fill=0)
+    b.grow(lens)
+    for i, n in enumerate(new):
+        if n == 0:
+            b.bt[i] = -1
+    b.grow(new)
+    assert api.pkv_get_error(b.ws)[0] == 0
+    assert b.lens.cpu().tolist() == [a + n for a, n in zip(lens, new)]
+    b.bt.copy_(dev(b.table))
+    k, v = b.read()
+    assert np.array_equal(bits(k), bits(np.concatenate([R.values(x) for x in b.k])))
+    assert np.array_equal(bits(v), bits(np.concatenate([R.values(x) for x in b.v])))
+    b.ok()
+
+
+def test_an_append_of_nothing_hands_the_lengths_on():
+    b = Batch([20, 20, 20], seed=82, fill=0)
+    b.grow([5, 9, 0])
+    keep = b.cache.clone()
+    none = torch.empty((0, 2, 128), dtype=torch.float16, device="cuda")
+    out = torch.full_like(b.lens, -1)
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    api.pkv_quant_append(b.shape, b.ws, none, none, b.bt, b.lens, b.cache, new_offsets=off, seq_lens_out=out)
+    api.pkv_quant_append(b.shape, b.ws, none, none, b.bt, b.lens, b.cache, new_offsets=off)
+    assert out.cpu().tolist() == [5, 9, 0] and b.lens.cpu().tolist() == [5, 9, 0]
+    assert torch.equal(b.cache, keep)
+    b.ok()
+    b.lens[1] = -4
+    api.pkv_quant_append(b.shape, b.ws, none, none, b.bt, b.lens, b.cache, new_offsets=off)
+    assert api.pkv_get_error(b.ws)[0] == _lib.PKV_EDEVICE and int(b.lens[1]) == -4
