@@ -35,4 +35,31 @@ __host__ __device__ inline int append_token(int pos, int off, int n, int N)
     return off + ((first < last ? first : last) - N);
 }
 
+// `n` things to do per token group (heads, or sides of heads) are split over
+// `parts` warps, `most` at most, until the launch has at least `want`; each warp
+// then does `per`.
+inline int split_work(int64_t warps, int n, int64_t want, int64_t most, int &per)
+{
+    int parts = 1;
+    while (parts < n && warps * parts < want && 2 * (int64_t)parts <= most)
+        parts *= 2;
+    per = (n + parts - 1) / parts;
+    return (n + per - 1) / per;
+}
+
+// CTAs of an append, of `ctas` resident ones of `cta_warps` warps each, and how
+// the groups' sides are split over their warps: a warp keeps its part and walks
+// the line, so the parts of a group are no more than the warps there are (very
+// many KV heads would make them so).  Some two to four units per warp: 42k
+// tokens of 8 heads 49.6 us; coarser ones, of which some warps get two and some
+// one, 62 us; finer ones, whose first tile nothing hides, 52 us.
+inline int64_t append_grid(int T, int B, int Hkv, int ctas, int cta_warps, int64_t &groups, int &parts, int &per)
+{
+    const int64_t resident = (int64_t)ctas * cta_warps;
+    groups = append_groups(T, B);
+    parts = split_work(groups, 2 * Hkv, 2 * resident, resident, per);
+    const int64_t grid = (groups * parts + cta_warps - 1) / cta_warps;
+    return grid < ctas ? grid : ctas;
+}
+
 }  // namespace pkv

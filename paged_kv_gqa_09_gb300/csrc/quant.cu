@@ -567,17 +567,6 @@ __global__ void __launch_bounds__(kThreads, 4) quant_read_kernel(const QuantRead
     }
 }
 
-// `n` things to do per token group (heads, or sides of heads) are split over
-// `parts` warps until the launch has at least `want`; each warp then does `per`.
-int split_work(int64_t warps, int n, int64_t want, int &per)
-{
-    int parts = 1;
-    while (parts < n && warps * parts < want)
-        parts *= 2;
-    per = (n + parts - 1) / parts;
-    return (n + per - 1) / per;
-}
-
 template <class K, class P>
 cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s)
 {
@@ -599,14 +588,7 @@ cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_
 {
     if (!p.offsets)
         return d == 128 ? launch(quant_append_one_kernel<128>, p, p.B, 64, s) : launch(quant_append_one_kernel<64>, p, p.B, 64, s);
-    p.groups = append_groups(p.T, p.B);
-    // resident CTAs walk the units, some two to four per warp (42k tokens of 8
-    // heads: 49.6 us; coarser ones, of which some warps get two and some one,
-    // 62 us; finer ones, whose first tile nothing hides, 52 us)
-    const int64_t ctas = kAppendCtas * (int64_t)sms;
-    p.parts = split_work(p.groups, 2 * p.Hkv, 2 * ctas * kWarps, p.its_per_part);
-    int64_t grid = (p.groups * p.parts + kWarps - 1) / kWarps;
-    grid = grid < ctas ? grid : ctas;
+    const int64_t grid = append_grid(p.T, p.B, p.Hkv, kAppendCtas * sms, kWarps, p.groups, p.parts, p.its_per_part);
     return d == 128 ? launch(quant_append_kernel<128>, p, grid, kThreads, s) : launch(quant_append_kernel<64>, p, grid, kThreads, s);
 }
 
@@ -617,7 +599,7 @@ cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
     // single wave: of eight heads, two per warp 38 us (42k tokens) and 99 us
     // (117k), one 42 and 111 us, four 41 and 101 us, all eight 49 and 106 us
     const int64_t wave = 32 * (int64_t)sms;
-    p.parts = split_work(chunks, p.Hkv, 8 * wave, p.heads_per_part);
+    p.parts = split_work(chunks, p.Hkv, 8 * wave, INT64_MAX, p.heads_per_part);
     if (p.heads_per_part == 1 && p.Hkv > 1 && chunks * p.parts > 2 * wave) {
         p.heads_per_part = 2;
         p.parts = (p.Hkv + 1) / 2;

@@ -34,3 +34,21 @@ extern "C" void append_map_all(int B, int T, const int *off, const int *lens, in
         }
     }
 }
+
+// Counts in units[g * 2 * Hkv + side] how often the launch's warps take that
+// side of group g; returns the number of groups.
+extern "C" long long append_units_all(int T, int B, int Hkv, int ctas, int cta_warps, int *units)
+{
+    int64_t groups;
+    int parts, per;
+    const int64_t grid = pkv::append_grid(T, B, Hkv, ctas, cta_warps, groups, parts, per), warps = grid * cta_warps, lines = warps / parts;
+    for (int64_t w = 0; w < warps; ++w) {
+        const int64_t line = w / parts, first = (w - line * parts) * per;
+        if (line >= lines)
+            continue;
+        for (int64_t g = line; g < groups; g += lines)
+            for (int64_t it = first; it < first + per && it < 2 * Hkv; ++it)
+                ++units[g * 2 * Hkv + it];
+    }
+    return groups;
+}

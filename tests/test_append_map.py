@@ -29,6 +29,8 @@ def amap(tmp_path_factory):
                     os.path.join(ROOT, "tests", "append_map_host.cu")], check=True)
     L = ctypes.CDLL(str(out))
     L.append_map_all.argtypes = [ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 6
+    L.append_units_all.argtypes = [ctypes.c_int] * 5 + [ctypes.c_void_p]
+    L.append_units_all.restype = ctypes.c_longlong
     return L
 
 
@@ -69,3 +71,15 @@ def test_random_batches(amap):
 def test_rows_at_the_end_of_int32(amap):
     end = 2 ** 31 - 1
     check(amap, [end - 20, 3, end - 1], [20, 0, 1])
+
+
+@pytest.mark.parametrize("ctas", [456, 3])
+@pytest.mark.parametrize("T,B,Hkv", [(1, 1, 2048), (1, 1, 1824), (1, 1, 1825), (5, 2, 5000), (1, 1, 1), (1, 1, 8), (400, 9, 3), (9, 3, 8),
+                                     (40000, 8, 8), (3000, 1, 100), (0, 4, 8)])
+def test_every_side_of_every_group_has_a_warp(amap, T, B, Hkv, ctas):
+    """Very many KV heads and few tokens among the calls: as many parts as a group has sides would be more than
+    there are warps."""
+    units = np.zeros((max(1, T // 8 + 2 * B), 2 * Hkv), np.int32)
+    groups = amap.append_units_all(T, B, Hkv, ctas, 8, units.ctypes.data)
+    assert groups == (T // 8 + 2 * B if T else 0)
+    assert (units[:groups] == 1).all()

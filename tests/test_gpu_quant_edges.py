@@ -1,12 +1,12 @@
 """Calls of the 4-bit cache and windowed decode at their edges: rows without
-new tokens."""
+new tokens, very many KV heads."""
 import numpy as np
 import pytest
 import torch
 
 import quant_ref as R
 from paged_kv_gqa_09_gb300 import _lib, api
-from test_gpu_quant import Batch, bits, dev
+from test_gpu_quant import Batch, bits, dev, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,17 @@ def test_an_append_of_nothing_hands_the_lengths_on():
     b.lens[1] = -4
     api.pkv_quant_append(b.shape, b.ws, none, none, b.bt, b.lens, b.cache, new_offsets=off)
     assert api.pkv_get_error(b.ws)[0] == _lib.PKV_EDEVICE and int(b.lens[1]) == -4
+
+
+# ------------------------------------------------------------------ very many KV heads
+
+@pytest.mark.parametrize("Hkv", [1824, 2048])
+def test_few_tokens_of_very_many_heads(Hkv):
+    b = Batch([16], Hkv=Hkv, G=1, d=64, P=8, seed=83, fill=0)
+    b.grow([3])
+    b.grow([2])
+    assert b.lens.cpu().tolist() == [5]
+    k, v = b.read()
+    assert np.array_equal(bits(k), bits(R.values(b.k[0])))
+    assert np.array_equal(bits(v), bits(R.values(b.v[0])))
+    b.check(queries(b))
