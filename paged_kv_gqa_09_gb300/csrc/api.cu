@@ -1129,7 +1129,7 @@ int64_t quant_page_head_bytes(const pkv_shape_t *s) { return (int64_t)s->page_si
 
 int tb_log2(const pkv_shape_t *s) { return ilog2(quant_block_tokens(s->page_size)); }
 
-// Threads of a launch that takes 16 bytes of one side of one token's head each.
+// Tokens packed `stride` elements apart, of rows and in numbers whose indices the kernels hold in an int32.
 int check_packed(const pkv_shape_t *s, int32_t T, int64_t stride, const char *name)
 {
     if (T < 0)
@@ -1139,6 +1139,8 @@ int check_packed(const pkv_shape_t *s, int32_t T, int64_t stride, const char *na
                     (long long)stride, s->Hkv * s->d);
     if ((int64_t)T * s->Hkv * s->d > (int64_t)0x7fffffff * 64)
         return fail(PKV_EUNSUPPORTED, "%s: %d tokens of %d heads exceed one launch", name, T, s->Hkv);
+    if (s->B > 1 << 30)  // sums of two rows' indices
+        return fail(PKV_EUNSUPPORTED, "B=%d rows (supported: up to 2^30)", s->B);
     return PKV_OK;
 }
 

@@ -76,6 +76,15 @@ def test_too_many_tokens_are_rejected(L):
     assert calls(L, s, **big)["read"]() == _lib.PKV_EUNSUPPORTED
 
 
+def test_too_many_rows_are_rejected(L):
+    """The search for a token's row adds two rows' indices, and the lengths' loop one and a CTA's threads."""
+    for B in ((1 << 30) + 1, (1 << 31) - 1):
+        s = shape(B=B)
+        assert calls(L, s, T=7, off=FAKE)["append"]() == _lib.PKV_EUNSUPPORTED
+        assert calls(L, s, T=7)["read"]() == _lib.PKV_EUNSUPPORTED
+        assert "rows" in _lib.last_error()
+
+
 def test_rows_at_the_end_of_int32_are_rejected(L):
     s = shape(page_size=8, bt_stride=(1 << 28) - 1)
     assert calls(L, s)["quant"]() == _lib.PKV_EUNSUPPORTED
