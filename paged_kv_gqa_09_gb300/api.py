@@ -8,6 +8,7 @@ raw pointers and the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional, Sequence
@@ -46,6 +47,15 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _on(stream):
+    """Inside, `stream` is torch's current stream (None: the one that is)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _dev(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, nullable: bool = False) -> int:
@@ -578,17 +588,22 @@ class PagedDecoder:
     def workspace(self, device) -> Optional[torch.Tensor]:
         return self._ws.get(device)
 
-    def attn_workspace(self, shape: Shape, device) -> torch.Tensor:
+    def attn_workspace(self, shape: Shape, device, stream=None) -> torch.Tensor:
         """The workspace of step_window, step_quant and append_quant for this
         kind of shape on this device, zeroed when it is made -- which is not while
-        a graph is captured, whose replay alone would do it.  The decoder's calls
-        must not overlap on the GPU."""
+        a graph is captured, whose replay alone would do it.  It is zero when this
+        returns, for calls on any stream: making it waits for `stream` (None: the
+        current one), once.  The decoder's calls must not overlap on the GPU."""
         key = (device, shape.Hq // shape.Hkv, shape.d)
         ws = self._attn.get(key)
         if ws is None:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("call the step (or attn_workspace) once before capturing it: its workspace is made by then")
-            ws = self._attn[key] = torch.zeros(pkv_attn_workspace_size(shape), dtype=torch.uint8, device=device)
+            with _on(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("call the step (or attn_workspace) once before capturing it: its workspace is made by then")
+                ws = torch.zeros(pkv_attn_workspace_size(shape), dtype=torch.uint8, device=device)
+                if ws.is_cuda:
+                    torch.cuda.current_stream(ws.device).synchronize()
+            self._attn[key] = ws
         return ws
 
     def step_window(self, q, k_cache, v_cache, block_table, seq_lens, window: int, sinks: int = 0,
@@ -597,8 +612,8 @@ class PagedDecoder:
         """One decode step of a layer whose queries see their row's first `sinks`
         and last `window` tokens; returns (o, lse)."""
         shape = make_shape(q, k_cache, block_table, scale)
-        o, lse = self._outputs(q, o, lse, want_lse)
-        pkv_window_decode(shape, self.attn_workspace(shape, q.device), q, k_cache, v_cache, block_table, seq_lens,
+        o, lse = self._outputs(q, o, lse, want_lse, stream)
+        pkv_window_decode(shape, self.attn_workspace(shape, q.device, stream), q, k_cache, v_cache, block_table, seq_lens,
                           window, sinks, o, lse, stream)
         return o, lse
 
@@ -609,8 +624,8 @@ class PagedDecoder:
         shape = make_quant_shape(q.shape[1], q.shape[2], quant_cache, block_table, scale)
         if shape.B != q.shape[0]:
             raise ValueError("q and block_table disagree on B")
-        o, lse = self._outputs(q, o, lse, want_lse)
-        pkv_quant_decode(shape, self.attn_workspace(shape, q.device), q, quant_cache, block_table, seq_lens, o, lse,
+        o, lse = self._outputs(q, o, lse, want_lse, stream)
+        pkv_quant_decode(shape, self.attn_workspace(shape, q.device, stream), q, quant_cache, block_table, seq_lens, o, lse,
                          window, sinks, stream)
         return o, lse
 
@@ -618,15 +633,17 @@ class PagedDecoder:
                      stream=None) -> None:
         """Quantise new tokens k_new, v_new [T, Hkv, d] into a 4-bit cache (see pkv_quant_append)."""
         shape = make_quant_shape(quant_cache.shape[1], k_new.shape[2], quant_cache, block_table)
-        pkv_quant_append(shape, self.attn_workspace(shape, quant_cache.device), k_new, v_new, block_table, seq_lens,
+        pkv_quant_append(shape, self.attn_workspace(shape, quant_cache.device, stream), k_new, v_new, block_table, seq_lens,
                          quant_cache, new_offsets, seq_lens_out, stream)
 
     @staticmethod
-    def _outputs(q, o, lse, want_lse):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    def _outputs(q, o, lse, want_lse, stream):
+        if o is None or (lse is None and want_lse):
+            with _on(stream):  # memory of the stream that writes it
+                if o is None:
+                    o = torch.empty_like(q)
+                if lse is None and want_lse:
+                    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         return o, lse
 
 

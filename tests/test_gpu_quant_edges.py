@@ -1,12 +1,12 @@
 """Calls of the 4-bit cache and windowed decode at their edges: rows without
-new tokens, very many KV heads."""
+new tokens, very many KV heads, a decoder on another stream."""
 import numpy as np
 import pytest
 import torch
 
 import quant_ref as R
 from paged_kv_gqa_09_gb300 import _lib, api
-from test_gpu_quant import Batch, bits, dev, queries
+from test_gpu_quant import Batch, Pages, bits, compare, dev, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,33 @@ def test_few_tokens_of_very_many_heads(Hkv):
     assert np.array_equal(bits(k), bits(R.values(b.k[0])))
     assert np.array_equal(bits(v), bits(R.values(b.v[0])))
     b.check(queries(b))
+
+
+# ------------------------------------------------------------------ a decoder on another stream
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_decoders_first_call_on_another_stream(handle):
+    """The current stream is busy while a new decoder appends and decodes on another one, its workspace taken from
+    memory that held other values."""
+    b = Batch([60, 33], Hkv=2, G=4, d=64, P=8, seed=84)
+    k, v = [b.normal(50), b.normal(20)], [b.normal(50), b.normal(20)]
+    kn, vn, off, q = dev(np.concatenate(k)), dev(np.concatenate(v)), dev(np.array([0, 50, 70], np.int32)), queries(b)
+    f = Pages([700, 5], Hkv=2, G=4, d=64, P=8, seed=85)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    for where in (torch.cuda.current_stream(), side):  # whichever pool the workspace comes from
+        with torch.cuda.stream(where):
+            stale = [torch.full((api.pkv_attn_workspace_size(s),), 1, dtype=torch.uint8, device="cuda") for s in (b.shape, f.shape)]
+        torch.cuda.synchronize()
+        del stale
+    dec = api.PagedDecoder()
+    torch.cuda._sleep(100_000_000)
+    dec.append_quant(kn, vn, b.cache, b.bt, b.lens, off, stream=stream)
+    got = dec.step_quant(q, b.cache, b.bt, b.lens, stream=stream)
+    win = dec.step_window(f.q, f.kc, f.vc, f.bt, f.lens, 600, 3, stream=stream)
+    side.synchronize()
+    torch.cuda.synchronize()
+    compare(*got, q, [R.values(x) for x in k], [R.values(x) for x in v], b.shape.scale, None, 0)
+    compare(*win, f.q, f.k, f.v, f.shape.scale, 600, 3)
+    assert b.lens.cpu().tolist() == [50, 20]

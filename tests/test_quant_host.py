@@ -127,6 +127,69 @@ def test_binding_refuses_what_the_library_cannot_see(L):
         api.make_quant_shape(8, 128, torch.zeros(4, 2, 1001, dtype=torch.uint8), bt)
 
 
+def test_a_decoders_buffers_belong_to_the_stream_of_the_call(L, monkeypatch):
+    """A decoder's first call on a stream that is not the current one: its workspace is zero before the launch, and
+    the outputs it makes are memory of that stream; a stream that is being captured makes no workspace."""
+    log, now, capturing = [], ["current"], []
+
+    class On:
+        def __init__(self, stream):
+            self.name = stream
+
+        def __enter__(self):
+            now.append(self.name)
+
+        def __exit__(self, *_):
+            now.pop()
+
+    class Stream(str):
+        pass
+
+    class Zeros(torch.Tensor):
+        is_cuda = True
+
+    def made(what, make, wrap=lambda t: t):
+        def f(*a, **k):
+            log.append((what, now[-1]))
+            return wrap(make(*a, **k))
+        return f
+
+    class Current:
+        def synchronize(self):
+            log.append(("wait", now[-1]))
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: Current())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[-1] in capturing)
+    monkeypatch.setattr(torch, "zeros", made("workspace", torch.zeros, lambda t: t.as_subclass(Zeros)))
+    monkeypatch.setattr(torch, "empty_like", made("o", torch.empty_like))
+    monkeypatch.setattr(torch, "empty", made("lse", torch.empty))
+    for name in ("pkv_quant_decode", "pkv_window_decode", "pkv_quant_append"):
+        monkeypatch.setattr(api, name, lambda *_: log.append(("launch", now[-1])))
+    q, bt = torch.ones(2, 8, 128, dtype=torch.float16), torch.ones(2, 16, dtype=torch.int32)
+    cache = torch.ones(64, 2, 16 * 128 * 5 // 4, dtype=torch.uint8)
+    pages = torch.ones(64, 16, 2, 128, dtype=torch.float16)
+    new = torch.ones(2, 2, 128, dtype=torch.float16)
+    side = Stream("side")
+    for step in (lambda d, s: d.step_quant(q, cache, bt, None, stream=s), lambda d, s: d.step_window(q, pages, pages, bt, None, 9, stream=s),
+                 lambda d, s: d.append_quant(new, new, cache, bt, None, stream=s)):
+        for stream, where in ((side, "side"), (None, "current")):
+            log.clear()
+            dec = api.PagedDecoder()
+            step(dec, stream)
+            assert {at for what, at in log if what != "launch"} == {where}, log
+            names = [what for what, _ in log]
+            assert names.index("workspace") < names.index("wait") < names.index("launch"), log
+            log.clear()
+            step(dec, stream)
+            assert "workspace" not in [what for what, _ in log] and "wait" not in [what for what, _ in log]
+        capturing.append("side")
+        with pytest.raises(RuntimeError, match="before capturing"):
+            step(api.PagedDecoder(), side)
+        capturing.clear()
+
+
 # ------------------------------------------------------------------ the plain model
 
 @pytest.mark.parametrize("P,d", [(8, 64), (16, 128), (64, 64), (128, 128)])
