@@ -576,11 +576,9 @@ class PagedDecoder:
         lengths (host scalars the caller knows; n_sum only for `learned`)."""
         shape = make_shape(q, k_cache, block_table, scale)
         cfg = self.plan_cfg(shape.B, int(n_max), path, split_tokens, n_sum)
-        ws, part = self.buffers(shape, cfg, q.device)
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        with _on(stream):  # the workspace is zeroed in order with the step's kernels
+            ws, part = self.buffers(shape, cfg, q.device)
+        o, lse = self._outputs(q, o, lse, want_lse, stream)
         pkv_decode_step(shape, cfg, ws, q, k_cache, v_cache, block_table, seq_lens, part, o, lse,
                         stream)
         return o, lse

@@ -190,6 +190,50 @@ def test_a_decoders_buffers_belong_to_the_stream_of_the_call(L, monkeypatch):
         capturing.clear()
 
 
+def test_the_fp16_step_makes_its_buffers_on_its_stream(L, monkeypatch):
+    """PagedDecoder.step on a stream that is not the current one: its workspace is zeroed in that stream, when it is
+    made and when the configuration changes, and its other buffers are memory of it."""
+    log, now = [], ["current"]
+
+    class On:
+        def __init__(self, stream):
+            self.name = stream
+
+        def __enter__(self):
+            now.append(self.name)
+
+        def __exit__(self, *_):
+            now.pop()
+
+    class Stream(str):
+        pass
+
+    class Workspace(torch.Tensor):
+        def zero_(self):
+            log.append(("zero", now[-1]))
+            return self
+
+    def made(what, make, kind=torch.Tensor):
+        def f(*a, **k):
+            log.append((what, now[-1]))
+            return make(*a, **k).as_subclass(kind)
+        return f
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch, "zeros", made("workspace", torch.zeros, Workspace))
+    monkeypatch.setattr(torch, "empty_like", made("o", torch.empty_like))
+    monkeypatch.setattr(torch, "empty", made("partials or lse", torch.empty))
+    monkeypatch.setattr(api, "pkv_decode_step", lambda *_: log.append(("launch", now[-1])))
+    q, bt = torch.ones(2, 8, 128, dtype=torch.float16), torch.ones(2, 64, dtype=torch.int32)
+    pages = torch.ones(64, 16, 2, 128, dtype=torch.float16)
+    dec = api.PagedDecoder()
+    for chunk, first in ((256, "workspace"), (512, "zero")):
+        log.clear()
+        dec.step(q, pages, pages, bt, None, 1000, path=_lib.PKV_PATH_WORKQUEUE, split_tokens=chunk, stream=Stream("side"))
+        assert log[0][0] == first and {at for what, at in log if what != "launch"} == {"side"}, log
+
+
 # ------------------------------------------------------------------ the plain model
 
 @pytest.mark.parametrize("P,d", [(8, 64), (16, 128), (64, 64), (128, 128)])
