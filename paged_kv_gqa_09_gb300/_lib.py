@@ -10,7 +10,7 @@ import importlib.util
 import os
 import threading
 
-from .build import CALL, LIB
+from .build import CALL, LIB, call_fits, call_for
 
 PKV_OK = 0
 PKV_EINVAL = -1
@@ -197,6 +197,9 @@ def load_call():
         L = load()
         if not os.path.exists(CALL):
             raise PkvLibraryError(f"_pkv_call.so not found at {CALL}: build it with "
+                                  "`python -c 'import __graft_entry__ as g; g.build()'`")
+        if not call_fits():  # it would read this PyTorch's tensors by another one's layout
+            raise PkvLibraryError(f"_pkv_call.so was not built for {call_for()}: build it with "
                                   "`python -c 'import __graft_entry__ as g; g.build()'`")
         spec = importlib.util.spec_from_file_location("_pkv_call", CALL)
         m = importlib.util.module_from_spec(spec)

@@ -21,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
 CALL = os.path.join(OUT_DIR, "_pkv_call.so")
+CALL_FOR = CALL + ".for"  # the Python and PyTorch it was compiled for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -57,8 +58,23 @@ def _call_command(out: str) -> list[str]:
             "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def call_for() -> str:
+    """What _pkv_call.so is compiled for: it reads tensors by this PyTorch's headers, through this Python's ABI."""
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__} cxx11_abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
+def call_fits() -> bool:
+    """Whether the built _pkv_call.so is for the running Python and PyTorch."""
+    try:
+        with open(CALL_FOR) as f:
+            return f.read() == call_for()
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALL)):
+    if not (os.path.exists(LIB) and os.path.exists(CALL) and call_fits()):
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
     return all(os.path.getmtime(f) <= t for f in [*_deps(), os.path.join(CSRC, "binding.cpp")])
@@ -101,7 +117,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    if os.path.exists(CALL_FOR):  # it names nothing while the module changes
+        os.remove(CALL_FOR)
     os.replace(call_tmp, CALL)
+    with open(CALL_FOR + f".tmp{os.getpid()}", "w") as f:
+        f.write(call_for())
+    os.replace(f.name, CALL_FOR)
     return LIB
 
 

@@ -127,6 +127,21 @@ def test_binding_refuses_what_the_library_cannot_see(L):
         api.make_quant_shape(8, 128, torch.zeros(4, 2, 1001, dtype=torch.uint8), bt)
 
 
+def test_a_binding_built_for_another_pytorch_is_not_used(L, monkeypatch, tmp_path):
+    """The compiled argument checks read tensors by the headers of the PyTorch that they were compiled against."""
+    monkeypatch.setattr(_lib, "_call", None)
+    assert build_mod.up_to_date()
+    _lib.load_call()
+    monkeypatch.setattr(_lib, "_call", None)
+    monkeypatch.setattr(torch, "__version__", "1.2.3")
+    assert not build_mod.up_to_date()
+    with pytest.raises(_lib.PkvLibraryError, match="1.2.3"):
+        _lib.load_call()
+    monkeypatch.undo()
+    monkeypatch.setattr(build_mod, "CALL_FOR", str(tmp_path / "none"))  # one that does not say
+    assert not build_mod.up_to_date()
+
+
 def test_a_decoders_buffers_belong_to_the_stream_of_the_call(L, monkeypatch):
     """A decoder's first call on a stream that is not the current one: its workspace is zero before the launch, and
     the outputs it makes are memory of that stream; a stream that is being captured makes no workspace."""
