@@ -455,7 +455,8 @@ int pkv_quant_read(const pkv_shape_t *shape, void *d_ws, const void *d_quant_cac
  * values that pkv_quant_read returns, with fp32 sums.  win NULL: every token
  * of the row; else only those a pkv_window_t leaves visible (the row's last
  * token is the query's own position).  A row that sees no token gets o = 0,
- * lse = -inf.  No token outside the visible ones' pages is read. */
+ * lse = -inf, as does a head whose scores are all -inf.  No token outside the
+ * visible ones' pages is read. */
 int pkv_quant_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d_ws, const void *d_q,
                      const void *d_quant_cache, const int32_t *d_block_table, const int32_t *d_seq_lens,
                      void *d_o, float *d_lse, void *stream);

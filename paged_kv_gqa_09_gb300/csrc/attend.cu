@@ -55,6 +55,7 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 20000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.402823466e38f;  // running maximum before the first score: the least finite value (-inf - it is -inf)
+constexpr float kNoTiles = -1.f;            // in place of a sum of weights: a cluster's CTA that has none to give
 constexpr float kHalfMax = 65504.f;
 
 // The running maximum of the softmax follows a tile's only when that exceeds it
@@ -110,6 +111,11 @@ struct Layout {
 // rounded than unrounded (see softmax_step()), so that a mean of values at the
 // type's end could pass it and become infinite: finite results stay finite.
 __device__ __forceinline__ float within_half(float x) { return fabsf(x) < INFINITY ? fminf(fmaxf(x, -kHalfMax), kHalfMax) : x; }
+// What an accumulator is multiplied by for o.  A head whose scores are all -inf
+// has weights of 0 alone: o = 0 (NaN where a value is infinite or NaN) and lse = -inf, as
+// for a row that sees nothing, whichever way the work was cut.
+__device__ __forceinline__ float over_sum(float l) { return l == 0.f ? 1.f : 1.f / l; }
+
 __device__ __forceinline__ __half out_half(float x) { return __float2half_rn(within_half(x)); }
 __device__ __forceinline__ uint32_t out_half2(float x, float y) { return pack_half2(within_half(x), within_half(y)); }
 
@@ -816,7 +822,7 @@ __device__ __forceinline__ void merge_pieces(const AttendParams &p, int unit, in
                 }
                 continue;
             }
-            const float inv = 1.f / L[q];
+            const float inv = over_sum(L[q]);
             const int64_t oh = (int64_t)unit * p.G + g;  // unit = row * Hkv + head
             if (sub == 0)
                 *reinterpret_cast<uint2 *>(p.o + oh * D + at * 4) =
@@ -932,7 +938,7 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
         return true;
     }
     if (CLUSTER || slot < 0) {
-        const float i0 = 1.f / L0, i1 = 1.f / L1;
+        const float i0 = over_sum(L0), i1 = over_sum(L1);
         __half *out = p.o + (int64_t)unit * G * D;
 #pragma unroll
         for (int y = 0; y < KQ; ++y) {
@@ -1111,7 +1117,7 @@ __device__ __forceinline__ void merge_cluster(const AttendParams &p, uint32_t st
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
             m[c] = kNoMax;
-            l[c] = 0.f;
+            l[c] = kNoTiles;
             a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (c < n) {
                 const uint32_t at = cluster_addr(state, c);
@@ -1125,21 +1131,19 @@ __device__ __forceinline__ void merge_cluster(const AttendParams &p, uint32_t st
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)
             M = fmaxf(M, m[c]);
-        bool live = false;
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
             const float f = ex2(m[c] - M);
-            Ls += l[c] * f;
-            if (l[c] != 0.f) {  // else a CTA without tiles, whose accumulator was never written
+            if (l[c] != kNoTiles) {  // else the accumulator was never written
+                Ls += l[c] * f;
                 A.x += a[c].x * f, A.y += a[c].y * f, A.z += a[c].z * f, A.w += a[c].w * f;
-                live = true;
             }
         }
         const int64_t oh = (int64_t)unit * p.G + g;
-        const float inv = live ? 1.f / Ls : 0.f;
+        const float inv = over_sum(Ls);
         *reinterpret_cast<uint2 *>(p.o + oh * D + d) = make_uint2(out_half2(A.x * inv, A.y * inv), out_half2(A.z * inv, A.w * inv));
         if (p.lse && d == 0)
-            p.lse[oh] = live ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+            p.lse[oh] = (M + log2f(Ls)) * kLn2;
     }
     cluster_meet();  // no CTA's shared memory goes away while another reads it
 }
@@ -1164,8 +1168,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, TBL, CLUSTER>::kCtasPerSm)
         mbar_init(cbar, kCW);
         fence_mbar_init();
     }
-    if (CLUSTER && threadIdx.x < 2 * kMaxG)  // no tiles yet: no maximum, no sum
-        reinterpret_cast<float *>(basep + L::kStateOff)[kMaxG * D + threadIdx.x] = threadIdx.x < kMaxG ? kNoMax : 0.f;
+    if (CLUSTER && threadIdx.x < 2 * kMaxG)  // no tiles yet
+        reinterpret_cast<float *>(basep + L::kStateOff)[kMaxG * D + threadIdx.x] = threadIdx.x < kMaxG ? kNoMax : kNoTiles;
     if (!L::QUANT && threadIdx.x == 32 * kCW) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);

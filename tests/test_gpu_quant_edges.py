@@ -1,12 +1,13 @@
 """Calls of the 4-bit cache and windowed decode at their edges: rows without
-new tokens, very many KV heads, a decoder on another stream."""
+new tokens, very many KV heads, a decoder on another stream,
+scores of -inf."""
 import numpy as np
 import pytest
 import torch
 
 import quant_ref as R
 from paged_kv_gqa_09_gb300 import _lib, api
-from test_gpu_quant import Batch, Pages, bits, compare, dev, queries
+from test_gpu_quant import Batch, Pages, bits, clean, compare, dev, queries, widen
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,60 @@ def test_a_decoders_first_call_on_another_stream(handle):
     compare(*got, q, [R.values(x) for x in k], [R.values(x) for x in v], b.shape.scale, None, 0)
     compare(*win, f.q, f.k, f.v, f.shape.scale, 600, 3)
     assert b.lens.cpu().tolist() == [50, 20]
+
+
+# ------------------------------------------------------------------ scores of -inf
+
+@pytest.mark.parametrize("d,lens", [(64, [700, 40, 0, 3000]), (128, [900, 1]), (128, [30] * 90)])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("every", [None, 1, 301])
+def test_keys_of_minus_infinity(d, lens, wide, every):
+    """Every `every`-th token's score is finite (None: no token's), the others' are -inf, in clusters and in runs: o
+    and lse are those of the finite ones alone, 0 and -inf where there is none."""
+    b = Pages(lens, Hkv=2, G=4, d=d, P=16, seed=86)
+    if wide:
+        b = widen(b)
+    b.q[..., 3] = 1.0
+    keep = [np.zeros(n, bool) for n in lens]
+    for i, n in enumerate(lens):
+        if every:
+            keep[i][n // 3::every] = True
+        gone = torch.from_numpy(np.flatnonzero(~keep[i])).cuda()
+        b.kc[b.bt[i, gone // 16].long(), gone % 16, :, 3] = -float("inf")
+    o, lse = b.decode(10 ** 6, 0)
+    compare(o, lse, b.q, [k[m] for k, m in zip(b.k, keep)], [v[m] for v, m in zip(b.v, keep)], b.shape.scale, None, 0)
+    assert api.pkv_get_error(b.ws)[0] == 0
+    clean(b.ws)
+    # a weight of 0 and an infinite value make NaN, as in the definition
+    i, t = len(lens) - 1, lens[-1] - 1
+    if keep[i][t]:
+        return
+    b.vc[int(b.bt[i, t // 16]), t % 16, 1, 5] = float("inf")
+    o, lse2 = b.decode(10 ** 6, 0)
+    nan = torch.zeros_like(o, dtype=torch.bool)
+    nan[i, 4:, 5] = True
+    assert torch.equal(torch.isnan(o), nan) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("finite", [0, 3])
+def test_scores_beyond_the_type_over_the_4_bit_cache(d, wide, finite):
+    """Scores of -1e40, which are -inf in fp32; of the last row's tokens the first, one in the middle and the last
+    have scores of 0."""
+    lens = [500, 1, 1200]
+    b = Batch(lens, Hkv=2, G=3, d=d, P=32, seed=87, scale=1e38)
+    ks = [np.zeros((n, 2, d), np.float16) for n in lens]
+    for k in ks:
+        k[:, :, 0] = -100
+    if finite:
+        ks[2][[0, 611, 1199]] = 0
+    b.append(ks, [b.normal(n) for n in lens])
+    if wide:
+        b = widen(b)
+    q = torch.zeros((3, 6, d), dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    o, lse = b.decode(q)
+    mean = [R.values(v[[0, 611, 1199]]) if i == 2 and finite else R.values(v[:0]) for i, v in enumerate(b.v)]
+    compare(o, lse, q, [np.zeros_like(v) for v in mean], mean, b.shape.scale, None, 0)
+    b.ok()
