@@ -63,6 +63,13 @@ constexpr float kHalfMax = 65504.f;
 // fp16, and most tiles need neither a reduction over tokens nor a rescaling.
 constexpr float kMaxSlack = 8.f;
 
+// x sl2 - m is one fused multiply-add, and m a rounded x sl2: the greatest
+// score's own difference from it is up to half a step of m, the same for all of
+// a head's tokens, and scales their weights and sum alike.  Past 2^28 that is 16
+// and more, beyond fp16; from kFar on, where it is 2^-4, the products are rounded
+// before the subtraction.
+constexpr float kFar = 1048576.f;
+
 constexpr int kTableLines = 32;  // lines of the block table each CTA brings into L2 at its start
 
 constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
@@ -512,12 +519,7 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
     constexpr uint32_t kAll = MT == 2 ? 0xffffffffu : 0xffffu;
     const int r0 = (threadIdx.x & 31) >> 2;
     float y[MT][4];
-    auto scaled = [&](float m0, float m1) {
-#pragma unroll
-        for (int u = 0; u < MT; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[u][e] = fmaf(x[u][e], sl2, (e & 1) ? -m1 : -m0);
+    auto hide = [&] {
         if (vis != kAll) {
 #pragma unroll
             for (int u = 0; u < MT; ++u)
@@ -527,6 +529,14 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
                         y[u][e] = -INFINITY;
         }
     };
+    auto scaled = [&](float m0, float m1) {
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[u][e] = fmaf(x[u][e], sl2, (e & 1) ? -m1 : -m0);
+        hide();
+    };
     auto most = [&](int odd) {
         float a = -INFINITY;
 #pragma unroll
@@ -535,7 +545,7 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
         return a;
     };
     scaled(st.m0, st.m1);
-    if (__any_sync(0xffffffffu, fmaxf(most(0), most(1)) > kMaxSlack)) {
+    if (__any_sync(0xffffffffu, fmaxf(most(0), most(1)) > kMaxSlack || fmaxf(fabsf(st.m0), fabsf(st.m1)) >= kFar)) {
         scaled(0.f, 0.f);
         float n0 = fmaxf(st.m0, most(0)), n1 = fmaxf(st.m1, most(1));
 #pragma unroll
@@ -555,7 +565,14 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
             st.O[z][2] *= f0;
             st.O[z][3] *= f1;
         }
-        scaled(n0, n1);
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float n = (e & 1) ? n1 : n0;
+                y[u][e] = fabsf(n) < kFar ? fmaf(x[u][e], sl2, -n) : __fmul_rn(x[u][e], sl2) - n;
+            }
+        hide();
     }
 #pragma unroll
     for (int u = 0; u < MT; ++u) {

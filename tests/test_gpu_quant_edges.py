@@ -1,6 +1,6 @@
 """Calls of the 4-bit cache and windowed decode at their edges: rows without
 new tokens, very many KV heads, a decoder on another stream,
-scores of -inf."""
+scores of -inf and very large ones."""
 import numpy as np
 import pytest
 import torch
@@ -151,3 +151,53 @@ def test_scores_beyond_the_type_over_the_4_bit_cache(d, wide, finite):
     mean = [R.values(v[[0, 611, 1199]]) if i == 2 and finite else R.values(v[:0]) for i, v in enumerate(b.v)]
     compare(o, lse, q, [np.zeros_like(v) for v in mean], mean, b.shape.scale, None, 0)
     b.ok()
+
+
+# ------------------------------------------------------------------ very large scores
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("top,rest", [(16000, (8000, 15992)), (-8000, (-16000, -8008))])
+@pytest.mark.parametrize("quant", [False, True])
+def test_equal_greatest_scores_far_from_zero(d, wide, top, rest, quant):
+    """Scores of 10^5 .. 10^10, of which three tokens' are the greatest, in tiles, warps and pieces of their own: o is
+    the mean of their values, however the scale's product is rounded."""
+    lens, Hkv, G, dims = [1500, 3, 700], 2, 4, 8
+    rng = np.random.default_rng(88)
+    ks = []
+    for n in lens:
+        c = rng.integers(rest[0] // 8, rest[1] // 8 + 1, (n, Hkv)) * 8.0
+        c[[0, n // 2, n - 1]] = top
+        k = np.zeros((n, Hkv, d), np.float16)
+        k[:, :, :32] = c[:, :, None]  # a group of one value is kept as it is
+        ks.append(k)
+    if quant:
+        b = Batch(lens, Hkv=Hkv, G=G, d=d, P=16, seed=89)
+        b.append(ks, [b.normal(n) for n in lens])
+        vs = [R.values(v) for v in b.v]
+    else:
+        b = Pages(lens, Hkv=Hkv, G=G, d=d, P=16, seed=89)
+        for i, n in enumerate(lens):
+            t = torch.arange(n, device="cuda")
+            b.kc[b.bt[i, t // 16].long(), t % 16] = dev(ks[i])
+        vs = b.v
+    if wide:
+        b = widen(b)
+    q = torch.zeros((3, Hkv * G, d), dtype=torch.float16, device="cuda")
+    q[..., :dims] = dev(np.array([60000, 31008, 7000, 1000, 301, 100, 20000, 50016], np.float16))[None, :, None]
+    if quant:
+        o, lse = b.decode(q)
+    else:
+        b.q = q
+        o, lse = b.decode(10 ** 6, 0)
+    o, lse = (x.cpu().numpy().astype(np.float64) for x in (o, lse))
+    score = q[0, :, 0].double().cpu().numpy() * dims * top * float(np.float32(b.shape.scale))
+    for i, n in enumerate(lens):
+        for h in range(Hkv * G):
+            v = vs[i][[0, n // 2, n - 1], h // G].astype(np.float64)
+            # o's rounding to fp16, and that of the weights, which are equal
+            assert (np.abs(o[i, h] - v.mean(0)) <= 2.0 ** -11 * (np.abs(v.mean(0)) + np.abs(v).mean(0)) + 2.0 ** -22).all()
+            # a score's product with the scale, that with log2 e, and the way back from log2 units: fp32
+            assert abs(lse[i, h] - score[h] - np.log(3)) <= 4 * 2.0 ** -24 * abs(score[h]) + 2.0 ** -20
+    assert api.pkv_get_error(b.ws)[0] == 0
+    clean(b.ws)
