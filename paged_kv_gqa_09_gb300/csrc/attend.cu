@@ -54,18 +54,23 @@ constexpr int kMaxG = 8;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 20000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -3.402823466e38f;  // running maximum before the first score: the least finite value (-inf - it is -inf)
+constexpr float kNoMax = -3.402823466e38f;  // m before the first score: the least finite value (-inf - it is -inf)
 constexpr float kNoTiles = -1.f;            // in place of a sum of weights: a cluster's CTA that has none to give
 constexpr float kHalfMax = 65504.f;
 
-// The running maximum of the softmax follows a tile's only when that exceeds it
-// by more than this (in log2 units): weights then stay below 2^8, well inside
-// fp16, and most tiles need neither a reduction over tokens nor a rescaling.
-constexpr float kMaxSlack = 8.f;
+// The m that scores are taken from is set this far below a warp's greatest score
+// (in log2 units), and set again only when one exceeds it by more than kMaxOver:
+// the greatest weights lie in 2^7 .. 2^15, at the upper end of fp16, and most
+// tiles need neither a reduction over tokens nor a rescaling.  fp16 ends at
+// 2^-24, 2^-31 of the greatest weight: what smaller ones lose in o, while they
+// count in the sum, is 2^-32 each at most.  (With the greatest weight at 1 it was
+// 2^-25: rows of 2^20 tokens, whose first one leads the others by 25.4 and whose
+// warps take a fifth of a row each, lost a fifth of what those add to o.)
+constexpr float kMaxUnder = 7.f, kMaxOver = 15.f;
 
-// x sl2 - m is one fused multiply-add, and m a rounded x sl2: the greatest
-// score's own difference from it is up to half a step of m, the same for all of
-// a head's tokens, and scales their weights and sum alike.  Past 2^28 that is 16
+// x sl2 - m is one fused multiply-add, and m comes of a rounded x sl2: the greatest
+// score is up to half a step of m off, the same for all of a head's tokens, which
+// scales their weights and sum alike.  Past 2^28 that is 16
 // and more, beyond fp16; from kFar on, where it is 2^-4, the products are rounded
 // before the subtraction.
 constexpr float kFar = 1048576.f;
@@ -512,7 +517,8 @@ struct State {
 // `vis` set where visible -- enter the running softmax in units of log2;
 // returns the weights as the B operands of the PV product.  The weights are
 // rounded to fp16, the tensor cores' operand type, which costs o about as much
-// as its own rounding; their sum is kept in fp32 before that rounding.
+// as its own rounding (2^-11 of the mean |v| at most); their sum is kept in fp32
+// before that rounding, so that lse is not rounded with them.
 template <int D, int MT>
 __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][4], uint32_t vis, float sl2, uint32_t (&P)[MT][2])
 {
@@ -545,9 +551,9 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
         return a;
     };
     scaled(st.m0, st.m1);
-    if (__any_sync(0xffffffffu, fmaxf(most(0), most(1)) > kMaxSlack || fmaxf(fabsf(st.m0), fabsf(st.m1)) >= kFar)) {
+    if (__any_sync(0xffffffffu, fmaxf(most(0), most(1)) > kMaxOver || fmaxf(fabsf(st.m0), fabsf(st.m1)) >= kFar)) {
         scaled(0.f, 0.f);
-        float n0 = fmaxf(st.m0, most(0)), n1 = fmaxf(st.m1, most(1));
+        float n0 = fmaxf(st.m0, most(0) - kMaxUnder), n1 = fmaxf(st.m1, most(1) - kMaxUnder);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));

@@ -1,6 +1,6 @@
 """Calls of the 4-bit cache and windowed decode at their edges: rows without
 new tokens, very many KV heads, a decoder on another stream,
-scores of -inf and very large ones."""
+scores of -inf and very large ones, weights far below the greatest."""
 import numpy as np
 import pytest
 import torch
@@ -199,5 +199,54 @@ def test_equal_greatest_scores_far_from_zero(d, wide, top, rest, quant):
             assert (np.abs(o[i, h] - v.mean(0)) <= 2.0 ** -11 * (np.abs(v.mean(0)) + np.abs(v).mean(0)) + 2.0 ** -22).all()
             # a score's product with the scale, that with log2 e, and the way back from log2 units: fp32
             assert abs(lse[i, h] - score[h] - np.log(3)) <= 4 * 2.0 ** -24 * abs(score[h]) + 2.0 ** -20
+    assert api.pkv_get_error(b.ws)[0] == 0
+    clean(b.ws)
+
+
+# ------------------------------------------------------------------ weights far below the greatest
+
+@pytest.mark.parametrize("lead", [20.0, 24.6, 25.4, 28.0])
+@pytest.mark.parametrize("B", [1, 80])  # many pieces of a row, and rows of a piece or two
+@pytest.mark.parametrize("quant", [False, True])
+def test_a_long_rows_tokens_far_behind_its_first(lead, B, quant):
+    """10^6 tokens with a weight of 2^-lead of the first one's, whose value is 0 where theirs is 1."""
+    P, d, Hkv, pages, times = 16, 64, 8, 64, 1040
+    k, v = np.zeros((P * pages, Hkv, d), np.float16), np.ones((P * pages, Hkv, d), np.float16)
+    k[0, :, 0] = 1
+    v[0] = 0
+    if quant:
+        b = Batch([P * pages], Hkv=Hkv, G=2, d=d, P=P, seed=90)
+        b.append([k], [v])
+        first = float(R.values(k[0])[0, 0])
+    else:
+        b = Pages([P * pages], Hkv=Hkv, G=2, d=d, P=P, seed=90)
+        t = torch.arange(P * pages, device="cuda")
+        b.kc[b.bt[0, t // P].long(), t % P] = dev(k)
+        b.vc[b.bt[0, t // P].long(), t % P] = dev(v)
+        first = 1.0
+    b.shape.scale = lead * float(np.log(2)) / first
+    # the row's first page, then the others again and again; B such rows
+    b.bt = torch.cat([b.bt[:, :1], b.bt[:, 1:].repeat(1, times)], 1).repeat(B, 1).contiguous()
+    b.shape.bt_stride, b.shape.B, b.B = b.bt.shape[1], B, B
+    n = P * (1 + (pages - 1) * times)
+    b.lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = torch.zeros((B, 2 * Hkv, d), dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    if quant:
+        o, lse = b.decode(q)
+    else:
+        b.q = q
+        o, lse = b.decode(1 << 30, 0)
+    o, lse = (x.cpu().numpy().astype(np.float64) for x in (o, lse))
+    score = first * float(np.float32(b.shape.scale))
+    rest = (n - 1) * np.exp(-score)
+    # roundings of o and of the weights; 2^-32 of each small weight; a warp's sums of up to n / 4 tokens, 16 a step,
+    # in fp32: 2^-24 of half their end for each step
+    tol = 2.0 ** -11 * 2 + n * 2.0 ** -32 / rest + n / 64 * 2.0 ** -25
+    # and the sum, in which a lane holds the first token's weight: what it adds to that, two tokens of sixteen of a
+    # quarter of the row, may be lost
+    assert np.abs(o * (rest + 1) / rest - 1).max() <= tol + rest / 32, (o.min(), o.max(), rest / (rest + 1))
+    # six roundings of 2^-24 between the score, up to 20, and lse, and those sums
+    assert np.abs(lse - score - np.log1p(rest)).max() <= 2.0 ** -16 + rest / 32 + n / 64 * 2.0 ** -25
     assert api.pkv_get_error(b.ws)[0] == 0
     clean(b.ws)
