@@ -399,8 +399,8 @@ int pkv_decode_step_noalloc(const pkv_shape_t *shape, const pkv_plan_cfg_t *cfg,
  * it again after one that reported PKV_ETIMEOUT), and pkv_get_error() reads its
  * error word.  Calls on one workspace must not
  * overlap on the GPU (two graphs that may run at once need one each).  They use
- * the shape's B (append and read: up to 2^30), Hkv, d, page_size, num_pages and
- * bt_stride; the decodes Hq and scale too. */
+ * the shape's B (append and read: up to 2^30; the decodes: up to 2^25), Hkv, d,
+ * page_size, num_pages and bt_stride; the decodes Hq and scale too. */
 
 /* Tokens a query sees: the first `sinks` of its row and the last `window`
  * (both >= 0; they may overlap).  With both 0 it sees none. */

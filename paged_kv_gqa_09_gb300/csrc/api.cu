@@ -1153,6 +1153,10 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     if ((int64_t)s->bt_stride * s->page_size > 0x7fffff00LL)  // the end of a row's last tile is an int32
         return fail(PKV_EUNSUPPORTED, "rows of %lld tokens (bt_stride * page_size; supported: up to 2^31 - 256)",
                     (long long)s->bt_stride * s->page_size);
+    // every CTA adds up the lengths of all rows before its first tile (a call of 2^20 rows of five
+    // tokens takes 24 ms), while its consumers wait for that, 1 s at most
+    if (s->B > 1 << 25)
+        return fail(PKV_EUNSUPPORTED, "B=%d rows (supported: up to 2^25)", s->B);
     // the work is counted in tiles of 64 tokens or more, in an int32
     const int64_t cap = len_cap(s), seen = win ? (int64_t)win->window + win->sinks + 128 : cap;
     if ((int64_t)s->B * s->Hkv > 0x7ff00000LL || (int64_t)s->B * s->Hkv * ((cap < seen ? cap : seen) / 64 + 2) > 0x7ff00000LL)

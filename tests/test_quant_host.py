@@ -85,6 +85,14 @@ def test_too_many_rows_are_rejected(L):
         assert "rows" in _lib.last_error()
 
 
+def test_rows_that_a_bounded_wait_does_not_cover_are_rejected(L):
+    """A decode's CTAs look through all rows' lengths first, while a wait of one second runs."""
+    s = shape(B=(1 << 25) + 1, Hq=1, Hkv=1, bt_stride=1, page_size=8)
+    for name in ("quant", "window"):
+        assert calls(L, s)[name]() == _lib.PKV_EUNSUPPORTED
+        assert "rows" in _lib.last_error()
+
+
 def test_rows_at_the_end_of_int32_are_rejected(L):
     s = shape(page_size=8, bt_stride=(1 << 28) - 1)
     assert calls(L, s)["quant"]() == _lib.PKV_EUNSUPPORTED
