@@ -183,11 +183,12 @@ __device__ __noinline__ uint4 quant_codes_exact(uint4 x, float s, float b)
 // below it in the low 16.  i is within 2^-23 of itself, which scales the at most
 // 16 steps from lo as a whole (2^-19); 16 s + b, c and n are rounded once each.
 // With a = |16 + b / s| that makes 2^-24 a, 2^-17 + 2^-21.9 a and 2^-17, less
-// than E = 3 + a / 16 units of 2^-16 together (a is at most 15 2^10 or so, since
-// lo and hi differ by a step of fp16 at least; the warp takes its groups'
-// greatest E).  A value whose low bits are E from a border or further has its code; elsewhere -- one in some 2000, nearly
-// all of them ties, since x, s and b lie on coarse grids -- and where lo or hi
-// come out beyond the codes, are beyond the limit or NaN, the border itself
+// than E = 3 + a / 16 units of 2^-16 together (a is at most 15 2^11, where lo is
+// just below a power of two and hi a step of fp16 above: E is 1924 or less; the
+// warp takes its groups' greatest).  A value whose low bits are E from a border
+// or further has its code; elsewhere -- of normal values one in some 2600, 98 in
+// a hundred of them ties, since x, s and b lie on coarse grids -- and where lo or
+// hi come out beyond the codes, are beyond the limit or NaN, the border itself
 // decides.
 template <int GR>
 __device__ __forceinline__ uint32_t quantise_rows(const uint32_t (&x)[GR][4], int t, uint32_t (&w)[GR])

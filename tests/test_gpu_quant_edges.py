@@ -1,6 +1,7 @@
 """Calls of the 4-bit cache and windowed decode at their edges: rows without
 new tokens, very many KV heads, a decoder on another stream,
-scores of -inf and very large ones, weights far below the greatest."""
+scores of -inf and very large ones, weights far below the greatest,
+groups of a few steps of fp16."""
 import numpy as np
 import pytest
 import torch
@@ -250,3 +251,27 @@ def test_a_long_rows_tokens_far_behind_its_first(lead, B, quant):
     assert np.abs(lse - score - np.log1p(rest)).max() <= 2.0 ** -16 + rest / 32 + n / 64 * 2.0 ** -25
     assert api.pkv_get_error(b.ws)[0] == 0
     clean(b.ws)
+
+
+# ------------------------------------------------------------------ groups of a few steps of fp16
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_that_span_a_few_steps(d):
+    """The values furthest from 0 in units of their range: one to three steps of fp16 at the limit, at either side of
+    a power of two and among the subnormals, with 15 times the range on and off the grid."""
+    rng = np.random.default_rng(91)
+    at = np.array([16384.0, 16360.0, 8192.0, 8184.0, 4095.0, 1.0, 2.0 - 2.0 ** -10, 2.0 ** -14, 3 * 2.0 ** -24])
+    rows = []
+    for base in at:
+        for steps in range(4):
+            x = np.abs(np.float16(base)).view(np.uint16) - rng.integers(0, steps + 1, (4, 2, d // 32, 32))
+            x[..., 0], x[..., 1] = x[..., 0].max(), x[..., 0].max() - steps
+            x = np.maximum(x, 0).astype(np.uint16).view(np.float16).reshape(4, 2, d)
+            rows += [x, -x]
+    x = np.concatenate(rows)
+    b = Batch([len(x) + 20], Hkv=2, G=1, d=d, P=16, seed=92, fill=0)
+    b.append([x], [-x])
+    k, v = b.read()
+    assert np.array_equal(bits(k), bits(R.values(x)))
+    assert np.array_equal(bits(v), bits(R.values(-x)))
+    b.ok()
