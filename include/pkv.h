@@ -442,9 +442,9 @@ int pkv_quant_append(const pkv_shape_t *shape, void *d_ws, const void *d_k_new, 
  * One kernel launch.  Rows d_out_offsets[i] .. d_out_offsets[i + 1] of d_k_out
  * and d_v_out ([Hkv][d] each, `out_stride` elements apart, as above) get tokens
  * d_first[i] .. of row i (d_first NULL: from token 0).  Output rows outside
- * every row's span are left as they were.  A token outside [0, seq_lens[i]) or
- * on a page id out of range is written as zeros and recorded in the error
- * word. */
+ * every row's span are left as they were, and tokens behind total_out are not
+ * read.  A token outside [0, seq_lens[i]) or on a page id out of range is
+ * written as zeros and recorded in the error word. */
 int pkv_quant_read(const pkv_shape_t *shape, void *d_ws, const void *d_quant_cache,
                    const int32_t *d_block_table, const int32_t *d_seq_lens, const int32_t *d_first,
                    const int32_t *d_out_offsets, int32_t total_out, void *d_k_out, void *d_v_out,

@@ -100,7 +100,9 @@ struct Layout {
     static constexpr int kKvBytes = QUANT ? kTile * D * 5 / 4 : 2 * kTileBytes;
     static constexpr int kQBytes = kMaxG * D * 2;
     static constexpr int kStageBytes = kKvBytes + kQBytes;
-    // as many CTAs as registers or shared memory hold.  fp16 pages with d = 64 (a
+    // as many CTAs as registers or shared memory hold; for the 4-bit cache's three
+    // and four the compiler keeps 12 to 36 bytes a thread (84 in clusters with d = 64)
+    // of its 128 and 96 registers' worth in local memory.  fp16 pages with d = 64 (a
     // head's token is one 128-byte line among the others' heads) want more loads
     // from more warps in flight: 64 rows in a window of 8191, three CTAs of two
     // stages 166 us, two of three 208 us; clusters the latter (12.8 and 14.9 us

@@ -7,8 +7,8 @@
 //
 // Both are one pass over their data: append reads 2 bytes per value and writes
 // 0.625, read the other way round.  42k tokens of 8 heads, d = 128, are 226 MB,
-// 33 us at the copy rate: read takes 38 us, append 50, where its some fourteen
-// instructions per value are the bound (issue 75%, ALU 64%, DRAM 50%).
+// 33 us at the copy rate: read takes 39 us, append 50, where its some fifteen
+// instructions per value are the bound (issue 73%, ALU 62%, DRAM 49%).
 //
 // A warp takes eight tokens, four lanes each, and loops over KV heads and sides,
 // so that rows, pages and offsets are looked up once for all of them; short
@@ -597,7 +597,7 @@ cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
 {
     const int64_t chunks = ((int64_t)p.T + 7) / 8;
     // several waves of warps, each with two heads or more unless the launch is a
-    // single wave: of eight heads, two per warp 38 us (42k tokens) and 99 us
+    // single wave: of eight heads, two per warp 39 us (42k tokens) and 99 us
     // (117k), one 42 and 111 us, four 41 and 101 us, all eight 49 and 106 us
     const int64_t wave = 32 * (int64_t)sms;
     p.parts = split_work(chunks, p.Hkv, 8 * wave, INT64_MAX, p.heads_per_part);
