@@ -30,7 +30,7 @@ ones need a greater one: then the earlier codes c * 2^e are rounded alike.
 
 A cache is uint8 [num_pages][Hkv][bytes]; a page of one head holds blocks of
 TB = min(P, 64) tokens, each of three parts:
-  K codes  [token][dim]; with d = 128 the two 64-byte halves of odd tokens swapped
+  K codes  [token][dim]; with d = 128 the two 64-byte halves of tokens 2, 3 of every four swapped
   V codes  [token / SB][dim / 4][token % SB / 4][dim % 4][token % 4]
   scales   [token / SB][K | V] fp32, padded to a multiple of 16 bytes
 """
@@ -401,11 +401,11 @@ def _parts(cache, P, d):
 
 
 def _turned(k, token):
-    """K codes [.., d] of tokens [..] with the halves of odd ones swapped, back or forth."""
+    """K codes [.., d] of tokens [..] with the halves of two in four swapped, back or forth."""
     if k.shape[-1] < 128:
         return k
-    odd = (token % 2 == 1).view(token.shape + (1,) * (k.dim() - token.dim()))
-    return torch.where(odd, k.roll(64, -1), k)
+    swapped = (token % 4 >= 2).view(token.shape + (1,) * (k.dim() - token.dim()))
+    return torch.where(swapped, k.roll(64, -1), k)
 
 
 def _decoded(c, fmt):
@@ -535,7 +535,7 @@ def _exact_bytes(cache, pages, n, P, d):
     head = torch.arange(cache.shape[1], device=cache.device).view(1, -1, 1)
     page, slot = tok // P, tok % P
     base, r = slot // tb * size, slot % tb
-    half = r % 2 * 64 if d == 128 else 0
+    half = r % 4 // 2 * 64 if d == 128 else 0
     u = r % sb
     k = held[page, head, base + r * d + torch.bitwise_xor(dim, torch.as_tensor(half, device=cache.device))]
     v = held[page, head, base + tb * d + r // sb * sb * d + (dim // 4 * (sb // 4) + u // 4) * 16 + dim % 4 * 4 + u % 4]
