@@ -289,8 +289,8 @@ def prepare(case, seed):
             st.update(offsets=_offsets(new), lens_out=torch.empty_like(st["lens"]), one=case["new_lo"] == case["new_hi"] == 1)
     if own:
         from paged_kv_gqa_09_gb300 import api
-        st["fmt"] = {"int8": api.PKV_Q8_INT8, "e4m3": api.PKV_Q8_E4M3}[case["fmt"]]
-        st["shape"] = api.make_q8_shape(case["Hq"], d, st["cache"], st["table"])
+        st["fmt"] = {"int8": api.PKV_BYTE_INT8, "e4m3": api.PKV_BYTE_E4M3}[case["fmt"]]
+        st["shape"] = api.make_byte_shape(case["Hq"], d, st["cache"], st["table"])
         st["ws"] = torch.zeros(api.pkv_attn_workspace_size(st["shape"]), dtype=torch.uint8, device="cuda")
     return st
 
@@ -317,19 +317,19 @@ def _run_own(st, op):
         api.pkv_append_slots(st["shape"], st["ws"], st["k_new"], st["v_new"], st["slots"], st["k"], st["v"])
         return {"k": st["k"], "v": st["v"]}
     if op == "append":
-        api.pkv_q8_append(st["shape"], st["ws"], st["fmt"], st["k_new"], st["v_new"], st["table"], st["lens"], st["cache"],
+        api.pkv_byte_append(st["shape"], st["ws"], st["fmt"], st["k_new"], st["v_new"], st["table"], st["lens"], st["cache"],
                           new_offsets=None if st["one"] else st["offsets"], seq_lens_out=st["lens_out"])
-        api.pkv_q8_read(st["shape"], st["ws"], st["fmt"], st["cache"], st["table"], st["lens_out"], st["out_offsets"],
+        api.pkv_byte_read(st["shape"], st["ws"], st["fmt"], st["cache"], st["table"], st["lens_out"], st["out_offsets"],
                         st["k_out"], st["v_out"], first=st["first"])
         return {"lens": st["lens_out"], "k": st["k_out"], "v": st["v_out"]}
     if op == "read":
-        api.pkv_q8_read(st["shape"], st["ws"], st["fmt"], st["cache"], st["table"], st["lens"], st["out_offsets"],
+        api.pkv_byte_read(st["shape"], st["ws"], st["fmt"], st["cache"], st["table"], st["lens"], st["out_offsets"],
                         st["k_out"], st["v_out"])
         return {"k": st["k_out"], "v": st["v_out"]}
     if c["window"] < 0:
-        api.pkv_q8_decode(st["shape"], st["ws"], st["fmt"], st["q"], st["cache"], st["table"], st["lens"], st["o"], st["lse"])
+        api.pkv_byte_decode(st["shape"], st["ws"], st["fmt"], st["q"], st["cache"], st["table"], st["lens"], st["o"], st["lse"])
     else:
-        api.pkv_q8_decode(st["shape"], st["ws"], st["fmt"], st["q"], st["cache"], st["table"], st["lens"], st["o"], st["lse"],
+        api.pkv_byte_decode(st["shape"], st["ws"], st["fmt"], st["q"], st["cache"], st["table"], st["lens"], st["o"], st["lse"],
                           window=c["window"], sinks=c["sinks"])
     return {"o": st["o"], "lse": st["lse"]}
 
