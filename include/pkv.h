@@ -469,6 +469,112 @@ int pkv_window_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d
                       const void *d_k_cache, const void *d_v_cache, const int32_t *d_block_table,
                       const int32_t *d_seq_lens, void *d_o, float *d_lse, void *stream);
 
+/* --------------------------------------------- pages and slots of new tokens */
+
+/* (Not steps of the pages' method: how requests of any length get their pages,
+ * and how their tokens get there, in a serving loop.)  These calls take the
+ * workspace of the calls above, under the same rules. */
+
+/* pkv_map_pages -- pages, slots and positions of new tokens, on the device.
+ * One kernel launch.  Row i holds N = seq_lens[i] tokens in ceil(N / page_size)
+ * pages, which its block table names, and gets n = new_lens[i] more (0 or more):
+ *   new_offsets[i] = new_lens[0] + .. + new_lens[i - 1] (int32 [B + 1]; at most
+ *     total_new): where its tokens lie among the packed ones;
+ *   block_table[i][..]: the need_i = ceil((N + n) / page_size) - ceil(N / page_size)
+ *     pages it lacks, taken in row order from the free list
+ *     d_free_pages[0 .. *d_free_count), whose top is its end;
+ *   slot_map[new_offsets[i] + k] = page * page_size + (N + k) % page_size (int64):
+ *     the slot of its k-th new token in the pool, of pkv_append_slots;
+ *   positions[new_offsets[i] + k] = N + k (int32; NULL: not wanted);
+ *   seq_lens_out[i] = N + n (it may be seq_lens: in place);
+ *   *d_free_count_out = what is left (it may be d_free_count).
+ * Entries of slot_map and positions behind the last token, up to total_new, are
+ * -1 and 0, so that a call captured for total_new tokens serves fewer.
+ * A row is refused whole, and the error word records the first that is, when it
+ * has a negative length or new length or no room in its block table, when its
+ * tokens pass total_new, or when it needs pages and the rows up to and including
+ * it need more than are free (a later row that needs none is served).  Its tokens
+ * get slot -1 and position 0, it keeps its length, and where only pages or packed
+ * room were lacking the entries of its new pages become -1 (those of the tokens
+ * within total_new), so that no append finds an old page there.  A page id out of
+ * range, of the free list or the table, gives the tokens on that page slot -1; the
+ * row keeps its length, its entries and its pages stay taken.
+ * free_capacity: entries of d_free_pages; a count outside [0, free_capacity] is
+ * taken as the nearest of the two.  B up to 2^30.  Counted as a plan launch. */
+int pkv_map_pages(const pkv_shape_t *shape, void *d_ws, const int32_t *d_seq_lens, const int32_t *d_new_lens,
+                  int32_t *d_seq_lens_out, int32_t *d_block_table, const int32_t *d_free_pages, int32_t free_capacity,
+                  const int32_t *d_free_count, int32_t *d_free_count_out, int32_t *d_new_offsets, int64_t *d_slot_map,
+                  int32_t *d_positions, int32_t total_new, void *stream);
+
+/* pkv_append_slots -- write new tokens into the fp16 pages by their slots.
+ * One kernel launch.  Packed token x of d_k_new and d_v_new ([Hkv][d] fp16 each,
+ * `new_stride` elements apart: as for pkv_quant_append) goes to slot
+ * slot_map[x] of k_cache and v_cache (slot s: page s / page_size, its token
+ * s % page_size).  A token with a negative slot is skipped; one with a slot beyond
+ * the pool too, and the error word records it.  Lengths are not touched (those of
+ * pkv_map_pages go with it).  Slots of one call must differ.  Of the shape, Hkv
+ * (up to 2^20), d, page_size and num_pages are used, and B = 0 is nothing. */
+int pkv_append_slots(const pkv_shape_t *shape, void *d_ws, const void *d_k_new, const void *d_v_new, int64_t new_stride,
+                     int32_t total_new, const int64_t *d_slot_map, void *d_k_cache, void *d_v_cache, void *stream);
+
+/* ------------------------------------------------------- 8-bit KV cache */
+
+/* (Not a step of the pages' method: a cache of half the bytes.)
+ *
+ * The 8-bit cache is one buffer for K and V, uint8
+ *   byte_cache [num_pages][Hkv][page_size / TB][2 * TB * d + S],
+ * TB = min(page_size, 64), S = 32 where TB is 64, else 16.  SB = min(page_size, 16)
+ * neighbouring tokens of one head and side (K or V) share a scale 2^e; code c
+ * stands for c 2^e exactly:
+ *   PKV_BYTE_INT8  c is an int8, its greatest magnitude Q = 127, e in -24 .. 9;
+ *   PKV_BYTE_E4M3  c is a float of 1 + 4 + 3 bits, bias 7 (fp8 e4m3: no infinities),
+ *                Q = 448, e in -15 .. 7.
+ * e is the least in its range with max |x| <= Q 2^e over the block's values, c the
+ * code nearest to x / 2^e, the even one on a tie; values beyond Q 2^9 or Q 2^7
+ * (infinities too) are taken as that.  Tokens that join a block with earlier ones
+ * keep its e unless they need a greater one: then the earlier codes, too, become
+ * the nearest to their values c 2^e_old.  A block that a NaN has joined reads back
+ * as NaNs from then on, until its first token is written anew.  Every value is an
+ * fp16 number.  A value is off by at most 2^(e-1) (int8), by 2^-4 of itself or
+ * 2^(e-10) (e4m3), once more for each time that its block's e has grown.
+ * A block of TB tokens is one contiguous run in three parts,
+ *   K codes  [token][dim]; with d = 128 the two 64-byte halves of tokens 2 and 3
+ *            of every four are swapped
+ *   V codes  [token / SB][dim / 4][token % SB / 4][dim % 4][token % 4]
+ *   scales   [token / SB][K | V] fp32, the numbers 2^e, then unused bytes up to S.
+ * A zero-filled cache holds zeros.
+ *
+ * The calls take the workspace of the calls above, under the same rules, and rows
+ * of up to 2^31 - 256 tokens (bt_stride * page_size). */
+#define PKV_BYTE_INT8 0
+#define PKV_BYTE_E4M3 1
+
+/* Bytes of one page of the 8-bit cache, all KV heads (0 for a bad shape). */
+size_t pkv_byte_page_bytes(const pkv_shape_t *shape);
+
+/* pkv_byte_append -- quantise new tokens into the 8-bit cache.  One kernel launch.
+ * Arguments, refusals and errors are those of pkv_quant_append.  A row or call that
+ * is refused on account of a page, or of offsets that do not ascend, may have
+ * rounded the earlier tokens of its last block to a greater scale already. */
+int pkv_byte_append(const pkv_shape_t *shape, void *d_ws, int32_t format, const void *d_k_new, const void *d_v_new,
+                  int64_t new_stride, int32_t total_new, const int32_t *d_new_offsets, const int32_t *d_block_table,
+                  const int32_t *d_seq_lens, int32_t *d_seq_lens_out, void *d_byte_cache, void *stream);
+
+/* pkv_byte_read -- read tokens of the 8-bit cache back as fp16.  One kernel launch.
+ * Arguments and errors are those of pkv_quant_read. */
+int pkv_byte_read(const pkv_shape_t *shape, void *d_ws, int32_t format, const void *d_byte_cache, const int32_t *d_block_table,
+                const int32_t *d_seq_lens, const int32_t *d_first, const int32_t *d_out_offsets, int32_t total_out,
+                void *d_k_out, void *d_v_out, int64_t out_stride, void *stream);
+
+/* pkv_byte_decode -- one decode step's attention over the 8-bit cache.  One kernel
+ * launch.  o and lse are those of pkv_single_pass over the values that
+ * pkv_byte_read returns, with fp32 sums; window, empty rows and heads whose scores
+ * are all -inf as for pkv_quant_decode.  A head that sees a token of a NaN block,
+ * of K or of V, gets NaN for o and lse. */
+int pkv_byte_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d_ws, int32_t format, const void *d_q,
+                  const void *d_byte_cache, const int32_t *d_block_table, const int32_t *d_seq_lens, void *d_o, float *d_lse,
+                  void *stream);
+
 /* ------------------------------------------------------------- policy */
 
 /* Thresholds of the calibrated policy (Methodology 2).  The pages route

@@ -29,6 +29,8 @@ PKV_MERGE_FUSED = 1     # merged on the decode kernel's tail
 PKV_PLAN_SEPARATE = 0   # the workqueue's plan is its own launch (pkv_plan)
 PKV_PLAN_IN_DECODE = 1  # the decode kernel builds the plan itself (B <= PKV_SELF_PLAN_MAX_B)
 PKV_SELF_PLAN_MAX_B = 512
+PKV_BYTE_INT8 = 0  # formats of the 8-bit cache
+PKV_BYTE_E4M3 = 1
 PATH_EXACT_BUCKETS = 3  # step-model only
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024  # PKV_NOALLOC_SCRATCH_BYTES in include/pkv.h
@@ -46,6 +48,7 @@ EXPORTS = [
     "pkv_single_pass", "pkv_decode_step", "pkv_decode_step_rows", "pkv_decode_step_noalloc",
     "pkv_decode_step_host", "pkv_append_decode_step_host",
     "pkv_append", "pkv_append_plan", "pkv_exact_length_groups", "pkv_policy_default", "pkv_policy",
+    "pkv_map_pages", "pkv_append_slots", "pkv_byte_page_bytes", "pkv_byte_append", "pkv_byte_read", "pkv_byte_decode",
     "pkv_cost_model_default", "pkv_policy_learned",
     "pkv_quant_page_bytes", "pkv_attn_workspace_size", "pkv_quant_append", "pkv_quant_read",
     "pkv_quant_decode", "pkv_window_decode",
@@ -164,6 +167,12 @@ def load() -> ctypes.CDLL:
             "pkv_quant_read": (ctypes.c_int, [S] + [vp] * 6 + [i32, vp, vp, ctypes.c_int64, vp]),
             "pkv_quant_decode": (ctypes.c_int, [S, W] + [vp] * 8),
             "pkv_window_decode": (ctypes.c_int, [S, W] + [vp] * 9),
+            "pkv_map_pages": (ctypes.c_int, [S] + [vp] * 6 + [i32] + [vp] * 5 + [i32, vp]),
+            "pkv_append_slots": (ctypes.c_int, [S, vp, vp, vp, ctypes.c_int64, i32] + [vp] * 4),
+            "pkv_byte_page_bytes": (sz, [S]),
+            "pkv_byte_append": (ctypes.c_int, [S, vp, i32, vp, vp, ctypes.c_int64, i32] + [vp] * 6),
+            "pkv_byte_read": (ctypes.c_int, [S, vp, i32] + [vp] * 5 + [i32, vp, vp, ctypes.c_int64, vp]),
+            "pkv_byte_decode": (ctypes.c_int, [S, W, vp, i32] + [vp] * 7),
             "pkv_policy_default": (None, [PC]),
             "pkv_policy": (ctypes.c_int, [i32, i32, PC, ctypes.POINTER(ctypes.c_int32),
                                           ctypes.POINTER(ctypes.c_int32)]),
@@ -206,7 +215,8 @@ def load_call():
         spec.loader.exec_module(m)
         m.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
                  ("pkv_attn_workspace_size", "pkv_quant_append", "pkv_quant_read", "pkv_quant_decode",
-                  "pkv_window_decode")))
+                  "pkv_window_decode", "pkv_map_pages", "pkv_append_slots", "pkv_byte_append", "pkv_byte_read",
+                  "pkv_byte_decode")))
         _call = m
     return _call
 

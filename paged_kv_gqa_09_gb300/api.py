@@ -19,7 +19,7 @@ import torch
 from . import _lib
 from ._lib import (PKV_MERGE_FUSED, PKV_MERGE_SEPARATE, PKV_PATH_BUCKETED_SPLIT,
                    PKV_PATH_SINGLE_PASS, PKV_PATH_WORKQUEUE, PKV_PLAN_IN_DECODE,
-                   PKV_PLAN_SEPARATE, PKV_SELF_PLAN_MAX_B, Counters,
+                   PKV_PLAN_SEPARATE, PKV_BYTE_E4M3, PKV_BYTE_INT8, PKV_SELF_PLAN_MAX_B, Counters,
                    PlanCfg, PolicyCfg, Shape, StepModel, Window, check)
 
 __all__ = [
@@ -32,7 +32,9 @@ __all__ = [
     "exact_length_buckets_step", "pkv_exact_length_groups", "pkv_append",
     "pkv_append_plan", "Window", "make_quant_shape", "quant_cache_zeros", "pkv_quant_page_bytes",
     "pkv_attn_workspace_size", "pkv_quant_append", "pkv_quant_read", "pkv_quant_decode",
-    "pkv_window_decode", "pkv_policy", "pkv_policy_default",
+    "pkv_window_decode", "pkv_map_pages", "pkv_append_slots", "PKV_BYTE_INT8", "PKV_BYTE_E4M3",
+    "make_byte_shape", "byte_cache_zeros", "pkv_byte_page_bytes", "pkv_byte_append", "pkv_byte_read",
+    "pkv_byte_decode", "pkv_policy", "pkv_policy_default",
     "pkv_cost_model_default", "pkv_policy_learned",
     "pkv_get_counters", "pkv_reset_counters", "pkv_step_model", "pkv_get_error", "pkv_version",
     "PagedDecoder", "HostDecodeLoop",
@@ -384,7 +386,7 @@ def pkv_attn_workspace_size(shape: Shape) -> int:
     return int(n)
 
 
-# These four are called per layer and token, where the host's share counts: their
+# These are called per layer and token, where the host's share counts: their
 # tensors are checked and unpacked by compiled code (csrc/binding.cpp), which
 # raises TypeError or ValueError as the functions above do.
 
@@ -435,6 +437,98 @@ def pkv_window_decode(shape, ws, q, k_cache, v_cache, block_table, seq_lens, win
         None if stream is None else _stream(stream))
     if st:
         check(st, "pkv_window_decode")
+
+
+# --------------------------------------------- pages and slots of new tokens
+
+def pkv_map_pages(shape, ws, seq_lens, new_lens, block_table, free_pages, free_count, slot_map, new_offsets,
+                  seq_lens_out=None, free_count_out=None, positions=None, stream=None) -> None:
+    """Give row i the pages that its new_lens[i] new tokens lack, from the free
+    list, and list every new token's slot (slot_map, int64, one entry per packed
+    token) and position; new_offsets [B + 1] are the rows' places among the packed
+    tokens.  The advanced lengths go to seq_lens_out and the free count to
+    free_count_out (None: in place).  See include/pkv.h for what is refused."""
+    st = (_lib._call or _lib.load_call()).map_pages(
+        shape, ws, seq_lens, new_lens, block_table, free_pages, free_count, slot_map, new_offsets, seq_lens_out,
+        free_count_out, positions, None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_map_pages")
+
+
+def pkv_append_slots(shape, ws, k_new, v_new, slot_map, k_cache, v_cache, stream=None) -> None:
+    """Write packed tokens k_new, v_new [T, Hkv, d] to their slots in the fp16
+    pages; those with a negative slot are skipped.  Tokens may be strided (a slice
+    of a fused projection)."""
+    st = (_lib._call or _lib.load_call()).append_slots(
+        shape, ws, k_new, v_new, slot_map, k_cache, v_cache, None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_append_slots")
+
+
+# ----------------------------------------------------------------- 8-bit cache
+
+def _byte_head_bytes(page_size: int, d: int) -> int:
+    tb = min(page_size, 64)
+    return page_size // tb * (2 * tb * d + (32 if tb == 64 else 16))
+
+
+def make_byte_shape(Hq: int, d: int, byte_cache: torch.Tensor, block_table: torch.Tensor,
+                  scale: Optional[float] = None) -> Shape:
+    """Shape of an 8-bit cache uint8 [num_pages, Hkv, bytes of a page of one head]
+    for Hq query heads of d dims and block_table [B, bt_stride]."""
+    num_pages, Hkv, nbytes = byte_cache.shape
+    for P in (8, 16, 32, 64, 128, 256):
+        if _byte_head_bytes(P, d) == nbytes:
+            return Shape(int(block_table.shape[0]), int(Hq), int(Hkv), int(d), P, int(num_pages),
+                         int(block_table.shape[1]), float(1.0 / math.sqrt(d) if scale is None else scale))
+    raise ValueError(f"byte_cache pages of {nbytes} bytes are no page size's of d={d}")
+
+
+def byte_cache_zeros(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda") -> torch.Tensor:
+    """An 8-bit cache of num_pages pages, of either format, every value 0."""
+    return torch.zeros((num_pages, Hkv, _byte_head_bytes(page_size, d)), dtype=torch.uint8, device=device)
+
+
+def pkv_byte_page_bytes(shape: Shape) -> int:
+    n = _lib.load().pkv_byte_page_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise _lib.PkvError(_lib.PKV_EINVAL, "pkv_byte_page_bytes", _lib.last_error())
+    return int(n)
+
+
+def pkv_byte_append(shape, ws, fmt, k_new, v_new, block_table, seq_lens, byte_cache, new_offsets=None,
+                  seq_lens_out=None, stream=None) -> None:
+    """Quantise new tokens into the 8-bit cache of format `fmt` (PKV_BYTE_INT8 or
+    PKV_BYTE_E4M3); the other arguments are those of pkv_quant_append."""
+    st = (_lib._call or _lib.load_call()).byte_append(
+        shape, ws, fmt, k_new, v_new, block_table, seq_lens, byte_cache, new_offsets, seq_lens_out,
+        None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_byte_append")
+
+
+def pkv_byte_read(shape, ws, fmt, byte_cache, block_table, seq_lens, out_offsets, k_out, v_out, first=None,
+                stream=None) -> None:
+    """Read tokens of the 8-bit cache back as fp16; the arguments are those of
+    pkv_quant_read."""
+    st = (_lib._call or _lib.load_call()).byte_read(
+        shape, ws, fmt, byte_cache, block_table, seq_lens, out_offsets, k_out, v_out, first,
+        None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_byte_read")
+
+
+def pkv_byte_decode(shape, ws, fmt, q, byte_cache, block_table, seq_lens, o, lse=None, window=None, sinks=0,
+                  stream=None) -> None:
+    """Decode attention over the 8-bit cache: the whole row (window None), or its
+    first `sinks` and last `window` tokens."""
+    if window is None and sinks:
+        raise ValueError("sinks go with a window")
+    st = (_lib._call or _lib.load_call()).byte_decode(
+        shape, ws, fmt, q, byte_cache, block_table, seq_lens, o, lse, window, sinks,
+        None if stream is None else _stream(stream))
+    if st:
+        check(st, "pkv_byte_decode")
 
 
 def pkv_policy_default() -> PolicyCfg:
@@ -587,8 +681,8 @@ class PagedDecoder:
         return self._ws.get(device)
 
     def attn_workspace(self, shape: Shape, device, stream=None) -> torch.Tensor:
-        """The workspace of step_window, step_quant and append_quant for this
-        kind of shape on this device, zeroed when it is made -- which is not while
+        """The workspace of step_window, step_quant, append_quant and the calls
+        below for this kind of shape on this device, zeroed when it is made -- which is not while
         a graph is captured, whose replay alone would do it.  It is zero when this
         returns, for calls on any stream: making it waits for `stream` (None: the
         current one), once.  The decoder's calls must not overlap on the GPU."""
@@ -633,6 +727,46 @@ class PagedDecoder:
         shape = make_quant_shape(quant_cache.shape[1], k_new.shape[2], quant_cache, block_table)
         pkv_quant_append(shape, self.attn_workspace(shape, quant_cache.device, stream), k_new, v_new, block_table, seq_lens,
                          quant_cache, new_offsets, seq_lens_out, stream)
+
+    def map_pages(self, shape: Shape, seq_lens, new_lens, block_table, free_pages, free_count, slot_map, new_offsets,
+                  seq_lens_out=None, free_count_out=None, positions=None, stream=None) -> None:
+        """Pages, slots and positions of new tokens (see pkv_map_pages); the shape
+        is that of the cache they go to (make_shape, make_quant_shape or
+        make_byte_shape)."""
+        pkv_map_pages(shape, self.attn_workspace(shape, seq_lens.device, stream), seq_lens, new_lens, block_table,
+                      free_pages, free_count, slot_map, new_offsets, seq_lens_out, free_count_out, positions, stream)
+
+    def append_slots(self, k_new, v_new, slot_map, k_cache, v_cache, stream=None) -> None:
+        """Write new tokens k_new, v_new [T, Hkv, d] to their slots in the fp16 pages (see pkv_append_slots)."""
+        num_pages, P, Hkv, d = k_cache.shape
+        shape = Shape(1, int(Hkv), int(Hkv), int(d), int(P), int(num_pages), 1, 1.0)
+        pkv_append_slots(shape, self.attn_workspace(shape, k_cache.device, stream), k_new, v_new, slot_map, k_cache, v_cache,
+                         stream)
+
+    def step_byte(self, fmt: int, q, byte_cache, block_table, seq_lens, window: Optional[int] = None, sinks: int = 0,
+                o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                scale: Optional[float] = None, stream=None):
+        """One decode step over an 8-bit cache, whole rows or a window; returns (o, lse)."""
+        shape = make_byte_shape(q.shape[1], q.shape[2], byte_cache, block_table, scale)
+        if shape.B != q.shape[0]:
+            raise ValueError("q and block_table disagree on B")
+        o, lse = self._outputs(q, o, lse, want_lse, stream)
+        pkv_byte_decode(shape, self.attn_workspace(shape, q.device, stream), fmt, q, byte_cache, block_table, seq_lens, o, lse,
+                      window, sinks, stream)
+        return o, lse
+
+    def append_byte(self, fmt: int, k_new, v_new, byte_cache, block_table, seq_lens, new_offsets=None, seq_lens_out=None,
+                  stream=None) -> None:
+        """Quantise new tokens k_new, v_new [T, Hkv, d] into an 8-bit cache (see pkv_byte_append)."""
+        shape = make_byte_shape(byte_cache.shape[1], k_new.shape[2], byte_cache, block_table)
+        pkv_byte_append(shape, self.attn_workspace(shape, byte_cache.device, stream), fmt, k_new, v_new, block_table, seq_lens,
+                      byte_cache, new_offsets, seq_lens_out, stream)
+
+    def read_byte(self, fmt: int, byte_cache, block_table, seq_lens, out_offsets, k_out, v_out, first=None, stream=None) -> None:
+        """Read tokens of an 8-bit cache back into k_out, v_out [T, Hkv, d] (see pkv_byte_read)."""
+        shape = make_byte_shape(byte_cache.shape[1], k_out.shape[2], byte_cache, block_table)
+        pkv_byte_read(shape, self.attn_workspace(shape, byte_cache.device, stream), fmt, byte_cache, block_table, seq_lens,
+                    out_offsets, k_out, v_out, first, stream)
 
     @staticmethod
     def _outputs(q, o, lse, want_lse, stream):

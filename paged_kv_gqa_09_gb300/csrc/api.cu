@@ -5,6 +5,7 @@
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "plan_map.cuh"
+#include "byte_format.cuh"
 #include "quant_format.cuh"
 
 #include <atomic>
@@ -110,6 +111,7 @@ int check_cfg(const pkv_shape_t *s, const pkv_plan_cfg_t *c)
     return PKV_OK;
 }
 
+static_assert((int)pkv::kInt8 == PKV_BYTE_INT8 && (int)pkv::kE4m3 == PKV_BYTE_E4M3, "one numbering of the 8-bit formats");
 static_assert(pkv::kSelfPlanMaxB == PKV_SELF_PLAN_MAX_B, "one row limit for the self-planning decode");
 
 // The workqueue decode of this shape and cfg builds its own plan.
@@ -1144,8 +1146,26 @@ int check_packed(const pkv_shape_t *s, int32_t T, int64_t stride, const char *na
     return PKV_OK;
 }
 
+int64_t byte_page_head_bytes(const pkv_shape_t *s)
+{
+    const int tb = byte_block_tokens(s->page_size);
+    return (int64_t)(s->page_size / tb) * byte_block_bytes(tb, s->d);
+}
+
+int check_byte(const pkv_shape_t *s, int32_t format)
+{
+    if (format != PKV_BYTE_INT8 && format != PKV_BYTE_E4M3)
+        return fail(PKV_EINVAL, "unknown 8-bit format %d", format);
+    if ((int64_t)s->bt_stride * s->page_size > 0x7fffff00LL)  // the end of a row's last block is an int32
+        return fail(PKV_EUNSUPPORTED, "rows of %lld tokens (bt_stride * page_size; supported: up to 2^31 - 256)",
+                    (long long)s->bt_stride * s->page_size);
+    return PKV_OK;
+}
+
+constexpr int kNo8Bit = -1;  // in place of an 8-bit format: the 4-bit cache, or fp16 pages
+
 int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const void *q, const void *k,
-               const void *v, const void *cache, const int32_t *bt, const int32_t *sl, void *o, float *lse,
+               const void *v, const void *cache, int format, const int32_t *bt, const int32_t *sl, void *o, float *lse,
                void *stream)
 {
     if (win && (win->window < 0 || win->sinks < 0))
@@ -1165,7 +1185,7 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     PKV_TRY(check_ptr(d_ws, "workspace"));
     PKV_TRY(check_ptr(q, "q"));
     if (cache) {
-        PKV_TRY(check_ptr(cache, "quant_cache"));
+        PKV_TRY(check_ptr(cache, format == kNo8Bit ? "quant_cache" : "byte_cache"));
     } else {
         PKV_TRY(check_ptr(k, "k_cache"));
         PKV_TRY(check_ptr(v, "v_cache"));
@@ -1184,7 +1204,7 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
     p.partials = reinterpret_cast<float *>(static_cast<char *>(d_ws) + kAttnPartialsOff);
     p.o = static_cast<__half *>(o);
     p.lse = lse;
-    p.page_head_bytes = quant_page_head_bytes(s);
+    p.page_head_bytes = format == kNo8Bit ? quant_page_head_bytes(s) : byte_page_head_bytes(s);
     p.B = s->B;
     p.Hq = s->Hq;
     p.Hkv = s->Hkv;
@@ -1207,7 +1227,10 @@ int run_attend(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const 
         PKV_TRY(encode_kv_map(&tk, k, s, box_tok));
         PKV_TRY(encode_kv_map(&tv, v, s, box_tok));
     }
-    cudaError_t e = launch_attend(s->d, tk, tv, p, sms, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = format == PKV_BYTE_INT8   ? launch_attend_int8(s->d, p, sms, st)
+                    : format == PKV_BYTE_E4M3 ? launch_attend_e4m3(s->d, p, sms, st)
+                                            : launch_attend(s->d, tk, tv, p, sms, st);
     if (e != cudaSuccess)
         return cuda_fail(e, "attention launch");
     g_cnt.decode++;
@@ -1329,7 +1352,7 @@ int pkv_quant_decode(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, 
         return PKV_OK;  // an empty batch: nothing to do
     if (!cache)
         return fail(PKV_EINVAL, "quant_cache is NULL");
-    return run_attend(s, win, d_ws, q, nullptr, nullptr, cache, bt, sl, o, lse, stream);
+    return run_attend(s, win, d_ws, q, nullptr, nullptr, cache, kNo8Bit, bt, sl, o, lse, stream);
 }
 
 int pkv_window_decode(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, const void *q, const void *k,
@@ -1340,7 +1363,202 @@ int pkv_window_decode(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws,
         return PKV_OK;  // an empty batch: nothing to do
     if (!win)
         return fail(PKV_EINVAL, "window is NULL");
-    return run_attend(s, win, d_ws, q, k, v, nullptr, bt, sl, o, lse, stream);
+    return run_attend(s, win, d_ws, q, k, v, nullptr, kNo8Bit, bt, sl, o, lse, stream);
+}
+
+size_t pkv_byte_page_bytes(const pkv_shape_t *s)
+{
+    if (check_shape(s))
+        return 0;
+    return (size_t)byte_page_head_bytes(s) * s->Hkv;
+}
+
+int pkv_byte_append(const pkv_shape_t *s, void *d_ws, int32_t format, const void *k_new, const void *v_new, int64_t new_stride,
+                  int32_t total_new, const int32_t *d_new_offsets, const int32_t *bt, const int32_t *sl, int32_t *sl_out,
+                  void *cache, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    PKV_TRY(check_byte(s, format));
+    if (s->B == 0)
+        return PKV_OK;  // an empty batch: nothing to do
+    PKV_TRY(check_packed(s, total_new, new_stride, "k_new"));
+    if (!d_new_offsets && total_new != s->B)
+        return fail(PKV_EINVAL, "without offsets every row has one token: total_new=%d, B=%d", total_new, s->B);
+    PKV_TRY(check_ptr(d_ws, "workspace"));
+    PKV_TRY(check_ptr(k_new, "k_new", total_new == 0));
+    PKV_TRY(check_ptr(v_new, "v_new", total_new == 0));
+    PKV_TRY(check_ptr(d_new_offsets, "new_offsets", true));
+    PKV_TRY(check_ptr(bt, "block_table"));
+    PKV_TRY(check_ptr(sl, "seq_lens"));
+    PKV_TRY(check_ptr(sl_out, "seq_lens_out"));
+    PKV_TRY(check_ptr(cache, "byte_cache"));
+    QuantAppendParams p = {};
+    p.k_new = static_cast<const __half *>(k_new);
+    p.v_new = static_cast<const __half *>(v_new);
+    p.new_stride = new_stride;
+    p.offsets = d_new_offsets;
+    p.bt = bt;
+    p.seq_lens = sl;
+    p.seq_lens_out = sl_out;
+    p.cache = static_cast<uint8_t *>(cache);
+    p.ws = ws_hdr(d_ws);
+    p.page_head_bytes = byte_page_head_bytes(s);
+    p.T = total_new;
+    p.B = s->B;
+    p.Hkv = s->Hkv;
+    p.log2P = ilog2(s->page_size);
+    p.tb_log2 = ilog2(byte_block_tokens(s->page_size));
+    p.num_pages = s->num_pages;
+    p.bt_stride = s->bt_stride;
+    p.len_cap = len_cap(s);
+    int sms = 0;
+    PKV_TRY(device_sms(&sms));
+    cudaError_t e = launch_byte_append(s->d, format, p, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "8-bit append launch");
+    g_cnt.append++;
+    return PKV_OK;
+}
+
+int pkv_byte_read(const pkv_shape_t *s, void *d_ws, int32_t format, const void *cache, const int32_t *bt, const int32_t *sl,
+                const int32_t *d_first, const int32_t *d_out_offsets, int32_t total_out, void *k_out, void *v_out,
+                int64_t out_stride, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    PKV_TRY(check_byte(s, format));
+    if (s->B == 0 || total_out == 0)
+        return PKV_OK;  // nothing to read
+    PKV_TRY(check_packed(s, total_out, out_stride, "k_out"));
+    PKV_TRY(check_ptr(d_ws, "workspace"));
+    PKV_TRY(check_ptr(cache, "byte_cache"));
+    PKV_TRY(check_ptr(bt, "block_table"));
+    PKV_TRY(check_ptr(sl, "seq_lens"));
+    PKV_TRY(check_ptr(d_first, "first", true));
+    PKV_TRY(check_ptr(d_out_offsets, "out_offsets"));
+    PKV_TRY(check_ptr(k_out, "k_out"));
+    PKV_TRY(check_ptr(v_out, "v_out"));
+    QuantReadParams p = {};
+    p.cache = static_cast<const uint8_t *>(cache);
+    p.bt = bt;
+    p.seq_lens = sl;
+    p.first = d_first;
+    p.offsets = d_out_offsets;
+    p.k_out = static_cast<__half *>(k_out);
+    p.v_out = static_cast<__half *>(v_out);
+    p.out_stride = out_stride;
+    p.ws = ws_hdr(d_ws);
+    p.page_head_bytes = byte_page_head_bytes(s);
+    p.T = total_out;
+    p.B = s->B;
+    p.Hkv = s->Hkv;
+    p.log2P = ilog2(s->page_size);
+    p.tb_log2 = ilog2(byte_block_tokens(s->page_size));
+    p.num_pages = s->num_pages;
+    p.bt_stride = s->bt_stride;
+    p.len_cap = len_cap(s);
+    int sms = 0;
+    PKV_TRY(device_sms(&sms));
+    cudaError_t e = launch_byte_read(s->d, format, p, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "8-bit read launch");
+    return PKV_OK;
+}
+
+int pkv_byte_decode(const pkv_shape_t *s, const pkv_window_t *win, void *d_ws, int32_t format, const void *q, const void *cache,
+                  const int32_t *bt, const int32_t *sl, void *o, float *lse, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    PKV_TRY(check_byte(s, format));
+    if (s->B == 0)
+        return PKV_OK;  // an empty batch: nothing to do
+    if (!cache)
+        return fail(PKV_EINVAL, "byte_cache is NULL");
+    return run_attend(s, win, d_ws, q, nullptr, nullptr, cache, format, bt, sl, o, lse, stream);
+}
+
+int pkv_map_pages(const pkv_shape_t *s, void *d_ws, const int32_t *sl, const int32_t *new_lens, int32_t *sl_out, int32_t *bt,
+                  const int32_t *free_pages, int32_t free_capacity, const int32_t *free_count, int32_t *free_count_out,
+                  int32_t *new_offsets, int64_t *slot_map, int32_t *positions, int32_t total_new, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    if (s->B == 0)
+        return PKV_OK;  // an empty batch: nothing to do
+    if (total_new < 0 || free_capacity < 0)
+        return fail(PKV_EINVAL, "negative total_new=%d or free_capacity=%d", total_new, free_capacity);
+    if (s->B > 1 << 30 || total_new > 0x7fffffff - 4)  // the ends of a thread's rows and of a group of tokens are int32s
+        return fail(PKV_EUNSUPPORTED, "B=%d rows, %d tokens (supported: up to 2^30 and 2^31 - 5)", s->B, total_new);
+    PKV_TRY(check_ptr(d_ws, "workspace"));
+    PKV_TRY(check_ptr(sl, "seq_lens"));
+    PKV_TRY(check_ptr(new_lens, "new_lens"));
+    PKV_TRY(check_ptr(sl_out, "seq_lens_out"));
+    PKV_TRY(check_ptr(bt, "block_table"));
+    PKV_TRY(check_ptr(free_pages, "free_pages", free_capacity == 0));
+    PKV_TRY(check_ptr(free_count, "free_count"));
+    PKV_TRY(check_ptr(free_count_out, "free_count_out"));
+    PKV_TRY(check_ptr(new_offsets, "new_offsets"));
+    PKV_TRY(check_ptr(slot_map, "slot_map", total_new == 0));
+    PKV_TRY(check_ptr(positions, "positions", true));
+    MapParams p = {};
+    p.seq_lens = sl;
+    p.new_lens = new_lens;
+    p.seq_lens_out = sl_out;
+    p.bt = bt;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.free_count_out = free_count_out;
+    p.offsets = new_offsets;
+    p.slots = slot_map;
+    p.positions = positions;
+    p.ws = ws_hdr(d_ws);
+    p.T = total_new;
+    p.B = s->B;
+    p.log2P = ilog2(s->page_size);
+    p.num_pages = s->num_pages;
+    p.bt_stride = s->bt_stride;
+    p.len_cap = len_cap(s);
+    p.free_cap = free_capacity;
+    int sms = 0;
+    PKV_TRY(device_sms(&sms));
+    cudaError_t e = launch_map_pages(p, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "page map launch");
+    g_cnt.plan++;
+    return PKV_OK;
+}
+
+int pkv_append_slots(const pkv_shape_t *s, void *d_ws, const void *k_new, const void *v_new, int64_t new_stride,
+                     int32_t total_new, const int64_t *slot_map, void *k_cache, void *v_cache, void *stream)
+{
+    PKV_TRY(check_shape(s));
+    if (s->B == 0 || total_new == 0)
+        return PKV_OK;  // nothing to append
+    PKV_TRY(check_packed(s, total_new, new_stride, "k_new"));
+    if (s->Hkv > 1 << 20)  // a token's 16-byte pieces are counted in an int32
+        return fail(PKV_EUNSUPPORTED, "Hkv=%d (supported: up to 2^20)", s->Hkv);
+    PKV_TRY(check_ptr(d_ws, "workspace"));
+    PKV_TRY(check_ptr(k_new, "k_new"));
+    PKV_TRY(check_ptr(v_new, "v_new"));
+    PKV_TRY(check_ptr(slot_map, "slot_map"));
+    PKV_TRY(check_ptr(k_cache, "k_cache"));
+    PKV_TRY(check_ptr(v_cache, "v_cache"));
+    SlotParams p = {};
+    p.k_new = static_cast<const __half *>(k_new);
+    p.v_new = static_cast<const __half *>(v_new);
+    p.new_stride = new_stride;
+    p.slots = slot_map;
+    p.k_cache = static_cast<__half *>(k_cache);
+    p.v_cache = static_cast<__half *>(v_cache);
+    p.ws = ws_hdr(d_ws);
+    p.num_slots = (int64_t)s->num_pages * s->page_size;
+    p.T = total_new;
+    p.pieces = s->Hkv * s->d / 8;
+    int sms = 0;
+    PKV_TRY(device_sms(&sms));
+    cudaError_t e = launch_append_slots(p, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "slot append launch");
+    g_cnt.append++;
+    return PKV_OK;
 }
 
 // ------------------------------------------------------------------ errors
@@ -1375,6 +1593,8 @@ int pkv_get_error(void *d_ws, void *stream)
                     h[2], h[3]);
     case kErrBadSpan:
         return fail(PKV_EDEVICE, "row %d has %d packed tokens from offset %d, outside the packed buffer", h[1], h[3], h[2]);
+    case kErrBadSlot:
+        return fail(PKV_EDEVICE, "packed token %d has slot %d, the pool %d", h[1], h[2], h[3]);
     case kErrBadRow:
         return fail(PKV_EDEVICE, "row list entry %d is %d, outside [0, %d)", h[1], h[2], h[3]);
     case kErrTimeout:

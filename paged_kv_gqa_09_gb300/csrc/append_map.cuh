@@ -1,8 +1,10 @@
-// append_map.cuh -- which packed tokens a warp of the 4-bit cache's append takes.
+// append_map.cuh -- which packed tokens a warp of the 4-bit and 8-bit caches'
+// appends takes.
 //
-// A warp takes eight cache positions 8 k .. 8 k + 7 of one row, a group: those
-// are whole words of V.  The rows' groups lie on one line, row i's from
-// offsets[i] / 8 + 2 i on, which leaves each room for a first and a last group
+// A warp takes 2^lg cache positions of one row, the first a multiple of that: a
+// group.  Eight are whole words of V in the 4-bit cache, eight or sixteen a block
+// of the 8-bit one.  The rows' groups lie on one line, row i's from
+// (offsets[i] >> lg) + 2 i on, which leaves each room for a first and a last group
 // that are not full and needs no sum over the rows before; what is left over is
 // idle.  A row without new tokens has places on the line all the same, but no
 // group there: its last page, partly filled as it may be, is not looked at.
@@ -14,17 +16,17 @@
 namespace pkv {
 
 // Row i's first group, its new tokens packed from `off` on.
-__host__ __device__ inline int64_t append_first_group(int off, int i) { return (int64_t)(off >> 3) + 2 * (int64_t)i; }
+__host__ __device__ inline int64_t append_first_group(int off, int i, int lg = 3) { return (int64_t)(off >> lg) + 2 * (int64_t)i; }
 
 // Groups on the line of T packed tokens of B rows.
-__host__ __device__ inline int64_t append_groups(int T, int B) { return T > 0 ? (int64_t)T / 8 + 2 * (int64_t)B : 0; }
+__host__ __device__ inline int64_t append_groups(int T, int B, int lg = 3) { return T > 0 ? ((int64_t)T >> lg) + 2 * (int64_t)B : 0; }
 
 // Whether group gs holds any of row i's n new tokens, which follow its N cached
 // ones; pos0: the group's first position.
-__host__ __device__ inline bool append_group(int64_t gs, int i, int off, int n, int N, int64_t &pos0)
+__host__ __device__ inline bool append_group(int64_t gs, int i, int off, int n, int N, int64_t &pos0, int lg = 3)
 {
-    const int k = (int)(gs - append_first_group(off, i));
-    pos0 = ((int64_t)(N >> 3) + k) * 8;
+    const int k = (int)(gs - append_first_group(off, i, lg));
+    pos0 = ((int64_t)(N >> lg) + k) * (1 << lg);
     return n > 0 && k >= 0 && pos0 < (int64_t)N + n;
 }
 
@@ -53,13 +55,35 @@ inline int split_work(int64_t warps, int n, int64_t want, int64_t most, int &per
 // many KV heads would make them so).  Some two to four units per warp: 42k
 // tokens of 8 heads 49.6 us; coarser ones, of which some warps get two and some
 // one, 62 us; finer ones, whose first tile nothing hides, 52 us.
-inline int64_t append_grid(int T, int B, int Hkv, int ctas, int cta_warps, int64_t &groups, int &parts, int &per)
+inline int64_t append_grid(int T, int B, int Hkv, int ctas, int cta_warps, int64_t &groups, int &parts, int &per, int lg = 3)
 {
     const int64_t resident = (int64_t)ctas * cta_warps;
-    groups = append_groups(T, B);
+    groups = append_groups(T, B, lg);
     parts = split_work(groups, 2 * Hkv, 2 * resident, resident, per);
     const int64_t grid = (groups * parts + cta_warps - 1) / cta_warps;
     return grid < ctas ? grid : ctas;
 }
+
+#ifdef __CUDACC__
+
+// The last i in [0, B] with key(i) <= x, for ascending key with key(0) <= x;
+// whole warps only, with one x: 33 keys at a time, so that up to 32 rows take
+// one round trip.
+template <class F>
+__device__ __forceinline__ int last_not_above(int B, int64_t x, F key)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = B;  // the answer is in [lo, lo + n]
+    while (n > 0) {
+        const int step = (n + 31) / 32, at = lo + (lane + 1) * step;  // lo + step, lo + 2 step, ..
+        const unsigned m = __ballot_sync(0xffffffffu, at <= lo + n && key(at) <= x);
+        const int up = __popc(m) * step;
+        lo += up;
+        n = min(n - up, step - 1);
+    }
+    return lo;
+}
+
+#endif  // __CUDACC__
 
 }  // namespace pkv

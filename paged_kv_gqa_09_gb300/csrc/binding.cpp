@@ -1,5 +1,5 @@
 // binding.cpp -- the Python side of the calls a serving loop makes per layer and
-// token (the 4-bit cache and windowed decode): it checks that every tensor lives
+// token (pages and slots, the 4-bit and 8-bit caches, windowed decode): it checks that every tensor lives
 // on the current CUDA device with the dtype, layout and size the C ABI expects
 // and forwards raw pointers and a stream.  ctypes did the same in about 5 us a
 // call on the host; this takes a few tenths.
@@ -30,11 +30,16 @@ struct {
     decltype(&pkv_quant_read) read;
     decltype(&pkv_quant_decode) quant;
     decltype(&pkv_window_decode) window;
+    decltype(&pkv_map_pages) map;
+    decltype(&pkv_append_slots) slots;
+    decltype(&pkv_byte_append) append8;
+    decltype(&pkv_byte_read) read8;
+    decltype(&pkv_byte_decode) decode8;
 } lib;
 
 const char *name_of(at::ScalarType t)
 {
-    return t == at::kHalf ? "torch.float16" : t == at::kInt ? "torch.int32" : t == at::kFloat ? "torch.float32" : "torch.uint8";
+    return t == at::kHalf ? "torch.float16" : t == at::kInt ? "torch.int32" : t == at::kFloat ? "torch.float32" : t == at::kLong ? "torch.int64" : "torch.uint8";
 }
 
 const at::Tensor &tensor(PyObject *o, const char *name)
@@ -112,6 +117,12 @@ struct Call {
     void *quant(PyObject *o)
     {
         return arg(o, "quant_cache", at::kByte, (int64_t)s.num_pages * s.Hkv * ((int64_t)s.page_size * s.d * 5 / 4));
+    }
+
+    void *codes(PyObject *o)
+    {
+        const int64_t tb = s.page_size < 64 ? s.page_size : 64;  // 0 or less: the call itself refuses the shape
+        return arg(o, "byte_cache", at::kByte, tb < 1 ? 0 : (int64_t)s.num_pages * s.Hkv * (s.page_size / tb) * (2 * tb * s.d + (tb == 64 ? 32 : 16)));
     }
 
     // Packed K and V [T, Hkv, d], whose tokens may be strided (alike in both);
@@ -254,15 +265,118 @@ PyObject *window_decode(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// Addresses of pkv_attn_workspace_size, pkv_quant_append, pkv_quant_read, pkv_quant_decode, pkv_window_decode
+// Tokens of a one-dimensional tensor that says how many a call is for.
+int32_t length(const at::Tensor &t, const char *name)
+{
+    if (t.numel() > INT32_MAX)
+        throw Refused{PyExc_ValueError, std::string(name) + " has too many entries"};
+    return (int32_t)t.numel();
+}
+
+// (shape, ws, seq_lens, new_lens, block_table, free_pages, free_count, slot_map, new_offsets, seq_lens_out,
+//  free_count_out, positions, stream)
+PyObject *map_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 13, [a] {
+        Call c(a[0]);
+        void *ws = c.workspace(a[1]);
+        int32_t *sl = c.lens(a[2]), *nl = c.lens(a[3], "new_lens"), *bt = c.table(a[4]);
+        int32_t *fp = c.arg<int32_t>(a[5], "free_pages", at::kInt, 0);
+        const int32_t cap = length(tensor(a[5], "free_pages"), "free_pages");
+        int32_t *fc = c.arg<int32_t>(a[6], "free_count", at::kInt, 1);
+        int64_t *slots = c.arg<int64_t>(a[7], "slot_map", at::kLong, 0);
+        const int32_t T = length(tensor(a[7], "slot_map"), "slot_map");
+        int32_t *off = c.offsets(a[8], "new_offsets", false);
+        int32_t *out = a[9] == Py_None ? sl : c.lens(a[9], "seq_lens_out");
+        int32_t *fout = a[10] == Py_None ? fc : c.arg<int32_t>(a[10], "free_count_out", at::kInt, 1);
+        int32_t *pos = c.arg<int32_t>(a[11], "positions", at::kInt, T, true);
+        void *st = c.stream(a[12]);
+        return [=] { return lib.map(&c.s, ws, sl, nl, out, bt, fp, cap, fc, fout, off, slots, pos, T, st); };
+    });
+}
+
+// (shape, ws, k_new, v_new, slot_map, k_cache, v_cache, stream)
+PyObject *append_slots(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 8, [a] {
+        Call c(a[0]);
+        void *k, *v;
+        int32_t T;
+        int64_t step;
+        c.packed(a[2], a[3], "k_new", "v_new", k, v, T, step);
+        void *ws = c.workspace(a[1]);
+        int64_t *slots = c.arg<int64_t>(a[4], "slot_map", at::kLong, T);
+        void *kc = c.pages(a[5], "k_cache"), *vc = c.pages(a[6], "v_cache");
+        void *st = c.stream(a[7]);
+        return [=] { return lib.slots(&c.s, ws, k, v, step, T, slots, kc, vc, st); };
+    });
+}
+
+// (shape, ws, format, k_new, v_new, block_table, seq_lens, byte_cache, new_offsets, seq_lens_out, stream)
+PyObject *byte_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 11, [a] {
+        Call c(a[0]);
+        const int32_t format = int32(a[2], "format");
+        void *k, *v;
+        int32_t T;
+        int64_t step;
+        c.packed(a[3], a[4], "k_new", "v_new", k, v, T, step);
+        void *ws = c.workspace(a[1]);
+        int32_t *bt = c.table(a[5]), *sl = c.lens(a[6]);
+        void *cache = c.codes(a[7]);
+        int32_t *off = c.offsets(a[8], "new_offsets", true);
+        int32_t *out = a[9] == Py_None ? sl : c.lens(a[9], "seq_lens_out");
+        void *st = c.stream(a[10]);
+        return [=] { return lib.append8(&c.s, ws, format, k, v, step, T, off, bt, sl, out, cache, st); };
+    });
+}
+
+// (shape, ws, format, byte_cache, block_table, seq_lens, out_offsets, k_out, v_out, first, stream)
+PyObject *byte_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 11, [a] {
+        Call c(a[0]);
+        const int32_t format = int32(a[2], "format");
+        void *k, *v;
+        int32_t T;
+        int64_t step;
+        c.packed(a[7], a[8], "k_out", "v_out", k, v, T, step);
+        void *ws = c.workspace(a[1]), *cache = c.codes(a[3]);
+        int32_t *bt = c.table(a[4]), *sl = c.lens(a[5]), *off = c.offsets(a[6], "out_offsets", false);
+        int32_t *first = c.lens(a[9], "first", true);
+        void *st = c.stream(a[10]);
+        return [=] { return lib.read8(&c.s, ws, format, cache, bt, sl, first, off, T, k, v, step, st); };
+    });
+}
+
+// (shape, ws, format, q, byte_cache, block_table, seq_lens, o, lse, window, sinks, stream)
+PyObject *byte_decode(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 12, [a] {
+        Call c(a[0]);
+        const int32_t format = int32(a[2], "format");
+        void *ws = c.workspace(a[1]), *q = c.rows(a[3], "q"), *cache = c.codes(a[4]);
+        int32_t *bt = c.table(a[5]), *sl = c.lens(a[6]);
+        void *o = c.rows(a[7], "o");
+        float *lse = c.lse(a[8]);
+        const bool whole = a[9] == Py_None;
+        const pkv_window_t win = {whole ? 0 : int32(a[9], "window"), int32(a[10], "sinks")};
+        void *st = c.stream(a[11]);
+        return [=] { return lib.decode8(&c.s, whole ? nullptr : &win, ws, format, q, cache, bt, sl, o, lse, st); };
+    });
+}
+
+// Addresses of pkv_attn_workspace_size, pkv_quant_append, pkv_quant_read, pkv_quant_decode, pkv_window_decode,
+// pkv_map_pages, pkv_append_slots, pkv_byte_append, pkv_byte_read, pkv_byte_decode
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    void *p[5];
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "five addresses");
+    void *p[10];
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "ten addresses");
         return nullptr;
     }
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 10; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred())
@@ -275,6 +389,11 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     lib.read = reinterpret_cast<decltype(lib.read)>(p[2]);
     lib.quant = reinterpret_cast<decltype(lib.quant)>(p[3]);
     lib.window = reinterpret_cast<decltype(lib.window)>(p[4]);
+    lib.map = reinterpret_cast<decltype(lib.map)>(p[5]);
+    lib.slots = reinterpret_cast<decltype(lib.slots)>(p[6]);
+    lib.append8 = reinterpret_cast<decltype(lib.append8)>(p[7]);
+    lib.read8 = reinterpret_cast<decltype(lib.read8)>(p[8]);
+    lib.decode8 = reinterpret_cast<decltype(lib.decode8)>(p[9]);
     Py_RETURN_NONE;
 }
 
@@ -285,6 +404,11 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"quant_read", fast(quant_read), METH_FASTCALL, nullptr},
                          {"quant_decode", fast(quant_decode), METH_FASTCALL, nullptr},
                          {"window_decode", fast(window_decode), METH_FASTCALL, nullptr},
+                         {"map_pages", fast(map_pages), METH_FASTCALL, nullptr},
+                         {"append_slots", fast(append_slots), METH_FASTCALL, nullptr},
+                         {"byte_append", fast(byte_append), METH_FASTCALL, nullptr},
+                         {"byte_read", fast(byte_read), METH_FASTCALL, nullptr},
+                         {"byte_decode", fast(byte_decode), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,407 @@
+// byte.cu -- writing the 8-bit KV cache and reading it back.
+//
+// append: K and V of new tokens, packed [T][Hkv][d] fp16 with a stride between
+// tokens, become codes in the pages their rows' block tables name, at positions
+// seq_lens[i] .. ; lengths advance once every CTA has read them.
+// read: tokens of the cache become packed fp16 K and V again.
+//
+// Both are one pass over their data: append reads 2 bytes per value and writes
+// one, read the other way round.
+//
+// A warp takes a scale block (16 tokens, 8 in pages of 8) of one head and side at
+// a time: a lane holds 8 dims of 8 or 4 neighbouring tokens, so that the block's
+// greatest magnitude is one reduction over the warp, a token's codes are 8 bytes
+// of a K row, and four tokens' are two whole pieces of V after a transposition in
+// registers.  Rows, pages and offsets are looked up once for all of a block's
+// heads and sides; short calls split those over more warps.
+#include "append_rows.cuh"
+#include "byte_format.cuh"
+
+#include <type_traits>
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCtas = 3;  // per SM
+
+// Which tokens and dims of a block of 2^LG tokens a lane holds: dims 8 piece ..,
+// tokens first .. first + kTokens - 1 (none where `first` is beyond the block).
+template <int D, int LG>
+struct Lane {
+    static constexpr int kPieces = D / 8, kGroups = 32 / kPieces;
+    static constexpr int kTokens = (1 << LG) / kGroups < 4 ? 4 : (1 << LG) / kGroups;
+    const int piece, first;
+    __device__ __forceinline__ Lane() : piece((threadIdx.x & 31) % kPieces), first((threadIdx.x & 31) / kPieces * kTokens) {}
+    __device__ __forceinline__ bool any() const { return kTokens * kGroups == 1 << LG || first < 1 << LG; }
+};
+
+__device__ __forceinline__ uint32_t greatest(uint4 x)
+{
+    const __half2 a = __hmax2_nan(__hmax2_nan(__habs2(byte_half2(x.x)), __habs2(byte_half2(x.y))),
+                                  __hmax2_nan(__habs2(byte_half2(x.z)), __habs2(byte_half2(x.w))));
+    return max((uint32_t)__half_as_ushort(__low2half(a)), (uint32_t)__half_as_ushort(__high2half(a)));
+}
+
+constexpr uint32_t kInf = 0x7c00u;
+constexpr uint32_t kNanBits = 0x7fffffffu;
+
+// A block's scale after tokens with the greatest magnitude `top` have joined
+// those it holds under the scale `was` (any: whether it holds some).
+template <int FMT>
+struct NewScale {
+    int e, grow;  // grow: how far the earlier codes have to be shifted, 0 for not at all
+    float s;
+    __device__ __forceinline__ NewScale(uint32_t top, bool any, float was)
+    {
+        e = byte_least_exponent<FMT>(top > kInf ? kInf : top);
+        grow = 0;
+        const bool nan = top > kInf || (any && was != was);
+        if (any) {
+            const int e0 = byte_exponent<FMT>(was);
+            if (e > e0 && !nan)
+                grow = e - e0;
+            e = max(e, e0);
+        }
+        s = nan ? __uint_as_float(kNanBits) : byte_pow2(e);
+    }
+};
+
+// A scale block (2^LG positions from pos0 on, the first token's place in its
+// page's block r0) for some of the heads' sides (2 h: K, 2 h + 1: V), then the
+// next such unit a grid further on.
+template <int D, int FMT, int LG>
+__global__ void __launch_bounds__(kThreads, kCtas) byte_append_kernel(const QuantAppendParams p)
+{
+    using Ln = Lane<D, LG>;
+    constexpr int TL = Ln::kTokens;
+    __shared__ int s_seen;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const Ln ln;
+    const int tb = 1 << p.tb_log2;
+    // what the last CTA needs of its first rows, on its way already
+    int my_off = 0, my_n = 0, my_N = 0;
+    if ((int)threadIdx.x < p.B) {
+        my_off = p.offsets[threadIdx.x];
+        my_n = p.offsets[threadIdx.x + 1] - my_off;
+        my_N = p.seq_lens[threadIdx.x];
+    }
+    bool bad = false;
+    // a warp keeps its part of the heads' sides (those left over when the parts do not divide the warps stay idle)
+    const unsigned warp = blockIdx.x * kWarps + (threadIdx.x >> 5), lines = gridDim.x * kWarps / (unsigned)p.parts;
+    const unsigned line = warp / (unsigned)p.parts;
+    const int it0 = (int)(warp - line * p.parts) * p.its_per_part, it1 = min(it0 + p.its_per_part, 2 * p.Hkv);
+    for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
+        const int i = min(last_not_above(p.B, gs, [&](int r) { return append_first_group(p.offsets[r], r, LG); }), p.B - 1);
+        const int off = p.offsets[i], n = p.offsets[i + 1] - off;
+        const int N = p.seq_lens[i];
+        int64_t pos0;
+        if (!append_group(gs, i, off, n, N, pos0, LG) || !append_fits(p, i, N, off, n, false))
+            continue;
+        const int page = p.bt[(int64_t)i * p.bt_stride + (pos0 >> p.log2P)];
+        if (page < 0 || page >= p.num_pages) {
+            if (lane == 0)
+                report_error(p.ws, kErrBadPage, i, (int)(pos0 >> p.log2P), page);
+            bad = true;
+            continue;
+        }
+        const int slot = (int)pos0 & ((1 << p.log2P) - 1), r0 = slot & (tb - 1);
+        uint8_t *blk = p.cache + (int64_t)page * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * byte_block_bytes(tb, D);
+        const int first = (int)pos0 + ln.first;  // of this lane's positions; the row's end is an int
+        const bool held = pos0 < N;              // the block has earlier tokens
+        const int64_t from = (int64_t)off * p.new_stride + 8 * ln.piece;
+        for (int it = it0; it < it1; ++it) {
+            const int h = it >> 1;
+            const bool v = it & 1;
+            uint8_t *hb = blk + h * p.page_head_bytes;
+            float *scale = reinterpret_cast<float *>(hb + byte_scale_part<D>(tb, r0, LG)) + v;
+            uint4 x[TL];
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < TL; ++u) {
+                const int pos = first + u;
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (ln.any() && pos >= N && pos < N + n)
+                    x[u] = *reinterpret_cast<const uint4 *>((v ? p.v_new : p.k_new) + from + (int64_t)(pos - N) * p.new_stride + h * D);
+            }
+            const float was = held ? *scale : 0.f;
+#pragma unroll
+            for (int u = 0; u < TL; ++u)
+                top = max(top, greatest(x[u]));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const NewScale<FMT> ns(top, held, was);
+            const ByteQuantiser<FMT> code(ns.e, top);
+            if (ln.any()) {
+                if (!v) {
+#pragma unroll
+                    for (int u = 0; u < TL; ++u) {
+                        const int pos = first + u;
+                        uint2 *to = reinterpret_cast<uint2 *>(hb + byte_k_at<D>(r0 + ln.first + u, 8 * ln.piece));
+                        if (pos >= N && pos < N + n) {
+                            *to = make_uint2(code(x[u].x, x[u].y), code(x[u].z, x[u].w));
+                        } else if (pos < N && ns.grow) {
+                            const uint2 c = *to;
+                            *to = make_uint2(byte_shift<FMT>(c.x, -ns.grow), byte_shift<FMT>(c.y, -ns.grow));
+                        }
+                    }
+                } else {
+                    uint8_t *part = hb + byte_v_part<D>(tb, r0, LG);
+#pragma unroll
+                    for (int q = 0; q < TL; q += 4) {
+                        const int pos = first + q;
+                        if (pos >= N + n || (pos + 4 <= N && !ns.grow))
+                            continue;
+                        uint4 lo = byte_transpose(code(x[q].x, x[q].y), code(x[q + 1].x, x[q + 1].y), code(x[q + 2].x, x[q + 2].y),
+                                                code(x[q + 3].x, x[q + 3].y));
+                        uint4 hi = byte_transpose(code(x[q].z, x[q].w), code(x[q + 1].z, x[q + 1].w), code(x[q + 2].z, x[q + 2].w),
+                                                code(x[q + 3].z, x[q + 3].w));
+                        uint4 *to = reinterpret_cast<uint4 *>(part + byte_v_at(2 * ln.piece, (ln.first + q) >> 2, LG));
+                        uint4 *to2 = reinterpret_cast<uint4 *>(part + byte_v_at(2 * ln.piece + 1, (ln.first + q) >> 2, LG));
+                        if (pos < N) {  // earlier tokens' bytes stay
+                            const uint32_t keep = 0xffffffffu >> (8 * max(pos + 4 - N, 0));
+                            const uint32_t all = pos + 4 <= N ? 0xffffffffu : keep;
+                            auto join = [&](uint32_t now, uint32_t old) {
+                                if (ns.grow)
+                                    old = byte_shift<FMT>(old, -ns.grow);
+                                return (old & all) | (now & ~all);
+                            };
+                            const uint4 a = *to, b = *to2;
+                            lo = make_uint4(join(lo.x, a.x), join(lo.y, a.y), join(lo.z, a.z), join(lo.w, a.w));
+                            hi = make_uint4(join(hi.x, b.x), join(hi.y, b.y), join(hi.z, b.z), join(hi.w, b.w));
+                        }
+                        *to = lo;
+                        *to2 = hi;
+                    }
+                }
+            }
+            if (lane == 0)
+                *scale = ns.s;
+        }
+    }
+    append_finish<kThreads>(p, bad, my_off, my_n, my_N, &s_seen);
+}
+
+// One new token per row: a CTA per row, which alone reads and advances its
+// length; a warp (d = 64: half a warp) takes a head's side, a lane four dims.
+template <int D, int FMT, int LG>
+__global__ void __launch_bounds__(kThreads) byte_append_one_kernel(const QuantAppendParams p)
+{
+    constexpr int kLanes = D / 4, kPer = 32 / kLanes;  // of a head's side, and sides per warp
+    pdl_wait();
+    pdl_trigger();
+    const int i = blockIdx.x, l = (threadIdx.x & 31) % kLanes;
+    const int N = p.seq_lens[i];
+    int page = -1;
+    if (N < 0 || N >= p.len_cap) {
+        if (threadIdx.x == 0)
+            report_error(p.ws, N < 0 ? kErrNegLen : kErrTooLong, i, N < 0 ? N : (int)min((int64_t)N + 1, (int64_t)0x7fffffff),
+                         N < 0 ? 0 : p.len_cap);
+    } else {
+        page = p.bt[(int64_t)i * p.bt_stride + (N >> p.log2P)];
+        if (page < 0 || page >= p.num_pages) {
+            if (threadIdx.x == 0)
+                report_error(p.ws, kErrBadPage, i, N >> p.log2P, page);
+            page = -1;
+        }
+    }
+    const int tb = 1 << p.tb_log2, slot = N & ((1 << p.log2P) - 1), r = slot & (tb - 1), u = r & ((1 << LG) - 1);
+    uint8_t *blk = p.cache + (int64_t)max(page, 0) * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * byte_block_bytes(tb, D);
+    const int at = (int)threadIdx.x / kLanes, step = (int)blockDim.x / kLanes;
+    for (int it = at - at % kPer; it < 2 * p.Hkv && page >= 0; it += step) {
+        const int mine = it + at % kPer, h = mine >> 1;
+        const bool there = mine < 2 * p.Hkv, v = mine & 1;
+        uint8_t *hb = blk + (int64_t)(there ? h : 0) * p.page_head_bytes;
+        float *scale = reinterpret_cast<float *>(hb + byte_scale_part<D>(tb, r, LG)) + v;
+        uint2 x = make_uint2(0, 0);
+        if (there)
+            x = *reinterpret_cast<const uint2 *>((v ? p.v_new : p.k_new) + (int64_t)i * p.new_stride + h * D + 4 * l);
+        const float was = there && u > 0 ? *scale : 0.f;
+        uint32_t top = greatest(make_uint4(x.x, x.y, 0, 0));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const NewScale<FMT> ns(top, u > 0, was);
+        const uint32_t c = ByteQuantiser<FMT>(ns.e, top)(x.x, x.y);
+        if (!there)
+            continue;
+        if (!v) {
+            if (ns.grow)
+                for (int o = r - u; o < r; ++o) {
+                    uint32_t *to = reinterpret_cast<uint32_t *>(hb + byte_k_at<D>(o, 4 * l));
+                    *to = byte_shift<FMT>(*to, -ns.grow);
+                }
+            *reinterpret_cast<uint32_t *>(hb + byte_k_at<D>(r, 4 * l)) = c;
+        } else {
+            uint8_t *part = hb + byte_v_part<D>(tb, r, LG);
+            if (ns.grow)
+                for (int t = 0; 4 * t < u; ++t) {
+                    uint4 *to = reinterpret_cast<uint4 *>(part + byte_v_at(l, t, LG));
+                    const uint4 w = *to;
+                    *to = make_uint4(byte_shift<FMT>(w.x, -ns.grow), byte_shift<FMT>(w.y, -ns.grow), byte_shift<FMT>(w.z, -ns.grow),
+                                     byte_shift<FMT>(w.w, -ns.grow));
+                }
+            uint8_t *to = part + byte_v_at(l, u >> 2, LG) + (u & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                to[4 * j] = (uint8_t)(c >> (8 * j));
+        }
+        if (l == 0)
+            *scale = ns.s;
+    }
+    __syncthreads();  // every thread has read N before it changes
+    if (threadIdx.x == 0)
+        p.seq_lens_out[i] = page >= 0 ? N + 1 : N;
+}
+
+// A scale block of a row for some of the heads' sides, as the append takes them:
+// its tokens among those that the row's span wants.
+template <int D, int FMT, int LG>
+__global__ void __launch_bounds__(kThreads, kCtas) byte_read_kernel(const QuantReadParams p)
+{
+    using Ln = Lane<D, LG>;
+    constexpr int TL = Ln::kTokens;
+    pdl_wait();
+    pdl_trigger();
+    const Ln ln;
+    const int tb = 1 << p.tb_log2;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), gs = unit / p.parts;
+    const int part_no = (int)(unit - gs * p.parts), it0 = part_no * p.heads_per_part, it1 = min(it0 + p.heads_per_part, 2 * p.Hkv);
+    if (gs >= p.groups)
+        return;
+    const int i = min(last_not_above(p.B, gs, [&](int r) { return append_first_group(p.offsets[r], r, LG); }), p.B - 1);
+    const int off = p.offsets[i], n = p.offsets[i + 1] - off, begin = p.first ? p.first[i] : 0;
+    int64_t pos0;
+    if (off < 0 || (int64_t)off + n > p.T || !append_group(gs, i, off, n, begin, pos0, LG))
+        return;  // offsets that do not ascend within the buffer have no tokens here
+    const int N = min(p.seq_lens[i], p.len_cap);
+    const int64_t from = max(pos0, (int64_t)begin), to = min(pos0 + (1 << LG), (int64_t)begin + n);
+    int page = -1;
+    if (pos0 >= 0 && from < N) {
+        page = p.bt[(int64_t)i * p.bt_stride + (pos0 >> p.log2P)];
+        if (page < 0 || page >= p.num_pages) {
+            if (part_no == 0 && (threadIdx.x & 31) == 0)
+                report_error(p.ws, kErrBadPage, i, (int)(pos0 >> p.log2P), page);
+            page = -1;
+        }
+    }
+    if ((from < 0 || to > N) && part_no == 0 && (threadIdx.x & 31) == 0)
+        report_error(p.ws, kErrTooLong, i, (int)(from < 0 ? max(from + 1, (int64_t)-0x7fffffff) : min(to, (int64_t)0x7fffffff)), N);
+    if (!ln.any())
+        return;
+    const int slot = (int)pos0 & ((1 << p.log2P) - 1), r0 = slot & (tb - 1);
+    const uint8_t *blk = p.cache + (int64_t)max(page, 0) * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * byte_block_bytes(tb, D);
+    const int64_t mine = pos0 + ln.first;  // this lane's first position
+    for (int it = it0; it < it1; ++it) {
+        const int h = it >> 1;
+        const bool v = it & 1;
+        const uint8_t *hb = blk + h * p.page_head_bytes;
+        __half *out = (v ? p.v_out : p.k_out) + h * D + 8 * ln.piece;
+        uint2 c[TL];
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < TL; ++u)
+            c[u] = make_uint2(0, 0);
+        if (page >= 0) {
+            s = reinterpret_cast<const float *>(hb + byte_scale_part<D>(tb, r0, LG))[v];
+            if (!v) {
+#pragma unroll
+                for (int u = 0; u < TL; ++u)
+                    c[u] = *reinterpret_cast<const uint2 *>(hb + byte_k_at<D>(r0 + ln.first + u, 8 * ln.piece));
+            } else {
+                const uint8_t *part = hb + byte_v_part<D>(tb, r0, LG);
+#pragma unroll
+                for (int q = 0; q < TL; q += 4) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(part + byte_v_at(2 * ln.piece, (ln.first + q) >> 2, LG));
+                    const uint4 b = *reinterpret_cast<const uint4 *>(part + byte_v_at(2 * ln.piece + 1, (ln.first + q) >> 2, LG));
+                    const uint4 lo = byte_transpose(a.x, a.y, a.z, a.w), hi = byte_transpose(b.x, b.y, b.z, b.w);
+                    c[q] = make_uint2(lo.x, hi.x);
+                    c[q + 1] = make_uint2(lo.y, hi.y);
+                    c[q + 2] = make_uint2(lo.z, hi.z);
+                    c[q + 3] = make_uint2(lo.w, hi.w);
+                }
+            }
+        }
+        // the scale is an fp16 number too, and so are the products
+        const __half2 s2 = __float2half2_rn(s != s ? s : byte_pow2(byte_exponent<FMT>(s) + kByteShift<FMT>));
+        auto value = [&](uint32_t w, uint32_t &lo, uint32_t &hi) {
+            uint32_t even, odd;
+            byte_numbers<FMT>(w, even, odd);
+            even = byte_word(__hmul2(byte_half2(even), s2));
+            odd = byte_word(__hmul2(byte_half2(odd), s2));
+            lo = __byte_perm(even, odd, 0x5410);
+            hi = __byte_perm(even, odd, 0x7632);
+        };
+#pragma unroll
+        for (int u = 0; u < TL; ++u) {
+            const int64_t pos = mine + u;
+            if (pos < from || pos >= to)
+                continue;
+            uint4 y;
+            value(c[u].x, y.x, y.y);
+            value(c[u].y, y.z, y.w);
+            if (pos >= N)
+                y = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(out + (off + (pos - begin)) * p.out_stride) = y;
+        }
+    }
+}
+
+template <class K, class P>
+cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, int FMT, int LG>
+cudaError_t launch_append(QuantAppendParams p, int sms, cudaStream_t s)
+{
+    if (!p.offsets) {
+        const int warps = (2 * p.Hkv * D + 127) / 128;
+        return launch(byte_append_one_kernel<D, FMT, LG>, p, p.B, 32 * (warps < kWarps ? warps : kWarps), s);
+    }
+    const int64_t grid = append_grid(p.T, p.B, p.Hkv, kCtas * sms, kWarps, p.groups, p.parts, p.its_per_part, LG);
+    return launch(byte_append_kernel<D, FMT, LG>, p, grid, kThreads, s);
+}
+
+template <int D, int FMT, int LG>
+cudaError_t launch_read(QuantReadParams p, int sms, cudaStream_t s)
+{
+    p.groups = append_groups(p.T, p.B, LG);
+    p.parts = split_work(p.groups, 2 * p.Hkv, (int64_t)4 * kCtas * kWarps * sms, INT64_MAX, p.heads_per_part);
+    return launch(byte_read_kernel<D, FMT, LG>, p, (p.groups * p.parts + kWarps - 1) / kWarps, kThreads, s);
+}
+
+// f<D, FMT, LG>() for the call's d, format and page size.
+template <class F>
+cudaError_t pick(int d, int fmt, int log2P, F f)
+{
+    auto page = [&](auto D, auto FMT) { return log2P == 3 ? f(D, FMT, std::integral_constant<int, 3>()) : f(D, FMT, std::integral_constant<int, 4>()); };
+    auto format = [&](auto D) { return fmt == kInt8 ? page(D, std::integral_constant<int, kInt8>()) : page(D, std::integral_constant<int, kE4m3>()); };
+    return d == 128 ? format(std::integral_constant<int, 128>()) : format(std::integral_constant<int, 64>());
+}
+
+}  // namespace
+
+cudaError_t launch_byte_append(int d, int fmt, const QuantAppendParams &p, int sms, cudaStream_t s)
+{
+    return pick(d, fmt, p.log2P, [&](auto D, auto FMT, auto LG) { return launch_append<D(), FMT(), LG()>(p, sms, s); });
+}
+
+cudaError_t launch_byte_read(int d, int fmt, const QuantReadParams &p, int sms, cudaStream_t s)
+{
+    return pick(d, fmt, p.log2P, [&](auto D, auto FMT, auto LG) { return launch_read<D(), FMT(), LG()>(p, sms, s); });
+}
+
+}  // namespace pkv

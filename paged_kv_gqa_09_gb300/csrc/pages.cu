@@ -1,0 +1,334 @@
+// pages.cu -- pages and slots for new tokens, and the fp16 append that goes by slots.
+//
+// map: row i holds N tokens in have = ceil(N / P) pages and gets n more, so that
+// it lacks need = ceil((N + n) / P) - have pages.  With off_i and rank_i the sums
+// of n and need over the rows before, its k-th new token is packed token off_i + k
+// and its j-th new page free_pages[count - 1 - rank_i - j]: every place follows
+// from two prefix sums over the rows, so every CTA takes those for itself (rows
+// are two ints each, tokens twelve bytes) and one launch without a grid-wide wait
+// does it all.  A page is entered in the block table by the thread of the token
+// at its start.  The last CTA to finish, when every other one has read the lengths
+// and the free count, advances them.
+//
+// slots: K and V of packed tokens go to their slots, 16 bytes a lane: a copy.
+#include "pkv_device.cuh"
+#include "pkv_kernels.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kMapThreads = 512;
+constexpr int kMapWarps = kMapThreads / 32;
+constexpr int kMapRows = 2 * kMapThreads;  // rows whose sums a CTA holds at a time
+constexpr int kInvalid = -2;               // in place of a row's rank: no length that the table could hold
+constexpr int kNotServed = -1;             // no pages left for it, or no room in the packed buffer
+constexpr int kBadCta = 1 << 20;           // CTAs that met a bad page count this much more
+
+// The rows [c0, c0 + kMapRows) as the map sees them: two of them per thread, and
+// what the tokens need of all of them in shared memory.
+struct MapRows {
+    int off[kMapRows + 1];  // first packed token, at most T
+    int len[kMapRows];      // N
+    int rank[kMapRows];     // pages that the rows before need, or one of the above
+    long long sum[2][kMapWarps];
+};
+
+struct MapRow {
+    int N, n, need, rank;  // as above
+    int status;            // DevErr, kErrNone when it is served
+    int off;               // at most T
+};
+
+__device__ __forceinline__ int pages_of(const MapParams &p, int N) { return (N >> p.log2P) + ((N & ((1 << p.log2P) - 1)) != 0); }
+
+// Rows c0 + 2 tid and the next of this thread; off0 and rank0 are the sums over
+// the rows before c0 and become those over the rows before the next chunk's.
+__device__ __forceinline__ void map_rows(const MapParams &p, int c0, int count, MapRows &s, MapRow (&row)[2], long long &off0,
+                                         long long &rank0)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    long long n2[2], need2[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = c0 + 2 * (int)threadIdx.x + u;
+        MapRow &r = row[u];
+        r.N = i < p.B ? p.seq_lens[i] : 0;
+        r.n = i < p.B ? p.new_lens[i] : 0;
+        r.status = r.N < 0 || r.n < 0 ? kErrNegLen : (long long)r.N + r.n > p.len_cap ? kErrTooLong : kErrNone;
+        r.n = max(r.n, 0);
+        r.need = r.status == kErrNone ? pages_of(p, r.N + r.n) - pages_of(p, r.N) : 0;
+        n2[u] = r.n;
+        need2[u] = r.need;
+    }
+    long long a = n2[0] + n2[1], b = need2[0] + need2[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+            a += x;
+            b += y;
+        }
+    }
+    if (lane == 31) {
+        s.sum[0][w] = a;
+        s.sum[1][w] = b;
+    }
+    __syncthreads();
+    long long off = off0 + a - n2[0] - n2[1], rank = rank0 + b - need2[0] - need2[1];
+#pragma unroll
+    for (int v = 0; v < kMapWarps; ++v) {
+        const long long x = s.sum[0][v], y = s.sum[1][v];
+        off += v < w ? x : 0;
+        rank += v < w ? y : 0;
+        off0 += x;
+        rank0 += y;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        MapRow &r = row[u];
+        const int x = 2 * (int)threadIdx.x + u;
+        r.off = (int)min(off, (long long)p.T);
+        if (r.status == kErrNone && off + r.n > p.T)
+            r.status = kErrBadSpan;
+        if (r.status == kErrNone && r.need > 0 && rank + r.need > count)
+            r.status = kErrNoPage;
+        r.rank = r.status == kErrNone ? (int)min(rank, 0x7fffffffll)
+                                      : r.status == kErrNoPage || r.status == kErrBadSpan ? kNotServed : kInvalid;
+        s.off[x] = r.off;
+        s.len[x] = r.N;
+        s.rank[x] = r.rank;
+        if (x == kMapRows - 1)
+            s.off[kMapRows] = (int)min(off + n2[u], (long long)p.T);
+        off += n2[u];
+        rank += need2[u];
+    }
+    __syncthreads();
+}
+
+// The lengths and the free count after the call, of the rows map_rows() has
+// just seen; `pages_bad`: some page id was out of range, so those are looked for.
+__device__ __forceinline__ void map_finish(const MapParams &p, int c0, int count, bool pages_bad, const MapRow (&row)[2], int *s_taken)
+{
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = c0 + 2 * (int)threadIdx.x + u;
+        if (i >= p.B)
+            continue;
+        const MapRow &r = row[u];
+        bool ok = r.status == kErrNone;
+        if (r.status == kErrNegLen)
+            report_error(p.ws, kErrNegLen, i, r.N < 0 ? r.N : p.new_lens[i], 0);
+        else if (r.status == kErrTooLong)
+            report_error(p.ws, kErrTooLong, i, (int)min((long long)r.N + r.n, 0x7fffffffll), p.len_cap);
+        else if (r.status == kErrBadSpan)
+            report_error(p.ws, kErrBadSpan, i, r.off, r.n);
+        else if (r.status == kErrNoPage)
+            report_error(p.ws, kErrNoPage, i, r.N, count);
+        if (ok && r.need > 0)
+            atomicMax(s_taken, r.rank + r.need);
+        if (ok && pages_bad && r.n > 0) {
+            auto good = [&](int page) { return page >= 0 && page < p.num_pages; };
+            const int have = pages_of(p, r.N);
+            if (r.N & ((1 << p.log2P) - 1))
+                ok = good(p.bt[(int64_t)i * p.bt_stride + have - 1]);
+            for (int j = 0; ok && j < r.need; ++j)
+                ok = good(p.free_pages[count - 1 - r.rank - j]);
+        }
+        p.seq_lens_out[i] = ok ? r.N + r.n : r.N;
+    }
+}
+
+__global__ void __launch_bounds__(kMapThreads) map_pages_kernel(const MapParams p)
+{
+    __shared__ MapRows s;
+    __shared__ int s_taken, s_seen;
+    pdl_wait();
+    pdl_trigger();
+    const bool alone = gridDim.x == 1;
+    if (threadIdx.x == 0)
+        s_taken = 0;
+    const int count = min(max(*p.free_count, 0), p.free_cap);
+    // this CTA's tokens [t0, t1), whole groups of four
+    const long long quads = ((long long)p.T + 3) / 4, per = (quads + gridDim.x - 1) / gridDim.x;
+    const int t0 = (int)min(4 * per * blockIdx.x, (long long)p.T), t1 = (int)min(4 * per * (blockIdx.x + 1), (long long)p.T);
+    long long off0 = 0, rank0 = 0;
+    bool bad = false;
+    // Slots and positions of tokens x .. x + 3, of which [lo, hi) are this call's, from `at`.
+    auto store4 = [&](int x, int lo, int hi, auto at) {
+        long long slot[4];
+        int pos[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            slot[u] = -1;
+            pos[u] = 0;
+            if (x + u >= lo && x + u < hi)
+                at(x + u, slot[u], pos[u]);
+        }
+        if (x >= lo && x + 4 <= hi) {
+            reinterpret_cast<longlong2 *>(p.slots + x)[0] = make_longlong2(slot[0], slot[1]);
+            reinterpret_cast<longlong2 *>(p.slots + x)[1] = make_longlong2(slot[2], slot[3]);
+            if (p.positions)
+                *reinterpret_cast<int4 *>(p.positions + x) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (x + u >= lo && x + u < hi) {
+                    p.slots[x + u] = slot[u];
+                    if (p.positions)
+                        p.positions[x + u] = pos[u];
+                }
+        }
+    };
+    for (int c0 = 0; c0 < p.B && (alone || blockIdx.x == 0 || off0 < t1); c0 += kMapRows) {
+        MapRow row[2];
+        map_rows(p, c0, count, s, row, off0, rank0);
+        const int nr = min(p.B - c0, kMapRows);
+        if (blockIdx.x == 0) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (2 * (int)threadIdx.x + u < nr)
+                    p.offsets[c0 + 2 * threadIdx.x + u] = row[u].off;
+        }
+        const int lo = max(t0, s.off[0]), hi = min(t1, s.off[nr]);
+        for (long long q = lo / 4 + threadIdx.x; q * 4 < hi; q += kMapThreads) {
+            const int x0 = (int)q * 4;
+            int r = 0, up = nr - 1;  // the last row at or before the group's first token
+            while (r < up) {
+                const int mid = (r + up + 1) >> 1;
+                if (s.off[mid] <= max(x0, lo))
+                    r = mid;
+                else
+                    up = mid - 1;
+            }
+            store4(x0, lo, hi, [&](int x, long long &slot, int &pos) {
+                while (r + 1 < nr && x >= s.off[r + 1])
+                    ++r;
+                const int N = s.len[r], rank = s.rank[r], at = N + (x - s.off[r]);
+                if (rank == kInvalid)
+                    return;
+                const int blk = at >> p.log2P, in = at & ((1 << p.log2P) - 1), j = blk - pages_of(p, N);
+                int32_t *entry = p.bt + (int64_t)(c0 + r) * p.bt_stride + blk;
+                if (rank == kNotServed) {
+                    if (j >= 0 && in == 0 && blk < p.bt_stride)
+                        *entry = -1;
+                    return;
+                }
+                int page = j < 0 ? *entry : p.free_pages[count - 1 - rank - j];
+                if (page < 0 || page >= p.num_pages) {
+                    report_error(p.ws, kErrBadPage, c0 + r, blk, page);
+                    bad = true;
+                    page = -1;
+                }
+                if (j >= 0 && in == 0)
+                    *entry = page;
+                if (page < 0)
+                    return;
+                slot = ((long long)page << p.log2P) + in;
+                pos = at;
+            });
+        }
+        const bool any_bad = __syncthreads_or(alone && bad) != 0;  // the sums are read until here
+        if (alone)
+            map_finish(p, c0, count, any_bad, row, &s_taken);
+    }
+    if (off0 < t1)  // behind the last token
+        for (long long q = max((long long)t0, off0) / 4 + threadIdx.x; q * 4 < t1; q += kMapThreads)
+            store4((int)q * 4, max(t0, (int)off0), t1, [](int, long long &, int &) {});
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        p.offsets[p.B] = (int)min(off0, (long long)p.T);
+    if (!alone) {
+        const int any_bad = __syncthreads_or(bad ? 1 : 0);
+        if (threadIdx.x == 0) {
+            const int add = any_bad ? 1 + kBadCta : 1;
+            s_seen = atomicAdd(&p.ws->append_done, add) + add;
+        }
+        __syncthreads();
+        if ((s_seen & (kBadCta - 1)) != (int)gridDim.x)
+            return;
+        off0 = rank0 = 0;
+        for (int c0 = 0; c0 < p.B; c0 += kMapRows) {
+            MapRow row[2];
+            map_rows(p, c0, count, s, row, off0, rank0);
+            map_finish(p, c0, count, s_seen >= kBadCta, row, &s_taken);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        *p.free_count_out = count - s_taken;
+        if (!alone)
+            p.ws->append_done = 0;
+    }
+}
+
+constexpr int kSlotThreads = 256;
+constexpr int kSlotBatch = 4;  // 16-byte pieces a lane has in flight
+
+// A warp per packed token, then the next one a grid further on; pieces of K and V in one line.
+__global__ void __launch_bounds__(kSlotThreads) append_slots_kernel(const SlotParams p)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int warps = (int)gridDim.x * (kSlotThreads / 32);
+    for (int64_t x = (int64_t)blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5); x < p.T; x += warps) {
+        const int64_t slot = p.slots[x];
+        if (slot < 0)
+            continue;
+        if (slot >= p.num_slots) {
+            if (lane == 0)
+                report_error(p.ws, kErrBadSlot, (int)x, (int)min(slot, (int64_t)0x7fffffff), (int)min(p.num_slots, (int64_t)0x7fffffff));
+            continue;
+        }
+        for (int c0 = lane; c0 < 2 * p.pieces; c0 += 32 * kSlotBatch) {
+            int4 v[kSlotBatch];
+#pragma unroll
+            for (int u = 0; u < kSlotBatch; ++u) {
+                const int c = c0 + 32 * u;
+                if (c < 2 * p.pieces)
+                    v[u] = c < p.pieces ? reinterpret_cast<const int4 *>(p.k_new + x * p.new_stride)[c]
+                                        : reinterpret_cast<const int4 *>(p.v_new + x * p.new_stride)[c - p.pieces];
+            }
+#pragma unroll
+            for (int u = 0; u < kSlotBatch; ++u) {
+                const int c = c0 + 32 * u;
+                if (c < 2 * p.pieces) {
+                    if (c < p.pieces)
+                        reinterpret_cast<int4 *>(p.k_cache)[slot * p.pieces + c] = v[u];
+                    else
+                        reinterpret_cast<int4 *>(p.v_cache)[slot * p.pieces + c - p.pieces] = v[u];
+                }
+            }
+        }
+    }
+}
+
+template <class K, class P>
+cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid > 0 ? grid : 1));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_map_pages(const MapParams &p, int sms, cudaStream_t s)
+{
+    const int64_t want = ((int64_t)p.T + 4 * kMapThreads - 1) / (4 * kMapThreads), most = 2 * (int64_t)sms;
+    return launch(map_pages_kernel, p, want < most ? want : most, kMapThreads, s);
+}
+
+cudaError_t launch_append_slots(const SlotParams &p, int sms, cudaStream_t s)
+{
+    const int64_t want = ((int64_t)p.T + kSlotThreads / 32 - 1) / (kSlotThreads / 32), most = 8 * (int64_t)sms;
+    return launch(append_slots_kernel, p, want < most ? want : most, kSlotThreads, s);
+}
+
+}  // namespace pkv

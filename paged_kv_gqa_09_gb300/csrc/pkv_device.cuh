@@ -23,6 +23,7 @@ enum DevErr : int32_t {
     kErrBadRow = 6,    // a row list entry outside [0, B): that row skipped
     kErrNoPage = 7,    // the free list ran out: that row's token not appended
     kErrBadSpan = 8,   // a row's packed tokens outside the packed buffer: row not appended
+    kErrBadSlot = 9,   // a slot beyond the pool: that token not written
 };
 
 // First 64 bytes of the plan workspace.

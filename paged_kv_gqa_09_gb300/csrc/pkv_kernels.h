@@ -142,14 +142,39 @@ struct QuantReadParams {
     WsHeader *ws;
     int64_t page_head_bytes;
     int T, B, Hkv, log2P, tb_log2, num_pages, bt_stride, len_cap;
-    int parts, heads_per_part;  // set by the launcher
+    int parts, heads_per_part;  // set by the launcher; of the 8-bit cache heads' sides
+    int64_t groups;             // 8-bit cache: scale blocks, set by the launcher
+};
+
+// Pages and slots of new tokens (pages.cu).
+struct MapParams {
+    const int32_t *seq_lens, *new_lens;
+    int32_t *seq_lens_out;      // may be seq_lens
+    int32_t *bt;
+    const int32_t *free_pages, *free_count;
+    int32_t *free_count_out;    // may be free_count
+    int32_t *offsets;           // [B + 1]
+    int64_t *slots;             // [T]
+    int32_t *positions;         // [T], nullable
+    WsHeader *ws;
+    int T, B, log2P, num_pages, bt_stride, len_cap, free_cap;
+};
+
+struct SlotParams {
+    const __half *k_new, *v_new;
+    int64_t new_stride;
+    const int64_t *slots;  // [T]
+    __half *k_cache, *v_cache;
+    WsHeader *ws;
+    int64_t num_slots;
+    int T, pieces;         // 16-byte pieces of a token, all heads
 };
 
 // Decode attention over the tokens [0, sinks) and [N - window, N) of each row.
 struct AttendParams {
     const __half *q;
     const int32_t *bt, *seq_lens;
-    const uint8_t *cache;     // the 4-bit cache (nullptr: fp16 pages, through the tensor maps)
+    const uint8_t *cache;     // the 4-bit or 8-bit cache (nullptr: fp16 pages, through the tensor maps)
     WsHeader *ws;
     int32_t *counters;        // [kAttnMaxSegs], zero between launches
     float *partials;
@@ -165,8 +190,14 @@ struct AttendParams {
 
 cudaError_t launch_quant_append(int d, QuantAppendParams p, int sms, cudaStream_t s);
 cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s);
+cudaError_t launch_byte_append(int d, int fmt, const QuantAppendParams &p, int sms, cudaStream_t s);
+cudaError_t launch_byte_read(int d, int fmt, const QuantReadParams &p, int sms, cudaStream_t s);
+cudaError_t launch_map_pages(const MapParams &p, int sms, cudaStream_t s);
+cudaError_t launch_append_slots(const SlotParams &p, int sms, cudaStream_t s);
 cudaError_t launch_attend(int d, const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms,
                           cudaStream_t s);
+cudaError_t launch_attend_int8(int d, const AttendParams &p, int sms, cudaStream_t s);
+cudaError_t launch_attend_e4m3(int d, const AttendParams &p, int sms, cudaStream_t s);
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t s, bool pdl);
 cudaError_t launch_decode(int d, int mode, const CUtensorMap &tk, const CUtensorMap &tv,

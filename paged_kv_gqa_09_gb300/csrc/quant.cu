@@ -20,7 +20,7 @@
 // (two instructions per value, 65 against 62 us when this was tried), four bytes
 // at a time many L1 lookups (d = 64: 39.2 against 37.7 us).  read does make that
 // exchange, since four-byte stores would reach L2 one by one.
-#include "append_map.cuh"
+#include "append_rows.cuh"
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "quant_format.cuh"
@@ -33,24 +33,6 @@ constexpr int kWarps = kThreads / 32;
 // CTAs per SM of the append: with 80 registers a thread 49.6 us (42k tokens of 8
 // heads), with the 64 of four CTAs 55.3 us, with two CTAs 53.7 us.
 constexpr int kAppendCtas = 3;
-
-// The last i in [0, B] with key(i) <= x, for ascending key with key(0) <= x;
-// whole warps only, with one x: 33 keys at a time, so that up to 32 rows take
-// one round trip.
-template <class F>
-__device__ __forceinline__ int last_not_above(int B, int64_t x, F key)
-{
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = B;  // the answer is in [lo, lo + n]
-    while (n > 0) {
-        const int step = (n + 31) / 32, at = lo + (lane + 1) * step;  // lo + step, lo + 2 step, ..
-        const unsigned m = __ballot_sync(0xffffffffu, at <= lo + n && key(at) <= x);
-        const int up = __popc(m) * step;
-        lo += up;
-        n = min(n - up, step - 1);
-    }
-    return lo;
-}
 
 // Row of packed token x, offsets[0] <= x < offsets[B]: the last i in [0, B) with offsets[i] <= x.
 __device__ __forceinline__ int row_of(const int32_t *offsets, int B, int x)
@@ -127,26 +109,6 @@ __device__ __forceinline__ float rcp_approx(float x)
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half lo, __half hi) { return as_word(__halves2half2(lo, hi)); }
-
-// Whether row i's n new tokens, packed from `off` on, are inside the packed
-// buffer and fit behind its N tokens; what is wrong with the length goes to the
-// error word when `report` is set.
-__device__ __forceinline__ bool append_fits(const QuantAppendParams &p, int i, int N, int off, int n, bool report)
-{
-    if (n < 0 || off < 0 || (int64_t)off + n > p.T)
-        return false;
-    if (N < 0) {
-        if (report)
-            report_error(p.ws, kErrNegLen, i, N, 0);
-        return false;
-    }
-    if ((int64_t)N + n > p.len_cap) {
-        if (report)
-            report_error(p.ws, kErrTooLong, i, (int)min((int64_t)N + n, (int64_t)0x7fffffff), p.len_cap);
-        return false;
-    }
-    return true;
-}
 
 // The four code pairs of quantise_rows() below, decided exactly; out of line, so
 // that the loop around it stays small.  y is near enough to tell the two codes
@@ -448,43 +410,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) quant_append_kernel(con
             }
         }
     }
-    // the last CTA to get here advances the lengths, which every other one has
-    // read by then; CTAs that met a bad page are counted above kBad
-    constexpr int kBad = 1 << 20;
-    const int any_bad = __syncthreads_or(bad ? 1 : 0);
-    if (threadIdx.x == 0) {
-        const int add = any_bad ? 1 + kBad : 1;
-        s_seen = atomicAdd(&p.ws->append_done, add) + add;
-    }
-    __syncthreads();
-    if ((s_seen & (kBad - 1)) != (int)gridDim.x)
-        return;
-    const bool pages_bad = s_seen >= kBad;  // then the rows that met them are looked for again
-    // offsets that do not ascend within the buffer give tokens to no row or to two: the whole call is refused
-    bool span = false;
-    for (int r = threadIdx.x; r < p.B; r += kThreads) {
-        const bool first = r < kThreads;
-        const int off = first ? my_off : p.offsets[r], nr = first ? my_n : p.offsets[r + 1] - off;
-        if (off < 0 || nr < 0 || (int64_t)off + nr > p.T) {
-            report_error(p.ws, kErrBadSpan, r, off, nr);
-            span = true;
-        }
-    }
-    span = __syncthreads_or(span ? 1 : 0) != 0;
-    for (int r = threadIdx.x; r < p.B; r += kThreads) {
-        const bool first = r < kThreads;
-        const int Nr = first ? my_N : p.seq_lens[r];
-        const int off = first ? my_off : p.offsets[r], nr = first ? my_n : p.offsets[r + 1] - off;
-        bool ok = !span && append_fits(p, r, Nr, off, nr, true);
-        if (pages_bad && ok && nr > 0)
-            for (int64_t b = Nr >> p.log2P; b <= ((int64_t)Nr + nr - 1) >> p.log2P; ++b) {
-                const int page = p.bt[(int64_t)r * p.bt_stride + b];
-                ok = ok && page >= 0 && page < p.num_pages;
-            }
-        p.seq_lens_out[r] = ok ? Nr + nr : Nr;
-    }
-    if (threadIdx.x == 0)
-        p.ws->append_done = 0;
+    append_finish<kThreads>(p, bad, my_off, my_n, my_N, &s_seen);
 }
 
 // A warp takes eight packed tokens, one per quad, and heads [h0, h0 + nh).  A
