@@ -490,7 +490,7 @@ int pkv_window_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d
  *   *d_free_count_out = what is left (it may be d_free_count).
  * Entries of slot_map and positions behind the last token, up to total_new, are
  * -1 and 0, so that a call captured for total_new tokens serves fewer.
- * A row is refused whole, and the error word records the first that is, when it
+ * A row is refused whole, and the error word records one that is, when it
  * has a negative length or new length or no room in its block table, when its
  * tokens pass total_new, or when it needs pages and the rows up to and including
  * it need more than are free (a later row that needs none is served).  Its tokens
