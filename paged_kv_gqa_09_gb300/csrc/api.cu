@@ -1552,9 +1552,7 @@ int pkv_append_slots(const pkv_shape_t *s, void *d_ws, const void *k_new, const 
     p.num_slots = (int64_t)s->num_pages * s->page_size;
     p.T = total_new;
     p.pieces = s->Hkv * s->d / 8;
-    int sms = 0;
-    PKV_TRY(device_sms(&sms));
-    cudaError_t e = launch_append_slots(p, sms, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_append_slots(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "slot append launch");
     g_cnt.append++;

@@ -6,7 +6,9 @@
 // read: tokens of the cache become packed fp16 K and V again.
 //
 // Both are one pass over their data: append reads 2 bytes per value and writes
-// one, read the other way round.
+// one, read the other way round.  35k tokens of 8 heads, d = 128, appended (213 MB,
+// 31 us at the copy rate) and read back at once take 73 us; 117k tokens read, 718
+// MB, 108 us, 0.97 of the copy rate; a token of each of 64 rows and its block 7.6 us.
 //
 // A warp takes a scale block (16 tokens, 8 in pages of 8) of one head and side at
 // a time: a lane holds 8 dims of 8 or 4 neighbouring tokens, so that the block's
@@ -24,7 +26,17 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 3;  // per SM
+constexpr int kOneThreads = 512;  // of the append of one token per row, at most
+// CTAs per SM, and a head's sides that a warp takes one after the other where
+// there is work for all warps.  A unit's warps should be near one another in time,
+// since a token's heads are neighbours in memory, but a warp has to look up its row
+// and page first.  35k tokens of 8 heads appended and read back: 2 sides each 73.4
+// us; the append with 4 77 us, 1 75 us, with 2 CTAs 78 us, 4 (spills) 81 us; the read
+// of 117k tokens with 2 sides 108.6 us, 1 114.6 us, 4 111 us, 8 116 us, with 3 CTAs 116
+// us, 5 (spills) 130 us.  Copies to shared memory ahead of use, or lines of
+// neighbouring blocks with the next one's page looked up ahead, took longer: 84 and
+// 82 us.
+constexpr int kAppendCtas = 3, kReadCtas = 4, kSides = 2;
 
 // Which tokens and dims of a block of 2^LG tokens a lane holds: dims 8 piece ..,
 // tokens first .. first + kTokens - 1 (none where `first` is beyond the block).
@@ -36,6 +48,37 @@ struct Lane {
     __device__ __forceinline__ Lane() : piece((threadIdx.x & 31) % kPieces), first((threadIdx.x & 31) / kPieces * kTokens) {}
     __device__ __forceinline__ bool any() const { return kTokens * kGroups == 1 << LG || first < 1 << LG; }
 };
+
+// The row that block gs is in: its first packed token, its tokens and what `a` and
+// `b` (nullptr: zeros) hold of it.  Of up to 64 rows every lane brings two, so that
+// all of it takes one round trip; whole warps only.
+struct Row {
+    int i, off, n, a, b;
+};
+template <int LG>
+__device__ __forceinline__ Row find_row(int64_t gs, const int32_t *offsets, int B, const int32_t *pa, const int32_t *pb)
+{
+    if (B > 64) {
+        const int i = min(last_not_above(B, gs, [&](int r) { return append_first_group(offsets[r], r, LG); }), B - 1);
+        const int off = offsets[i];
+        return {i, off, offsets[i + 1] - off, pa[i], pb ? pb[i] : 0};
+    }
+    const int lane = threadIdx.x & 31;
+    int o[2], e[2], x[2], y[2];
+    unsigned m[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int r = min(lane + 32 * u, B - 1);
+        o[u] = offsets[r], e[u] = offsets[r + 1], x[u] = pa[r], y[u] = pb ? pb[r] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        m[u] = __ballot_sync(0xffffffffu, lane + 32 * u < B && append_first_group(o[u], lane + 32 * u, LG) <= gs);
+    const int i = max(__popc(m[0]) + __popc(m[1]) - 1, 0);
+    auto of = [&](const int (&v)[2]) { return __shfl_sync(0xffffffffu, i >= 32 ? v[1] : v[0], i & 31); };
+    const int off = of(o);
+    return {i, off, of(e) - off, of(x), of(y)};
+}
 
 __device__ __forceinline__ uint32_t greatest(uint4 x)
 {
@@ -72,7 +115,7 @@ struct NewScale {
 // page's block r0) for some of the heads' sides (2 h: K, 2 h + 1: V), then the
 // next such unit a grid further on.
 template <int D, int FMT, int LG>
-__global__ void __launch_bounds__(kThreads, kCtas) byte_append_kernel(const QuantAppendParams p)
+__global__ void __launch_bounds__(kThreads, kAppendCtas) byte_append_kernel(const QuantAppendParams p)
 {
     using Ln = Lane<D, LG>;
     constexpr int TL = Ln::kTokens;
@@ -95,9 +138,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) byte_append_kernel(const Quan
     const unsigned line = warp / (unsigned)p.parts;
     const int it0 = (int)(warp - line * p.parts) * p.its_per_part, it1 = min(it0 + p.its_per_part, 2 * p.Hkv);
     for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
-        const int i = min(last_not_above(p.B, gs, [&](int r) { return append_first_group(p.offsets[r], r, LG); }), p.B - 1);
-        const int off = p.offsets[i], n = p.offsets[i + 1] - off;
-        const int N = p.seq_lens[i];
+        const Row row = find_row<LG>(gs, p.offsets, p.B, p.seq_lens, nullptr);
+        const int i = row.i, off = row.off, n = row.n, N = row.a;
         int64_t pos0;
         if (!append_group(gs, i, off, n, N, pos0, LG) || !append_fits(p, i, N, off, n, false))
             continue;
@@ -187,12 +229,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) byte_append_kernel(const Quan
 // One new token per row: a CTA per row, which alone reads and advances its
 // length; a warp (d = 64: half a warp) takes a head's side, a lane four dims.
 template <int D, int FMT, int LG>
-__global__ void __launch_bounds__(kThreads) byte_append_one_kernel(const QuantAppendParams p)
+__global__ void __launch_bounds__(kOneThreads) byte_append_one_kernel(const QuantAppendParams p)
 {
     constexpr int kLanes = D / 4, kPer = 32 / kLanes;  // of a head's side, and sides per warp
     pdl_wait();
     pdl_trigger();
     const int i = blockIdx.x, l = (threadIdx.x & 31) % kLanes;
+    const int at = (int)threadIdx.x / kLanes, step = (int)blockDim.x / kLanes;
+    // the first side's values do not depend on the three loads a token's place hangs on
+    auto load = [&](int side) {
+        return side < 2 * p.Hkv ? *reinterpret_cast<const uint2 *>((side & 1 ? p.v_new : p.k_new) + (int64_t)i * p.new_stride +
+                                                                   (side >> 1) * D + 4 * l)
+                                : make_uint2(0, 0);
+    };
+    uint2 x = load(at);
     const int N = p.seq_lens[i];
     int page = -1;
     if (N < 0 || N >= p.len_cap) {
@@ -209,15 +259,13 @@ __global__ void __launch_bounds__(kThreads) byte_append_one_kernel(const QuantAp
     }
     const int tb = 1 << p.tb_log2, slot = N & ((1 << p.log2P) - 1), r = slot & (tb - 1), u = r & ((1 << LG) - 1);
     uint8_t *blk = p.cache + (int64_t)max(page, 0) * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * byte_block_bytes(tb, D);
-    const int at = (int)threadIdx.x / kLanes, step = (int)blockDim.x / kLanes;
     for (int it = at - at % kPer; it < 2 * p.Hkv && page >= 0; it += step) {
         const int mine = it + at % kPer, h = mine >> 1;
         const bool there = mine < 2 * p.Hkv, v = mine & 1;
         uint8_t *hb = blk + (int64_t)(there ? h : 0) * p.page_head_bytes;
         float *scale = reinterpret_cast<float *>(hb + byte_scale_part<D>(tb, r, LG)) + v;
-        uint2 x = make_uint2(0, 0);
-        if (there)
-            x = *reinterpret_cast<const uint2 *>((v ? p.v_new : p.k_new) + (int64_t)i * p.new_stride + h * D + 4 * l);
+        if (it >= step)
+            x = load(mine);
         const float was = there && u > 0 ? *scale : 0.f;
         uint32_t top = greatest(make_uint4(x.x, x.y, 0, 0));
 #pragma unroll
@@ -259,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) byte_append_one_kernel(const QuantAp
 // A scale block of a row for some of the heads' sides, as the append takes them:
 // its tokens among those that the row's span wants.
 template <int D, int FMT, int LG>
-__global__ void __launch_bounds__(kThreads, kCtas) byte_read_kernel(const QuantReadParams p)
+__global__ void __launch_bounds__(kThreads, kReadCtas) byte_read_kernel(const QuantReadParams p)
 {
     using Ln = Lane<D, LG>;
     constexpr int TL = Ln::kTokens;
@@ -271,12 +319,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) byte_read_kernel(const QuantR
     const int part_no = (int)(unit - gs * p.parts), it0 = part_no * p.heads_per_part, it1 = min(it0 + p.heads_per_part, 2 * p.Hkv);
     if (gs >= p.groups)
         return;
-    const int i = min(last_not_above(p.B, gs, [&](int r) { return append_first_group(p.offsets[r], r, LG); }), p.B - 1);
-    const int off = p.offsets[i], n = p.offsets[i + 1] - off, begin = p.first ? p.first[i] : 0;
+    const Row row = find_row<LG>(gs, p.offsets, p.B, p.seq_lens, p.first);
+    const int i = row.i, off = row.off, n = row.n, begin = row.b;
     int64_t pos0;
     if (off < 0 || (int64_t)off + n > p.T || !append_group(gs, i, off, n, begin, pos0, LG))
         return;  // offsets that do not ascend within the buffer have no tokens here
-    const int N = min(p.seq_lens[i], p.len_cap);
+    const int N = min(row.a, p.len_cap);
     const int64_t from = max(pos0, (int64_t)begin), to = min(pos0 + (1 << LG), (int64_t)begin + n);
     int page = -1;
     if (pos0 >= 0 && from < N) {
@@ -364,22 +412,38 @@ cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// How the blocks' sides are split over warps: kSides each, one where that makes
+// less than 4096 warps; of an append, which walks the line, no more parts than
+// there are warps.
+template <class P>
+void split_sides(P &p, int lg, int64_t most, int &per)
+{
+    p.groups = append_groups(p.T, p.B, lg);
+    per = p.groups * p.Hkv < 4096 ? 1 : kSides;
+    const int64_t parts = (2 * (int64_t)p.Hkv + per - 1) / per;
+    if (parts > most)
+        per = (int)((2 * (int64_t)p.Hkv + most - 1) / most);
+    p.parts = (2 * p.Hkv + per - 1) / per;
+}
+
 template <int D, int FMT, int LG>
 cudaError_t launch_append(QuantAppendParams p, int sms, cudaStream_t s)
 {
     if (!p.offsets) {
-        const int warps = (2 * p.Hkv * D + 127) / 128;
-        return launch(byte_append_one_kernel<D, FMT, LG>, p, p.B, 32 * (warps < kWarps ? warps : kWarps), s);
+        const int64_t threads = 32 * ((2 * (int64_t)p.Hkv * D + 127) / 128);
+        return launch(byte_append_one_kernel<D, FMT, LG>, p, p.B, (int)(threads < kOneThreads ? threads : kOneThreads), s);
     }
-    const int64_t grid = append_grid(p.T, p.B, p.Hkv, kCtas * sms, kWarps, p.groups, p.parts, p.its_per_part, LG);
+    const int64_t resident = (int64_t)kAppendCtas * sms * kWarps;
+    split_sides(p, LG, resident, p.its_per_part);
+    const int64_t all = (p.groups * p.parts + kWarps - 1) / kWarps, most = resident / kWarps;
+    const int64_t grid = all < most ? all : most;
     return launch(byte_append_kernel<D, FMT, LG>, p, grid, kThreads, s);
 }
 
 template <int D, int FMT, int LG>
 cudaError_t launch_read(QuantReadParams p, int sms, cudaStream_t s)
 {
-    p.groups = append_groups(p.T, p.B, LG);
-    p.parts = split_work(p.groups, 2 * p.Hkv, (int64_t)4 * kCtas * kWarps * sms, INT64_MAX, p.heads_per_part);
+    split_sides(p, LG, INT64_MAX, p.heads_per_part);
     return launch(byte_read_kernel<D, FMT, LG>, p, (p.groups * p.parts + kWarps - 1) / kWarps, kThreads, s);
 }
 

@@ -17,25 +17,26 @@
 namespace pkv {
 namespace {
 
-constexpr int kMapThreads = 512;
-constexpr int kMapWarps = kMapThreads / 32;
-constexpr int kMapRows = 2 * kMapThreads;  // rows whose sums a CTA holds at a time
-constexpr int kInvalid = -2;               // in place of a row's rank: no length that the table could hold
-constexpr int kNotServed = -1;             // no pages left for it, or no room in the packed buffer
-constexpr int kBadCta = 1 << 20;           // CTAs that met a bad page count this much more
+constexpr int kInvalid = -2;      // in place of a row's rank: no length that the table could hold
+constexpr int kNotServed = -1;    // no pages left for it, or no room in the packed buffer
+constexpr int kBadCta = 1 << 20;  // CTAs that met a bad page of the free list count this much more
+constexpr int kFewTokens = 4;     // new tokens of a row up to which its own thread places them
 
-// The rows [c0, c0 + kMapRows) as the map sees them: two of them per thread, and
-// what the tokens need of all of them in shared memory.
+// Two rows per thread are held at a time, with what their tokens need in shared memory.
+template <int THREADS>
 struct MapRows {
-    int off[kMapRows + 1];  // first packed token, at most T
-    int len[kMapRows];      // N
-    int rank[kMapRows];     // pages that the rows before need, or one of the above
-    long long sum[2][kMapWarps];
+    static constexpr int kRows = 2 * THREADS, kWarps = THREADS / 32;
+    int off[kRows + 1];  // first packed token, at most T
+    int len[kRows];      // N
+    int rank[kRows];     // pages that the rows before need, or one of the above
+    int page[kRows];     // of the row's last tokens, where that has room for more
+    long long sum[2][kWarps];
 };
 
 struct MapRow {
     int N, n, need, rank;  // as above
-    int status;            // DevErr, kErrNone when it is served
+    int page;              // as above; -1 where there is none, -2 where its id is out of range
+    int status;            // DevErr, kErrNone when the row is served
     int off;               // at most T
 };
 
@@ -43,22 +44,33 @@ __device__ __forceinline__ int pages_of(const MapParams &p, int N) { return (N >
 
 // Rows c0 + 2 tid and the next of this thread; off0 and rank0 are the sums over
 // the rows before c0 and become those over the rows before the next chunk's.
-__device__ __forceinline__ void map_rows(const MapParams &p, int c0, int count, MapRows &s, MapRow (&row)[2], long long &off0,
+// Returns whether every row has few new tokens.
+template <int THREADS>
+__device__ __forceinline__ bool map_rows(const MapParams &p, int c0, int count, MapRows<THREADS> &s, MapRow (&row)[2], long long &off0,
                                          long long &rank0)
 {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    constexpr int kWarps = MapRows<THREADS>::kWarps;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, mask = (1 << p.log2P) - 1;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = c0 + 2 * (int)threadIdx.x + u;
+        row[u].N = i < p.B ? p.seq_lens[i] : 0;
+        row[u].n = i < p.B ? p.new_lens[i] : 0;
+    }
+    bool few = true;
     long long n2[2], need2[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int i = c0 + 2 * (int)threadIdx.x + u;
         MapRow &r = row[u];
-        r.N = i < p.B ? p.seq_lens[i] : 0;
-        r.n = i < p.B ? p.new_lens[i] : 0;
         r.status = r.N < 0 || r.n < 0 ? kErrNegLen : (long long)r.N + r.n > p.len_cap ? kErrTooLong : kErrNone;
         r.n = max(r.n, 0);
         r.need = r.status == kErrNone ? pages_of(p, r.N + r.n) - pages_of(p, r.N) : 0;
+        // on its way while the sums are taken
+        r.page = r.status == kErrNone && r.n > 0 && (r.N & mask) ? p.bt[(int64_t)i * p.bt_stride + (r.N >> p.log2P)] : -1;
         n2[u] = r.n;
         need2[u] = r.need;
+        few &= r.n <= kFewTokens;
     }
     long long a = n2[0] + n2[1], b = need2[0] + need2[1];
 #pragma unroll
@@ -73,10 +85,10 @@ __device__ __forceinline__ void map_rows(const MapParams &p, int c0, int count, 
         s.sum[0][w] = a;
         s.sum[1][w] = b;
     }
-    __syncthreads();
+    few = __syncthreads_and(few) != 0;
     long long off = off0 + a - n2[0] - n2[1], rank = rank0 + b - need2[0] - need2[1];
 #pragma unroll
-    for (int v = 0; v < kMapWarps; ++v) {
+    for (int v = 0; v < kWarps; ++v) {
         const long long x = s.sum[0][v], y = s.sum[1][v];
         off += v < w ? x : 0;
         rank += v < w ? y : 0;
@@ -94,19 +106,25 @@ __device__ __forceinline__ void map_rows(const MapParams &p, int c0, int count, 
             r.status = kErrNoPage;
         r.rank = r.status == kErrNone ? (int)min(rank, 0x7fffffffll)
                                       : r.status == kErrNoPage || r.status == kErrBadSpan ? kNotServed : kInvalid;
+        if (r.page != -1 || (r.status == kErrNone && r.n > 0 && (r.N & mask)))
+            if (r.page < 0 || r.page >= p.num_pages)
+                r.page = -2;
         s.off[x] = r.off;
         s.len[x] = r.N;
         s.rank[x] = r.rank;
-        if (x == kMapRows - 1)
-            s.off[kMapRows] = (int)min(off + n2[u], (long long)p.T);
+        s.page[x] = r.page;
+        if (x == MapRows<THREADS>::kRows - 1)
+            s.off[MapRows<THREADS>::kRows] = (int)min(off + n2[u], (long long)p.T);
         off += n2[u];
         rank += need2[u];
     }
     __syncthreads();
+    return few;
 }
 
 // The lengths and the free count after the call, of the rows map_rows() has
-// just seen; `pages_bad`: some page id was out of range, so those are looked for.
+// just seen; `pages_bad`: some id of the free list was out of range, so those are
+// looked for.
 __device__ __forceinline__ void map_finish(const MapParams &p, int c0, int count, bool pages_bad, const MapRow (&row)[2], int *s_taken)
 {
 #pragma unroll
@@ -126,114 +144,152 @@ __device__ __forceinline__ void map_finish(const MapParams &p, int c0, int count
             report_error(p.ws, kErrNoPage, i, r.N, count);
         if (ok && r.need > 0)
             atomicMax(s_taken, r.rank + r.need);
-        if (ok && pages_bad && r.n > 0) {
-            auto good = [&](int page) { return page >= 0 && page < p.num_pages; };
-            const int have = pages_of(p, r.N);
-            if (r.N & ((1 << p.log2P) - 1))
-                ok = good(p.bt[(int64_t)i * p.bt_stride + have - 1]);
-            for (int j = 0; ok && j < r.need; ++j)
-                ok = good(p.free_pages[count - 1 - r.rank - j]);
+        if (ok && r.page == -2) {
+            report_error(p.ws, kErrBadPage, i, r.N >> p.log2P, p.bt[(int64_t)i * p.bt_stride + (r.N >> p.log2P)]);
+            ok = false;
         }
+        if (ok && pages_bad)
+            for (int j = 0; ok && j < r.need; ++j) {
+                const int page = p.free_pages[count - 1 - r.rank - j];
+                ok = page >= 0 && page < p.num_pages;
+            }
         p.seq_lens_out[i] = ok ? r.N + r.n : r.N;
     }
 }
 
-__global__ void __launch_bounds__(kMapThreads) map_pages_kernel(const MapParams p)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
 {
-    __shared__ MapRows s;
+    constexpr int kRows = MapRows<THREADS>::kRows;
+    __shared__ MapRows<THREADS> s;
     __shared__ int s_taken, s_seen;
     pdl_wait();
     pdl_trigger();
     const bool alone = gridDim.x == 1;
     if (threadIdx.x == 0)
         s_taken = 0;
-    const int count = min(max(*p.free_count, 0), p.free_cap);
+    const int count = min(max(*p.free_count, 0), p.free_cap), mask = (1 << p.log2P) - 1;
     // this CTA's tokens [t0, t1), whole groups of four
     const long long quads = ((long long)p.T + 3) / 4, per = (quads + gridDim.x - 1) / gridDim.x;
     const int t0 = (int)min(4 * per * blockIdx.x, (long long)p.T), t1 = (int)min(4 * per * (blockIdx.x + 1), (long long)p.T);
     long long off0 = 0, rank0 = 0;
     bool bad = false;
-    // Slots and positions of tokens x .. x + 3, of which [lo, hi) are this call's, from `at`.
-    auto store4 = [&](int x, int lo, int hi, auto at) {
-        long long slot[4];
-        int pos[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            slot[u] = -1;
-            pos[u] = 0;
-            if (x + u >= lo && x + u < hi)
-                at(x + u, slot[u], pos[u]);
-        }
-        if (x >= lo && x + 4 <= hi) {
-            reinterpret_cast<longlong2 *>(p.slots + x)[0] = make_longlong2(slot[0], slot[1]);
-            reinterpret_cast<longlong2 *>(p.slots + x)[1] = make_longlong2(slot[2], slot[3]);
-            if (p.positions)
-                *reinterpret_cast<int4 *>(p.positions + x) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (x + u >= lo && x + u < hi) {
-                    p.slots[x + u] = slot[u];
-                    if (p.positions)
-                        p.positions[x + u] = pos[u];
-                }
+    // The page of block blk of row i, the j-th new one of a row of this rank or (j < 0) the one that has room; -1 where
+    // its id is out of range.
+    auto page_of = [&](int i, int blk, int j, int rank, int held) {
+        if (j < 0)
+            return max(held, -1);
+        const int page = p.free_pages[count - 1 - rank - j];
+        if (page >= 0 && page < p.num_pages)
+            return page;
+        report_error(p.ws, kErrBadPage, i, blk, page);
+        bad = true;
+        return -1;
+    };
+    // Token x, the k-th new one of row i.
+    auto place = [&](int x, int i, int N, int k, int rank, int held, long long &slot, int &pos) {
+        const int at = N + k, blk = at >> p.log2P, in = at & mask, j = blk - pages_of(p, N);
+        slot = -1;
+        pos = 0;
+        if (rank == kInvalid)
+            return;
+        const int page = rank == kNotServed ? -1 : page_of(i, blk, j, rank, held);
+        if (j >= 0 && in == 0)
+            p.bt[(int64_t)i * p.bt_stride + blk] = page;
+        if (page >= 0) {
+            slot = ((long long)page << p.log2P) + in;
+            pos = at;
         }
     };
-    for (int c0 = 0; c0 < p.B && (alone || blockIdx.x == 0 || off0 < t1); c0 += kMapRows) {
-        MapRow row[2];
-        map_rows(p, c0, count, s, row, off0, rank0);
-        const int nr = min(p.B - c0, kMapRows);
+    auto store = [&](int x, long long slot, int pos) {
+        p.slots[x] = slot;
+        if (p.positions)
+            p.positions[x] = pos;
+    };
+    auto store4 = [&](int x, const long long (&slot)[4], const int (&pos)[4]) {
+        reinterpret_cast<longlong2 *>(p.slots + x)[0] = make_longlong2(slot[0], slot[1]);
+        reinterpret_cast<longlong2 *>(p.slots + x)[1] = make_longlong2(slot[2], slot[3]);
+        if (p.positions)
+            *reinterpret_cast<int4 *>(p.positions + x) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    };
+    MapRow row[2];
+    for (int c0 = 0; c0 < p.B && (alone || blockIdx.x == 0 || off0 < t1); c0 += kRows) {
+        const bool few = map_rows(p, c0, count, s, row, off0, rank0);
+        const int nr = min(p.B - c0, kRows);
         if (blockIdx.x == 0) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 if (2 * (int)threadIdx.x + u < nr)
                     p.offsets[c0 + 2 * threadIdx.x + u] = row[u].off;
         }
-        const int lo = max(t0, s.off[0]), hi = min(t1, s.off[nr]);
-        for (long long q = lo / 4 + threadIdx.x; q * 4 < hi; q += kMapThreads) {
-            const int x0 = (int)q * 4;
-            int r = 0, up = nr - 1;  // the last row at or before the group's first token
-            while (r < up) {
-                const int mid = (r + up + 1) >> 1;
-                if (s.off[mid] <= max(x0, lo))
-                    r = mid;
-                else
-                    up = mid - 1;
+        if (few) {
+            // a step of a token per row or a few: from the thread that has the row, without a search
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                for (int k = max(t0 - row[u].off, 0); k < min(row[u].n, t1 - row[u].off); ++k) {
+                    long long slot;
+                    int pos;
+                    place(row[u].off + k, c0 + 2 * (int)threadIdx.x + u, row[u].N, k, row[u].rank, row[u].page, slot, pos);
+                    store(row[u].off + k, slot, pos);
+                }
+        } else {
+            const int lo = max(t0, s.off[0]), hi = min(t1, s.off[nr]);
+            for (long long q = lo / 4 + threadIdx.x; q * 4 < hi; q += THREADS) {
+                const int x0 = (int)q * 4;
+                int r = 0, up = nr - 1;  // the last row at or before the group's first token
+                while (r < up) {
+                    const int mid = (r + up + 1) >> 1;
+                    if (s.off[mid] <= max(x0, lo))
+                        r = mid;
+                    else
+                        up = mid - 1;
+                }
+                long long slot[4];
+                int pos[4];
+                if (x0 >= lo && x0 + 4 <= min(hi, s.off[r + 1]) && s.rank[r] >= 0) {
+                    // four tokens of one row, on one page or two
+                    const int N = s.len[r], at = N + (x0 - s.off[r]), have = pages_of(p, N), rank = s.rank[r], held = s.page[r];
+                    const int b0 = at >> p.log2P, b1 = (at + 3) >> p.log2P;
+                    const int p0 = page_of(c0 + r, b0, b0 - have, rank, held);
+                    const int p1 = b1 == b0 ? p0 : page_of(c0 + r, b1, b1 - have, rank, held);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int in = (at + u) & mask, page = (at + u) >> p.log2P == b0 ? p0 : p1;
+                        slot[u] = page < 0 ? -1 : ((long long)page << p.log2P) + in;
+                        pos[u] = page < 0 ? 0 : at + u;
+                        if (in == 0)  // a new page starts with a new token
+                            p.bt[(int64_t)(c0 + r) * p.bt_stride + ((at + u) >> p.log2P)] = page;
+                    }
+                    store4(x0, slot, pos);
+                    continue;
+                }
+                for (int u = 0; u < 4; ++u) {
+                    const int x = x0 + u;
+                    if (x < lo || x >= hi)
+                        continue;
+                    while (r + 1 < nr && x >= s.off[r + 1])
+                        ++r;
+                    place(x, c0 + r, s.len[r], x - s.off[r], s.rank[r], s.page[r], slot[0], pos[0]);
+                    store(x, slot[0], pos[0]);
+                }
             }
-            store4(x0, lo, hi, [&](int x, long long &slot, int &pos) {
-                while (r + 1 < nr && x >= s.off[r + 1])
-                    ++r;
-                const int N = s.len[r], rank = s.rank[r], at = N + (x - s.off[r]);
-                if (rank == kInvalid)
-                    return;
-                const int blk = at >> p.log2P, in = at & ((1 << p.log2P) - 1), j = blk - pages_of(p, N);
-                int32_t *entry = p.bt + (int64_t)(c0 + r) * p.bt_stride + blk;
-                if (rank == kNotServed) {
-                    if (j >= 0 && in == 0 && blk < p.bt_stride)
-                        *entry = -1;
-                    return;
-                }
-                int page = j < 0 ? *entry : p.free_pages[count - 1 - rank - j];
-                if (page < 0 || page >= p.num_pages) {
-                    report_error(p.ws, kErrBadPage, c0 + r, blk, page);
-                    bad = true;
-                    page = -1;
-                }
-                if (j >= 0 && in == 0)
-                    *entry = page;
-                if (page < 0)
-                    return;
-                slot = ((long long)page << p.log2P) + in;
-                pos = at;
-            });
         }
-        const bool any_bad = __syncthreads_or(alone && bad) != 0;  // the sums are read until here
-        if (alone)
+        if (alone) {
+            const bool any_bad = __syncthreads_or(bad) != 0;
             map_finish(p, c0, count, any_bad, row, &s_taken);
+        } else if (p.B > kRows) {
+            __syncthreads();  // the sums are read until here
+        }
     }
-    if (off0 < t1)  // behind the last token
-        for (long long q = max((long long)t0, off0) / 4 + threadIdx.x; q * 4 < t1; q += kMapThreads)
-            store4((int)q * 4, max(t0, (int)off0), t1, [](int, long long &, int &) {});
+    // behind the last token
+    for (long long q = max((long long)t0, off0) / 4 + threadIdx.x; off0 < t1 && q * 4 < t1; q += THREADS) {
+        const int x0 = (int)q * 4, lo = max(t0, (int)off0);
+        if (x0 >= lo && x0 + 4 <= t1)
+            store4(x0, {-1, -1, -1, -1}, {0, 0, 0, 0});
+        else
+            for (int x = max(x0, lo); x < min(x0 + 4, t1); ++x)
+                store(x, -1, 0);
+    }
     if (blockIdx.x == 0 && threadIdx.x == 0)
         p.offsets[p.B] = (int)min(off0, (long long)p.T);
     if (!alone) {
@@ -245,11 +301,15 @@ __global__ void __launch_bounds__(kMapThreads) map_pages_kernel(const MapParams 
         __syncthreads();
         if ((s_seen & (kBadCta - 1)) != (int)gridDim.x)
             return;
-        off0 = rank0 = 0;
-        for (int c0 = 0; c0 < p.B; c0 += kMapRows) {
-            MapRow row[2];
-            map_rows(p, c0, count, s, row, off0, rank0);
-            map_finish(p, c0, count, s_seen >= kBadCta, row, &s_taken);
+        if (p.B <= kRows) {  // its rows are all there are
+            map_finish(p, 0, count, s_seen >= kBadCta, row, &s_taken);
+        } else {
+            off0 = rank0 = 0;
+            for (int c0 = 0; c0 < p.B; c0 += kRows) {
+                map_rows(p, c0, count, s, row, off0, rank0);
+                map_finish(p, c0, count, s_seen >= kBadCta, row, &s_taken);
+                __syncthreads();
+            }
         }
     }
     __syncthreads();
@@ -261,42 +321,42 @@ __global__ void __launch_bounds__(kMapThreads) map_pages_kernel(const MapParams 
 }
 
 constexpr int kSlotThreads = 256;
-constexpr int kSlotBatch = 4;  // 16-byte pieces a lane has in flight
+constexpr int kSlotBatch = 8;  // 16-byte pieces a lane has in flight
 
-// A warp per packed token, then the next one a grid further on; pieces of K and V in one line.
+// A warp per packed token; pieces of K and V in one line.
 __global__ void __launch_bounds__(kSlotThreads) append_slots_kernel(const SlotParams p)
 {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int warps = (int)gridDim.x * (kSlotThreads / 32);
-    for (int64_t x = (int64_t)blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5); x < p.T; x += warps) {
-        const int64_t slot = p.slots[x];
-        if (slot < 0)
-            continue;
-        if (slot >= p.num_slots) {
-            if (lane == 0)
-                report_error(p.ws, kErrBadSlot, (int)x, (int)min(slot, (int64_t)0x7fffffff), (int)min(p.num_slots, (int64_t)0x7fffffff));
-            continue;
+    const int64_t x = (int64_t)blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5);
+    if (x >= p.T)
+        return;
+    const int64_t slot = p.slots[x];
+    if (slot < 0)
+        return;
+    if (slot >= p.num_slots) {
+        if (lane == 0)
+            report_error(p.ws, kErrBadSlot, (int)x, (int)min(slot, (int64_t)0x7fffffff), (int)min(p.num_slots, (int64_t)0x7fffffff));
+        return;
+    }
+    for (int c0 = lane; c0 < 2 * p.pieces; c0 += 32 * kSlotBatch) {
+        int4 v[kSlotBatch];
+#pragma unroll
+        for (int u = 0; u < kSlotBatch; ++u) {
+            const int c = c0 + 32 * u;
+            if (c < 2 * p.pieces)
+                v[u] = c < p.pieces ? reinterpret_cast<const int4 *>(p.k_new + x * p.new_stride)[c]
+                                    : reinterpret_cast<const int4 *>(p.v_new + x * p.new_stride)[c - p.pieces];
         }
-        for (int c0 = lane; c0 < 2 * p.pieces; c0 += 32 * kSlotBatch) {
-            int4 v[kSlotBatch];
 #pragma unroll
-            for (int u = 0; u < kSlotBatch; ++u) {
-                const int c = c0 + 32 * u;
-                if (c < 2 * p.pieces)
-                    v[u] = c < p.pieces ? reinterpret_cast<const int4 *>(p.k_new + x * p.new_stride)[c]
-                                        : reinterpret_cast<const int4 *>(p.v_new + x * p.new_stride)[c - p.pieces];
-            }
-#pragma unroll
-            for (int u = 0; u < kSlotBatch; ++u) {
-                const int c = c0 + 32 * u;
-                if (c < 2 * p.pieces) {
-                    if (c < p.pieces)
-                        reinterpret_cast<int4 *>(p.k_cache)[slot * p.pieces + c] = v[u];
-                    else
-                        reinterpret_cast<int4 *>(p.v_cache)[slot * p.pieces + c - p.pieces] = v[u];
-                }
+        for (int u = 0; u < kSlotBatch; ++u) {
+            const int c = c0 + 32 * u;
+            if (c < 2 * p.pieces) {
+                if (c < p.pieces)
+                    reinterpret_cast<int4 *>(p.k_cache)[slot * p.pieces + c] = v[u];
+                else
+                    reinterpret_cast<int4 *>(p.v_cache)[slot * p.pieces + c - p.pieces] = v[u];
             }
         }
     }
@@ -321,14 +381,16 @@ cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s
 
 cudaError_t launch_map_pages(const MapParams &p, int sms, cudaStream_t s)
 {
-    const int64_t want = ((int64_t)p.T + 4 * kMapThreads - 1) / (4 * kMapThreads), most = 2 * (int64_t)sms;
-    return launch(map_pages_kernel, p, want < most ? want : most, kMapThreads, s);
+    constexpr int kSmall = 128, kLarge = 256;
+    if (p.B <= 2 * kSmall && p.T <= 16 * kSmall)
+        return launch(map_pages_kernel<kSmall>, p, 1, kSmall, s);
+    const int64_t want = ((int64_t)p.T + 4 * kLarge - 1) / (4 * kLarge), most = 2 * (int64_t)sms;
+    return launch(map_pages_kernel<kLarge>, p, want < most ? want : most, kLarge, s);
 }
 
-cudaError_t launch_append_slots(const SlotParams &p, int sms, cudaStream_t s)
+cudaError_t launch_append_slots(const SlotParams &p, cudaStream_t s)
 {
-    const int64_t want = ((int64_t)p.T + kSlotThreads / 32 - 1) / (kSlotThreads / 32), most = 8 * (int64_t)sms;
-    return launch(append_slots_kernel, p, want < most ? want : most, kSlotThreads, s);
+    return launch(append_slots_kernel, p, ((int64_t)p.T + kSlotThreads / 32 - 1) / (kSlotThreads / 32), kSlotThreads, s);
 }
 
 }  // namespace pkv

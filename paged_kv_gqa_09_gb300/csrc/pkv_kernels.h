@@ -193,7 +193,7 @@ cudaError_t launch_quant_read(int d, QuantReadParams p, int sms, cudaStream_t s)
 cudaError_t launch_byte_append(int d, int fmt, const QuantAppendParams &p, int sms, cudaStream_t s);
 cudaError_t launch_byte_read(int d, int fmt, const QuantReadParams &p, int sms, cudaStream_t s);
 cudaError_t launch_map_pages(const MapParams &p, int sms, cudaStream_t s);
-cudaError_t launch_append_slots(const SlotParams &p, int sms, cudaStream_t s);
+cudaError_t launch_append_slots(const SlotParams &p, cudaStream_t s);
 cudaError_t launch_attend(int d, const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int sms,
                           cudaStream_t s);
 cudaError_t launch_attend_int8(int d, const AttendParams &p, int sms, cudaStream_t s);
