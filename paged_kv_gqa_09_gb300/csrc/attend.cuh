@@ -7,11 +7,12 @@
 //   s_t = scale q_h . K_t,  o = sum_t exp(s_t - m) V_t / l,  lse = m + ln l,
 //   m = max_t s_t,  l = sum_t exp(s_t - m).
 // One pass over the cache: 4 d flops per visible token and query head against
-// 1.25 d bytes (4-bit) or 4 d (fp16) per token and KV head.  HBM bounds long
-// batches (d = 128: 64 rows, 1.9M tokens of the 4-bit cache, 2.44 GB in 383 us;
-// 64 rows in a window of 8191 over fp16 pages, 1.85 GB in 274 us at most); the
-// 4-bit cache's unpacking and latency short ones (117k tokens, 150 MB, 33.6 us;
-// one row of 32k, 42 MB, 18.2 us).
+// 1.25 d bytes (4-bit), 2 d (8-bit) or 4 d (fp16) per token and KV head.  HBM
+// bounds long batches (d = 128: 64 rows, 1.9M tokens of the 4-bit cache, 2.44 GB in
+// 383 us; 2.1M of the 8-bit cache, 4.32 GB in 615 us; 64 rows in a window of 8191
+// over fp16 pages, 1.85 GB in 274 us at most); the 4-bit cache's unpacking and
+// latency short ones (117k tokens, 150 MB, 33.6 us; 120k of the 8-bit cache, 247 MB,
+// 40.5 us; one row of 32k, 42 MB, 18.2 us).
 //
 // Work split.  A row's visible tokens lie in T_i tiles of 128 tokens (64 of fp16
 // pages with d = 128, 256 of the 4-bit cache with d = 64; those between the sinks
@@ -32,14 +33,14 @@
 // CTA: warp 4 is the producer, warps 0..3 the consumers.  The producer walks
 // the run, reads block-table entries a batch of tiles ahead and streams each
 // tile into a ring of shared-memory stages: fp16 pages with tiled TMA copies
-// (128-byte swizzle), the 4-bit cache -- whose pages hold K and V of a head in
-// one contiguous run per 64 tokens or page -- with plain bulk copies; a piece's
-// first tile brings its q rows.  Consumer warp w takes a quarter of every tile's
+// (128-byte swizzle), the 4-bit and 8-bit caches -- whose pages hold K and V of a
+// head in one contiguous run per 64 tokens or page -- with plain bulk copies; a
+// piece's first tile brings its q rows.  Consumer warp w takes a quarter of every tile's
 // tokens, 16 or 32 at a time, with its own online softmax: scores S^T = K q^T (16 tokens x
 // 8 heads) and O^T += V^T P^T (d x 8 heads) on mma.sync m16n8k16, fp16 in, fp32
 // accumulate.  N = 8 heads is all a KV head has, so a tcgen05 tile would be
-// 1/16 full; the registers that mma.sync reads are what the 4-bit codes are
-// unpacked into.  Every wait is bounded (1 s).
+// 1/16 full; the registers that mma.sync reads are what the codes are unpacked
+// into.  Every wait is bounded (1 s).
 #pragma once
 
 #include "pkv_device.cuh"
@@ -140,9 +141,15 @@ struct Layout {
     // head's token is one 128-byte line among the others' heads) want more loads
     // from more warps in flight: 64 rows in a window of 8191, three CTAs of two
     // stages 166 us, two of three 208 us; clusters the latter (12.8 and 14.9 us
-    // for eight rows)
-    static constexpr int kCtasPerSm = BYTE ? (D == 64 ? 3 : 2) : QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
-    static constexpr int kStages = BYTE ? 3 : QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
+    // for eight rows).  The 8-bit cache's tiles are 32 KB with d = 128: two CTAs of
+    // three stages (eight rows of up to 32k tokens 42.4 us, one of 32k 19.8 us;
+    // three of two 43.2 and 21.0 us, though 64 rows in a window of 4096 take 82 and 77
+    // us); tiles of 64 tokens, in five stages, leave a warp one block at a time
+    // (eight rows 57 us).  With d = 64, 64 rows of up to 32k: four CTAs of three stages
+    // 177.5 us, three of four 179.5 us, but in clusters 8.1 and 7.4 us (five rows in a
+    // window)
+    static constexpr int kCtasPerSm = BYTE ? (D == 128 ? 2 : CLUSTER ? 3 : 4) : QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
+    static constexpr int kStages = BYTE ? (D == 64 && CLUSTER ? 4 : 3) : QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
@@ -284,6 +291,86 @@ __device__ __forceinline__ float4 cluster_float4(uint32_t a)
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
     return v;
+}
+
+// The 8-bit cache's first tiles of this CTA on their way to L2, by one warp while
+// the producer still waits for the kernel before: three DRAM latencies (lengths,
+// table, pages) less after the wait.  What that kernel may still be writing is read
+// past L1 and only as a hint, of batches of a few windows of 32 rows: whatever it
+// says, the tiles are looked up again.  Eight rows of up to 32k tokens 45.4 us
+// without, 43.4 with one tile, 42.4 with two, 41.9 with three, 42.1 with four; one row
+// of 32k 20.2, 19.2, 19.9, 21.2 and 21.6 us; 16 rows of 1k 11.1, 10.2, 9.6, 9.8 and 10.0
+// us.
+constexpr int kHintRows = 128, kHintTiles = 2;
+
+template <int D, int KIND, bool CLUSTER>
+__device__ __forceinline__ void hint_first_tiles(const AttendParams &p)
+{
+    using L = Layout<D, KIND, CLUSTER>;
+    constexpr int kTile = L::kTile, TBL = kBlockLog2<KIND>, NBL = L::kTileLog2 - TBL;
+    const int lane = threadIdx.x & 31, cta = (int)blockIdx.x;
+    RowSpan rs;
+    int i = 0, h = 0, k0 = 0, k1 = 0;
+    if constexpr (CLUSTER) {
+        const int cl = p.cluster_log2, unit = cta >> cl, r = cta - (unit << cl);
+        i = unit / p.Hkv;
+        h = unit - i * p.Hkv;
+        rs = row_span<kTile>(p, __ldcg(p.seq_lens + i));
+        const int up = (1 << cl) - 1;
+        k0 = (rs.T * r + up) >> cl;
+        k1 = (rs.T * (r + 1) + up) >> cl;
+    } else {
+        if (p.B > kHintRows)
+            return;
+        int W = 0;
+        for (int at = 0; at < p.B; at += 32)
+            W += at + lane < p.B ? row_span<kTile>(p, __ldcg(p.seq_lens + at + lane)).line() : 0;
+        const Cuts cuts(__reduce_add_sync(0xffffffffu, W) * p.Hkv, (int)gridDim.x, p.B);
+        int f = cuts.begin(cta, 0);
+        const int end = cuts.end(cta, 0);
+        for (int at = 0; at < p.B; at += 32) {
+            const RowSpan mine = row_span<kTile>(p, at + lane < p.B ? __ldcg(p.seq_lens + at + lane) : 0);
+            int incl = mine.line();
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += y;
+            }
+            const int tot = __shfl_sync(0xffffffffu, incl, 31) * p.Hkv;
+            if (f >= tot) {
+                f -= tot;
+                continue;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, f < incl * p.Hkv);
+            const int src = __ffs(m) - 1;
+            f -= __shfl_sync(0xffffffffu, incl - mine.line(), src) * p.Hkv;
+            i = at + src;
+            rs.N = __shfl_sync(0xffffffffu, mine.N, src);
+            rs.ns = __shfl_sync(0xffffffffu, mine.ns, src);
+            rs.w0 = __shfl_sync(0xffffffffu, mine.w0, src);
+            rs.a = __shfl_sync(0xffffffffu, mine.a, src);
+            rs.b = __shfl_sync(0xffffffffu, mine.b, src);
+            rs.T = __shfl_sync(0xffffffffu, mine.T, src);
+            h = (int)((unsigned)f / (unsigned)(rs.T + 1));
+            k0 = f - h * (rs.T + 1);
+            k1 = min(rs.T, k0 + end - cuts.begin(cta, 0));
+            break;
+        }
+    }
+    const int k = k0 + (lane >> NBL);
+    if (k >= k1 || (lane >> NBL) >= kHintTiles)
+        return;
+    const int tok = rs.tile(k) * kTile + ((lane & ((1 << NBL) - 1)) << TBL);
+    if (!(tok < rs.ns || (tok + (1 << TBL) > rs.w0 && tok < rs.N)))
+        return;
+    const int pg = __ldcg(p.bt + (int64_t)i * p.bt_stride + (tok >> p.log2P));
+    if (pg < 0 || pg >= p.num_pages)
+        return;
+    const uint32_t bytes = Block<D, KIND>::bytes();
+    const uint8_t *from = p.cache + ((int64_t)pg * p.Hkv + h) * p.page_head_bytes +
+                          (int64_t)((tok & ((1 << p.log2P) - 1)) >> TBL) * bytes;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
 }
 
 // ---------------------------------------------------------------- producer
@@ -819,10 +906,11 @@ __device__ __forceinline__ uint32_t byte_rows(uint32_t vis)
 // One tile of the 8-bit cache, of which this warp takes 32 tokens, two blocks of
 // 16 for the tensor cores.  Of K, a lane reads 16 bytes, dims 64 c + 16 t .. of a
 // token, whose words w are its share of A in step 4 c + w: dims 64 c + 16 t + 4 w
-// and 2 further on at k = 2 t, 2 t + 1, the other two at 2 t + 8, 2 t + 9 (q's
-// fragments follow that).  Of V, it reads tokens 4 t .. 4 t + 3 of dims
-// 4 (r0 + 8 c) ..: tokens 4 t and 4 t + 2 at k = 2 t, 2 t + 1, the others at
-// 2 t + 8, 2 t + 9; so that row r0 < 8 of K's A is token 2 r0, row r0 + 8 the next.
+// and the next at k = 2 t, 2 t + 1, the other two at 2 t + 8, 2 t + 9 (q's fragments
+// follow that).  Row r0 < 8 of K's A is token 2 r0, row r0 + 8 the next: the rows
+// that lanes read at a time have different halves swapped.  Of V, a lane reads
+// tokens 4 t .. 4 t + 3 of dims 4 (r0 + 8 c) ..; the weights, which come as those of
+// tokens 4 t and 4 t + 2, and of the two others, change places to match.
 template <int D, int KIND>
 __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], const uint8_t *kv, uint32_t vis, int w, float sl2)
 {
@@ -847,11 +935,11 @@ __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D /
         const uint2 s = *reinterpret_cast<const uint2 *>(blk + byte_scale_part<D>(TB, r, LG));
         // a lane's tokens are both in its block.  K: the scale as it is, NaN too; V: within 2^-60 .. 2^60, so that
         // tokens which are masked, whatever their scale, stay harmless; NaN, which only visible ones keep, as NaN
-        sc.k[u] = sl2 * (float)(1 << kByteShift<FMT>) * __uint_as_float(s.x);
+        sc.k[u] = sl2 * __uint_as_float(s.x);
         const uint32_t eb = s.y >> 23 & 255u, in_range = min(max(eb, 67u), 187u);
         sc.e[u] = eb == 255u ? __uint_as_float(0x7fffffffu)
-                             : __uint_as_float(0x4b000000u | in_range) - (float)(8388608 + 127 - kByteShift<FMT>);
-        sc.inv[u] = __uint_as_float((254u - kByteShift<FMT> - in_range) << 23);
+                             : __uint_as_float(0x4b000000u | in_range) - (float)(8388608 + 127);
+        sc.inv[u] = __uint_as_float((254u - in_range) << 23);
         x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
     }
 #pragma unroll
@@ -871,17 +959,24 @@ __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D /
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const int at = 32 * w + 16 * u + (LG == 3 ? 8 * (t >> 1) : 0), r = at & (TB - 1);
-        const uint8_t *part = kv + (at >> TBL) * BYTES + byte_v_part<D>(TB, r, LG);
+        const uint8_t *vp = kv + (at >> TBL) * BYTES + byte_v_part<D>(TB, r, LG);
+        const uint32_t p0 = __byte_perm(P[u][0], P[u][1], 0x5410), p1 = __byte_perm(P[u][0], P[u][1], 0x7632);
+        // masked tokens' bytes may be a NaN's, which a weight of 0 does not hide
+        uint32_t keep = 0xffffffffu;
+        if (FMT == kE4m3 && vis != 0xffffffffu)
+            keep = ((vis >> (16 * u + 4 * t) & 15u) * 0x00204081u & 0x01010101u) * 255u;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(part + byte_v_at(r0 + 8 * c, LG == 3 ? t & 1 : t, LG));
+            uint4 v = *reinterpret_cast<const uint4 *>(vp + byte_v_at(r0 + 8 * c, LG == 3 ? t & 1 : t, LG));
+            if (FMT == kE4m3)
+                v.x &= keep, v.y &= keep, v.z &= keep, v.w &= keep;
             uint32_t a0, a1, a2, a3;
             byte_numbers<FMT>(v.x, a0, a2);
             byte_numbers<FMT>(v.y, a1, a3);
-            mma_16816(st.O[2 * c], a0, a1, a2, a3, P[u][0], P[u][1]);
+            mma_16816(st.O[2 * c], a0, a1, a2, a3, p0, p1);
             byte_numbers<FMT>(v.z, a0, a2);
             byte_numbers<FMT>(v.w, a1, a3);
-            mma_16816(st.O[2 * c + 1], a0, a1, a2, a3, P[u][0], P[u][1]);
+            mma_16816(st.O[2 * c + 1], a0, a1, a2, a3, p0, p1);
         }
     }
 }
@@ -1220,10 +1315,10 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
                 if (r0 < p.G) {
                     const uint32_t *row = reinterpret_cast<const uint32_t *>(qs + r0 * D * 2);
                     if constexpr (L::BYTE) {
-                        // dims 4 w + 16 t + 64 c .. of step x = 4 c + w: 0 and 2, 1 and 3 (see byte_tile())
+                        // dims 4 w + 16 t + 64 c .. of step x = 4 c + w (see byte_tile())
                         const uint2 q4 = *reinterpret_cast<const uint2 *>(row + 32 * (x >> 2) + 8 * (lane & 3) + 2 * (x & 3));
-                        qf[x][0] = __byte_perm(q4.x, q4.y, 0x5410);
-                        qf[x][1] = __byte_perm(q4.x, q4.y, 0x7632);
+                        qf[x][0] = q4.x;
+                        qf[x][1] = q4.y;
                     } else {
                         qf[x][0] = row[8 * x + (lane & 3)];
                         qf[x][1] = row[8 * x + 4 + (lane & 3)];
@@ -1362,6 +1457,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, KIND, CLUSTER>::kCtasPerSm
         if (line * 128 < (int64_t)p.B * p.bt_stride * 4)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.bt) + line * 128));
     }
+    if constexpr (L::BYTE)
+        if (threadIdx.x < 32)
+            hint_first_tiles<D, KIND, CLUSTER>(p);
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x >= 32 * kCW)
@@ -1428,10 +1526,12 @@ struct Launch {
 // CTA with an SM of its own: 4 tiles, 9.0 and 12.0 us (one row of 8k); 8 tiles,
 // 13.3 and 14.4 us (one row of 16k), which two CTAs an SM of 4 tiles each better
 // where there can be (two rows of 2k .. 8k, 7.9 and 8.5 us); 4 tiles, two an SM,
-// 10.1 and 10.5 us (four rows), 8 tiles 15.0 and 13.4 us (eight).
+// 10.1 and 10.5 us (four rows), 8 tiles 15.0 and 13.4 us (eight).  8-bit, two an SM:
+// 8 tiles, 16.0 and 18.6 us (eight rows of 4k); 10 tiles, 15.6 and 19.5 us (32 rows in a
+// window of 1000); 16 tiles, 23.1 and 21.9 us (32 rows of 512 .. 2048).
 constexpr int kMaxTilesFp16 = 20;
 constexpr int kMaxTilesOwn[2] = {6, 8};  // CTAs with an SM of their own: tried first, tried last
-constexpr int kMaxTilesShared = 4;
+constexpr int kMaxTilesShared[2] = {4, 10};  // 4-bit, 8-bit
 
 template <int D, int KIND>
 cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParams p, int sms, cudaStream_t s)
@@ -1460,7 +1560,7 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
     const int n = top + 1, tries = most < 2 || units > room ? 0 : L::QUANT ? 2 * n : n;
     for (int t = 0; t < tries; ++t) {
         const int cl = L::QUANT ? own + t % n : top - t;
-        const int limit = !L::QUANT ? kMaxTilesFp16 : units << cl <= sms ? kMaxTilesOwn[t / n] : kMaxTilesShared;
+        const int limit = !L::QUANT ? kMaxTilesFp16 : units << cl <= sms ? kMaxTilesOwn[t / n] : kMaxTilesShared[L::BYTE];
         if (cl > top || most > (int64_t)limit << cl)
             continue;
         cudaError_t e = prepare<D, KIND, true>(k);

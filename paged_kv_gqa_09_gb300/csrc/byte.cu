@@ -373,14 +373,11 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) byte_read_kernel(const Qu
             }
         }
         // the scale is an fp16 number too, and so are the products
-        const __half2 s2 = __float2half2_rn(s != s ? s : byte_pow2(byte_exponent<FMT>(s) + kByteShift<FMT>));
+        const __half2 s2 = __float2half2_rn(s != s ? s : byte_pow2(byte_exponent<FMT>(s)));
         auto value = [&](uint32_t w, uint32_t &lo, uint32_t &hi) {
-            uint32_t even, odd;
-            byte_numbers<FMT>(w, even, odd);
-            even = byte_word(__hmul2(byte_half2(even), s2));
-            odd = byte_word(__hmul2(byte_half2(odd), s2));
-            lo = __byte_perm(even, odd, 0x5410);
-            hi = __byte_perm(even, odd, 0x7632);
+            byte_numbers<FMT>(w, lo, hi);
+            lo = byte_word(__hmul2(byte_half2(lo), s2));
+            hi = byte_word(__hmul2(byte_half2(hi), s2));
         };
 #pragma unroll
         for (int u = 0; u < TL; ++u) {

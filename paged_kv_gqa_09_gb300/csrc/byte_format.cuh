@@ -107,48 +107,47 @@ struct ByteQuantiser {
     }
 };
 
-// Codes as fp16 numbers: bytes 0 and 2 of a word, and bytes 1 and 3.  e4m3: 2^-8
-// of the number each, exactly: exponent and mantissa bits under fp16's bias,
-// subnormals included (a NaN's bits, which no code has, are a number too).
+// The codes of a word as fp16 numbers: bytes 0 and 1, and bytes 2 and 3.
 template <int FMT>
-__device__ __forceinline__ void byte_numbers(uint32_t w, uint32_t &even, uint32_t &odd)
+__device__ __forceinline__ void byte_numbers(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
     if constexpr (FMT == kInt8) {
         // n + 128 as the low byte of 1024 + (n + 128)
         const __half2 bias = byte_half2(0x64806480u);  // 1152
         const uint32_t u = w ^ 0x80808080u;
-        even = byte_word(__hsub2(byte_half2((u & 0x00ff00ffu) | 0x64006400u), bias));
-        odd = byte_word(__hsub2(byte_half2(__byte_perm(u, 0x64646464u, 0x4341)), bias));
+        lo = byte_word(__hsub2(byte_half2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
+        hi = byte_word(__hsub2(byte_half2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
     } else {
-        odd = ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u);
-        const uint32_t v = w << 8;
-        even = ((v >> 1) & 0x3f803f80u) | (v & 0x80008000u);
+        // the conversion of the type: shifts and masks of exponent and mantissa under fp16's bias take seven
+        // instructions a word instead of two (120k tokens of 8 heads decoded in 45.4 us, 43.7 with this)
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     }
 }
-
-// What byte_numbers() leaves out of a number's size.
-template <int FMT>
-constexpr int kByteShift = FMT == kInt8 ? 0 : 8;
 
 // Four codes c 2^k (k <= 0) rounded to codes again, ties to even.
 template <int FMT>
 __device__ __forceinline__ uint32_t byte_shift(uint32_t w, int k)
 {
-    uint32_t even, odd;
-    byte_numbers<FMT>(w, even, odd);
-    const float f = byte_pow2(max(k + kByteShift<FMT>, -100));
+    uint32_t lo, hi;
+    byte_numbers<FMT>(w, lo, hi);
+    const float f = byte_pow2(max(k, -100));
     auto scaled = [&](uint32_t x) {
         const float2 v = __half22float2(byte_half2(x));
         return make_float2(v.x * f, v.y * f);
     };
-    const float2 a = scaled(even), b = scaled(odd);
+    const float2 a = scaled(lo), b = scaled(hi);
     auto code = [](float x) -> uint32_t {
         if constexpr (FMT == kInt8)
             return (uint32_t)__float2int_rn(x) & 255u;
         else
             return (uint32_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
     };
-    return code(a.x) | code(b.x) << 8 | code(a.y) << 16 | code(b.y) << 24;
+    return code(a.x) | code(a.y) << 8 | code(b.x) << 16 | code(b.y) << 24;
 }
 
 // A 4 x 4 transposition of bytes.
