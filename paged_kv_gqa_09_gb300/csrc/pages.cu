@@ -234,34 +234,39 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
                 }
         } else {
             const int lo = max(t0, s.off[0]), hi = min(t1, s.off[nr]);
-            for (long long q = lo / 4 + threadIdx.x; q * 4 < hi; q += THREADS) {
+            int r = 0;
+            for (long long q = lo / 4 + threadIdx.x; lo < hi && q * 4 < hi; q += THREADS) {
                 const int x0 = (int)q * 4;
-                int r = 0, up = nr - 1;  // the last row at or before the group's first token
-                while (r < up) {
-                    const int mid = (r + up + 1) >> 1;
-                    if (s.off[mid] <= max(x0, lo))
-                        r = mid;
-                    else
-                        up = mid - 1;
+                if (max(x0, lo) >= s.off[r + 1]) {  // the last row at or before the group's first token
+                    int up = nr - 1;
+                    for (++r; r < up;) {
+                        const int mid = (r + up + 1) >> 1;
+                        if (s.off[mid] <= max(x0, lo))
+                            r = mid;
+                        else
+                            up = mid - 1;
+                    }
                 }
                 long long slot[4];
                 int pos[4];
                 if (x0 >= lo && x0 + 4 <= min(hi, s.off[r + 1]) && s.rank[r] >= 0) {
                     // four tokens of one row, on one page or two
-                    const int N = s.len[r], at = N + (x0 - s.off[r]), have = pages_of(p, N), rank = s.rank[r], held = s.page[r];
-                    const int b0 = at >> p.log2P, b1 = (at + 3) >> p.log2P;
-                    const int p0 = page_of(c0 + r, b0, b0 - have, rank, held);
-                    const int p1 = b1 == b0 ? p0 : page_of(c0 + r, b1, b1 - have, rank, held);
+                    const int N = s.len[r], at = N + (x0 - s.off[r]), in = at & mask, left = mask + 1 - in, blk = at >> p.log2P;
+                    const int j = blk - pages_of(p, N), top = count - 1 - s.rank[r] - j;
+                    const int page0 = j < 0 ? s.page[r] : p.free_pages[top], page1 = left < 4 ? p.free_pages[top - 1] : page0;
+                    if ((unsigned)page0 < (unsigned)p.num_pages && (unsigned)page1 < (unsigned)p.num_pages) {
+                        const long long a = ((long long)page0 << p.log2P) + in, b = ((long long)page1 << p.log2P) - left;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int in = (at + u) & mask, page = (at + u) >> p.log2P == b0 ? p0 : p1;
-                        slot[u] = page < 0 ? -1 : ((long long)page << p.log2P) + in;
-                        pos[u] = page < 0 ? 0 : at + u;
-                        if (in == 0)  // a new page starts with a new token
-                            p.bt[(int64_t)(c0 + r) * p.bt_stride + ((at + u) >> p.log2P)] = page;
+                        for (int u = 0; u < 4; ++u) {
+                            slot[u] = (u < left ? a : b) + u;
+                            pos[u] = at + u;
+                        }
+                        store4(x0, slot, pos);
+                        // a new page starts with a new token, at most one page among four tokens
+                        if (in == 0 || left < 4)
+                            p.bt[(int64_t)(c0 + r) * p.bt_stride + blk + (in != 0)] = page1;
+                        continue;
                     }
-                    store4(x0, slot, pos);
-                    continue;
                 }
                 for (int u = 0; u < 4; ++u) {
                     const int x = x0 + u;
