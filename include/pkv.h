@@ -394,13 +394,13 @@ int pkv_decode_step_noalloc(const pkv_shape_t *shape, const pkv_plan_cfg_t *cfg,
  * where field 0 of a half is bits 6-9, field 1 bits 2-5, field 2 bits 10-13 and
  * field 3 the code's low two bits at 14-15 and its high two at 0-1.
  *
- * The calls below take one workspace of pkv_attn_workspace_size() bytes, zeroed
- * once after allocation; its counters are back at zero after every launch (zero
- * it again after one that reported PKV_ETIMEOUT), and pkv_get_error() reads its
- * error word.  Calls on one workspace must not
- * overlap on the GPU (two graphs that may run at once need one each).  They use
- * the shape's B (append and read: up to 2^30; the decodes: up to 2^25), Hkv, d,
- * page_size, num_pages and bt_stride; the decodes Hq and scale too. */
+ * The calls from here to the 8-bit cache's take one workspace of
+ * pkv_attn_workspace_size() bytes, zeroed once after allocation; its counters are
+ * back at zero after every launch (zero it again after one that reported
+ * PKV_ETIMEOUT), and pkv_get_error() reads its error word.  Calls on one workspace
+ * must not overlap on the GPU (two graphs that may run at once need one each).
+ * They use the shape's B (append and read: up to 2^30; the decodes: up to 2^25),
+ * Hkv, d, page_size, num_pages and bt_stride; the decodes Hq and scale too. */
 
 /* Tokens a query sees: the first `sinks` of its row and the last `window`
  * (both >= 0; they may overlap).  With both 0 it sees none. */
@@ -413,7 +413,7 @@ typedef struct {
  * (0 for a bad shape). */
 size_t pkv_quant_page_bytes(const pkv_shape_t *shape);
 
-/* Bytes of the workspace of the four calls below (0 for a bad shape).  It grows
+/* Bytes of the workspace of the calls below (0 for a bad shape).  It grows
  * with Hq / Hkv and d only; one of a larger size serves every smaller shape, so
  * batches of any B can share one. */
 size_t pkv_attn_workspace_size(const pkv_shape_t *shape);
@@ -555,7 +555,8 @@ size_t pkv_byte_page_bytes(const pkv_shape_t *shape);
 /* pkv_byte_append -- quantise new tokens into the 8-bit cache.  One kernel launch.
  * Arguments, refusals and errors are those of pkv_quant_append.  A row or call that
  * is refused on account of a page, or of offsets that do not ascend, may have
- * rounded the earlier tokens of its last block to a greater scale already. */
+ * rounded the earlier tokens of its last block to a greater scale already.  New
+ * tokens of two rows must not share a scale block either (a page's SB tokens). */
 int pkv_byte_append(const pkv_shape_t *shape, void *d_ws, int32_t format, const void *d_k_new, const void *d_v_new,
                   int64_t new_stride, int32_t total_new, const int32_t *d_new_offsets, const int32_t *d_block_table,
                   const int32_t *d_seq_lens, int32_t *d_seq_lens_out, void *d_byte_cache, void *stream);

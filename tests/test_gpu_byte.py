@@ -341,6 +341,20 @@ def test_a_zero_filled_cache_holds_zeros():
         b.ok()
 
 
+@FORMATS
+@pytest.mark.parametrize("B", [33, 64, 65, 130, 1100])
+def test_many_rows(fmt, B):
+    """Rows found in one look and by a search, with and without new tokens, written, read and decoded."""
+    rng = np.random.default_rng(B)
+    first, new = rng.integers(0, 20, B).tolist(), (rng.integers(0, 40, B) * rng.integers(0, 2, B)).tolist()
+    b = Batch(fmt, [x + y for x, y in zip(first, new)], Hkv=1, G=2, d=64, P=16, seed=B)
+    b.grow(first)
+    b.grow(new)
+    b.same()
+    b.same([x // 2 for x in first])
+    b.check(queries(b))
+
+
 @pytest.mark.parametrize("Hkv", [1824, 2048])
 def test_few_tokens_of_very_many_heads(Hkv):
     b = Batch(R.E4M3, [16], Hkv=Hkv, G=1, d=64, P=8, seed=14)
