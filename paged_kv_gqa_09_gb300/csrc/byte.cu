@@ -44,6 +44,7 @@ template <int D, int LG>
 struct Lane {
     static constexpr int kPieces = D / 8, kGroups = 32 / kPieces;
     static constexpr int kTokens = (1 << LG) / kGroups < 4 ? 4 : (1 << LG) / kGroups;
+    static constexpr int kAtOnce = 8 / kTokens;  // sides whose loads a lane may have on their way together
     const int piece, first;
     __device__ __forceinline__ Lane() : piece((threadIdx.x & 31) % kPieces), first((threadIdx.x & 31) / kPieces * kTokens) {}
     __device__ __forceinline__ bool any() const { return kTokens * kGroups == 1 << LG || first < 1 << LG; }
@@ -111,10 +112,99 @@ struct NewScale {
     }
 };
 
-// A scale block (2^LG positions from pos0 on, the first token's place in its
-// page's block r0) for some of the heads' sides (2 h: K, 2 h + 1: V), then the
-// next such unit a grid further on.
+// One head's side of a scale block: positions `first` .. of this lane's tokens x of
+// a row whose N cached tokens n new ones follow (zeros where there is no new one).
+// hb: the head's block in its page; r0: the scale block's first token there.
 template <int D, int FMT, int LG>
+__device__ __forceinline__ void store_side(const Lane<D, LG> &ln, uint8_t *hb, int tb, int r0, bool v,
+                                           const uint4 (&x)[Lane<D, LG>::kTokens], int first, int N, int n, bool held)
+{
+    constexpr int TL = Lane<D, LG>::kTokens;
+    float *scale = reinterpret_cast<float *>(hb + byte_scale_part<D>(tb, r0, LG)) + v;
+    const float was = held ? *scale : 0.f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < TL; ++u)
+        top = max(top, greatest(x[u]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    const NewScale<FMT> ns(top, held, was);
+    const ByteQuantiser<FMT> code(ns.e, top);
+    if (ln.any() && !v) {
+#pragma unroll
+        for (int u = 0; u < TL; ++u) {
+            const int pos = first + u;
+            uint2 *to = reinterpret_cast<uint2 *>(hb + byte_k_at<D>(r0 + ln.first + u, 8 * ln.piece));
+            if (pos >= N && pos < N + n) {
+                *to = make_uint2(code(x[u].x, x[u].y), code(x[u].z, x[u].w));
+            } else if (pos < N && ns.grow) {
+                const uint2 c = *to;
+                *to = make_uint2(byte_shift<FMT>(c.x, -ns.grow), byte_shift<FMT>(c.y, -ns.grow));
+            }
+        }
+    } else if (ln.any()) {
+        uint8_t *part = hb + byte_v_part<D>(tb, r0, LG);
+#pragma unroll
+        for (int q = 0; q < TL; q += 4) {
+            const int pos = first + q;
+            if (pos >= N + n || (pos + 4 <= N && !ns.grow))
+                continue;
+            uint4 lo = byte_transpose(code(x[q].x, x[q].y), code(x[q + 1].x, x[q + 1].y), code(x[q + 2].x, x[q + 2].y),
+                                      code(x[q + 3].x, x[q + 3].y));
+            uint4 hi = byte_transpose(code(x[q].z, x[q].w), code(x[q + 1].z, x[q + 1].w), code(x[q + 2].z, x[q + 2].w),
+                                      code(x[q + 3].z, x[q + 3].w));
+            uint4 *to = reinterpret_cast<uint4 *>(part + byte_v_at(2 * ln.piece, (ln.first + q) >> 2, LG));
+            uint4 *to2 = reinterpret_cast<uint4 *>(part + byte_v_at(2 * ln.piece + 1, (ln.first + q) >> 2, LG));
+            if (pos < N) {  // earlier tokens' bytes stay
+                const uint32_t keep = pos + 4 <= N ? 0xffffffffu : 0xffffffffu >> (8 * (pos + 4 - N));
+                auto join = [&](uint32_t now, uint32_t old) {
+                    if (ns.grow)
+                        old = byte_shift<FMT>(old, -ns.grow);
+                    return (old & keep) | (now & ~keep);
+                };
+                const uint4 a = *to, b = *to2;
+                lo = make_uint4(join(lo.x, a.x), join(lo.y, a.y), join(lo.z, a.z), join(lo.w, a.w));
+                hi = make_uint4(join(hi.x, b.x), join(hi.y, b.y), join(hi.z, b.z), join(hi.w, b.w));
+            }
+            *to = lo;
+            *to2 = hi;
+        }
+    }
+    __syncwarp();  // every lane has read the scale
+    if ((threadIdx.x & 31) == 0)
+        *scale = ns.s;
+}
+
+// A group's scale block: found, fitting, and its page; `bad` where its id is out of range.
+struct Block {
+    int64_t pos0;
+    int off, n, N, page, r0;
+    bool any, bad;
+};
+template <int LG>
+__device__ __forceinline__ Block find_block(const QuantAppendParams &p, int64_t gs)
+{
+    Block b = {};
+    const Row row = find_row<LG>(gs, p.offsets, p.B, p.seq_lens, nullptr);
+    b.off = row.off, b.n = row.n, b.N = row.a;
+    if (!append_group(gs, row.i, b.off, b.n, b.N, b.pos0, LG) || !append_fits(p, row.i, b.N, b.off, b.n, false))
+        return b;
+    b.page = p.bt[(int64_t)row.i * p.bt_stride + (b.pos0 >> p.log2P)];
+    b.any = b.page >= 0 && b.page < p.num_pages;
+    b.bad = !b.any;
+    if (b.bad && (threadIdx.x & 31) == 0)
+        report_error(p.ws, kErrBadPage, row.i, (int)(b.pos0 >> p.log2P), b.page);
+    b.r0 = (int)b.pos0 & ((1 << p.log2P) - 1);  // within the page
+    return b;
+}
+template <int D>
+__device__ __forceinline__ uint8_t *block_of(const QuantAppendParams &p, int page, int slot)
+{
+    return p.cache + (int64_t)page * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * byte_block_bytes(1 << p.tb_log2, D);
+}
+
+// A scale block for some of the heads' sides (2 h: K, 2 h + 1: V), AT of them at
+// once, then the next such unit a grid further on.
+template <int D, int FMT, int LG, int AT>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) byte_append_kernel(const QuantAppendParams p)
 {
     using Ln = Lane<D, LG>;
@@ -122,7 +212,6 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) byte_append_kernel(cons
     __shared__ int s_seen;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
     const Ln ln;
     const int tb = 1 << p.tb_log2;
     // what the last CTA needs of its first rows, on its way already
@@ -138,89 +227,32 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) byte_append_kernel(cons
     const unsigned line = warp / (unsigned)p.parts;
     const int it0 = (int)(warp - line * p.parts) * p.its_per_part, it1 = min(it0 + p.its_per_part, 2 * p.Hkv);
     for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
-        const Row row = find_row<LG>(gs, p.offsets, p.B, p.seq_lens, nullptr);
-        const int i = row.i, off = row.off, n = row.n, N = row.a;
-        int64_t pos0;
-        if (!append_group(gs, i, off, n, N, pos0, LG) || !append_fits(p, i, N, off, n, false))
+        const Block b = find_block<LG>(p, gs);
+        bad |= b.bad;
+        if (!b.any)
             continue;
-        const int page = p.bt[(int64_t)i * p.bt_stride + (pos0 >> p.log2P)];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0)
-                report_error(p.ws, kErrBadPage, i, (int)(pos0 >> p.log2P), page);
-            bad = true;
-            continue;
-        }
-        const int slot = (int)pos0 & ((1 << p.log2P) - 1), r0 = slot & (tb - 1);
-        uint8_t *blk = p.cache + (int64_t)page * p.Hkv * p.page_head_bytes + (int64_t)(slot >> p.tb_log2) * byte_block_bytes(tb, D);
-        const int first = (int)pos0 + ln.first;  // of this lane's positions; the row's end is an int
-        const bool held = pos0 < N;              // the block has earlier tokens
-        const int64_t from = (int64_t)off * p.new_stride + 8 * ln.piece;
-        for (int it = it0; it < it1; ++it) {
-            const int h = it >> 1;
-            const bool v = it & 1;
-            uint8_t *hb = blk + h * p.page_head_bytes;
-            float *scale = reinterpret_cast<float *>(hb + byte_scale_part<D>(tb, r0, LG)) + v;
-            uint4 x[TL];
-            uint32_t top = 0;
+        uint8_t *blk = block_of<D>(p, b.page, b.r0);
+        const int first = (int)b.pos0 + ln.first;  // of this lane's positions; the row's end is an int
+        const int64_t from = (int64_t)b.off * p.new_stride + 8 * ln.piece;
+        for (int it2 = it0; it2 < it1; it2 += AT) {
+            uint4 x[AT][TL];
 #pragma unroll
-            for (int u = 0; u < TL; ++u) {
-                const int pos = first + u;
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (ln.any() && pos >= N && pos < N + n)
-                    x[u] = *reinterpret_cast<const uint4 *>((v ? p.v_new : p.k_new) + from + (int64_t)(pos - N) * p.new_stride + h * D);
-            }
-            const float was = held ? *scale : 0.f;
+            for (int e = 0; e < AT; ++e)
 #pragma unroll
-            for (int u = 0; u < TL; ++u)
-                top = max(top, greatest(x[u]));
-            top = __reduce_max_sync(0xffffffffu, top);
-            const NewScale<FMT> ns(top, held, was);
-            const ByteQuantiser<FMT> code(ns.e, top);
-            if (ln.any()) {
-                if (!v) {
-#pragma unroll
-                    for (int u = 0; u < TL; ++u) {
-                        const int pos = first + u;
-                        uint2 *to = reinterpret_cast<uint2 *>(hb + byte_k_at<D>(r0 + ln.first + u, 8 * ln.piece));
-                        if (pos >= N && pos < N + n) {
-                            *to = make_uint2(code(x[u].x, x[u].y), code(x[u].z, x[u].w));
-                        } else if (pos < N && ns.grow) {
-                            const uint2 c = *to;
-                            *to = make_uint2(byte_shift<FMT>(c.x, -ns.grow), byte_shift<FMT>(c.y, -ns.grow));
-                        }
-                    }
-                } else {
-                    uint8_t *part = hb + byte_v_part<D>(tb, r0, LG);
-#pragma unroll
-                    for (int q = 0; q < TL; q += 4) {
-                        const int pos = first + q;
-                        if (pos >= N + n || (pos + 4 <= N && !ns.grow))
-                            continue;
-                        uint4 lo = byte_transpose(code(x[q].x, x[q].y), code(x[q + 1].x, x[q + 1].y), code(x[q + 2].x, x[q + 2].y),
-                                                code(x[q + 3].x, x[q + 3].y));
-                        uint4 hi = byte_transpose(code(x[q].z, x[q].w), code(x[q + 1].z, x[q + 1].w), code(x[q + 2].z, x[q + 2].w),
-                                                code(x[q + 3].z, x[q + 3].w));
-                        uint4 *to = reinterpret_cast<uint4 *>(part + byte_v_at(2 * ln.piece, (ln.first + q) >> 2, LG));
-                        uint4 *to2 = reinterpret_cast<uint4 *>(part + byte_v_at(2 * ln.piece + 1, (ln.first + q) >> 2, LG));
-                        if (pos < N) {  // earlier tokens' bytes stay
-                            const uint32_t keep = 0xffffffffu >> (8 * max(pos + 4 - N, 0));
-                            const uint32_t all = pos + 4 <= N ? 0xffffffffu : keep;
-                            auto join = [&](uint32_t now, uint32_t old) {
-                                if (ns.grow)
-                                    old = byte_shift<FMT>(old, -ns.grow);
-                                return (old & all) | (now & ~all);
-                            };
-                            const uint4 a = *to, b = *to2;
-                            lo = make_uint4(join(lo.x, a.x), join(lo.y, a.y), join(lo.z, a.z), join(lo.w, a.w));
-                            hi = make_uint4(join(hi.x, b.x), join(hi.y, b.y), join(hi.z, b.z), join(hi.w, b.w));
-                        }
-                        *to = lo;
-                        *to2 = hi;
-                    }
+                for (int u = 0; u < TL; ++u) {
+                    const int it = it2 + e, pos = first + u;
+                    x[e][u] = make_uint4(0, 0, 0, 0);
+                    if (ln.any() && it < it1 && pos >= b.N && pos < b.N + b.n)
+                        x[e][u] = *reinterpret_cast<const uint4 *>((it & 1 ? p.v_new : p.k_new) + from +
+                                                                   (int64_t)(pos - b.N) * p.new_stride + (it >> 1) * D);
                 }
+#pragma unroll
+            for (int e = 0; e < AT; ++e) {
+                const int it = it2 + e;
+                if (it < it1)
+                    store_side<D, FMT, LG>(ln, blk + (it >> 1) * p.page_head_bytes, tb, b.r0 & (tb - 1), it & 1, x[e], first, b.N,
+                                           b.n, b.pos0 < b.N);
             }
-            if (lane == 0)
-                *scale = ns.s;
         }
     }
     append_finish<kThreads>(p, bad, my_off, my_n, my_N, &s_seen);
@@ -273,6 +305,7 @@ __global__ void __launch_bounds__(kOneThreads) byte_append_one_kernel(const Quan
             top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const NewScale<FMT> ns(top, u > 0, was);
         const uint32_t c = ByteQuantiser<FMT>(ns.e, top)(x.x, x.y);
+        __syncwarp();  // every lane has read the scale
         if (!there)
             continue;
         if (!v) {
@@ -409,17 +442,14 @@ cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// How the blocks' sides are split over warps: kSides each, one where that makes
-// less than 4096 warps; of an append, which walks the line, no more parts than
-// there are warps.
+// How the blocks' sides are split over warps: one each where that is no more than
+// one wave of them, else kSides.  Of eight heads appended, one and kSides a warp: 500
+// tokens 4.3 and 5.7 us, 2k 6.0 and 6.2, 4k 10.8 and 9.7 us.
 template <class P>
-void split_sides(P &p, int lg, int64_t most, int &per)
+void split_sides(P &p, int lg, int64_t wave, int &per)
 {
     p.groups = append_groups(p.T, p.B, lg);
-    per = p.groups * p.Hkv < 4096 ? 1 : kSides;
-    const int64_t parts = (2 * (int64_t)p.Hkv + per - 1) / per;
-    if (parts > most)
-        per = (int)((2 * (int64_t)p.Hkv + most - 1) / most);
+    per = 2 * p.groups * p.Hkv <= wave ? 1 : kSides;
     p.parts = (2 * p.Hkv + per - 1) / per;
 }
 
@@ -430,17 +460,23 @@ cudaError_t launch_append(QuantAppendParams p, int sms, cudaStream_t s)
         const int64_t threads = 32 * ((2 * (int64_t)p.Hkv * D + 127) / 128);
         return launch(byte_append_one_kernel<D, FMT, LG>, p, p.B, (int)(threads < kOneThreads ? threads : kOneThreads), s);
     }
-    const int64_t resident = (int64_t)kAppendCtas * sms * kWarps;
-    split_sides(p, LG, resident, p.its_per_part);
-    const int64_t all = (p.groups * p.parts + kWarps - 1) / kWarps, most = resident / kWarps;
-    const int64_t grid = all < most ? all : most;
-    return launch(byte_append_kernel<D, FMT, LG>, p, grid, kThreads, s);
+    const int64_t most = (int64_t)kAppendCtas * sms, wave = most * kWarps;
+    split_sides(p, LG, wave, p.its_per_part);
+    if (p.parts > wave) {  // a warp keeps its part: no more of them than there are warps
+        p.its_per_part = (int)((2 * (int64_t)p.Hkv + wave - 1) / wave);
+        p.parts = (2 * p.Hkv + p.its_per_part - 1) / p.its_per_part;
+    }
+    const int64_t all = (p.groups * p.parts + kWarps - 1) / kWarps, grid = all < most ? all : most;
+    // 64k tokens of 32 heads of d = 64: two sides at once 149 us, one after the other 161 us
+    constexpr int AT = Lane<D, LG>::kAtOnce;
+    return p.its_per_part < AT ? launch(byte_append_kernel<D, FMT, LG, 1>, p, grid, kThreads, s)
+                               : launch(byte_append_kernel<D, FMT, LG, AT>, p, grid, kThreads, s);
 }
 
 template <int D, int FMT, int LG>
 cudaError_t launch_read(QuantReadParams p, int sms, cudaStream_t s)
 {
-    split_sides(p, LG, INT64_MAX, p.heads_per_part);
+    split_sides(p, LG, (int64_t)kReadCtas * kWarps * sms, p.heads_per_part);
     return launch(byte_read_kernel<D, FMT, LG>, p, (p.groups * p.parts + kWarps - 1) / kWarps, kThreads, s);
 }
 

@@ -61,7 +61,9 @@ class Side:
         fmt, n = self.fmt, len(self.y)
         x = np.asarray(x).astype(np.float64)
         bound = TOP[fmt] * 2.0 ** MOST[fmt]
-        for b in range(n // self.sb, -(-(n + len(x)) // self.sb) if len(x) else 0):
+        first = n // self.sb
+        ys, es = [self.y[:first * self.sb]], [self.e[:first]]
+        for b in range(first, -(-(n + len(x)) // self.sb) if len(x) else 0):
             old = self.y[b * self.sb:]
             new = x[max(0, b * self.sb - n):(b + 1) * self.sb - n]
             nan = np.isnan(new).any((0, 2))
@@ -75,8 +77,10 @@ class Side:
                 nan |= np.isnan(was)
                 e = np.maximum(e, np.where(np.isnan(was), e, was))
                 old = nearest(old * 2.0 ** (np.where(np.isnan(was), e, was) - e)[:, None], fmt)
-            self.y = np.concatenate([self.y[:b * self.sb], old, nearest(clipped * 2.0 ** -e[:, None], fmt)])
-            self.e = np.concatenate([self.e[:b], np.where(nan, np.nan, e)[None]])
+            ys += [old, nearest(clipped * 2.0 ** -e[:, None], fmt)]
+            es.append(np.where(nan, np.nan, e)[None])
+        if len(x):
+            self.y, self.e = np.concatenate(ys), np.concatenate(es)
 
     def scales(self):
         """2^e of every token [n, Hkv]."""

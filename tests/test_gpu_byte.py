@@ -355,6 +355,34 @@ def test_many_rows(fmt, B):
     b.check(queries(b))
 
 
+@FORMATS
+@pytest.mark.parametrize("d,P,Hkv,new", [(128, 16, 4, [5000, 0, 3, 4300, 1]), (64, 8, 8, [8200]), (128, 64, 11, [8000, 17, 700]),
+                                         (64, 16, 19, [3, 9000]), (128, 8, 8, [1] * 100 + [8300]), (64, 256, 3, [8192, 64])])
+def test_many_tokens(fmt, d, P, Hkv, new):
+    """Prompts of many tokens behind rows of any length: blocks that hold earlier tokens, chunks of heads that are
+    not whole, tokens with a stride, a page out of range in the middle."""
+    first = [(7 * i) % 37 for i in range(len(new))]
+    b = Batch(fmt, [x + y for x, y in zip(first, new)], Hkv=Hkv, G=1, d=d, P=P, seed=len(new) + d)
+    b.grow(first, scale=0.1)
+    b.grow(new, pad=40)
+    b.same()
+    b.ok()
+    long = int(np.argmax(new))
+    b.lens[long] = first[long]
+    keep = b.bt.clone()
+    bad = (first[long] + 100) // P + 1
+    b.bt[long, bad] = b.num_pages + 3
+    before = [len(x.y) for x in b.k]
+    x = torch.zeros((8192 + sum(new), Hkv, d), dtype=torch.float16, device="cuda")  # tokens behind the last offset
+    off = np.array([0] * (long + 1) + [new[long]] * (b.B - long), np.int32)
+    api.pkv_byte_append(b.shape, b.ws, fmt, x, x, b.bt, b.lens, b.cache, new_offsets=dev(off))
+    assert b.lens.tolist() == [first[long] if i == long else n for i, n in enumerate(before)]  # the row keeps its length
+    st, msg = api.pkv_get_error(b.ws)
+    assert st == _lib.PKV_EDEVICE and f"row {long}, logical page {bad}" in msg
+    b.bt.copy_(keep)
+    b.ok()
+
+
 @pytest.mark.parametrize("Hkv", [1824, 2048])
 def test_few_tokens_of_very_many_heads(Hkv):
     b = Batch(R.E4M3, [16], Hkv=Hkv, G=1, d=64, P=8, seed=14)
