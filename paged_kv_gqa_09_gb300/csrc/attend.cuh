@@ -89,13 +89,14 @@ constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 // of its tokens per block added to what it is, so that its tiles' addresses are
 // constants.
 constexpr int kFp16 = 0, k4Bit = 0, k8Bit = 16;  // k8Bit + 16 FMT
+constexpr int kMany = 64;                        // + kMany: the 8-bit cache with d = 128, for many (row, head)s
 
 template <int KIND>
 constexpr bool kIs8Bit = KIND >= k8Bit;
 template <int KIND>
 constexpr int kBlockLog2 = KIND & 15;
 template <int KIND>
-constexpr int kFormat = KIND / 16 - 1;  // of an 8-bit cache
+constexpr int kFormat = KIND % kMany / 16 - 1;  // of an 8-bit cache
 
 // Bytes of a block, and of the numbers that scale its codes, with where they are:
 // where those are zero every value is.
@@ -143,13 +144,12 @@ struct Layout {
     // stages 166 us, two of three 208 us; clusters the latter (12.8 and 14.9 us
     // for eight rows).  The 8-bit cache's tiles are 32 KB with d = 128: two CTAs of
     // three stages (eight rows of up to 32k tokens 42.4 us, one of 32k 19.8 us;
-    // three of two 43.2 and 21.0 us, though 64 rows in a window of 4096 take 82 and 77
-    // us); tiles of 64 tokens, in five stages, leave a warp one block at a time
-    // (eight rows 57 us).  With d = 64, 64 rows of up to 32k: four CTAs of three stages
+    // three of two 43.2 and 21.0 us), but see launch_one() for kMany; tiles of 64
+    // tokens, in five stages, leave a warp one block at a time (eight rows 57 us).  With d = 64, 64 rows of up to 32k: four CTAs of three stages
     // 177.5 us, three of four 179.5 us, but in clusters 8.1 and 7.4 us (five rows in a
     // window)
-    static constexpr int kCtasPerSm = BYTE ? (D == 128 ? 2 : CLUSTER ? 3 : 4) : QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
-    static constexpr int kStages = BYTE ? (D == 64 && CLUSTER ? 4 : 3) : QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
+    static constexpr int kCtasPerSm = BYTE ? (D == 128 ? (KIND < kMany ? 2 : 3) : CLUSTER ? 3 : 4) : QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
+    static constexpr int kStages = BYTE ? (KIND >= kMany ? 2 : D == 64 && CLUSTER ? 4 : 3) : QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
@@ -1532,6 +1532,22 @@ struct Launch {
 constexpr int kMaxTilesFp16 = 20;
 constexpr int kMaxTilesOwn[2] = {6, 8};  // CTAs with an SM of their own: tried first, tried last
 constexpr int kMaxTilesShared[2] = {4, 10};  // 4-bit, 8-bit
+constexpr int kMaxTilesMany = 256;
+
+// The line of tiles in runs, a CTA each.
+template <int D, int KIND>
+cudaError_t launch_runs(const CUtensorMap &tk, const CUtensorMap &tv, const AttendParams &p, int64_t tiles, int sms, cudaStream_t s)
+{
+    using L = Layout<D, KIND, false>;
+    KernelOnDevice *k;
+    cudaError_t e = prepare<D, KIND, false>(k);
+    if (e != cudaSuccess)
+        return e;
+    int64_t grid = (int64_t)sms * L::kCtasPerSm;
+    grid = grid < kAttnMaxCtas ? grid : kAttnMaxCtas;
+    Launch l(grid < tiles ? grid : tiles, L::kAlloc, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, attend_kernel<D, KIND, false>, tk, tv, p);
+}
 
 template <int D, int KIND>
 cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParams p, int sms, cudaStream_t s)
@@ -1579,13 +1595,14 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
         p.cluster_log2 = cl;
         return cudaLaunchKernelEx(&l.cfg, attend_kernel<D, KIND, true>, tk, tv, p);
     }
-    cudaError_t e = prepare<D, KIND, false>(k);
-    if (e != cudaSuccess)
-        return e;
-    int64_t grid = (int64_t)sms * L::kCtasPerSm;
-    grid = grid < kAttnMaxCtas ? grid : kAttnMaxCtas;
-    Launch l(grid < tiles ? grid : tiles, L::kAlloc, 0, s);
-    return cudaLaunchKernelEx(&l.cfg, attend_kernel<D, KIND, false>, tk, tv, p);
+    // more (row, head)s than CTAs: their ends, which cost a CTA some microseconds without a load, are hidden by a third
+    // CTA per SM better than by a third stage.  64 rows in a window of 4096 82.6 and 76.6 us, 300 rows of up to 8k 106.9
+    // and 103.2 us, 100 of 100 15.0 and 13.2 us; but 64 rows of up to 60k 604 and 608 us, eight of up to 32k 42.4 and
+    // 43.2 us
+    if constexpr (L::BYTE && D == 128 && KIND < kMany)
+        if (units > (int64_t)sms * L::kCtasPerSm && most <= kMaxTilesMany)
+            return launch_runs<D, KIND + kMany>(tk, tv, p, tiles, sms, s);
+    return launch_runs<D, KIND>(tk, tv, p, tiles, sms, s);
 }
 
 }  // namespace
