@@ -8,9 +8,18 @@
 // are two ints each, tokens twelve bytes) and one launch without a grid-wide wait
 // does it all.  A page is entered in the block table by the thread of the token
 // at its start.  The last CTA to finish, when every other one has read the lengths
-// and the free count, advances them.
+// and the free count, advances them.  Latency bounds it: 1.1M tokens of 256 rows,
+// 14 MB, take 8.6 us, of which 1.8 are lengths and sums, 4 the tokens and 2.5 the
+// launch and the last CTA; a token for each of 64 rows 3.2 us, little more than an
+// empty launch among others.  A thread places pairs of tokens, four at a time: what
+// a warp stores is whole sectors (four tokens a thread left halves: 9.3 us), and the
+// loads of four pages are on their way at once (two 9.6, eight 9.0 us); two CTAs of
+// 256 threads per SM (one 10.8, two of 512 threads 12.3 us).
 //
-// slots: K and V of packed tokens go to their slots, 16 bytes a lane: a copy.
+// slots: K and V of packed tokens go to their slots, 16 bytes a lane: a copy.  35k
+// tokens of 8 heads, d = 128, 290 MB, take 44.4 us, 0.96 of the copy rate, with eight
+// pieces a lane on their way (four 44.8, two 47.1 us) and a warp per token (a grid of
+// 8 CTAs per SM 46.2 us).
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 
@@ -20,6 +29,7 @@ namespace {
 constexpr int kInvalid = -2;      // in place of a row's rank: no length that the table could hold
 constexpr int kNotServed = -1;    // no pages left for it, or no room in the packed buffer
 constexpr int kBadCta = 1 << 20;  // CTAs that met a bad page of the free list count this much more
+constexpr int kPairs = 4;         // of tokens that a thread has on their way at a time
 constexpr int kFewTokens = 4;     // new tokens of a row up to which its own thread places them
 
 // Two rows per thread are held at a time, with what their tokens need in shared memory.
@@ -174,43 +184,34 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
     const int t0 = (int)min(4 * per * blockIdx.x, (long long)p.T), t1 = (int)min(4 * per * (blockIdx.x + 1), (long long)p.T);
     long long off0 = 0, rank0 = 0;
     bool bad = false;
-    // The page of block blk of row i, the j-th new one of a row of this rank or (j < 0) the one that has room; -1 where
-    // its id is out of range.
-    auto page_of = [&](int i, int blk, int j, int rank, int held) {
-        if (j < 0)
-            return max(held, -1);
-        const int page = p.free_pages[count - 1 - rank - j];
-        if (page >= 0 && page < p.num_pages)
-            return page;
-        report_error(p.ws, kErrBadPage, i, blk, page);
-        bad = true;
-        return -1;
-    };
-    // Token x, the k-th new one of row i.
-    auto place = [&](int x, int i, int N, int k, int rank, int held, long long &slot, int &pos) {
-        const int at = N + k, blk = at >> p.log2P, in = at & mask, j = blk - pages_of(p, N);
-        slot = -1;
-        pos = 0;
-        if (rank == kInvalid)
-            return;
-        const int page = rank == kNotServed ? -1 : page_of(i, blk, j, rank, held);
-        if (j >= 0 && in == 0)
-            p.bt[(int64_t)i * p.bt_stride + blk] = page;
-        if (page >= 0) {
-            slot = ((long long)page << p.log2P) + in;
-            pos = at;
-        }
-    };
     auto store = [&](int x, long long slot, int pos) {
         p.slots[x] = slot;
         if (p.positions)
             p.positions[x] = pos;
     };
-    auto store4 = [&](int x, const long long (&slot)[4], const int (&pos)[4]) {
-        reinterpret_cast<longlong2 *>(p.slots + x)[0] = make_longlong2(slot[0], slot[1]);
-        reinterpret_cast<longlong2 *>(p.slots + x)[1] = make_longlong2(slot[2], slot[3]);
+    // Token x at position `at` of row i, which is on this page (of a row that is served).
+    auto place = [&](int x, int i, int at, int N, int rank, int page) {
+        const int blk = at >> p.log2P, in = at & mask, j = blk - pages_of(p, N);
+        if (rank < 0) {
+            if (rank == kNotServed && j >= 0 && in == 0)
+                p.bt[(int64_t)i * p.bt_stride + blk] = -1;
+            store(x, -1, 0);
+            return;
+        }
+        const bool there = page >= 0 && page < p.num_pages;
+        if (!there && j >= 0) {  // the page that had room is seen to elsewhere
+            report_error(p.ws, kErrBadPage, i, blk, page);
+            bad = true;
+        }
+        if (j >= 0 && in == 0)
+            p.bt[(int64_t)i * p.bt_stride + blk] = there ? page : -1;
+        store(x, there ? ((long long)page << p.log2P) + in : -1, there ? at : 0);
+    };
+    // Two tokens from an even one on.
+    auto store2 = [&](int x, long long slot0, long long slot1, int pos0, int pos1) {
+        *reinterpret_cast<longlong2 *>(p.slots + x) = make_longlong2(slot0, slot1);
         if (p.positions)
-            *reinterpret_cast<int4 *>(p.positions + x) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int2 *>(p.positions + x) = make_int2(pos0, pos1);
     };
     MapRow row[2];
     for (int c0 = 0; c0 < p.B && (alone || blockIdx.x == 0 || off0 < t1); c0 += kRows) {
@@ -227,55 +228,62 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 for (int k = max(t0 - row[u].off, 0); k < min(row[u].n, t1 - row[u].off); ++k) {
-                    long long slot;
-                    int pos;
-                    place(row[u].off + k, c0 + 2 * (int)threadIdx.x + u, row[u].N, k, row[u].rank, row[u].page, slot, pos);
-                    store(row[u].off + k, slot, pos);
+                    const int at = row[u].N + k, j = (at >> p.log2P) - pages_of(p, row[u].N);
+                    place(row[u].off + k, c0 + 2 * (int)threadIdx.x + u, at, row[u].N, row[u].rank,
+                          row[u].rank < 0 || j < 0 ? row[u].page : p.free_pages[count - 1 - row[u].rank - j]);
                 }
         } else {
             const int lo = max(t0, s.off[0]), hi = min(t1, s.off[nr]);
             int r = 0;
-            for (long long q = lo / 4 + threadIdx.x; lo < hi && q * 4 < hi; q += THREADS) {
-                const int x0 = (int)q * 4;
-                if (max(x0, lo) >= s.off[r + 1]) {  // the last row at or before the group's first token
-                    int up = nr - 1;
-                    for (++r; r < up;) {
-                        const int mid = (r + up + 1) >> 1;
-                        if (s.off[mid] <= max(x0, lo))
-                            r = mid;
-                        else
-                            up = mid - 1;
-                    }
-                }
-                long long slot[4];
-                int pos[4];
-                if (x0 >= lo && x0 + 4 <= min(hi, s.off[r + 1]) && s.rank[r] >= 0) {
-                    // four tokens of one row, on one page or two
-                    const int N = s.len[r], at = N + (x0 - s.off[r]), in = at & mask, left = mask + 1 - in, blk = at >> p.log2P;
-                    const int j = blk - pages_of(p, N), top = count - 1 - s.rank[r] - j;
-                    const int page0 = j < 0 ? s.page[r] : p.free_pages[top], page1 = left < 4 ? p.free_pages[top - 1] : page0;
-                    if ((unsigned)page0 < (unsigned)p.num_pages && (unsigned)page1 < (unsigned)p.num_pages) {
-                        const long long a = ((long long)page0 << p.log2P) + in, b = ((long long)page1 << p.log2P) - left;
+            for (long long x8 = lo & ~1; lo < hi && x8 < hi; x8 += 2 * kPairs * THREADS) {
+                // pairs of tokens, neighbouring threads' next to one another; all pages' loads before the first store
+                int row_of[kPairs], at[kPairs], page0[kPairs], page1[kPairs];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            slot[u] = (u < left ? a : b) + u;
-                            pos[u] = at + u;
+                for (int k = 0; k < kPairs; ++k) {
+                    const long long xl = x8 + 2 * (k * THREADS + (int)threadIdx.x);
+                    row_of[k] = -1;
+                    if (xl >= hi)
+                        continue;
+                    const int x = max((int)xl, lo);
+                    if (x >= s.off[r + 1]) {  // the last row at or before the pair's first token
+                        int up = nr - 1;
+                        for (++r; r < up;) {
+                            const int mid = (r + up + 1) >> 1;
+                            if (s.off[mid] <= x)
+                                r = mid;
+                            else
+                                up = mid - 1;
                         }
-                        store4(x0, slot, pos);
-                        // a new page starts with a new token, at most one page among four tokens
-                        if (in == 0 || left < 4)
-                            p.bt[(int64_t)(c0 + r) * p.bt_stride + blk + (in != 0)] = page1;
+                    }
+                    row_of[k] = r;
+                    at[k] = s.len[r] + (x - s.off[r]);
+                    const int j = (at[k] >> p.log2P) - pages_of(p, s.len[r]), top = count - 1 - s.rank[r] - j;
+                    const bool whole = x == (int)xl && x + 2 <= min(hi, s.off[r + 1]);  // both tokens are this row's
+                    page0[k] = s.rank[r] < 0 || j < 0 ? s.page[r] : p.free_pages[top];
+                    page1[k] = !whole || s.rank[r] < 0 ? -1 : (at[k] & mask) == mask ? p.free_pages[top - 1] : page0[k];
+                }
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) {
+                    if (row_of[k] < 0)
+                        continue;
+                    int y = row_of[k];
+                    const int in = at[k] & mask, blk = at[k] >> p.log2P, x = max((int)(x8 + 2 * (k * THREADS + (int)threadIdx.x)), lo);
+                    if ((unsigned)page0[k] < (unsigned)p.num_pages && (unsigned)page1[k] < (unsigned)p.num_pages) {
+                        const long long a = ((long long)page0[k] << p.log2P) + in;
+                        store2(x, a, in == mask ? (long long)page1[k] << p.log2P : a + 1, at[k], at[k] + 1);
+                        if (in == 0 || in == mask)  // a new page starts with a new token
+                            p.bt[(int64_t)(c0 + y) * p.bt_stride + blk + (in != 0)] = page1[k];
                         continue;
                     }
-                }
-                for (int u = 0; u < 4; ++u) {
-                    const int x = x0 + u;
-                    if (x < lo || x >= hi)
+                    // of two rows, of one that is not served, or on a page out of range
+                    place(x, c0 + y, at[k], s.len[y], s.rank[y], page0[k]);
+                    if ((x & 1) || x + 1 >= hi)
                         continue;
-                    while (r + 1 < nr && x >= s.off[r + 1])
-                        ++r;
-                    place(x, c0 + r, s.len[r], x - s.off[r], s.rank[r], s.page[r], slot[0], pos[0]);
-                    store(x, slot[0], pos[0]);
+                    while (y + 1 < nr && x + 1 >= s.off[y + 1])
+                        ++y;
+                    const int next = s.len[y] + (x + 1 - s.off[y]), j = (next >> p.log2P) - pages_of(p, s.len[y]);
+                    place(x + 1, c0 + y, next, s.len[y], s.rank[y],
+                          s.rank[y] < 0 || j < 0 ? s.page[y] : p.free_pages[count - 1 - s.rank[y] - j]);
                 }
             }
         }
@@ -287,13 +295,11 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
         }
     }
     // behind the last token
-    for (long long q = max((long long)t0, off0) / 4 + threadIdx.x; off0 < t1 && q * 4 < t1; q += THREADS) {
-        const int x0 = (int)q * 4, lo = max(t0, (int)off0);
-        if (x0 >= lo && x0 + 4 <= t1)
-            store4(x0, {-1, -1, -1, -1}, {0, 0, 0, 0});
+    for (long long x = (max((long long)t0, off0) & ~1ll) + 2 * threadIdx.x; off0 < t1 && x < t1; x += 2 * THREADS) {
+        if (x >= off0 && x + 2 <= t1)
+            store2((int)x, -1, -1, 0, 0);
         else
-            for (int x = max(x0, lo); x < min(x0 + 4, t1); ++x)
-                store(x, -1, 0);
+            store((int)(x < off0 ? x + 1 : x), -1, 0);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0)
         p.offsets[p.B] = (int)min(off0, (long long)p.T);
