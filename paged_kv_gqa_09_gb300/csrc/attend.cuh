@@ -98,8 +98,8 @@ constexpr int kBlockLog2 = KIND & 15;
 template <int KIND>
 constexpr int kFormat = KIND % kMany / 16 - 1;  // of an 8-bit cache
 
-// Bytes of a block, and of the numbers that scale its codes, with where they are:
-// where those are zero every value is.
+// Bytes of a block, and how one becomes zeros: by the numbers that scale its codes
+// or, where a code's own bits may be a NaN's (whatever shared memory held), whole.
 template <int D, int KIND>
 struct Block {
     using Q = QuantLayout<D>;
@@ -108,8 +108,8 @@ struct Block {
     __device__ static void clear(uint8_t *blk)
     {
         if constexpr (kIs8Bit<KIND>) {
-            for (int x = 0; x < byte_scale_bytes(kTokens); x += 4)
-                *reinterpret_cast<uint32_t *>(blk + 2 * kTokens * D + x) = 0;
+            for (int x = 0; x < byte_block_bytes(kTokens, D); x += 16)
+                *reinterpret_cast<uint4 *>(blk + x) = make_uint4(0, 0, 0, 0);
         } else {
             for (int x = 0; x < kTokens * Q::kParamRow; x += 4) {
                 *reinterpret_cast<uint32_t *>(blk + Q::k_params(kTokens) + x) = 0;

@@ -432,6 +432,32 @@ def test_decode_in_a_window(fmt, window, sinks, d, P):
 
 
 @FORMATS
+@pytest.mark.parametrize("P", [8, 16, 32, 64, 128])
+def test_more_heads_than_the_gpu_holds_ctas(fmt, P):
+    """Batches of many rows, whose (row, head)s come to more than two CTAs per SM."""
+    rng = np.random.default_rng(P)
+    lens = rng.integers(0, 400, 90).tolist()
+    lens[3] = lens[40] = 0
+    b = Batch(fmt, lens, Hkv=4, G=3, d=128, P=P, seed=P)
+    b.grow(lens)
+    b.check(queries(b))
+    b.check(queries(b, seed=6), 100, 5)
+    first = b.decode(queries(b))
+    again = b.decode(queries(b))
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    b.bt[7, 0] = -1
+    for side in (b.k[7], b.v[7]):
+        side.y[:P] = 0
+    o, lse = b.decode(queries(b))
+    assert lens[7] > 0 and api.pkv_get_error(b.ws)[0] == _lib.PKV_EDEVICE
+    b.compare(o, lse, queries(b))
+    assert _lib.load().pkv_test_starve_next_decodes(1) == 0
+    b.decode(queries(b))
+    assert api.pkv_get_error(b.ws)[0] in (_lib.PKV_ETIMEOUT, _lib.PKV_EDEVICE)
+    b.ws.zero_()
+
+
+@FORMATS
 @pytest.mark.parametrize("wide", [0, 4096])
 def test_blocks_of_very_unequal_scales(fmt, wide):
     """V blocks from 2^-20 to 2^14, K blocks alike with queries to match: the weights carry V's scales."""
@@ -537,6 +563,26 @@ def test_decode_reports_bad_pages_and_lengths(fmt):
     b.decode(q, 0, 4)
     assert api.pkv_get_error(b.ws)[0] == _lib.PKV_EDEVICE
     b.ok()
+
+
+@FORMATS
+@pytest.mark.parametrize("wide", [0, 4096])
+@pytest.mark.parametrize("d,P", [(128, 8), (64, 16), (128, 64), (64, 128)])
+def test_a_bad_page_counts_as_zeros(fmt, wide, d, P):
+    """Whatever the memory it would have gone to held: a batch whose bytes behind the rows are NaNs' goes first."""
+    b = Batch(fmt, [3 * P] * 6, d=d, P=P, seed=P, wide=wide)
+    b.grow([3 * P] * 6)
+    q = queries(b)
+    dirty = Batch(fmt, [1] * 300, d=d, P=P, seed=1, fill=0x7F, wide=wide)
+    dirty.grow([1] * 300)
+    b.bt[:, 1] = -5
+    for side in b.k + b.v:
+        side.y[P:2 * P] = 0
+    for _ in range(3):
+        dirty.decode(queries(dirty))
+        o, lse = b.decode(q)
+        b.compare(o, lse, q)
+        assert api.pkv_get_error(b.ws)[0] == _lib.PKV_EDEVICE
 
 
 @FORMATS
