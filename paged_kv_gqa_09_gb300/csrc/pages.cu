@@ -30,17 +30,16 @@ constexpr int kInvalid = -2;      // in place of a row's rank: no length that th
 constexpr int kNotServed = -1;    // no pages left for it, or no room in the packed buffer
 constexpr int kBadCta = 1 << 20;  // CTAs that met a bad page of the free list count this much more
 constexpr int kPairs = 4;         // of tokens that a thread has on their way at a time
-constexpr int kFewTokens = 4;     // new tokens of a row up to which its own thread places them
+constexpr int kFewTokens = 4;     // new tokens of a row up to which its own thread places them (64 rows 3.2 us, searched for 3.5)
 
 // Two rows per thread are held at a time, with what their tokens need in shared memory.
-template <int THREADS>
+constexpr int kMapThreads = 256, kMapRows = 2 * kMapThreads, kMapWarps = kMapThreads / 32;
 struct MapRows {
-    static constexpr int kRows = 2 * THREADS, kWarps = THREADS / 32;
-    int off[kRows + 1];  // first packed token, at most T
-    int len[kRows];      // N
-    int rank[kRows];     // pages that the rows before need, or one of the above
-    int page[kRows];     // of the row's last tokens, where that has room for more
-    long long sum[2][kWarps];
+    int off[kMapRows + 1];  // first packed token, at most T
+    int len[kMapRows];      // N
+    int rank[kMapRows];     // pages that the rows before need, or one of the above
+    int page[kMapRows];     // of the row's last tokens, where that has room for more
+    long long sum[2][kMapWarps];
 };
 
 struct MapRow {
@@ -55,11 +54,9 @@ __device__ __forceinline__ int pages_of(const MapParams &p, int N) { return (N >
 // Rows c0 + 2 tid and the next of this thread; off0 and rank0 are the sums over
 // the rows before c0 and become those over the rows before the next chunk's.
 // Returns whether every row has few new tokens.
-template <int THREADS>
-__device__ __forceinline__ bool map_rows(const MapParams &p, int c0, int count, MapRows<THREADS> &s, MapRow (&row)[2], long long &off0,
+__device__ __forceinline__ bool map_rows(const MapParams &p, int c0, int count, MapRows &s, MapRow (&row)[2], long long &off0,
                                          long long &rank0)
 {
-    constexpr int kWarps = MapRows<THREADS>::kWarps;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, mask = (1 << p.log2P) - 1;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -98,7 +95,7 @@ __device__ __forceinline__ bool map_rows(const MapParams &p, int c0, int count, 
     few = __syncthreads_and(few) != 0;
     long long off = off0 + a - n2[0] - n2[1], rank = rank0 + b - need2[0] - need2[1];
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
+    for (int v = 0; v < kMapWarps; ++v) {
         const long long x = s.sum[0][v], y = s.sum[1][v];
         off += v < w ? x : 0;
         rank += v < w ? y : 0;
@@ -123,8 +120,8 @@ __device__ __forceinline__ bool map_rows(const MapParams &p, int c0, int count, 
         s.len[x] = r.N;
         s.rank[x] = r.rank;
         s.page[x] = r.page;
-        if (x == MapRows<THREADS>::kRows - 1)
-            s.off[MapRows<THREADS>::kRows] = (int)min(off + n2[u], (long long)p.T);
+        if (x == kMapRows - 1)
+            s.off[kMapRows] = (int)min(off + n2[u], (long long)p.T);
         off += n2[u];
         rank += need2[u];
     }
@@ -167,11 +164,9 @@ __device__ __forceinline__ void map_finish(const MapParams &p, int c0, int count
     }
 }
 
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
+__global__ void __launch_bounds__(kMapThreads) map_pages_kernel(const MapParams p)
 {
-    constexpr int kRows = MapRows<THREADS>::kRows;
-    __shared__ MapRows<THREADS> s;
+    __shared__ MapRows s;
     __shared__ int s_taken, s_seen;
     pdl_wait();
     pdl_trigger();
@@ -214,9 +209,9 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
             *reinterpret_cast<int2 *>(p.positions + x) = make_int2(pos0, pos1);
     };
     MapRow row[2];
-    for (int c0 = 0; c0 < p.B && (alone || blockIdx.x == 0 || off0 < t1); c0 += kRows) {
+    for (int c0 = 0; c0 < p.B && (alone || blockIdx.x == 0 || off0 < t1); c0 += kMapRows) {
         const bool few = map_rows(p, c0, count, s, row, off0, rank0);
-        const int nr = min(p.B - c0, kRows);
+        const int nr = min(p.B - c0, kMapRows);
         if (blockIdx.x == 0) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -235,12 +230,12 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
         } else {
             const int lo = max(t0, s.off[0]), hi = min(t1, s.off[nr]);
             int r = 0;
-            for (long long x8 = lo & ~1; lo < hi && x8 < hi; x8 += 2 * kPairs * THREADS) {
+            for (long long x8 = lo & ~1; lo < hi && x8 < hi; x8 += 2 * kPairs * kMapThreads) {
                 // pairs of tokens, neighbouring threads' next to one another; all pages' loads before the first store
                 int row_of[kPairs], at[kPairs], page0[kPairs], page1[kPairs];
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) {
-                    const long long xl = x8 + 2 * (k * THREADS + (int)threadIdx.x);
+                    const long long xl = x8 + 2 * (k * kMapThreads + (int)threadIdx.x);
                     row_of[k] = -1;
                     if (xl >= hi)
                         continue;
@@ -267,7 +262,7 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
                     if (row_of[k] < 0)
                         continue;
                     int y = row_of[k];
-                    const int in = at[k] & mask, blk = at[k] >> p.log2P, x = max((int)(x8 + 2 * (k * THREADS + (int)threadIdx.x)), lo);
+                    const int in = at[k] & mask, blk = at[k] >> p.log2P, x = max((int)(x8 + 2 * (k * kMapThreads + (int)threadIdx.x)), lo);
                     if ((unsigned)page0[k] < (unsigned)p.num_pages && (unsigned)page1[k] < (unsigned)p.num_pages) {
                         const long long a = ((long long)page0[k] << p.log2P) + in;
                         store2(x, a, in == mask ? (long long)page1[k] << p.log2P : a + 1, at[k], at[k] + 1);
@@ -290,12 +285,12 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
         if (alone) {
             const bool any_bad = __syncthreads_or(bad) != 0;
             map_finish(p, c0, count, any_bad, row, &s_taken);
-        } else if (p.B > kRows) {
+        } else if (p.B > kMapRows) {
             __syncthreads();  // the sums are read until here
         }
     }
     // behind the last token
-    for (long long x = (max((long long)t0, off0) & ~1ll) + 2 * threadIdx.x; off0 < t1 && x < t1; x += 2 * THREADS) {
+    for (long long x = (max((long long)t0, off0) & ~1ll) + 2 * threadIdx.x; off0 < t1 && x < t1; x += 2 * kMapThreads) {
         if (x >= off0 && x + 2 <= t1)
             store2((int)x, -1, -1, 0, 0);
         else
@@ -312,11 +307,11 @@ __global__ void __launch_bounds__(THREADS) map_pages_kernel(const MapParams p)
         __syncthreads();
         if ((s_seen & (kBadCta - 1)) != (int)gridDim.x)
             return;
-        if (p.B <= kRows) {  // its rows are all there are
+        if (p.B <= kMapRows) {  // its rows are all there are
             map_finish(p, 0, count, s_seen >= kBadCta, row, &s_taken);
         } else {
             off0 = rank0 = 0;
-            for (int c0 = 0; c0 < p.B; c0 += kRows) {
+            for (int c0 = 0; c0 < p.B; c0 += kMapRows) {
                 map_rows(p, c0, count, s, row, off0, rank0);
                 map_finish(p, c0, count, s_seen >= kBadCta, row, &s_taken);
                 __syncthreads();
@@ -392,11 +387,8 @@ cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s
 
 cudaError_t launch_map_pages(const MapParams &p, int sms, cudaStream_t s)
 {
-    constexpr int kSmall = 128, kLarge = 256;
-    if (p.B <= 2 * kSmall && p.T <= 16 * kSmall)
-        return launch(map_pages_kernel<kSmall>, p, 1, kSmall, s);
-    const int64_t want = ((int64_t)p.T + 4 * kLarge - 1) / (4 * kLarge), most = 2 * (int64_t)sms;
-    return launch(map_pages_kernel<kLarge>, p, want < most ? want : most, kLarge, s);
+    const int64_t want = ((int64_t)p.T + 8 * kMapThreads - 1) / (8 * kMapThreads), most = 2 * (int64_t)sms;
+    return launch(map_pages_kernel, p, want < most ? want : most, kMapThreads, s);
 }
 
 cudaError_t launch_append_slots(const SlotParams &p, cudaStream_t s)

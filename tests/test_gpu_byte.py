@@ -483,6 +483,15 @@ def test_decode_of_large_and_tiny_values(fmt):
 
 
 @FORMATS
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
+def test_any_scale_of_the_scores(fmt, scale):
+    b = Batch(fmt, [300, 17], Hkv=2, G=3, d=128, P=32, seed=21, scale=scale)
+    b.grow([300, 17])
+    b.check(queries(b))
+    b.check(queries(b), 40, 3)
+
+
+@FORMATS
 @pytest.mark.parametrize("wide", [0, 4096])
 def test_scores_that_rise_and_fall_along_the_row(fmt, wide):
     b = Batch(fmt, [600, 600], Hkv=1, G=4, d=64, P=16, seed=17, scale=1.0, wide=wide)

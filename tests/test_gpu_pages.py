@@ -217,6 +217,37 @@ def test_binding_refuses_wrong_tensors():
             api.pkv_append_slots(**{**good, **bad})
 
 
+def test_calls_of_nothing():
+    """Empty batches, calls without tokens, an empty free list."""
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    half = lambda *n: torch.zeros(n, dtype=torch.float16, device="cuda")
+    i64 = torch.zeros(0, dtype=torch.int64, device="cuda")
+    cache, pool, table = api.byte_cache_zeros(4, 16, 2, 64), half(4, 16, 2, 64), i32(0).view(0, 3)
+    shape = api.make_byte_shape(8, 64, cache, table)
+    assert shape.B == 0
+    ws = torch.zeros(api.pkv_attn_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    api.pkv_map_pages(shape, ws, i32(0), i32(0), table, i32(0), i32(1), i64, i32(1))
+    api.pkv_append_slots(shape, ws, half(0, 2, 64), half(0, 2, 64), i64, pool, pool)
+    for fmt in (R.INT8, R.E4M3):
+        api.pkv_byte_append(shape, ws, fmt, half(0, 2, 64), half(0, 2, 64), table, i32(0), cache)
+        api.pkv_byte_read(shape, ws, fmt, cache, table, i32(0), i32(1), half(0, 2, 64), half(0, 2, 64))
+        api.pkv_byte_decode(shape, ws, fmt, half(0, 8, 64), cache, table, i32(0), half(0, 8, 64))
+    m = Map([5, 16, 0], 16, 2, 0)  # rows, but no pages and no tokens
+    m.free, m.fp = m.free[:0], i32(0)
+    m.count, m.fc = 0, i32(1)
+    m.check([0, 0, 0])
+    m.check([11, 0, 0], 16)  # what fits without a page
+    table = dev(np.array([[0, 1, 2], [3, 2, 1]], np.int32))
+    shape = api.make_byte_shape(8, 64, cache, table)
+    lens = dev(np.array([20, 0], np.int32))
+    out = i32(2)
+    for fmt in (R.INT8, R.E4M3):
+        api.pkv_byte_append(shape, ws, fmt, half(0, 2, 64), half(0, 2, 64), table, lens, cache, new_offsets=i32(3), seq_lens_out=out)
+        assert out.tolist() == [20, 0]
+    assert int(cache.count_nonzero()) == 0
+    assert api.pkv_get_error(ws)[0] == 0
+
+
 # ------------------------------------------------------------------ as they are used
 
 def serve(kind, steps, captured):
