@@ -85,6 +85,12 @@ constexpr int kTableLines = 32;  // lines of the block table each CTA brings int
 
 constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 
+// Small calls go to clusters of 1, 2, 4, 8 or 16 CTAs, one cluster per (row, KV
+// head): each CTA streams its share of the tiles, and the states are merged
+// through distributed shared memory instead of global memory and an arrival
+// there, which takes 2 us less.
+constexpr int kMaxClusterLog2 = 4, kMaxCluster = 1 << kMaxClusterLog2;
+
 // What a tile is made of.  kFp16: the fp16 pages; else a cache of codes, the log2
 // of its tokens per block added to what it is, so that its tiles' addresses are
 // constants.
@@ -153,8 +159,8 @@ struct Layout {
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
-    static constexpr int kStateOff = (kBarOff + (2 * kStages + 1) * 8 + 15) & ~15;  // cluster: acc [head][D], m, l [head]
-    static constexpr int kBytes = kStateOff + kMaxG * (D + 2) * 4;
+    static constexpr int kStateOff = (kBarOff + (2 * kStages + 1) * 8 + 15) & ~15;  // cluster: what its CTAs send this one
+    static constexpr int kBytes = kStateOff + (CLUSTER ? kMaxG * (D + 2 * kMaxCluster) * 4 : 0);
     static constexpr int kAlloc = kBytes + 1024;
     // at a piece's end the warps exchange their states through its last stage
     static_assert(kStageBytes >= (kCW - 1) * kMaxG * D * 4, "a stage holds three warps' states");
@@ -262,36 +268,54 @@ struct Cuts {
     __device__ __forceinline__ int end(int r, int part) const { return part == parts - 1 ? start(r + 1) : begin(r, part + 1); }
 };
 
-// Small calls go to clusters of 1, 2, 4, 8 or 16 CTAs, one cluster per (row, KV
-// head): each CTA streams its share of the tiles, and the states are merged
-// through distributed shared memory instead of global memory and an arrival
-// there, which takes 2 us less.
-constexpr int kMaxClusterLog2 = 4, kMaxCluster = 1 << kMaxClusterLog2;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-__device__ __forceinline__ void cluster_meet()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// The same shared-memory place in CTA `rank` of the cluster, and loads from it.
+// The same shared-memory place in CTA `rank` of the cluster, and a store to it.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank)
 {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
     return a;
 }
-__device__ __forceinline__ float cluster_float(uint32_t a)
+__device__ __forceinline__ void cluster_store(uint32_t a, float v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
-__device__ __forceinline__ float4 cluster_float4(uint32_t a)
+__device__ __forceinline__ void cluster_store(uint32_t a, float2 v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
+__device__ __forceinline__ void cluster_store(uint32_t a, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// What a cluster's 2^cl CTAs send CTA r, which merges dims r D / 2^cl ..: of each
+// one's accumulators those dims, [rank][head][dim], then m and l [rank][head].
+template <int D>
+struct Inbox {
+    uint32_t base;
+    int cl, rank;  // of the sender
+    template <class V>  // one dim, or two or four from a multiple of that on
+    __device__ __forceinline__ void acc(int head, int dim, V v) const
+    {
+        constexpr int kLog2 = D == 128 ? 7 : 6;
+        const int per = kLog2 - cl;
+        cluster_store(cluster_addr(base + (((((rank * kMaxG) + head) << per) + (dim & ((1 << per) - 1))) << 2), dim >> per), v);
+    }
+    // to all of them, by a warp whose lanes h0 / 2 + 4 r0 hold heads h0 and h0 + 1
+    __device__ __forceinline__ void sums(int h0, int r0, float m0, float m1, float l0, float l1) const
+    {
+        for (int r = r0; r < 1 << cl; r += 8) {
+            const uint32_t m = cluster_addr(base + (kMaxG * D + rank * kMaxG + h0) * 4, r);
+            cluster_store(m, m0);
+            cluster_store(m + 4, m1);
+            cluster_store(m + (kMaxG << (cl + 2)), l0);
+            cluster_store(m + (kMaxG << (cl + 2)) + 4, l1);
+        }
+    }
+};
 
 // The 8-bit cache's first tiles of this CTA on their way to L2, by one warp while
 // the producer still waits for the kernel before: three DRAM latencies (lengths,
@@ -1111,10 +1135,10 @@ constexpr int kMaxBatches = 6;
 
 // A piece's end: the four warps' states become one, each warp merging its
 // quarter of the dims, and go to o and lse (slot < 0), to the piece's slot or, in
-// a cluster, to the CTA's state in shared memory.
+// a cluster, to the CTAs that merge its dims.
 template <int D, int KIND, bool CLUSTER>
-__device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st, uint8_t *stage, float *red, int *s_last, float *state,
-                                             uint32_t cbar, uint32_t &cph, uint32_t empty, int4 mt, int4 mt2)
+__device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st, uint8_t *stage, float *red, int *s_last,
+                                             const Inbox<D> &inbox, uint32_t cbar, uint32_t &cph, uint32_t empty, int4 mt, int4 mt2)
 {
     constexpr int KS = D / 16, KQ = KS / kCW;  // 16-dim blocks a warp merges
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = lane >> 2, h0 = 2 * (lane & 3);
@@ -1184,29 +1208,51 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
         mbar_arrive(empty);
     const int unit = mt.x, slot = mt.w;
     const bool ok0 = h0 < G, ok1 = h0 + 1 < G;
+    // over the 8-bit cache a lane's dims are neighbours: the accumulators of heads h0 and h0 + 1 from dim dr on
+    constexpr bool BYTE = kIs8Bit<KIND>;
+    using Run = std::conditional_t<KQ == 2, float4, float2>;
+    const int dr = dim_of<KIND>(w * KQ, r0);
+    auto run = [&](int e) {
+        if constexpr (KQ == 2)
+            return make_float4(R[0][e], R[0][2 + e], R[1][e], R[1][2 + e]);
+        else
+            return make_float2(R[0][e], R[0][2 + e]);
+    };
+    if (CLUSTER && slot >= 0 && BYTE) {
+        inbox.acc(h0, dr, run(0));
+        inbox.acc(h0 + 1, dr, run(1));
+        if (w == 0)
+            inbox.sums(h0, r0, M0, M1, L0, L1);
+        return true;
+    }
     if (CLUSTER && slot >= 0) {
 #pragma unroll
         for (int y = 0; y < KQ; ++y) {
             const int d0 = dim_of<KIND>(w * KQ + y, r0);
-            state[h0 * D + d0] = R[y][0];
-            state[h0 * D + d0 + kDimStep<KIND>] = R[y][2];
-            state[(h0 + 1) * D + d0] = R[y][1];
-            state[(h0 + 1) * D + d0 + kDimStep<KIND>] = R[y][3];
+            inbox.acc(h0, d0, R[y][0]);
+            inbox.acc(h0, d0 + kDimStep<KIND>, R[y][2]);
+            inbox.acc(h0 + 1, d0, R[y][1]);
+            inbox.acc(h0 + 1, d0 + kDimStep<KIND>, R[y][3]);
         }
-        if (w == 0 && lane < 4) {
-            float *ml = state + kMaxG * D;
-            ml[h0] = M0;
-            ml[h0 + 1] = M1;
-            ml[kMaxG + h0] = L0;
-            ml[kMaxG + h0 + 1] = L1;
-        }
+        if (w == 0)
+            inbox.sums(h0, r0, M0, M1, L0, L1);
         return true;
     }
     if (CLUSTER || slot < 0) {
         const float i0 = over_sum(L0), i1 = over_sum(L1);
         __half *out = p.o + (int64_t)unit * G * D;
+        auto give = [&](int h, Run v, float inv) {
+            if constexpr (KQ == 2)
+                *reinterpret_cast<uint2 *>(out + h * D + dr) = make_uint2(out_half2(v.x * inv, v.y * inv), out_half2(v.z * inv, v.w * inv));
+            else
+                *reinterpret_cast<uint32_t *>(out + h * D + dr) = out_half2(v.x * inv, v.y * inv);
+        };
+        if (BYTE && ok0)
+            give(h0, run(0), i0);
+        if (BYTE && ok1)
+            give(h0 + 1, run(1), i1);
 #pragma unroll
-        for (int y = 0; y < KQ; ++y) {
+        for (int y = 0; y < (BYTE ? 0 : KQ); ++y) {
             const int d0 = dim_of<KIND>(w * KQ + y, r0);
             if (ok0) {
                 out[h0 * D + d0] = out_half(R[y][0] * i0);
@@ -1227,8 +1273,12 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
     }
     {
         float *acc = p.partials + (int64_t)slot * G * D;
+        if (BYTE && ok0)
+            *reinterpret_cast<Run *>(acc + h0 * D + dr) = run(0);
+        if (BYTE && ok1)
+            *reinterpret_cast<Run *>(acc + (h0 + 1) * D + dr) = run(1);
 #pragma unroll
-        for (int y = 0; y < KQ; ++y) {
+        for (int y = 0; y < (BYTE ? 0 : KQ); ++y) {
             const int d0 = dim_of<KIND>(w * KQ + y, r0);
             if (ok0) {
                 acc[h0 * D + d0] = R[y][0];
@@ -1298,14 +1348,18 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
     uint32_t qf[KS][2];
     int stage = 0;
     uint32_t ph = 0, cph = 0;
+    const Inbox<D> inbox = {sbase + L::kStateOff, p.cluster_log2, (int)blockIdx.x & ((1 << p.cluster_log2) - 1)};
     for (;;) {
         if (!__all_sync(0xffffffffu, mbar_wait(full0 + stage * 8, ph, kWaitNs))) {
             report_error(p.ws, kErrTimeout, (int)blockIdx.x, stage, 2);
             return;
         }
         const int4 mt = meta[2 * stage];
-        if (mt.z & kEnd)
+        if (mt.z & kEnd) {
+            if (CLUSTER && p.cluster_log2 > 0 && w == 0)  // a CTA without a tile
+                inbox.sums(2 * (lane & 3), r0, kNoMax, kNoMax, kNoTiles, kNoTiles);
             break;
+        }
         uint8_t *sp = basep + stage * L::kStageBytes;
         if (mt.z & kFirst) {
             const uint8_t *qs = sp + L::kKvBytes;
@@ -1346,11 +1400,13 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
         }
         __syncwarp();
         if (mt.z & kLast) {
-            if (!finish_piece<D, KIND, CLUSTER>(p, st, sp, red + parity * kCW * 2 * kMaxG, s_last,
-                                          reinterpret_cast<float *>(basep + L::kStateOff), cbar, cph, empty0 + stage * 8, mt, mt2)) {
+            if (!finish_piece<D, KIND, CLUSTER>(p, st, sp, red + parity * kCW * 2 * kMaxG, s_last, inbox, cbar, cph,
+                                                empty0 + stage * 8, mt, mt2)) {
                 report_error(p.ws, kErrTimeout, (int)blockIdx.x, stage, 3);
                 return;
             }
+            if (CLUSTER)
+                break;  // the only piece
             st.clear();
             parity ^= 1;
         } else if (lane == 0) {
@@ -1375,42 +1431,39 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
 }
 
 // The states of a cluster's CTAs become the (row, head)'s o and lse, each CTA
-// taking its share of the dims, a thread four of them.
+// taking its share of the dims, a thread four of them, from what it was sent: no
+// other CTA's memory is looked at, so none has to wait for the others' end, and
+// the way there is over when the cluster has met.  (Reading the others' states took
+// 0.3 to 0.7 us more: 16 rows of 1k of the 8-bit cache 9.7 us, now 9.0; one row of 1k
+// of the 4-bit cache 5.4, now 5.0.  Sent one dim at a time, the 8-bit cache's, four
+// neighbouring ones a lane, took 1.8 us more in clusters of 16.)
 template <int D>
-__device__ __forceinline__ void merge_cluster(const AttendParams &p, uint32_t state)
+__device__ __forceinline__ void merge_cluster(const AttendParams &p, const float *inbox)
 {
     const int cl = p.cluster_log2, n = 1 << cl, per = (D / 4) >> cl;  // float4s of a head in this CTA's share
     if (cl == 0)
         return;  // the one CTA has written o and lse
     const int unit = (int)blockIdx.x >> cl, r = (int)blockIdx.x - (unit << cl);
-    cluster_meet();  // every CTA's state is written
+    const float *ms = inbox + kMaxG * D, *ls = ms + (kMaxG << cl);
+    cluster_arrive();
+    cluster_wait();  // everything is there
     for (int x = threadIdx.x; x < p.G * per; x += kThreads) {
-        const int g = x / per, d = 4 * (r * per + x - g * per);
-        float m[kMaxCluster], l[kMaxCluster];
-        float4 a[kMaxCluster];
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            m[c] = kNoMax;
-            l[c] = kNoTiles;
-            a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < n) {
-                const uint32_t at = cluster_addr(state, c);
-                m[c] = cluster_float(at + (kMaxG * D + g) * 4);
-                l[c] = cluster_float(at + (kMaxG * D + kMaxG + g) * 4);
-                a[c] = cluster_float4(at + (g * D + d) * 4);
-            }
-        }
+        const int g = x / per, q = x - g * per, d = 4 * (r * per + q);
         float M = kNoMax, Ls = 0.f;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)
-            M = fmaxf(M, m[c]);
+            if (c < n)
+                M = fmaxf(M, ms[c * kMaxG + g]);
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
-            const float f = ex2(m[c] - M);
-            if (l[c] != kNoTiles) {  // else the accumulator was never written
-                Ls += l[c] * f;
-                A.x += a[c].x * f, A.y += a[c].y * f, A.z += a[c].z * f, A.w += a[c].w * f;
+            if (c >= n)
+                continue;
+            const float l = ls[c * kMaxG + g], f = ex2(ms[c * kMaxG + g] - M);
+            if (l != kNoTiles) {  // else nothing else was sent
+                const float4 a = reinterpret_cast<const float4 *>(inbox)[(c * kMaxG + g) * per + q];
+                Ls += l * f;
+                A.x += a.x * f, A.y += a.y * f, A.z += a.z * f, A.w += a.w * f;
             }
         }
         const int64_t oh = (int64_t)unit * p.G + g;
@@ -1419,7 +1472,6 @@ __device__ __forceinline__ void merge_cluster(const AttendParams &p, uint32_t st
         if (p.lse && d == 0)
             p.lse[oh] = (M + log2f(Ls)) * kLn2;
     }
-    cluster_meet();  // no CTA's shared memory goes away while another reads it
 }
 
 template <int D, int KIND, bool CLUSTER>
@@ -1442,8 +1494,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, KIND, CLUSTER>::kCtasPerSm
         mbar_init(cbar, kCW);
         fence_mbar_init();
     }
-    if (CLUSTER && threadIdx.x < 2 * kMaxG)  // no tiles yet
-        reinterpret_cast<float *>(basep + L::kStateOff)[kMaxG * D + threadIdx.x] = threadIdx.x < kMaxG ? kNoMax : kNoTiles;
+    if (CLUSTER && p.cluster_log2 > 0)
+        cluster_arrive();  // here: the others may send
     if (!L::QUANT && threadIdx.x == 32 * kCW) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
@@ -1462,12 +1514,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, KIND, CLUSTER>::kCtasPerSm
             hint_first_tiles<D, KIND, CLUSTER>(p);
     pdl_wait();
     pdl_trigger();
+    if (CLUSTER && p.cluster_log2 > 0)
+        cluster_wait();
     if (threadIdx.x >= 32 * kCW)
         run_producer<D, KIND, CLUSTER>(&tmK, &tmV, p, sbase, basep, meta, full0, empty0);
     else
         run_consumer<D, KIND, CLUSTER>(p, sbase, basep, meta, full0, empty0, cbar, &s_last);
     if constexpr (CLUSTER)
-        merge_cluster<D>(p, sbase + L::kStateOff);
+        merge_cluster<D>(p, reinterpret_cast<const float *>(basep + L::kStateOff));
 }
 
 // What is asked of a device once per kernel: whether its shared memory limit is
