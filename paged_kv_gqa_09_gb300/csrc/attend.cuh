@@ -664,25 +664,16 @@ __device__ __forceinline__ int dim_of(int x, int r0)
 template <int KIND>
 constexpr int kDimStep = kIs8Bit<KIND> ? 1 : 8;
 
-// What turns a raw score of block u into units of log2, what a weight's exponent
-// gets more, and a sum of weights with two more of block u: one scale for all.
+// What turns a raw score of block u into units of log2: one factor for all, or K's
+// scale with it, that of a lane's two tokens.
 struct OneScale {
     float sl2;
     __device__ __forceinline__ float times(int) const { return sl2; }
-    __device__ __forceinline__ float plus(int, float y) const { return y; }
-    __device__ __forceinline__ float add(int, float p, float l) const { return l + p; }
 };
-
-// The same for blocks with scales of their own, those of a lane's two tokens: K's
-// scale is a factor of the score; V's, 2^e, goes into the weight that multiplies
-// V's codes, as e into its exponent, and out of the sum again.  Both are exact:
-// powers of two.  The maximum that a state keeps is then one of weights so scaled.
 template <int MT>
 struct BlockScales {
-    float k[MT], e[MT], inv[MT];
+    float k[MT];
     __device__ __forceinline__ float times(int u) const { return k[u]; }
-    __device__ __forceinline__ float plus(int u, float y) const { return y + e[u]; }
-    __device__ __forceinline__ float add(int u, float p, float l) const { return fmaf(p, inv[u], l); }
 };
 
 // Raw scores x[b] of MT blocks of 16 tokens -- x[b][0], x[b][1]: token r0 with
@@ -691,7 +682,11 @@ struct BlockScales {
 // returns the weights as the B operands of the PV product.  The weights are
 // rounded to fp16, the tensor cores' operand type, which costs o about as much
 // as its own rounding (2^-11 of the mean |v| at most); their sum is kept in fp32
-// before that rounding, so that lse is not rounded with them.
+// before that rounding, so that lse is not rounded with them.  (Over the 8-bit
+// cache o is off by 2.1e-4 to 2.7e-4 of its size, where its own rounding alone is
+// 2.0e-4.  A second product with what the weights' rounding left brings that down
+// to 2.0e-4, and takes 16 rows of 1k from 9.1 to 9.6 us, eight of 4k from 14.0 to 15.0,
+// 100 of 100 from 13.2 to 14.7.)
 template <int D, int MT, class Scales>
 __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][4], uint32_t vis, const Scales &sc, uint32_t (&P)[MT][2])
 {
@@ -713,7 +708,7 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
         for (int u = 0; u < MT; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                y[u][e] = sc.plus(u, fmaf(x[u][e], sc.times(u), (e & 1) ? -m1 : -m0));
+                y[u][e] = fmaf(x[u][e], sc.times(u), (e & 1) ? -m1 : -m0);
         hide();
     };
     auto most = [&](int odd) {
@@ -749,15 +744,15 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float n = (e & 1) ? n1 : n0;
-                y[u][e] = sc.plus(u, fabsf(n) < kFar ? fmaf(x[u][e], sc.times(u), -n) : __fmul_rn(x[u][e], sc.times(u)) - n);
+                y[u][e] = fabsf(n) < kFar ? fmaf(x[u][e], sc.times(u), -n) : __fmul_rn(x[u][e], sc.times(u)) - n;
             }
         hide();
     }
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const float p0 = ex2(y[u][0]), p1 = ex2(y[u][1]), p2 = ex2(y[u][2]), p3 = ex2(y[u][3]);
-        st.l0 = sc.add(u, p0 + p2, st.l0);
-        st.l1 = sc.add(u, p1 + p3, st.l1);
+        st.l0 += p0 + p2;
+        st.l1 += p1 + p3;
         P[u][0] = movmatrix_t(pack_half2(p0, p1));
         P[u][1] = movmatrix_t(pack_half2(p2, p3));
     }
@@ -935,6 +930,11 @@ __device__ __forceinline__ uint32_t byte_rows(uint32_t vis)
 // that lanes read at a time have different halves swapped.  Of V, a lane reads
 // tokens 4 t .. 4 t + 3 of dims 4 (r0 + 8 c) ..; the weights, which come as those of
 // tokens 4 t and 4 t + 2, and of the two others, change places to match.
+// K's scale is a factor of the scores.  V's multiplies what a block's codes add to
+// O, in fp32; in pages of 8, where a product is over two blocks, the codes, whose
+// values are exact fp16 numbers.  (In the weights' exponents, and out of the sum
+// again, it costs 1% less, 3% in pages of 8, but then the fp16 weights have to span the scales too:
+// beside a block of a scale 2^31 times as great, values were lost.)
 template <int D, int KIND>
 __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], const uint8_t *kv, uint32_t vis, int w, float sl2)
 {
@@ -943,8 +943,10 @@ __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D /
     const int lane = threadIdx.x & 31, r0 = lane >> 2, t = lane & 3;
     const int tok = 2 * r0;  // of row r0
     BlockScales<MT> sc;
-    float x[MT][4];
+    float x[MT][4], sv[MT];
     uint4 kc[MT][2][NC];
+    // V's scale; one outside the format's range, which only masked tokens' blocks may have, as the nearest in it
+    auto scale_of = [](uint32_t s) { return byte_pow2(byte_exponent<FMT>(__uint_as_float(s))); };
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const int at = 32 * w + 16 * u + (LG == 3 ? tok & 8 : 0), r = at & (TB - 1);  // this lane's scale block
@@ -957,13 +959,9 @@ __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D /
             kc[u][1][c] = *reinterpret_cast<const uint4 *>(blk + in + D);
         }
         const uint2 s = *reinterpret_cast<const uint2 *>(blk + byte_scale_part<D>(TB, r, LG));
-        // a lane's tokens are both in its block.  K: the scale as it is, NaN too; V: within 2^-60 .. 2^60, so that
-        // tokens which are masked, whatever their scale, stay harmless; NaN, which only visible ones keep, as NaN
-        sc.k[u] = sl2 * __uint_as_float(s.x);
-        const uint32_t eb = s.y >> 23 & 255u, in_range = min(max(eb, 67u), 187u);
-        sc.e[u] = eb == 255u ? __uint_as_float(0x7fffffffu)
-                             : __uint_as_float(0x4b000000u | in_range) - (float)(8388608 + 127);
-        sc.inv[u] = __uint_as_float((254u - in_range) << 23);
+        // a lane's tokens are both in its block; where V's scale is NaN their scores are too
+        sc.k[u] = (s.y & 0x7fffffffu) > 0x7f800000u ? __uint_as_float(0x7fffffffu) : sl2 * __uint_as_float(s.x);
+        sv[u] = scale_of(s.y);
         x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
     }
 #pragma unroll
@@ -985,22 +983,41 @@ __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D /
         const int at = 32 * w + 16 * u + (LG == 3 ? 8 * (t >> 1) : 0), r = at & (TB - 1);
         const uint8_t *vp = kv + (at >> TBL) * BYTES + byte_v_part<D>(TB, r, LG);
         const uint32_t p0 = __byte_perm(P[u][0], P[u][1], 0x5410), p1 = __byte_perm(P[u][0], P[u][1], 0x7632);
-        // masked tokens' bytes may be a NaN's, which a weight of 0 does not hide
+        // masked tokens' bytes may be any: a weight of 0 does not hide an e4m3 NaN, nor an infinity that a scale makes
         uint32_t keep = 0xffffffffu;
-        if (FMT == kE4m3 && vis != 0xffffffffu)
+        if ((FMT == kE4m3 || LG == 3) && vis != 0xffffffffu)
             keep = ((vis >> (16 * u + 4 * t) & 15u) * 0x00204081u & 0x01010101u) * 255u;
+        __half2 s2;
+        if constexpr (LG == 3)
+            s2 = __float2half2_rn(scale_of(*reinterpret_cast<const uint32_t *>(kv + (at >> TBL) * BYTES + byte_scale_part<D>(TB, r, LG) + 4)));
+        auto values = [&](uint32_t w, uint32_t &lo, uint32_t &hi) {
+            byte_numbers<FMT>(w & keep, lo, hi);
+            if constexpr (LG == 3) {
+                lo = byte_word(__hmul2(byte_half2(lo), s2));
+                hi = byte_word(__hmul2(byte_half2(hi), s2));
+            }
+        };
+        auto add = [&](float (&O)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            if constexpr (LG == 3) {
+                mma_16816(O, a0, a1, a2, a3, p0, p1);
+            } else {
+                float o[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(o, a0, a1, a2, a3, p0, p1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    O[e] = fmaf(o[e], sv[u], O[e]);
+            }
+        };
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            uint4 v = *reinterpret_cast<const uint4 *>(vp + byte_v_at(r0 + 8 * c, LG == 3 ? t & 1 : t, LG));
-            if (FMT == kE4m3)
-                v.x &= keep, v.y &= keep, v.z &= keep, v.w &= keep;
+            const uint4 v = *reinterpret_cast<const uint4 *>(vp + byte_v_at(r0 + 8 * c, LG == 3 ? t & 1 : t, LG));
             uint32_t a0, a1, a2, a3;
-            byte_numbers<FMT>(v.x, a0, a2);
-            byte_numbers<FMT>(v.y, a1, a3);
-            mma_16816(st.O[2 * c], a0, a1, a2, a3, p0, p1);
-            byte_numbers<FMT>(v.z, a0, a2);
-            byte_numbers<FMT>(v.w, a1, a3);
-            mma_16816(st.O[2 * c + 1], a0, a1, a2, a3, p0, p1);
+            values(v.x, a0, a2);
+            values(v.y, a1, a3);
+            add(st.O[2 * c], a0, a1, a2, a3);
+            values(v.z, a0, a2);
+            values(v.w, a1, a3);
+            add(st.O[2 * c + 1], a0, a1, a2, a3);
         }
     }
 }

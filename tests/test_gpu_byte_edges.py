@@ -1,0 +1,104 @@
+"""The 8-bit cache where it could lose what it holds: decode of blocks of unequal
+scales, element by element."""
+import numpy as np
+import pytest
+
+import byte_ref as R
+from test_gpu_byte import Batch, dev, queries
+
+pytestmark = pytest.mark.gpu
+FORMATS = pytest.mark.parametrize("fmt", [R.INT8, R.E4M3], ids=["int8", "e4m3"])
+
+
+def per_element(b, q, window=None, sinks=0):
+    """o of the model, and what a kernel with fp32 sums may be off at each element, whatever the other dims of a
+    value's block hold:
+      - half an fp16 step of o, 2^-11 |o|, or 2^-25 among the subnormals;
+      - weights held to 2^-11 of themselves or, the smallest, to 2^-25 where the greatest is 1 or more:
+        (2^-11 sum p |v| + 2^-25 sum |v|) / l;
+      - scores and exponentials in fp32, as in byte_ref.attention()."""
+    ro, rl, to, tl = R.attention(q.cpu().numpy(), b.k, b.v, float(np.float32(b.shape.scale)), window, sinks)
+    x = q.cpu().numpy().astype(np.float64)
+    bound = np.zeros_like(to)
+    for i in range(b.B):
+        t = R.visible(len(b.k[i].y), window, sinks)
+        for h in range(b.Hq if t.size else 0):
+            k, v = b.k[i].values()[t, h // b.G], np.abs(b.v[i].values()[t, h // b.G])
+            s = k @ x[i, h] * float(np.float32(b.shape.scale))
+            p = np.exp(s - s.max())
+            es = 2 * b.d * 2.0 ** -24 * (np.abs(k) @ np.abs(x[i, h])).max() * abs(b.shape.scale) + 2.0 ** -20
+            bound[i, h] = 2.0 ** -11 * np.abs(ro[i, h]) + 2.0 ** -25 + ((2.0 ** -11 + 2 * es) * (p @ v) + 2.0 ** -25 * v.sum(0)) / p.sum()
+    return ro, bound
+
+
+# ------------------------------------------------------------------ decode
+
+@FORMATS
+@pytest.mark.parametrize("wide", [0, 4096])
+@pytest.mark.parametrize("d,P", [(128, 16), (64, 8), (128, 8), (64, 64), (128, 128)])
+def test_small_values_beside_a_block_of_a_large_scale(fmt, wide, d, P):
+    """One value at the format's end, in one dim of one block; the other dims are left to blocks whose scale and
+    softmax weight come to less than 2^-33 of that block's."""
+    size, score = (2.0 ** -15, -4.0) if fmt == R.INT8 else (2.0 ** -9, -8.0)
+    n = [64, 40, 17, 200]
+    b = Batch(fmt, n, Hkv=2, G=4, d=d, P=P, seed=d + P, scale=1.0, wide=wide)
+    ks, vs = [], []
+    for i, m in enumerate(n):
+        k, v = np.zeros((m, 2, d), np.float16), (np.clip(b.normal(m), -3, 3) * size).astype(np.float16)
+        first = 8 * (i % 2)  # also a block that is not the row's first
+        k[:, :, 0] = score
+        k[first:first + 8, :, 0] = 0
+        v[first:16 if P > 8 else first + 8] = 0
+        v[first, :, 0] = R.TOP[fmt] * 2.0 ** R.MOST[fmt]
+        ks.append(k)
+        vs.append(v)
+    b.append(ks, vs)
+    q = np.zeros((4, 8, d), np.float16)
+    q[:, :, 0] = 1.0
+    q = dev(q)
+    for window, sinks in ((None, 0), (9, 16)):
+        ro, bound = per_element(b, q, window, sinks)
+        o, lse = b.decode(q, window, sinks)
+        x = o.cpu().numpy().astype(np.float64)
+        bad = ~(np.abs(x - ro) <= bound)
+        assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4], x[bad][:4], ro[bad][:4], bound[bad][:4])
+        assert (np.abs(ro[:, :, 1:]).max((1, 2)) > 2.0 ** -23).all()  # to lose them is beyond the bound, some 2^-25 there
+        b.compare(o, lse, q, window, sinks)
+    b.ok()
+
+
+@FORMATS
+@pytest.mark.parametrize("wide", [0, 4096])
+def test_every_element_of_blocks_of_unequal_scales(fmt, wide):
+    lens = [700, 33, 400]
+    b = Batch(fmt, lens, Hkv=2, G=4, d=128, P=16, seed=15, wide=wide)
+    ks, vs = [], []
+    for n in lens:
+        size = (2.0 ** b.rng.integers(-20, 14, (n + 15) // 16)).repeat(16)[:n, None, None]
+        ks.append(b.normal(n))
+        vs.append((np.clip(b.normal(n), -3, 3) * size * (b.rng.random((n, 2, 128)) < 0.2)).astype(np.float16))
+    b.append(ks, vs)
+    for scale in (0.0, 0.3, 1.0, 3.0):
+        q = queries(b, scale=scale)
+        for window, sinks in ((None, 0), (100, 20)):
+            ro, bound = per_element(b, q, window, sinks)
+            o, _ = b.decode(q, window, sinks)
+            assert (np.abs(o.cpu().numpy().astype(np.float64) - ro) <= bound).all()
+    b.ok()
+
+
+@FORMATS
+@pytest.mark.parametrize("d,P", [(128, 16), (64, 8), (128, 256)])
+def test_bytes_behind_the_rows_beside_the_greatest_scale(fmt, d, P):
+    """Masked tokens of a block whose scale is the format's greatest: any code there, -128 and NaNs among them, counts
+    as nothing."""
+    for fill in (0x80, 0x7F, 0xFF, 0x81):
+        b = Batch(fmt, [5, 21, 100, 3], d=d, P=P, seed=31, fill=fill)
+        top = R.TOP[fmt] * 2.0 ** R.MOST[fmt]
+        with np.errstate(over="ignore"):  # to infinity, and back to the greatest
+            vs = [np.clip(b.normal(n, top / 2), -top, top) for n in (5, 21, 100, 3)]
+        for v in vs:
+            v[-1] = top
+        b.append([b.normal(n) for n in (5, 21, 100, 3)], [v.astype(np.float16) for v in vs])
+        b.check(queries(b))
+        b.check(queries(b), 3, 2)
