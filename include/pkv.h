@@ -478,8 +478,10 @@ int pkv_window_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d
 /* pkv_map_pages -- pages, slots and positions of new tokens, on the device.
  * One kernel launch.  Row i holds N = seq_lens[i] tokens in ceil(N / page_size)
  * pages, which its block table names, and gets n = new_lens[i] more (0 or more):
- *   new_offsets[i] = new_lens[0] + .. + new_lens[i - 1] (int32 [B + 1]; at most
- *     total_new): where its tokens lie among the packed ones;
+ *   new_offsets[i] = new_lens[0] + .. + new_lens[i - 1] (int32 [B + 1]): where its
+ *     tokens lie among the packed ones.  From the first row whose tokens pass
+ *     total_new on, all further offsets are that row's own: an append by them gives
+ *     it and the rows behind it nothing;
  *   block_table[i][..]: the need_i = ceil((N + n) / page_size) - ceil(N / page_size)
  *     pages it lacks, taken in row order from the free list
  *     d_free_pages[0 .. *d_free_count), whose top is its end;

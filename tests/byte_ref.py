@@ -170,8 +170,10 @@ def map_pages(lens, new, table, free, count, P, num_pages, T):
     count = min(max(count, 0), len(free))
     slots, positions, offsets, out = [-1] * T, [0] * T, [], []
     off = rank = taken = 0
+    last = 0  # where a row begins, behind one whose tokens pass T the latter's place
     for i, (N, n) in enumerate(zip(lens, new)):
-        offsets.append(min(off, T))
+        last = off if off <= T else last
+        offsets.append(last)
         valid = N >= 0 and n >= 0 and N + n <= cap
         have, need = -(-N // P), (-(-(N + n) // P) - -(-N // P)) if valid else 0
         served = valid and off + max(n, 0) <= T and (need == 0 or rank + need <= count)
@@ -193,4 +195,4 @@ def map_pages(lens, new, table, free, count, P, num_pages, T):
         rank += need
         off += max(n, 0)
         out.append(N + n if good else N)
-    return table, slots, positions, offsets + [min(off, T)], out, count - taken
+    return table, slots, positions, offsets + [off if off <= T else last], out, count - taken

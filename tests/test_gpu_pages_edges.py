@@ -1,0 +1,51 @@
+"""The page map and the appends after it: rows that the map refuses take no
+tokens in either cache."""
+import numpy as np
+import pytest
+import torch
+
+import byte_ref as R
+from gpu_util import dev
+from paged_kv_gqa_09_gb300 import _lib, api
+from test_gpu_pages import Map
+
+pytestmark = pytest.mark.gpu
+
+
+def append(kind, m, cache, x, lens, off):
+    """Packed tokens x into the 4-bit or 8-bit cache by the map's table and offsets; the lengths after it."""
+    out = torch.full_like(lens, -7)
+    if kind == "4-bit":
+        shape = _lib.Shape(m.B, 1, 1, 128, m.P, m.num_pages, m.table.shape[1], 1.0)
+        api.pkv_quant_append(shape, m.ws, x, x, m.bt, lens, cache, new_offsets=off, seq_lens_out=out)
+    else:
+        api.pkv_byte_append(m.shape, m.ws, {"int8": R.INT8, "e4m3": R.E4M3}[kind], x, x, m.bt, lens, cache, new_offsets=off,
+                            seq_lens_out=out)
+    return out
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3", "4-bit"])
+@pytest.mark.parametrize("lens,new,T", [
+    ([5, 7, 3, 40], [3, 4, 8, 2], 11),      # row 2's first four tokens would fit behind its three
+    ([5, 7, 3, 40], [3, 4, 40, 2], 11),     # and where it would need pages for the rest
+    ([5, 60, 9], [3, 9, 4], 5),             # a row too long for its table, whose first two would fit
+    ([5, 7, 9], [3, 4, 5], 10), ([3], [8], 4), ([3, 20], [8, 0], 0), ([1, 2, 3], [5, 0, 0], 4),
+    ([4] * 700, [3] * 700, 3 * 650 + 2), ([4] * 1300, [1, 2] * 650, 1502)])
+def test_rows_that_pass_the_packed_tokens_are_not_appended(kind, lens, new, T):
+    stride = 4
+    m = Map(lens, 16, stride, 12 + sum(new) // 8)
+    out, _ = m.run(new, T)
+    want = [a + b if sum(new[:i + 1]) <= T and a + b <= 64 else a for i, (a, b) in enumerate(zip(lens, new))]
+    assert out.tolist() == want and api.pkv_get_error(m.ws)[0] == _lib.PKV_EDEVICE
+    off = m.off.tolist()
+    assert off[0] == 0 and all(0 <= b - a <= n for a, b, n in zip(off, off[1:], new)) and off[-1] <= T
+    if kind == "4-bit":
+        cache = torch.full((m.num_pages, 1, m.P * 128 * 5 // 4), 0x5A, dtype=torch.uint8, device="cuda")
+    else:
+        cache = torch.full((m.num_pages, 1, R.head_bytes(16, 128)), 0x5A, dtype=torch.uint8, device="cuda")
+    before = cache.clone()
+    x = torch.randn((T, 1, 128), device="cuda").half()
+    assert append(kind, m, cache, x, m.sl, m.off).tolist() == want
+    served = {int(p) for i, n in enumerate(want) if n > lens[i] for p in m.bt[i, :-(-n // 16)].tolist()}
+    rest = [p for p in range(m.num_pages) if p not in served]
+    assert torch.equal(cache[rest], before[rest])
