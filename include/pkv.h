@@ -555,10 +555,9 @@ int pkv_append_slots(const pkv_shape_t *shape, void *d_ws, const void *d_k_new, 
 size_t pkv_byte_page_bytes(const pkv_shape_t *shape);
 
 /* pkv_byte_append -- quantise new tokens into the 8-bit cache.  One kernel launch.
- * Arguments, refusals and errors are those of pkv_quant_append.  A row or call that
- * is refused on account of a page, or of offsets that do not ascend, may have
- * rounded the earlier tokens of its last block to a greater scale already.  New
- * tokens of two rows must not share a scale block either (a page's SB tokens). */
+ * Arguments, refusals and errors are those of pkv_quant_append; the earlier tokens
+ * of a row or call that is refused keep their values.  New tokens of two rows must
+ * not share a scale block either (a page's SB tokens). */
 int pkv_byte_append(const pkv_shape_t *shape, void *d_ws, int32_t format, const void *d_k_new, const void *d_v_new,
                   int64_t new_stride, int32_t total_new, const int32_t *d_new_offsets, const int32_t *d_block_table,
                   const int32_t *d_seq_lens, int32_t *d_seq_lens_out, void *d_byte_cache, void *stream);

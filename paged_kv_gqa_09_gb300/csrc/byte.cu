@@ -51,18 +51,21 @@ struct Lane {
 };
 
 // The row that block gs is in: its first packed token, its tokens and what `a` and
-// `b` (nullptr: zeros) hold of it.  Of up to 64 rows every lane brings two, so that
-// all of it takes one round trip; whole warps only.
+// `b` (nullptr: zeros) hold of it.  Of up to kFewRows rows every lane brings two, so
+// that all of it takes one round trip, and sees whether the offsets ascend within T;
+// whole warps only.
+constexpr int kFewRows = 64;
 struct Row {
     int i, off, n, a, b;
+    bool ascend;
 };
 template <int LG>
-__device__ __forceinline__ Row find_row(int64_t gs, const int32_t *offsets, int B, const int32_t *pa, const int32_t *pb)
+__device__ __forceinline__ Row find_row(int64_t gs, const int32_t *offsets, int B, int T, const int32_t *pa, const int32_t *pb)
 {
-    if (B > 64) {
+    if (B > kFewRows) {
         const int i = min(last_not_above(B, gs, [&](int r) { return append_first_group(offsets[r], r, LG); }), B - 1);
         const int off = offsets[i];
-        return {i, off, offsets[i + 1] - off, pa[i], pb ? pb[i] : 0};
+        return {i, off, offsets[i + 1] - off, pa[i], pb ? pb[i] : 0, true};
     }
     const int lane = threadIdx.x & 31;
     int o[2], e[2], x[2], y[2];
@@ -78,7 +81,7 @@ __device__ __forceinline__ Row find_row(int64_t gs, const int32_t *offsets, int 
     const int i = max(__popc(m[0]) + __popc(m[1]) - 1, 0);
     auto of = [&](const int (&v)[2]) { return __shfl_sync(0xffffffffu, i >= 32 ? v[1] : v[0], i & 31); };
     const int off = of(o);
-    return {i, off, of(e) - off, of(x), of(y)};
+    return {i, off, of(e) - off, of(x), of(y), __all_sync(0xffffffffu, min(o[0], o[1]) >= 0 && o[0] <= e[0] && o[1] <= e[1] && max(e[0], e[1]) <= T) != 0};
 }
 
 __device__ __forceinline__ uint32_t greatest(uint4 x)
@@ -182,19 +185,36 @@ struct Block {
     int off, n, N, page, r0;
     bool any, bad;
 };
+// A block that holds earlier tokens is touched only where its row and the call
+// stand, since their codes change with its scale: those of a refused row stay.  So
+// the warps that have one look at all of the row's pages, a lane each, in the round
+// trip of the block's own.  `ascend`: the offsets of more than kFewRows rows are in
+// order, else the whole call is refused.  (64 rows of one token 5.00 us without, 5.17
+// with; 256 of four 10.8 and 11.3; 1000 of one 24.8 and 25.7; 37k in 8 prompts 31.2 and 31.6.)
 template <int LG>
-__device__ __forceinline__ Block find_block(const QuantAppendParams &p, int64_t gs)
+__device__ __forceinline__ Block find_block(const QuantAppendParams &p, int64_t gs, bool ascend)
 {
     Block b = {};
-    const Row row = find_row<LG>(gs, p.offsets, p.B, p.seq_lens, nullptr);
+    const Row row = find_row<LG>(gs, p.offsets, p.B, p.T, p.seq_lens, nullptr);
     b.off = row.off, b.n = row.n, b.N = row.a;
     if (!append_group(gs, row.i, b.off, b.n, b.N, b.pos0, LG) || !append_fits(p, row.i, b.N, b.off, b.n, false))
         return b;
-    b.page = p.bt[(int64_t)row.i * p.bt_stride + (b.pos0 >> p.log2P)];
-    b.any = b.page >= 0 && b.page < p.num_pages;
-    b.bad = !b.any;
-    if (b.bad && (threadIdx.x & 31) == 0)
-        report_error(p.ws, kErrBadPage, row.i, (int)(b.pos0 >> p.log2P), b.page);
+    const int32_t *pages = p.bt + (int64_t)row.i * p.bt_stride;
+    const int lane = threadIdx.x & 31, at = (int)(b.pos0 >> p.log2P), last = (int)(((int64_t)b.N + b.n - 1) >> p.log2P);
+    const bool held = b.pos0 < b.N;
+    auto there = [&p](int page) { return page >= 0 && page < p.num_pages; };
+    const int mine = pages[held ? min(at + lane, last) : at];
+    b.page = __shfl_sync(0xffffffffu, mine, 0);
+    bool stands = there(mine);
+    if (held) {
+        for (int x = at + 32; x <= last; x += 32)
+            stands &= there(pages[min(x + lane, last)]);
+        stands = __all_sync(0xffffffffu, stands) && ascend && row.ascend;
+    }
+    b.any = stands;
+    b.bad = !there(b.page);
+    if (b.bad && lane == 0)
+        report_error(p.ws, kErrBadPage, row.i, at, b.page);
     b.r0 = (int)b.pos0 & ((1 << p.log2P) - 1);  // within the page
     return b;
 }
@@ -228,8 +248,15 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) byte_append_kernel(cons
     const unsigned warp = blockIdx.x * kWarps + (threadIdx.x >> 5), lines = gridDim.x * kWarps / (unsigned)p.parts;
     const unsigned line = warp / (unsigned)p.parts;
     const int it0 = (int)(warp - line * p.parts) * p.its_per_part, it1 = min(it0 + p.its_per_part, 2 * p.Hkv);
+    bool ascend = true;
+    if (p.B > kFewRows) {  // else every find_row() sees them all
+        ascend = p.offsets[0] >= 0 && p.offsets[p.B] <= p.T && my_n >= 0;
+        for (int r = (int)threadIdx.x + kThreads; r < p.B; r += kThreads)
+            ascend &= p.offsets[r] <= p.offsets[r + 1];
+        ascend = __syncthreads_and(ascend) != 0;
+    }
     for (int64_t gs = line < lines ? (int64_t)line : p.groups; gs < p.groups; gs += lines) {
-        const Block b = find_block<LG>(p, gs);
+        const Block b = find_block<LG>(p, gs, ascend);
         bad |= b.bad;
         if (!b.any)
             continue;
@@ -365,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) byte_read_kernel(const Qu
     const int part_no = (int)(unit - gs * p.parts), it0 = part_no * p.heads_per_part, it1 = min(it0 + p.heads_per_part, 2 * p.Hkv);
     if (gs >= p.groups)
         return;
-    const Row row = find_row<LG>(gs, p.offsets, p.B, p.seq_lens, p.first);
+    const Row row = find_row<LG>(gs, p.offsets, p.B, p.T, p.seq_lens, p.first);
     const int i = row.i, off = row.off, n = row.n, begin = row.b;
     int64_t pos0;
     if (off < 0 || (int64_t)off + n > p.T || !append_group(gs, i, off, n, begin, pos0, LG))

@@ -1,10 +1,12 @@
 """The 8-bit cache where it could lose what it holds: decode of blocks of unequal
-scales, element by element."""
+scales, element by element, and appends that are refused."""
 import numpy as np
 import pytest
+import torch
 
 import byte_ref as R
-from test_gpu_byte import Batch, dev, queries
+from paged_kv_gqa_09_gb300 import _lib, api
+from test_gpu_byte import Batch, bits, dev, queries
 
 pytestmark = pytest.mark.gpu
 FORMATS = pytest.mark.parametrize("fmt", [R.INT8, R.E4M3], ids=["int8", "e4m3"])
@@ -102,3 +104,62 @@ def test_bytes_behind_the_rows_beside_the_greatest_scale(fmt, d, P):
         b.append([b.normal(n) for n in (5, 21, 100, 3)], [v.astype(np.float16) for v in vs])
         b.check(queries(b))
         b.check(queries(b), 3, 2)
+
+
+# ------------------------------------------------------------------ refused appends
+
+@FORMATS
+@pytest.mark.parametrize("d,P,Hkv,rows", [(128, 16, 2, 3), (64, 8, 3, 3), (128, 64, 8, 3), (64, 16, 1, 70), (128, 256, 1, 130)])
+@pytest.mark.parametrize("value", [3000.0, np.inf, np.nan])
+def test_a_refused_row_keeps_its_earlier_tokens(fmt, d, P, Hkv, rows, value):
+    """A row whose last page is partly filled and whose new tokens need a page that is not there: neither the length
+    nor a value of the earlier tokens changes, whatever the new ones are; the other rows are served."""
+    held = [P + 3 + i % 4 for i in range(rows)]
+    new = [2 * P + i % 5 for i in range(rows)]
+    new[1] = 40 * P  # the missing page is far off
+    b = Batch(fmt, [x + y for x, y in zip(held, new)], Hkv=Hkv, G=1, d=d, P=P, seed=rows + P)
+    b.grow(held)
+    before = [(x.y.copy(), x.e.copy()) for side in (b.k, b.v) for x in side]
+    refused = {0: 3, 1: 41, rows - 1: 2}
+    keep = b.bt.clone()
+    for i, page in refused.items():
+        b.bt[i, page] = -1 if i else b.num_pages
+    x = [b.normal(n) for n in new]
+    for y in x:
+        y[:, :, 5] = value
+        y[0, :, 7] = 1.0
+    b.append(x, [y[::-1].copy() for y in x])
+    assert api.pkv_get_error(b.ws)[0] == _lib.PKV_EDEVICE
+    assert b.lens.tolist() == [held[i] if i in refused else held[i] + new[i] for i in range(rows)]
+    for j, side in enumerate((b.k, b.v)):
+        for i in refused:
+            side[i].y, side[i].e = before[j * rows + i]
+    b.bt.copy_(keep)
+    b.same()
+    b.ok()
+
+
+@FORMATS
+@pytest.mark.parametrize("rows", [4, 64, 65, 300])
+@pytest.mark.parametrize("value", [3000.0, np.nan])
+def test_a_call_with_bad_offsets_keeps_every_row(fmt, rows, value):
+    """Offsets that descend, pass the packed tokens or begin before them, in any row: no row's value changes."""
+    held, new = [5 + i % 9 for i in range(rows)], [1 + i % 4 for i in range(rows)]
+    b = Batch(fmt, [x + y for x, y in zip(held, new)], Hkv=2, G=1, d=128, P=16, seed=rows)
+    b.grow(held)
+    want = b.read()
+    off = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(off[-1])
+    x = torch.full((T, 2, 128), value, dtype=torch.float16, device="cuda")
+    down, past, ahead, middle = off.copy(), off.copy(), off.copy(), off.copy()
+    down[rows // 2] = off[rows // 2 + 1] + 1
+    past[rows] = T + 1
+    ahead[0] = -1
+    middle[rows - 1] = -4
+    for bad in (down, past, ahead, middle):
+        api.pkv_byte_append(b.shape, b.ws, fmt, x, x, b.bt, b.lens, b.cache, new_offsets=dev(bad))
+        assert api.pkv_get_error(b.ws)[0] == _lib.PKV_EDEVICE
+        assert b.lens.tolist() == held
+        for got, was in zip(b.read(), want):
+            assert np.array_equal(bits(got), bits(was))
+    b.ok()

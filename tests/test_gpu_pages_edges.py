@@ -49,3 +49,23 @@ def test_rows_that_pass_the_packed_tokens_are_not_appended(kind, lens, new, T):
     served = {int(p) for i, n in enumerate(want) if n > lens[i] for p in m.bt[i, :-(-n // 16)].tolist()}
     rest = [p for p in range(m.num_pages) if p not in served]
     assert torch.equal(cache[rest], before[rest])
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3", "4-bit"])
+def test_rows_that_find_no_page_are_not_appended(kind):
+    """A row whose partly filled page has room for the first of its tokens, and no page for the others."""
+    m = Map([3, 20, 5], 16, 4, 2)
+    new = [9, 30, 4]  # row 1 needs two pages, after row 0, which needs none
+    m.free, m.count = m.free[:1], 1
+    m.fp, m.fc = dev(m.free), dev(np.array([1], np.int32))
+    out, _ = m.run(new, 43)
+    assert out.tolist() == [12, 20, 9]
+    assert "no free page" in api.pkv_get_error(m.ws)[1]
+    if kind == "4-bit":
+        cache = torch.zeros((m.num_pages, 1, m.P * 128 * 5 // 4), dtype=torch.uint8, device="cuda")
+    else:
+        cache = torch.zeros((m.num_pages, 1, R.head_bytes(16, 128)), dtype=torch.uint8, device="cuda")
+    x = torch.randn((43, 1, 128), device="cuda").half()
+    assert append(kind, m, cache, x, m.sl, m.off).tolist() == [12, 20, 9]
+    if kind != "4-bit":  # whose scales are each token's own: what lies behind a row's end is nobody's
+        assert int(cache[m.table[1, :2].tolist()].count_nonzero()) == 0
