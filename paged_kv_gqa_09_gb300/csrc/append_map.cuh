@@ -55,14 +55,54 @@ inline int split_work(int64_t warps, int n, int64_t want, int64_t most, int &per
 // many KV heads would make them so).  Some two to four units per warp: 42k
 // tokens of 8 heads 49.6 us; coarser ones, of which some warps get two and some
 // one, 62 us; finer ones, whose first tile nothing hides, 52 us.
-inline int64_t append_grid(int T, int B, int Hkv, int ctas, int cta_warps, int64_t &groups, int &parts, int &per, int lg = 3)
+inline int64_t append_grid(int T, int B, int Hkv, int ctas, int cta_warps, int64_t &groups, int &parts, int &per)
 {
     const int64_t resident = (int64_t)ctas * cta_warps;
-    groups = append_groups(T, B, lg);
+    groups = append_groups(T, B);
     parts = split_work(groups, 2 * Hkv, 2 * resident, resident, per);
     const int64_t grid = (groups * parts + cta_warps - 1) / cta_warps;
     return grid < ctas ? grid : ctas;
 }
+
+// How a scale block's sides (heads' K and V) are split over warps by the 8-bit
+// cache's append and read: one each where that is no more than the `wave` of warps
+// that are resident, else kByteSides.  A unit's warps should be near one another in
+// time, since a token's heads are neighbours in memory, but a warp has to look up its
+// row and page first.  Of eight heads appended, one and two a warp: 500 tokens 4.3 and
+// 5.7 us, 2k 6.0 and 6.2, 4k 10.8 and 9.7 us.  35k tokens of 8 heads appended and read
+// back: 2 sides each 73.4 us; the append with 4 77 us, 1 75 us; the read of 117k
+// tokens with 2 sides 108.6 us, 1 114.6 us, 4 111 us, 8 116 us.
+constexpr int kByteSides = 2;
+inline void byte_split(int T, int B, int Hkv, int lg, int64_t wave, int64_t &groups, int &parts, int &per)
+{
+    groups = append_groups(T, B, lg);
+    per = 2 * groups * Hkv <= wave ? 1 : kByteSides;
+    parts = (int)((2 * (int64_t)Hkv + per - 1) / per);
+}
+
+// CTAs of an 8-bit append, of `ctas` resident ones of `cta_warps` warps each: warp w
+// keeps part w % parts of the sides and takes groups w / parts, and so on, w / parts
+// below warps / parts.
+inline int64_t byte_append_grid(int T, int B, int Hkv, int lg, int64_t ctas, int cta_warps, int64_t &groups, int &parts, int &per)
+{
+    const int64_t wave = ctas * cta_warps;
+    byte_split(T, B, Hkv, lg, wave, groups, parts, per);
+    if (parts > wave) {  // a warp keeps its part: no more of them than there are warps
+        per = (int)((2 * (int64_t)Hkv + wave - 1) / wave);
+        parts = (int)((2 * (int64_t)Hkv + per - 1) / per);
+    }
+    const int64_t all = (groups * parts + cta_warps - 1) / cta_warps;
+    return all < ctas ? all : ctas;
+}
+
+// CTAs of an 8-bit read: warp w has part w % parts of group w / parts, and no
+// other.
+inline int64_t byte_read_grid(int T, int B, int Hkv, int lg, int64_t ctas, int cta_warps, int64_t &groups, int &parts, int &per)
+{
+    byte_split(T, B, Hkv, lg, ctas * cta_warps, groups, parts, per);
+    return (groups * parts + cta_warps - 1) / cta_warps;
+}
+constexpr int kByteWarps = 8;  // of a CTA of either
 
 #ifdef __CUDACC__
 

@@ -24,19 +24,14 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = kByteWarps, kThreads = 32 * kWarps;
 constexpr int kOneThreads = 512;  // of the append of one token per row, at most
-// CTAs per SM, and a head's sides that a warp takes one after the other where
-// there is work for all warps.  A unit's warps should be near one another in time,
-// since a token's heads are neighbours in memory, but a warp has to look up its row
-// and page first.  35k tokens of 8 heads appended and read back: 2 sides each 73.4
-// us; the append with 4 77 us, 1 75 us, with 2 CTAs 78 us, 4 (spills) 81 us; the read
-// of 117k tokens with 2 sides 108.6 us, 1 114.6 us, 4 111 us, 8 116 us, with 3 CTAs 116
-// us, 5 (spills) 130 us.  Copies to shared memory ahead of use, or lines of
+// CTAs per SM.  35k tokens of 8 heads appended and read back 73.4 us; with 2 CTAs of
+// the append 78 us, 4 (spills) 81 us; the read of 117k tokens 108.6 us, with 3 CTAs
+// 116 us, 5 (spills) 130 us.  Copies to shared memory ahead of use, or lines of
 // neighbouring blocks with the next one's page looked up ahead, took longer: 84 and
 // 82 us.
-constexpr int kAppendCtas = 3, kReadCtas = 4, kSides = 2;
+constexpr int kAppendCtas = 3, kReadCtas = 4;
 
 // Which tokens and dims of a block of 2^LG tokens a lane holds: dims 8 piece ..,
 // tokens first .. first + kTokens - 1 (none where `first` is beyond the block).
@@ -482,17 +477,6 @@ cudaError_t launch(K kern, const P &p, int64_t grid, int threads, cudaStream_t s
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// How the blocks' sides are split over warps: one each where that is no more than
-// one wave of them, else kSides.  Of eight heads appended, one and kSides a warp: 500
-// tokens 4.3 and 5.7 us, 2k 6.0 and 6.2, 4k 10.8 and 9.7 us.
-template <class P>
-void split_sides(P &p, int lg, int64_t wave, int &per)
-{
-    p.groups = append_groups(p.T, p.B, lg);
-    per = 2 * p.groups * p.Hkv <= wave ? 1 : kSides;
-    p.parts = (2 * p.Hkv + per - 1) / per;
-}
-
 template <int D, int FMT, int LG>
 cudaError_t launch_append(QuantAppendParams p, int sms, cudaStream_t s)
 {
@@ -500,13 +484,7 @@ cudaError_t launch_append(QuantAppendParams p, int sms, cudaStream_t s)
         const int64_t threads = 32 * ((2 * (int64_t)p.Hkv * D + 127) / 128);
         return launch(byte_append_one_kernel<D, FMT, LG>, p, p.B, (int)(threads < kOneThreads ? threads : kOneThreads), s);
     }
-    const int64_t most = (int64_t)kAppendCtas * sms, wave = most * kWarps;
-    split_sides(p, LG, wave, p.its_per_part);
-    if (p.parts > wave) {  // a warp keeps its part: no more of them than there are warps
-        p.its_per_part = (int)((2 * (int64_t)p.Hkv + wave - 1) / wave);
-        p.parts = (2 * p.Hkv + p.its_per_part - 1) / p.its_per_part;
-    }
-    const int64_t all = (p.groups * p.parts + kWarps - 1) / kWarps, grid = all < most ? all : most;
+    const int64_t grid = byte_append_grid(p.T, p.B, p.Hkv, LG, (int64_t)kAppendCtas * sms, kWarps, p.groups, p.parts, p.its_per_part);
     // 64k tokens of 32 heads of d = 64: two sides at once 149 us, one after the other 161 us
     constexpr int AT = Lane<D, LG>::kAtOnce;
     return p.its_per_part < AT ? launch(byte_append_kernel<D, FMT, LG, 1>, p, grid, kThreads, s)
@@ -516,8 +494,8 @@ cudaError_t launch_append(QuantAppendParams p, int sms, cudaStream_t s)
 template <int D, int FMT, int LG>
 cudaError_t launch_read(QuantReadParams p, int sms, cudaStream_t s)
 {
-    split_sides(p, LG, (int64_t)kReadCtas * kWarps * sms, p.heads_per_part);
-    return launch(byte_read_kernel<D, FMT, LG>, p, (p.groups * p.parts + kWarps - 1) / kWarps, kThreads, s);
+    const int64_t grid = byte_read_grid(p.T, p.B, p.Hkv, LG, (int64_t)kReadCtas * sms, kWarps, p.groups, p.parts, p.heads_per_part);
+    return launch(byte_read_kernel<D, FMT, LG>, p, grid, kThreads, s);
 }
 
 // f<D, FMT, LG>() for the call's d, format and page size.
