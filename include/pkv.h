@@ -563,7 +563,8 @@ int pkv_byte_append(const pkv_shape_t *shape, void *d_ws, int32_t format, const 
                   const int32_t *d_seq_lens, int32_t *d_seq_lens_out, void *d_byte_cache, void *stream);
 
 /* pkv_byte_read -- read tokens of the 8-bit cache back as fp16.  One kernel launch.
- * Arguments and errors are those of pkv_quant_read. */
+ * Arguments and errors are those of pkv_quant_read; (2 B + total_out / SB) Hkv up to
+ * 2^34 - 8. */
 int pkv_byte_read(const pkv_shape_t *shape, void *d_ws, int32_t format, const void *d_byte_cache, const int32_t *d_block_table,
                 const int32_t *d_seq_lens, const int32_t *d_first, const int32_t *d_out_offsets, int32_t total_out,
                 void *d_k_out, void *d_v_out, int64_t out_stride, void *stream);

@@ -2,6 +2,7 @@
 // validation, TMA descriptor encoding, kernel launches on the caller's stream,
 // launch counters, the calibrated path policy and error reporting.
 #include "pkv.h"
+#include "append_map.cuh"
 #include "pkv_device.cuh"
 #include "pkv_kernels.h"
 #include "plan_map.cuh"
@@ -1429,6 +1430,10 @@ int pkv_byte_read(const pkv_shape_t *s, void *d_ws, int32_t format, const void *
     if (s->B == 0 || total_out == 0)
         return PKV_OK;  // nothing to read
     PKV_TRY(check_packed(s, total_out, out_stride, "k_out"));
+    int64_t groups;
+    int parts, per;
+    if (byte_read_grid(total_out, s->B, s->Hkv, ilog2(byte_scale_tokens(s->page_size)), 0, kByteWarps, groups, parts, per) > kMostCtas)
+        return fail(PKV_EUNSUPPORTED, "B=%d rows and %d tokens of %d KV heads exceed one launch", s->B, total_out, s->Hkv);
     PKV_TRY(check_ptr(d_ws, "workspace"));
     PKV_TRY(check_ptr(cache, "byte_cache"));
     PKV_TRY(check_ptr(bt, "block_table"));

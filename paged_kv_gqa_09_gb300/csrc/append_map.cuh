@@ -96,13 +96,14 @@ inline int64_t byte_append_grid(int T, int B, int Hkv, int lg, int64_t ctas, int
 }
 
 // CTAs of an 8-bit read: warp w has part w % parts of group w / parts, and no
-// other.
+// other.  With ctas = 0 the most there may be for any number of resident ones.
 inline int64_t byte_read_grid(int T, int B, int Hkv, int lg, int64_t ctas, int cta_warps, int64_t &groups, int &parts, int &per)
 {
     byte_split(T, B, Hkv, lg, ctas * cta_warps, groups, parts, per);
     return (groups * parts + cta_warps - 1) / cta_warps;
 }
 constexpr int kByteWarps = 8;  // of a CTA of either
+constexpr int64_t kMostCtas = 0x7fffffff;
 
 #ifdef __CUDACC__
 

@@ -1,5 +1,5 @@
 """The launches of the 8-bit append and read on the CPU: every side of every scale
-block has one warp."""
+block has one warp, and calls beyond one launch are refused."""
 import ctypes
 import os
 import shutil
@@ -8,7 +8,11 @@ import subprocess
 import numpy as np
 import pytest
 
+from paged_kv_gqa_09_gb300 import _lib
+from test_byte_host import L, calls, shape  # noqa: F401 (L is a fixture)
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+MOST = 2 ** 31 - 1  # CTAs of a launch
 
 
 @pytest.fixture(scope="module")
@@ -50,3 +54,11 @@ def test_the_sizes_of_large_launches(grid):
         assert out[0] == groups and out[3] == -(-groups * Hkv // 8)  # two sides a warp, eight warps a CTA
         grid.byte_append_units(T, B, Hkv, lg, 456, None, out.ctypes.data)
         assert out[0] == groups and out[3] == 456
+
+
+def test_reads_beyond_one_launch_are_refused(L):
+    for B, Hkv, P in ((1 << 30, 8, 16), (1 << 28, 64, 16), (1 << 28, 32, 256), (1 << 30, 128, 8)):
+        s = shape(B=B, Hq=Hkv, Hkv=Hkv, page_size=P, bt_stride=1)
+        assert -(-2 * B * Hkv // 8) > MOST
+        assert calls(L, s, T=5, stride=Hkv * 128)["read"]() == _lib.PKV_EUNSUPPORTED
+        assert "one launch" in _lib.last_error()
