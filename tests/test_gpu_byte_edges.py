@@ -106,6 +106,22 @@ def test_bytes_behind_the_rows_beside_the_greatest_scale(fmt, d, P):
         b.check(queries(b), 3, 2)
 
 
+@pytest.mark.parametrize("P", [8, 16, 32, 64, 128])
+def test_a_wait_that_runs_out_with_more_heads_than_ctas(P):
+    rng = np.random.default_rng(P)
+    lens = rng.integers(100, 400, 90).tolist()
+    for fmt in (R.INT8, R.E4M3):
+        b = Batch(fmt, lens, Hkv=4, G=3, d=128, P=P, seed=P)
+        b.grow(lens)
+        q = queries(b)
+        b.check(q)
+        assert _lib.load().pkv_test_starve_next_decodes(1) == 0
+        b.decode(q)
+        assert api.pkv_get_error(b.ws)[0] == _lib.PKV_ETIMEOUT
+        b.ws.zero_()  # the counters of a launch that gave up
+        b.check(q)
+
+
 # ------------------------------------------------------------------ refused appends
 
 @FORMATS
