@@ -491,7 +491,8 @@ int pkv_window_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d
  *   seq_lens_out[i] = N + n (it may be seq_lens: in place);
  *   *d_free_count_out = what is left (it may be d_free_count).
  * Entries of slot_map and positions behind the last token, up to total_new, are
- * -1 and 0, so that a call captured for total_new tokens serves fewer.
+ * -1 and 0, so that a call captured for total_new tokens serves fewer; those, the
+ * offsets and the free count are written with B = 0 too.
  * A row is refused whole, and the error word records one that is, when it
  * has a negative length or new length or no room in its block table, when its
  * tokens pass total_new, or when it needs pages and the rows up to and including

@@ -1486,17 +1486,18 @@ int pkv_map_pages(const pkv_shape_t *s, void *d_ws, const int32_t *sl, const int
                   int32_t *new_offsets, int64_t *slot_map, int32_t *positions, int32_t total_new, void *stream)
 {
     PKV_TRY(check_shape(s));
-    if (s->B == 0)
-        return PKV_OK;  // an empty batch: nothing to do
+    const bool empty = s->B == 0;  // then offsets, free count and padding are all that is written
+    if (empty && total_new == 0 && !new_offsets && !free_count_out)
+        return PKV_OK;
     if (total_new < 0 || free_capacity < 0)
         return fail(PKV_EINVAL, "negative total_new=%d or free_capacity=%d", total_new, free_capacity);
     if (s->B > 1 << 30 || total_new > 0x7fffffff - 4)  // the ends of a thread's rows and of a group of tokens are int32s
         return fail(PKV_EUNSUPPORTED, "B=%d rows, %d tokens (supported: up to 2^30 and 2^31 - 5)", s->B, total_new);
     PKV_TRY(check_ptr(d_ws, "workspace"));
-    PKV_TRY(check_ptr(sl, "seq_lens"));
-    PKV_TRY(check_ptr(new_lens, "new_lens"));
-    PKV_TRY(check_ptr(sl_out, "seq_lens_out"));
-    PKV_TRY(check_ptr(bt, "block_table"));
+    PKV_TRY(check_ptr(sl, "seq_lens", empty));
+    PKV_TRY(check_ptr(new_lens, "new_lens", empty));
+    PKV_TRY(check_ptr(sl_out, "seq_lens_out", empty));
+    PKV_TRY(check_ptr(bt, "block_table", empty));
     PKV_TRY(check_ptr(free_pages, "free_pages", free_capacity == 0));
     PKV_TRY(check_ptr(free_count, "free_count"));
     PKV_TRY(check_ptr(free_count_out, "free_count_out"));

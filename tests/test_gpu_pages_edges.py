@@ -69,3 +69,20 @@ def test_rows_that_find_no_page_are_not_appended(kind):
     assert append(kind, m, cache, x, m.sl, m.off).tolist() == [12, 20, 9]
     if kind != "4-bit":  # whose scales are each token's own: what lies behind a row's end is nobody's
         assert int(cache[m.table[1, :2].tolist()].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("T", [0, 5, 4099, 700000])
+@pytest.mark.parametrize("positions", [False, True])
+def test_a_map_of_no_rows_writes_what_needs_none(T, positions):
+    """A padded batch without a request: no slot of an earlier call is left, and no page is taken."""
+    i32 = lambda n, x=-77: torch.full((n,), x, dtype=torch.int32, device="cuda")
+    table = torch.zeros((0, 3), dtype=torch.int32, device="cuda")
+    shape = _lib.Shape(0, 1, 1, 128, 16, 9, 3, 1.0)
+    ws = torch.zeros(api.pkv_attn_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    slots, pos = torch.full((T,), 3, dtype=torch.int64, device="cuda"), i32(T) if positions else None
+    off, count, left = i32(1), i32(1, 4), i32(1)
+    for out in (left, None):
+        api.pkv_map_pages(shape, ws, i32(0), i32(0), table, i32(9, 1), count, slots, off, free_count_out=out, positions=pos)
+        assert (slots == -1).all() and (pos is None or (pos == 0).all()) and off.tolist() == [0] and count.tolist() == [4]
+    assert left.tolist() == [4] and api.pkv_get_error(ws)[0] == 0
+    assert int(ws.view(torch.int32).abs().sum()) == 0
