@@ -13,6 +13,7 @@
 
 #include <cstdint>
 #include <exception>
+#include <initializer_list>
 #include <string>
 
 #include "pkv.h"
@@ -111,18 +112,32 @@ struct Call {
     int32_t *table(PyObject *o) { return arg<int32_t>(o, "block_table", at::kInt, (int64_t)s.B * s.bt_stride); }
     int32_t *lens(PyObject *o, const char *name = "seq_lens", bool nullable = false) { return arg<int32_t>(o, name, at::kInt, s.B, nullable); }
     int32_t *offsets(PyObject *o, const char *name, bool nullable) { return arg<int32_t>(o, name, at::kInt, (int64_t)s.B + 1, nullable); }
-    void *rows(PyObject *o, const char *name) { return arg(o, name, at::kHalf, (int64_t)s.B * s.Hq * s.d); }
+    // Elements of an array of these extents, INT64_MAX where that many cannot be
+    // counted; 0 with an extent of a bad shape, which the call itself refuses.
+    static int64_t elements(std::initializer_list<int64_t> extents)
+    {
+        int64_t n = 1;
+        for (int64_t x : extents)
+            if (x <= 0)
+                return 0;
+        for (int64_t x : extents)
+            if (__builtin_mul_overflow(n, x, &n))
+                return INT64_MAX;
+        return n;
+    }
+
+    void *rows(PyObject *o, const char *name) { return arg(o, name, at::kHalf, elements({s.B, s.Hq, s.d})); }
     float *lse(PyObject *o) { return arg<float>(o, "lse", at::kFloat, (int64_t)s.B * s.Hq, true); }
-    void *pages(PyObject *o, const char *name) { return arg(o, name, at::kHalf, (int64_t)s.num_pages * s.page_size * s.Hkv * s.d); }
+    void *pages(PyObject *o, const char *name) { return arg(o, name, at::kHalf, elements({s.num_pages, s.page_size, s.Hkv, s.d})); }
     void *quant(PyObject *o)
     {
-        return arg(o, "quant_cache", at::kByte, (int64_t)s.num_pages * s.Hkv * ((int64_t)s.page_size * s.d * 5 / 4));
+        return arg(o, "quant_cache", at::kByte, elements({s.num_pages, s.Hkv, (int64_t)s.page_size * s.d * 5 / 4}));
     }
 
     void *codes(PyObject *o)
     {
-        const int64_t tb = s.page_size < 64 ? s.page_size : 64;  // 0 or less: the call itself refuses the shape
-        return arg(o, "byte_cache", at::kByte, tb < 1 ? 0 : (int64_t)s.num_pages * s.Hkv * (s.page_size / tb) * (2 * tb * s.d + (tb == 64 ? 32 : 16)));
+        const int64_t tb = s.page_size < 64 ? s.page_size : 64, blocks = tb < 1 ? 0 : s.page_size / tb;
+        return arg(o, "byte_cache", at::kByte, elements({s.num_pages, s.Hkv, blocks, 2 * tb * s.d + (tb == 64 ? 32 : 16)}));
     }
 
     // Packed K and V [T, Hkv, d], whose tokens may be strided (alike in both);

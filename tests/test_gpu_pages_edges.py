@@ -86,3 +86,23 @@ def test_a_map_of_no_rows_writes_what_needs_none(T, positions):
         assert (slots == -1).all() and (pos is None or (pos == 0).all()) and off.tolist() == [0] and count.tolist() == [4]
     assert left.tolist() == [4] and api.pkv_get_error(ws)[0] == 0
     assert int(ws.view(torch.int32).abs().sum()) == 0
+
+
+@pytest.mark.parametrize("pages,Hkv", [(2 ** 31 - 1, 2 ** 18), (2 ** 30, 2 ** 17), (2 ** 31 - 1, 2 ** 17)])
+def test_caches_whose_size_passes_64_bits_are_refused(pages, Hkv):
+    """A shape that names more pages and heads than can be counted is no small cache's."""
+    half = lambda *n: torch.zeros(n, dtype=torch.float16, device="cuda")
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    shape = _lib.Shape(1, Hkv, Hkv, 128, 256, pages, 1, 1.0)
+    ws = torch.zeros(api.pkv_attn_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    q, small, codes, bt, lens = half(1, Hkv, 128), half(1, 256, 1, 128), torch.zeros(70000, dtype=torch.uint8, device="cuda"), i32(1, 1), i32(1)
+    slots = torch.full((1,), -1, dtype=torch.int64, device="cuda")
+    for call in (lambda: api.pkv_byte_decode(shape, ws, R.INT8, q, codes, bt, lens, torch.empty_like(q)),
+                 lambda: api.pkv_byte_append(shape, ws, R.E4M3, q, q, bt, lens, codes),
+                 lambda: api.pkv_byte_read(shape, ws, R.E4M3, codes, bt, lens, i32(2), q, q),
+                 lambda: api.pkv_quant_decode(shape, ws, q, codes, bt, lens, torch.empty_like(q)),
+                 lambda: api.pkv_quant_append(shape, ws, q, q, bt, lens, codes),
+                 lambda: api.pkv_window_decode(shape, ws, q, small, small, bt, lens, 4, 0, torch.empty_like(q)),
+                 lambda: api.pkv_append_slots(shape, ws, q, q, slots, small, small)):
+        with pytest.raises(ValueError, match="elements, needs"):
+            call()
