@@ -9,10 +9,10 @@
 // One pass over the cache: 4 d flops per visible token and query head against
 // 1.25 d bytes (4-bit), 2 d (8-bit) or 4 d (fp16) per token and KV head.  HBM
 // bounds long batches (d = 128: 64 rows, 1.9M tokens of the 4-bit cache, 2.44 GB in
-// 383 us; 2.1M of the 8-bit cache, 4.32 GB in 615 us; 64 rows in a window of 8191
+// 383 us; 2.1M of the 8-bit cache, 4.32 GB in 617 us; 64 rows in a window of 8191
 // over fp16 pages, 1.85 GB in 274 us at most); the 4-bit cache's unpacking and
 // latency short ones (117k tokens, 150 MB, 33.6 us; 120k of the 8-bit cache, 247 MB,
-// 40.5 us; one row of 32k, 42 MB, 18.2 us).
+// 40.9 us; one row of 32k, 42 MB, 18.2 us).
 //
 // Work split.  A row's visible tokens lie in T_i tiles of 128 tokens (64 of fp16
 // pages with d = 128, 256 of the 4-bit cache with d = 64; those between the sinks
@@ -142,18 +142,20 @@ struct Layout {
     static constexpr int kKvBytes = BYTE ? (kTile >> kBlockLog2<KIND>) * byte_block_bytes(1 << kBlockLog2<KIND>, D) : QUANT ? kTile * D * 5 / 4 : 2 * kTileBytes;
     static constexpr int kQBytes = kMaxG * D * 2;
     static constexpr int kStageBytes = kKvBytes + kQBytes;
-    // as many CTAs as registers or shared memory hold; for the 4-bit cache's three
-    // and four the compiler keeps 12 to 36 bytes a thread (84 in clusters with d = 64)
-    // of its 128 and 96 registers' worth in local memory.  fp16 pages with d = 64 (a
+    // as many CTAs as registers or shared memory hold; where that is three of 128
+    // registers or four of 96 the compiler keeps some of a thread's in local memory:
+    // 8 to 24 bytes over the 4-bit cache (in clusters of d = 128 and blocks of 64
+    // alone), over the 8-bit one 8 in runs of d = 64 and 24 to 32 in kMany's of e4m3
+    // and blocks of 16 to 64.  fp16 pages with d = 64 (a
     // head's token is one 128-byte line among the others' heads) want more loads
     // from more warps in flight: 64 rows in a window of 8191, three CTAs of two
     // stages 166 us, two of three 208 us; clusters the latter (12.8 and 14.9 us
     // for eight rows).  The 8-bit cache's tiles are 32 KB with d = 128: two CTAs of
     // three stages (eight rows of up to 32k tokens 42.4 us, one of 32k 19.8 us;
     // three of two 43.2 and 21.0 us), but see launch_one() for kMany; tiles of 64
-    // tokens, in five stages, leave a warp one block at a time (eight rows 57 us).  With d = 64, 64 rows of up to 32k: four CTAs of three stages
-    // 177.5 us, three of four 179.5 us, but in clusters 8.1 and 7.4 us (five rows in a
-    // window)
+    // tokens, in five stages, leave a warp one block at a time (eight rows 57 us).
+    // With d = 64, 64 rows of up to 32k: four CTAs of three stages 177.5 us, three of
+    // four 179.5 us, but in clusters 8.1 and 7.4 us (five rows in a window)
     static constexpr int kCtasPerSm = BYTE ? (D == 128 ? (KIND < kMany ? 2 : 3) : CLUSTER ? 3 : 4) : QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
     static constexpr int kStages = BYTE ? (KIND >= kMany ? 2 : D == 64 && CLUSTER ? 4 : 3) : QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
@@ -933,8 +935,8 @@ __device__ __forceinline__ uint32_t byte_rows(uint32_t vis)
 // K's scale is a factor of the scores.  V's multiplies what a block's codes add to
 // O, in fp32; in pages of 8, where a product is over two blocks, the codes, whose
 // values are exact fp16 numbers.  (In the weights' exponents, and out of the sum
-// again, it costs 1% less, 3% in pages of 8, but then the fp16 weights have to span the scales too:
-// beside a block of a scale 2^31 times as great, values were lost.)
+// again, it costs 1% less, 3% in pages of 8, but then the fp16 weights have to span
+// the scales too: beside a block of a scale 2^31 times as great, values were lost.)
 template <int D, int KIND>
 __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D / 16][2], const uint8_t *kv, uint32_t vis, int w, float sl2)
 {
@@ -1599,7 +1601,10 @@ struct Launch {
 // where there can be (two rows of 2k .. 8k, 7.9 and 8.5 us); 4 tiles, two an SM,
 // 10.1 and 10.5 us (four rows), 8 tiles 15.0 and 13.4 us (eight).  8-bit, two an SM:
 // 8 tiles, 16.0 and 18.6 us (eight rows of 4k); 10 tiles, 15.6 and 19.5 us (32 rows in a
-// window of 1000); 16 tiles, 23.1 and 21.9 us (32 rows of 512 .. 2048).
+// window of 1000); 16 tiles, 23.1 and 21.9 us (32 rows of 512 .. 2048).  With an SM of
+// its own (e4m3, one KV head) a limit of 6, then 8, is right there too: with 3, then 4,
+// 15 rows of 4k take 7.2 instead of 6.8 us (d = 64) and 16 of 8k 12.9 instead of 11.9 (d =
+// 128); with 12, then 16, 37 rows of 4k 9.7 instead of 8.4 us (d = 64).
 constexpr int kMaxTilesFp16 = 20;
 constexpr int kMaxTilesOwn[2] = {6, 8};  // CTAs with an SM of their own: tried first, tried last
 constexpr int kMaxTilesShared[2] = {4, 10};  // 4-bit, 8-bit

@@ -8,7 +8,7 @@
 // Both are one pass over their data: append reads 2 bytes per value and writes
 // one, read the other way round.  35k tokens of 8 heads, d = 128, appended (213 MB,
 // 31 us at the copy rate) and read back at once take 73 us; 117k tokens read, 718
-// MB, 108 us, 0.97 of the copy rate; a token of each of 64 rows and its block 7.6 us.
+// MB, 109 us, 0.97 of the copy rate; a token of each of 64 rows and its block 7.6 us.
 //
 // A warp takes a scale block (16 tokens, 8 in pages of 8) of one head and side at
 // a time: a lane holds 8 dims of 8 or 4 neighbouring tokens, so that the block's
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) byte_append_kernel(cons
         const int first = (int)b.pos0 + ln.first;  // of this lane's positions; the row's end is an int
         const int64_t from = (int64_t)b.off * p.new_stride + 8 * ln.piece;
         // Blocks of new tokens alone go without the tests of each token: 64 x 1000
-        // tokens of 8 heads, d = 64, in 37.1 us against 41.7; of d = 128, whose lanes hold
+        // tokens of 8 heads, d = 64, in 37.6 us against 42.0; of d = 128, whose lanes hold
         // twice the tokens, no gain (67.0 and 66.8 us), and registers spill.
         const bool whole = TL == 4 && b.pos0 >= b.N && b.pos0 + (1 << LG) <= (int64_t)b.N + b.n;
         auto sides = [&](auto all) {
@@ -485,7 +485,7 @@ cudaError_t launch_append(QuantAppendParams p, int sms, cudaStream_t s)
         return launch(byte_append_one_kernel<D, FMT, LG>, p, p.B, (int)(threads < kOneThreads ? threads : kOneThreads), s);
     }
     const int64_t grid = byte_append_grid(p.T, p.B, p.Hkv, LG, (int64_t)kAppendCtas * sms, kWarps, p.groups, p.parts, p.its_per_part);
-    // 64k tokens of 32 heads of d = 64: two sides at once 149 us, one after the other 161 us
+    // 64k tokens of 32 heads of d = 64: two sides at once 132 us, one after the other 150 us
     constexpr int AT = Lane<D, LG>::kAtOnce;
     return p.its_per_part < AT ? launch(byte_append_kernel<D, FMT, LG, 1>, p, grid, kThreads, s)
                                : launch(byte_append_kernel<D, FMT, LG, AT>, p, grid, kThreads, s);
