@@ -573,8 +573,8 @@ int pkv_byte_read(const pkv_shape_t *shape, void *d_ws, int32_t format, const vo
 /* pkv_byte_decode -- one decode step's attention over the 8-bit cache.  One kernel
  * launch.  o and lse are those of pkv_single_pass over the values that
  * pkv_byte_read returns, with fp32 sums; in the product with V, not in their sum, a
- * head's softmax weights are rounded to fp16 (by 2^-11 of each, or the smallest by
- * 2^-32 of the greatest).  Window, empty rows and heads whose scores are all -inf
+ * head's softmax weights are two fp16 numbers each (off by 2^-22 of it, the smallest
+ * by 2^-32 of the greatest).  Window, empty rows and heads whose scores are all -inf
  * as for pkv_quant_decode.  A head that sees a token of a NaN block,
  * of K or of V, gets NaN for o and lse. */
 int pkv_byte_decode(const pkv_shape_t *shape, const pkv_window_t *win, void *d_ws, int32_t format, const void *d_q,

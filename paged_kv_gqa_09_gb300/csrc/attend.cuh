@@ -9,10 +9,10 @@
 // One pass over the cache: 4 d flops per visible token and query head against
 // 1.25 d bytes (4-bit), 2 d (8-bit) or 4 d (fp16) per token and KV head.  HBM
 // bounds long batches (d = 128: 64 rows, 1.9M tokens of the 4-bit cache, 2.44 GB in
-// 383 us; 2.1M of the 8-bit cache, 4.32 GB in 617 us; 64 rows in a window of 8191
+// 383 us; 2.1M of the 8-bit cache, 4.32 GB in 624 us; 64 rows in a window of 8191
 // over fp16 pages, 1.85 GB in 274 us at most); the 4-bit cache's unpacking and
 // latency short ones (117k tokens, 150 MB, 33.6 us; 120k of the 8-bit cache, 247 MB,
-// 40.9 us; one row of 32k, 42 MB, 18.2 us).
+// 41.1 us; one row of 32k, 42 MB, 18.2 us).
 //
 // Work split.  A row's visible tokens lie in T_i tiles of 128 tokens (64 of fp16
 // pages with d = 128, 256 of the 4-bit cache with d = 64; those between the sinks
@@ -64,6 +64,30 @@ constexpr float kNoMax = -3.402823466e38f;  // m before the first score: the lea
 constexpr float kNoTiles = -1.f;            // in place of a sum of weights: a cluster's CTA that has none to give
 constexpr float kHalfMax = 65504.f;
 
+// What a tile is made of.  kFp16: the fp16 pages; else a cache of codes, the log2
+// of its tokens per block added to what it is, so that its tiles' addresses are
+// constants.
+constexpr int kFp16 = 0, k4Bit = 0, k8Bit = 16;  // k8Bit + 16 FMT
+constexpr int kMany = 64;                        // + kMany: the 8-bit cache with d = 128, for many (row, head)s
+constexpr int kFew = 128;                        // + kFew: the 8-bit cache, four query heads per KV head or less
+
+template <int KIND>
+constexpr bool kIs8Bit = KIND >= k8Bit;
+template <int KIND>
+constexpr int kBlockLog2 = KIND & 15;
+template <int KIND>
+constexpr int kFormat = KIND % kMany / 16 - 1;  // of an 8-bit cache
+
+// The softmax weights that enter the product with V: fp16, the tensor cores' operand
+// type, holds 11 bits of each, and what that rounding leaves is one more fp16 number.
+// It is left out, is the weight of another column of the operand's eight -- a KV
+// head's query heads, up to four then -- or has a product of its own.
+enum class Weights { kRounded, kBeside, kTwice };
+template <int KIND>
+constexpr Weights kWeights = !kIs8Bit<KIND> ? Weights::kRounded : KIND & kFew ? Weights::kBeside : Weights::kTwice;
+template <Weights W>
+constexpr int kProducts = W == Weights::kTwice ? 2 : 1;
+
 // The m that scores are taken from is set this far below a warp's greatest score
 // (in log2 units), and set again only when one exceeds it by more than kMaxOver:
 // the greatest weights lie in 2^7 .. 2^15, at the upper end of fp16, and most
@@ -90,19 +114,6 @@ constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 // through distributed shared memory instead of global memory and an arrival
 // there, which takes 2 us less.
 constexpr int kMaxClusterLog2 = 4, kMaxCluster = 1 << kMaxClusterLog2;
-
-// What a tile is made of.  kFp16: the fp16 pages; else a cache of codes, the log2
-// of its tokens per block added to what it is, so that its tiles' addresses are
-// constants.
-constexpr int kFp16 = 0, k4Bit = 0, k8Bit = 16;  // k8Bit + 16 FMT
-constexpr int kMany = 64;                        // + kMany: the 8-bit cache with d = 128, for many (row, head)s
-
-template <int KIND>
-constexpr bool kIs8Bit = KIND >= k8Bit;
-template <int KIND>
-constexpr int kBlockLog2 = KIND & 15;
-template <int KIND>
-constexpr int kFormat = KIND % kMany / 16 - 1;  // of an 8-bit cache
 
 // Bytes of a block, and how one becomes zeros: by the numbers that scale its codes
 // or, where a code's own bits may be a NaN's (whatever shared memory held), whole.
@@ -145,8 +156,8 @@ struct Layout {
     // as many CTAs as registers or shared memory hold; where that is three of 128
     // registers or four of 96 the compiler keeps some of a thread's in local memory:
     // 8 to 24 bytes over the 4-bit cache (in clusters of d = 128 and blocks of 64
-    // alone), over the 8-bit one 8 in runs of d = 64 and 24 to 32 in kMany's of e4m3
-    // and blocks of 16 to 64.  fp16 pages with d = 64 (a
+    // alone), over the 8-bit one 8 in runs of d = 64 and, in blocks of 16 to 64 of
+    // kMany, 24 with kFew and e4m3 and 40 without kFew.  fp16 pages with d = 64 (a
     // head's token is one 128-byte line among the others' heads) want more loads
     // from more warps in flight: 64 rows in a window of 8191, three CTAs of two
     // stages 166 us, two of three 208 us; clusters the latter (12.8 and 14.9 us
@@ -156,8 +167,8 @@ struct Layout {
     // tokens, in five stages, leave a warp one block at a time (eight rows 57 us).
     // With d = 64, 64 rows of up to 32k: four CTAs of three stages 177.5 us, three of
     // four 179.5 us, but in clusters 8.1 and 7.4 us (five rows in a window)
-    static constexpr int kCtasPerSm = BYTE ? (D == 128 ? (KIND < kMany ? 2 : 3) : CLUSTER ? 3 : 4) : QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
-    static constexpr int kStages = BYTE ? (KIND >= kMany ? 2 : D == 64 && CLUSTER ? 4 : 3) : QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
+    static constexpr int kCtasPerSm = BYTE ? (D == 128 ? (KIND & kMany ? 3 : 2) : CLUSTER ? 3 : 4) : QUANT ? (D == 64 ? 4 : 3) : D == 64 && !CLUSTER ? 3 : 2;
+    static constexpr int kStages = BYTE ? (KIND & kMany ? 2 : D == 64 && CLUSTER ? 4 : 3) : QUANT ? (D == 64 ? (CLUSTER ? 4 : 2) : 3) : D == 64 && !CLUSTER ? 2 : 3;
     static constexpr int kMetaOff = kStages * kStageBytes;          // two int4 per stage
     static constexpr int kRedOff = kMetaOff + kStages * 32;         // m, l of [piece parity][warp][head]
     static constexpr int kBarOff = kRedOff + 2 * kCW * kMaxG * 2 * 4;   // full[S], empty[S], consumers
@@ -666,6 +677,8 @@ __device__ __forceinline__ int dim_of(int x, int r0)
 template <int KIND>
 constexpr int kDimStep = kIs8Bit<KIND> ? 1 : 8;
 
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+
 // What turns a raw score of block u into units of log2: one factor for all, or K's
 // scale with it, that of a lane's two tokens.
 struct OneScale {
@@ -681,16 +694,20 @@ struct BlockScales {
 // Raw scores x[b] of MT blocks of 16 tokens -- x[b][0], x[b][1]: token r0 with
 // heads h0 and h0 + 1, x[b][2], x[b][3]: token r0 + 8; bit 16 b + token of
 // `vis` set where visible -- enter the running softmax in units of log2;
-// returns the weights as the B operands of the PV product.  The weights are
-// rounded to fp16, the tensor cores' operand type, which costs o about as much
-// as its own rounding (2^-11 of the mean |v| at most); their sum is kept in fp32
-// before that rounding, so that lse is not rounded with them.  (Over the 8-bit
-// cache o is off by 2.1e-4 to 2.7e-4 of its size, where its own rounding alone is
-// 2.0e-4.  A second product with what the weights' rounding left brings that down
-// to 2.0e-4, and takes 16 rows of 1k from 9.1 to 9.6 us, eight of 4k from 14.0 to 15.0,
-// 100 of 100 from 13.2 to 14.7.)
-template <int D, int MT, class Scales>
-__device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][4], uint32_t vis, const Scales &sc, uint32_t (&P)[MT][2])
+// returns the weights as the B operands of the PV product, rounded to fp16 and, with
+// kTwice, what that left; with kBeside that is in place of heads 4 and more, whose
+// scores have to be those of heads 0 and more once again.  Rounded alone they cost o
+// about as much as its own rounding (2^-11 of the mean |v| at most; o is off by
+// 2.1e-4 to 2.9e-4 of its size, else by 2.0e-4 to 2.1e-4).  Their sum is kept in fp32
+// before that rounding, so that lse is not rounded with them.  Over the 8-bit cache
+// nothing is left out.  That takes, beside: 16 rows of 1k 9.05 -> 9.30 us, eight of 4k
+// 13.96 -> 14.2, 100 of 100 13.2 -> 13.6, 64 in a window of 4096 78.0 -> 78.4; twice, with
+// eight heads, the same: 9.2 -> 9.7, 14.1 -> 15.0, 13.7 -> 15.3, 79.1 -> 81.5; 64 rows of up
+// to 60k 0.4% and 1.2%.  (One kernel for either, which picks by the head count, took a
+// row of 1k from 4.9 to 5.4.)
+template <int D, int MT, Weights W, class Scales>
+__device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][4], uint32_t vis, const Scales &sc,
+                                             uint32_t (&P)[kProducts<W>][MT][2])
 {
     constexpr uint32_t kAll = MT == 2 ? 0xffffffffu : 0xffffu;
     const int r0 = (threadIdx.x & 31) >> 2;
@@ -755,8 +772,20 @@ __device__ __forceinline__ void softmax_step(State<D> &st, const float (&x)[MT][
         const float p0 = ex2(y[u][0]), p1 = ex2(y[u][1]), p2 = ex2(y[u][2]), p3 = ex2(y[u][3]);
         st.l0 += p0 + p2;
         st.l1 += p1 + p3;
-        P[u][0] = movmatrix_t(pack_half2(p0, p1));
-        P[u][1] = movmatrix_t(pack_half2(p2, p3));
+        uint32_t a = pack_half2(p0, p1), b = pack_half2(p2, p3);
+        if constexpr (W != Weights::kRounded) {
+            const float2 fa = __half22float2(as_half2(a)), fb = __half22float2(as_half2(b));
+            const uint32_t ra = pack_half2(p0 - fa.x, p1 - fa.y), rb = pack_half2(p2 - fb.x, p3 - fb.y);
+            if constexpr (W == Weights::kBeside) {
+                if (threadIdx.x & 2)
+                    a = ra, b = rb;
+            } else {
+                P[1][u][0] = movmatrix_t(ra);
+                P[1][u][1] = movmatrix_t(rb);
+            }
+        }
+        P[0][u][0] = movmatrix_t(a);
+        P[0][u][1] = movmatrix_t(b);
     }
 }
 
@@ -799,8 +828,8 @@ __device__ __forceinline__ void fp16_tile(State<D> &st, const uint32_t (&qf)[D /
         for (int e = 0; e < 4; ++e)
             x[u][e] = sa[e] + sb[e];
     }
-    uint32_t P[MT][2];
-    softmax_step<D, MT>(st, x, vis, OneScale{sl2}, P);
+    uint32_t P[1][MT][2];
+    softmax_step<D, MT, Weights::kRounded>(st, x, vis, OneScale{sl2}, P);
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const uint32_t rowV = row_base<D>(TW * w + 16 * u + (mi >> 1) * 8 + r8, btl);
@@ -809,7 +838,7 @@ __device__ __forceinline__ void fp16_tile(State<D> &st, const uint32_t (&qf)[D /
             const uint32_t cc = (uint32_t)((((2 * z) & 7) + (mi & 1)) ^ r8) << 4;
             uint32_t a0, a1, a2, a3;
             ldsm_x4_t(vt + rowV + (z >> 2) * blk + cc, a0, a1, a2, a3);
-            mma_16816(st.O[z], a0, a1, a2, a3, P[u][0], P[u][1]);
+            mma_16816(st.O[z], a0, a1, a2, a3, P[0][u][0], P[0][u][1]);
         }
     }
 }
@@ -829,8 +858,6 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[GR])
         w[1] = v.y;
     }
 }
-
-__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 
 // One tile of the 4-bit cache, of which this warp takes 32 tokens, four groups
 // of eight: codes go from shared memory to the fragments of the tensor cores' A
@@ -870,8 +897,8 @@ __device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D 
                       quant_value(quant_field<3>(k0[u][j]), s0j, b0j), quant_value(quant_field<3>(k1[u][j]), s1j, b1j),
                       qf[2 * j + 1][0], qf[2 * j + 1][1]);
         }
-    uint32_t P[MT][2];
-    softmax_step<D, MT>(st, x, vis, OneScale{sl2}, P);
+    uint32_t P[1][MT][2];
+    softmax_step<D, MT, Weights::kRounded>(st, x, vis, OneScale{sl2}, P);
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         uint32_t v0[GR], v1[GR], c0[2 * GR], c1[2 * GR];
@@ -902,9 +929,9 @@ __device__ __forceinline__ void quant_tile(State<D> &st, const uint32_t (&qf)[D 
             const __half2 s0 = as_half2(c0[2 * j]), b0 = as_half2(c0[2 * j + 1]);
             const __half2 s1 = as_half2(c1[2 * j]), b1 = as_half2(c1[2 * j + 1]);
             mma_16816(st.O[2 * j], quant_value(quant_field<0>(v0[j]), s0, b0), quant_value(quant_field<1>(v0[j]), s0, b0),
-                      quant_value(quant_field<0>(v1[j]), s1, b1), quant_value(quant_field<1>(v1[j]), s1, b1), P[u][0], P[u][1]);
+                      quant_value(quant_field<0>(v1[j]), s1, b1), quant_value(quant_field<1>(v1[j]), s1, b1), P[0][u][0], P[0][u][1]);
             mma_16816(st.O[2 * j + 1], quant_value(quant_field<2>(v0[j]), s0, b0), quant_value(quant_field<3>(v0[j]), s0, b0),
-                      quant_value(quant_field<2>(v1[j]), s1, b1), quant_value(quant_field<3>(v1[j]), s1, b1), P[u][0], P[u][1]);
+                      quant_value(quant_field<2>(v1[j]), s1, b1), quant_value(quant_field<3>(v1[j]), s1, b1), P[0][u][0], P[0][u][1]);
         }
     }
 }
@@ -978,13 +1005,19 @@ __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D /
                 byte_numbers<FMT>(word(kc[u][1][c]), a1, a3);
                 mma_16816(x[u], a0, a1, a2, a3, qf[4 * c + j][0], qf[4 * c + j][1]);
             }
-    uint32_t P[MT][2];
-    softmax_step<D, MT>(st, x, byte_rows(vis), sc, P);
+    constexpr Weights W = kWeights<KIND>;
+    uint32_t P[kProducts<W>][MT][2];
+    softmax_step<D, MT, W>(st, x, byte_rows(vis), sc, P);
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const int at = 32 * w + 16 * u + (LG == 3 ? 8 * (t >> 1) : 0), r = at & (TB - 1);
         const uint8_t *vp = kv + (at >> TBL) * BYTES + byte_v_part<D>(TB, r, LG);
-        const uint32_t p0 = __byte_perm(P[u][0], P[u][1], 0x5410), p1 = __byte_perm(P[u][0], P[u][1], 0x7632);
+        uint32_t p[kProducts<W>][2];
+#pragma unroll
+        for (int z = 0; z < kProducts<W>; ++z) {
+            p[z][0] = __byte_perm(P[z][u][0], P[z][u][1], 0x5410);
+            p[z][1] = __byte_perm(P[z][u][0], P[z][u][1], 0x7632);
+        }
         // masked tokens' bytes may be any: a weight of 0 does not hide an e4m3 NaN, nor an infinity that a scale makes
         uint32_t keep = 0xffffffffu;
         if ((FMT == kE4m3 || LG == 3) && vis != 0xffffffffu)
@@ -999,12 +1032,17 @@ __device__ __forceinline__ void byte_tile(State<D> &st, const uint32_t (&qf)[D /
                 hi = byte_word(__hmul2(byte_half2(hi), s2));
             }
         };
+        auto products = [&](float (&o)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int z = kProducts<W> - 1; z >= 0; --z)
+                mma_16816(o, a0, a1, a2, a3, p[z][0], p[z][1]);
+        };
         auto add = [&](float (&O)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
             if constexpr (LG == 3) {
-                mma_16816(O, a0, a1, a2, a3, p0, p1);
+                products(O, a0, a1, a2, a3);
             } else {
                 float o[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(o, a0, a1, a2, a3, p0, p1);
+                products(o, a0, a1, a2, a3);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     O[e] = fmaf(o[e], sv[u], O[e]);
@@ -1225,6 +1263,12 @@ __device__ __forceinline__ bool finish_piece(const AttendParams &p, State<D> &st
     __syncwarp();
     if (lane == 0)
         mbar_arrive(empty);
+    if constexpr (kWeights<KIND> == Weights::kBeside)  // what the remainders in heads 4 .. 7 add to heads 0 .. 3
+#pragma unroll
+        for (int y = 0; y < KQ; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                R[y][e] += __shfl_xor_sync(0xffffffffu, R[y][e], 2);
     const int unit = mt.x, slot = mt.w;
     const bool ok0 = h0 < G, ok1 = h0 + 1 < G;
     // over the 8-bit cache a lane's dims are neighbours: the accumulators of heads h0 and h0 + 1 from dim dr on
@@ -1385,8 +1429,9 @@ __device__ __forceinline__ void run_consumer(const AttendParams &p, uint32_t sba
 #pragma unroll
             for (int x = 0; x < KS; ++x) {
                 qf[x][0] = qf[x][1] = 0u;
-                if (r0 < p.G) {
-                    const uint32_t *row = reinterpret_cast<const uint32_t *>(qs + r0 * D * 2);
+                const int g = kWeights<KIND> == Weights::kBeside ? r0 & (kMaxG / 2 - 1) : r0;  // this column's head
+                if (g < p.G) {
+                    const uint32_t *row = reinterpret_cast<const uint32_t *>(qs + g * D * 2);
                     if constexpr (L::BYTE) {
                         // dims 4 w + 16 t + 64 c .. of step x = 4 c + w (see byte_tile())
                         const uint2 q4 = *reinterpret_cast<const uint2 *>(row + 32 * (x >> 2) + 8 * (lane & 3) + 2 * (x & 3));
@@ -1675,10 +1720,33 @@ cudaError_t launch_one(const CUtensorMap &tk, const CUtensorMap &tv, AttendParam
     // CTA per SM better than by a third stage.  64 rows in a window of 4096 82.6 and 76.6 us, 300 rows of up to 8k 106.9
     // and 103.2 us, 100 of 100 15.0 and 13.2 us; but 64 rows of up to 60k 604 and 608 us, eight of up to 32k 42.4 and
     // 43.2 us
-    if constexpr (L::BYTE && D == 128 && KIND < kMany)
+    if constexpr (L::BYTE && D == 128 && !(KIND & kMany))
         if (units > (int64_t)sms * L::kCtasPerSm && most <= kMaxTilesMany)
             return launch_runs<D, KIND + kMany>(tk, tv, p, tiles, sms, s);
     return launch_runs<D, KIND>(tk, tv, p, tiles, sms, s);
+}
+
+// The 8-bit cache's kernels, by the tokens of its blocks and the heads that share a KV head.
+template <int D, int KIND>
+cudaError_t launch_blocks(const AttendParams &p, int sms, cudaStream_t s)
+{
+    const CUtensorMap none = {};
+    switch (p.tb_log2) {
+    case 3:
+        return launch_one<D, KIND + 3>(none, none, p, sms, s);
+    case 4:
+        return launch_one<D, KIND + 4>(none, none, p, sms, s);
+    case 5:
+        return launch_one<D, KIND + 5>(none, none, p, sms, s);
+    default:
+        return launch_one<D, KIND + 6>(none, none, p, sms, s);
+    }
+}
+template <int D, int FMT>
+cudaError_t launch_byte(const AttendParams &p, int sms, cudaStream_t s)
+{
+    constexpr int kKind = k8Bit + 16 * FMT;
+    return p.G <= kMaxG / 2 ? launch_blocks<D, kKind + kFew>(p, sms, s) : launch_blocks<D, kKind>(p, sms, s);
 }
 
 }  // namespace

@@ -90,6 +90,44 @@ def test_every_element_of_blocks_of_unequal_scales(fmt, wide):
 
 
 @FORMATS
+@pytest.mark.parametrize("wide", [0, 4096])
+@pytest.mark.parametrize("d,P,G", [(128, 16, 1), (128, 8, 3), (64, 16, 4), (64, 8, 4), (128, 64, 4), (128, 16, 5), (64, 32, 7), (128, 8, 8),
+                                   (64, 8, 6), (128, 256, 8)])
+def test_weights_are_not_rounded_to_a_half(fmt, wide, d, P, G):
+    """Scores that are exact, one dim of K alone, so that nothing but weights, sums and o's rounding is off:
+      - o's rounding, 2^-11 |o| or 2^-25;
+      - a weight's exponent and exponential, 2^-20 of it, and no more than that again where it is held in two fp16
+        numbers: 2^-22, or 2^-25 of the least where the greatest is 1 or more;
+      - sums in fp32: no term passes more than 64 roundings of 2^-23 (16 in a product, some 20 blocks of a warp's, the
+        merges): 2^-17 sum p |v| / l."""
+    lens = [33, 700, 64, 5, 300]
+    b = Batch(fmt, lens, Hkv=2, G=G, d=d, P=P, seed=d + P + G, scale=1.0, wide=wide)
+    ks = []
+    for n in lens:
+        k = np.zeros((n, 2, d), np.float16)
+        k[:, :, 0] = b.rng.uniform(-4, 4, (n, 2))
+        ks.append(k)
+    b.append(ks, [b.normal(n) for n in lens])
+    q = np.zeros((5, 2 * G, d), np.float16)
+    q[:, :, 0] = np.linspace(0.3, 1.5, 2 * G)
+    q = dev(q)
+    for window, sinks in ((None, 0), (40, 9)):
+        o, lse = b.decode(q, window, sinks)
+        b.compare(o, lse, q, window, sinks)
+        x, qn = o.cpu().numpy().astype(np.float64), q.cpu().numpy().astype(np.float64)
+        for i, n in enumerate(lens):
+            t = R.visible(n, window, sinks)
+            for h in range(2 * G):
+                v = b.v[i].values()[t, h // G]
+                s = b.k[i].values()[t, h // G, 0] * qn[i, h, 0]
+                p = np.exp(s - s.max())
+                want = p @ v / p.sum()
+                bound = 2.0 ** -11 * np.abs(want) + 2.0 ** -25 + ((2.0 ** -17 + 2.0 ** -19) * (p @ np.abs(v)) + 2.0 ** -25 * np.abs(v).sum(0)) / p.sum()
+                assert (np.abs(x[i, h] - want) <= bound).all(), (i, h, np.abs(x[i, h] - want).max(), bound.max())
+    b.ok()
+
+
+@FORMATS
 @pytest.mark.parametrize("d,P", [(128, 16), (64, 8), (128, 256)])
 def test_bytes_behind_the_rows_beside_the_greatest_scale(fmt, d, P):
     """Masked tokens of a block whose scale is the format's greatest: any code there, -128 and NaNs among them, counts
